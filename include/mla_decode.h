@@ -364,6 +364,98 @@ typedef struct mla_combine_desc {
 int mla_lse_combine(const void *partials, const float *lses, int num_parts, void *out,
                     const mla_combine_desc *d, mla_stream_t stream);
 
+/*
+ * Page operations.  A pool of cache pages is described by four device arrays
+ * that the caller owns and the calls update in place:
+ *
+ *  kv_pages    [num_pages, 64, 576], bf16 or e4m3 bytes per kv_dtype;
+ *  block_table int32 [num_requests, max_pages_per_seq]: request b's logical
+ *              pages, -1 where it holds none;
+ *  seq_lens    int32 [num_requests];
+ *  ref_counts  int32 [num_pages]: table entries that name the page, 0: free.
+ *
+ * Results depend on the inputs alone: new pages are the lowest free ids, in
+ * the order of the forks (or requests) that need them.  A bad index, length
+ * or table entry is skipped and ORs MLA_PAGES_BAD_ENTRY into the optional
+ * device `error_word`, a request for which no page is left gains none and
+ * ORs MLA_PAGES_FULL.  Calls on one pool are ordered by their stream.
+ * Nothing is allocated or synchronised, and every call can be captured.
+ */
+typedef struct mla_pages_desc {
+  int32_t num_requests;      /* rows of block_table (0 is a no-op)                */
+  int32_t max_pages_per_seq; /* columns of block_table (>= 1)                     */
+  int32_t num_pages;         /* pages of the pool (>= 1)                          */
+  int32_t page_size;         /* must be 64                                        */
+  int32_t head_dim_qk;       /* must be 576                                       */
+  int32_t kv_dtype;          /* enum mla_kv_dtype                                 */
+} mla_pages_desc;
+
+enum mla_pages_error { MLA_PAGES_BAD_ENTRY = 1, MLA_PAGES_FULL = 2 };
+
+/* Bytes of scratch that fork, alloc and compact need for a pool of num_pages
+ * pages (0 if num_pages < 1).  No initial contents are required. */
+size_t mla_pages_workspace_size(int num_pages);
+
+/*
+ * Copies page src[i] of src_pages to page dst[i] of dst_pages, i < n, whole
+ * pages as stored.  The two pools may be one; a dst page must not repeat and,
+ * in one pool, must not be a src page of the same call.  dst_num_pages is
+ * the second pool's size, d->num_pages the first's (d->num_requests and
+ * max_pages_per_seq are not used).  One kernel.
+ */
+int mla_pages_copy(const void *src_pages, void *dst_pages, const int32_t *src, const int32_t *dst, int n,
+                   int dst_num_pages, const mla_pages_desc *d, int32_t *error_word, mla_stream_t stream);
+
+/*
+ * Request children[k] becomes a copy of request parents[k], k < n: its row
+ * names the parent's full pages (one more reference each; entries of -1 stay
+ * -1), a partial last page is copied to a new page of its own (the rows in
+ * use; the rest of the new page keeps what it held), and its length is the
+ * parent's.  The child's row is overwritten: it holds no pages before the
+ * call.  A child must not repeat and must not be a parent of the same call.
+ * When no page is left the child is empty.  Two kernels.
+ */
+int mla_pages_fork(void *kv_pages, int32_t *block_table, int32_t *seq_lens, int32_t *ref_counts,
+                   const int32_t *parents, const int32_t *children, int n, const mla_pages_desc *d,
+                   void *workspace, size_t workspace_bytes, int32_t *error_word, mla_stream_t stream);
+
+/*
+ * Gives every request the pages for new_lens[b] >= seq_lens[b] tokens, in the
+ * order of the requests: logical pages ceil(seq_lens[b] / 64) up to
+ * ceil(new_lens[b] / 64), with one reference each.  Requests that do not grow
+ * are left alone.  A request whose need, with those of the requests before
+ * it, exceeds the free pages gains none.  seq_lens is not changed (the rows
+ * are not written yet), and the pages must not be there already.  Two kernels.
+ */
+int mla_pages_alloc(int32_t *block_table, const int32_t *seq_lens, int32_t *ref_counts,
+                    const int32_t *new_lens, const mla_pages_desc *d, void *workspace,
+                    size_t workspace_bytes, int32_t *error_word, mla_stream_t stream);
+
+/*
+ * Shortens every request to new_lens[b] <= seq_lens[b] tokens (0 ends it; its
+ * own length leaves it): entries past ceil(new_lens[b] / 64) become -1 and
+ * give up their reference; a page without references is free.  With window >
+ * 0, so do the pages that no query at position new_lens[b] or later sees
+ * through mla_decode_window(window, sinks): those past the sinks whose last
+ * token is at or before new_lens[b] - window.  seq_lens is set to new_lens.
+ * One kernel.
+ */
+int mla_pages_free(int32_t *block_table, int32_t *seq_lens, int32_t *ref_counts, const int32_t *new_lens,
+                   int window, int sinks, const mla_pages_desc *d, int32_t *error_word,
+                   mla_stream_t stream);
+
+/*
+ * Moves the live pages to ids 0 .. live - 1: the k-th live page at or past
+ * `live` goes to the k-th free page below it, the others stay.  block_table
+ * and ref_counts follow.  remap: optional int32 [num_pages], each page's new
+ * id, -1 for a page that was free.  Freed ids keep their old contents.  The
+ * first two words of the workspace receive the number of live pages and of
+ * moves.  Three kernels.
+ */
+int mla_pages_compact(void *kv_pages, int32_t *block_table, int32_t *ref_counts, int32_t *remap,
+                      const mla_pages_desc *d, void *workspace, size_t workspace_bytes,
+                      int32_t *error_word, mla_stream_t stream);
+
 /* Static text for a status code. */
 const char *mla_status_string(int status);
 

@@ -17,13 +17,16 @@ import torch
 __all__ = [
     "MlaError", "LSE_NATURAL", "LSE_BASE2", "decode_partial", "lse_combine",
     "workspace_size", "make_workspace", "check_workspace", "library_path", "load_library",
-    "decode_partial_noalloc",
+    "decode_partial_noalloc", "pages_workspace_size", "make_pages_workspace", "pages_copy",
+    "pages_fork", "pages_alloc", "pages_free", "pages_compact", "PAGES_BAD_ENTRY", "PAGES_FULL",
 ]
 
 LSE_NATURAL = 0
 LSE_BASE2 = 1
 KV_BF16 = 0
 KV_E4M3 = 1
+PAGES_BAD_ENTRY = 1
+PAGES_FULL = 2
 _HERE = os.path.dirname(os.path.abspath(__file__))
 _LIB_PATH = os.path.join(_HERE, "_lib", "libmla_decode.so")
 _lib = None
@@ -61,6 +64,12 @@ class DcpMetaDesc(ctypes.Structure):
                 ("page_size", ctypes.c_int32)]
 
 
+class PagesDesc(ctypes.Structure):
+    _fields_ = [("num_requests", ctypes.c_int32), ("max_pages_per_seq", ctypes.c_int32),
+                ("num_pages", ctypes.c_int32), ("page_size", ctypes.c_int32),
+                ("head_dim_qk", ctypes.c_int32), ("kv_dtype", ctypes.c_int32)]
+
+
 def load_library():
     """Loads the built library (raises if it is missing)."""
     global _lib
@@ -91,6 +100,17 @@ def load_library():
         lib.mla_kv_append.restype = i32
         lib.mla_lse_combine.argtypes = [vp, vp, i32, vp, ctypes.POINTER(CombineDesc), vp]
         lib.mla_lse_combine.restype = i32
+        pd = ctypes.POINTER(PagesDesc)
+        lib.mla_pages_workspace_size.argtypes = [i32]
+        lib.mla_pages_workspace_size.restype = sz
+        lib.mla_pages_copy.argtypes = [vp, vp, vp, vp, i32, i32, pd, vp, vp]
+        lib.mla_pages_fork.argtypes = [vp, vp, vp, vp, vp, vp, i32, pd, vp, sz, vp, vp]
+        lib.mla_pages_alloc.argtypes = [vp, vp, vp, vp, pd, vp, sz, vp, vp]
+        lib.mla_pages_free.argtypes = [vp, vp, vp, vp, i32, i32, pd, vp, vp]
+        lib.mla_pages_compact.argtypes = [vp, vp, vp, vp, pd, vp, sz, vp, vp]
+        for f in (lib.mla_pages_copy, lib.mla_pages_fork, lib.mla_pages_alloc, lib.mla_pages_free,
+                  lib.mla_pages_compact):
+            f.restype = i32
         lib.mla_status_string.argtypes = [i32]
         lib.mla_status_string.restype = ctypes.c_char_p
         lib.mla_last_cuda_error.argtypes = []
@@ -438,3 +458,153 @@ def decode_partial_noalloc(q, kv_pages, block_table, seq_lens, part_id: int, num
                 lse.data_ptr(), ctypes.byref(d), _stream_ptr(stream, dev))
     _check(st)
     return out, lse
+
+
+def pages_workspace_size(num_pages: int) -> int:
+    n = load_library().mla_pages_workspace_size(int(num_pages))
+    if n == 0:
+        raise MlaError(-2, "a pool has at least one page")
+    return n
+
+
+def make_pages_workspace(ref_counts) -> torch.Tensor:
+    """Scratch for pages_fork, pages_alloc and pages_compact on the pool that
+    ref_counts [num_pages] describes; reusable, on the counts' device."""
+    return torch.empty(pages_workspace_size(ref_counts.numel()), dtype=torch.uint8,
+                       device=ref_counts.device)
+
+
+_KV_TYPES = (torch.bfloat16, torch.uint8, torch.float8_e4m3fn)
+
+
+def _pages_call(what, anchor, kv_pages, block_table, seq_lens, ref_counts, error_word, **lists):
+    """Checks the arrays of a page operation; returns (device, descriptor)."""
+    dev = anchor.device
+    if dev.type != "cuda":
+        raise ValueError(f"{what} runs on CUDA tensors only")
+    if kv_pages is not None:
+        _need(kv_pages, "kv_pages", _KV_TYPES, dev)
+        if kv_pages.dim() != 3:
+            raise ValueError("kv_pages must be [num_pages, 64, 576]")
+    rows, width, pages = 0, 1, kv_pages.shape[0] if kv_pages is not None else 0
+    if block_table is not None:
+        _need(block_table, "block_table", (torch.int32,), dev)
+        _need(ref_counts, "ref_counts", (torch.int32,), dev)
+        if block_table.dim() != 2:
+            raise ValueError("block_table must be [num_requests, max_pages]")
+        rows, width = block_table.shape
+        if ref_counts.dim() != 1 or (kv_pages is not None and ref_counts.numel() != pages):
+            raise ValueError("ref_counts must be [num_pages]")
+        pages = ref_counts.numel()
+        if seq_lens is not None:
+            _need(seq_lens, "seq_lens", (torch.int32,), dev)
+            if seq_lens.dim() != 1 or seq_lens.numel() != rows:
+                raise ValueError("seq_lens must be [num_requests]")
+    for name, t in lists.items():
+        _need(t, name, (torch.int32,), dev)
+        if t.dim() != 1:
+            raise ValueError(f"{name} must be one-dimensional")
+    if error_word is not None:
+        _need(error_word, "error_word", (torch.int32,), dev)
+    return dev, PagesDesc(num_requests=rows, max_pages_per_seq=width, num_pages=pages,
+                          page_size=kv_pages.shape[1] if kv_pages is not None else 64,
+                          head_dim_qk=kv_pages.shape[2] if kv_pages is not None else 576,
+                          kv_dtype=_kv_dtype_code(kv_pages) if kv_pages is not None else KV_BF16)
+
+
+def _opt(t):
+    return t.data_ptr() if t is not None else None
+
+
+def _pages_ws(workspace, ref_counts):
+    if workspace is None:
+        return make_pages_workspace(ref_counts)
+    _need(workspace, "workspace", (torch.uint8,), ref_counts.device)
+    return workspace
+
+
+def pages_copy(src_pages, dst_pages, src, dst, *, error_word=None, stream=None):
+    """mla_pages_copy: page src[i] of src_pages to page dst[i] of dst_pages
+    (int32 [n] each; two pools of one dtype, or one pool twice)."""
+    dev, d = _pages_call("pages_copy", src_pages, src_pages, None, None, None, error_word, src=src, dst=dst)
+    _need(dst_pages, "dst_pages", (src_pages.dtype,), dev)
+    if dst_pages.dim() != 3 or dst_pages.shape[1:] != src_pages.shape[1:]:
+        raise ValueError("dst_pages must be [num_pages, 64, 576]")
+    if src.numel() != dst.numel():
+        raise ValueError("src and dst must have the same length")
+    with _on(dev):
+        st = load_library().mla_pages_copy(
+            src_pages.data_ptr(), dst_pages.data_ptr(), src.data_ptr(), dst.data_ptr(), src.numel(),
+            dst_pages.shape[0], ctypes.byref(d), _opt(error_word), _stream_ptr(stream, dev))
+    _check(st)
+    return dst_pages
+
+
+def pages_fork(kv_pages, block_table, seq_lens, ref_counts, parents, children, *, workspace=None,
+               error_word=None, stream=None):
+    """mla_pages_fork: request children[k] becomes a copy of parents[k]
+    (int32 [n] each): full pages shared, a partial last page copied.  The
+    table [R, W], lengths [R] and counts [num_pages] are updated in place."""
+    dev, d = _pages_call("pages_fork", kv_pages, kv_pages, block_table, seq_lens, ref_counts, error_word,
+                         parents=parents, children=children)
+    if parents.numel() != children.numel():
+        raise ValueError("parents and children must have the same length")
+    ws = _pages_ws(workspace, ref_counts)
+    with _on(dev):
+        st = load_library().mla_pages_fork(
+            kv_pages.data_ptr(), block_table.data_ptr(), seq_lens.data_ptr(), ref_counts.data_ptr(),
+            parents.data_ptr(), children.data_ptr(), parents.numel(), ctypes.byref(d), ws.data_ptr(),
+            ws.numel(), _opt(error_word), _stream_ptr(stream, dev))
+    _check(st)
+
+
+def pages_alloc(block_table, seq_lens, ref_counts, new_lens, *, workspace=None, error_word=None,
+                stream=None):
+    """mla_pages_alloc: every request gets the pages for new_lens[b] >=
+    seq_lens[b] tokens, lowest free pages first (seq_lens is not changed)."""
+    dev, d = _pages_call("pages_alloc", block_table, None, block_table, seq_lens, ref_counts, error_word,
+                         new_lens=new_lens)
+    if new_lens.numel() != d.num_requests:
+        raise ValueError("new_lens must be [num_requests]")
+    ws = _pages_ws(workspace, ref_counts)
+    with _on(dev):
+        st = load_library().mla_pages_alloc(
+            block_table.data_ptr(), seq_lens.data_ptr(), ref_counts.data_ptr(), new_lens.data_ptr(),
+            ctypes.byref(d), ws.data_ptr(), ws.numel(), _opt(error_word), _stream_ptr(stream, dev))
+    _check(st)
+
+
+def pages_free(block_table, seq_lens, ref_counts, new_lens, *, window: int = 0, sinks: int = 0,
+               error_word=None, stream=None):
+    """mla_pages_free: every request is shortened to new_lens[b] tokens (0
+    ends it, its own length leaves it) and, with a window, gives up the pages
+    that decode_window(window, sinks) no longer sees."""
+    dev, d = _pages_call("pages_free", block_table, None, block_table, seq_lens, ref_counts, error_word,
+                         new_lens=new_lens)
+    if new_lens.numel() != d.num_requests:
+        raise ValueError("new_lens must be [num_requests]")
+    with _on(dev):
+        st = load_library().mla_pages_free(
+            block_table.data_ptr(), seq_lens.data_ptr(), ref_counts.data_ptr(), new_lens.data_ptr(),
+            int(window), int(sinks), ctypes.byref(d), _opt(error_word), _stream_ptr(stream, dev))
+    _check(st)
+
+
+def pages_compact(kv_pages, block_table, ref_counts, *, remap=None, workspace=None, error_word=None,
+                  stream=None):
+    """mla_pages_compact: the live pages move to ids 0 .. live - 1 and the
+    table [R, W] and counts follow.  remap: optional int32 [num_pages], each
+    page's new id (-1: it was free).  Returns the workspace's first two words,
+    a device int32 [2]: live pages, moves."""
+    dev, d = _pages_call("pages_compact", kv_pages, kv_pages, block_table, None, ref_counts, error_word)
+    if remap is not None:
+        _need(remap, "remap", (torch.int32,), dev)
+        if remap.numel() != d.num_pages:
+            raise ValueError("remap must be [num_pages]")
+    ws = _pages_ws(workspace, ref_counts)
+    with _on(dev):
+        st = load_library().mla_pages_compact(
+            kv_pages.data_ptr(), block_table.data_ptr(), ref_counts.data_ptr(), _opt(remap),
+            ctypes.byref(d), ws.data_ptr(), ws.numel(), _opt(error_word), _stream_ptr(stream, dev))
+    _check(st)
+    return ws[:8].view(torch.int32)

@@ -12,6 +12,7 @@
 #include <mutex>
 
 #include "common.cuh"
+#include "pages.cuh"
 
 namespace mla {
 cudaError_t launch_decode_simt(const DecodeParams &p, int grid, cudaStream_t stream);
@@ -32,6 +33,18 @@ cudaError_t launch_decode_tc(const DecodeParams &p, int npv, int q_rows, int gro
 cudaError_t launch_lse_combine(const void *partials, const float *lses, int num_parts, void *out,
                                float *out_lse, int rows, int dim, int base2, cudaStream_t stream);
 int combine_max_parts();
+cudaError_t launch_pages_copy(const void *src_pool, void *dst_pool, const int32_t *src, const int32_t *dst,
+                              int n, int src_pages, int dst_pages, int row_bytes, int32_t *error_word,
+                              cudaStream_t stream);
+cudaError_t launch_pages_fork(const PagesTable &t, void *pool, int row_bytes, const int32_t *parents,
+                              const int32_t *children, int n, const PagesWorkspace &ws, int32_t *error_word,
+                              cudaStream_t stream);
+cudaError_t launch_pages_alloc(const PagesTable &t, const int32_t *new_lens, const PagesWorkspace &ws,
+                               int32_t *error_word, cudaStream_t stream);
+cudaError_t launch_pages_free(const PagesTable &t, const int32_t *new_lens, int window, int sinks,
+                              int32_t *error_word, cudaStream_t stream);
+cudaError_t launch_pages_compact(const PagesTable &t, void *pool, int row_bytes, int32_t *remap, int grid,
+                                 const PagesWorkspace &ws, int32_t *error_word, cudaStream_t stream);
 }  // namespace mla
 
 namespace {
@@ -322,6 +335,22 @@ int check_cache_desc(const mla_decode_desc *d) {
   if (d->kv_dtype == MLA_KV_E4M3 && !(std::isfinite(d->kv_scale) && d->kv_scale > 0.f))
     return MLA_ERR_ARG;
   return MLA_OK;
+}
+
+int check_pages_desc(const mla_pages_desc *d) {
+  if (!d) return MLA_ERR_NULL;
+  if (d->num_requests < 0 || d->max_pages_per_seq < 1 || d->num_pages < 1) return MLA_ERR_SHAPE;
+  if (d->head_dim_qk != mla::kDqk || d->page_size != mla::kPage) return MLA_ERR_SHAPE;
+  if (d->kv_dtype != MLA_KV_BF16 && d->kv_dtype != MLA_KV_E4M3) return MLA_ERR_ARG;
+  return MLA_OK;
+}
+
+int pages_row_bytes(const mla_pages_desc *d) { return mla::kDqk * (d->kv_dtype == MLA_KV_E4M3 ? 1 : 2); }
+
+mla::PagesTable pages_table(int32_t *block_table, const int32_t *seq_lens, int32_t *ref_counts,
+                            const mla_pages_desc *d) {
+  return mla::PagesTable{block_table, const_cast<int32_t *>(seq_lens), ref_counts, d->num_requests,
+                         d->max_pages_per_seq, d->num_pages};
 }
 
 // Rows of one request: q_len query tokens x num_heads heads.
@@ -624,6 +653,108 @@ int mla_lse_combine(const void *partials, const float *lses, int num_parts, void
   cudaError_t e = mla::launch_lse_combine(partials, lses, num_parts, out, d->out_lse, int(rows),
                                           d->head_dim, d->lse_base == MLA_LSE_BASE2,
                                           reinterpret_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? MLA_OK : cuda_fail(e);
+}
+
+size_t mla_pages_workspace_size(int num_pages) {
+  return num_pages < 1 ? 0 : mla::pages_workspace_bytes(num_pages);
+}
+
+int mla_pages_copy(const void *src_pages, void *dst_pages, const int32_t *src, const int32_t *dst, int n,
+                   int dst_num_pages, const mla_pages_desc *d, int32_t *error_word, mla_stream_t stream) {
+  int st = check_pages_desc(d);
+  if (st != MLA_OK) return st;
+  if (n < 0) return MLA_ERR_ARG;
+  if (dst_num_pages < 1) return MLA_ERR_SHAPE;
+  if (n == 0) return MLA_OK;
+  if (!src_pages || !dst_pages || !src || !dst) return MLA_ERR_NULL;
+  if (!aligned(src_pages, 16) || !aligned(dst_pages, 16) || !aligned(src, 4) || !aligned(dst, 4) ||
+      !aligned(error_word, 4))
+    return MLA_ERR_ALIGN;
+  current_device(&st);
+  if (st != MLA_OK) return st;
+  cudaError_t e = mla::launch_pages_copy(src_pages, dst_pages, src, dst, n, d->num_pages, dst_num_pages,
+                                         pages_row_bytes(d), error_word,
+                                         reinterpret_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? MLA_OK : cuda_fail(e);
+}
+
+int mla_pages_fork(void *kv_pages, int32_t *block_table, int32_t *seq_lens, int32_t *ref_counts,
+                   const int32_t *parents, const int32_t *children, int n, const mla_pages_desc *d,
+                   void *workspace, size_t workspace_bytes, int32_t *error_word, mla_stream_t stream) {
+  int st = check_pages_desc(d);
+  if (st != MLA_OK) return st;
+  if (n < 0) return MLA_ERR_ARG;
+  if (n == 0 || d->num_requests == 0) return MLA_OK;
+  if (!kv_pages || !block_table || !seq_lens || !ref_counts || !parents || !children || !workspace)
+    return MLA_ERR_NULL;
+  if (!aligned(kv_pages, 16) || !aligned(block_table, 4) || !aligned(seq_lens, 4) ||
+      !aligned(ref_counts, 4) || !aligned(parents, 4) || !aligned(children, 4) || !aligned(workspace, 256) ||
+      !aligned(error_word, 4))
+    return MLA_ERR_ALIGN;
+  if (workspace_bytes < mla_pages_workspace_size(d->num_pages)) return MLA_ERR_WORKSPACE;
+  current_device(&st);
+  if (st != MLA_OK) return st;
+  cudaError_t e = mla::launch_pages_fork(pages_table(block_table, seq_lens, ref_counts, d), kv_pages,
+                                         pages_row_bytes(d), parents, children, n,
+                                         mla::pages_workspace(workspace, d->num_pages), error_word,
+                                         reinterpret_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? MLA_OK : cuda_fail(e);
+}
+
+int mla_pages_alloc(int32_t *block_table, const int32_t *seq_lens, int32_t *ref_counts,
+                    const int32_t *new_lens, const mla_pages_desc *d, void *workspace,
+                    size_t workspace_bytes, int32_t *error_word, mla_stream_t stream) {
+  int st = check_pages_desc(d);
+  if (st != MLA_OK) return st;
+  if (d->num_requests == 0) return MLA_OK;
+  if (!block_table || !seq_lens || !ref_counts || !new_lens || !workspace) return MLA_ERR_NULL;
+  if (!aligned(block_table, 4) || !aligned(seq_lens, 4) || !aligned(ref_counts, 4) ||
+      !aligned(new_lens, 4) || !aligned(workspace, 256) || !aligned(error_word, 4))
+    return MLA_ERR_ALIGN;
+  if (workspace_bytes < mla_pages_workspace_size(d->num_pages)) return MLA_ERR_WORKSPACE;
+  current_device(&st);
+  if (st != MLA_OK) return st;
+  cudaError_t e = mla::launch_pages_alloc(pages_table(block_table, seq_lens, ref_counts, d), new_lens,
+                                          mla::pages_workspace(workspace, d->num_pages), error_word,
+                                          reinterpret_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? MLA_OK : cuda_fail(e);
+}
+
+int mla_pages_free(int32_t *block_table, int32_t *seq_lens, int32_t *ref_counts, const int32_t *new_lens,
+                   int window, int sinks, const mla_pages_desc *d, int32_t *error_word,
+                   mla_stream_t stream) {
+  int st = check_pages_desc(d);
+  if (st != MLA_OK) return st;
+  if (window < 0 || sinks < 0) return MLA_ERR_ARG;
+  if (d->num_requests == 0) return MLA_OK;
+  if (!block_table || !seq_lens || !ref_counts || !new_lens) return MLA_ERR_NULL;
+  if (!aligned(block_table, 4) || !aligned(seq_lens, 4) || !aligned(ref_counts, 4) ||
+      !aligned(new_lens, 4) || !aligned(error_word, 4))
+    return MLA_ERR_ALIGN;
+  current_device(&st);
+  if (st != MLA_OK) return st;
+  cudaError_t e = mla::launch_pages_free(pages_table(block_table, seq_lens, ref_counts, d), new_lens, window,
+                                         sinks, error_word, reinterpret_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? MLA_OK : cuda_fail(e);
+}
+
+int mla_pages_compact(void *kv_pages, int32_t *block_table, int32_t *ref_counts, int32_t *remap,
+                      const mla_pages_desc *d, void *workspace, size_t workspace_bytes,
+                      int32_t *error_word, mla_stream_t stream) {
+  int st = check_pages_desc(d);
+  if (st != MLA_OK) return st;
+  if (!kv_pages || (!block_table && d->num_requests > 0) || !ref_counts || !workspace) return MLA_ERR_NULL;
+  if (!aligned(kv_pages, 16) || !aligned(block_table, 4) || !aligned(ref_counts, 4) || !aligned(remap, 4) ||
+      !aligned(workspace, 256) || !aligned(error_word, 4))
+    return MLA_ERR_ALIGN;
+  if (workspace_bytes < mla_pages_workspace_size(d->num_pages)) return MLA_ERR_WORKSPACE;
+  DeviceFacts f = current_device(&st);
+  if (st != MLA_OK) return st;
+  cudaError_t e = mla::launch_pages_compact(pages_table(block_table, nullptr, ref_counts, d), kv_pages,
+                                            pages_row_bytes(d), remap, 4 * f.sms,
+                                            mla::pages_workspace(workspace, d->num_pages), error_word,
+                                            reinterpret_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? MLA_OK : cuda_fail(e);
 }
 
