@@ -365,6 +365,62 @@ int mla_lse_combine(const void *partials, const float *lses, int num_parts, void
                     const mla_combine_desc *d, mla_stream_t stream);
 
 /*
+ * Decode with a bounded view: a query at position p attends to the tokens t
+ * <= p with t > p - window, and to the first `sinks` tokens of its request.
+ * Query token i of q_len sits at position L - q_len + i, as in
+ * mla_decode_partial; a query that sees nothing gets the neutral pair.
+ *
+ *  window      tokens of the sliding window, the query's own among them (>= 1).
+ *  sinks       first tokens that stay visible (>= 0).
+ *  all others  as for mla_decode_partial with num_parts = 1, the workspace of
+ *              mla_decode_workspace_size included (q_len 1..16).
+ *
+ * Reads the pages that hold the sinks and those from the first query's window
+ * on; entries of other pages are never read, so that pages given up with
+ * mla_pages_free(window, sinks) may be -1.  What a request's rows outside its
+ * queries' views hold does not matter; a row that only some of its q_len
+ * queries see must be finite.  Arithmetic and errors as for
+ * mla_decode_partial, except that lse takes the unrounded softmax weights of
+ * a bf16 cache too.  Two kernels.
+ */
+int mla_decode_window(const void *q, const void *kv_pages, const int32_t *block_table,
+                      const int32_t *seq_lens, int window, int sinks, float sm_scale, int lse_base,
+                      void *out, float *lse, const mla_decode_desc *d, void *workspace,
+                      size_t workspace_bytes, mla_stream_t stream);
+
+/*
+ * Decode of a batch whose requests share pages: the result of
+ * mla_decode_partial with num_parts = 1, with the shared pages read and
+ * multiplied once for all requests of a group.
+ *
+ *  group_starts int32 [num_groups + 1]: group g is the requests
+ *               group_starts[g] .. group_starts[g + 1] - 1; the first entry is
+ *               0, the last the batch, none is below its predecessor (an empty
+ *               group is allowed).
+ *  shared_pages int32 [num_groups]: the first shared_pages[g] entries of the
+ *               group's block-table rows are the same pages (the first
+ *               request's are read; 0: nothing is shared).  A request shorter
+ *               than its group's shared pages sees its own tokens only.
+ *  workspace    >= mla_decode_shared_workspace_size(d, num_groups, 0) bytes,
+ *               same rules as for mla_decode_partial.
+ *  all others   as for mla_decode_partial with num_parts = 1.
+ *
+ * The rows of a group (q_len x num_heads of each of its requests) attend to
+ * the shared pages in blocks of 64, each request's rows to its own pages, and
+ * the partial results are merged by their LSE.  A request outside every group
+ * or a page number outside [0, max_pages_per_seq] is reported as
+ * MLA_ERR_BOUNDS by mla_decode_check_workspace.  Arithmetic as for
+ * mla_decode_window.  Two kernels.
+ */
+size_t mla_decode_shared_workspace_size(const mla_decode_desc *d, int num_groups, int num_sms);
+
+int mla_decode_shared(const void *q, const void *kv_pages, const int32_t *block_table,
+                      const int32_t *seq_lens, const int32_t *group_starts, const int32_t *shared_pages,
+                      int num_groups, float sm_scale, int lse_base, void *out, float *lse,
+                      const mla_decode_desc *d, void *workspace, size_t workspace_bytes,
+                      mla_stream_t stream);
+
+/*
  * Page operations.  A pool of cache pages is described by four device arrays
  * that the caller owns and the calls update in place:
  *

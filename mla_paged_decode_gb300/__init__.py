@@ -17,7 +17,7 @@ import torch
 __all__ = [
     "MlaError", "LSE_NATURAL", "LSE_BASE2", "decode_partial", "lse_combine",
     "workspace_size", "make_workspace", "check_workspace", "library_path", "load_library",
-    "decode_partial_noalloc", "pages_workspace_size", "make_pages_workspace", "pages_copy",
+    "decode_partial_noalloc", "decode_window", "decode_shared", "make_shared_workspace", "pages_workspace_size", "make_pages_workspace", "pages_copy",
     "pages_fork", "pages_alloc", "pages_free", "pages_compact", "PAGES_BAD_ENTRY", "PAGES_FULL",
 ]
 
@@ -100,6 +100,13 @@ def load_library():
         lib.mla_kv_append.restype = i32
         lib.mla_lse_combine.argtypes = [vp, vp, i32, vp, ctypes.POINTER(CombineDesc), vp]
         lib.mla_lse_combine.restype = i32
+        dd = ctypes.POINTER(DecodeDesc)
+        lib.mla_decode_window.argtypes = [vp, vp, vp, vp, i32, i32, f32, i32, vp, vp, dd, vp, sz, vp]
+        lib.mla_decode_window.restype = i32
+        lib.mla_decode_shared_workspace_size.argtypes = [dd, i32, i32]
+        lib.mla_decode_shared_workspace_size.restype = sz
+        lib.mla_decode_shared.argtypes = [vp, vp, vp, vp, vp, vp, i32, f32, i32, vp, vp, dd, vp, sz, vp]
+        lib.mla_decode_shared.restype = i32
         pd = ctypes.POINTER(PagesDesc)
         lib.mla_pages_workspace_size.argtypes = [i32]
         lib.mla_pages_workspace_size.restype = sz
@@ -153,6 +160,7 @@ def _kv_dtype_code(kv_pages: torch.Tensor) -> int:
     raise TypeError(f"kv_pages must be bf16 or e4m3 bytes, got {kv_pages.dtype}")
 
 
+_KV_TYPES = (torch.bfloat16, torch.uint8, torch.float8_e4m3fn)
 _DESCS: dict = {}
 
 
@@ -460,6 +468,83 @@ def decode_partial_noalloc(q, kv_pages, block_table, seq_lens, part_id: int, num
     return out, lse
 
 
+def _view_args(what, q, kv_pages, block_table, seq_lens, out, lse, kv_scale):
+    """Checks what decode_window and decode_shared have in common; returns the
+    device and the descriptor."""
+    dev = q.device
+    if dev.type != "cuda":
+        raise ValueError(f"{what} runs on CUDA tensors only")
+    _need(q, "q", (torch.bfloat16,), dev)
+    _need(kv_pages, "kv_pages", _KV_TYPES, dev)
+    _need(block_table, "block_table", (torch.int32,), dev)
+    _need(seq_lens, "seq_lens", (torch.int32,), dev)
+    _need(out, "out", (torch.bfloat16,), dev)
+    _need(lse, "lse", (torch.float32,), dev)
+    d = _decode_desc(q, kv_pages, block_table, kv_scale)
+    if seq_lens.numel() != d.batch or block_table.dim() != 2 or block_table.shape[0] != d.batch:
+        raise ValueError("seq_lens / block_table do not match the batch")
+    if kv_pages.shape[2] != 576:
+        raise ValueError("kv_pages must be [num_pages, 64, 576]")
+    rows = d.batch * d.q_len * d.num_heads
+    if out.numel() != rows * 512 or lse.numel() != rows:
+        raise ValueError("out must be [B,q_len,H,512] and lse [B,q_len,H]")
+    return dev, d
+
+
+def decode_window(q, kv_pages, block_table, seq_lens, window: int, sinks: int, sm_scale: float,
+                  lse_base: int, out, lse, *, kv_scale: float = 1.0, workspace=None, stream=None):
+    """mla_decode_window: each query sees the last `window` tokens up to its
+    own and the request's first `sinks` tokens.  Tensors as for
+    decode_partial (q [B,q_len,H,576], 1..16 query tokens); the workspace is
+    make_workspace's.  Entries of pages out of view may be -1."""
+    dev, d = _view_args("decode_window", q, kv_pages, block_table, seq_lens, out, lse, kv_scale)
+    if workspace is None:
+        workspace = make_workspace(q, kv_pages, block_table, kv_scale)
+    _need(workspace, "workspace", (torch.uint8,), dev)
+    with _on(dev):
+        st = load_library().mla_decode_window(
+            q.data_ptr(), kv_pages.data_ptr(), block_table.data_ptr(), seq_lens.data_ptr(), int(window),
+            int(sinks), float(sm_scale), int(lse_base), out.data_ptr(), lse.data_ptr(), ctypes.byref(d),
+            workspace.data_ptr(), workspace.numel(), _stream_ptr(stream, dev))
+    _check(st)
+    return out, lse
+
+
+def make_shared_workspace(q, kv_pages, block_table, num_groups: int, kv_scale: float = 1.0):
+    """A zero-filled workspace for decode_shared over num_groups groups."""
+    d = _decode_desc(q, kv_pages, block_table, kv_scale)
+    with torch.cuda.device(q.device):
+        n = load_library().mla_decode_shared_workspace_size(ctypes.byref(d), int(num_groups), 0)
+    if n == 0:
+        raise MlaError(-2, "cannot size a workspace for these shapes")
+    return torch.zeros(n, dtype=torch.uint8, device=q.device)
+
+
+def decode_shared(q, kv_pages, block_table, seq_lens, group_starts, shared_pages, sm_scale: float,
+                  lse_base: int, out, lse, *, kv_scale: float = 1.0, workspace=None, stream=None):
+    """mla_decode_shared: the requests group_starts[g] .. group_starts[g + 1]
+    (int32 [G + 1], from 0 to B) have their first shared_pages[g] (int32 [G])
+    pages in common, which are read and multiplied once for the group.
+    Tensors as for decode_partial; the workspace is make_shared_workspace's."""
+    dev, d = _view_args("decode_shared", q, kv_pages, block_table, seq_lens, out, lse, kv_scale)
+    _need(group_starts, "group_starts", (torch.int32,), dev)
+    _need(shared_pages, "shared_pages", (torch.int32,), dev)
+    groups = shared_pages.numel()
+    if groups < 1 or group_starts.numel() != groups + 1:
+        raise ValueError("group_starts must be [G + 1] and shared_pages [G], G >= 1")
+    if workspace is None:
+        workspace = make_shared_workspace(q, kv_pages, block_table, groups, kv_scale)
+    _need(workspace, "workspace", (torch.uint8,), dev)
+    with _on(dev):
+        st = load_library().mla_decode_shared(
+            q.data_ptr(), kv_pages.data_ptr(), block_table.data_ptr(), seq_lens.data_ptr(),
+            group_starts.data_ptr(), shared_pages.data_ptr(), groups, float(sm_scale), int(lse_base),
+            out.data_ptr(), lse.data_ptr(), ctypes.byref(d), workspace.data_ptr(), workspace.numel(),
+            _stream_ptr(stream, dev))
+    _check(st)
+    return out, lse
+
+
 def pages_workspace_size(num_pages: int) -> int:
     n = load_library().mla_pages_workspace_size(int(num_pages))
     if n == 0:
@@ -472,9 +557,6 @@ def make_pages_workspace(ref_counts) -> torch.Tensor:
     ref_counts [num_pages] describes; reusable, on the counts' device."""
     return torch.empty(pages_workspace_size(ref_counts.numel()), dtype=torch.uint8,
                        device=ref_counts.device)
-
-
-_KV_TYPES = (torch.bfloat16, torch.uint8, torch.float8_e4m3fn)
 
 
 def _pages_call(what, anchor, kv_pages, block_table, seq_lens, ref_counts, error_word, **lists):

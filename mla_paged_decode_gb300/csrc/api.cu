@@ -163,7 +163,7 @@ bool fused_path(const mla_decode_desc *d, int num_parts) {
   return num_parts >= 1 && (8 % num_parts == 0 || strided_path(d, num_parts));
 }
 
-// Q as [B*H rows, 576] bf16, one 64-column swizzled box of min(64, H) rows;
+// Q as [B*H rows, 576] bf16, one 64-column swizzled box of q_rows rows;
 // partition rows of a bf16 cache as a 5-D view (64 dims, 8 rows of stride P,
 // 9 blocks of 64 dims, groups of 8 rows, partitions), one box = one page's
 // owned rows; of an e4m3 cache as a 3-D view (576 bytes, rows of stride P,
@@ -174,7 +174,7 @@ bool fused_path(const mla_decode_desc *d, int num_parts) {
 // first row and the partition dimension is left off (4-D / 2-D maps, the
 // faster boxes); for all P partitions (`all_parts`) it is added, with a stride
 // of one row (5-D / 3-D maps, coordinate r).
-int make_tensor_maps(const void *q, const void *kv, const mla_decode_desc *d, int part_id,
+int make_tensor_maps(const void *q, const void *kv, const mla_decode_desc *d, int q_rows, int part_id,
                      int num_parts, bool all_parts, bool strided, CUtensorMap *tm_q,
                      CUtensorMap *tm_kv, CUtensorMap *tm_kvg, CUtensorMap *tm_kvb) {
   EncodeTiled enc = encode_tiled();
@@ -187,7 +187,7 @@ int make_tensor_maps(const void *q, const void *kv, const mla_decode_desc *d, in
     const cuuint64_t qrows = cuuint64_t(d->q_len) * cuuint64_t(d->num_heads);
     cuuint64_t dims[2] = {cuuint64_t(mla::kDqk), cuuint64_t(d->batch) * qrows};
     cuuint64_t strides[1] = {row};
-    cuuint32_t box[2] = {64, cuuint32_t(qrows < 64 ? qrows : 64)};
+    cuuint32_t box[2] = {64, cuuint32_t(q_rows)};
     cuuint32_t es[2] = {1, 1};
     CUresult r = enc(tm_q, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void *>(q), dims, strides,
                      box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
@@ -419,10 +419,10 @@ int enqueue_decode(const void *q, const void *kv_pages, const int32_t *block_tab
   cudaError_t e;
   if (tc) {
     CUtensorMap tm_q, tm_kv, tm_kvg, tm_kvb;
-    int st = make_tensor_maps(q, kv_pages, d, p.part_id, p.num_parts, fused, strided, &tm_q,
+    const int h = rows < kTcHeadsPerGroup ? rows : kTcHeadsPerGroup;
+    int st = make_tensor_maps(q, kv_pages, d, h, p.part_id, p.num_parts, fused, strided, &tm_q,
                               &tm_kv, &tm_kvg, &tm_kvb);
     if (st != MLA_OK) return st;
-    const int h = rows < kTcHeadsPerGroup ? rows : kTcHeadsPerGroup;
     const int npv = ((h + 15) / 16) * 16;
     e = mla::launch_decode_tc(p, npv, h, strided ? 1 : 8 / p.num_parts, tm_q, tm_kv, tm_kvg, tm_kvb,
                               grid, s);
@@ -431,6 +431,73 @@ int enqueue_decode(const void *q, const void *kv_pages, const int32_t *block_tab
   }
   return e == cudaSuccess ? MLA_OK : cuda_fail(e);
 }
+
+// A view of the whole cache (one partition): see ViewReq.  `view` carries the
+// view's own fields; everything else is filled in here.
+int enqueue_view(mla::DecodeParams p, const void *q, const void *kv_pages, const int32_t *block_table,
+                 const int32_t *seq_lens, float sm_scale, int lse_base, void *out, float *lse,
+                 const mla_decode_desc *d, void *workspace, const mla::WorkspaceLayout &wl, int grid,
+                 cudaStream_t s) {
+  const int rows = rows_of(d);
+  p.q = static_cast<const __nv_bfloat16 *>(q);
+  p.kv = kv_pages;
+  p.block_table = block_table;
+  p.seq_lens = seq_lens;
+  p.out = static_cast<__nv_bfloat16 *>(out);
+  p.lse = lse;
+  p.ws = static_cast<unsigned char *>(workspace);
+  p.wl = wl;
+  p.batch = p.req_batch = d->batch;
+  p.heads = rows;
+  p.head_groups = (rows + kTcHeadsPerGroup - 1) / kTcHeadsPerGroup;
+  p.heads_per_group = kTcHeadsPerGroup;
+  p.q_len = d->q_len;
+  p.q_heads = d->num_heads;
+  p.num_pages = d->num_pages;
+  p.max_pages = d->max_pages_per_seq;
+  p.part_id = 0;
+  p.num_parts = 1;
+  p.kv_e4m3 = d->kv_dtype == MLA_KV_E4M3;
+  p.kv_scale = p.kv_e4m3 ? d->kv_scale : 1.f;
+  p.score_scale_log2 = sm_scale * mla::kLog2e;
+  p.lse_base2 = lse_base == MLA_LSE_BASE2;
+  // blocks of the shared pages hold up to 64 rows whatever a request's rows
+  const long long most = p.view == mla::kViewShared ? (long long)d->batch * rows : rows;
+  const int h = int(most < kTcHeadsPerGroup ? most : kTcHeadsPerGroup);
+  CUtensorMap tm_q, tm_kv, tm_kvg, tm_kvb;
+  const int st = make_tensor_maps(q, kv_pages, d, h, 0, 1, false, false, &tm_q, &tm_kv, &tm_kvg, &tm_kvb);
+  if (st != MLA_OK) return st;
+  const cudaError_t e = mla::launch_decode_tc(p, (h + 15) / 16 * 16, h, 8, tm_q, tm_kv, tm_kvg, tm_kvb, grid, s);
+  return e == cudaSuccess ? MLA_OK : cuda_fail(e);
+}
+
+// The checks of a view call's common arguments.
+int check_view_call(const void *q, const void *kv_pages, const int32_t *block_table, const int32_t *seq_lens,
+                    float sm_scale, int lse_base, const void *out, const float *lse,
+                    const mla_decode_desc *d, const void *workspace) {
+  if (lse_base != MLA_LSE_NATURAL && lse_base != MLA_LSE_BASE2) return MLA_ERR_ARG;
+  if (!std::isfinite(sm_scale)) return MLA_ERR_ARG;
+  if ((long long)d->batch * rows_of(d) > (1LL << 30)) return MLA_ERR_SHAPE;
+  if (d->batch == 0) return MLA_OK;
+  if (!q || !kv_pages || !block_table || !seq_lens || !out || !lse || !workspace) return MLA_ERR_NULL;
+  if (!aligned(q, 16) || !aligned(kv_pages, 16) || !aligned(out, 16) || !aligned(lse, 4) ||
+      !aligned(block_table, 4) || !aligned(seq_lens, 4) || !aligned(workspace, 256))
+    return MLA_ERR_ALIGN;
+  return MLA_OK;
+}
+
+// Shared pages: 64-row blocks of all groups' rows (an upper bound known on
+// the host), and the workspace with a slot for every (virtual request, CTA).
+int shared_blocks(const mla_decode_desc *d, int num_groups) {
+  return int((long long)d->batch * rows_of(d) / kTcHeadsPerGroup) + num_groups;
+}
+mla::WorkspaceLayout shared_layout(const mla_decode_desc *d, int num_groups, int grid) {
+  const int groups = (rows_of(d) + kTcHeadsPerGroup - 1) / kTcHeadsPerGroup;
+  const int v = shared_blocks(d, num_groups) + d->batch * groups;
+  return mla::workspace_layout(v, (v + grid + 1) / 2);
+}
+constexpr int kMaxGroups = 1 << 20;
+constexpr int kMaxView = 1 << 30;
 
 }  // namespace
 
@@ -756,6 +823,66 @@ int mla_pages_compact(void *kv_pages, int32_t *block_table, int32_t *ref_counts,
                                             mla::pages_workspace(workspace, d->num_pages), error_word,
                                             reinterpret_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? MLA_OK : cuda_fail(e);
+}
+
+int mla_decode_window(const void *q, const void *kv_pages, const int32_t *block_table,
+                      const int32_t *seq_lens, int window, int sinks, float sm_scale, int lse_base,
+                      void *out, float *lse, const mla_decode_desc *d, void *workspace,
+                      size_t workspace_bytes, mla_stream_t stream) {
+  int st = check_desc(d);
+  if (st != MLA_OK) return st;
+  if (window < 1 || sinks < 0) return MLA_ERR_ARG;
+  st = check_view_call(q, kv_pages, block_table, seq_lens, sm_scale, lse_base, out, lse, d, workspace);
+  if (st != MLA_OK || d->batch == 0) return st;
+  DeviceFacts f = current_device(&st);
+  if (st != MLA_OK) return st;
+  const auto wl = mla::workspace_layout(d->batch * head_groups_of(d), f.sms);
+  if (workspace_bytes < wl.total) return MLA_ERR_WORKSPACE;
+  mla::DecodeParams p;
+  p.view = mla::kViewWindow;
+  // (longer than any request: the kernel's sums with them stay in 32 bits)
+  p.window = window < kMaxView ? window : kMaxView;
+  p.sinks = sinks < kMaxView ? sinks : kMaxView;
+  return enqueue_view(p, q, kv_pages, block_table, seq_lens, sm_scale, lse_base, out, lse, d, workspace, wl,
+                      f.sms, reinterpret_cast<cudaStream_t>(stream));
+}
+
+size_t mla_decode_shared_workspace_size(const mla_decode_desc *d, int num_groups, int num_sms) {
+  if (check_desc(d) != MLA_OK || num_groups < 1 || num_groups > kMaxGroups) return 0;
+  if ((long long)d->batch * rows_of(d) > (1LL << 30)) return 0;
+  if (num_sms <= 0) {
+    int st = 0;
+    DeviceFacts f = current_device(&st);
+    if (f.sms <= 0) return 0;
+    num_sms = f.sms;
+  }
+  return shared_layout(d, num_groups, num_sms).total;
+}
+
+int mla_decode_shared(const void *q, const void *kv_pages, const int32_t *block_table,
+                      const int32_t *seq_lens, const int32_t *group_starts, const int32_t *shared_pages,
+                      int num_groups, float sm_scale, int lse_base, void *out, float *lse,
+                      const mla_decode_desc *d, void *workspace, size_t workspace_bytes,
+                      mla_stream_t stream) {
+  int st = check_desc(d);
+  if (st != MLA_OK) return st;
+  if (num_groups < 1 || num_groups > kMaxGroups) return MLA_ERR_ARG;
+  st = check_view_call(q, kv_pages, block_table, seq_lens, sm_scale, lse_base, out, lse, d, workspace);
+  if (st != MLA_OK || d->batch == 0) return st;
+  if (!group_starts || !shared_pages) return MLA_ERR_NULL;
+  if (!aligned(group_starts, 4) || !aligned(shared_pages, 4)) return MLA_ERR_ALIGN;
+  DeviceFacts f = current_device(&st);
+  if (st != MLA_OK) return st;
+  const auto wl = shared_layout(d, num_groups, f.sms);
+  if (workspace_bytes < wl.total) return MLA_ERR_WORKSPACE;
+  mla::DecodeParams p;
+  p.view = mla::kViewShared;
+  p.group_starts = group_starts;
+  p.shared_pages = shared_pages;
+  p.num_groups = num_groups;
+  p.prefix_blocks = shared_blocks(d, num_groups);
+  return enqueue_view(p, q, kv_pages, block_table, seq_lens, sm_scale, lse_base, out, lse, d, workspace, wl,
+                      f.sms, reinterpret_cast<cudaStream_t>(stream));
 }
 
 }  // extern "C"

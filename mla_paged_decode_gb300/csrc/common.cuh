@@ -90,6 +90,14 @@ struct DecodeParams {
   // slots ends just past its last owned token.  Otherwise strided = 0.
   int strided = 0, apg = 0;
   int s_q63 = 0, s_r63 = 0, s_c64 = 0;  // strided: 63 / P, 63 mod P, 64 mod P
+  // Views (tensor-core kernel, MULTI == 3; see ViewReq): 0 none, kViewWindow
+  // (window, sinks) or kViewShared (groups of requests with shared pages;
+  // `prefix_blocks` bounds the 64-row blocks of all groups).
+  int view = 0;
+  int window = 0, sinks = 0;
+  const int32_t *group_starts = nullptr;  // [num_groups + 1]
+  const int32_t *shared_pages = nullptr;  // [num_groups]
+  int num_groups = 0, prefix_blocks = 0;
   int kv_e4m3;
   float kv_scale;             // 1 for bf16
   float score_scale_log2;     // sm_scale * log2(e): scores kept in the base-2 domain
@@ -213,6 +221,112 @@ struct StridedMask {
   }
 };
 
+// ---------------------------------------------------------------- views
+//
+// A view is what a 64-row block of queries attends to: `tiles` pages of one
+// block-table row, first the `nsink` pages from page 0, then those from page
+// `first` on, up to token `end`.
+//
+// Window: virtual request v is head group v / B of request v mod B.  The
+// block sees its sinks and the pages from the first token of its first
+// query's window to its last query.
+//
+// Shared: the first prefix_blocks virtual requests are 64-row blocks of the
+// groups' rows over the shared pages, the others (request, head group) pairs
+// over the request's own pages.  Group g's blocks have ids block_base(g) and
+// up: rows / 64 rounded down at its first row, plus g, which leaves every
+// group at least the ids it needs (ceil(m / 64) <= floor((a + m) / 64) -
+// floor(a / 64) + 1); ids between are empty.
+constexpr int kViewWindow = 1, kViewShared = 2;
+
+struct ViewReq {
+  int tiles = 0;
+  int row0 = 0, rows = 0;  // first row of q / out / lse, rows of the block
+  int req = 0;             // block-table row
+  int first = 0, nsink = 0;
+  int end = 0;             // tokens from here on are not seen by any row
+  int lead = 0;            // window: tokens below are not seen, sinks aside
+  __device__ __forceinline__ int page(long long t) const {
+    return t < nsink ? int(t) : int(t) - nsink + first;
+  }
+  // tokens of tile t that some row sees, counted from the tile's start
+  __device__ __forceinline__ int seen(const DecodeParams &p, long long t) const {
+    const int base = page(t) * kPage;
+    return t < nsink ? min(kPage, p.sinks - base) : min(kPage, end - base);
+  }
+};
+
+__device__ __forceinline__ int group_start(const DecodeParams &p, int g) {
+  return min(max(p.group_starts[g], 0), p.batch);
+}
+__device__ __forceinline__ int block_base(const DecodeParams &p, int g) {
+  return int((long long)group_start(p, g) * p.heads / 64) + g;
+}
+__device__ __forceinline__ int group_shared_pages(const DecodeParams &p, int g) {
+  return min(max(p.shared_pages[g], 0), p.max_pages);
+}
+// The last group that starts at or before request b.
+__device__ __forceinline__ int group_of_request(const DecodeParams &p, int b) {
+  int lo = 0, hi = p.num_groups - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (p.group_starts[mid] <= b) lo = mid;
+    else hi = mid - 1;
+  }
+  return lo;
+}
+
+__device__ inline ViewReq view_req(const DecodeParams &p, int v) {
+  ViewReq r;
+  if (p.view == kViewShared && v < p.prefix_blocks) {
+    int lo = 0, hi = p.num_groups - 1;  // the last group whose blocks start at or before v
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (block_base(p, mid) <= v) lo = mid;
+      else hi = mid - 1;
+    }
+    const int b0 = group_start(p, lo), rows = (group_start(p, lo + 1) - b0) * p.heads;
+    const int k = v - block_base(p, lo);
+    if (k < 0 || 64 * k >= rows) return r;
+    r.row0 = b0 * p.heads + 64 * k;
+    r.rows = min(64, rows - 64 * k);
+    r.req = b0;
+    r.tiles = group_shared_pages(p, lo);
+    r.end = r.tiles * kPage;
+    return r;
+  }
+  const int u = p.view == kViewShared ? v - p.prefix_blocks : v;
+  const int b = u % p.batch, g = u / p.batch;
+  r.req = b;
+  r.row0 = b * p.heads + 64 * g;
+  r.rows = min(64, p.heads - 64 * g);
+  const int L = checked_len(p, b, nullptr);
+  r.end = group_len(p, L, g);
+  if (p.view == kViewShared) {
+    r.first = group_shared_pages(p, group_of_request(p, b));
+    r.tiles = max(0, (r.end + kPage - 1) / kPage - r.first);
+    return r;
+  }
+  if (r.end == 0) return r;
+  // the block's first query sits at position L - T + 64 g / q_heads
+  r.lead = max(0, L - p.q_len + (64 * g) / p.q_heads + 1 - p.window);
+  r.first = r.lead / kPage;
+  r.nsink = min((p.sinks + kPage - 1) / kPage, r.first);
+  r.tiles = r.nsink + (r.end + kPage - 1) / kPage - r.first;
+  return r;
+}
+
+// What row `row` (of all rows) of a block sees: tokens below `hi`, and of
+// those the ones from `lo` on or below the sinks.
+struct RowView {
+  int lo, hi;
+};
+__device__ __forceinline__ RowView row_view(const DecodeParams &p, const ViewReq &r, int row) {
+  const int b = min(row / p.heads, p.batch - 1);
+  const int pos = checked_len(p, b, nullptr) - p.q_len + (row - b * p.heads) / p.q_heads;
+  return RowView{p.view == kViewWindow ? max(0, pos + 1 - p.window) : 0, min(max(0, pos + 1), r.end)};
+}
+
 // Owned tokens of virtual request v (its group's widest row).
 // MULTI: rows may differ in the tokens they see (several query tokens, or an
 // owner mask); MULTI == 2: the strided gather, whose lengths count slots.  A
@@ -260,6 +374,7 @@ __device__ inline OwnerMask owner_mask_of(const DecodeParams &p) {
 
 template <int MULTI = 0>
 __device__ __forceinline__ int request_tiles(const DecodeParams &p, int v) {
+  if constexpr (MULTI == 3) return view_req(p, v).tiles;
   return (request_len<MULTI>(p, v, nullptr) + kTile - 1) / kTile;
 }
 
@@ -279,6 +394,12 @@ __device__ __forceinline__ int request_tiles(const DecodeParams &p, int v) {
 // split writes a normalised fp32 partial into slot 2c (the CTA's first
 // request) or 2c+1 (its last); the request's first CTA records {itself,
 // split count, its slot} and a second kernel merges the splits.
+
+// Virtual requests of a launch.
+template <int MULTI = 0>
+__device__ __forceinline__ int virtual_requests(const DecodeParams &p) {
+  return p.batch * p.head_groups + (MULTI == 3 ? p.prefix_blocks : 0);
+}
 
 struct CtaRange {
   long long start, end;   // cost range of this CTA
@@ -305,7 +426,7 @@ __device__ __forceinline__ long long request_cost(int tiles, int piece_cost) {
 // `scratch` needs blockDim.x / 32 + 1 long longs of shared memory.
 template <int MULTI = 0, int PC = kPieceCost>
 __device__ inline void cta_schedule(const DecodeParams &p, CtaRange *r, long long *scratch) {
-  const int V = p.batch * p.head_groups;
+  const int V = virtual_requests<MULTI>(p);
   const int tid = threadIdx.x, nw = blockDim.x / 32, lane = tid & 31, warp = tid >> 5;
   // pass 1: total cost
   long long mine = 0;

@@ -25,6 +25,7 @@ cudaError_t launch_decode_tc(const DecodeParams &p, int npv, int q_rows, int gro
   cudaError_t e = p.kv_e4m3 ? launch_tc_variants<true>(tp, tm_q, tm_kv, tm_kvg, tm_kvb, grid, stream)
                             : launch_tc_variants<false>(tp, tm_q, tm_kv, tm_kvg, tm_kvb, grid, stream);
   if (e != cudaSuccess) return e;
+  if (p.view == kViewShared) return launch_shared_merge(p, grid, stream);
   // all partitions in one launch: the split merge also combines the partitions
   return p.fused && p.comb_out ? launch_dcp_merge_combine(p, grid, stream)
                                : launch_split_merge(p, grid, stream);

@@ -56,6 +56,8 @@
 // every read of an input.
 #pragma once
 
+#include <type_traits>
+
 #include "common.cuh"
 #include "sm100.cuh"
 #include "splits.cuh"
@@ -184,6 +186,9 @@ constexpr int piece_cost() { return F8 ? kPieceCostE4m3 : kPieceCost; }
 // The requests (and tile ranges) this CTA owns, in order; every role walks it.
 // FUSED: all partitions in one launch (output row b = partition * B + input
 // request); otherwise one partition, p.part_id, and row b is request b.
+// MULTI == 3: the pieces are views (see ViewReq), one page a tile.
+struct NoView {};
+
 template <bool FUSED, int MULTI, int PC>
 struct Walk {
   const DecodeParams &p;
@@ -191,10 +196,20 @@ struct Walk {
   int V, v, b, g, n, tiles;
   int rb, part, pc;  // input request of output row b, its partition, the map's partition coordinate
   long long pv, t0, t1;
+  std::conditional_t<MULTI == 3, ViewReq, NoView> view;
   __device__ Walk(const DecodeParams &p_, const CtaRange &r_)
-      : p(p_), r(r_), V(p_.batch * p_.head_groups), v(r_.v_begin), pv(r_.p_begin) {}
+      : p(p_), r(r_), V(virtual_requests<MULTI>(p_)), v(r_.v_begin), pv(r_.p_begin) {}
   __device__ bool next() {
     while (v < V && pv < r.end) {
+      if constexpr (MULTI == 3) {
+        view = view_req(p, v);
+        tiles = view.tiles;
+        if (tiles == 0) { ++v; continue; }
+        t0 = max(r.start, pv) - pv;
+        t1 = min(r.end, pv + tiles) - pv;
+        rb = view.req;
+        return true;
+      }
       tiles = request_tiles<MULTI>(p, v);
       if (tiles == 0) { ++v; continue; }
       t0 = max(r.start, pv) - pv;
@@ -213,6 +228,20 @@ struct Walk {
     return false;
   }
   __device__ void advance() { pv += request_cost(tiles, PC); ++v; }
+  // the piece's rows: the first in q / out / lse, and their number (at most 64)
+  __device__ __forceinline__ int q_row0() const {
+    if constexpr (MULTI == 3) return view.row0;
+    return rb * p.heads + g * tc::kHeads;
+  }
+  __device__ __forceinline__ int rows() const {
+    if constexpr (MULTI == 3) return view.rows;
+    return min(tc::kHeads, p.heads - g * tc::kHeads);
+  }
+  // tokens of tile t that some row of the piece sees
+  __device__ __forceinline__ int seen(long long t) const {
+    if constexpr (MULTI == 3) return view.seen(p, t);
+    return min(kTile, n - int(t) * kTile);
+  }
 };
 
 // One position in the walk: request + tile.
@@ -234,7 +263,7 @@ struct TileCursor {
   }
   __device__ bool first() const { return t == w.t0; }
   __device__ bool last() const { return t == w.t1 - 1; }
-  __device__ int nv() const { return min(kTile, w.n - int(t) * kTile); }
+  __device__ int nv() const { return w.seen(t); }
 };
 
 __device__ __forceinline__ uint32_t bar_addr(uint64_t &b) { return smem_u32(&b); }
@@ -267,6 +296,17 @@ __device__ __forceinline__ bool lane_page(const DecodeParams &p, int part, long 
   *lp = lp0 + lane;
   *row0 = 0;
   return lane <= lp1 - lp0;
+}
+
+template <bool FUSED, int MULTI, int PC>
+__device__ __forceinline__ bool cursor_page(const DecodeParams &p, const TileCursor<FUSED, MULTI, PC> &c, int lane,
+                                            int *lp, int *row0) {
+  if constexpr (MULTI == 3) {
+    *lp = c.w.view.page(c.t);
+    *row0 = 0;
+    return lane == 0;
+  }
+  return lane_page<MULTI == 2>(p, c.w.part, c.t, c.w.n, lane, lp, row0);
 }
 
 // ------------------------------------------------------------------ producer
@@ -310,7 +350,7 @@ __device__ __forceinline__ void tc_producer(const TcParams &tp, const CtaRange &
     int pg = -1;
     if (ahead.live) {
       int lp, row0;
-      if (lane_page<STRIDED>(p, ahead.w.part, ahead.t, ahead.w.n, lane, &lp, &row0)) {
+      if (cursor_page(p, ahead, lane, &lp, &row0)) {
         pg = p.block_table[size_t(ahead.w.rb) * p.max_pages + lp];
         if (pg >= 0 && pg < p.num_pages) {
           if (F8 && STRIDED) {
@@ -350,15 +390,14 @@ __device__ __forceinline__ void tc_producer(const TcParams &tp, const CtaRange &
       if (lane == 0) mbar_arrive_expect_tx(bar_addr(m.q_full), uint32_t(kKb * tp.q_rows * 128));
       __syncwarp();
       if (lane < kKb)
-        tma_load_2d(sQ + lane * (64 * 128), tm_q, bar_addr(m.q_full), lane * 64,
-                    cur.w.rb * p.heads + cur.w.g * kHeads);
+        tma_load_2d(sQ + lane * (64 * 128), tm_q, bar_addr(m.q_full), lane * 64, cur.w.q_row0());
       last_q = q_it & 1;
       ++q_it;
     }
     if (F8 && cur.first()) checked_len(p, cur.w.rb, err);
     const int s = kv_it % NS;
     int lp, row0;
-    const bool mine = lane_page<STRIDED>(p, cur.w.part, cur.t, cur.w.n, lane, &lp, &row0);
+    const bool mine = cursor_page(p, cur, lane, &lp, &row0);
     int pg = ring[0];
     if (mine && (pg < 0 || pg >= p.num_pages)) {
       atomicOr(err, kErrBadPage);
@@ -722,11 +761,30 @@ static __device__ __noinline__ void zero_value_tail(unsigned char *stage, int nv
   }
 }
 
+// Value rows [r0, r1) of a stage (0 <= r0 < r1 <= 64), zeroed by the softmax
+// warpgroup (rank gt).
+template <bool F8, int KBG>
+static __device__ __noinline__ void zero_value_rows(unsigned char *stage, int r0, int r1, int gt) {
+  using namespace tc;
+  constexpr int kBlocks = F8 ? 4 : 8;  // 128-byte blocks of a value row
+  for (int i = gt; i < (r1 - r0) * kBlocks * 8; i += 128) {
+    const int rr = r0 + i / (kBlocks * 8), kb = (i >> 3) % kBlocks, ch = i & 7;
+    const uint32_t off = F8 ? kb * kFxBlkStride + (rr >> 3) * kFxAtomStride
+                            : kb_off<KBG>(kb) + (rr >> 3) * atom_stride<KBG>();
+    *reinterpret_cast<uint4 *>(stage + off + (rr & 7) * 128 + ch * 16) = make_uint4(0, 0, 0, 0);
+  }
+}
+
 template <bool F8, bool FUSED, int MULTI, int KBG>
 __device__ __forceinline__ void tc_softmax(const TcParams &tp, const CtaRange &r, TcMiscFor<F8> &m,
                            unsigned char *smem, uint32_t tmem, int *err) {
   using namespace tc;
   constexpr bool STRIDED = MULTI == 2;
+  constexpr bool VIEW = MULTI == 3;
+  // the sum that gives the LSE takes P before rounding (a bf16 cache's other
+  // variants take the rounded P: its error, up to 2^-9 of the LSE's argument,
+  // shows in the LSE of a short view)
+  constexpr bool XSUM = F8 || VIEW;
   constexpr int NS = num_stages<F8>();
   constexpr float kThreshold = F8 ? kFxRescaleThreshold : kRescaleThreshold;
   const DecodeParams &p = tp.p;
@@ -743,14 +801,14 @@ __device__ __forceinline__ void tc_softmax(const TcParams &tp, const CtaRange &r
   uint32_t kv_it = 0, p_it = 0, o_it = 0;
   bool ok = true;
   // an owner mask: the gathered tiles hold other partitions' tokens too
-  const bool masked = MULTI && p.own_parts > p.num_parts;
+  const bool masked = MULTI && !VIEW && p.own_parts > p.num_parts;
   OwnerMask own{};
   if (masked) own = owner_mask_of(p);
 
   uint32_t piece = 0;
   Walk<FUSED, MULTI, piece_cost<F8>()> w(p, r);
   for (; ok && w.next(); w.advance(), ++piece) {
-    const int hn = min(kHeads, p.heads - w.g * kHeads);
+    const int hn = w.rows();
     if (F8) {
       // Q's scale, written by warps 9..11 before the scores of this piece
       // were computed (its slot is checked against the request: bounded)
@@ -766,8 +824,13 @@ __device__ __forceinline__ void tc_softmax(const TcParams &tp, const CtaRange &r
     }
     // owned tokens each of this lane's two rows sees (all w.n unless a request
     // carries several query tokens, each with its own causal bound)
-    int nrow[2] = {w.n, w.n};
-    if (MULTI) {  // query token i of T sees the global tokens t < L - T + i + 1
+    int nrow[2] = {0, 0};
+    if constexpr (!VIEW) nrow[0] = nrow[1] = w.n;
+    RowView rv[2];  // views: what each of the two rows sees
+    if constexpr (VIEW) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) rv[h] = row_view(p, w.view, w.view.row0 + row[h]);
+    } else if (MULTI) {  // query token i of T sees the global tokens t < L - T + i + 1
       const int L = checked_len(p, w.rb, nullptr);
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
@@ -782,12 +845,12 @@ __device__ __forceinline__ void tc_softmax(const TcParams &tp, const CtaRange &r
     if (STRIDED) smask.start(p, w.part, w.t0);
     float mrun[2] = {-INFINITY, -INFINITY};  // running max (base-2 units) of each head
     float ellp[2] = {0.f, 0.f};              // this lane's share of each head's sum
-    float ellx[2] = {0.f, 0.f};              // e4m3: the same of P before rounding
+    float ellx[2] = {0.f, 0.f};              // XSUM: the same of P before rounding
     for (long long t = w.t0; t < w.t1; ++t, ++kv_it, ++p_it) {
       const int s = kv_it & 1;          // S buffer
       const int st = kv_it % NS;        // shared-memory stage
       const uint32_t ph = (kv_it >> 1) & 1;
-      const int nv = min(kTile, w.n - int(t) * kTile);
+      const int nv = w.seen(t);
       // Every wait of the warpgroup is followed by a group vote, so that a
       // wait that gave up in one warp never strands the others at a barrier.
       bool got = __all_sync(0xffffffffu, mbar_wait(bar_addr(m.s_full[s]), ph, abort, kTimeoutNs));
@@ -808,8 +871,23 @@ __device__ __forceinline__ void tc_softmax(const TcParams &tp, const CtaRange &r
         __syncwarp();
         if (lane == 0) mbar_arrive(bar_addr(m.s_free[s]));
       }
+      if constexpr (VIEW) {  // rows that do not see the whole tile
+        const int base = w.view.page(t) * kPage, sink = p.sinks - base;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int hi = rv[h].hi - base, lo = rv[h].lo - base;
+          if (hi < kTile || (lo > 0 && sink < kTile)) {
+#pragma unroll
+            for (int k = h; k < 16; k += 2) {
+              const int tok = 8 * (k >> 1) + pair;
+              xp[k].x = tok < hi && (tok >= lo || tok < sink) ? xp[k].x : -INFINITY;
+              xp[k].y = tok + 1 < hi && (tok + 1 >= lo || tok + 1 < sink) ? xp[k].y : -INFINITY;
+            }
+          }
+        }
+      }
       const int nv0 = MULTI ? nrow[0] - int(t) * kTile : nv, nv1 = MULTI ? nrow[1] - int(t) * kTile : nv;
-      if ((MULTI ? min(nv0, nv1) : nv) < kTile) {  // the tile's tail: tokens past a row's last visible one
+      if (!VIEW && (MULTI ? min(nv0, nv1) : nv) < kTile) {  // the tile's tail: tokens past a row's last visible one
 #pragma unroll
         for (int k = 0; k < 16; ++k) {
           const int tok = 8 * (k >> 1) + pair, lim = (k & 1) ? nv1 : nv0;
@@ -927,22 +1005,32 @@ __device__ __forceinline__ void tc_softmax(const TcParams &tp, const CtaRange &r
           // a row that has seen no token yet keeps a -inf max: its P is 0
           const float mref = MULTI && mnew[h] == -INFINITY ? 0.f : mnew[h];
           const float2 c2 = make_float2(cs, cs), m2 = make_float2(-mref, -mref);
-          float2 lsum = make_float2(0.f, 0.f);
+          float2 lsum = make_float2(0.f, 0.f), xsum = make_float2(0.f, 0.f);
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
             const float2 arg = fma2(xp[2 * j + h], c2, m2);
             const float e0 = ex2(arg.x), e1 = ex2(arg.y);
+            if (XSUM) xsum = add2(xsum, make_float2(e0, e1));
             __nv_bfloat162 v = __floats2bfloat162_rn(e0, e1);
             const uint32_t bits = *reinterpret_cast<uint32_t *>(&v);
             lsum = add2(lsum, make_float2(__uint_as_float(bits << 16), __uint_as_float(bits & 0xffff0000u)));
             *reinterpret_cast<uint32_t *>(prow + ((j ^ (row[h] & 7)) << 4)) = bits;
           }
           ellp[h] = ellp[h] * alpha[h] + (lsum.x + lsum.y);
+          if (XSUM) ellx[h] = ellx[h] * alpha[h] + (xsum.x + xsum.y);
           mrun[h] = mnew[h];
         }
         // rows [nv, roundup16(nv)) of V are read by the last PV step but hold no
         // owned token (stale or unowned data): zero their 512 value dims
         if (nv & 15) zero_value_tail<KBG>(smem + kOffKv + s * kStageBytes, nv, gt);
+      }
+      if constexpr (VIEW) {
+        // a window's first page: rows before it (unless they are sinks) have
+        // P = 0, and whatever they hold must not reach the product
+        const int base = w.view.page(t) * kPage, lead = min(w.view.lead - base, nv);
+        const int sunk = max(0, p.sinks - base);
+        if (t >= w.view.nsink && sunk < lead)
+          zero_value_rows<F8, KBG>(smem + off_kv<F8>() + st * stage_bytes<F8>(), sunk, lead, gt);
       }
       fence_proxy_async_smem();
       tc_fence_before();
@@ -957,7 +1045,7 @@ __device__ __forceinline__ void tc_softmax(const TcParams &tp, const CtaRange &r
     for (int h = 0; h < 2; ++h) {
       ell[h] = ellp[h] + __shfl_xor_sync(0xffffffffu, ellp[h], 1);
       ell[h] += __shfl_xor_sync(0xffffffffu, ell[h], 2);
-      if (F8) {
+      if (XSUM) {
         elx[h] = ellx[h] + __shfl_xor_sync(0xffffffffu, ellx[h], 1);
         elx[h] += __shfl_xor_sync(0xffffffffu, elx[h], 2);
       } else {
@@ -972,9 +1060,20 @@ __device__ __forceinline__ void tc_softmax(const TcParams &tp, const CtaRange &r
     const bool got_o = mbar_wait(bar_addr(m.o_full), o_it & 1, abort, kTimeoutNs);
     if (!named_sync_and(2, 128, got_o)) { ok = false; break; }
     tc_fence_after();
-    const SplitInfo si = split_info(r, w.v, w.pv, w.tiles);
-    const bool split = si.nsplits > 1;
-    const size_t out_row0 = size_t(w.b) * p.heads + size_t(w.g) * kHeads;
+    SplitInfo si = split_info(r, w.v, w.pv, w.tiles);
+    bool split = si.nsplits > 1;
+    size_t out_row0;
+    if constexpr (VIEW) {
+      out_row0 = w.view.row0;
+      // shared pages: every piece leaves a partial, in the slot of its CTA
+      // and virtual request (both grow along the walk, so the sum is its own)
+      if (p.view == kViewShared) {
+        split = true;
+        si.slot = int(blockIdx.x) + w.v;
+      }
+    } else {
+      out_row0 = size_t(w.b) * p.heads + size_t(w.g) * kHeads;
+    }
     // This warp owns value dims 128c + 32q .. + 31 of each chunk c (its TMEM
     // lanes).  Values go through a 2 KB per-warp buffer, transposed to
     // [head][dim], so that each lane stores 16-byte runs of dims: 8 (bf16)
@@ -1072,9 +1171,8 @@ __device__ __forceinline__ uint32_t piece_q_max(const DecodeParams &p,
                                                 TcMisc<3> &m, int ct) {
   using namespace tc;
   constexpr int kRowChunks = kDqk / 8;
-  const int hn = min(kHeads, p.heads - w.g * kHeads), n = hn * kRowChunks;
-  const uint4 *qg =
-      reinterpret_cast<const uint4 *>(p.q + (size_t(w.rb) * p.heads + size_t(w.g) * kHeads) * kDqk);
+  const int hn = w.rows(), n = hn * kRowChunks;
+  const uint4 *qg = reinterpret_cast<const uint4 *>(p.q + size_t(w.q_row0()) * kDqk);
   uint32_t mx = 0;
   for (int i0 = ct; i0 < n; i0 += 16 * kConvThreads) {
     uint4 v[16];
@@ -1124,9 +1222,8 @@ __device__ __forceinline__ void tc_split_q(const TcParams &tp, const CtaRange &r
   for (; w.next(); w.advance(), ++q_it) {
     const bool got = mbar_wait(bar_addr(m.q_empty), (q_it & 1) ^ 1, abort, kTimeoutNs);
     if (!named_sync_and(3, kConvThreads, got)) { ok = false; break; }
-    const int hn = min(kHeads, p.heads - w.g * kHeads);
-    const uint4 *qg =
-        reinterpret_cast<const uint4 *>(p.q + (size_t(w.rb) * p.heads + size_t(w.g) * kHeads) * kDqk);
+    const int hn = w.rows();
+    const uint4 *qg = reinterpret_cast<const uint4 *>(p.q + size_t(w.q_row0()) * kDqk);
     // |q| bits are ordered like magnitudes; an Inf or NaN keeps k = 0
     int k = 0;
     if (mx < 0x7f80u) k = min(126, max(-126, 134 - int(mx >> 7)));
@@ -1288,6 +1385,7 @@ __global__ void __launch_bounds__(tc_threads<F8>(), 1)
 
 cudaError_t launch_split_merge(const DecodeParams &p, int grid, cudaStream_t stream);
 cudaError_t launch_dcp_merge_combine(const DecodeParams &p, int grid, cudaStream_t stream);
+cudaError_t launch_shared_merge(const DecodeParams &p, int grid, cudaStream_t stream);
 
 template <bool F8, bool FUSED, int MULTI, int AHEAD>
 static cudaError_t launch_tc(const TcParams &tp, const CUtensorMap &tm_q, const CUtensorMap &tm_kv,
@@ -1318,6 +1416,7 @@ template <bool F8>
 cudaError_t launch_tc_variants(const TcParams &tp, const CUtensorMap &tm_q,
                                const CUtensorMap &tm_kv, const CUtensorMap &tm_kvg,
                                const CUtensorMap &tm_kvb, int grid, cudaStream_t stream) {
+  if (tp.p.view) return launch_tc<F8, false, 3, F8 ? 2 : 1>(tp, tm_q, tm_kv, tm_kvg, tm_kvb, grid, stream);
   if (tp.p.strided)
     return tp.p.fused ? launch_tc<F8, true, 2, 2>(tp, tm_q, tm_kv, tm_kvg, tm_kvb, grid, stream)
                       : launch_tc<F8, false, 2, 2>(tp, tm_q, tm_kv, tm_kvg, tm_kvb, grid, stream);

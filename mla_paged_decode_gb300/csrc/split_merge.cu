@@ -209,6 +209,91 @@ __global__ void __launch_bounds__(kDcpMaxParts * 32) dcp_merge_combine_kernel(De
   }
 }
 
+// Shared pages: a row's partials are those of its group's block over the
+// shared pages and those of its request over its own.  One warp per row, each
+// lane 16 value dims; the LSE-weighted combine of all of them.
+__global__ void __launch_bounds__(kMergeWarps * 32, 7) shared_merge_kernel(DecodeParams p, int slots) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int lane = threadIdx.x & 31;
+  const int row = blockIdx.x * kMergeWarps + (threadIdx.x >> 5);
+  if (row >= p.batch * p.heads) return;
+  const int b = row / p.heads, r = row - b * p.heads;
+  const int g = group_of_request(p, b);
+  const int local = row - group_start(p, g) * p.heads;
+  int first[2] = {0, 0}, num[2] = {0, 0}, hl[2] = {local & 63, r & 63};  // slots of the two sets, row in them
+  const int vp = block_base(p, g) + (local >> 6), vt = p.prefix_blocks + (r >> 6) * p.batch + b;
+  if (local >= 0 && vp < p.prefix_blocks) {
+    const int4 i = info_ptr(p)[vp];
+    if (i.y > 0 && i.z >= 0 && i.z + i.y <= slots) first[0] = i.z, num[0] = i.y;
+  }
+  {
+    const int4 i = info_ptr(p)[vt];
+    if (i.y > 0 && i.z >= 0 && i.z + i.y <= slots) first[1] = i.z, num[1] = i.y;
+  }
+  const int ns = num[0] + num[1];
+  const float *sl = slot_lse_ptr(p);
+  const float *so = slot_out_ptr(p);
+  auto at = [&](int k) {
+    const int s = k >= num[0];
+    return size_t(first[s] + (s ? k - num[0] : k)) * kSlotHeads + hl[s];
+  };
+  float mx = -INFINITY;
+  for (int k = lane; k < ns; k += 32) mx = fmaxf(mx, sl[at(k)]);
+  for (int o = 16; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+  const float mref = mx == -INFINITY ? 0.f : mx;
+  float4 acc[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+  float sum = 0.f;
+  for (int k0 = 0; k0 < ns; k0 += kMergeBatch) {
+    float4 x[kMergeBatch][4];
+    float w[kMergeBatch];
+#pragma unroll
+    for (int u = 0; u < kMergeBatch; ++u) {
+      const bool in = k0 + u < ns;
+      const size_t a = at(in ? k0 + u : k0);
+      w[u] = in ? exp2f(sl[a] - mref) : 0.f;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) x[u][i] = reinterpret_cast<const float4 *>(so + a * kDv)[4 * lane + i];
+    }
+#pragma unroll
+    for (int u = 0; u < kMergeBatch; ++u) {
+      sum += w[u];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        acc[i].x += w[u] * x[u][i].x; acc[i].y += w[u] * x[u][i].y;
+        acc[i].z += w[u] * x[u][i].z; acc[i].w += w[u] * x[u][i].w;
+      }
+    }
+  }
+  const float inv = sum > 0.f ? 1.f / sum : 0.f;
+  uint32_t pk[8];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    __nv_bfloat162 lo = __floats2bfloat162_rn(acc[i].x * inv, acc[i].y * inv);
+    __nv_bfloat162 hi = __floats2bfloat162_rn(acc[i].z * inv, acc[i].w * inv);
+    pk[2 * i] = *reinterpret_cast<uint32_t *>(&lo);
+    pk[2 * i + 1] = *reinterpret_cast<uint32_t *>(&hi);
+  }
+  store_row(p.out + size_t(row) * kDv, pk);
+  if (lane == 0) p.lse[row] = sum > 0.f ? lse_out(p, mref + log2f(sum)) : -INFINITY;
+}
+
+cudaError_t launch_shared_merge(const DecodeParams &p, int grid, cudaStream_t stream) {
+  const int rows = p.batch * p.heads;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((rows + kMergeWarps - 1) / kMergeWarps);
+  cfg.blockDim = dim3(kMergeWarps * 32);
+  cfg.dynamicSmemBytes = 0;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, shared_merge_kernel, p, p.batch * p.head_groups + p.prefix_blocks + grid);
+}
+
 cudaError_t launch_split_merge(const DecodeParams &p, int grid, cudaStream_t stream) {
   const int V = p.batch * p.head_groups;
   if (V == 0) return cudaSuccess;

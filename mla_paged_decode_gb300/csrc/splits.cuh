@@ -39,14 +39,42 @@ __device__ __forceinline__ float lse_out(const DecodeParams &p, float lse2) {
   return p.lse_base2 ? lse2 : lse2 * kLn2;
 }
 
+// Flags what is out of range in the inputs of virtual request v of a view:
+// a request's length, a group's pages, a request outside its group.
+__device__ __forceinline__ void check_view(const DecodeParams &p, int v, int *err) {
+  if (p.view == kViewShared) {
+    if (v < p.prefix_blocks) return;
+    v -= p.prefix_blocks;
+    if (v < p.batch) {
+      const int g = group_of_request(p, v);
+      const bool in = p.group_starts[g] <= v && v < p.group_starts[g + 1];
+      if (!in || p.shared_pages[g] < 0 || p.shared_pages[g] > p.max_pages) atomicOr(err, kErrBadLen);
+    }
+  }
+  checked_len(p, v % p.batch, err);
+}
+
 // The neutral pair (0, -inf) for every virtual request with no owned token,
 // and its split record {-1, 0, 0} (no splits), so that every record is
 // rewritten by each call and the merge reads no lengths.  Virtual request v
 // is handled by CTA v mod gridDim.x.  Block-wide.
 template <int MULTI = 0>
 __device__ inline void write_empty_requests(const DecodeParams &p) {
-  const int V = p.batch * p.head_groups;
+  const int V = virtual_requests<MULTI>(p);
   int *err = error_word(p);
+  if constexpr (MULTI == 3) {
+    for (int v = blockIdx.x; v < V; v += gridDim.x) {
+      const ViewReq r = view_req(p, v);
+      if (threadIdx.x == 0) check_view(p, v, err);
+      if (r.tiles != 0) continue;
+      if (threadIdx.x == 0) info_ptr(p)[v] = make_int4(-1, 0, 0, 0);
+      if (p.view == kViewShared) continue;  // the merge writes every row
+      uint4 *dst = reinterpret_cast<uint4 *>(p.out + size_t(r.row0) * kDv);
+      for (int i = threadIdx.x; i < r.rows * kDv / 8; i += blockDim.x) dst[i] = make_uint4(0, 0, 0, 0);
+      for (int i = threadIdx.x; i < r.rows; i += blockDim.x) p.lse[size_t(r.row0) + i] = -INFINITY;
+    }
+    return;
+  }
   for (int v = blockIdx.x; v < V; v += gridDim.x) {
     int b = vreq_row(p, v), g = vreq_group(p, v);  // b: output row
     if (request_len<MULTI>(p, v, threadIdx.x == 0 ? err : nullptr) != 0) continue;
