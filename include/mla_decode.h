@@ -372,6 +372,7 @@ int mla_lse_combine(const void *partials, const float *lses, int num_parts, void
  *
  *  window      tokens of the sliding window, the query's own among them (>= 1).
  *  sinks       first tokens that stay visible (>= 0).
+ *  sm_scale    finite and > 0.
  *  all others  as for mla_decode_partial with num_parts = 1, the workspace of
  *              mla_decode_workspace_size included (q_len 1..16).
  *
@@ -403,14 +404,16 @@ int mla_decode_window(const void *q, const void *kv_pages, const int32_t *block_
  *               than its group's shared pages sees its own tokens only.
  *  workspace    >= mla_decode_shared_workspace_size(d, num_groups, 0) bytes,
  *               same rules as for mla_decode_partial.
+ *  sm_scale     finite and > 0.
  *  all others   as for mla_decode_partial with num_parts = 1.
  *
  * The rows of a group (q_len x num_heads of each of its requests) attend to
- * the shared pages in blocks of 64, each request's rows to its own pages, and
- * the partial results are merged by their LSE.  A request outside every group
+ * the shared pages in blocks, each request's rows to its own pages, and the
+ * partial results are merged by their LSE.  A bf16 cache whose groups have 128
+ * rows or more on average takes blocks of 128 rows on pairs of SMs.  A request outside every group
  * or a page number outside [0, max_pages_per_seq] is reported as
  * MLA_ERR_BOUNDS by mla_decode_check_workspace.  Arithmetic as for
- * mla_decode_window.  Two kernels.
+ * mla_decode_window.  Two or three kernels.
  */
 size_t mla_decode_shared_workspace_size(const mla_decode_desc *d, int num_groups, int num_sms);
 

@@ -30,6 +30,8 @@ cudaError_t launch_decode_tc(const DecodeParams &p, int npv, int q_rows, int gro
                              const CUtensorMap &tm_q, const CUtensorMap &tm_kv,
                              const CUtensorMap &tm_kvg, const CUtensorMap &tm_kvb, int grid,
                              cudaStream_t stream);
+cudaError_t launch_decode_pair(const DecodeParams &p, const CUtensorMap &tm_q, const CUtensorMap &tm_k,
+                               const CUtensorMap &tm_v, cudaStream_t stream);
 cudaError_t launch_lse_combine(const void *partials, const float *lses, int num_parts, void *out,
                                float *out_lse, int rows, int dim, int base2, cudaStream_t stream);
 int combine_max_parts();
@@ -308,6 +310,30 @@ int make_tensor_maps(const void *q, const void *kv, const mla_decode_desc *d, in
   return MLA_OK;
 }
 
+// The pair kernel's loads of a bf16 cache, on (64 dims, 8 rows, 9 blocks of 64
+// dims, 8-row groups): one dim block of a page's 64 rows (K), four dim blocks
+// of half a page (V).
+int make_pair_maps(const void *kv, const mla_decode_desc *d, CUtensorMap *tm_k, CUtensorMap *tm_v) {
+  EncodeTiled enc = encode_tiled();
+  if (!enc) {
+    std::snprintf(g_cuda_error, sizeof(g_cuda_error), "cuTensorMapEncodeTiled unavailable");
+    return MLA_ERR_CUDA;
+  }
+  const cuuint64_t row = cuuint64_t(mla::kDqk) * 2;
+  cuuint64_t dims[4] = {64, 8, cuuint64_t(mla::kDqk / 64), cuuint64_t(d->num_pages) * 8};
+  cuuint64_t strides[3] = {row, 128, 8 * row};
+  cuuint32_t box_k[4] = {64, 8, 1, 8}, box_v[4] = {64, 8, 4, 4}, es[4] = {1, 1, 1, 1};
+  CUresult r = enc(tm_k, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(kv), dims, strides, box_k, es,
+                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return tensor_map_fail("kv pair K", r);
+  r = enc(tm_v, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(kv), dims, strides, box_v, es,
+          CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return tensor_map_fail("kv pair V", r);
+  return MLA_OK;
+}
+
 constexpr int kSimtHeadsPerGroup = 32;
 // Query tokens per request: several (multi-token prediction / target verify)
 // only on the tensor-core path; the CUDA-core kernel takes one.
@@ -465,8 +491,15 @@ int enqueue_view(mla::DecodeParams p, const void *q, const void *kv_pages, const
   const long long most = p.view == mla::kViewShared ? (long long)d->batch * rows : rows;
   const int h = int(most < kTcHeadsPerGroup ? most : kTcHeadsPerGroup);
   CUtensorMap tm_q, tm_kv, tm_kvg, tm_kvb;
-  const int st = make_tensor_maps(q, kv_pages, d, h, 0, 1, false, false, &tm_q, &tm_kv, &tm_kvg, &tm_kvb);
+  int st = make_tensor_maps(q, kv_pages, d, h, 0, 1, false, false, &tm_q, &tm_kv, &tm_kvg, &tm_kvb);
   if (st != MLA_OK) return st;
+  if (p.pair_blocks) {
+    CUtensorMap tm_k, tm_v;
+    st = make_pair_maps(kv_pages, d, &tm_k, &tm_v);
+    if (st != MLA_OK) return st;
+    const cudaError_t e = mla::launch_decode_pair(p, tm_q, tm_k, tm_v, s);
+    if (e != cudaSuccess) return cuda_fail(e);
+  }
   const cudaError_t e = mla::launch_decode_tc(p, (h + 15) / 16 * 16, h, 8, tm_q, tm_kv, tm_kvg, tm_kvb, grid, s);
   return e == cudaSuccess ? MLA_OK : cuda_fail(e);
 }
@@ -476,7 +509,7 @@ int check_view_call(const void *q, const void *kv_pages, const int32_t *block_ta
                     float sm_scale, int lse_base, const void *out, const float *lse,
                     const mla_decode_desc *d, const void *workspace) {
   if (lse_base != MLA_LSE_NATURAL && lse_base != MLA_LSE_BASE2) return MLA_ERR_ARG;
-  if (!std::isfinite(sm_scale)) return MLA_ERR_ARG;
+  if (!(std::isfinite(sm_scale) && sm_scale > 0.f)) return MLA_ERR_ARG;
   if ((long long)d->batch * rows_of(d) > (1LL << 30)) return MLA_ERR_SHAPE;
   if (d->batch == 0) return MLA_OK;
   if (!q || !kv_pages || !block_table || !seq_lens || !out || !lse || !workspace) return MLA_ERR_NULL;
@@ -486,15 +519,23 @@ int check_view_call(const void *q, const void *kv_pages, const int32_t *block_ta
   return MLA_OK;
 }
 
-// Shared pages: 64-row blocks of all groups' rows (an upper bound known on
-// the host), and the workspace with a slot for every (virtual request, CTA).
-int shared_blocks(const mla_decode_desc *d, int num_groups) {
-  return int((long long)d->batch * rows_of(d) / kTcHeadsPerGroup) + num_groups;
+// Shared pages: blocks of `rows` rows of all groups (an upper bound known on
+// the host), and the workspace: a record for every virtual request, and slots
+// for every (virtual request, CTA) -- two for every (block, pair) -- enough
+// for either kernel of the shared pages.
+int shared_blocks(const mla_decode_desc *d, int num_groups, int rows) {
+  return int((long long)d->batch * rows_of(d) / rows) + num_groups;
 }
 mla::WorkspaceLayout shared_layout(const mla_decode_desc *d, int num_groups, int grid) {
   const int groups = (rows_of(d) + kTcHeadsPerGroup - 1) / kTcHeadsPerGroup;
-  const int v = shared_blocks(d, num_groups) + d->batch * groups;
-  return mla::workspace_layout(v, (v + grid + 1) / 2);
+  const int v = shared_blocks(d, num_groups, 64) + d->batch * groups;
+  // 2 (blocks of 128 rows + grid / 2) <= blocks of 64 rows + num_groups + grid
+  return mla::workspace_layout(v + num_groups, (v + num_groups + 2 * grid + 1) / 2);
+}
+// The pair kernel takes the shared pages of a bf16 cache when the groups fill
+// its blocks of 128 rows on average.
+bool pair_path(const mla_decode_desc *d, int num_groups) {
+  return d->kv_dtype == MLA_KV_BF16 && (long long)d->batch * rows_of(d) >= 128LL * num_groups;
 }
 constexpr int kMaxGroups = 1 << 20;
 constexpr int kMaxView = 1 << 30;
@@ -880,7 +921,12 @@ int mla_decode_shared(const void *q, const void *kv_pages, const int32_t *block_
   p.group_starts = group_starts;
   p.shared_pages = shared_pages;
   p.num_groups = num_groups;
-  p.prefix_blocks = shared_blocks(d, num_groups);
+  if (pair_path(d, num_groups)) {
+    p.pair_blocks = shared_blocks(d, num_groups, 128);
+    p.pairs = f.sms / 2;
+  } else {
+    p.prefix_blocks = shared_blocks(d, num_groups, 64);
+  }
   return enqueue_view(p, q, kv_pages, block_table, seq_lens, sm_scale, lse_base, out, lse, d, workspace, wl,
                       f.sms, reinterpret_cast<cudaStream_t>(stream));
 }

@@ -98,6 +98,9 @@ struct DecodeParams {
   const int32_t *group_starts = nullptr;  // [num_groups + 1]
   const int32_t *shared_pages = nullptr;  // [num_groups]
   int num_groups = 0, prefix_blocks = 0;
+  // Shared pages attended by the pair kernel (csrc/decode_pair.cu) in
+  // pair_blocks blocks of 128 rows on `pairs` CTA pairs; prefix_blocks is then 0.
+  int pair_blocks = 0, pairs = 0;
   int kv_e4m3;
   float kv_scale;             // 1 for bf16
   float score_scale_log2;     // sm_scale * log2(e): scores kept in the base-2 domain
@@ -259,8 +262,9 @@ struct ViewReq {
 __device__ __forceinline__ int group_start(const DecodeParams &p, int g) {
   return min(max(p.group_starts[g], 0), p.batch);
 }
+template <int R = 64>
 __device__ __forceinline__ int block_base(const DecodeParams &p, int g) {
-  return int((long long)group_start(p, g) * p.heads / 64) + g;
+  return int((long long)group_start(p, g) * p.heads / R) + g;
 }
 __device__ __forceinline__ int group_shared_pages(const DecodeParams &p, int g) {
   return min(max(p.shared_pages[g], 0), p.max_pages);
@@ -276,25 +280,30 @@ __device__ __forceinline__ int group_of_request(const DecodeParams &p, int b) {
   return lo;
 }
 
-__device__ inline ViewReq view_req(const DecodeParams &p, int v) {
+// Block v of R rows over a group's shared pages.
+template <int R = 64>
+__device__ inline ViewReq shared_block(const DecodeParams &p, int v) {
   ViewReq r;
-  if (p.view == kViewShared && v < p.prefix_blocks) {
-    int lo = 0, hi = p.num_groups - 1;  // the last group whose blocks start at or before v
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) >> 1;
-      if (block_base(p, mid) <= v) lo = mid;
-      else hi = mid - 1;
-    }
-    const int b0 = group_start(p, lo), rows = (group_start(p, lo + 1) - b0) * p.heads;
-    const int k = v - block_base(p, lo);
-    if (k < 0 || 64 * k >= rows) return r;
-    r.row0 = b0 * p.heads + 64 * k;
-    r.rows = min(64, rows - 64 * k);
-    r.req = b0;
-    r.tiles = group_shared_pages(p, lo);
-    r.end = r.tiles * kPage;
-    return r;
+  int lo = 0, hi = p.num_groups - 1;  // the last group whose blocks start at or before v
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (block_base<R>(p, mid) <= v) lo = mid;
+    else hi = mid - 1;
   }
+  const int b0 = group_start(p, lo), rows = (group_start(p, lo + 1) - b0) * p.heads;
+  const int k = v - block_base<R>(p, lo);
+  if (k < 0 || R * k >= rows) return r;
+  r.row0 = b0 * p.heads + R * k;
+  r.rows = min(R, rows - R * k);
+  r.req = b0;
+  r.tiles = group_shared_pages(p, lo);
+  r.end = r.tiles * kPage;
+  return r;
+}
+
+__device__ inline ViewReq view_req(const DecodeParams &p, int v) {
+  if (p.view == kViewShared && v < p.prefix_blocks) return shared_block(p, v);
+  ViewReq r;
   const int u = p.view == kViewShared ? v - p.prefix_blocks : v;
   const int b = u % p.batch, g = u / p.batch;
   r.req = b;
@@ -422,15 +431,16 @@ __device__ __forceinline__ long long request_cost(int tiles, int piece_cost) {
   return tiles > 0 ? tiles + piece_cost : 0;
 }
 
-// Block-wide: computes this CTA's range.  All threads must call it.
-// `scratch` needs blockDim.x / 32 + 1 long longs of shared memory.
-template <int MULTI = 0, int PC = kPieceCost>
-__device__ inline void cta_schedule(const DecodeParams &p, CtaRange *r, long long *scratch) {
-  const int V = virtual_requests<MULTI>(p);
+// Block-wide: computes worker `idx`'s range of V requests over `workers`
+// workers.  All threads must call it.  `scratch` needs blockDim.x / 32 + 1
+// long longs of shared memory.
+template <int PC, typename Tiles>
+__device__ __forceinline__ void schedule_range(int V, int idx, int workers, Tiles tiles_of, CtaRange *r,
+                                               long long *scratch) {
   const int tid = threadIdx.x, nw = blockDim.x / 32, lane = tid & 31, warp = tid >> 5;
   // pass 1: total cost
   long long mine = 0;
-  for (int v = tid; v < V; v += blockDim.x) mine += request_cost(request_tiles<MULTI>(p, v), PC);
+  for (int v = tid; v < V; v += blockDim.x) mine += request_cost(tiles_of(v), PC);
   for (int o = 16; o; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
   if (lane == 0) scratch[warp] = mine;
   __syncthreads();
@@ -438,12 +448,12 @@ __device__ inline void cta_schedule(const DecodeParams &p, CtaRange *r, long lon
     long long C = 0;
     for (int w = 0; w < nw; ++w) C += scratch[w];
     r->total = C;
-    r->g_eff = int(C < (long long)gridDim.x ? C : (long long)gridDim.x);
+    r->g_eff = int(C < (long long)workers ? C : (long long)workers);
     r->v_begin = V;
     r->p_begin = 0;
-    if (r->g_eff > 0 && (int)blockIdx.x < r->g_eff) {
-      r->start = sched_start(blockIdx.x, C, r->g_eff);
-      r->end = sched_start(blockIdx.x + 1, C, r->g_eff);
+    if (r->g_eff > 0 && idx < r->g_eff) {
+      r->start = sched_start(idx, C, r->g_eff);
+      r->end = sched_start(idx + 1, C, r->g_eff);
     } else {
       r->start = r->end = 0;
     }
@@ -456,7 +466,7 @@ __device__ inline void cta_schedule(const DecodeParams &p, CtaRange *r, long lon
   long long base = 0;
   for (int v0 = 0; v0 < V; v0 += blockDim.x) {
     int v = v0 + tid;
-    const int tiles = v < V ? request_tiles<MULTI>(p, v) : 0;
+    const int tiles = v < V ? tiles_of(v) : 0;
     const long long cst = request_cost(tiles, PC);
     long long incl = cst;
     for (int o = 1; o < 32; o <<= 1) {
@@ -481,6 +491,13 @@ __device__ inline void cta_schedule(const DecodeParams &p, CtaRange *r, long lon
     if (r->v_begin < V) break;  // uniform: read after the barrier
   }
   __syncthreads();
+}
+
+// This CTA's range of a launch whose workers are its CTAs.
+template <int MULTI = 0, int PC = kPieceCost>
+__device__ inline void cta_schedule(const DecodeParams &p, CtaRange *r, long long *scratch) {
+  schedule_range<PC>(virtual_requests<MULTI>(p), int(blockIdx.x), int(gridDim.x),
+                     [&](int v) { return request_tiles<MULTI>(p, v); }, r, scratch);
 }
 
 // ---------------------------------------------------------------- conversions

@@ -1,0 +1,567 @@
+// Shared-prefix attention on CTA pairs: the rows of a group (all heads and
+// query tokens of its requests) over the pages they share, bf16.
+//
+// The product is [rows x 576] x [576 x tokens] and [rows x tokens] x [tokens x
+// 512]: 2176 flops per row and cached token, compute bound from about 150 rows
+// on.  O for 128 rows is 128 x 512 fp32, all of an SM's TMEM, so a pair of
+// CTAs holds one block of 128 rows, 64 each (cta_group::2, M = 128): O takes
+// 256 columns and two S buffers of 256 tokens the other 256, and each SM's
+// shared memory supplies half of the B operand, so that the tensor cores see
+// N = 256 (6 KB of operands per 64 cycles; one CTA at M = N = 64 reads 4 KB per
+// 32 and starves).  In this shape each SM holds its 64 rows in all 128 TMEM
+// lanes: lanes 0..63 columns 0 .. N/2 - 1, lanes 64..127 the others.
+//
+// Per tile of 256 tokens (4 pages), CTA r of the pair loads
+//   K: pages 2r, 2r + 1, nine units of 64 dims x 128 tokens (its half of N);
+//   V: dims 256r .. 256r + 255 of all four pages, eight units of 32 tokens
+//      (its half of N of the two PV products),
+// 17 units of 16 KB through one ring of seven; a page is read twice, from L2.
+//
+// Roles (384 threads): warp 0 producer, warp 1 score MMAs and TMEM, warp 2 PV
+// MMAs (both in the even CTA only), warps 4..11 softmax and epilogue.  Thread
+// (lane l of TMEM, half g) handles the 64 tokens of page 2 (l / 64) + g for row
+// l mod 64: four threads share a row, and exchange their maxima through shared
+// memory once a tile.  O is rescaled only when a row's maximum grew by more
+// than 2^8, as in the decode kernel.  Per tile i: S_i -> softmax -> P_i (one
+// buffer, free when PV_{i-1} is done) -> PV_i, while S_{i+1} runs.
+//
+// Work is split as in the decode kernel: the tiles of all blocks in one line,
+// cut into equal ranges, one per pair; every piece leaves an fp32 partial.
+#include "common.cuh"
+#include "sm100.cuh"
+#include "splits.cuh"
+
+namespace mla {
+using namespace sm100;
+
+namespace pair {
+constexpr int kThreads = 384;
+constexpr int kRows = 64;                       // per CTA
+constexpr int kBlockRows = 128;                 // per pair
+constexpr int kTilePages = 4;
+constexpr int kUnitBytes = 16384;
+constexpr int kRing = 7;
+constexpr int kKUnits = 9, kVUnits = 8;
+constexpr int kQBytes = 9 * kRows * 128;        // [dim block][64 rows][128 B]
+constexpr int kPBytes = kTilePages * kRows * 128;  // [page][64 rows][128 B]
+constexpr int kOffQ = 0;
+constexpr int kOffP = kOffQ + kQBytes;
+constexpr int kOffRing = kOffP + kPBytes;
+constexpr int kOffMisc = kOffRing + kRing * kUnitBytes;
+constexpr uint32_t kColO = 0, kColS = 256;      // S buffer b: 128 columns from 256 + 128 b
+constexpr int kSoftWarps = 8, kSoftThreads = 256;
+constexpr int kPieceTiles = 1;                  // a piece's boundary, in tiles
+constexpr uint64_t kTimeoutNs = 2000000000ull;
+constexpr uint64_t kDrainNs = 200000000ull;
+constexpr float kRescaleThreshold = 8.f;        // base-2 units
+
+struct Misc {
+  uint64_t full[kRing], empty[kRing], q_full, q_empty, s_full[2], s_free[2];
+  uint64_t p_full, p_free, o_full, o_free, drain;
+  uint32_t tmem_base;
+  int abort;
+  float red[2][4][kRows];  // row maxima by page, double-buffered; then row sums
+  CtaRange range;
+  long long scratch[kThreads / 32 + 1];
+};
+constexpr int kSmemBytes = kOffMisc + int(sizeof(Misc)) + 1024;
+static_assert(kSmemBytes <= 232448, "shared memory budget");
+}  // namespace pair
+
+namespace {
+using namespace pair;
+
+__device__ __forceinline__ uint32_t bar(uint64_t &b) { return smem_u32(&b); }
+
+__device__ __forceinline__ int block_tiles(const DecodeParams &p, int v) {
+  return (shared_block<kBlockRows>(p, v).tiles + kTilePages - 1) / kTilePages;
+}
+
+// The pieces of this pair's range, in order.
+struct Pieces {
+  const DecodeParams &p;
+  const CtaRange &r;
+  int v, tiles;
+  long long pv, t0, t1;
+  ViewReq view;
+  __device__ Pieces(const DecodeParams &p_, const CtaRange &r_) : p(p_), r(r_), v(r_.v_begin), pv(r_.p_begin) {}
+  __device__ bool next() {
+    while (v < p.pair_blocks && pv < r.end) {
+      view = shared_block<kBlockRows>(p, v);
+      tiles = (view.tiles + kTilePages - 1) / kTilePages;
+      if (tiles == 0) { ++v; continue; }
+      t0 = max(r.start, pv) - pv;
+      t1 = min(r.end, pv + tiles) - pv;
+      if (t0 < t1) return true;
+      advance();
+    }
+    return false;
+  }
+  __device__ void advance() { pv += request_cost(tiles, kPieceTiles); ++v; }
+};
+
+__device__ __forceinline__ long long total_tiles(const DecodeParams &p, const CtaRange &r) {
+  long long n = 0;
+  for (Pieces w(p, r); w.next(); w.advance()) n += w.t1 - w.t0;
+  return n;
+}
+
+// Units in load order: K_0, K_1, V_0, K_2, V_1, ...  First unit of K_n and V_n.
+__device__ __forceinline__ long long k_unit(long long n) { return n == 0 ? 0 : kKUnits + 17 * (n - 1); }
+__device__ __forceinline__ long long v_unit(long long n, long long total) {
+  return kKUnits + 17 * n + (n < total - 1 ? kKUnits : 0);
+}
+
+// ------------------------------------------------------------------ producer
+
+// One position in the tiles of a range, with the pages of the tile in lanes 0..3.
+struct TileWalk {
+  Pieces w;
+  long long t;
+  bool live;
+  int page;
+  __device__ TileWalk(const DecodeParams &p, const CtaRange &r, int *err) : w(p, r), t(0), page(0) {
+    live = w.next();
+    if (live) t = w.t0;
+    load(err);
+  }
+  // This lane's page of the tile; a page past the view repeats the last one
+  // (its tokens are masked), an entry out of range reads page 0.
+  __device__ void load(int *err) {
+    if (!live) return;
+    const int lane = threadIdx.x & 31;
+    const int i = min(int(t) * kTilePages + (lane & 3), w.view.tiles - 1);
+    page = w.p.block_table[size_t(w.view.req) * w.p.max_pages + i];
+    if (page < 0 || page >= w.p.num_pages) {
+      if (lane < 4) atomicOr(err, kErrBadPage);
+      page = 0;
+    }
+  }
+  __device__ bool first() const { return t == w.t0; }
+  __device__ void step(int *err) {
+    if (++t >= w.t1) {
+      w.advance();
+      live = w.next();
+      if (live) t = w.t0;
+    }
+    load(err);
+  }
+};
+
+__device__ __forceinline__ void produce(const DecodeParams &p, const CtaRange &r, Misc &m, uint32_t sQ,
+                                        uint32_t sRing, uint32_t rank, const CUtensorMap *tm_q,
+                                        const CUtensorMap *tm_k, const CUtensorMap *tm_v, int *err) {
+  volatile int *abort = &m.abort;
+  const int lane = threadIdx.x & 31;
+  const bool leader = rank == 0;
+  long long unit = 0;
+  uint32_t q_it = 0;
+  bool ok = true;
+  // slot of the next unit, emptied; the even CTA announces both CTAs' bytes
+  auto slot = [&](uint32_t *full) {
+    const int s = int(unit % kRing);
+    const bool got = mbar_wait_cluster(bar(m.empty[s]), (uint32_t(unit / kRing) & 1) ^ 1, abort, kTimeoutNs);
+    if (!__all_sync(0xffffffffu, got)) return -1;
+    if (leader && lane == 0) mbar_arrive_expect_tx(bar(m.full[s]), 2 * kUnitBytes);
+    __syncwarp();
+    *full = map_to_rank(bar(m.full[s]), 0);
+    ++unit;
+    return s;
+  };
+  auto load_k = [&](const TileWalk &c) {
+    if (c.first()) {
+      if (!__all_sync(0xffffffffu, mbar_wait_cluster(bar(m.q_empty), (q_it & 1) ^ 1, abort, kTimeoutNs)))
+        return false;
+      ++q_it;
+      if (leader && lane == 0) mbar_arrive_expect_tx(bar(m.q_full), 2 * kQBytes);
+      __syncwarp();
+      if (lane < 9)
+        tma_load_2d_pair(sQ + lane * kRows * 128, tm_q, map_to_rank(bar(m.q_full), 0), lane * 64,
+                         c.w.view.row0 + int(rank) * kRows);
+    }
+    const int pg = __shfl_sync(0xffffffffu, c.page, 2 * rank + (lane & 1));
+    for (int kb = 0; kb < kKUnits; ++kb) {
+      uint32_t full;
+      const int s = slot(&full);
+      if (s < 0) return false;
+      if (lane < 2) tma_load_4d_pair(sRing + s * kUnitBytes + lane * 8192, tm_k, full, 0, 0, kb, pg * 8);
+    }
+    return true;
+  };
+  auto load_v = [&](int page) {  // `page`: the tile's pages in lanes 0..3
+    for (int u = 0; u < kVUnits; ++u) {
+      uint32_t full;
+      const int pg = __shfl_sync(0xffffffffu, page, u >> 1);
+      const int s = slot(&full);
+      if (s < 0) return false;
+      if (lane == 0)
+        tma_load_4d_pair(sRing + s * kUnitBytes, tm_v, full, 0, 0, 4 * int(rank), pg * 8 + 4 * (u & 1));
+    }
+    return true;
+  };
+  TileWalk c(p, r, err);
+  if (c.live) ok = load_k(c);  // (a range may hold no tile, only a piece's cost)
+  while (ok && c.live) {
+    const int page = c.page;
+    c.step(err);
+    if (c.live) ok = load_k(c);
+    if (ok) ok = load_v(page);
+  }
+  if (!ok && lane == 0) atomicOr(err, kErrTimeout);
+}
+
+// ------------------------------------------------------------------ MMAs (even CTA)
+
+__device__ __forceinline__ void score_mmas(const DecodeParams &p, const CtaRange &r, Misc &m, uint32_t sQ,
+                                           uint32_t sRing, uint32_t tmem, int *err) {
+  volatile int *abort = &m.abort;
+  const uint32_t idesc = idesc_bf16_f32(128, 256, false, false);
+  const uint64_t dq = smem_desc_sw128(sQ, 16, 1024), dk = smem_desc_sw128(sRing, 16, 1024);
+  long long n = 0;
+  uint32_t q_it = 0;
+  bool ok = true;
+  for (Pieces w(p, r); ok && w.next(); w.advance()) {
+    for (long long t = w.t0; ok && t < w.t1; ++t, ++n) {
+      const int b = int(n & 1);
+      ok = mbar_wait_cluster(bar(m.s_free[b]), (uint32_t(n >> 1) & 1) ^ 1, abort, kTimeoutNs);
+      if (ok && t == w.t0) {
+        ok = mbar_wait_cluster(bar(m.q_full), q_it & 1, abort, kTimeoutNs);
+        ++q_it;
+      }
+      const long long u0 = k_unit(n);
+      for (int kb = 0; ok && kb < kKUnits; ++kb) {
+        const int s = int((u0 + kb) % kRing);
+        ok = mbar_wait_cluster(bar(m.full[s]), uint32_t((u0 + kb) / kRing) & 1, abort, kTimeoutNs);
+        if (!ok) break;
+        tc_fence_after();
+#pragma unroll
+        for (int ks = 0; ks < 4; ++ks)
+          mma_bf16_ss_pair(tmem + kColS + 128 * b, dq + ((kb * kRows * 128 + ks * 32) >> 4),
+                           dk + ((s * kUnitBytes + ks * 32) >> 4), idesc, kb > 0 || ks > 0);
+        mma_commit_pair(bar(m.empty[s]));
+      }
+      if (!ok) break;
+      mma_commit_pair(bar(m.s_full[b]));
+      if (t == w.t1 - 1) mma_commit_pair(bar(m.q_empty));
+    }
+  }
+  if (!ok) atomicOr(err, kErrTimeout);
+  mma_commit_pair(bar(m.drain));
+}
+
+__device__ __forceinline__ void pv_mmas(const DecodeParams &p, const CtaRange &r, Misc &m, uint32_t sP,
+                                        uint32_t sRing, uint32_t tmem, int *err) {
+  volatile int *abort = &m.abort;
+  const uint32_t idesc = idesc_bf16_f32(128, 256, false, true);
+  const uint64_t dp = smem_desc_sw128(sP, 16, 1024);
+  // V, MN-major: 64-dim blocks 1 KB apart, 8-token groups 4 KB apart
+  const uint64_t dv = smem_desc_sw128(sRing, 1024, 4096);
+  const long long total = total_tiles(p, r);
+  long long n = 0;
+  uint32_t o_it = 0;
+  bool ok = true;
+  for (Pieces w(p, r); ok && w.next(); w.advance(), ++o_it) {
+    for (long long t = w.t0; ok && t < w.t1; ++t, ++n) {
+      ok = mbar_wait_cluster(bar(m.p_full), uint32_t(n) & 1, abort, kTimeoutNs);
+      if (ok && t == w.t0) ok = mbar_wait_cluster(bar(m.o_free), (o_it & 1) ^ 1, abort, kTimeoutNs);
+      const long long u0 = v_unit(n, total);
+      for (int u = 0; ok && u < kVUnits; ++u) {
+        const int s = int((u0 + u) % kRing);
+        ok = mbar_wait_cluster(bar(m.full[s]), uint32_t((u0 + u) / kRing) & 1, abort, kTimeoutNs);
+        if (!ok) break;
+        tc_fence_after();
+#pragma unroll
+        for (int ks = 0; ks < 2; ++ks)
+#pragma unroll
+          for (int j = 0; j < 2; ++j)
+            mma_bf16_ss_pair(tmem + kColO + 128 * j,
+                             dp + (((u >> 1) * kRows * 128 + ((u & 1) * 2 + ks) * 32) >> 4),
+                             dv + ((s * kUnitBytes + ks * 8192 + j * 2048) >> 4), idesc,
+                             t > w.t0 || u > 0 || ks > 0);
+        mma_commit_pair(bar(m.empty[s]));
+      }
+      if (!ok) break;
+      mma_commit_pair(bar(m.p_free));
+      if (t == w.t1 - 1) mma_commit_pair(bar(m.o_full));
+    }
+  }
+  if (!ok) atomicOr(err, kErrTimeout);
+  mma_commit_pair(bar(m.drain));
+}
+
+// ------------------------------------------------------------------ softmax and epilogue
+
+__device__ __forceinline__ float exp2_approx(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
+// O *= alpha (this thread's row), 128 columns of this warp's TMEM lanes.
+static __device__ __noinline__ void rescale_rows(uint32_t taddr, float alpha) {
+  for (int c = 0; c < 128; c += 16) {
+    uint32_t o[16];
+    tmem_ld16(taddr + c, o);
+    tmem_wait_ld();
+#pragma unroll
+    for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
+    tmem_st16(taddr + c, o);
+  }
+  tmem_wait_st();
+}
+
+__device__ __forceinline__ void st_global_v8(float *dst, const float (&v)[8]) {
+  asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "f"(v[0]), "f"(v[1]),
+               "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7])
+               : "memory");
+}
+
+// A failed wait never leaves the loop: the warp goes on without working, so
+// that the others find it at their barriers (later waits fail at once).
+__device__ __forceinline__ void softmax(const DecodeParams &p, const CtaRange &r, Misc &m, unsigned char *smem,
+                                        uint32_t tmem, uint32_t rank, int pair_id, int *err) {
+  volatile int *abort = &m.abort;
+  const int st = int(threadIdx.x) - 128, warp = st >> 5, lane = st & 31;  // warps 0..7
+  const int g = warp >> 2, q = warp & 3;             // column half, TMEM quarter (lanes 32q ..)
+  const int row = 32 * (q & 1) + lane, pb = 2 * (q >> 1) + g;
+  const uint32_t lanes = uint32_t(32 * q) << 16;
+  const uint32_t t_s = tmem + lanes + kColS + 64 * g, t_o = tmem + lanes + kColO + 128 * g;
+  const float cs = p.score_scale_log2;
+  unsigned char *prow = smem + kOffP + pb * kRows * 128 + row * 128;
+  const uint32_t s_free0 = map_to_rank(bar(m.s_free[0]), 0), s_free1 = map_to_rank(bar(m.s_free[1]), 0);
+  const uint32_t p_full = map_to_rank(bar(m.p_full), 0), o_free = map_to_rank(bar(m.o_free), 0);
+  long long n = 0;
+  uint32_t o_it = 0;
+  bool ok = true;
+  for (Pieces w(p, r); w.next(); w.advance(), ++o_it) {
+    const int grow = w.view.row0 + int(rank) * kRows + row;
+    const int hi = row_view(p, w.view, min(grow, p.batch * p.heads - 1)).hi;
+    const bool mine = int(rank) * kRows + row < w.view.rows;
+    float mrun = -INFINITY, ell = 0.f, ellx = 0.f;
+    for (long long t = w.t0; t < w.t1; ++t, ++n) {
+      const int b = int(n & 1);
+      ok = ok && __all_sync(0xffffffffu, mbar_wait_cluster(bar(m.s_full[b]), uint32_t(n >> 1) & 1, abort, kTimeoutNs));
+      float x[64];
+      if (ok) {
+        tc_fence_after();
+        uint32_t a[32], c[32];
+        tmem_ld32(t_s + 128 * b, a);
+        tmem_ld32(t_s + 128 * b + 32, c);
+        tmem_wait_ld();
+#pragma unroll
+        for (int i = 0; i < 32; ++i) {
+          x[i] = __uint_as_float(a[i]);
+          x[32 + i] = __uint_as_float(c[i]);
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster(b ? s_free1 : s_free0);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 64; ++i) x[i] = 0.f;
+      }
+      const int left = hi - (int(t) * kTilePages + pb) * kPage;  // tokens of the page this row sees
+      if (left < kPage) {
+#pragma unroll
+        for (int i = 0; i < 64; ++i) x[i] = i < left ? x[i] : -INFINITY;
+      }
+      float mx4[4] = {x[0], x[1], x[2], x[3]};
+#pragma unroll
+      for (int i = 4; i < 64; i += 4)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) mx4[k] = fmaxf(mx4[k], x[i + k]);
+      m.red[b][pb][row] = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3]));
+      named_sync(1, kSoftThreads);
+      const float top = fmaxf(fmaxf(m.red[b][0][row], m.red[b][1][row]), fmaxf(m.red[b][2][row], m.red[b][3][row])) * cs;
+      float alpha = 1.f;
+      bool resc = false;
+      if (t == w.t0) {
+        mrun = top;
+      } else if (top > mrun + kRescaleThreshold) {
+        alpha = exp2f(mrun - top);
+        mrun = top;
+        resc = true;
+      }
+      // a row that has seen no token yet keeps a -inf maximum: its weights are 0
+      const float mref = mrun == -INFINITY ? 0.f : mrun;
+      uint32_t pk[32];
+      float lsum[2] = {0.f, 0.f}, xsum[2] = {0.f, 0.f};
+#pragma unroll
+      for (int i = 0; i < 32; ++i) {
+        const float e0 = exp2_approx(fmaf(x[2 * i], cs, -mref)), e1 = exp2_approx(fmaf(x[2 * i + 1], cs, -mref));
+        __nv_bfloat162 v = __floats2bfloat162_rn(e0, e1);
+        pk[i] = *reinterpret_cast<uint32_t *>(&v);
+        xsum[0] += e0;
+        xsum[1] += e1;
+        lsum[0] += __uint_as_float(pk[i] << 16);
+        lsum[1] += __uint_as_float(pk[i] & 0xffff0000u);
+      }
+      ell = ell * alpha + (lsum[0] + lsum[1]);
+      ellx = ellx * alpha + (xsum[0] + xsum[1]);
+      // P's buffer and O are free once the previous tile's products are done
+      if (n > 0)
+        ok = ok && __all_sync(0xffffffffu,
+                              mbar_wait_cluster(bar(m.p_free), uint32_t(n - 1) & 1, abort, kTimeoutNs));
+      if (ok) {
+        if (__any_sync(0xffffffffu, resc)) {
+          tc_fence_after();
+          rescale_rows(t_o, alpha);
+        }
+#pragma unroll
+        for (int c = 0; c < 8; ++c)
+          *reinterpret_cast<uint4 *>(prow + ((c ^ (row & 7)) << 4)) =
+              make_uint4(pk[4 * c], pk[4 * c + 1], pk[4 * c + 2], pk[4 * c + 3]);
+        fence_proxy_async_smem();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster(p_full);
+      }
+    }
+    // ---- this piece's partial: O / sum and the LSE of its rows
+    named_sync(1, kSoftThreads);  // every thread is past its last read of the maxima
+    m.red[0][pb][row] = ell;
+    m.red[1][pb][row] = ellx;
+    named_sync(1, kSoftThreads);
+    const float sum = (m.red[0][0][row] + m.red[0][1][row]) + (m.red[0][2][row] + m.red[0][3][row]);
+    const float sumx = (m.red[1][0][row] + m.red[1][1][row]) + (m.red[1][2][row] + m.red[1][3][row]);
+    named_sync(1, kSoftThreads);  // read before the next piece writes maxima
+    const float inv = sum > 0.f ? 1.f / sum : 0.f;
+    ok = ok && __all_sync(0xffffffffu, mbar_wait_cluster(bar(m.o_full), o_it & 1, abort, kTimeoutNs));
+    const int c_first = sched_owner(w.pv, r.total, r.g_eff);
+    if (ok) {
+      tc_fence_after();
+      const size_t slot = 2 * size_t(pair_id + w.v) + rank;
+      float *dst = slot_out_ptr(p) + (slot * kSlotHeads + row) * kDv + 256 * (q >> 1) + 128 * g;
+#pragma unroll 1
+      for (int c = 0; c < 128; c += 32) {
+        uint32_t o[32];
+        tmem_ld32(t_o + c, o);
+        tmem_wait_ld();
+        if (mine) {
+#pragma unroll
+          for (int i = 0; i < 32; i += 8) {
+            float v[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) v[k] = __uint_as_float(o[i + k]) * inv;
+            st_global_v8(dst + c + i, v);
+          }
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cluster(o_free);
+      if (mine && pb == 0) slot_lse_ptr(p)[slot * kSlotHeads + row] = mrun + log2f(sumx);
+      if (st == 0 && rank == 0 && pair_id == c_first) {
+        const int c_last = sched_owner(w.pv + w.tiles - 1, r.total, r.g_eff);
+        info_ptr(p)[p.batch * p.head_groups + w.v] = make_int4(c_first, c_last - c_first + 1, pair_id + w.v, 0);
+      }
+    }
+  }
+  if (!ok) atomicOr(err, kErrTimeout);
+}
+
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+    decode_pair_kernel(const __grid_constant__ DecodeParams p, const __grid_constant__ CUtensorMap tm_q,
+                       const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v) {
+  extern __shared__ unsigned char smem_raw[];
+  const uint32_t raw = smem_u32(smem_raw), pad = ((raw + 1023u) & ~1023u) - raw;
+  unsigned char *smem = smem_raw + pad;
+  const uint32_t sbase = raw + pad;
+  Misc &m = *reinterpret_cast<Misc *>(smem + kOffMisc);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const uint32_t rank = cluster_rank();
+  const int pair_id = int(blockIdx.x) >> 1;
+  int *err = error_word(p);
+
+  if (tid == 0) {
+    for (int s = 0; s < kRing; ++s) {
+      mbar_init(bar(m.full[s]), 1);
+      mbar_init(bar(m.empty[s]), 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(bar(m.s_full[b]), 1);
+      mbar_init(bar(m.s_free[b]), 2 * kSoftWarps);
+    }
+    mbar_init(bar(m.q_full), 1);
+    mbar_init(bar(m.q_empty), 1);
+    mbar_init(bar(m.p_full), 2 * kSoftWarps);
+    mbar_init(bar(m.p_free), 1);
+    mbar_init(bar(m.o_full), 1);
+    mbar_init(bar(m.o_free), 2 * kSoftWarps);
+    mbar_init(bar(m.drain), 2);
+    m.abort = 0;
+    fence_barrier_init();
+  }
+  if (warp == 1) {
+    tmem_alloc_pair(smem_u32(&m.tmem_base), 512);
+    tmem_relinquish_pair();
+  }
+  if (warp == 0 && lane == 0) {
+    tma_prefetch_desc(&tm_q);
+    tma_prefetch_desc(&tm_k);
+    tma_prefetch_desc(&tm_v);
+  }
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  // blocks without pages have no partials
+  for (int v = int(blockIdx.x) * kThreads + tid; v < p.pair_blocks; v += int(gridDim.x) * kThreads)
+    if (block_tiles(p, v) == 0) info_ptr(p)[p.batch * p.head_groups + v] = make_int4(-1, 0, 0, 0);
+  schedule_range<kPieceTiles>(p.pair_blocks, pair_id, p.pairs, [&](int v) { return block_tiles(p, v); }, &m.range,
+                             m.scratch);
+  tc_fence_before();
+  cluster_sync();  // both CTAs' barriers and TMEM are ready
+  tc_fence_after();
+  const uint32_t tmem = m.tmem_base;
+  const CtaRange r = m.range;
+
+  if (r.start < r.end) {
+    if (warp == 0) {
+      produce(p, r, m, sbase + kOffQ, sbase + kOffRing, rank, &tm_q, &tm_k, &tm_v, err);
+    } else if (warp == 1) {
+      if (rank == 0 && lane == 0) score_mmas(p, r, m, sbase + kOffQ, sbase + kOffRing, tmem, err);
+    } else if (warp == 2) {
+      if (rank == 0 && lane == 0) pv_mmas(p, r, m, sbase + kOffP, sbase + kOffRing, tmem, err);
+    } else if (warp >= 4) {
+      softmax(p, r, m, smem, tmem, rank, pair_id, err);
+    }
+    // no MMA may still read this CTA's shared memory, and no copy write it:
+    // the MMAs waited for every copy unless a wait gave up
+    __syncthreads();
+    if (tid == 0) {
+      mbar_wait_drain(bar(m.drain), 0, kDrainNs);
+      if (m.abort) {  // let copies in flight land
+        const uint64_t t0 = globaltimer();
+        while (globaltimer() - t0 < 1000000ull) {
+        }
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc_pair(tmem, 512);
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_decode_pair(const DecodeParams &p, const CUtensorMap &tm_q, const CUtensorMap &tm_k,
+                               const CUtensorMap &tm_v, cudaStream_t stream) {
+  static SmemLimitOnce smem_limit;
+  const cudaError_t e = smem_limit.ensure(decode_pair_kernel, pair::kSmemBytes);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(2 * p.pairs);
+  cfg.blockDim = dim3(pair::kThreads);
+  cfg.dynamicSmemBytes = pair::kSmemBytes;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, decode_pair_kernel, p, tm_q, tm_k, tm_v);
+}
+
+}  // namespace mla

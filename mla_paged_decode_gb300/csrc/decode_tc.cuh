@@ -1066,10 +1066,11 @@ __device__ __forceinline__ void tc_softmax(const TcParams &tp, const CtaRange &r
     if constexpr (VIEW) {
       out_row0 = w.view.row0;
       // shared pages: every piece leaves a partial, in the slot of its CTA
-      // and virtual request (both grow along the walk, so the sum is its own)
+      // and virtual request (both grow along the walk, so the sum is its own),
+      // after the pair kernel's slots
       if (p.view == kViewShared) {
         split = true;
-        si.slot = int(blockIdx.x) + w.v;
+        si.slot = 2 * (p.pair_blocks + p.pairs) + int(blockIdx.x) + w.v;
       }
     } else {
       out_row0 = size_t(w.b) * p.heads + size_t(w.g) * kHeads;

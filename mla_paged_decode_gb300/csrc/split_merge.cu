@@ -220,22 +220,29 @@ __global__ void __launch_bounds__(kMergeWarps * 32, 7) shared_merge_kernel(Decod
   const int b = row / p.heads, r = row - b * p.heads;
   const int g = group_of_request(p, b);
   const int local = row - group_start(p, g) * p.heads;
-  int first[2] = {0, 0}, num[2] = {0, 0}, hl[2] = {local & 63, r & 63};  // slots of the two sets, row in them
-  const int vp = block_base(p, g) + (local >> 6), vt = p.prefix_blocks + (r >> 6) * p.batch + b;
-  if (local >= 0 && vp < p.prefix_blocks) {
-    const int4 i = info_ptr(p)[vp];
-    if (i.y > 0 && i.z >= 0 && i.z + i.y <= slots) first[0] = i.z, num[0] = i.y;
+  // slots of the two sets: first, stride, number; the row's place in them
+  int first[2] = {0, 0}, num[2] = {0, 0}, hl[2] = {local & 63, r & 63};
+  const int stride = p.pair_blocks ? 2 : 1;  // a pair's piece has two slots, 64 rows each
+  const int V = p.batch * p.head_groups + p.prefix_blocks;
+  if (local >= 0) {
+    const int blocks = p.pair_blocks ? p.pair_blocks : p.prefix_blocks;
+    const int v = p.pair_blocks ? block_base<128>(p, g) + (local >> 7) : block_base<64>(p, g) + (local >> 6);
+    if (v < blocks) {
+      const int4 i = info_ptr(p)[p.pair_blocks ? V + v : v];
+      if (i.y > 0 && i.z >= 0 && (i.z + i.y) * stride <= slots)
+        first[0] = i.z * stride + (p.pair_blocks ? (local >> 6) & 1 : 0), num[0] = i.y;
+    }
   }
   {
-    const int4 i = info_ptr(p)[vt];
+    const int4 i = info_ptr(p)[p.prefix_blocks + (r >> 6) * p.batch + b];
     if (i.y > 0 && i.z >= 0 && i.z + i.y <= slots) first[1] = i.z, num[1] = i.y;
   }
   const int ns = num[0] + num[1];
   const float *sl = slot_lse_ptr(p);
   const float *so = slot_out_ptr(p);
   auto at = [&](int k) {
-    const int s = k >= num[0];
-    return size_t(first[s] + (s ? k - num[0] : k)) * kSlotHeads + hl[s];
+    const int s = k < num[0] ? first[0] + k * stride : first[1] + k - num[0];
+    return size_t(s) * kSlotHeads + hl[k < num[0] ? 0 : 1];
   };
   float mx = -INFINITY;
   for (int k = lane; k < ns; k += 32) mx = fmaxf(mx, sl[at(k)]);
@@ -291,7 +298,8 @@ cudaError_t launch_shared_merge(const DecodeParams &p, int grid, cudaStream_t st
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, shared_merge_kernel, p, p.batch * p.head_groups + p.prefix_blocks + grid);
+  const int slots = 2 * (p.pair_blocks + p.pairs) + p.batch * p.head_groups + p.prefix_blocks + grid;
+  return cudaLaunchKernelEx(&cfg, shared_merge_kernel, p, slots);
 }
 
 cudaError_t launch_split_merge(const DecodeParams &p, int grid, cudaStream_t stream) {

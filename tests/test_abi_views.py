@@ -34,6 +34,7 @@ def test_bad_descriptors(lib, call, kw, code):  # noqa: F811
 def test_common_refusals(lib, call):  # noqa: F811
     assert call(lib, None) == -1
     assert call(lib, _desc(), base=2) == call(lib, _desc(), scale=math.nan) == -6
+    assert call(lib, _desc(), scale=0.0) == call(lib, _desc(), scale=-1.0) == -6
     for name in ("q", "kv", "out", "ws"):
         assert call(lib, _desc(), **{name: None}) == -1, name
         assert call(lib, _desc(), **{name: FAKE + 8}) == -4, name
