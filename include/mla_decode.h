@@ -472,7 +472,7 @@ int mla_pages_copy(const void *src_pages, void *dst_pages, const int32_t *src, c
  * use; the rest of the new page keeps what it held), and its length is the
  * parent's.  The child's row is overwritten: it holds no pages before the
  * call.  A child must not repeat and must not be a parent of the same call.
- * When no page is left the child is empty.  Two kernels.
+ * When no page is left the child is empty.  n <= 524288.  Two kernels.
  */
 int mla_pages_fork(void *kv_pages, int32_t *block_table, int32_t *seq_lens, int32_t *ref_counts,
                    const int32_t *parents, const int32_t *children, int n, const mla_pages_desc *d,
@@ -509,7 +509,7 @@ int mla_pages_free(int32_t *block_table, int32_t *seq_lens, int32_t *ref_counts,
  * and ref_counts follow.  remap: optional int32 [num_pages], each page's new
  * id, -1 for a page that was free.  Freed ids keep their old contents.  The
  * first two words of the workspace receive the number of live pages and of
- * moves.  Three kernels.
+ * moves.  Two or three kernels.
  */
 int mla_pages_compact(void *kv_pages, int32_t *block_table, int32_t *ref_counts, int32_t *remap,
                       const mla_pages_desc *d, void *workspace, size_t workspace_bytes,

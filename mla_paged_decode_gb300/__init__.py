@@ -73,6 +73,8 @@ class PagesDesc(ctypes.Structure):
 def load_library():
     """Loads the built library (raises if it is missing)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib
@@ -139,17 +141,35 @@ def _check(status: int):
         raise MlaError(status, msg)
 
 
+# The current stream's handle and the current device without the Python
+# objects around them (2 us and 0.4 us of a small call's host time).
+_raw_stream = torch._C._cuda_getCurrentRawStream if hasattr(torch._C, "_cuda_getCurrentRawStream") else \
+    lambda index: torch.cuda.current_stream(index).cuda_stream
+_NO_SWITCH = contextlib.nullcontext()
+
+
 def _on(device):
     """The device context for a call: nothing to switch when it is current
     (the switch costs a few microseconds, felt by small decodes)."""
     if torch.cuda.current_device() == device.index:
-        return contextlib.nullcontext()
+        return _NO_SWITCH
     return torch.cuda.device(device)
 
 
 def _stream_ptr(stream, device) -> int:
-    s = stream if stream is not None else torch.cuda.current_stream(device)
-    return int(s.cuda_stream)
+    return int(stream.cuda_stream) if stream is not None else _raw_stream(device.index)
+
+
+def _launch(fn, device, stream, *args):
+    """fn(*args, stream) on the tensors' device; raises on a bad status."""
+    s = _stream_ptr(stream, device)
+    if torch.cuda.current_device() == device.index:
+        st = fn(*args, s)
+    else:
+        with torch.cuda.device(device):
+            st = fn(*args, s)
+    if st != 0:
+        _check(st)
 
 
 def _kv_dtype_code(kv_pages: torch.Tensor) -> int:
@@ -161,6 +181,7 @@ def _kv_dtype_code(kv_pages: torch.Tensor) -> int:
 
 
 _KV_TYPES = (torch.bfloat16, torch.uint8, torch.float8_e4m3fn)
+_I32, _BF16, _F32, _U8 = (torch.int32,), (torch.bfloat16,), (torch.float32,), (torch.uint8,)
 _DESCS: dict = {}
 
 
@@ -501,12 +522,10 @@ def decode_window(q, kv_pages, block_table, seq_lens, window: int, sinks: int, s
     if workspace is None:
         workspace = make_workspace(q, kv_pages, block_table, kv_scale)
     _need(workspace, "workspace", (torch.uint8,), dev)
-    with _on(dev):
-        st = load_library().mla_decode_window(
-            q.data_ptr(), kv_pages.data_ptr(), block_table.data_ptr(), seq_lens.data_ptr(), int(window),
-            int(sinks), float(sm_scale), int(lse_base), out.data_ptr(), lse.data_ptr(), ctypes.byref(d),
-            workspace.data_ptr(), workspace.numel(), _stream_ptr(stream, dev))
-    _check(st)
+    _launch(load_library().mla_decode_window, dev, stream, q.data_ptr(), kv_pages.data_ptr(),
+            block_table.data_ptr(), seq_lens.data_ptr(), int(window), int(sinks), float(sm_scale),
+            int(lse_base), out.data_ptr(), lse.data_ptr(), ctypes.byref(d), workspace.data_ptr(),
+            workspace.numel())
     return out, lse
 
 
@@ -535,13 +554,10 @@ def decode_shared(q, kv_pages, block_table, seq_lens, group_starts, shared_pages
     if workspace is None:
         workspace = make_shared_workspace(q, kv_pages, block_table, groups, kv_scale)
     _need(workspace, "workspace", (torch.uint8,), dev)
-    with _on(dev):
-        st = load_library().mla_decode_shared(
-            q.data_ptr(), kv_pages.data_ptr(), block_table.data_ptr(), seq_lens.data_ptr(),
-            group_starts.data_ptr(), shared_pages.data_ptr(), groups, float(sm_scale), int(lse_base),
-            out.data_ptr(), lse.data_ptr(), ctypes.byref(d), workspace.data_ptr(), workspace.numel(),
-            _stream_ptr(stream, dev))
-    _check(st)
+    _launch(load_library().mla_decode_shared, dev, stream, q.data_ptr(), kv_pages.data_ptr(),
+            block_table.data_ptr(), seq_lens.data_ptr(), group_starts.data_ptr(), shared_pages.data_ptr(),
+            groups, float(sm_scale), int(lse_base), out.data_ptr(), lse.data_ptr(), ctypes.byref(d),
+            workspace.data_ptr(), workspace.numel())
     return out, lse
 
 
@@ -559,39 +575,52 @@ def make_pages_workspace(ref_counts) -> torch.Tensor:
                        device=ref_counts.device)
 
 
-def _pages_call(what, anchor, kv_pages, block_table, seq_lens, ref_counts, error_word, **lists):
-    """Checks the arrays of a page operation; returns (device, descriptor)."""
-    dev = anchor.device
+def _ints(t, name, device, dim):
+    _need(t, name, _I32, device)
+    if t.dim() != dim:
+        raise ValueError(f"{name} must be {'one' if dim == 1 else 'two'}-dimensional")
+
+
+_PAGES_DESCS: dict = {}
+
+
+def _pages_desc(rows, width, pages, page_size, row, kv_dtype):
+    """The call's size descriptor (by reference), built once per set of sizes."""
+    key = (rows, width, pages, page_size, row, kv_dtype)
+    d = _PAGES_DESCS.get(key)
+    if d is None:
+        if len(_PAGES_DESCS) > 256:
+            _PAGES_DESCS.clear()
+        d = _PAGES_DESCS[key] = PagesDesc(*key)
+    return ctypes.byref(d)
+
+
+def _pool(kv_pages, name="kv_pages"):
+    """Checks a pool; returns its device, shape and dtype code."""
+    dev = kv_pages.device
     if dev.type != "cuda":
-        raise ValueError(f"{what} runs on CUDA tensors only")
-    if kv_pages is not None:
-        _need(kv_pages, "kv_pages", _KV_TYPES, dev)
-        if kv_pages.dim() != 3:
-            raise ValueError("kv_pages must be [num_pages, 64, 576]")
-    rows, width, pages = 0, 1, kv_pages.shape[0] if kv_pages is not None else 0
-    if block_table is not None:
-        _need(block_table, "block_table", (torch.int32,), dev)
-        _need(ref_counts, "ref_counts", (torch.int32,), dev)
-        if block_table.dim() != 2:
-            raise ValueError("block_table must be [num_requests, max_pages]")
-        rows, width = block_table.shape
-        if ref_counts.dim() != 1 or (kv_pages is not None and ref_counts.numel() != pages):
-            raise ValueError("ref_counts must be [num_pages]")
-        pages = ref_counts.numel()
-        if seq_lens is not None:
-            _need(seq_lens, "seq_lens", (torch.int32,), dev)
-            if seq_lens.dim() != 1 or seq_lens.numel() != rows:
-                raise ValueError("seq_lens must be [num_requests]")
-    for name, t in lists.items():
-        _need(t, name, (torch.int32,), dev)
-        if t.dim() != 1:
-            raise ValueError(f"{name} must be one-dimensional")
+        raise ValueError(f"{name} must be a CUDA tensor")
+    _need(kv_pages, name, _KV_TYPES, dev)
+    shape = kv_pages.shape
+    if len(shape) != 3:
+        raise ValueError(f"{name} must be [num_pages, 64, 576]")
+    return dev, shape, _kv_dtype_code(kv_pages)
+
+
+def _books(dev, block_table, seq_lens, ref_counts, error_word):
+    """Checks a pool's table, lengths and counts; returns (rows, width, pages)."""
+    if dev.type != "cuda":
+        raise ValueError("the page operations run on CUDA tensors only")
+    _ints(block_table, "block_table", dev, 2)
+    _ints(ref_counts, "ref_counts", dev, 1)
+    rows, width = block_table.shape
+    if seq_lens is not None:
+        _ints(seq_lens, "seq_lens", dev, 1)
+        if seq_lens.numel() != rows:
+            raise ValueError("seq_lens must be [num_requests]")
     if error_word is not None:
-        _need(error_word, "error_word", (torch.int32,), dev)
-    return dev, PagesDesc(num_requests=rows, max_pages_per_seq=width, num_pages=pages,
-                          page_size=kv_pages.shape[1] if kv_pages is not None else 64,
-                          head_dim_qk=kv_pages.shape[2] if kv_pages is not None else 576,
-                          kv_dtype=_kv_dtype_code(kv_pages) if kv_pages is not None else KV_BF16)
+        _need(error_word, "error_word", _I32, dev)
+    return rows, width, ref_counts.numel()
 
 
 def _opt(t):
@@ -608,17 +637,20 @@ def _pages_ws(workspace, ref_counts):
 def pages_copy(src_pages, dst_pages, src, dst, *, error_word=None, stream=None):
     """mla_pages_copy: page src[i] of src_pages to page dst[i] of dst_pages
     (int32 [n] each; two pools of one dtype, or one pool twice)."""
-    dev, d = _pages_call("pages_copy", src_pages, src_pages, None, None, None, error_word, src=src, dst=dst)
+    dev, shape, code = _pool(src_pages, "src_pages")
     _need(dst_pages, "dst_pages", (src_pages.dtype,), dev)
-    if dst_pages.dim() != 3 or dst_pages.shape[1:] != src_pages.shape[1:]:
+    if dst_pages.dim() != 3 or dst_pages.shape[1:] != shape[1:]:
         raise ValueError("dst_pages must be [num_pages, 64, 576]")
-    if src.numel() != dst.numel():
+    _ints(src, "src", dev, 1)
+    _ints(dst, "dst", dev, 1)
+    n = src.numel()
+    if dst.numel() != n:
         raise ValueError("src and dst must have the same length")
-    with _on(dev):
-        st = load_library().mla_pages_copy(
-            src_pages.data_ptr(), dst_pages.data_ptr(), src.data_ptr(), dst.data_ptr(), src.numel(),
-            dst_pages.shape[0], ctypes.byref(d), _opt(error_word), _stream_ptr(stream, dev))
-    _check(st)
+    if error_word is not None:
+        _need(error_word, "error_word", _I32, dev)
+    _launch(load_library().mla_pages_copy, dev, stream, src_pages.data_ptr(), dst_pages.data_ptr(),
+            src.data_ptr(), dst.data_ptr(), n, dst_pages.shape[0],
+            _pages_desc(0, 1, shape[0], shape[1], shape[2], code), _opt(error_word))
     return dst_pages
 
 
@@ -627,33 +659,35 @@ def pages_fork(kv_pages, block_table, seq_lens, ref_counts, parents, children, *
     """mla_pages_fork: request children[k] becomes a copy of parents[k]
     (int32 [n] each): full pages shared, a partial last page copied.  The
     table [R, W], lengths [R] and counts [num_pages] are updated in place."""
-    dev, d = _pages_call("pages_fork", kv_pages, kv_pages, block_table, seq_lens, ref_counts, error_word,
-                         parents=parents, children=children)
-    if parents.numel() != children.numel():
+    dev, shape, code = _pool(kv_pages)
+    rows, width, pages = _books(dev, block_table, seq_lens, ref_counts, error_word)
+    if pages != shape[0]:
+        raise ValueError("ref_counts must be [num_pages]")
+    _ints(parents, "parents", dev, 1)
+    _ints(children, "children", dev, 1)
+    n = parents.numel()
+    if children.numel() != n:
         raise ValueError("parents and children must have the same length")
     ws = _pages_ws(workspace, ref_counts)
-    with _on(dev):
-        st = load_library().mla_pages_fork(
-            kv_pages.data_ptr(), block_table.data_ptr(), seq_lens.data_ptr(), ref_counts.data_ptr(),
-            parents.data_ptr(), children.data_ptr(), parents.numel(), ctypes.byref(d), ws.data_ptr(),
-            ws.numel(), _opt(error_word), _stream_ptr(stream, dev))
-    _check(st)
+    _launch(load_library().mla_pages_fork, dev, stream, kv_pages.data_ptr(), block_table.data_ptr(),
+            seq_lens.data_ptr(), ref_counts.data_ptr(), parents.data_ptr(), children.data_ptr(), n,
+            _pages_desc(rows, width, pages, shape[1], shape[2], code), ws.data_ptr(), ws.numel(),
+            _opt(error_word))
 
 
 def pages_alloc(block_table, seq_lens, ref_counts, new_lens, *, workspace=None, error_word=None,
                 stream=None):
     """mla_pages_alloc: every request gets the pages for new_lens[b] >=
     seq_lens[b] tokens, lowest free pages first (seq_lens is not changed)."""
-    dev, d = _pages_call("pages_alloc", block_table, None, block_table, seq_lens, ref_counts, error_word,
-                         new_lens=new_lens)
-    if new_lens.numel() != d.num_requests:
+    dev = block_table.device
+    rows, width, pages = _books(dev, block_table, seq_lens, ref_counts, error_word)
+    _ints(new_lens, "new_lens", dev, 1)
+    if new_lens.numel() != rows:
         raise ValueError("new_lens must be [num_requests]")
     ws = _pages_ws(workspace, ref_counts)
-    with _on(dev):
-        st = load_library().mla_pages_alloc(
-            block_table.data_ptr(), seq_lens.data_ptr(), ref_counts.data_ptr(), new_lens.data_ptr(),
-            ctypes.byref(d), ws.data_ptr(), ws.numel(), _opt(error_word), _stream_ptr(stream, dev))
-    _check(st)
+    _launch(load_library().mla_pages_alloc, dev, stream, block_table.data_ptr(), seq_lens.data_ptr(),
+            ref_counts.data_ptr(), new_lens.data_ptr(), _pages_desc(rows, width, pages, 64, 576, KV_BF16),
+            ws.data_ptr(), ws.numel(), _opt(error_word))
 
 
 def pages_free(block_table, seq_lens, ref_counts, new_lens, *, window: int = 0, sinks: int = 0,
@@ -661,32 +695,32 @@ def pages_free(block_table, seq_lens, ref_counts, new_lens, *, window: int = 0, 
     """mla_pages_free: every request is shortened to new_lens[b] tokens (0
     ends it, its own length leaves it) and, with a window, gives up the pages
     that decode_window(window, sinks) no longer sees."""
-    dev, d = _pages_call("pages_free", block_table, None, block_table, seq_lens, ref_counts, error_word,
-                         new_lens=new_lens)
-    if new_lens.numel() != d.num_requests:
+    dev = block_table.device
+    rows, width, pages = _books(dev, block_table, seq_lens, ref_counts, error_word)
+    _ints(new_lens, "new_lens", dev, 1)
+    if new_lens.numel() != rows:
         raise ValueError("new_lens must be [num_requests]")
-    with _on(dev):
-        st = load_library().mla_pages_free(
-            block_table.data_ptr(), seq_lens.data_ptr(), ref_counts.data_ptr(), new_lens.data_ptr(),
-            int(window), int(sinks), ctypes.byref(d), _opt(error_word), _stream_ptr(stream, dev))
-    _check(st)
+    _launch(load_library().mla_pages_free, dev, stream, block_table.data_ptr(), seq_lens.data_ptr(),
+            ref_counts.data_ptr(), new_lens.data_ptr(), int(window), int(sinks),
+            _pages_desc(rows, width, pages, 64, 576, KV_BF16), _opt(error_word))
 
 
 def pages_compact(kv_pages, block_table, ref_counts, *, remap=None, workspace=None, error_word=None,
                   stream=None):
     """mla_pages_compact: the live pages move to ids 0 .. live - 1 and the
     table [R, W] and counts follow.  remap: optional int32 [num_pages], each
-    page's new id (-1: it was free).  Returns the workspace's first two words,
-    a device int32 [2]: live pages, moves."""
-    dev, d = _pages_call("pages_compact", kv_pages, kv_pages, block_table, None, ref_counts, error_word)
+    page's new id (-1: it was free).  Returns the workspace, whose first two
+    int32 words are the number of live pages and of moves."""
+    dev, shape, code = _pool(kv_pages)
+    rows, width, pages = _books(dev, block_table, None, ref_counts, error_word)
+    if pages != shape[0]:
+        raise ValueError("ref_counts must be [num_pages]")
     if remap is not None:
-        _need(remap, "remap", (torch.int32,), dev)
-        if remap.numel() != d.num_pages:
+        _ints(remap, "remap", dev, 1)
+        if remap.numel() != pages:
             raise ValueError("remap must be [num_pages]")
     ws = _pages_ws(workspace, ref_counts)
-    with _on(dev):
-        st = load_library().mla_pages_compact(
-            kv_pages.data_ptr(), block_table.data_ptr(), ref_counts.data_ptr(), _opt(remap),
-            ctypes.byref(d), ws.data_ptr(), ws.numel(), _opt(error_word), _stream_ptr(stream, dev))
-    _check(st)
-    return ws[:8].view(torch.int32)
+    _launch(load_library().mla_pages_compact, dev, stream, kv_pages.data_ptr(), block_table.data_ptr(),
+            ref_counts.data_ptr(), _opt(remap), _pages_desc(rows, width, pages, shape[1], shape[2], code),
+            ws.data_ptr(), ws.numel(), _opt(error_word))
+    return ws

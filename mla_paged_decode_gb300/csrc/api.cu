@@ -792,7 +792,7 @@ int mla_pages_fork(void *kv_pages, int32_t *block_table, int32_t *seq_lens, int3
                    void *workspace, size_t workspace_bytes, int32_t *error_word, mla_stream_t stream) {
   int st = check_pages_desc(d);
   if (st != MLA_OK) return st;
-  if (n < 0) return MLA_ERR_ARG;
+  if (n < 0 || n > mla::kMaxForks) return MLA_ERR_ARG;
   if (n == 0 || d->num_requests == 0) return MLA_OK;
   if (!kv_pages || !block_table || !seq_lens || !ref_counts || !parents || !children || !workspace)
     return MLA_ERR_NULL;

@@ -100,17 +100,30 @@ struct Pieces {
   __device__ void advance() { pv += request_cost(tiles, kPieceTiles); ++v; }
 };
 
-__device__ __forceinline__ long long total_tiles(const DecodeParams &p, const CtaRange &r) {
-  long long n = 0;
-  for (Pieces w(p, r); w.next(); w.advance()) n += w.t1 - w.t0;
+__device__ __forceinline__ uint32_t total_tiles(const DecodeParams &p, const CtaRange &r) {
+  uint32_t n = 0;
+  for (Pieces w(p, r); w.next(); w.advance()) n += uint32_t(w.t1 - w.t0);
   return n;
 }
 
 // Units in load order: K_0, K_1, V_0, K_2, V_1, ...  First unit of K_n and V_n.
-__device__ __forceinline__ long long k_unit(long long n) { return n == 0 ? 0 : kKUnits + 17 * (n - 1); }
-__device__ __forceinline__ long long v_unit(long long n, long long total) {
+// (32-bit counters: the issuing threads pay for every division.)
+__device__ __forceinline__ uint32_t k_unit(uint32_t n) { return n == 0 ? 0 : kKUnits + 17 * (n - 1); }
+__device__ __forceinline__ uint32_t v_unit(uint32_t n, uint32_t total) {
   return kKUnits + 17 * n + (n < total - 1 ? kKUnits : 0);
 }
+// A place in the ring: slot and the parity of its phase.
+struct Place {
+  int s;
+  uint32_t phase;
+  __device__ explicit Place(uint32_t unit) : s(int(unit % kRing)), phase((unit / kRing) & 1) {}
+  __device__ __forceinline__ void step() {
+    if (++s == kRing) {
+      s = 0;
+      phase ^= 1;
+    }
+  }
+};
 
 // ------------------------------------------------------------------ producer
 
@@ -154,18 +167,19 @@ __device__ __forceinline__ void produce(const DecodeParams &p, const CtaRange &r
   volatile int *abort = &m.abort;
   const int lane = threadIdx.x & 31;
   const bool leader = rank == 0;
-  long long unit = 0;
+  Place at(0);
   uint32_t q_it = 0;
   bool ok = true;
+  const uint32_t full0 = map_to_rank(bar(m.full[0]), 0);
   // slot of the next unit, emptied; the even CTA announces both CTAs' bytes
   auto slot = [&](uint32_t *full) {
-    const int s = int(unit % kRing);
-    const bool got = mbar_wait_cluster(bar(m.empty[s]), (uint32_t(unit / kRing) & 1) ^ 1, abort, kTimeoutNs);
+    const int s = at.s;
+    const bool got = mbar_wait_cluster(bar(m.empty[s]), at.phase ^ 1, abort, kTimeoutNs);
     if (!__all_sync(0xffffffffu, got)) return -1;
     if (leader && lane == 0) mbar_arrive_expect_tx(bar(m.full[s]), 2 * kUnitBytes);
     __syncwarp();
-    *full = map_to_rank(bar(m.full[s]), 0);
-    ++unit;
+    *full = full0 + 8 * s;
+    at.step();
     return s;
   };
   auto load_k = [&](const TileWalk &c) {
@@ -217,21 +231,21 @@ __device__ __forceinline__ void score_mmas(const DecodeParams &p, const CtaRange
   volatile int *abort = &m.abort;
   const uint32_t idesc = idesc_bf16_f32(128, 256, false, false);
   const uint64_t dq = smem_desc_sw128(sQ, 16, 1024), dk = smem_desc_sw128(sRing, 16, 1024);
-  long long n = 0;
+  uint32_t n = 0;
   uint32_t q_it = 0;
   bool ok = true;
   for (Pieces w(p, r); ok && w.next(); w.advance()) {
     for (long long t = w.t0; ok && t < w.t1; ++t, ++n) {
       const int b = int(n & 1);
-      ok = mbar_wait_cluster(bar(m.s_free[b]), (uint32_t(n >> 1) & 1) ^ 1, abort, kTimeoutNs);
+      ok = mbar_wait_cluster(bar(m.s_free[b]), ((n >> 1) & 1) ^ 1, abort, kTimeoutNs);
       if (ok && t == w.t0) {
         ok = mbar_wait_cluster(bar(m.q_full), q_it & 1, abort, kTimeoutNs);
         ++q_it;
       }
-      const long long u0 = k_unit(n);
-      for (int kb = 0; ok && kb < kKUnits; ++kb) {
-        const int s = int((u0 + kb) % kRing);
-        ok = mbar_wait_cluster(bar(m.full[s]), uint32_t((u0 + kb) / kRing) & 1, abort, kTimeoutNs);
+      Place at(k_unit(n));
+      for (int kb = 0; ok && kb < kKUnits; ++kb, at.step()) {
+        const int s = at.s;
+        ok = mbar_wait_cluster(bar(m.full[s]), at.phase, abort, kTimeoutNs);
         if (!ok) break;
         tc_fence_after();
 #pragma unroll
@@ -256,18 +270,18 @@ __device__ __forceinline__ void pv_mmas(const DecodeParams &p, const CtaRange &r
   const uint64_t dp = smem_desc_sw128(sP, 16, 1024);
   // V, MN-major: 64-dim blocks 1 KB apart, 8-token groups 4 KB apart
   const uint64_t dv = smem_desc_sw128(sRing, 1024, 4096);
-  const long long total = total_tiles(p, r);
-  long long n = 0;
+  const uint32_t total = total_tiles(p, r);
+  uint32_t n = 0;
   uint32_t o_it = 0;
   bool ok = true;
   for (Pieces w(p, r); ok && w.next(); w.advance(), ++o_it) {
     for (long long t = w.t0; ok && t < w.t1; ++t, ++n) {
-      ok = mbar_wait_cluster(bar(m.p_full), uint32_t(n) & 1, abort, kTimeoutNs);
+      ok = mbar_wait_cluster(bar(m.p_full), n & 1, abort, kTimeoutNs);
       if (ok && t == w.t0) ok = mbar_wait_cluster(bar(m.o_free), (o_it & 1) ^ 1, abort, kTimeoutNs);
-      const long long u0 = v_unit(n, total);
-      for (int u = 0; ok && u < kVUnits; ++u) {
-        const int s = int((u0 + u) % kRing);
-        ok = mbar_wait_cluster(bar(m.full[s]), uint32_t((u0 + u) / kRing) & 1, abort, kTimeoutNs);
+      Place at(v_unit(n, total));
+      for (int u = 0; ok && u < kVUnits; ++u, at.step()) {
+        const int s = at.s;
+        ok = mbar_wait_cluster(bar(m.full[s]), at.phase, abort, kTimeoutNs);
         if (!ok) break;
         tc_fence_after();
 #pragma unroll
@@ -330,7 +344,7 @@ __device__ __forceinline__ void softmax(const DecodeParams &p, const CtaRange &r
   unsigned char *prow = smem + kOffP + pb * kRows * 128 + row * 128;
   const uint32_t s_free0 = map_to_rank(bar(m.s_free[0]), 0), s_free1 = map_to_rank(bar(m.s_free[1]), 0);
   const uint32_t p_full = map_to_rank(bar(m.p_full), 0), o_free = map_to_rank(bar(m.o_free), 0);
-  long long n = 0;
+  uint32_t n = 0;
   uint32_t o_it = 0;
   bool ok = true;
   for (Pieces w(p, r); w.next(); w.advance(), ++o_it) {
@@ -340,7 +354,7 @@ __device__ __forceinline__ void softmax(const DecodeParams &p, const CtaRange &r
     float mrun = -INFINITY, ell = 0.f, ellx = 0.f;
     for (long long t = w.t0; t < w.t1; ++t, ++n) {
       const int b = int(n & 1);
-      ok = ok && __all_sync(0xffffffffu, mbar_wait_cluster(bar(m.s_full[b]), uint32_t(n >> 1) & 1, abort, kTimeoutNs));
+      ok = ok && __all_sync(0xffffffffu, mbar_wait_cluster(bar(m.s_full[b]), (n >> 1) & 1, abort, kTimeoutNs));
       float x[64];
       if (ok) {
         tc_fence_after();
@@ -401,7 +415,7 @@ __device__ __forceinline__ void softmax(const DecodeParams &p, const CtaRange &r
       // P's buffer and O are free once the previous tile's products are done
       if (n > 0)
         ok = ok && __all_sync(0xffffffffu,
-                              mbar_wait_cluster(bar(m.p_free), uint32_t(n - 1) & 1, abort, kTimeoutNs));
+                              mbar_wait_cluster(bar(m.p_free), (n - 1) & 1, abort, kTimeoutNs));
       if (ok) {
         if (__any_sync(0xffffffffu, resc)) {
           tc_fence_after();
@@ -539,9 +553,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   __syncthreads();
   cluster_sync();
   if (warp == 1) {
+    __syncwarp();
     tc_fence_after();
     tmem_dealloc_pair(tmem, 512);
   }
+  cluster_sync();  // the pair leaves together: neither SM takes another CTA before both gave up their TMEM
 }
 
 }  // namespace

@@ -32,7 +32,9 @@ struct PagesWorkspace {
   int32_t *holes;       // the same memory, as one list (compaction)
   int32_t *movers;      // [num_pages], by rank among the live pages
   int32_t *rank;        // [num_pages]: a live page's rank
+  int32_t *fork_count;  // the same memory as movers and rank: forks that need a page, by blocks
 };
+constexpr int kMaxForks = 1 << 19;  // what a one-chunk workspace's fork_count holds
 
 constexpr size_t pages_workspace_bytes(int num_pages) {
   const size_t c = size_t(pages_chunks(num_pages));
@@ -46,7 +48,7 @@ inline PagesWorkspace pages_workspace(void *base, int num_pages) {
   w.totals = p;
   w.chunk_free = p + 64;
   w.free_list = w.holes = w.chunk_free + (c + 63) / 64 * 64;
-  w.movers = w.free_list + c * kPagesChunk;
+  w.movers = w.fork_count = w.free_list + c * kPagesChunk;
   w.rank = w.movers + c * kPagesChunk;
   return w;
 }

@@ -48,6 +48,7 @@ def test_null_and_misaligned_pointers(lib):  # noqa: F811
 def test_bad_arguments(lib):  # noqa: F811
     got = calls(lib, desc(), n=-1)
     assert got["copy"] == got["fork"] == -6
+    assert calls(lib, desc(), n=(1 << 19) + 1)["fork"] == -6
     assert calls(lib, desc(), window=-1)["free"] == calls(lib, desc(), sinks=-1)["free"] == -6
     assert lib.mla_pages_copy(FAKE, FAKE, FAKE, FAKE, 1, 0, desc(), None, None) == -2
     short = mla.pages_workspace_size(16) - 1

@@ -132,7 +132,7 @@ def test_compact(kv_dtype, rows, pages):
     err, want, n, m = po.compact(p.host[0], p.host[1], p.host[3])
     p.check(err)
     np.testing.assert_array_equal(remap.cpu().numpy(), want)
-    assert totals.tolist() == [n, m]
+    assert totals[:8].view(torch.int32).tolist() == [n, m]
 
 
 @pytest.mark.parametrize("live", ["none", "all"])
