@@ -56,7 +56,7 @@ constexpr uint64_t kDrainNs = 200000000ull;
 constexpr float kRescaleThreshold = 8.f;        // base-2 units
 
 struct Misc {
-  uint64_t full[kRing], empty[kRing], q_full, q_empty, s_full[2], s_free[2];
+  uint64_t full[2][kRing], empty[kRing], q_full, q_empty, s_full[2], s_free[2];
   uint64_t p_full, p_free, o_full, o_free, drain;
   uint32_t tmem_base;
   int abort;
@@ -107,23 +107,23 @@ __device__ __forceinline__ uint32_t total_tiles(const DecodeParams &p, const Cta
 }
 
 // Units in load order: K_0, K_1, V_0, K_2, V_1, ...  First unit of K_n and V_n.
-// (32-bit counters: the issuing threads pay for every division.)
 __device__ __forceinline__ uint32_t k_unit(uint32_t n) { return n == 0 ? 0 : kKUnits + 17 * (n - 1); }
 __device__ __forceinline__ uint32_t v_unit(uint32_t n, uint32_t total) {
   return kKUnits + 17 * n + (n < total - 1 ? kKUnits : 0);
 }
-// A place in the ring: slot and the parity of its phase.
-struct Place {
-  int s;
-  uint32_t phase;
-  __device__ explicit Place(uint32_t unit) : s(int(unit % kRing)), phase((unit / kRing) & 1) {}
-  __device__ __forceinline__ void step() {
-    if (++s == kRing) {
-      s = 0;
-      phase ^= 1;
-    }
+// A slot has one "landed" barrier for K units and one for V units: the score
+// and PV threads wait at their own pace, and a barrier shared by both kinds
+// could complete a phase that one of them has not looked at yet, which its
+// parity cannot tell from the phase before.
+struct Landed {
+  uint32_t phases = 0;  // bit s: parity of the kind's next use of slot s
+  __device__ __forceinline__ uint32_t take(int s) {
+    const uint32_t ph = (phases >> s) & 1u;
+    phases ^= 1u << s;
+    return ph;
   }
 };
+__device__ __forceinline__ int next_slot(int s) { return s + 1 == kRing ? 0 : s + 1; }
 
 // ------------------------------------------------------------------ producer
 
@@ -167,24 +167,27 @@ __device__ __forceinline__ void produce(const DecodeParams &p, const CtaRange &r
   volatile int *abort = &m.abort;
   const int lane = threadIdx.x & 31;
   const bool leader = rank == 0;
-  Place at(0);
+  int at = 0;
+  uint32_t lap = 1;  // parity of the empty barriers' last phase
   uint32_t q_it = 0;
   bool ok = true;
-  const uint32_t full0 = map_to_rank(bar(m.full[0]), 0);
-  // slot of the next unit, emptied; the even CTA announces both CTAs' bytes
-  auto slot = [&](uint32_t *full) {
-    const int s = at.s;
-    const bool got = mbar_wait_cluster(bar(m.empty[s]), at.phase ^ 1, abort, kTimeoutNs);
+  const uint32_t full0 = map_to_rank(bar(m.full[0][0]), 0);
+  // slot of the next unit (kind 0: K, 1: V), emptied; the even CTA announces
+  // both CTAs' bytes
+  auto slot = [&](int kind, uint32_t *full) {
+    const int s = at;
+    const bool got = mbar_wait(bar(m.empty[s]), lap, abort, kTimeoutNs);
     if (!__all_sync(0xffffffffu, got)) return -1;
-    if (leader && lane == 0) mbar_arrive_expect_tx(bar(m.full[s]), 2 * kUnitBytes);
+    if (leader && lane == 0) mbar_arrive_expect_tx(bar(m.full[kind][s]), 2 * kUnitBytes);
     __syncwarp();
-    *full = full0 + 8 * s;
-    at.step();
+    *full = full0 + 8 * (kind * kRing + s);
+    at = next_slot(s);
+    if (at == 0) lap ^= 1;
     return s;
   };
   auto load_k = [&](const TileWalk &c) {
     if (c.first()) {
-      if (!__all_sync(0xffffffffu, mbar_wait_cluster(bar(m.q_empty), (q_it & 1) ^ 1, abort, kTimeoutNs)))
+      if (!__all_sync(0xffffffffu, mbar_wait(bar(m.q_empty), (q_it & 1) ^ 1, abort, kTimeoutNs)))
         return false;
       ++q_it;
       if (leader && lane == 0) mbar_arrive_expect_tx(bar(m.q_full), 2 * kQBytes);
@@ -196,7 +199,7 @@ __device__ __forceinline__ void produce(const DecodeParams &p, const CtaRange &r
     const int pg = __shfl_sync(0xffffffffu, c.page, 2 * rank + (lane & 1));
     for (int kb = 0; kb < kKUnits; ++kb) {
       uint32_t full;
-      const int s = slot(&full);
+      const int s = slot(0, &full);
       if (s < 0) return false;
       if (lane < 2) tma_load_4d_pair(sRing + s * kUnitBytes + lane * 8192, tm_k, full, 0, 0, kb, pg * 8);
     }
@@ -206,7 +209,7 @@ __device__ __forceinline__ void produce(const DecodeParams &p, const CtaRange &r
     for (int u = 0; u < kVUnits; ++u) {
       uint32_t full;
       const int pg = __shfl_sync(0xffffffffu, page, u >> 1);
-      const int s = slot(&full);
+      const int s = slot(1, &full);
       if (s < 0) return false;
       if (lane == 0)
         tma_load_4d_pair(sRing + s * kUnitBytes, tm_v, full, 0, 0, 4 * int(rank), pg * 8 + 4 * (u & 1));
@@ -231,21 +234,21 @@ __device__ __forceinline__ void score_mmas(const DecodeParams &p, const CtaRange
   volatile int *abort = &m.abort;
   const uint32_t idesc = idesc_bf16_f32(128, 256, false, false);
   const uint64_t dq = smem_desc_sw128(sQ, 16, 1024), dk = smem_desc_sw128(sRing, 16, 1024);
+  Landed landed;
   uint32_t n = 0;
   uint32_t q_it = 0;
   bool ok = true;
   for (Pieces w(p, r); ok && w.next(); w.advance()) {
     for (long long t = w.t0; ok && t < w.t1; ++t, ++n) {
       const int b = int(n & 1);
-      ok = mbar_wait_cluster(bar(m.s_free[b]), ((n >> 1) & 1) ^ 1, abort, kTimeoutNs);
+      ok = mbar_wait(bar(m.s_free[b]), ((n >> 1) & 1) ^ 1, abort, kTimeoutNs);
       if (ok && t == w.t0) {
-        ok = mbar_wait_cluster(bar(m.q_full), q_it & 1, abort, kTimeoutNs);
+        ok = mbar_wait(bar(m.q_full), q_it & 1, abort, kTimeoutNs);
         ++q_it;
       }
-      Place at(k_unit(n));
-      for (int kb = 0; ok && kb < kKUnits; ++kb, at.step()) {
-        const int s = at.s;
-        ok = mbar_wait_cluster(bar(m.full[s]), at.phase, abort, kTimeoutNs);
+      int s = int(k_unit(n) % kRing);
+      for (int kb = 0; ok && kb < kKUnits; ++kb, s = next_slot(s)) {
+        ok = mbar_wait(bar(m.full[0][s]), landed.take(s), abort, kTimeoutNs);
         if (!ok) break;
         tc_fence_after();
 #pragma unroll
@@ -271,17 +274,17 @@ __device__ __forceinline__ void pv_mmas(const DecodeParams &p, const CtaRange &r
   // V, MN-major: 64-dim blocks 1 KB apart, 8-token groups 4 KB apart
   const uint64_t dv = smem_desc_sw128(sRing, 1024, 4096);
   const uint32_t total = total_tiles(p, r);
+  Landed landed;
   uint32_t n = 0;
   uint32_t o_it = 0;
   bool ok = true;
   for (Pieces w(p, r); ok && w.next(); w.advance(), ++o_it) {
     for (long long t = w.t0; ok && t < w.t1; ++t, ++n) {
-      ok = mbar_wait_cluster(bar(m.p_full), n & 1, abort, kTimeoutNs);
-      if (ok && t == w.t0) ok = mbar_wait_cluster(bar(m.o_free), (o_it & 1) ^ 1, abort, kTimeoutNs);
-      Place at(v_unit(n, total));
-      for (int u = 0; ok && u < kVUnits; ++u, at.step()) {
-        const int s = at.s;
-        ok = mbar_wait_cluster(bar(m.full[s]), at.phase, abort, kTimeoutNs);
+      ok = mbar_wait(bar(m.p_full), n & 1, abort, kTimeoutNs);
+      if (ok && t == w.t0) ok = mbar_wait(bar(m.o_free), (o_it & 1) ^ 1, abort, kTimeoutNs);
+      int s = int(v_unit(n, total) % kRing);
+      for (int u = 0; ok && u < kVUnits; ++u, s = next_slot(s)) {
+        ok = mbar_wait(bar(m.full[1][s]), landed.take(s), abort, kTimeoutNs);
         if (!ok) break;
         tc_fence_after();
 #pragma unroll
@@ -354,7 +357,7 @@ __device__ __forceinline__ void softmax(const DecodeParams &p, const CtaRange &r
     float mrun = -INFINITY, ell = 0.f, ellx = 0.f;
     for (long long t = w.t0; t < w.t1; ++t, ++n) {
       const int b = int(n & 1);
-      ok = ok && __all_sync(0xffffffffu, mbar_wait_cluster(bar(m.s_full[b]), (n >> 1) & 1, abort, kTimeoutNs));
+      ok = ok && __all_sync(0xffffffffu, mbar_wait(bar(m.s_full[b]), (n >> 1) & 1, abort, kTimeoutNs));
       float x[64];
       if (ok) {
         tc_fence_after();
@@ -415,7 +418,7 @@ __device__ __forceinline__ void softmax(const DecodeParams &p, const CtaRange &r
       // P's buffer and O are free once the previous tile's products are done
       if (n > 0)
         ok = ok && __all_sync(0xffffffffu,
-                              mbar_wait_cluster(bar(m.p_free), (n - 1) & 1, abort, kTimeoutNs));
+                              mbar_wait(bar(m.p_free), (n - 1) & 1, abort, kTimeoutNs));
       if (ok) {
         if (__any_sync(0xffffffffu, resc)) {
           tc_fence_after();
@@ -440,7 +443,7 @@ __device__ __forceinline__ void softmax(const DecodeParams &p, const CtaRange &r
     const float sumx = (m.red[1][0][row] + m.red[1][1][row]) + (m.red[1][2][row] + m.red[1][3][row]);
     named_sync(1, kSoftThreads);  // read before the next piece writes maxima
     const float inv = sum > 0.f ? 1.f / sum : 0.f;
-    ok = ok && __all_sync(0xffffffffu, mbar_wait_cluster(bar(m.o_full), o_it & 1, abort, kTimeoutNs));
+    ok = ok && __all_sync(0xffffffffu, mbar_wait(bar(m.o_full), o_it & 1, abort, kTimeoutNs));
     const int c_first = sched_owner(w.pv, r.total, r.g_eff);
     if (ok) {
       tc_fence_after();
@@ -489,7 +492,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 
   if (tid == 0) {
     for (int s = 0; s < kRing; ++s) {
-      mbar_init(bar(m.full[s]), 1);
+      mbar_init(bar(m.full[0][s]), 1);
+      mbar_init(bar(m.full[1][s]), 1);
       mbar_init(bar(m.empty[s]), 1);
     }
     for (int b = 0; b < 2; ++b) {
@@ -506,7 +510,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     m.abort = 0;
     fence_barrier_init();
   }
+  // Allocating TMEM for a pair acts on both SMs: the other CTA has to be
+  // running by then.
+  __syncthreads();
+  cluster_sync();
   if (warp == 1) {
+    __syncwarp();
     tmem_alloc_pair(smem_u32(&m.tmem_base), 512);
     tmem_relinquish_pair();
   }
