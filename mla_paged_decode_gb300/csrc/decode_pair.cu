@@ -22,11 +22,13 @@
 // (lane l of TMEM, half g) handles the 64 tokens of page 2 (l / 64) + g for row
 // l mod 64: four threads share a row, and exchange their maxima through shared
 // memory once a tile.  O is rescaled only when a row's maximum grew by more
-// than 2^8, as in the decode kernel.  Per tile i: S_i -> softmax -> P_i (one
-// buffer, free when PV_{i-1} is done) -> PV_i, while S_{i+1} runs.
+// than 2^8, as in the decode kernel.  Per tile i: S_i -> softmax -> P_i -> PV_i,
+// while S_{i+1} runs.  P has one buffer, handed over page by page (p_full,
+// p_free): P_{i+1} of a page is written while PV_i works on the next ones, and
+// PV_{i+1} follows PV_i without a gap.
 //
 // Work is split as in the decode kernel: the tiles of all blocks in one line,
-// cut into equal ranges, one per pair; every piece leaves an fp32 partial.
+// cut into equal ranges, one per cluster; every piece leaves an fp32 partial.
 #include "common.cuh"
 #include "sm100.cuh"
 #include "splits.cuh"
@@ -37,7 +39,7 @@ using namespace sm100;
 namespace pair {
 constexpr int kThreads = 384;
 constexpr int kRows = 64;                       // per CTA
-constexpr int kBlockRows = 128;                 // per pair
+constexpr int kPairRows = 128;                  // per pair
 constexpr int kTilePages = 4;
 constexpr int kUnitBytes = 16384;
 constexpr int kRing = 7;
@@ -57,7 +59,7 @@ constexpr float kRescaleThreshold = 8.f;        // base-2 units
 
 struct Misc {
   uint64_t full[2][kRing], empty[kRing], q_full, q_empty, s_full[2], s_free[2];
-  uint64_t p_full, p_free, o_full, o_free, drain;
+  uint64_t p_full[kTilePages], p_free[kTilePages], o_ready[2], o_full, o_free, drain;
   uint32_t tmem_base;
   int abort;
   float red[2][4][kRows];  // row maxima by page, double-buffered; then row sums
@@ -73,11 +75,19 @@ using namespace pair;
 
 __device__ __forceinline__ uint32_t bar(uint64_t &b) { return smem_u32(&b); }
 
+template <int NP>
 __device__ __forceinline__ int block_tiles(const DecodeParams &p, int v) {
-  return (shared_block<kBlockRows>(p, v).tiles + kTilePages - 1) / kTilePages;
+  return (shared_block<NP * kPairRows>(p, v).tiles + kTilePages - 1) / kTilePages;
 }
 
-// The pieces of this pair's range, in order.
+// This CTA's place: its rank in the cluster, its half of the pair's operands.
+struct Seat {
+  uint32_t rank, half, leader;  // leader: the even CTA of the pair
+  uint16_t pair_mask;           // both CTAs of the pair
+};
+
+// The pieces of this cluster's range, in order.
+template <int NP>
 struct Pieces {
   const DecodeParams &p;
   const CtaRange &r;
@@ -87,7 +97,7 @@ struct Pieces {
   __device__ Pieces(const DecodeParams &p_, const CtaRange &r_) : p(p_), r(r_), v(r_.v_begin), pv(r_.p_begin) {}
   __device__ bool next() {
     while (v < p.pair_blocks && pv < r.end) {
-      view = shared_block<kBlockRows>(p, v);
+      view = shared_block<NP * kPairRows>(p, v);
       tiles = (view.tiles + kTilePages - 1) / kTilePages;
       if (tiles == 0) { ++v; continue; }
       t0 = max(r.start, pv) - pv;
@@ -100,9 +110,10 @@ struct Pieces {
   __device__ void advance() { pv += request_cost(tiles, kPieceTiles); ++v; }
 };
 
+template <int NP>
 __device__ __forceinline__ uint32_t total_tiles(const DecodeParams &p, const CtaRange &r) {
   uint32_t n = 0;
-  for (Pieces w(p, r); w.next(); w.advance()) n += uint32_t(w.t1 - w.t0);
+  for (Pieces<NP> w(p, r); w.next(); w.advance()) n += uint32_t(w.t1 - w.t0);
   return n;
 }
 
@@ -128,8 +139,9 @@ __device__ __forceinline__ int next_slot(int s) { return s + 1 == kRing ? 0 : s 
 // ------------------------------------------------------------------ producer
 
 // One position in the tiles of a range, with the pages of the tile in lanes 0..3.
+template <int NP>
 struct TileWalk {
-  Pieces w;
+  Pieces<NP> w;
   long long t;
   bool live;
   int page;
@@ -161,17 +173,20 @@ struct TileWalk {
   }
 };
 
+template <int NP>
 __device__ __forceinline__ void produce(const DecodeParams &p, const CtaRange &r, Misc &m, uint32_t sQ,
-                                        uint32_t sRing, uint32_t rank, const CUtensorMap *tm_q,
+                                        uint32_t sRing, const Seat &seat, const CUtensorMap *tm_q,
                                         const CUtensorMap *tm_k, const CUtensorMap *tm_v, int *err) {
   volatile int *abort = &m.abort;
   const int lane = threadIdx.x & 31;
-  const bool leader = rank == 0;
+  const bool leader = seat.half == 0;
+  const int pair = int(seat.rank >> 1);  // of the cluster
+  const uint16_t twins = uint16_t(5u << seat.half);  // the CTAs of both pairs with this half
   int at = 0;
   uint32_t lap = 1;  // parity of the empty barriers' last phase
   uint32_t q_it = 0;
   bool ok = true;
-  const uint32_t full0 = map_to_rank(bar(m.full[0][0]), 0);
+  const uint32_t full0 = map_to_rank(bar(m.full[0][0]), seat.leader);
   // slot of the next unit (kind 0: K, 1: V), emptied; the even CTA announces
   // both CTAs' bytes
   auto slot = [&](int kind, uint32_t *full) {
@@ -185,23 +200,28 @@ __device__ __forceinline__ void produce(const DecodeParams &p, const CtaRange &r
     if (at == 0) lap ^= 1;
     return s;
   };
-  auto load_k = [&](const TileWalk &c) {
+  auto load_k = [&](const TileWalk<NP> &c) {
     if (c.first()) {
-      if (!__all_sync(0xffffffffu, mbar_wait(bar(m.q_empty), (q_it & 1) ^ 1, abort, kTimeoutNs)))
-        return false;
+      if (!__all_sync(0xffffffffu, mbar_wait(bar(m.q_empty), (q_it & 1) ^ 1, abort, kTimeoutNs))) return false;
       ++q_it;
       if (leader && lane == 0) mbar_arrive_expect_tx(bar(m.q_full), 2 * kQBytes);
       __syncwarp();
       if (lane < 9)
-        tma_load_2d_pair(sQ + lane * kRows * 128, tm_q, map_to_rank(bar(m.q_full), 0), lane * 64,
-                         c.w.view.row0 + int(rank) * kRows);
+        tma_load_2d_pair(sQ + lane * kRows * 128, tm_q, map_to_rank(bar(m.q_full), seat.leader), lane * 64,
+                         c.w.view.row0 + int(seat.rank) * kRows);
     }
-    const int pg = __shfl_sync(0xffffffffu, c.page, 2 * rank + (lane & 1));
+    // the unit's two pages; with two pairs each loads one of them for both
+    const int pg = __shfl_sync(0xffffffffu, c.page, 2 * seat.half + (NP == 2 ? pair : (lane & 1)));
     for (int kb = 0; kb < kKUnits; ++kb) {
       uint32_t full;
       const int s = slot(0, &full);
       if (s < 0) return false;
-      if (lane < 2) tma_load_4d_pair(sRing + s * kUnitBytes + lane * 8192, tm_k, full, 0, 0, kb, pg * 8);
+      if (NP == 2) {
+        if (lane == 0)
+          tma_load_4d_pair_multicast(sRing + s * kUnitBytes + pair * 8192, tm_k, full, 0, 0, kb, pg * 8, twins);
+      } else if (lane < 2) {
+        tma_load_4d_pair(sRing + s * kUnitBytes + lane * 8192, tm_k, full, 0, 0, kb, pg * 8);
+      }
     }
     return true;
   };
@@ -211,12 +231,18 @@ __device__ __forceinline__ void produce(const DecodeParams &p, const CtaRange &r
       const int pg = __shfl_sync(0xffffffffu, page, u >> 1);
       const int s = slot(1, &full);
       if (s < 0) return false;
-      if (lane == 0)
-        tma_load_4d_pair(sRing + s * kUnitBytes, tm_v, full, 0, 0, 4 * int(rank), pg * 8 + 4 * (u & 1));
+      if (lane == 0) {
+        const int atom = pg * 8 + 4 * (u & 1);
+        if (NP == 2)
+          tma_load_4d_pair_multicast(sRing + s * kUnitBytes + pair * 8192, tm_v, full, 0, 0, 4 * int(seat.half),
+                                     atom + 2 * pair, twins);
+        else
+          tma_load_4d_pair(sRing + s * kUnitBytes, tm_v, full, 0, 0, 4 * int(seat.half), atom);
+      }
     }
     return true;
   };
-  TileWalk c(p, r, err);
+  TileWalk<NP> c(p, r, err);
   if (c.live) ok = load_k(c);  // (a range may hold no tile, only a piece's cost)
   while (ok && c.live) {
     const int page = c.page;
@@ -229,16 +255,18 @@ __device__ __forceinline__ void produce(const DecodeParams &p, const CtaRange &r
 
 // ------------------------------------------------------------------ MMAs (even CTA)
 
+template <int NP>
 __device__ __forceinline__ void score_mmas(const DecodeParams &p, const CtaRange &r, Misc &m, uint32_t sQ,
-                                           uint32_t sRing, uint32_t tmem, int *err) {
+                                           uint32_t sRing, uint32_t tmem, const Seat &seat, int *err) {
   volatile int *abort = &m.abort;
+  constexpr uint16_t kAll = (1u << (2 * NP)) - 1;  // a ring slot is free when every pair has read it
   const uint32_t idesc = idesc_bf16_f32(128, 256, false, false);
   const uint64_t dq = smem_desc_sw128(sQ, 16, 1024), dk = smem_desc_sw128(sRing, 16, 1024);
   Landed landed;
   uint32_t n = 0;
   uint32_t q_it = 0;
   bool ok = true;
-  for (Pieces w(p, r); ok && w.next(); w.advance()) {
+  for (Pieces<NP> w(p, r); ok && w.next(); w.advance()) {
     for (long long t = w.t0; ok && t < w.t1; ++t, ++n) {
       const int b = int(n & 1);
       ok = mbar_wait(bar(m.s_free[b]), ((n >> 1) & 1) ^ 1, abort, kTimeoutNs);
@@ -255,55 +283,59 @@ __device__ __forceinline__ void score_mmas(const DecodeParams &p, const CtaRange
         for (int ks = 0; ks < 4; ++ks)
           mma_bf16_ss_pair(tmem + kColS + 128 * b, dq + ((kb * kRows * 128 + ks * 32) >> 4),
                            dk + ((s * kUnitBytes + ks * 32) >> 4), idesc, kb > 0 || ks > 0);
-        mma_commit_pair(bar(m.empty[s]));
+        mma_commit_pair(bar(m.empty[s]), kAll);
       }
       if (!ok) break;
-      mma_commit_pair(bar(m.s_full[b]));
-      if (t == w.t1 - 1) mma_commit_pair(bar(m.q_empty));
+      mma_commit_pair(bar(m.s_full[b]), seat.pair_mask);
+      if (t == w.t1 - 1) mma_commit_pair(bar(m.q_empty), seat.pair_mask);
     }
   }
   if (!ok) atomicOr(err, kErrTimeout);
-  mma_commit_pair(bar(m.drain));
+  mma_commit_pair(bar(m.drain), seat.pair_mask);
 }
 
+template <int NP>
 __device__ __forceinline__ void pv_mmas(const DecodeParams &p, const CtaRange &r, Misc &m, uint32_t sP,
-                                        uint32_t sRing, uint32_t tmem, int *err) {
+                                        uint32_t sRing, uint32_t tmem, const Seat &seat, int *err) {
   volatile int *abort = &m.abort;
+  constexpr uint16_t kAll = (1u << (2 * NP)) - 1;
   const uint32_t idesc = idesc_bf16_f32(128, 256, false, true);
   const uint64_t dp = smem_desc_sw128(sP, 16, 1024);
   // V, MN-major: 64-dim blocks 1 KB apart, 8-token groups 4 KB apart
   const uint64_t dv = smem_desc_sw128(sRing, 1024, 4096);
-  const uint32_t total = total_tiles(p, r);
+  const uint32_t total = total_tiles<NP>(p, r);
   Landed landed;
   uint32_t n = 0;
   uint32_t o_it = 0;
   bool ok = true;
-  for (Pieces w(p, r); ok && w.next(); w.advance(), ++o_it) {
+  for (Pieces<NP> w(p, r); ok && w.next(); w.advance(), ++o_it) {
     for (long long t = w.t0; ok && t < w.t1; ++t, ++n) {
-      ok = mbar_wait(bar(m.p_full), n & 1, abort, kTimeoutNs);
+      ok = mbar_wait(bar(m.o_ready[n & 1]), (n >> 1) & 1, abort, kTimeoutNs);
       if (ok && t == w.t0) ok = mbar_wait(bar(m.o_free), (o_it & 1) ^ 1, abort, kTimeoutNs);
       int s = int(v_unit(n, total) % kRing);
-      for (int u = 0; ok && u < kVUnits; ++u, s = next_slot(s)) {
-        ok = mbar_wait(bar(m.full[1][s]), landed.take(s), abort, kTimeoutNs);
-        if (!ok) break;
-        tc_fence_after();
+      for (int pg = 0; ok && pg < kTilePages; ++pg) {
+        ok = mbar_wait(bar(m.p_full[pg]), n & 1, abort, kTimeoutNs);
+        for (int h = 0; ok && h < 2; ++h, s = next_slot(s)) {  // a page's two units of 32 tokens
+          ok = mbar_wait(bar(m.full[1][s]), landed.take(s), abort, kTimeoutNs);
+          if (!ok) break;
+          tc_fence_after();
 #pragma unroll
-        for (int ks = 0; ks < 2; ++ks)
+          for (int ks = 0; ks < 2; ++ks)
 #pragma unroll
-          for (int j = 0; j < 2; ++j)
-            mma_bf16_ss_pair(tmem + kColO + 128 * j,
-                             dp + (((u >> 1) * kRows * 128 + ((u & 1) * 2 + ks) * 32) >> 4),
-                             dv + ((s * kUnitBytes + ks * 8192 + j * 2048) >> 4), idesc,
-                             t > w.t0 || u > 0 || ks > 0);
-        mma_commit_pair(bar(m.empty[s]));
+            for (int j = 0; j < 2; ++j)
+              mma_bf16_ss_pair(tmem + kColO + 128 * j, dp + ((pg * kRows * 128 + (h * 2 + ks) * 32) >> 4),
+                               dv + ((s * kUnitBytes + ks * 8192 + j * 2048) >> 4), idesc,
+                               t > w.t0 || pg > 0 || h > 0 || ks > 0);
+          mma_commit_pair(bar(m.empty[s]), kAll);
+        }
+        if (ok) mma_commit_pair(bar(m.p_free[pg]), seat.pair_mask);
       }
       if (!ok) break;
-      mma_commit_pair(bar(m.p_free));
-      if (t == w.t1 - 1) mma_commit_pair(bar(m.o_full));
+      if (t == w.t1 - 1) mma_commit_pair(bar(m.o_full), seat.pair_mask);
     }
   }
   if (!ok) atomicOr(err, kErrTimeout);
-  mma_commit_pair(bar(m.drain));
+  mma_commit_pair(bar(m.drain), seat.pair_mask);
 }
 
 // ------------------------------------------------------------------ softmax and epilogue
@@ -335,8 +367,9 @@ __device__ __forceinline__ void st_global_v8(float *dst, const float (&v)[8]) {
 
 // A failed wait never leaves the loop: the warp goes on without working, so
 // that the others find it at their barriers (later waits fail at once).
+template <int NP>
 __device__ __forceinline__ void softmax(const DecodeParams &p, const CtaRange &r, Misc &m, unsigned char *smem,
-                                        uint32_t tmem, uint32_t rank, int pair_id, int *err) {
+                                        uint32_t tmem, const Seat &seat, int cluster, int *err) {
   volatile int *abort = &m.abort;
   const int st = int(threadIdx.x) - 128, warp = st >> 5, lane = st & 31;  // warps 0..7
   const int g = warp >> 2, q = warp & 3;             // column half, TMEM quarter (lanes 32q ..)
@@ -345,15 +378,17 @@ __device__ __forceinline__ void softmax(const DecodeParams &p, const CtaRange &r
   const uint32_t t_s = tmem + lanes + kColS + 64 * g, t_o = tmem + lanes + kColO + 128 * g;
   const float cs = p.score_scale_log2;
   unsigned char *prow = smem + kOffP + pb * kRows * 128 + row * 128;
-  const uint32_t s_free0 = map_to_rank(bar(m.s_free[0]), 0), s_free1 = map_to_rank(bar(m.s_free[1]), 0);
-  const uint32_t p_full = map_to_rank(bar(m.p_full), 0), o_free = map_to_rank(bar(m.o_free), 0);
+  const uint32_t s_free0 = map_to_rank(bar(m.s_free[0]), seat.leader);
+  const uint32_t s_free1 = map_to_rank(bar(m.s_free[1]), seat.leader);
+  const uint32_t p_full = map_to_rank(bar(m.p_full[pb]), seat.leader);
+  const uint32_t o_ready = map_to_rank(bar(m.o_ready[0]), seat.leader), o_free = map_to_rank(bar(m.o_free), seat.leader);
   uint32_t n = 0;
   uint32_t o_it = 0;
   bool ok = true;
-  for (Pieces w(p, r); w.next(); w.advance(), ++o_it) {
-    const int grow = w.view.row0 + int(rank) * kRows + row;
+  for (Pieces<NP> w(p, r); w.next(); w.advance(), ++o_it) {
+    const int grow = w.view.row0 + int(seat.rank) * kRows + row;
     const int hi = row_view(p, w.view, min(grow, p.batch * p.heads - 1)).hi;
-    const bool mine = int(rank) * kRows + row < w.view.rows;
+    const bool mine = int(seat.rank) * kRows + row < w.view.rows;
     float mrun = -INFINITY, ell = 0.f, ellx = 0.f;
     for (long long t = w.t0; t < w.t1; ++t, ++n) {
       const int b = int(n & 1);
@@ -415,21 +450,29 @@ __device__ __forceinline__ void softmax(const DecodeParams &p, const CtaRange &r
       }
       ell = ell * alpha + (lsum[0] + lsum[1]);
       ellx = ellx * alpha + (xsum[0] + xsum[1]);
-      // P's buffer and O are free once the previous tile's products are done
-      if (n > 0)
-        ok = ok && __all_sync(0xffffffffu,
-                              mbar_wait(bar(m.p_free), (n - 1) & 1, abort, kTimeoutNs));
-      if (ok) {
-        if (__any_sync(0xffffffffu, resc)) {
+      // O is this tile's to add to once every warp has said so: at once, or
+      // after the rare rescale, which waits for the previous tile's products.
+      // (Two barriers in turn: a warp may say so for tile i + 1 before the PV
+      // thread has asked about tile i, but not for i + 2.)
+      if (__any_sync(0xffffffffu, resc)) {
+        ok = ok && __all_sync(0xffffffffu, mbar_wait(bar(m.p_free[kTilePages - 1]), (n - 1) & 1, abort, kTimeoutNs));
+        if (ok) {
           tc_fence_after();
           rescale_rows(t_o, alpha);
+          tc_fence_before();
         }
+      }
+      __syncwarp();
+      if (ok && lane == 0) mbar_arrive_cluster(o_ready + 8 * b);
+      // the page's part of P is free once the previous tile's product with it is done
+      if (n > 0)
+        ok = ok && __all_sync(0xffffffffu, mbar_wait(bar(m.p_free[pb]), (n - 1) & 1, abort, kTimeoutNs));
+      if (ok) {
 #pragma unroll
         for (int c = 0; c < 8; ++c)
           *reinterpret_cast<uint4 *>(prow + ((c ^ (row & 7)) << 4)) =
               make_uint4(pk[4 * c], pk[4 * c + 1], pk[4 * c + 2], pk[4 * c + 3]);
         fence_proxy_async_smem();
-        tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive_cluster(p_full);
       }
@@ -447,7 +490,7 @@ __device__ __forceinline__ void softmax(const DecodeParams &p, const CtaRange &r
     const int c_first = sched_owner(w.pv, r.total, r.g_eff);
     if (ok) {
       tc_fence_after();
-      const size_t slot = 2 * size_t(pair_id + w.v) + rank;
+      const size_t slot = 2 * NP * size_t(cluster + w.v) + seat.rank;
       float *dst = slot_out_ptr(p) + (slot * kSlotHeads + row) * kDv + 256 * (q >> 1) + 128 * g;
 #pragma unroll 1
       for (int c = 0; c < 128; c += 32) {
@@ -468,16 +511,20 @@ __device__ __forceinline__ void softmax(const DecodeParams &p, const CtaRange &r
       __syncwarp();
       if (lane == 0) mbar_arrive_cluster(o_free);
       if (mine && pb == 0) slot_lse_ptr(p)[slot * kSlotHeads + row] = mrun + log2f(sumx);
-      if (st == 0 && rank == 0 && pair_id == c_first) {
+      if (st == 0 && seat.rank == 0 && cluster == c_first) {
         const int c_last = sched_owner(w.pv + w.tiles - 1, r.total, r.g_eff);
-        info_ptr(p)[p.batch * p.head_groups + w.v] = make_int4(c_first, c_last - c_first + 1, pair_id + w.v, 0);
+        info_ptr(p)[p.batch * p.head_groups + w.v] = make_int4(c_first, c_last - c_first + 1, cluster + w.v, 0);
       }
     }
   }
   if (!ok) atomicOr(err, kErrTimeout);
 }
 
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+// NP: pairs of a cluster.  Two pairs take 256 rows and walk the same tiles: each
+// CTA loads half of its units and multicasts them to its twin in the other pair,
+// which halves what is read from L2.
+template <int NP>
+__global__ void __launch_bounds__(kThreads, 1)
     decode_pair_kernel(const __grid_constant__ DecodeParams p, const __grid_constant__ CUtensorMap tm_q,
                        const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v) {
   extern __shared__ unsigned char smem_raw[];
@@ -486,24 +533,31 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   const uint32_t sbase = raw + pad;
   Misc &m = *reinterpret_cast<Misc *>(smem + kOffMisc);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const uint32_t rank = cluster_rank();
-  const int pair_id = int(blockIdx.x) >> 1;
+  Seat seat;
+  seat.rank = cluster_rank();
+  seat.half = seat.rank & 1u;
+  seat.leader = seat.rank & ~1u;
+  seat.pair_mask = uint16_t(3u << seat.leader);
+  const int cluster = int(blockIdx.x) / (2 * NP);
   int *err = error_word(p);
 
   if (tid == 0) {
     for (int s = 0; s < kRing; ++s) {
       mbar_init(bar(m.full[0][s]), 1);
       mbar_init(bar(m.full[1][s]), 1);
-      mbar_init(bar(m.empty[s]), 1);
+      mbar_init(bar(m.empty[s]), NP);
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(bar(m.s_full[b]), 1);
       mbar_init(bar(m.s_free[b]), 2 * kSoftWarps);
+      mbar_init(bar(m.o_ready[b]), 2 * kSoftWarps);
     }
     mbar_init(bar(m.q_full), 1);
     mbar_init(bar(m.q_empty), 1);
-    mbar_init(bar(m.p_full), 2 * kSoftWarps);
-    mbar_init(bar(m.p_free), 1);
+    for (int i = 0; i < kTilePages; ++i) {
+      mbar_init(bar(m.p_full[i]), 4);  // a page's two warps in each CTA
+      mbar_init(bar(m.p_free[i]), 1);
+    }
     mbar_init(bar(m.o_full), 1);
     mbar_init(bar(m.o_free), 2 * kSoftWarps);
     mbar_init(bar(m.drain), 2);
@@ -527,9 +581,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   asm volatile("griddepcontrol.wait;" ::: "memory");
   // blocks without pages have no partials
   for (int v = int(blockIdx.x) * kThreads + tid; v < p.pair_blocks; v += int(gridDim.x) * kThreads)
-    if (block_tiles(p, v) == 0) info_ptr(p)[p.batch * p.head_groups + v] = make_int4(-1, 0, 0, 0);
-  schedule_range<kPieceTiles>(p.pair_blocks, pair_id, p.pairs, [&](int v) { return block_tiles(p, v); }, &m.range,
-                             m.scratch);
+    if (block_tiles<NP>(p, v) == 0) info_ptr(p)[p.batch * p.head_groups + v] = make_int4(-1, 0, 0, 0);
+  schedule_range<kPieceTiles>(p.pair_blocks, cluster, p.clusters, [&](int v) { return block_tiles<NP>(p, v); },
+                              &m.range, m.scratch);
   tc_fence_before();
   cluster_sync();  // both CTAs' barriers and TMEM are ready
   tc_fence_after();
@@ -538,13 +592,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 
   if (r.start < r.end) {
     if (warp == 0) {
-      produce(p, r, m, sbase + kOffQ, sbase + kOffRing, rank, &tm_q, &tm_k, &tm_v, err);
+      produce<NP>(p, r, m, sbase + kOffQ, sbase + kOffRing, seat, &tm_q, &tm_k, &tm_v, err);
     } else if (warp == 1) {
-      if (rank == 0 && lane == 0) score_mmas(p, r, m, sbase + kOffQ, sbase + kOffRing, tmem, err);
+      if (seat.half == 0 && lane == 0) score_mmas<NP>(p, r, m, sbase + kOffQ, sbase + kOffRing, tmem, seat, err);
     } else if (warp == 2) {
-      if (rank == 0 && lane == 0) pv_mmas(p, r, m, sbase + kOffP, sbase + kOffRing, tmem, err);
+      if (seat.half == 0 && lane == 0) pv_mmas<NP>(p, r, m, sbase + kOffP, sbase + kOffRing, tmem, seat, err);
     } else if (warp >= 4) {
-      softmax(p, r, m, smem, tmem, rank, pair_id, err);
+      softmax<NP>(p, r, m, smem, tmem, seat, cluster, err);
     }
     // no MMA may still read this CTA's shared memory, and no copy write it:
     // the MMAs waited for every copy unless a wait gave up
@@ -569,24 +623,61 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   cluster_sync();  // the pair leaves together: neither SM takes another CTA before both gave up their TMEM
 }
 
+template <int NP>
+cudaLaunchConfig_t pair_config(int clusters, cudaStream_t stream, cudaLaunchAttribute (&attr)[2]) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(2 * NP * clusters);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = kSmemBytes;
+  cfg.stream = stream;
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2 * NP;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cfg;
+}
+
+template <int NP>
+cudaError_t ensure_smem() {
+  static SmemLimitOnce smem_limit;
+  return smem_limit.ensure(decode_pair_kernel<NP>, kSmemBytes);
+}
+
+template <int NP>
+cudaError_t launch(const DecodeParams &p, const CUtensorMap &tm_q, const CUtensorMap &tm_k, const CUtensorMap &tm_v,
+                   cudaStream_t stream) {
+  const cudaError_t e = ensure_smem<NP>();
+  if (e != cudaSuccess) return e;
+  cudaLaunchAttribute attr[2];
+  const cudaLaunchConfig_t cfg = pair_config<NP>(p.clusters, stream, attr);
+  return cudaLaunchKernelEx(&cfg, decode_pair_kernel<NP>, p, tm_q, tm_k, tm_v);
+}
+
+template <int NP>
+int resident_clusters() {
+  int n = 0;
+  cudaLaunchAttribute attr[2];
+  const cudaLaunchConfig_t cfg = pair_config<NP>(1, nullptr, attr);
+  if (ensure_smem<NP>() != cudaSuccess ||
+      cudaOccupancyMaxActiveClusters(&n, decode_pair_kernel<NP>, &cfg) != cudaSuccess) {
+    cudaGetLastError();  // leaves no error behind for the next launch
+    return 0;
+  }
+  return n;
+}
+
 }  // namespace
+
+// Clusters of `pairs` (1 or 2) CTA pairs that fit the current device at once
+// (0 on an error).
+int pair_clusters(int pairs) { return pairs == 2 ? resident_clusters<2>() : resident_clusters<1>(); }
 
 cudaError_t launch_decode_pair(const DecodeParams &p, const CUtensorMap &tm_q, const CUtensorMap &tm_k,
                                const CUtensorMap &tm_v, cudaStream_t stream) {
-  static SmemLimitOnce smem_limit;
-  const cudaError_t e = smem_limit.ensure(decode_pair_kernel, pair::kSmemBytes);
-  if (e != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(2 * p.pairs);
-  cfg.blockDim = dim3(pair::kThreads);
-  cfg.dynamicSmemBytes = pair::kSmemBytes;
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, decode_pair_kernel, p, tm_q, tm_k, tm_v);
+  return p.cluster_pairs == 2 ? launch<2>(p, tm_q, tm_k, tm_v, stream) : launch<1>(p, tm_q, tm_k, tm_v, stream);
 }
 
 }  // namespace mla

@@ -1070,7 +1070,7 @@ __device__ __forceinline__ void tc_softmax(const TcParams &tp, const CtaRange &r
       // after the pair kernel's slots
       if (p.view == kViewShared) {
         split = true;
-        si.slot = 2 * (p.pair_blocks + p.pairs) + int(blockIdx.x) + w.v;
+        si.slot = pair_slots(p) + int(blockIdx.x) + w.v;
       }
     } else {
       out_row0 = size_t(w.b) * p.heads + size_t(w.g) * kHeads;

@@ -222,15 +222,17 @@ __global__ void __launch_bounds__(kMergeWarps * 32, 7) shared_merge_kernel(Decod
   const int local = row - group_start(p, g) * p.heads;
   // slots of the two sets: first, stride, number; the row's place in them
   int first[2] = {0, 0}, num[2] = {0, 0}, hl[2] = {local & 63, r & 63};
-  const int stride = p.pair_blocks ? 2 : 1;  // a pair's piece has two slots, 64 rows each
+  const int stride = p.pair_blocks ? 2 * p.cluster_pairs : 1;  // a cluster's piece has a slot per CTA
   const int V = p.batch * p.head_groups + p.prefix_blocks;
   if (local >= 0) {
     const int blocks = p.pair_blocks ? p.pair_blocks : p.prefix_blocks;
-    const int v = p.pair_blocks ? block_base<128>(p, g) + (local >> 7) : block_base<64>(p, g) + (local >> 6);
+    const int v = p.cluster_pairs == 2   ? block_base<256>(p, g) + (local >> 8)
+                  : p.cluster_pairs == 1 ? block_base<128>(p, g) + (local >> 7)
+                                         : block_base<64>(p, g) + (local >> 6);
     if (v < blocks) {
       const int4 i = info_ptr(p)[p.pair_blocks ? V + v : v];
       if (i.y > 0 && i.z >= 0 && (i.z + i.y) * stride <= slots)
-        first[0] = i.z * stride + (p.pair_blocks ? (local >> 6) & 1 : 0), num[0] = i.y;
+        first[0] = i.z * stride + ((local >> 6) & (stride - 1)), num[0] = i.y;
     }
   }
   {
@@ -298,7 +300,7 @@ cudaError_t launch_shared_merge(const DecodeParams &p, int grid, cudaStream_t st
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  const int slots = 2 * (p.pair_blocks + p.pairs) + p.batch * p.head_groups + p.prefix_blocks + grid;
+  const int slots = pair_slots(p) + p.batch * p.head_groups + p.prefix_blocks + grid;
   return cudaLaunchKernelEx(&cfg, shared_merge_kernel, p, slots);
 }
 

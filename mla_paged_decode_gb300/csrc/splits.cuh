@@ -22,6 +22,11 @@ __device__ __forceinline__ SplitInfo split_info(const CtaRange &r, int v, long l
   return s;
 }
 
+// Slots (of 64 rows) that the pair kernel's pieces take, before the others:
+// one per CTA of a cluster for every (cluster, block).
+__host__ __device__ __forceinline__ int pair_slots(const DecodeParams &p) {
+  return 2 * p.cluster_pairs * (p.pair_blocks + p.clusters);
+}
 __device__ __forceinline__ float *slot_lse_ptr(const DecodeParams &p) {
   return reinterpret_cast<float *>(p.ws + p.wl.slot_lse);
 }
