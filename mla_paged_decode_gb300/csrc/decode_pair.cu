@@ -53,7 +53,7 @@ constexpr int kOffMisc = kOffRing + kRing * kUnitBytes;
 constexpr uint32_t kColO = 0, kColS = 256;      // S buffer b: 128 columns from 256 + 128 b
 constexpr int kSoftWarps = 8, kSoftThreads = 256;
 constexpr int kPieceTiles = 1;                  // a piece's boundary, in tiles
-constexpr uint64_t kTimeoutNs = 2000000000ull;
+constexpr long long kTimeoutClk = 4000000000ll;  // about 2 s
 constexpr uint64_t kDrainNs = 200000000ull;
 constexpr float kRescaleThreshold = 8.f;        // base-2 units
 
@@ -138,29 +138,31 @@ __device__ __forceinline__ int next_slot(int s) { return s + 1 == kRing ? 0 : s 
 
 // ------------------------------------------------------------------ producer
 
-// One position in the tiles of a range, with the pages of the tile in lanes 0..3.
+// One position in the tiles of a range, with the tile's pages.
 template <int NP>
 struct TileWalk {
   Pieces<NP> w;
   long long t;
   bool live;
-  int page;
-  __device__ TileWalk(const DecodeParams &p, const CtaRange &r, int *err) : w(p, r), t(0), page(0) {
+  int page[kTilePages];
+  __device__ TileWalk(const DecodeParams &p, const CtaRange &r, int *err) : w(p, r), t(0) {
     live = w.next();
     if (live) t = w.t0;
     load(err);
   }
-  // This lane's page of the tile; a page past the view repeats the last one
-  // (its tokens are masked), an entry out of range reads page 0.
+  // A page past the view repeats the last one (its tokens are masked), an
+  // entry out of range reads page 0.
   __device__ void load(int *err) {
     if (!live) return;
-    const int lane = threadIdx.x & 31;
-    const int i = min(int(t) * kTilePages + (lane & 3), w.view.tiles - 1);
-    page = w.p.block_table[size_t(w.view.req) * w.p.max_pages + i];
-    if (page < 0 || page >= w.p.num_pages) {
-      if (lane < 4) atomicOr(err, kErrBadPage);
-      page = 0;
-    }
+    const int32_t *row = w.p.block_table + size_t(w.view.req) * w.p.max_pages;
+#pragma unroll
+    for (int i = 0; i < kTilePages; ++i) page[i] = __ldg(row + min(int(t) * kTilePages + i, w.view.tiles - 1));
+#pragma unroll
+    for (int i = 0; i < kTilePages; ++i)
+      if (page[i] < 0 || page[i] >= w.p.num_pages) {
+        atomicOr(err, kErrBadPage);
+        page[i] = 0;
+      }
   }
   __device__ bool first() const { return t == w.t0; }
   __device__ void step(int *err) {
@@ -173,12 +175,13 @@ struct TileWalk {
   }
 };
 
+// One thread produces: a warp's votes and shuffles between the units made
+// the producer the slowest role (470 cycles a unit, all 17 of a tile).
 template <int NP>
 __device__ __forceinline__ void produce(const DecodeParams &p, const CtaRange &r, Misc &m, uint32_t sQ,
                                         uint32_t sRing, const Seat &seat, const CUtensorMap *tm_q,
                                         const CUtensorMap *tm_k, const CUtensorMap *tm_v, int *err) {
   volatile int *abort = &m.abort;
-  const int lane = threadIdx.x & 31;
   const bool leader = seat.half == 0;
   const int pair = int(seat.rank >> 1);  // of the cluster
   const uint16_t twins = uint16_t(5u << seat.half);  // the CTAs of both pairs with this half
@@ -187,14 +190,13 @@ __device__ __forceinline__ void produce(const DecodeParams &p, const CtaRange &r
   uint32_t q_it = 0;
   bool ok = true;
   const uint32_t full0 = map_to_rank(bar(m.full[0][0]), seat.leader);
+  const uint32_t q_full = map_to_rank(bar(m.q_full), seat.leader);
   // slot of the next unit (kind 0: K, 1: V), emptied; the even CTA announces
   // both CTAs' bytes
   auto slot = [&](int kind, uint32_t *full) {
     const int s = at;
-    const bool got = mbar_wait(bar(m.empty[s]), lap, abort, kTimeoutNs);
-    if (!__all_sync(0xffffffffu, got)) return -1;
-    if (leader && lane == 0) mbar_arrive_expect_tx(bar(m.full[kind][s]), 2 * kUnitBytes);
-    __syncwarp();
+    if (!mbar_wait_clk(bar(m.empty[s]), lap, abort, kTimeoutClk)) return -1;
+    if (leader) mbar_arrive_expect_tx(bar(m.full[kind][s]), 2 * kUnitBytes);
     *full = full0 + 8 * (kind * kRing + s);
     at = next_slot(s);
     if (at == 0) lap ^= 1;
@@ -202,42 +204,42 @@ __device__ __forceinline__ void produce(const DecodeParams &p, const CtaRange &r
   };
   auto load_k = [&](const TileWalk<NP> &c) {
     if (c.first()) {
-      if (!__all_sync(0xffffffffu, mbar_wait(bar(m.q_empty), (q_it & 1) ^ 1, abort, kTimeoutNs))) return false;
+      if (!mbar_wait_clk(bar(m.q_empty), (q_it & 1) ^ 1, abort, kTimeoutClk)) return false;
       ++q_it;
-      if (leader && lane == 0) mbar_arrive_expect_tx(bar(m.q_full), 2 * kQBytes);
-      __syncwarp();
-      if (lane < 9)
-        tma_load_2d_pair(sQ + lane * kRows * 128, tm_q, map_to_rank(bar(m.q_full), seat.leader), lane * 64,
-                         c.w.view.row0 + int(seat.rank) * kRows);
+      if (leader) mbar_arrive_expect_tx(bar(m.q_full), 2 * kQBytes);
+      for (int i = 0; i < 9; ++i)
+        tma_load_2d_pair(sQ + i * kRows * 128, tm_q, q_full, i * 64, c.w.view.row0 + int(seat.rank) * kRows);
     }
     // the unit's two pages; with two pairs each loads one of them for both
-    const int pg = __shfl_sync(0xffffffffu, c.page, 2 * seat.half + (NP == 2 ? pair : (lane & 1)));
+    const int pg0 = seat.half ? c.page[2] : c.page[0], pg1 = seat.half ? c.page[3] : c.page[1];
+    const int mine = (pair ? pg1 : pg0) * 8;
     for (int kb = 0; kb < kKUnits; ++kb) {
       uint32_t full;
       const int s = slot(0, &full);
       if (s < 0) return false;
+      const uint32_t dst = sRing + s * kUnitBytes;
       if (NP == 2) {
-        if (lane == 0)
-          tma_load_4d_pair_multicast(sRing + s * kUnitBytes + pair * 8192, tm_k, full, 0, 0, kb, pg * 8, twins);
-      } else if (lane < 2) {
-        tma_load_4d_pair(sRing + s * kUnitBytes + lane * 8192, tm_k, full, 0, 0, kb, pg * 8);
+        tma_load_4d_pair_multicast(dst + pair * 8192, tm_k, full, 0, 0, kb, mine, twins);
+      } else {
+        tma_load_4d_pair(dst, tm_k, full, 0, 0, kb, pg0 * 8);
+        tma_load_4d_pair(dst + 8192, tm_k, full, 0, 0, kb, pg1 * 8);
       }
     }
     return true;
   };
-  auto load_v = [&](int page) {  // `page`: the tile's pages in lanes 0..3
-    for (int u = 0; u < kVUnits; ++u) {
-      uint32_t full;
-      const int pg = __shfl_sync(0xffffffffu, page, u >> 1);
-      const int s = slot(1, &full);
-      if (s < 0) return false;
-      if (lane == 0) {
-        const int atom = pg * 8 + 4 * (u & 1);
+  auto load_v = [&](const int (&page)[kTilePages]) {
+#pragma unroll
+    for (int i = 0; i < kTilePages; ++i) {
+      for (int h = 0; h < 2; ++h) {
+        uint32_t full;
+        const int s = slot(1, &full);
+        if (s < 0) return false;
+        const uint32_t dst = sRing + s * kUnitBytes;
+        const int atom = page[i] * 8 + 4 * h;
         if (NP == 2)
-          tma_load_4d_pair_multicast(sRing + s * kUnitBytes + pair * 8192, tm_v, full, 0, 0, 4 * int(seat.half),
-                                     atom + 2 * pair, twins);
+          tma_load_4d_pair_multicast(dst + pair * 8192, tm_v, full, 0, 0, 4 * int(seat.half), atom + 2 * pair, twins);
         else
-          tma_load_4d_pair(sRing + s * kUnitBytes, tm_v, full, 0, 0, 4 * int(seat.half), atom);
+          tma_load_4d_pair(dst, tm_v, full, 0, 0, 4 * int(seat.half), atom);
       }
     }
     return true;
@@ -245,12 +247,14 @@ __device__ __forceinline__ void produce(const DecodeParams &p, const CtaRange &r
   TileWalk<NP> c(p, r, err);
   if (c.live) ok = load_k(c);  // (a range may hold no tile, only a piece's cost)
   while (ok && c.live) {
-    const int page = c.page;
+    int page[kTilePages];
+#pragma unroll
+    for (int i = 0; i < kTilePages; ++i) page[i] = c.page[i];
     c.step(err);
     if (c.live) ok = load_k(c);
     if (ok) ok = load_v(page);
   }
-  if (!ok && lane == 0) atomicOr(err, kErrTimeout);
+  if (!ok) atomicOr(err, kErrTimeout);
 }
 
 // ------------------------------------------------------------------ MMAs (even CTA)
@@ -269,16 +273,18 @@ __device__ __forceinline__ void score_mmas(const DecodeParams &p, const CtaRange
   for (Pieces<NP> w(p, r); ok && w.next(); w.advance()) {
     for (long long t = w.t0; ok && t < w.t1; ++t, ++n) {
       const int b = int(n & 1);
-      ok = mbar_wait(bar(m.s_free[b]), ((n >> 1) & 1) ^ 1, abort, kTimeoutNs);
+      ok = mbar_wait_clk(bar(m.s_free[b]), ((n >> 1) & 1) ^ 1, abort, kTimeoutClk);
       if (ok && t == w.t0) {
-        ok = mbar_wait(bar(m.q_full), q_it & 1, abort, kTimeoutNs);
+        ok = mbar_wait_clk(bar(m.q_full), q_it & 1, abort, kTimeoutClk);
         ++q_it;
       }
+      // orders these MMAs behind the reads of the S buffer; the waits for landed
+      // units need no such fence
+      tc_fence_after();
       int s = int(k_unit(n) % kRing);
       for (int kb = 0; ok && kb < kKUnits; ++kb, s = next_slot(s)) {
-        ok = mbar_wait(bar(m.full[0][s]), landed.take(s), abort, kTimeoutNs);
+        ok = mbar_wait_clk(bar(m.full[0][s]), landed.take(s), abort, kTimeoutClk);
         if (!ok) break;
-        tc_fence_after();
 #pragma unroll
         for (int ks = 0; ks < 4; ++ks)
           mma_bf16_ss_pair(tmem + kColS + 128 * b, dq + ((kb * kRows * 128 + ks * 32) >> 4),
@@ -310,15 +316,15 @@ __device__ __forceinline__ void pv_mmas(const DecodeParams &p, const CtaRange &r
   bool ok = true;
   for (Pieces<NP> w(p, r); ok && w.next(); w.advance(), ++o_it) {
     for (long long t = w.t0; ok && t < w.t1; ++t, ++n) {
-      ok = mbar_wait(bar(m.o_ready[n & 1]), (n >> 1) & 1, abort, kTimeoutNs);
-      if (ok && t == w.t0) ok = mbar_wait(bar(m.o_free), (o_it & 1) ^ 1, abort, kTimeoutNs);
+      ok = mbar_wait_clk(bar(m.o_ready[n & 1]), (n >> 1) & 1, abort, kTimeoutClk);
+      if (ok && t == w.t0) ok = mbar_wait_clk(bar(m.o_free), (o_it & 1) ^ 1, abort, kTimeoutClk);
+      tc_fence_after();
       int s = int(v_unit(n, total) % kRing);
       for (int pg = 0; ok && pg < kTilePages; ++pg) {
-        ok = mbar_wait(bar(m.p_full[pg]), n & 1, abort, kTimeoutNs);
+        ok = mbar_wait_clk(bar(m.p_full[pg]), n & 1, abort, kTimeoutClk);
         for (int h = 0; ok && h < 2; ++h, s = next_slot(s)) {  // a page's two units of 32 tokens
-          ok = mbar_wait(bar(m.full[1][s]), landed.take(s), abort, kTimeoutNs);
+          ok = mbar_wait_clk(bar(m.full[1][s]), landed.take(s), abort, kTimeoutClk);
           if (!ok) break;
-          tc_fence_after();
 #pragma unroll
           for (int ks = 0; ks < 2; ++ks)
 #pragma unroll
@@ -392,7 +398,7 @@ __device__ __forceinline__ void softmax(const DecodeParams &p, const CtaRange &r
     float mrun = -INFINITY, ell = 0.f, ellx = 0.f;
     for (long long t = w.t0; t < w.t1; ++t, ++n) {
       const int b = int(n & 1);
-      ok = ok && __all_sync(0xffffffffu, mbar_wait(bar(m.s_full[b]), (n >> 1) & 1, abort, kTimeoutNs));
+      ok = ok && __all_sync(0xffffffffu, mbar_wait_clk(bar(m.s_full[b]), (n >> 1) & 1, abort, kTimeoutClk));
       float x[64];
       if (ok) {
         tc_fence_after();
@@ -455,7 +461,7 @@ __device__ __forceinline__ void softmax(const DecodeParams &p, const CtaRange &r
       // (Two barriers in turn: a warp may say so for tile i + 1 before the PV
       // thread has asked about tile i, but not for i + 2.)
       if (__any_sync(0xffffffffu, resc)) {
-        ok = ok && __all_sync(0xffffffffu, mbar_wait(bar(m.p_free[kTilePages - 1]), (n - 1) & 1, abort, kTimeoutNs));
+        ok = ok && __all_sync(0xffffffffu, mbar_wait_clk(bar(m.p_free[kTilePages - 1]), (n - 1) & 1, abort, kTimeoutClk));
         if (ok) {
           tc_fence_after();
           rescale_rows(t_o, alpha);
@@ -466,7 +472,7 @@ __device__ __forceinline__ void softmax(const DecodeParams &p, const CtaRange &r
       if (ok && lane == 0) mbar_arrive_cluster(o_ready + 8 * b);
       // the page's part of P is free once the previous tile's product with it is done
       if (n > 0)
-        ok = ok && __all_sync(0xffffffffu, mbar_wait(bar(m.p_free[pb]), (n - 1) & 1, abort, kTimeoutNs));
+        ok = ok && __all_sync(0xffffffffu, mbar_wait_clk(bar(m.p_free[pb]), (n - 1) & 1, abort, kTimeoutClk));
       if (ok) {
 #pragma unroll
         for (int c = 0; c < 8; ++c)
@@ -486,7 +492,7 @@ __device__ __forceinline__ void softmax(const DecodeParams &p, const CtaRange &r
     const float sumx = (m.red[1][0][row] + m.red[1][1][row]) + (m.red[1][2][row] + m.red[1][3][row]);
     named_sync(1, kSoftThreads);  // read before the next piece writes maxima
     const float inv = sum > 0.f ? 1.f / sum : 0.f;
-    ok = ok && __all_sync(0xffffffffu, mbar_wait(bar(m.o_full), o_it & 1, abort, kTimeoutNs));
+    ok = ok && __all_sync(0xffffffffu, mbar_wait_clk(bar(m.o_full), o_it & 1, abort, kTimeoutClk));
     const int c_first = sched_owner(w.pv, r.total, r.g_eff);
     if (ok) {
       tc_fence_after();
@@ -592,7 +598,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (r.start < r.end) {
     if (warp == 0) {
-      produce<NP>(p, r, m, sbase + kOffQ, sbase + kOffRing, seat, &tm_q, &tm_k, &tm_v, err);
+      if (lane == 0) produce<NP>(p, r, m, sbase + kOffQ, sbase + kOffRing, seat, &tm_q, &tm_k, &tm_v, err);
     } else if (warp == 1) {
       if (seat.half == 0 && lane == 0) score_mmas<NP>(p, r, m, sbase + kOffQ, sbase + kOffRing, tmem, seat, err);
     } else if (warp == 2) {

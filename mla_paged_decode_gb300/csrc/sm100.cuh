@@ -69,6 +69,23 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatil
   }
 }
 
+// The same with the limit in SM clocks: reading the global timer takes several
+// hundred cycles, which a wait that is satisfied soon afterwards adds to the
+// pipeline's round trip.
+__device__ __forceinline__ bool mbar_wait_clk(uint32_t bar, uint32_t parity, volatile int *abort,
+                                              long long timeout_clk) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const long long t0 = clock64();
+  while (true) {
+    if (mbar_try_wait(bar, parity)) return true;
+    if (*abort) return false;
+    if (clock64() - t0 > timeout_clk) {
+      *abort = 1;
+      return false;
+    }
+  }
+}
+
 // Waits for the phase of parity `parity` for at most `timeout_ns`, whatever
 // any abort flag says (used to drain copies and MMAs in flight before exit).
 __device__ __forceinline__ bool mbar_wait_drain(uint32_t bar, uint32_t parity,
