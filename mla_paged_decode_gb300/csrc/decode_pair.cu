@@ -145,18 +145,20 @@ struct TileWalk {
   long long t;
   bool live;
   int page[kTilePages];
-  __device__ TileWalk(const DecodeParams &p, const CtaRange &r, int *err) : w(p, r), t(0) {
+  __device__ TileWalk(const DecodeParams &p, const CtaRange &r) : w(p, r), t(0) {
     live = w.next();
     if (live) t = w.t0;
-    load(err);
+    load();
   }
   // A page past the view repeats the last one (its tokens are masked), an
   // entry out of range reads page 0.
-  __device__ void load(int *err) {
+  __device__ void load() {
     if (!live) return;
     const int32_t *row = w.p.block_table + size_t(w.view.req) * w.p.max_pages;
 #pragma unroll
     for (int i = 0; i < kTilePages; ++i) page[i] = __ldg(row + min(int(t) * kTilePages + i, w.view.tiles - 1));
+  }
+  __device__ void check(int *err) {
 #pragma unroll
     for (int i = 0; i < kTilePages; ++i)
       if (page[i] < 0 || page[i] >= w.p.num_pages) {
@@ -165,13 +167,13 @@ struct TileWalk {
       }
   }
   __device__ bool first() const { return t == w.t0; }
-  __device__ void step(int *err) {
+  __device__ void step() {
     if (++t >= w.t1) {
       w.advance();
       live = w.next();
       if (live) t = w.t0;
     }
-    load(err);
+    load();
   }
 };
 
@@ -211,7 +213,7 @@ __device__ __forceinline__ void produce(const DecodeParams &p, const CtaRange &r
         tma_load_2d_pair(sQ + i * kRows * 128, tm_q, q_full, i * 64, c.w.view.row0 + int(seat.rank) * kRows);
     }
     // the unit's two pages; with two pairs each loads one of them for both
-    const int pg0 = seat.half ? c.page[2] : c.page[0], pg1 = seat.half ? c.page[3] : c.page[1];
+    const int pg0 = seat.half ? c.page[2] : c.page[0], pg1 = seat.half ? c.page[3] : c.page[1];  // checked
     const int mine = (pair ? pg1 : pg0) * 8;
     for (int kb = 0; kb < kKUnits; ++kb) {
       uint32_t full;
@@ -244,20 +246,35 @@ __device__ __forceinline__ void produce(const DecodeParams &p, const CtaRange &r
     }
     return true;
   };
-  TileWalk<NP> c(p, r, err);
-  if (c.live) ok = load_k(c);  // (a range may hold no tile, only a piece's cost)
-  while (ok && c.live) {
-    int page[kTilePages];
+  // c: the next tile to load K of; its pages are read a tile early, so that
+  // their latency hides behind the units of the tile before
+  TileWalk<NP> c(p, r);
+  int last[kTilePages];  // pages of the tile whose V comes next
+  bool have = false;
+  while (ok && (c.live || have)) {
+    int pages[kTilePages];
+    const bool more = c.live;
+    if (more) {
+      c.check(err);
 #pragma unroll
-    for (int i = 0; i < kTilePages; ++i) page[i] = c.page[i];
-    c.step(err);
-    if (c.live) ok = load_k(c);
-    if (ok) ok = load_v(page);
+      for (int i = 0; i < kTilePages; ++i) pages[i] = c.page[i];
+      ok = load_k(c);
+      c.step();
+    }
+    if (ok && have) ok = load_v(last);
+#pragma unroll
+    for (int i = 0; i < kTilePages; ++i) last[i] = pages[i];
+    have = more;
   }
   if (!ok) atomicOr(err, kErrTimeout);
 }
 
 // ------------------------------------------------------------------ MMAs (even CTA)
+
+// A wait of a whole warp (the same answer in every lane).
+__device__ __forceinline__ bool warp_wait(uint32_t b, uint32_t parity, volatile int *abort) {
+  return __all_sync(0xffffffffu, mbar_wait_clk(b, parity, abort, kTimeoutClk));
+}
 
 template <int NP>
 __device__ __forceinline__ void score_mmas(const DecodeParams &p, const CtaRange &r, Misc &m, uint32_t sQ,
@@ -273,9 +290,9 @@ __device__ __forceinline__ void score_mmas(const DecodeParams &p, const CtaRange
   for (Pieces<NP> w(p, r); ok && w.next(); w.advance()) {
     for (long long t = w.t0; ok && t < w.t1; ++t, ++n) {
       const int b = int(n & 1);
-      ok = mbar_wait_clk(bar(m.s_free[b]), ((n >> 1) & 1) ^ 1, abort, kTimeoutClk);
+      ok = warp_wait(bar(m.s_free[b]), ((n >> 1) & 1) ^ 1, abort);
       if (ok && t == w.t0) {
-        ok = mbar_wait_clk(bar(m.q_full), q_it & 1, abort, kTimeoutClk);
+        ok = warp_wait(bar(m.q_full), q_it & 1, abort);
         ++q_it;
       }
       // orders these MMAs behind the reads of the S buffer; the waits for landed
@@ -283,21 +300,28 @@ __device__ __forceinline__ void score_mmas(const DecodeParams &p, const CtaRange
       tc_fence_after();
       int s = int(k_unit(n) % kRing);
       for (int kb = 0; ok && kb < kKUnits; ++kb, s = next_slot(s)) {
-        ok = mbar_wait_clk(bar(m.full[0][s]), landed.take(s), abort, kTimeoutClk);
+        ok = warp_wait(bar(m.full[0][s]), landed.take(s), abort);
         if (!ok) break;
+        if (elect_one()) {
 #pragma unroll
-        for (int ks = 0; ks < 4; ++ks)
-          mma_bf16_ss_pair(tmem + kColS + 128 * b, dq + ((kb * kRows * 128 + ks * 32) >> 4),
-                           dk + ((s * kUnitBytes + ks * 32) >> 4), idesc, kb > 0 || ks > 0);
-        mma_commit_pair(bar(m.empty[s]), kAll);
+          for (int ks = 0; ks < 4; ++ks)
+            mma_bf16_ss_pair(tmem + kColS + 128 * b, dq + ((kb * kRows * 128 + ks * 32) >> 4),
+                             dk + ((s * kUnitBytes + ks * 32) >> 4), idesc, kb > 0 || ks > 0);
+          mma_commit_pair(bar(m.empty[s]), kAll);
+          if (kb == kKUnits - 1) {
+            mma_commit_pair(bar(m.s_full[b]), seat.pair_mask);
+            if (t == w.t1 - 1) mma_commit_pair(bar(m.q_empty), seat.pair_mask);
+          }
+        }
+        __syncwarp();
       }
-      if (!ok) break;
-      mma_commit_pair(bar(m.s_full[b]), seat.pair_mask);
-      if (t == w.t1 - 1) mma_commit_pair(bar(m.q_empty), seat.pair_mask);
     }
   }
-  if (!ok) atomicOr(err, kErrTimeout);
-  mma_commit_pair(bar(m.drain), seat.pair_mask);
+  if (elect_one()) {
+    if (!ok) atomicOr(err, kErrTimeout);
+    mma_commit_pair(bar(m.drain), seat.pair_mask);
+  }
+  __syncwarp();
 }
 
 template <int NP>
@@ -316,32 +340,39 @@ __device__ __forceinline__ void pv_mmas(const DecodeParams &p, const CtaRange &r
   bool ok = true;
   for (Pieces<NP> w(p, r); ok && w.next(); w.advance(), ++o_it) {
     for (long long t = w.t0; ok && t < w.t1; ++t, ++n) {
-      ok = mbar_wait_clk(bar(m.o_ready[n & 1]), (n >> 1) & 1, abort, kTimeoutClk);
-      if (ok && t == w.t0) ok = mbar_wait_clk(bar(m.o_free), (o_it & 1) ^ 1, abort, kTimeoutClk);
+      ok = warp_wait(bar(m.o_ready[n & 1]), (n >> 1) & 1, abort);
+      if (ok && t == w.t0) ok = warp_wait(bar(m.o_free), (o_it & 1) ^ 1, abort);
       tc_fence_after();
       int s = int(v_unit(n, total) % kRing);
       for (int pg = 0; ok && pg < kTilePages; ++pg) {
-        ok = mbar_wait_clk(bar(m.p_full[pg]), n & 1, abort, kTimeoutClk);
+        ok = warp_wait(bar(m.p_full[pg]), n & 1, abort);
         for (int h = 0; ok && h < 2; ++h, s = next_slot(s)) {  // a page's two units of 32 tokens
-          ok = mbar_wait_clk(bar(m.full[1][s]), landed.take(s), abort, kTimeoutClk);
+          ok = warp_wait(bar(m.full[1][s]), landed.take(s), abort);
           if (!ok) break;
+          if (elect_one()) {
 #pragma unroll
-          for (int ks = 0; ks < 2; ++ks)
+            for (int ks = 0; ks < 2; ++ks)
 #pragma unroll
-            for (int j = 0; j < 2; ++j)
-              mma_bf16_ss_pair(tmem + kColO + 128 * j, dp + ((pg * kRows * 128 + (h * 2 + ks) * 32) >> 4),
-                               dv + ((s * kUnitBytes + ks * 8192 + j * 2048) >> 4), idesc,
-                               t > w.t0 || pg > 0 || h > 0 || ks > 0);
-          mma_commit_pair(bar(m.empty[s]), kAll);
+              for (int j = 0; j < 2; ++j)
+                mma_bf16_ss_pair(tmem + kColO + 128 * j, dp + ((pg * kRows * 128 + (h * 2 + ks) * 32) >> 4),
+                                 dv + ((s * kUnitBytes + ks * 8192 + j * 2048) >> 4), idesc,
+                                 t > w.t0 || pg > 0 || h > 0 || ks > 0);
+            mma_commit_pair(bar(m.empty[s]), kAll);
+            if (h == 1) {
+              mma_commit_pair(bar(m.p_free[pg]), seat.pair_mask);
+              if (pg == kTilePages - 1 && t == w.t1 - 1) mma_commit_pair(bar(m.o_full), seat.pair_mask);
+            }
+          }
+          __syncwarp();
         }
-        if (ok) mma_commit_pair(bar(m.p_free[pg]), seat.pair_mask);
       }
-      if (!ok) break;
-      if (t == w.t1 - 1) mma_commit_pair(bar(m.o_full), seat.pair_mask);
     }
   }
-  if (!ok) atomicOr(err, kErrTimeout);
-  mma_commit_pair(bar(m.drain), seat.pair_mask);
+  if (elect_one()) {
+    if (!ok) atomicOr(err, kErrTimeout);
+    mma_commit_pair(bar(m.drain), seat.pair_mask);
+  }
+  __syncwarp();
 }
 
 // ------------------------------------------------------------------ softmax and epilogue
@@ -600,9 +631,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == 0) {
       if (lane == 0) produce<NP>(p, r, m, sbase + kOffQ, sbase + kOffRing, seat, &tm_q, &tm_k, &tm_v, err);
     } else if (warp == 1) {
-      if (seat.half == 0 && lane == 0) score_mmas<NP>(p, r, m, sbase + kOffQ, sbase + kOffRing, tmem, seat, err);
+      if (seat.half == 0) score_mmas<NP>(p, r, m, sbase + kOffQ, sbase + kOffRing, tmem, seat, err);
     } else if (warp == 2) {
-      if (seat.half == 0 && lane == 0) pv_mmas<NP>(p, r, m, sbase + kOffP, sbase + kOffRing, tmem, seat, err);
+      if (seat.half == 0) pv_mmas<NP>(p, r, m, sbase + kOffP, sbase + kOffRing, tmem, seat, err);
     } else if (warp >= 4) {
       softmax<NP>(p, r, m, smem, tmem, seat, cluster, err);
     }

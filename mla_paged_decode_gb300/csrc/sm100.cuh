@@ -342,6 +342,15 @@ __device__ __forceinline__ uint32_t cluster_rank() {
   return r;
 }
 
+// True in one lane of a converged warp.  MMAs issued under it, by a warp that
+// runs its loop as a whole, take their descriptors from uniform registers; a
+// loop that a single lane runs moves them there for every instruction.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile("{ .reg .pred p; elect.sync _|p, 0xffffffff; selp.u32 %0, 1, 0, p; }" : "=r"(r));
+  return r != 0;
+}
+
 // The cluster address of `addr` (a shared address of this CTA) in CTA `rank`.
 __device__ __forceinline__ uint32_t map_to_rank(uint32_t addr, uint32_t rank) {
   uint32_t r;
