@@ -30,7 +30,6 @@ cudaError_t launch_decode_tc(const DecodeParams &p, int npv, int q_rows, int gro
                              const CUtensorMap &tm_q, const CUtensorMap &tm_kv,
                              const CUtensorMap &tm_kvg, const CUtensorMap &tm_kvb, int grid,
                              cudaStream_t stream);
-int pair_clusters(int pairs);
 cudaError_t launch_decode_pair(const DecodeParams &p, const CUtensorMap &tm_q, const CUtensorMap &tm_k,
                                const CUtensorMap &tm_v, cudaStream_t stream);
 cudaError_t launch_lse_combine(const void *partials, const float *lses, int num_parts, void *out,
@@ -63,7 +62,6 @@ int cuda_fail(cudaError_t e) {
 struct DeviceFacts {
   int sms = 0;
   int major = 0, minor = 0;
-  int clusters[2] = {0, 0};  // the pair kernel's clusters of one and of two pairs resident at once
 };
 
 constexpr int kMaxDevices = 64;
@@ -96,8 +94,6 @@ DeviceFacts current_device(int *st, int *dev_out = nullptr) {
     f.sms = sms;
     f.major = mj;
     f.minor = mn;
-    if (mla_arch_supported(mj, mn))
-      for (int i = 0; i < 2; ++i) f.clusters[i] = mla::pair_clusters(i + 1);
   }
   *st = mla_arch_supported(f.major, f.minor) ? MLA_OK : MLA_ERR_DEVICE;
   return f;
@@ -317,7 +313,7 @@ int make_tensor_maps(const void *q, const void *kv, const mla_decode_desc *d, in
 // The pair kernel's loads of a bf16 cache, on (64 dims, 8 rows, 9 blocks of 64
 // dims, 8-row groups): one dim block of a page's 64 rows (K), four dim blocks
 // of half a page (V).
-int make_pair_maps(const void *kv, const mla_decode_desc *d, int pairs, CUtensorMap *tm_k, CUtensorMap *tm_v) {
+int make_pair_maps(const void *kv, const mla_decode_desc *d, CUtensorMap *tm_k, CUtensorMap *tm_v) {
   EncodeTiled enc = encode_tiled();
   if (!enc) {
     std::snprintf(g_cuda_error, sizeof(g_cuda_error), "cuTensorMapEncodeTiled unavailable");
@@ -326,7 +322,7 @@ int make_pair_maps(const void *kv, const mla_decode_desc *d, int pairs, CUtensor
   const cuuint64_t row = cuuint64_t(mla::kDqk) * 2;
   cuuint64_t dims[4] = {64, 8, cuuint64_t(mla::kDqk / 64), cuuint64_t(d->num_pages) * 8};
   cuuint64_t strides[3] = {row, 128, 8 * row};
-  cuuint32_t box_k[4] = {64, 8, 1, 8}, box_v[4] = {64, 8, 4, cuuint32_t(pairs == 2 ? 2 : 4)}, es[4] = {1, 1, 1, 1};
+  cuuint32_t box_k[4] = {64, 8, 1, 8}, box_v[4] = {64, 8, 4, 4}, es[4] = {1, 1, 1, 1};
   CUresult r = enc(tm_k, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(kv), dims, strides, box_k, es,
                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
@@ -499,7 +495,7 @@ int enqueue_view(mla::DecodeParams p, const void *q, const void *kv_pages, const
   if (st != MLA_OK) return st;
   if (p.pair_blocks) {
     CUtensorMap tm_k, tm_v;
-    st = make_pair_maps(kv_pages, d, p.cluster_pairs, &tm_k, &tm_v);
+    st = make_pair_maps(kv_pages, d, &tm_k, &tm_v);
     if (st != MLA_OK) return st;
     const cudaError_t e = mla::launch_decode_pair(p, tm_q, tm_k, tm_v, s);
     if (e != cudaSuccess) return cuda_fail(e);
@@ -533,12 +529,10 @@ int shared_blocks(const mla_decode_desc *d, int num_groups, int rows) {
 mla::WorkspaceLayout shared_layout(const mla_decode_desc *d, int num_groups, int grid) {
   const int groups = (rows_of(d) + kTcHeadsPerGroup - 1) / kTcHeadsPerGroup;
   const int v = shared_blocks(d, num_groups, 64) + d->batch * groups;
-  // 4 (blocks of 256 rows + grid / 4) <= rows / 64 + 4 num_groups + grid
-  const int slots = v + 3 * num_groups + 2 * grid;
+  // 2 (blocks of 128 rows + grid / 2) <= rows / 64 + 2 num_groups + grid
+  const int slots = v + num_groups + 2 * grid;
   return mla::workspace_layout(v, (slots + 1) / 2);
 }
-// Groups of this many rows on average take clusters of two pairs.
-constexpr long long kTwoPairRows = 256;
 // The pair kernel takes the shared pages of a bf16 cache when the groups fill
 // its blocks of 128 rows on average.
 bool pair_path(const mla_decode_desc *d, int num_groups) {
@@ -929,12 +923,9 @@ int mla_decode_shared(const void *q, const void *kv_pages, const int32_t *block_
   p.shared_pages = shared_pages;
   p.num_groups = num_groups;
   if (pair_path(d, num_groups)) {
-    p.cluster_pairs = (long long)d->batch * rows_of(d) >= kTwoPairRows * num_groups ? 2 : 1;
-    p.clusters = f.clusters[p.cluster_pairs - 1];
-    p.pair_blocks = shared_blocks(d, num_groups, 128 * p.cluster_pairs);
-  }
-  if (p.clusters == 0) {  // (also when no cluster fits the device)
-    p.cluster_pairs = p.pair_blocks = 0;
+    p.pair_blocks = shared_blocks(d, num_groups, 128);
+    p.pairs = f.sms / 2;
+  } else {
     p.prefix_blocks = shared_blocks(d, num_groups, 64);
   }
   return enqueue_view(p, q, kv_pages, block_table, seq_lens, sm_scale, lse_base, out, lse, d, workspace, wl,

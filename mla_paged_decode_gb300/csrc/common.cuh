@@ -99,9 +99,8 @@ struct DecodeParams {
   const int32_t *shared_pages = nullptr;  // [num_groups]
   int num_groups = 0, prefix_blocks = 0;
   // Shared pages attended by the pair kernel (csrc/decode_pair.cu) in
-  // pair_blocks blocks of 128 cluster_pairs rows on `clusters` clusters of
-  // cluster_pairs CTA pairs; prefix_blocks is then 0.
-  int pair_blocks = 0, cluster_pairs = 0, clusters = 0;
+  // pair_blocks blocks of 128 rows on `pairs` CTA pairs; prefix_blocks is then 0.
+  int pair_blocks = 0, pairs = 0;
   int kv_e4m3;
   float kv_scale;             // 1 for bf16
   float score_scale_log2;     // sm_scale * log2(e): scores kept in the base-2 domain

@@ -28,7 +28,7 @@
 // PV_{i+1} follows PV_i without a gap.
 //
 // Work is split as in the decode kernel: the tiles of all blocks in one line,
-// cut into equal ranges, one per cluster; every piece leaves an fp32 partial.
+// cut into equal ranges, one per pair; every piece leaves an fp32 partial.
 #include "common.cuh"
 #include "sm100.cuh"
 #include "splits.cuh"
@@ -75,19 +75,11 @@ using namespace pair;
 
 __device__ __forceinline__ uint32_t bar(uint64_t &b) { return smem_u32(&b); }
 
-template <int NP>
 __device__ __forceinline__ int block_tiles(const DecodeParams &p, int v) {
-  return (shared_block<NP * kPairRows>(p, v).tiles + kTilePages - 1) / kTilePages;
+  return (shared_block<kPairRows>(p, v).tiles + kTilePages - 1) / kTilePages;
 }
 
-// This CTA's place: its rank in the cluster, its half of the pair's operands.
-struct Seat {
-  uint32_t rank, half, leader;  // leader: the even CTA of the pair
-  uint16_t pair_mask;           // both CTAs of the pair
-};
-
-// The pieces of this cluster's range, in order.
-template <int NP>
+// The pieces of this pair's range, in order.
 struct Pieces {
   const DecodeParams &p;
   const CtaRange &r;
@@ -97,7 +89,7 @@ struct Pieces {
   __device__ Pieces(const DecodeParams &p_, const CtaRange &r_) : p(p_), r(r_), v(r_.v_begin), pv(r_.p_begin) {}
   __device__ bool next() {
     while (v < p.pair_blocks && pv < r.end) {
-      view = shared_block<NP * kPairRows>(p, v);
+      view = shared_block<kPairRows>(p, v);
       tiles = (view.tiles + kTilePages - 1) / kTilePages;
       if (tiles == 0) { ++v; continue; }
       t0 = max(r.start, pv) - pv;
@@ -110,10 +102,9 @@ struct Pieces {
   __device__ void advance() { pv += request_cost(tiles, kPieceTiles); ++v; }
 };
 
-template <int NP>
 __device__ __forceinline__ uint32_t total_tiles(const DecodeParams &p, const CtaRange &r) {
   uint32_t n = 0;
-  for (Pieces<NP> w(p, r); w.next(); w.advance()) n += uint32_t(w.t1 - w.t0);
+  for (Pieces w(p, r); w.next(); w.advance()) n += uint32_t(w.t1 - w.t0);
   return n;
 }
 
@@ -139,9 +130,8 @@ __device__ __forceinline__ int next_slot(int s) { return s + 1 == kRing ? 0 : s 
 // ------------------------------------------------------------------ producer
 
 // One position in the tiles of a range, with the tile's pages.
-template <int NP>
 struct TileWalk {
-  Pieces<NP> w;
+  Pieces w;
   long long t;
   bool live;
   int page[kTilePages];
@@ -179,20 +169,17 @@ struct TileWalk {
 
 // One thread produces: a warp's votes and shuffles between the units made
 // the producer the slowest role (470 cycles a unit, all 17 of a tile).
-template <int NP>
 __device__ __forceinline__ void produce(const DecodeParams &p, const CtaRange &r, Misc &m, uint32_t sQ,
-                                        uint32_t sRing, const Seat &seat, const CUtensorMap *tm_q,
+                                        uint32_t sRing, uint32_t rank, const CUtensorMap *tm_q,
                                         const CUtensorMap *tm_k, const CUtensorMap *tm_v, int *err) {
   volatile int *abort = &m.abort;
-  const bool leader = seat.half == 0;
-  const int pair = int(seat.rank >> 1);  // of the cluster
-  const uint16_t twins = uint16_t(5u << seat.half);  // the CTAs of both pairs with this half
+  const bool leader = rank == 0;
   int at = 0;
   uint32_t lap = 1;  // parity of the empty barriers' last phase
   uint32_t q_it = 0;
   bool ok = true;
-  const uint32_t full0 = map_to_rank(bar(m.full[0][0]), seat.leader);
-  const uint32_t q_full = map_to_rank(bar(m.q_full), seat.leader);
+  const uint32_t full0 = map_to_rank(bar(m.full[0][0]), 0);
+  const uint32_t q_full = map_to_rank(bar(m.q_full), 0);
   // slot of the next unit (kind 0: K, 1: V), emptied; the even CTA announces
   // both CTAs' bytes
   auto slot = [&](int kind, uint32_t *full) {
@@ -204,28 +191,22 @@ __device__ __forceinline__ void produce(const DecodeParams &p, const CtaRange &r
     if (at == 0) lap ^= 1;
     return s;
   };
-  auto load_k = [&](const TileWalk<NP> &c) {
+  auto load_k = [&](const TileWalk &c) {
     if (c.first()) {
       if (!mbar_wait_clk(bar(m.q_empty), (q_it & 1) ^ 1, abort, kTimeoutClk)) return false;
       ++q_it;
       if (leader) mbar_arrive_expect_tx(bar(m.q_full), 2 * kQBytes);
       for (int i = 0; i < 9; ++i)
-        tma_load_2d_pair(sQ + i * kRows * 128, tm_q, q_full, i * 64, c.w.view.row0 + int(seat.rank) * kRows);
+        tma_load_2d_pair(sQ + i * kRows * 128, tm_q, q_full, i * 64, c.w.view.row0 + int(rank) * kRows);
     }
-    // the unit's two pages; with two pairs each loads one of them for both
-    const int pg0 = seat.half ? c.page[2] : c.page[0], pg1 = seat.half ? c.page[3] : c.page[1];  // checked
-    const int mine = (pair ? pg1 : pg0) * 8;
+    const int pg0 = rank ? c.page[2] : c.page[0], pg1 = rank ? c.page[3] : c.page[1];  // checked
     for (int kb = 0; kb < kKUnits; ++kb) {
       uint32_t full;
       const int s = slot(0, &full);
       if (s < 0) return false;
       const uint32_t dst = sRing + s * kUnitBytes;
-      if (NP == 2) {
-        tma_load_4d_pair_multicast(dst + pair * 8192, tm_k, full, 0, 0, kb, mine, twins);
-      } else {
-        tma_load_4d_pair(dst, tm_k, full, 0, 0, kb, pg0 * 8);
-        tma_load_4d_pair(dst + 8192, tm_k, full, 0, 0, kb, pg1 * 8);
-      }
+      tma_load_4d_pair(dst, tm_k, full, 0, 0, kb, pg0 * 8);
+      tma_load_4d_pair(dst + 8192, tm_k, full, 0, 0, kb, pg1 * 8);
     }
     return true;
   };
@@ -236,19 +217,14 @@ __device__ __forceinline__ void produce(const DecodeParams &p, const CtaRange &r
         uint32_t full;
         const int s = slot(1, &full);
         if (s < 0) return false;
-        const uint32_t dst = sRing + s * kUnitBytes;
-        const int atom = page[i] * 8 + 4 * h;
-        if (NP == 2)
-          tma_load_4d_pair_multicast(dst + pair * 8192, tm_v, full, 0, 0, 4 * int(seat.half), atom + 2 * pair, twins);
-        else
-          tma_load_4d_pair(dst, tm_v, full, 0, 0, 4 * int(seat.half), atom);
+        tma_load_4d_pair(sRing + s * kUnitBytes, tm_v, full, 0, 0, 4 * int(rank), page[i] * 8 + 4 * h);
       }
     }
     return true;
   };
   // c: the next tile to load K of; its pages are read a tile early, so that
   // their latency hides behind the units of the tile before
-  TileWalk<NP> c(p, r);
+  TileWalk c(p, r);
   int last[kTilePages];  // pages of the tile whose V comes next
   bool have = false;
   while (ok && (c.live || have)) {
@@ -276,18 +252,16 @@ __device__ __forceinline__ bool warp_wait(uint32_t b, uint32_t parity, volatile 
   return __all_sync(0xffffffffu, mbar_wait_clk(b, parity, abort, kTimeoutClk));
 }
 
-template <int NP>
 __device__ __forceinline__ void score_mmas(const DecodeParams &p, const CtaRange &r, Misc &m, uint32_t sQ,
-                                           uint32_t sRing, uint32_t tmem, const Seat &seat, int *err) {
+                                           uint32_t sRing, uint32_t tmem, int *err) {
   volatile int *abort = &m.abort;
-  constexpr uint16_t kAll = (1u << (2 * NP)) - 1;  // a ring slot is free when every pair has read it
   const uint32_t idesc = idesc_bf16_f32(128, 256, false, false);
   const uint64_t dq = smem_desc_sw128(sQ, 16, 1024), dk = smem_desc_sw128(sRing, 16, 1024);
   Landed landed;
   uint32_t n = 0;
   uint32_t q_it = 0;
   bool ok = true;
-  for (Pieces<NP> w(p, r); ok && w.next(); w.advance()) {
+  for (Pieces w(p, r); ok && w.next(); w.advance()) {
     for (long long t = w.t0; ok && t < w.t1; ++t, ++n) {
       const int b = int(n & 1);
       ok = warp_wait(bar(m.s_free[b]), ((n >> 1) & 1) ^ 1, abort);
@@ -307,10 +281,10 @@ __device__ __forceinline__ void score_mmas(const DecodeParams &p, const CtaRange
           for (int ks = 0; ks < 4; ++ks)
             mma_bf16_ss_pair(tmem + kColS + 128 * b, dq + ((kb * kRows * 128 + ks * 32) >> 4),
                              dk + ((s * kUnitBytes + ks * 32) >> 4), idesc, kb > 0 || ks > 0);
-          mma_commit_pair(bar(m.empty[s]), kAll);
+          mma_commit_pair(bar(m.empty[s]));
           if (kb == kKUnits - 1) {
-            mma_commit_pair(bar(m.s_full[b]), seat.pair_mask);
-            if (t == w.t1 - 1) mma_commit_pair(bar(m.q_empty), seat.pair_mask);
+            mma_commit_pair(bar(m.s_full[b]));
+            if (t == w.t1 - 1) mma_commit_pair(bar(m.q_empty));
           }
         }
         __syncwarp();
@@ -319,26 +293,24 @@ __device__ __forceinline__ void score_mmas(const DecodeParams &p, const CtaRange
   }
   if (elect_one()) {
     if (!ok) atomicOr(err, kErrTimeout);
-    mma_commit_pair(bar(m.drain), seat.pair_mask);
+    mma_commit_pair(bar(m.drain));
   }
   __syncwarp();
 }
 
-template <int NP>
 __device__ __forceinline__ void pv_mmas(const DecodeParams &p, const CtaRange &r, Misc &m, uint32_t sP,
-                                        uint32_t sRing, uint32_t tmem, const Seat &seat, int *err) {
+                                        uint32_t sRing, uint32_t tmem, int *err) {
   volatile int *abort = &m.abort;
-  constexpr uint16_t kAll = (1u << (2 * NP)) - 1;
   const uint32_t idesc = idesc_bf16_f32(128, 256, false, true);
   const uint64_t dp = smem_desc_sw128(sP, 16, 1024);
   // V, MN-major: 64-dim blocks 1 KB apart, 8-token groups 4 KB apart
   const uint64_t dv = smem_desc_sw128(sRing, 1024, 4096);
-  const uint32_t total = total_tiles<NP>(p, r);
+  const uint32_t total = total_tiles(p, r);
   Landed landed;
   uint32_t n = 0;
   uint32_t o_it = 0;
   bool ok = true;
-  for (Pieces<NP> w(p, r); ok && w.next(); w.advance(), ++o_it) {
+  for (Pieces w(p, r); ok && w.next(); w.advance(), ++o_it) {
     for (long long t = w.t0; ok && t < w.t1; ++t, ++n) {
       ok = warp_wait(bar(m.o_ready[n & 1]), (n >> 1) & 1, abort);
       if (ok && t == w.t0) ok = warp_wait(bar(m.o_free), (o_it & 1) ^ 1, abort);
@@ -357,10 +329,10 @@ __device__ __forceinline__ void pv_mmas(const DecodeParams &p, const CtaRange &r
                 mma_bf16_ss_pair(tmem + kColO + 128 * j, dp + ((pg * kRows * 128 + (h * 2 + ks) * 32) >> 4),
                                  dv + ((s * kUnitBytes + ks * 8192 + j * 2048) >> 4), idesc,
                                  t > w.t0 || pg > 0 || h > 0 || ks > 0);
-            mma_commit_pair(bar(m.empty[s]), kAll);
+            mma_commit_pair(bar(m.empty[s]));
             if (h == 1) {
-              mma_commit_pair(bar(m.p_free[pg]), seat.pair_mask);
-              if (pg == kTilePages - 1 && t == w.t1 - 1) mma_commit_pair(bar(m.o_full), seat.pair_mask);
+              mma_commit_pair(bar(m.p_free[pg]));
+              if (pg == kTilePages - 1 && t == w.t1 - 1) mma_commit_pair(bar(m.o_full));
             }
           }
           __syncwarp();
@@ -370,7 +342,7 @@ __device__ __forceinline__ void pv_mmas(const DecodeParams &p, const CtaRange &r
   }
   if (elect_one()) {
     if (!ok) atomicOr(err, kErrTimeout);
-    mma_commit_pair(bar(m.drain), seat.pair_mask);
+    mma_commit_pair(bar(m.drain));
   }
   __syncwarp();
 }
@@ -404,9 +376,8 @@ __device__ __forceinline__ void st_global_v8(float *dst, const float (&v)[8]) {
 
 // A failed wait never leaves the loop: the warp goes on without working, so
 // that the others find it at their barriers (later waits fail at once).
-template <int NP>
 __device__ __forceinline__ void softmax(const DecodeParams &p, const CtaRange &r, Misc &m, unsigned char *smem,
-                                        uint32_t tmem, const Seat &seat, int cluster, int *err) {
+                                        uint32_t tmem, uint32_t rank, int pair_id, int *err) {
   volatile int *abort = &m.abort;
   const int st = int(threadIdx.x) - 128, warp = st >> 5, lane = st & 31;  // warps 0..7
   const int g = warp >> 2, q = warp & 3;             // column half, TMEM quarter (lanes 32q ..)
@@ -415,17 +386,17 @@ __device__ __forceinline__ void softmax(const DecodeParams &p, const CtaRange &r
   const uint32_t t_s = tmem + lanes + kColS + 64 * g, t_o = tmem + lanes + kColO + 128 * g;
   const float cs = p.score_scale_log2;
   unsigned char *prow = smem + kOffP + pb * kRows * 128 + row * 128;
-  const uint32_t s_free0 = map_to_rank(bar(m.s_free[0]), seat.leader);
-  const uint32_t s_free1 = map_to_rank(bar(m.s_free[1]), seat.leader);
-  const uint32_t p_full = map_to_rank(bar(m.p_full[pb]), seat.leader);
-  const uint32_t o_ready = map_to_rank(bar(m.o_ready[0]), seat.leader), o_free = map_to_rank(bar(m.o_free), seat.leader);
+  const uint32_t s_free0 = map_to_rank(bar(m.s_free[0]), 0);
+  const uint32_t s_free1 = map_to_rank(bar(m.s_free[1]), 0);
+  const uint32_t p_full = map_to_rank(bar(m.p_full[pb]), 0);
+  const uint32_t o_ready = map_to_rank(bar(m.o_ready[0]), 0), o_free = map_to_rank(bar(m.o_free), 0);
   uint32_t n = 0;
   uint32_t o_it = 0;
   bool ok = true;
-  for (Pieces<NP> w(p, r); w.next(); w.advance(), ++o_it) {
-    const int grow = w.view.row0 + int(seat.rank) * kRows + row;
+  for (Pieces w(p, r); w.next(); w.advance(), ++o_it) {
+    const int grow = w.view.row0 + int(rank) * kRows + row;
     const int hi = row_view(p, w.view, min(grow, p.batch * p.heads - 1)).hi;
-    const bool mine = int(seat.rank) * kRows + row < w.view.rows;
+    const bool mine = int(rank) * kRows + row < w.view.rows;
     float mrun = -INFINITY, ell = 0.f, ellx = 0.f;
     for (long long t = w.t0; t < w.t1; ++t, ++n) {
       const int b = int(n & 1);
@@ -527,7 +498,7 @@ __device__ __forceinline__ void softmax(const DecodeParams &p, const CtaRange &r
     const int c_first = sched_owner(w.pv, r.total, r.g_eff);
     if (ok) {
       tc_fence_after();
-      const size_t slot = 2 * NP * size_t(cluster + w.v) + seat.rank;
+      const size_t slot = 2 * size_t(pair_id + w.v) + rank;
       float *dst = slot_out_ptr(p) + (slot * kSlotHeads + row) * kDv + 256 * (q >> 1) + 128 * g;
 #pragma unroll 1
       for (int c = 0; c < 128; c += 32) {
@@ -548,20 +519,16 @@ __device__ __forceinline__ void softmax(const DecodeParams &p, const CtaRange &r
       __syncwarp();
       if (lane == 0) mbar_arrive_cluster(o_free);
       if (mine && pb == 0) slot_lse_ptr(p)[slot * kSlotHeads + row] = mrun + log2f(sumx);
-      if (st == 0 && seat.rank == 0 && cluster == c_first) {
+      if (st == 0 && rank == 0 && pair_id == c_first) {
         const int c_last = sched_owner(w.pv + w.tiles - 1, r.total, r.g_eff);
-        info_ptr(p)[p.batch * p.head_groups + w.v] = make_int4(c_first, c_last - c_first + 1, cluster + w.v, 0);
+        info_ptr(p)[p.batch * p.head_groups + w.v] = make_int4(c_first, c_last - c_first + 1, pair_id + w.v, 0);
       }
     }
   }
   if (!ok) atomicOr(err, kErrTimeout);
 }
 
-// NP: pairs of a cluster.  Two pairs take 256 rows and walk the same tiles: each
-// CTA loads half of its units and multicasts them to its twin in the other pair,
-// which halves what is read from L2.
-template <int NP>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     decode_pair_kernel(const __grid_constant__ DecodeParams p, const __grid_constant__ CUtensorMap tm_q,
                        const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v) {
   extern __shared__ unsigned char smem_raw[];
@@ -570,19 +537,15 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t sbase = raw + pad;
   Misc &m = *reinterpret_cast<Misc *>(smem + kOffMisc);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  Seat seat;
-  seat.rank = cluster_rank();
-  seat.half = seat.rank & 1u;
-  seat.leader = seat.rank & ~1u;
-  seat.pair_mask = uint16_t(3u << seat.leader);
-  const int cluster = int(blockIdx.x) / (2 * NP);
+  const uint32_t rank = cluster_rank();
+  const int pair_id = int(blockIdx.x) >> 1;
   int *err = error_word(p);
 
   if (tid == 0) {
     for (int s = 0; s < kRing; ++s) {
       mbar_init(bar(m.full[0][s]), 1);
       mbar_init(bar(m.full[1][s]), 1);
-      mbar_init(bar(m.empty[s]), NP);
+      mbar_init(bar(m.empty[s]), 1);
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(bar(m.s_full[b]), 1);
@@ -618,8 +581,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   asm volatile("griddepcontrol.wait;" ::: "memory");
   // blocks without pages have no partials
   for (int v = int(blockIdx.x) * kThreads + tid; v < p.pair_blocks; v += int(gridDim.x) * kThreads)
-    if (block_tiles<NP>(p, v) == 0) info_ptr(p)[p.batch * p.head_groups + v] = make_int4(-1, 0, 0, 0);
-  schedule_range<kPieceTiles>(p.pair_blocks, cluster, p.clusters, [&](int v) { return block_tiles<NP>(p, v); },
+    if (block_tiles(p, v) == 0) info_ptr(p)[p.batch * p.head_groups + v] = make_int4(-1, 0, 0, 0);
+  schedule_range<kPieceTiles>(p.pair_blocks, pair_id, p.pairs, [&](int v) { return block_tiles(p, v); },
                               &m.range, m.scratch);
   tc_fence_before();
   cluster_sync();  // both CTAs' barriers and TMEM are ready
@@ -629,13 +592,13 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (r.start < r.end) {
     if (warp == 0) {
-      if (lane == 0) produce<NP>(p, r, m, sbase + kOffQ, sbase + kOffRing, seat, &tm_q, &tm_k, &tm_v, err);
+      if (lane == 0) produce(p, r, m, sbase + kOffQ, sbase + kOffRing, rank, &tm_q, &tm_k, &tm_v, err);
     } else if (warp == 1) {
-      if (seat.half == 0) score_mmas<NP>(p, r, m, sbase + kOffQ, sbase + kOffRing, tmem, seat, err);
+      if (rank == 0) score_mmas(p, r, m, sbase + kOffQ, sbase + kOffRing, tmem, err);
     } else if (warp == 2) {
-      if (seat.half == 0) pv_mmas<NP>(p, r, m, sbase + kOffP, sbase + kOffRing, tmem, seat, err);
+      if (rank == 0) pv_mmas(p, r, m, sbase + kOffP, sbase + kOffRing, tmem, err);
     } else if (warp >= 4) {
-      softmax<NP>(p, r, m, smem, tmem, seat, cluster, err);
+      softmax(p, r, m, smem, tmem, rank, pair_id, err);
     }
     // no MMA may still read this CTA's shared memory, and no copy write it:
     // the MMAs waited for every copy unless a wait gave up
@@ -660,61 +623,24 @@ __global__ void __launch_bounds__(kThreads, 1)
   cluster_sync();  // the pair leaves together: neither SM takes another CTA before both gave up their TMEM
 }
 
-template <int NP>
-cudaLaunchConfig_t pair_config(int clusters, cudaStream_t stream, cudaLaunchAttribute (&attr)[2]) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(2 * NP * clusters);
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = kSmemBytes;
-  cfg.stream = stream;
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = 2 * NP;
-  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[1].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 2;
-  return cfg;
-}
-
-template <int NP>
-cudaError_t ensure_smem() {
-  static SmemLimitOnce smem_limit;
-  return smem_limit.ensure(decode_pair_kernel<NP>, kSmemBytes);
-}
-
-template <int NP>
-cudaError_t launch(const DecodeParams &p, const CUtensorMap &tm_q, const CUtensorMap &tm_k, const CUtensorMap &tm_v,
-                   cudaStream_t stream) {
-  const cudaError_t e = ensure_smem<NP>();
-  if (e != cudaSuccess) return e;
-  cudaLaunchAttribute attr[2];
-  const cudaLaunchConfig_t cfg = pair_config<NP>(p.clusters, stream, attr);
-  return cudaLaunchKernelEx(&cfg, decode_pair_kernel<NP>, p, tm_q, tm_k, tm_v);
-}
-
-template <int NP>
-int resident_clusters() {
-  int n = 0;
-  cudaLaunchAttribute attr[2];
-  const cudaLaunchConfig_t cfg = pair_config<NP>(1, nullptr, attr);
-  if (ensure_smem<NP>() != cudaSuccess ||
-      cudaOccupancyMaxActiveClusters(&n, decode_pair_kernel<NP>, &cfg) != cudaSuccess) {
-    cudaGetLastError();  // leaves no error behind for the next launch
-    return 0;
-  }
-  return n;
-}
-
 }  // namespace
-
-// Clusters of `pairs` (1 or 2) CTA pairs that fit the current device at once
-// (0 on an error).
-int pair_clusters(int pairs) { return pairs == 2 ? resident_clusters<2>() : resident_clusters<1>(); }
 
 cudaError_t launch_decode_pair(const DecodeParams &p, const CUtensorMap &tm_q, const CUtensorMap &tm_k,
                                const CUtensorMap &tm_v, cudaStream_t stream) {
-  return p.cluster_pairs == 2 ? launch<2>(p, tm_q, tm_k, tm_v, stream) : launch<1>(p, tm_q, tm_k, tm_v, stream);
+  static SmemLimitOnce smem_limit;
+  const cudaError_t e = smem_limit.ensure(decode_pair_kernel, pair::kSmemBytes);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(2 * p.pairs);
+  cfg.blockDim = dim3(pair::kThreads);
+  cfg.dynamicSmemBytes = pair::kSmemBytes;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, decode_pair_kernel, p, tm_q, tm_k, tm_v);
 }
 
 }  // namespace mla

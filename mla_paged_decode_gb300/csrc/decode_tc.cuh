@@ -475,6 +475,23 @@ __device__ __forceinline__ void tc_producer(const TcParams &tp, const CtaRange &
 
 // Descriptors: an offset is added to the encoded start address (bits 0..13,
 // address >> 4), which never carries because shared addresses stay below 256 KB.
+// Views run an issuer's loop with the whole warp and elect the lane that
+// issues, which leaves the descriptors in uniform registers: see elect_one.
+// The other variants' issuers are single lanes.
+template <bool WARP>
+__device__ __forceinline__ bool issuer() {
+  if constexpr (WARP) {
+    __syncwarp();
+    return elect_one();
+  }
+  return true;
+}
+template <bool WARP>
+__device__ __forceinline__ bool issuer_wait(uint32_t b, uint32_t parity, volatile int *abort, uint64_t timeout_ns) {
+  if constexpr (WARP) return __all_sync(0xffffffffu, mbar_wait(b, parity, abort, timeout_ns));
+  return mbar_wait(b, parity, abort, timeout_ns);
+}
+
 template <bool F8, bool FUSED, int MULTI, int KBG>
 __device__ __forceinline__ void tc_mma_s(const TcParams &tp, const CtaRange &r, TcMiscFor<F8> &m,
                          uint32_t sQ, uint32_t sKv, uint32_t tmem, int chain, int *err) {
@@ -499,35 +516,39 @@ __device__ __forceinline__ void tc_mma_s(const TcParams &tp, const CtaRange &r, 
       const int st = s_it % NS, sb = s_it & 1;
       const uint32_t ph = (s_it / NS) & 1;
       if (sc.first()) {
-        if (!mbar_wait(bar_addr(q_ready), q_it & 1, abort, kTimeoutNs)) { ok = false; break; }
+        if (!issuer_wait<MULTI == 3>(bar_addr(q_ready), q_it & 1, abort, kTimeoutNs)) { ok = false; break; }
         ++q_it;
       }
-      if (!mbar_wait(bar_addr(m.s_free[sb]), ((s_it >> 1) & 1) ^ 1, abort, kTimeoutNs)) {
+      if (!issuer_wait<MULTI == 3>(bar_addr(m.s_free[sb]), ((s_it >> 1) & 1) ^ 1, abort, kTimeoutNs)) {
         ok = false;
         break;
       }
       const uint32_t d = tmem + kColS + 64 * (2 * sb + chain);
       bool landed = true;
 #pragma unroll
-      for (int j = 0; j < kFxBlocks; ++j) {
-        const int kb = (j + 4) % kFxBlocks;  // block 4 first, then blocks 0..3
-        if (j < 2) {
-          landed = mbar_wait(bar_addr(m.kv_full[st][1 - j]), ph, abort, kTimeoutNs);
-          if (!landed) break;
-          tc_fence_after();
-        }
-        const uint64_t dk = (kb < 4 ? dk0 + ((kb * kFxBlkStride) >> 4) : dk4) + st * kStageEnc;
+      for (int half = 0; half < 2; ++half) {  // block 4 first, then blocks 0..3
+        landed = issuer_wait<MULTI == 3>(bar_addr(m.kv_full[st][1 - half]), ph, abort, kTimeoutNs);
+        if (!landed) break;
+        tc_fence_after();
+        if (issuer<MULTI == 3>()) {
 #pragma unroll
-        for (int ks = 0; ks < (kb < 4 ? 4 : 2); ++ks)
-          mma_f8_ss(d, dq + ((kb * kFxBlock + ks * 32) >> 4), dk + ((ks * 32) >> 4), idesc_s,
-                    j > 0 || ks > 0);
+          for (int kb = half ? 0 : 4; kb < (half ? 4 : 5); ++kb) {
+            const uint64_t dk = (kb < 4 ? dk0 + ((kb * kFxBlkStride) >> 4) : dk4) + st * kStageEnc;
+#pragma unroll
+            for (int ks = 0; ks < (kb < 4 ? 4 : 2); ++ks)
+              mma_f8_ss(d, dq + ((kb * kFxBlock + ks * 32) >> 4), dk + ((ks * 32) >> 4), idesc_s,
+                        half > 0 || ks > 0);
+          }
+        }
       }
       if (!landed) { ok = false; break; }
-      mma_commit(bar_addr(m.s_full[sb]));
-      if (sc.last()) mma_commit(bar_addr(m.q_empty));
+      if (issuer<MULTI == 3>()) {
+        mma_commit(bar_addr(m.s_full[sb]));
+        if (sc.last()) mma_commit(bar_addr(m.q_empty));
+      }
     }
     if (!ok) atomicOr(err, kErrTimeout);
-    mma_commit(bar_addr(m.drain));
+    if (issuer<MULTI == 3>()) mma_commit(bar_addr(m.drain));
     mbar_wait_drain(bar_addr(m.drain), 0, kDrainNs);
     return;
   }
@@ -540,38 +561,46 @@ __device__ __forceinline__ void tc_mma_s(const TcParams &tp, const CtaRange &r, 
   for (TileCursor<FUSED, MULTI, piece_cost<F8>()> sc(p, r); sc.live; sc.step(), ++s_it) {
     const int st = s_it & 1;
     const uint32_t ph = (s_it >> 1) & 1;
-    if (!mbar_wait(bar_addr(m.kv_full[st][0]), ph, abort, kTimeoutNs)) {
+    if (!issuer_wait<MULTI == 3>(bar_addr(m.kv_full[st][0]), ph, abort, kTimeoutNs)) {
       ok = false;
       break;
     }
     if (sc.first()) {
-      if (!mbar_wait(bar_addr(q_ready), q_it & 1, abort, kTimeoutNs)) { ok = false; break; }
+      if (!issuer_wait<MULTI == 3>(bar_addr(q_ready), q_it & 1, abort, kTimeoutNs)) { ok = false; break; }
       ++q_it;
     }
-    if (!mbar_wait(bar_addr(m.s_free[st]), ph ^ 1, abort, kTimeoutNs)) { ok = false; break; }
+    if (!issuer_wait<MULTI == 3>(bar_addr(m.s_free[st]), ph ^ 1, abort, kTimeoutNs)) { ok = false; break; }
     tc_fence_after();
     const uint64_t dk = dk0 + st * kStageEnc;
     const uint32_t d = tmem + kColS + 64 * (2 * st + chain);
-    // K-step ks = 2 i + chain: dim block i / 2, 16-dim slice 2 (i % 2) + chain
+    // K-step ks = 2 i + chain: dim block i / 2, 16-dim slice 2 (i % 2) + chain;
+    // column group by column group, as their boxes land
     bool landed = true;
 #pragma unroll
-    for (int i = 0; i < kKb * 2; ++i) {
-      const int kb = i >> 1;
-      if (i > 0 && kb % KBG == 0 && (i & 1) == 0) {
-        landed = mbar_wait(bar_addr(m.kv_full[st][kb / KBG]), ph, abort, kTimeoutNs);
+    for (int g = 0; g < kKb / KBG; ++g) {
+      if (g > 0) {
+        landed = issuer_wait<MULTI == 3>(bar_addr(m.kv_full[st][g]), ph, abort, kTimeoutNs);
         if (!landed) break;
         tc_fence_after();
       }
-      const uint32_t sub = 64u * uint32_t(i & 1) + 32u * uint32_t(chain);
-      mma_bf16_ss(d, dq + ((kb * (64 * 128) + sub) >> 4),
-                  dk + ((kb_off<KBG>(kb) + 64u * uint32_t(i & 1)) >> 4), idesc_s, i > 0);
+      if (issuer<MULTI == 3>()) {
+#pragma unroll
+        for (int i = 2 * KBG * g; i < 2 * KBG * (g + 1); ++i) {
+          const int kb = i >> 1;
+          const uint32_t sub = 64u * uint32_t(i & 1) + 32u * uint32_t(chain);
+          mma_bf16_ss(d, dq + ((kb * (64 * 128) + sub) >> 4),
+                      dk + ((kb_off<KBG>(kb) + 64u * uint32_t(i & 1)) >> 4), idesc_s, i > 0);
+        }
+      }
     }
     if (!landed) { ok = false; break; }
-    mma_commit(bar_addr(m.s_full[st]));
-    if (sc.last()) mma_commit(bar_addr(m.q_empty));
+    if (issuer<MULTI == 3>()) {
+      mma_commit(bar_addr(m.s_full[st]));
+      if (sc.last()) mma_commit(bar_addr(m.q_empty));
+    }
   }
   if (!ok) atomicOr(err, kErrTimeout);
-  mma_commit(bar_addr(m.drain));
+  if (issuer<MULTI == 3>()) mma_commit(bar_addr(m.drain));
   mbar_wait_drain(bar_addr(m.drain), 0, kDrainNs);
 }
 
@@ -600,18 +629,19 @@ __device__ __forceinline__ void tc_mma_pv(const TcParams &tp, const CtaRange &r,
     bool ok = true;
     for (TileCursor<FUSED, MULTI, piece_cost<F8>()> pc(p, r); pc.live; pc.step(), ++pv_it) {
       const int st = pv_it % NS;
-      if (!mbar_wait(bar_addr(m.p_full[st]), (pv_it / NS) & 1, abort, kTimeoutNs)) {
+      if (!issuer_wait<MULTI == 3>(bar_addr(m.p_full[st]), (pv_it / NS) & 1, abort, kTimeoutNs)) {
         ok = false;
         break;
       }
       const bool fresh = pc.first();
-      if (fresh && !mbar_wait(bar_addr(m.o_free), (o_it & 1) ^ 1, abort, kTimeoutNs)) {
+      if (fresh && !issuer_wait<MULTI == 3>(bar_addr(m.o_free), (o_it & 1) ^ 1, abort, kTimeoutNs)) {
         ok = false;
         break;
       }
       tc_fence_after();
       const uint64_t dp = dp0 + st * kStageEnc;
       const int ksteps = (pc.nv() + 31) >> 5;
+      if (issuer<MULTI == 3>())
 #pragma unroll
       for (int ks = 0; ks < 2; ++ks) {
         if (ks < ksteps) {
@@ -624,15 +654,15 @@ __device__ __forceinline__ void tc_mma_pv(const TcParams &tp, const CtaRange &r,
           }
         }
       }
-      mma_commit(bar_addr(m.kv_empty[st]));
-      mma_commit(bar_addr(m.p_free[st]));
-      if (pc.last()) {
-        mma_commit(bar_addr(m.o_full));
-        ++o_it;
+      if (issuer<MULTI == 3>()) {
+        mma_commit(bar_addr(m.kv_empty[st]));
+        mma_commit(bar_addr(m.p_free[st]));
+        if (pc.last()) mma_commit(bar_addr(m.o_full));
       }
+      if (pc.last()) ++o_it;
     }
     if (!ok) atomicOr(err, kErrTimeout);
-    mma_commit(bar_addr(m.drain));
+    if (issuer<MULTI == 3>()) mma_commit(bar_addr(m.drain));
     mbar_wait_drain(bar_addr(m.drain), 0, kDrainNs);
     return;
   }
@@ -650,12 +680,12 @@ __device__ __forceinline__ void tc_mma_pv(const TcParams &tp, const CtaRange &r,
   uint32_t pv_it = 0, o_it = 0;
   bool ok = true;
   for (TileCursor<FUSED, MULTI, piece_cost<F8>()> pc(p, r); pc.live; pc.step(), ++pv_it) {
-    if (!mbar_wait(bar_addr(m.p_full[pv_it & 1]), (pv_it >> 1) & 1, abort, kTimeoutNs)) {
+    if (!issuer_wait<MULTI == 3>(bar_addr(m.p_full[pv_it & 1]), (pv_it >> 1) & 1, abort, kTimeoutNs)) {
       ok = false;
       break;
     }
     const bool fresh = pc.first();
-    if (fresh && !mbar_wait(bar_addr(m.o_free), (o_it & 1) ^ 1, abort, kTimeoutNs)) {
+    if (fresh && !issuer_wait<MULTI == 3>(bar_addr(m.o_free), (o_it & 1) ^ 1, abort, kTimeoutNs)) {
       ok = false;
       break;
     }
@@ -663,6 +693,7 @@ __device__ __forceinline__ void tc_mma_pv(const TcParams &tp, const CtaRange &r,
     const int st = pv_it & 1;
     const uint64_t dp = dp0 + st * kStageEnc;
     const int ksteps = (pc.nv() + 15) >> 4;
+    if (issuer<MULTI == 3>())
 #pragma unroll
     for (int ks = 0; ks < 4; ++ks) {
       if (ks < ksteps) {
@@ -675,15 +706,15 @@ __device__ __forceinline__ void tc_mma_pv(const TcParams &tp, const CtaRange &r,
         }
       }
     }
-    mma_commit(bar_addr(m.kv_empty[st]));
-    mma_commit(bar_addr(m.p_free[st]));
-    if (pc.last()) {
-      mma_commit(bar_addr(m.o_full));
-      ++o_it;
+    if (issuer<MULTI == 3>()) {
+      mma_commit(bar_addr(m.kv_empty[st]));
+      mma_commit(bar_addr(m.p_free[st]));
+      if (pc.last()) mma_commit(bar_addr(m.o_full));
     }
+    if (pc.last()) ++o_it;
   }
   if (!ok) atomicOr(err, kErrTimeout);
-  mma_commit(bar_addr(m.drain));
+  if (issuer<MULTI == 3>()) mma_commit(bar_addr(m.drain));
   mbar_wait_drain(bar_addr(m.drain), 0, kDrainNs);
 }
 
@@ -1367,9 +1398,9 @@ __global__ void __launch_bounds__(tc_threads<F8>(), 1)
       tc_producer<F8, FUSED, MULTI, AHEAD>(tp, r, m, sbase + kOffQ, sKv, &tm_q, &tm_kv, &tm_kvg, &tm_kvb,
                                            err);
     } else if (warp == 1 || warp == 2) {
-      if (lane == 0) tc_mma_s<F8, FUSED, MULTI, KBG>(tp, r, m, sbase + kOffQ, sKv, tmem, warp - 1, err);
+      if (MULTI == 3 || lane == 0) tc_mma_s<F8, FUSED, MULTI, KBG>(tp, r, m, sbase + kOffQ, sKv, tmem, warp - 1, err);
     } else if (warp == 3 || warp == 8) {
-      if (lane == 0) tc_mma_pv<F8, FUSED, MULTI, KBG>(tp, r, m, sKv, tmem, warp == 8, err);
+      if (MULTI == 3 || lane == 0) tc_mma_pv<F8, FUSED, MULTI, KBG>(tp, r, m, sKv, tmem, warp == 8, err);
     } else if (warp < 8) {
       tc_softmax<F8, FUSED, MULTI, KBG>(tp, r, m, smem, tmem, err);
     } else if constexpr (F8) {

@@ -379,15 +379,6 @@ __device__ __forceinline__ void tma_load_4d_pair(uint32_t dst, const void *tmap,
       "l"(reinterpret_cast<uint64_t>(tmap)), "r"(bar), "r"(c0), "r"(c1), "r"(c2), "r"(c3)
       : "memory");
 }
-// The same box into this offset of every CTA of `mask`, its bytes counted on the
-// barrier of each one's pair.
-__device__ __forceinline__ void tma_load_4d_pair_multicast(uint32_t dst, const void *tmap, uint32_t bar, int c0,
-                                                           int c1, int c2, int c3, uint16_t mask) {
-  asm volatile(
-      "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes.multicast::cluster.cta_group::2 [%0], [%1, {%3, %4, %5, %6}], [%2], %7;" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(tmap)), "r"(bar), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "h"(mask)
-      : "memory");
-}
 __device__ __forceinline__ void tma_load_2d_pair(uint32_t dst, const void *tmap, uint32_t bar, int c0, int c1) {
   asm volatile(
       "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes.cta_group::2 [%0], [%1, {%3, %4}], [%2];" ::"r"(dst),
@@ -415,12 +406,12 @@ __device__ __forceinline__ void mma_bf16_ss_pair(uint32_t d_tmem, uint64_t a_des
       : "memory");
 }
 
-// Arrive once on the barrier at this offset in every CTA of `mask` when all
+// Arrive once on the barrier at this offset in both CTAs of the pair when all
 // MMAs this thread issued before are complete.
-__device__ __forceinline__ void mma_commit_pair(uint32_t bar, uint16_t mask) {
+__device__ __forceinline__ void mma_commit_pair(uint32_t bar) {
   asm volatile(
       "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
-      "h"(mask)
+      "h"(uint16_t(3))
       : "memory");
 }
 

@@ -222,13 +222,11 @@ __global__ void __launch_bounds__(kMergeWarps * 32, 7) shared_merge_kernel(Decod
   const int local = row - group_start(p, g) * p.heads;
   // slots of the two sets: first, stride, number; the row's place in them
   int first[2] = {0, 0}, num[2] = {0, 0}, hl[2] = {local & 63, r & 63};
-  const int stride = p.pair_blocks ? 2 * p.cluster_pairs : 1;  // a cluster's piece has a slot per CTA
+  const int stride = p.pair_blocks ? 2 : 1;  // a pair's piece has a slot per CTA
   const int V = p.batch * p.head_groups + p.prefix_blocks;
   if (local >= 0) {
     const int blocks = p.pair_blocks ? p.pair_blocks : p.prefix_blocks;
-    const int v = p.cluster_pairs == 2   ? block_base<256>(p, g) + (local >> 8)
-                  : p.cluster_pairs == 1 ? block_base<128>(p, g) + (local >> 7)
-                                         : block_base<64>(p, g) + (local >> 6);
+    const int v = p.pair_blocks ? block_base<128>(p, g) + (local >> 7) : block_base<64>(p, g) + (local >> 6);
     if (v < blocks) {
       const int4 i = info_ptr(p)[p.pair_blocks ? V + v : v];
       if (i.y > 0 && i.z >= 0 && (i.z + i.y) * stride <= slots)

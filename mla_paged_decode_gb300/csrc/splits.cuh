@@ -23,9 +23,9 @@ __device__ __forceinline__ SplitInfo split_info(const CtaRange &r, int v, long l
 }
 
 // Slots (of 64 rows) that the pair kernel's pieces take, before the others:
-// one per CTA of a cluster for every (cluster, block).
+// one per CTA of a pair for every (pair, block).
 __host__ __device__ __forceinline__ int pair_slots(const DecodeParams &p) {
-  return 2 * p.cluster_pairs * (p.pair_blocks + p.clusters);
+  return 2 * (p.pair_blocks + p.pairs);
 }
 __device__ __forceinline__ float *slot_lse_ptr(const DecodeParams &p) {
   return reinterpret_cast<float *>(p.ws + p.wl.slot_lse);
