@@ -433,11 +433,47 @@ __device__ __forceinline__ long long request_cost(int tiles, int piece_cost) {
 
 // Block-wide: computes worker `idx`'s range of V requests over `workers`
 // workers.  All threads must call it.  `scratch` needs blockDim.x / 32 + 1
-// long longs of shared memory.
-template <int PC, typename Tiles>
+// long longs of shared memory.  ONCE: with at most a request per thread,
+// tiles_of runs once and a single scan finds the range.
+template <int PC, bool ONCE, typename Tiles>
 __device__ __forceinline__ void schedule_range(int V, int idx, int workers, Tiles tiles_of, CtaRange *r,
                                                long long *scratch) {
   const int tid = threadIdx.x, nw = blockDim.x / 32, lane = tid & 31, warp = tid >> 5;
+  if constexpr (ONCE) {
+    if (V <= int(blockDim.x)) {  // a request per thread: one scan gives the total and every start
+      const int tiles = tid < V ? tiles_of(tid) : 0;
+      const long long cst = request_cost(tiles, PC);
+      long long incl = cst;
+      for (int o = 1; o < 32; o <<= 1) {
+        const long long y = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += y;
+      }
+      if (lane == 31) scratch[warp] = incl;
+      if (tid == 0) r->v_begin = V;
+      __syncthreads();
+      long long before = 0, C = 0;
+      for (int w = 0; w < nw; ++w) {
+        if (w < warp) before += scratch[w];
+        C += scratch[w];
+      }
+      const int g_eff = int(C < (long long)workers ? C : (long long)workers);
+      const bool has = g_eff > 0 && idx < g_eff;
+      const long long start = has ? sched_start(idx, C, g_eff) : 0;
+      const long long excl = before + incl - cst;
+      if (tid == 0) {
+        r->total = C;
+        r->g_eff = g_eff;
+        r->start = start;
+        r->end = has ? sched_start(idx + 1, C, g_eff) : 0;
+      }
+      if (has && tiles > 0 && excl + tiles > start && excl - PC <= start) {
+        r->v_begin = tid;
+        r->p_begin = excl;
+      }
+      __syncthreads();
+      return;
+    }
+  }
   // pass 1: total cost
   long long mine = 0;
   for (int v = tid; v < V; v += blockDim.x) mine += request_cost(tiles_of(v), PC);
@@ -496,8 +532,8 @@ __device__ __forceinline__ void schedule_range(int V, int idx, int workers, Tile
 // This CTA's range of a launch whose workers are its CTAs.
 template <int MULTI = 0, int PC = kPieceCost>
 __device__ inline void cta_schedule(const DecodeParams &p, CtaRange *r, long long *scratch) {
-  schedule_range<PC>(virtual_requests<MULTI>(p), int(blockIdx.x), int(gridDim.x),
-                     [&](int v) { return request_tiles<MULTI>(p, v); }, r, scratch);
+  schedule_range<PC, false>(virtual_requests<MULTI>(p), int(blockIdx.x), int(gridDim.x),
+                            [&](int v) { return request_tiles<MULTI>(p, v); }, r, scratch);
 }
 
 // ---------------------------------------------------------------- conversions

@@ -582,8 +582,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   // blocks without pages have no partials
   for (int v = int(blockIdx.x) * kThreads + tid; v < p.pair_blocks; v += int(gridDim.x) * kThreads)
     if (block_tiles(p, v) == 0) info_ptr(p)[p.batch * p.head_groups + v] = make_int4(-1, 0, 0, 0);
-  schedule_range<kPieceTiles>(p.pair_blocks, pair_id, p.pairs, [&](int v) { return block_tiles(p, v); },
-                              &m.range, m.scratch);
+  schedule_range<kPieceTiles, true>(p.pair_blocks, pair_id, p.pairs, [&](int v) { return block_tiles(p, v); },
+                                    &m.range, m.scratch);
   tc_fence_before();
   cluster_sync();  // both CTAs' barriers and TMEM are ready
   tc_fence_after();

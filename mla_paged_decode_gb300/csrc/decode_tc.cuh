@@ -171,6 +171,7 @@ struct TcMisc {
   alignas(16) unsigned char stage_out[4][2048];  // epilogue: per-warp transpose buffer
   uint32_t conv_max[4];
   CtaRange range;
+  ViewReq view0;                  // views only: the first piece's view
   long long scratch[tc::kThreadsF8 / 32 + 1];
 };
 static_assert(sizeof(TcMisc<2>) + 1024 <= tc::kSmemBytes - tc::off_misc<false>(), "shared memory budget");
@@ -197,12 +198,13 @@ struct Walk {
   int rb, part, pc;  // input request of output row b, its partition, the map's partition coordinate
   long long pv, t0, t1;
   std::conditional_t<MULTI == 3, ViewReq, NoView> view;
-  __device__ Walk(const DecodeParams &p_, const CtaRange &r_)
-      : p(p_), r(r_), V(virtual_requests<MULTI>(p_)), v(r_.v_begin), pv(r_.p_begin) {}
+  const ViewReq *first;  // views: the first piece's, in shared memory
+  __device__ Walk(const DecodeParams &p_, const CtaRange &r_, const ViewReq *first_)
+      : p(p_), r(r_), V(virtual_requests<MULTI>(p_)), v(r_.v_begin), pv(r_.p_begin), first(first_) {}
   __device__ bool next() {
     while (v < V && pv < r.end) {
       if constexpr (MULTI == 3) {
-        view = view_req(p, v);
+        view = v == r.v_begin ? *first : view_req(p, v);
         tiles = view.tiles;
         if (tiles == 0) { ++v; continue; }
         t0 = max(r.start, pv) - pv;
@@ -250,7 +252,7 @@ struct TileCursor {
   Walk<FUSED, MULTI, PC> w;
   long long t;
   bool live;
-  __device__ TileCursor(const DecodeParams &p, const CtaRange &r) : w(p, r), t(0) {
+  __device__ TileCursor(const DecodeParams &p, const CtaRange &r, const ViewReq *first) : w(p, r, first), t(0) {
     live = w.next();
     if (live) t = w.t0;
   }
@@ -345,7 +347,7 @@ __device__ __forceinline__ void tc_producer(const TcParams &tp, const CtaRange &
   // one or two tiles early, when the page is prefetched into L2 (the
   // 129 MB L2 gives the two shared-memory stages more HBM requests in
   // flight), and carried in `ring` until its tile is loaded.
-  TileCursor<FUSED, MULTI, piece_cost<F8>()> ahead(p, r);
+  TileCursor<FUSED, MULTI, piece_cost<F8>()> ahead(p, r, &m.view0);
   auto next_ahead = [&]() {
     int pg = -1;
     if (ahead.live) {
@@ -379,7 +381,7 @@ __device__ __forceinline__ void tc_producer(const TcParams &tp, const CtaRange &
 #pragma unroll
   for (int i = 0; i < AHEAD; ++i) ring[i] = next_ahead();
 
-  TileCursor<FUSED, MULTI, piece_cost<F8>()> cur(p, r);
+  TileCursor<FUSED, MULTI, piece_cost<F8>()> cur(p, r, &m.view0);
   while (cur.live) {
     if (!F8 && cur.first()) {  // (e4m3: warps 9..11 load and split Q)
       checked_len(p, cur.w.rb, err);
@@ -512,7 +514,7 @@ __device__ __forceinline__ void tc_mma_s(const TcParams &tp, const CtaRange &r, 
     constexpr uint64_t kStageEnc = uint64_t(kFxStageBytes) >> 4;
     uint32_t s_it = 0, q_it = 0;
     bool ok = true;
-    for (TileCursor<FUSED, MULTI, piece_cost<F8>()> sc(p, r); sc.live; sc.step(), ++s_it) {
+    for (TileCursor<FUSED, MULTI, piece_cost<F8>()> sc(p, r, &m.view0); sc.live; sc.step(), ++s_it) {
       const int st = s_it % NS, sb = s_it & 1;
       const uint32_t ph = (s_it / NS) & 1;
       if (sc.first()) {
@@ -558,7 +560,7 @@ __device__ __forceinline__ void tc_mma_s(const TcParams &tp, const CtaRange &r, 
   constexpr uint64_t kStageEnc = uint64_t(kStageBytes) >> 4;
   uint32_t s_it = 0, q_it = 0;
   bool ok = true;
-  for (TileCursor<FUSED, MULTI, piece_cost<F8>()> sc(p, r); sc.live; sc.step(), ++s_it) {
+  for (TileCursor<FUSED, MULTI, piece_cost<F8>()> sc(p, r, &m.view0); sc.live; sc.step(), ++s_it) {
     const int st = s_it & 1;
     const uint32_t ph = (s_it >> 1) & 1;
     if (!issuer_wait<MULTI == 3>(bar_addr(m.kv_full[st][0]), ph, abort, kTimeoutNs)) {
@@ -627,7 +629,7 @@ __device__ __forceinline__ void tc_mma_pv(const TcParams &tp, const CtaRange &r,
     const uint64_t dp0 = smem_desc_noswz(sKv + 4 * kFxBlock, kFxPLbo, kFxPSbo);
     uint32_t pv_it = 0, o_it = 0;
     bool ok = true;
-    for (TileCursor<FUSED, MULTI, piece_cost<F8>()> pc(p, r); pc.live; pc.step(), ++pv_it) {
+    for (TileCursor<FUSED, MULTI, piece_cost<F8>()> pc(p, r, &m.view0); pc.live; pc.step(), ++pv_it) {
       const int st = pv_it % NS;
       if (!issuer_wait<MULTI == 3>(bar_addr(m.p_full[st]), (pv_it / NS) & 1, abort, kTimeoutNs)) {
         ok = false;
@@ -679,7 +681,7 @@ __device__ __forceinline__ void tc_mma_pv(const TcParams &tp, const CtaRange &r,
   constexpr uint64_t kStageEnc = uint64_t(kStageBytes) >> 4;
   uint32_t pv_it = 0, o_it = 0;
   bool ok = true;
-  for (TileCursor<FUSED, MULTI, piece_cost<F8>()> pc(p, r); pc.live; pc.step(), ++pv_it) {
+  for (TileCursor<FUSED, MULTI, piece_cost<F8>()> pc(p, r, &m.view0); pc.live; pc.step(), ++pv_it) {
     if (!issuer_wait<MULTI == 3>(bar_addr(m.p_full[pv_it & 1]), (pv_it >> 1) & 1, abort, kTimeoutNs)) {
       ok = false;
       break;
@@ -806,6 +808,50 @@ static __device__ __noinline__ void zero_value_rows(unsigned char *stage, int r0
   }
 }
 
+// A view's epilogue: 16 rows at a time, a warp's 32 value dims of a chunk
+// (dims d0 + 128 c) go through its 2 KB buffer and leave as 16-byte runs, fp32
+// to the partial `part` or bf16 to `out`.  Only the block's own rows are read
+// and stored: 16 rows take 2,800 cycles, 64 rows 8,100 (the other variants'
+// epilogue: 6,300 and 8,100).  Asking L2 to keep the partials, as that one
+// does, cost 1 to 4 % of these calls.
+__device__ __forceinline__ void view_epilogue(uint32_t tq, const float *scale, unsigned char *stg, float *part,
+                                              __nv_bfloat16 *out, int rows, int d0) {
+  using namespace tc;
+  const int lane = threadIdx.x & 31;
+  float *buf = reinterpret_cast<float *>(stg);
+#pragma unroll 1
+  for (int hb = 0; hb < rows; hb += 16) {
+    float sc[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) sc[i] = scale[hb + i];
+#pragma unroll 1
+    for (int c = 0; c < 4; ++c) {
+      uint32_t o[16];
+      tmem_ld16(tq + kColO + 64 * c + hb, o);
+      tmem_wait_ld();
+#pragma unroll
+      for (int i = 0; i < 16; ++i) buf[i * 32 + lane] = __uint_as_float(o[i]) * sc[i];
+      __syncwarp();
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {  // 16 rows x 8 runs of 4 dims
+        const int h = hb + (lane >> 3) + 4 * j;
+        const float4 v = reinterpret_cast<const float4 *>(buf)[lane + 32 * j];
+        const size_t at = size_t(h) * kDv + d0 + 128 * c + 4 * (lane & 7);
+        if (h < rows) {
+          if (part) {
+            *reinterpret_cast<float4 *>(part + at) = v;
+          } else {
+            __nv_bfloat162 lo = __floats2bfloat162_rn(v.x, v.y), hi = __floats2bfloat162_rn(v.z, v.w);
+            *reinterpret_cast<uint2 *>(out + at) =
+                make_uint2(*reinterpret_cast<uint32_t *>(&lo), *reinterpret_cast<uint32_t *>(&hi));
+          }
+        }
+      }
+      __syncwarp();
+    }
+  }
+}
+
 template <bool F8, bool FUSED, int MULTI, int KBG>
 __device__ __forceinline__ void tc_softmax(const TcParams &tp, const CtaRange &r, TcMiscFor<F8> &m,
                            unsigned char *smem, uint32_t tmem, int *err) {
@@ -837,7 +883,7 @@ __device__ __forceinline__ void tc_softmax(const TcParams &tp, const CtaRange &r
   if (masked) own = owner_mask_of(p);
 
   uint32_t piece = 0;
-  Walk<FUSED, MULTI, piece_cost<F8>()> w(p, r);
+  Walk<FUSED, MULTI, piece_cost<F8>()> w(p, r, &m.view0);
   for (; ok && w.next(); w.advance(), ++piece) {
     const int hn = w.rows();
     if (F8) {
@@ -1106,6 +1152,10 @@ __device__ __forceinline__ void tc_softmax(const TcParams &tp, const CtaRange &r
     } else {
       out_row0 = size_t(w.b) * p.heads + size_t(w.g) * kHeads;
     }
+    if constexpr (VIEW) {
+      view_epilogue(tq, m.ell, m.stage_out[q], split ? slot_out_ptr(p) + size_t(si.slot) * kSlotHeads * kDv : nullptr,
+                    p.out + out_row0 * kDv, hn, 32 * q);
+    } else {
     // This warp owns value dims 128c + 32q .. + 31 of each chunk c (its TMEM
     // lanes).  Values go through a 2 KB per-warp buffer, transposed to
     // [head][dim], so that each lane stores 16-byte runs of dims: 8 (bf16)
@@ -1163,6 +1213,7 @@ __device__ __forceinline__ void tc_softmax(const TcParams &tp, const CtaRange &r
           __syncwarp();
         }
       }
+    }
     }
     tc_fence_before();
     __syncwarp();
@@ -1244,7 +1295,7 @@ __device__ __forceinline__ void tc_split_q(const TcParams &tp, const CtaRange &r
   static_assert(kHeads * kRowChunks % (16 * kConvThreads) == 0, "Q split batches");
   uint32_t q_it = 0;
   bool ok = true;
-  Walk<FUSED, MULTI, kPieceCostE4m3> w(p, r), wa(p, r);  // wa: the piece after w
+  Walk<FUSED, MULTI, kPieceCostE4m3> w(p, r, &m.view0), wa(p, r, &m.view0);  // wa: the piece after w
   bool ahead = wa.next();
   uint32_t mx = ahead ? piece_q_max(p, wa, m, ct) : 0u;
   if (ahead) {
@@ -1384,14 +1435,32 @@ __global__ void __launch_bounds__(tc_threads<F8>(), 1)
   // before reading any input or writing any output.  (Releasing this
   // launch's own dependent, the split merge, early as well measured slower.)
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  write_empty_requests<MULTI>(p);
-  cta_schedule<MULTI, piece_cost<F8>()>(p, &m.range, m.scratch);
+  // (views leave this to a warp that has nothing to do yet)
+  if (MULTI != 3) write_empty_requests<MULTI>(p);
+  if constexpr (MULTI == 3) {
+    const int V = virtual_requests<3>(p);
+    ViewReq mine;
+    schedule_range<piece_cost<F8>(), true>(V, int(blockIdx.x), int(gridDim.x), [&](int v) {
+      mine = view_req(p, v);
+      return mine.tiles;
+    }, &m.range, m.scratch);
+    // the roles start from the first piece's view and its page's entry
+    const int v0 = m.range.v_begin;
+    if (V > int(blockDim.x) && v0 < V) mine = view_req(p, v0);
+    if (v0 < V && tid == (V > int(blockDim.x) ? 0 : v0)) {
+      m.view0 = mine;
+      prefetch_l2(p.block_table + size_t(mine.req) * p.max_pages + mine.page(max(m.range.start - m.range.p_begin, 0ll)));
+    }
+  } else {
+    cta_schedule<MULTI, piece_cost<F8>()>(p, &m.range, m.scratch);
+  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = m.tmem_base;
   const CtaRange r = m.range;
 
+  if (MULTI == 3 && warp == 8) write_empty_views(p);
   if (r.start < r.end) {
     const uint32_t sKv = sbase + off_kv<F8>();
     if (warp == 0) {

@@ -211,7 +211,7 @@ __global__ void __launch_bounds__(kDcpMaxParts * 32) dcp_merge_combine_kernel(De
 
 // Shared pages: a row's partials are those of its group's block over the
 // shared pages and those of its request over its own.  One warp per row, each
-// lane 16 value dims; the LSE-weighted combine of all of them.
+// lane four runs of four value dims; the LSE-weighted combine of all of them.
 __global__ void __launch_bounds__(kMergeWarps * 32, 7) shared_merge_kernel(DecodeParams p, int slots) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int lane = threadIdx.x & 31;
@@ -244,6 +244,17 @@ __global__ void __launch_bounds__(kMergeWarps * 32, 7) shared_merge_kernel(Decod
     const int s = k < num[0] ? first[0] + k * stride : first[1] + k - num[0];
     return size_t(s) * kSlotHeads + hl[k < num[0] ? 0 : 1];
   };
+  // the first partials' loads go out before the weights are known
+  float4 x[kMergeBatch][4];
+  auto load = [&](int k0) {
+#pragma unroll
+    for (int u = 0; u < kMergeBatch; ++u) {
+      const float4 *src = reinterpret_cast<const float4 *>(so + at(min(k0 + u, ns - 1)) * kDv);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) x[u][i] = src[lane + 32 * i];
+    }
+  };
+  if (ns > 0) load(0);
   float mx = -INFINITY;
   for (int k = lane; k < ns; k += 32) mx = fmaxf(mx, sl[at(k)]);
   for (int o = 16; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
@@ -253,36 +264,26 @@ __global__ void __launch_bounds__(kMergeWarps * 32, 7) shared_merge_kernel(Decod
   for (int i = 0; i < 4; ++i) acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
   float sum = 0.f;
   for (int k0 = 0; k0 < ns; k0 += kMergeBatch) {
-    float4 x[kMergeBatch][4];
-    float w[kMergeBatch];
+    if (k0 > 0) load(k0);
 #pragma unroll
     for (int u = 0; u < kMergeBatch; ++u) {
-      const bool in = k0 + u < ns;
-      const size_t a = at(in ? k0 + u : k0);
-      w[u] = in ? exp2f(sl[a] - mref) : 0.f;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) x[u][i] = reinterpret_cast<const float4 *>(so + a * kDv)[4 * lane + i];
-    }
-#pragma unroll
-    for (int u = 0; u < kMergeBatch; ++u) {
-      sum += w[u];
+      const float w = k0 + u < ns ? exp2f(sl[at(k0 + u)] - mref) : 0.f;
+      sum += w;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        acc[i].x += w[u] * x[u][i].x; acc[i].y += w[u] * x[u][i].y;
-        acc[i].z += w[u] * x[u][i].z; acc[i].w += w[u] * x[u][i].w;
+        acc[i].x += w * x[u][i].x; acc[i].y += w * x[u][i].y;
+        acc[i].z += w * x[u][i].z; acc[i].w += w * x[u][i].w;
       }
     }
   }
   const float inv = sum > 0.f ? 1.f / sum : 0.f;
-  uint32_t pk[8];
+  uint2 *dst = reinterpret_cast<uint2 *>(p.out + size_t(row) * kDv);
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     __nv_bfloat162 lo = __floats2bfloat162_rn(acc[i].x * inv, acc[i].y * inv);
     __nv_bfloat162 hi = __floats2bfloat162_rn(acc[i].z * inv, acc[i].w * inv);
-    pk[2 * i] = *reinterpret_cast<uint32_t *>(&lo);
-    pk[2 * i + 1] = *reinterpret_cast<uint32_t *>(&hi);
+    dst[lane + 32 * i] = make_uint2(*reinterpret_cast<uint32_t *>(&lo), *reinterpret_cast<uint32_t *>(&hi));
   }
-  store_row(p.out + size_t(row) * kDv, pk);
   if (lane == 0) p.lse[row] = sum > 0.f ? lse_out(p, mref + log2f(sum)) : -INFINITY;
 }
 

@@ -65,21 +65,8 @@ __device__ __forceinline__ void check_view(const DecodeParams &p, int v, int *er
 // is handled by CTA v mod gridDim.x.  Block-wide.
 template <int MULTI = 0>
 __device__ inline void write_empty_requests(const DecodeParams &p) {
-  const int V = virtual_requests<MULTI>(p);
+  const int V = p.batch * p.head_groups;
   int *err = error_word(p);
-  if constexpr (MULTI == 3) {
-    for (int v = blockIdx.x; v < V; v += gridDim.x) {
-      const ViewReq r = view_req(p, v);
-      if (threadIdx.x == 0) check_view(p, v, err);
-      if (r.tiles != 0) continue;
-      if (threadIdx.x == 0) info_ptr(p)[v] = make_int4(-1, 0, 0, 0);
-      if (p.view == kViewShared) continue;  // the merge writes every row
-      uint4 *dst = reinterpret_cast<uint4 *>(p.out + size_t(r.row0) * kDv);
-      for (int i = threadIdx.x; i < r.rows * kDv / 8; i += blockDim.x) dst[i] = make_uint4(0, 0, 0, 0);
-      for (int i = threadIdx.x; i < r.rows; i += blockDim.x) p.lse[size_t(r.row0) + i] = -INFINITY;
-    }
-    return;
-  }
   for (int v = blockIdx.x; v < V; v += gridDim.x) {
     int b = vreq_row(p, v), g = vreq_group(p, v);  // b: output row
     if (request_len<MULTI>(p, v, threadIdx.x == 0 ? err : nullptr) != 0) continue;
@@ -91,6 +78,22 @@ __device__ inline void write_empty_requests(const DecodeParams &p) {
     for (int i = threadIdx.x; i < hn; i += blockDim.x)
       p.lse[size_t(b) * p.heads + h0 + i] = -INFINITY;
   }
+}
+
+// The same for views, by one warp of the CTA, with the checks of the inputs.
+__device__ inline void write_empty_views(const DecodeParams &p) {
+  const int lane = threadIdx.x & 31, V = virtual_requests<3>(p);
+  for (int v = blockIdx.x; v < V; v += gridDim.x) {
+    if (lane == 0) check_view(p, v, error_word(p));
+    const ViewReq r = view_req(p, v);
+    if (r.tiles != 0) continue;
+    if (lane == 0) info_ptr(p)[v] = make_int4(-1, 0, 0, 0);
+    if (p.view == kViewShared) continue;  // the merge writes every row
+    uint4 *dst = reinterpret_cast<uint4 *>(p.out + size_t(r.row0) * kDv);
+    for (int i = lane; i < r.rows * kDv / 8; i += 32) dst[i] = make_uint4(0, 0, 0, 0);
+    for (int i = lane; i < r.rows; i += 32) p.lse[size_t(r.row0) + i] = -INFINITY;
+  }
+  __syncwarp();
 }
 
 // Called (by one thread) in each CTA that worked on request v: the CTA that
