@@ -210,13 +210,19 @@ __global__ void __launch_bounds__(kDcpMaxParts * 32) dcp_merge_combine_kernel(De
 }
 
 // Shared pages: a row's partials are those of its group's block over the
-// shared pages and those of its request over its own.  One warp per row, each
-// lane four runs of four value dims; the LSE-weighted combine of all of them.
+// shared pages and those of its request over its own; the result is the
+// LSE-weighted combine of all of them, each lane of a warp four runs of four
+// value dims.  Many rows: a warp per row.  Few rows (WIDE): the schedule
+// spreads them over all SMs, a row may have over a hundred partials, and a CTA
+// takes a row, each of its warps every fourth partial (64 rows over 8K shared
+// tokens: 45 us a call with a warp per row).
+template <bool WIDE>
 __global__ void __launch_bounds__(kMergeWarps * 32, 7) shared_merge_kernel(DecodeParams p, int slots) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int lane = threadIdx.x & 31;
-  const int row = blockIdx.x * kMergeWarps + (threadIdx.x >> 5);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int row = WIDE ? blockIdx.x : blockIdx.x * kMergeWarps + warp;
   if (row >= p.batch * p.heads) return;
+  const int k_first = WIDE ? warp : 0, k_step = WIDE ? kMergeWarps : 1;  // this warp's partials
   const int b = row / p.heads, r = row - b * p.heads;
   const int g = group_of_request(p, b);
   const int local = row - group_start(p, g) * p.heads;
@@ -249,12 +255,12 @@ __global__ void __launch_bounds__(kMergeWarps * 32, 7) shared_merge_kernel(Decod
   auto load = [&](int k0) {
 #pragma unroll
     for (int u = 0; u < kMergeBatch; ++u) {
-      const float4 *src = reinterpret_cast<const float4 *>(so + at(min(k0 + u, ns - 1)) * kDv);
+      const float4 *src = reinterpret_cast<const float4 *>(so + at(min(k0 + u * k_step, ns - 1)) * kDv);
 #pragma unroll
       for (int i = 0; i < 4; ++i) x[u][i] = src[lane + 32 * i];
     }
   };
-  if (ns > 0) load(0);
+  if (ns > 0) load(k_first);
   float mx = -INFINITY;
   for (int k = lane; k < ns; k += 32) mx = fmaxf(mx, sl[at(k)]);
   for (int o = 16; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
@@ -263,16 +269,35 @@ __global__ void __launch_bounds__(kMergeWarps * 32, 7) shared_merge_kernel(Decod
 #pragma unroll
   for (int i = 0; i < 4; ++i) acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
   float sum = 0.f;
-  for (int k0 = 0; k0 < ns; k0 += kMergeBatch) {
-    if (k0 > 0) load(k0);
+  for (int k0 = k_first; k0 < ns; k0 += kMergeBatch * k_step) {
+    if (k0 > k_first) load(k0);
 #pragma unroll
     for (int u = 0; u < kMergeBatch; ++u) {
-      const float w = k0 + u < ns ? exp2f(sl[at(k0 + u)] - mref) : 0.f;
+      const int k = k0 + u * k_step;
+      const float w = k < ns ? exp2f(sl[at(k)] - mref) : 0.f;
       sum += w;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         acc[i].x += w * x[u][i].x; acc[i].y += w * x[u][i].y;
         acc[i].z += w * x[u][i].z; acc[i].w += w * x[u][i].w;
+      }
+    }
+  }
+  if constexpr (WIDE) {  // the warps' sums, in the order of the warps
+    __shared__ float4 s_acc[kMergeWarps][4][32];
+    __shared__ float s_sum[kMergeWarps];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) s_acc[warp][i][lane] = acc[i];
+    if (lane == 0) s_sum[warp] = sum;
+    __syncthreads();
+    if (warp != 0) return;
+#pragma unroll
+    for (int w = 1; w < kMergeWarps; ++w) {
+      sum += s_sum[w];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float4 o = s_acc[w][i][lane];
+        acc[i].x += o.x; acc[i].y += o.y; acc[i].z += o.z; acc[i].w += o.w;
       }
     }
   }
@@ -289,8 +314,9 @@ __global__ void __launch_bounds__(kMergeWarps * 32, 7) shared_merge_kernel(Decod
 
 cudaError_t launch_shared_merge(const DecodeParams &p, int grid, cudaStream_t stream) {
   const int rows = p.batch * p.heads;
+  const bool wide = rows <= 7 * grid;  // a CTA per row still fits the device in one wave
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((rows + kMergeWarps - 1) / kMergeWarps);
+  cfg.gridDim = dim3(wide ? rows : (rows + kMergeWarps - 1) / kMergeWarps);
   cfg.blockDim = dim3(kMergeWarps * 32);
   cfg.dynamicSmemBytes = 0;
   cfg.stream = stream;
@@ -300,7 +326,8 @@ cudaError_t launch_shared_merge(const DecodeParams &p, int grid, cudaStream_t st
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   const int slots = pair_slots(p) + p.batch * p.head_groups + p.prefix_blocks + grid;
-  return cudaLaunchKernelEx(&cfg, shared_merge_kernel, p, slots);
+  return wide ? cudaLaunchKernelEx(&cfg, shared_merge_kernel<true>, p, slots)
+              : cudaLaunchKernelEx(&cfg, shared_merge_kernel<false>, p, slots);
 }
 
 cudaError_t launch_split_merge(const DecodeParams &p, int grid, cudaStream_t stream) {

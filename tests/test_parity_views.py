@@ -65,35 +65,43 @@ GROUPS = [
 ]
 
 
-@pytest.mark.parametrize("kv_dtype", ["bf16", "e4m3"])
+# A wide block table, whose rows x tokens bound the work, takes a bf16 cache's
+# groups of 128 rows and more to the pair kernel.
+WIDE = 2200
+
+
+@pytest.mark.parametrize("kv_dtype,width", [("bf16", 0), ("bf16", WIDE), ("e4m3", 0), ("e4m3", WIDE)])
 @pytest.mark.parametrize("heads,q_len", [(16, 1), (64, 1), (1, 1), (20, 3), (128, 2), (7, 16), (65, 1)])
 @pytest.mark.parametrize("group", range(len(GROUPS)))
-def test_shared(kv_dtype, heads, q_len, group):
+def test_shared(kv_dtype, width, heads, q_len, group):
     lens, starts, pages = GROUPS[group]
-    c = make(lens, heads, q_len, kv_dtype, causal_seen(q_len), seed=heads + group, shared=(starts, pages))
+    c = make(lens, heads, q_len, kv_dtype, causal_seen(q_len), seed=heads + group, shared=(starts, pages),
+             width=width)
     base = group % 2
     out, lse = run_shared(c, starts, pages, base)
     check(c, out, lse, base, f"group {group}")
 
 
-@pytest.mark.parametrize("kv_dtype", ["bf16", "e4m3"])
+@pytest.mark.parametrize("kv_dtype,width", [("bf16", 0), ("bf16", WIDE), ("e4m3", 0), ("e4m3", WIDE)])
 @pytest.mark.parametrize("n,heads,pages,q_len", [(40, 16, 70, 1), (9, 128, 200, 1), (3, 64, 301, 2), (33, 40, 50, 1)])
-def test_shared_long_prefix(kv_dtype, n, heads, pages, q_len):
+def test_shared_long_prefix(kv_dtype, width, n, heads, pages, q_len):
     lens = [64 * pages + (37 * b) % 300 for b in range(n)]
-    c = make(lens, heads, q_len, kv_dtype, causal_seen(q_len), seed=n, shared=([0, n], [pages]))
+    c = make(lens, heads, q_len, kv_dtype, causal_seen(q_len), seed=n, shared=([0, n], [pages]), width=width)
     check(c, *run_shared(c, [0, n], [pages]), what="long prefix")
 
 
-def test_shared_scores_of_a_wide_range():
+@pytest.mark.parametrize("kv_dtype,width", [("bf16", 0), ("bf16", WIDE), ("e4m3", WIDE)])
+def test_shared_scores_of_a_wide_range(kv_dtype, width):
     """Running maxima that grow across tiles and rows whose weights sit on few tokens."""
     lens = [64 * 30 + 17] * 6
-    c = make(lens, 64, 1, "bf16", causal_seen(1), seed=8, shared=([0, 6], [30]), q_gain=6.0)
+    c = make(lens, 64, 1, kv_dtype, causal_seen(1), seed=8, shared=([0, 6], [30]), q_gain=6.0, width=width)
     check(c, *run_shared(c, [0, 6], [30]), what="wide scores")
 
 
-def test_results_repeat_bit_for_bit_and_workspaces_are_reusable():
+@pytest.mark.parametrize("kv_dtype,width", [("bf16", 0), ("bf16", WIDE), ("e4m3", 0), ("e4m3", WIDE)])
+def test_results_repeat_bit_for_bit_and_workspaces_are_reusable(kv_dtype, width):
     lens = [64 * 40 + 100 * b for b in range(9)]
-    c = make(lens, 64, 1, "bf16", causal_seen(1), seed=4, shared=([0, 4, 9], [40, 40]))
+    c = make(lens, 64, 1, kv_dtype, causal_seen(1), seed=4, shared=([0, 4, 9], [40, 40]), width=width)
     ws = mla.make_shared_workspace(c.q, c.kv, c.table, 2, c.kv_scale)
     first = run_shared(c, [0, 4, 9], [40, 40], ws=ws)
     for _ in range(3):

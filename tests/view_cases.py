@@ -42,9 +42,11 @@ def _rows(c):
     return x
 
 
-def make(lens, heads, q_len, kv_dtype, seen_of, seed, device="cuda", shared=None, spare=3, q_gain=1.0):
+def make(lens, heads, q_len, kv_dtype, seen_of, seed, device="cuda", shared=None, spare=3, q_gain=1.0,
+         width=0):
     """seen_of(L, i): token indices query token i of a request of length L
-    sees.  shared: (group_starts, shared_pages) as lists."""
+    sees.  shared: (group_starts, shared_pages) as lists.  width: columns of
+    the block table, at least."""
     g = torch.Generator().manual_seed(seed)
     need = [-(-L // 64) for L in lens]
     sp = [0] * len(lens)
@@ -53,7 +55,7 @@ def make(lens, heads, q_len, kv_dtype, seen_of, seed, device="cuda", shared=None
         for k, n in enumerate(pages):
             for b in range(starts[k], starts[k + 1]):
                 sp[b] = n
-    width = max(1, max(need, default=1), max(sp, default=1))
+    width = max(1, width, max(need, default=1), max(sp, default=1))
     total = sum(max(0, n - s) for n, s in zip(need, sp)) + (sum(shared[1]) if shared else 0) + spare
     perm = torch.randperm(total, generator=g).to(torch.int32)
     kv = torch.randn(total, 64, 576, generator=g)
