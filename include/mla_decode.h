@@ -409,9 +409,10 @@ int mla_decode_window(const void *q, const void *kv_pages, const int32_t *block_
  *
  * The rows of a group (q_len x num_heads of each of its requests) attend to
  * the shared pages in blocks, each request's rows to its own pages, and the
- * partial results are merged by their LSE.  A bf16 cache whose groups have 128
- * rows or more on average takes blocks of 128 rows on pairs of SMs when rows x
- * tokens (64 * max_pages_per_seq) reach 16 M.  A request outside every group
+ * partial results are merged by their LSE.  Groups of 128 rows or more on
+ * average take blocks of 128 rows on pairs of SMs when rows x tokens (64 *
+ * max_pages_per_seq) reach 16 M.  The shared pages' rows must be finite, also
+ * where a shorter request does not see them.  A request outside every group
  * or a page number outside [0, max_pages_per_seq] is reported as
  * MLA_ERR_BOUNDS by mla_decode_check_workspace.  Arithmetic as for
  * mla_decode_window.  Two or three kernels.

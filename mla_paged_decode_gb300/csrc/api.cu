@@ -31,7 +31,7 @@ cudaError_t launch_decode_tc(const DecodeParams &p, int npv, int q_rows, int gro
                              const CUtensorMap &tm_kvg, const CUtensorMap &tm_kvb, int grid,
                              cudaStream_t stream);
 cudaError_t launch_decode_pair(const DecodeParams &p, const CUtensorMap &tm_q, const CUtensorMap &tm_k,
-                               const CUtensorMap &tm_v, cudaStream_t stream);
+                               const CUtensorMap &tm_k4, const CUtensorMap &tm_v, cudaStream_t stream);
 cudaError_t launch_lse_combine(const void *partials, const float *lses, int num_parts, void *out,
                                float *out_lse, int rows, int dim, int base2, cudaStream_t stream);
 int combine_max_parts();
@@ -310,27 +310,40 @@ int make_tensor_maps(const void *q, const void *kv, const mla_decode_desc *d, in
   return MLA_OK;
 }
 
-// The pair kernel's loads of a bf16 cache, on (64 dims, 8 rows, 9 blocks of 64
-// dims, 8-row groups): one dim block of a page's 64 rows (K), four dim blocks
-// of half a page (V).
-int make_pair_maps(const void *kv, const mla_decode_desc *d, CUtensorMap *tm_k, CUtensorMap *tm_v) {
+// The pair kernel's loads, on (128 bytes, 8 rows, dim blocks of 128 bytes, 8-row
+// groups): one dim block of a page's 64 rows (K); the value dims of one CTA,
+// four blocks of half a bf16 page or two of an e4m3 page (V).  The last 64 dims
+// of an e4m3 page's rows come through tm_k4, 64 bytes a row.
+int make_pair_maps(const void *kv, const mla_decode_desc *d, CUtensorMap *tm_k, CUtensorMap *tm_k4,
+                   CUtensorMap *tm_v) {
   EncodeTiled enc = encode_tiled();
   if (!enc) {
     std::snprintf(g_cuda_error, sizeof(g_cuda_error), "cuTensorMapEncodeTiled unavailable");
     return MLA_ERR_CUDA;
   }
-  const cuuint64_t row = cuuint64_t(mla::kDqk) * 2;
-  cuuint64_t dims[4] = {64, 8, cuuint64_t(mla::kDqk / 64), cuuint64_t(d->num_pages) * 8};
+  const bool f8 = d->kv_dtype == MLA_KV_E4M3;
+  const auto type = f8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+  const cuuint32_t x = f8 ? 128 : 64;  // elements of a 128-byte row
+  const cuuint64_t row = cuuint64_t(mla::kDqk) * (f8 ? 1 : 2);
+  cuuint64_t dims[4] = {x, 8, cuuint64_t(f8 ? 4 : 9), cuuint64_t(d->num_pages) * 8};
   cuuint64_t strides[3] = {row, 128, 8 * row};
-  cuuint32_t box_k[4] = {64, 8, 1, 8}, box_v[4] = {64, 8, 4, 4}, es[4] = {1, 1, 1, 1};
-  CUresult r = enc(tm_k, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(kv), dims, strides, box_k, es,
-                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+  cuuint32_t box_k[4] = {x, 8, 1, 8}, box_v[4] = {x, 8, f8 ? 2u : 4u, f8 ? 8u : 4u}, es[4] = {1, 1, 1, 1};
+  CUresult r = enc(tm_k, type, 4, const_cast<void *>(kv), dims, strides, box_k, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                   CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   if (r != CUDA_SUCCESS) return tensor_map_fail("kv pair K", r);
-  r = enc(tm_v, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(kv), dims, strides, box_v, es,
-          CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  r = enc(tm_v, type, 4, const_cast<void *>(kv), dims, strides, box_v, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+          CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   if (r != CUDA_SUCCESS) return tensor_map_fail("kv pair V", r);
+  *tm_k4 = *tm_k;
+  if (f8) {
+    cuuint64_t dims4[2] = {row, cuuint64_t(d->num_pages) * mla::kPage};
+    cuuint64_t strides4[1] = {row};
+    cuuint32_t box4[2] = {64, mla::kPage};
+    r = enc(tm_k4, type, 2, const_cast<void *>(kv), dims4, strides4, box4, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS) return tensor_map_fail("kv pair rope", r);
+  }
   return MLA_OK;
 }
 
@@ -494,10 +507,10 @@ int enqueue_view(mla::DecodeParams p, const void *q, const void *kv_pages, const
   int st = make_tensor_maps(q, kv_pages, d, h, 0, 1, false, false, &tm_q, &tm_kv, &tm_kvg, &tm_kvb);
   if (st != MLA_OK) return st;
   if (p.pair_blocks) {
-    CUtensorMap tm_k, tm_v;
-    st = make_pair_maps(kv_pages, d, &tm_k, &tm_v);
+    CUtensorMap tm_k, tm_k4, tm_v;
+    st = make_pair_maps(kv_pages, d, &tm_k, &tm_k4, &tm_v);
     if (st != MLA_OK) return st;
-    const cudaError_t e = mla::launch_decode_pair(p, tm_q, tm_k, tm_v, s);
+    const cudaError_t e = mla::launch_decode_pair(p, tm_q, tm_k, tm_k4, tm_v, s);
     if (e != cudaSuccess) return cuda_fail(e);
   }
   const cudaError_t e = mla::launch_decode_tc(p, (h + 15) / 16 * 16, h, 8, tm_q, tm_kv, tm_kvg, tm_kvb, grid, s);
@@ -533,17 +546,17 @@ mla::WorkspaceLayout shared_layout(const mla_decode_desc *d, int num_groups, int
   const int slots = v + num_groups + 2 * grid;
   return mla::workspace_layout(v, (slots + 1) / 2);
 }
-// The pair kernel takes the shared pages of a bf16 cache when the groups fill
-// its blocks of 128 rows on average and there is enough to multiply: it is a
-// kernel more (about 9 us), and nearly twice as fast in the long run.  Rows x
-// tokens of the block table bound the work.  Measured, us a call, pair kernel /
-// blocks of 64 rows in the one kernel: 4096 rows x 1K shared tokens 44 / 34,
-// 1024 x 8K 44 / 38, 256 x 32K 42 / 42, 512 x 32K 57 / 62, 4096 x 8K 79 / 102,
-// 4096 x 32K 214 / 363.
+// The pair kernel takes the shared pages when the groups fill its blocks of 128
+// rows on average and there is enough to multiply: it is a kernel more (9 to 13
+// us), and nearly twice as fast in the long run.  Rows x tokens of the block
+// table bound the work.  Measured, us a call, pair kernel / blocks of 64 rows in
+// the one kernel, bf16: 4096 rows x 1K shared tokens 44 / 34, 1024 x 8K 44 / 38,
+// 256 x 32K 42 / 42, 512 x 32K 57 / 62, 4096 x 8K 79 / 102, 4096 x 32K 214 / 363;
+// e4m3: 50 / 44, 53 / 43, 49 / 42, 60 / 57, 85 / 95, 193 / 277.
 constexpr long long kPairWork = 16LL << 20;
 bool pair_path(const mla_decode_desc *d, int num_groups) {
   const long long rows = (long long)d->batch * rows_of(d);
-  return d->kv_dtype == MLA_KV_BF16 && rows >= 128LL * num_groups &&
+  return rows >= 128LL * num_groups &&
          rows * mla::kPage >= kPairWork / d->max_pages_per_seq;
 }
 constexpr int kMaxGroups = 1 << 20;

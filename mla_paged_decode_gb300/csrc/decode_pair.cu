@@ -16,6 +16,8 @@
 //   V: dims 256r .. 256r + 255 of all four pages, eight units of 32 tokens
 //      (its half of N of the two PV products),
 // 17 units of 16 KB through one ring of seven; a page is read twice, from L2.
+// (e4m3 caches: five units of 128 dims and four of a page, Q and P as two fp8
+// terms each, with the decode kernel's arithmetic.)
 //
 // Roles (384 threads): warp 0 producer, warp 1 score MMAs and TMEM, warp 2 PV
 // MMAs (both in the even CTA only), warps 4..11 softmax and epilogue.  Thread
@@ -42,32 +44,43 @@ constexpr int kRows = 64;                       // per CTA
 constexpr int kPairRows = 128;                  // per pair
 constexpr int kTilePages = 4;
 constexpr int kUnitBytes = 16384;
-constexpr int kRing = 7;
-constexpr int kKUnits = 9, kVUnits = 8;
-constexpr int kQBytes = 9 * kRows * 128;        // [dim block][64 rows][128 B]
-constexpr int kPBytes = kTilePages * kRows * 128;  // [page][64 rows][128 B]
+constexpr int kMaxRing = 7;
+constexpr int kPBytes = kTilePages * kRows * 128;
+// bf16: Q as [dim block of 64][64 rows][128 B], P as [page][64 rows][128 B], both
+// swizzled.  e4m3: Q as two terms of [block of 128 dims][64 rows][128 B],
+// swizzled; P as [page][term][8-row group][16-token chunk][8 rows][16 B].
+constexpr int kQTerm = 5 * kRows * 128;   // e4m3
+constexpr int kPTerm = kRows * kPage;     // e4m3
+template <bool F8>
+struct Cfg {
+  static constexpr int kRing = F8 ? 6 : 7;
+  static constexpr int kKUnits = F8 ? 5 : 9, kVUnits = F8 ? 4 : 8;
+  static constexpr int kQBytes = F8 ? 2 * kQTerm : 9 * kRows * 128;
+  static constexpr int kOffP = kQBytes;
+  static constexpr int kOffRing = kOffP + kPBytes;
+  static constexpr int kOffMisc = kOffRing + kRing * kUnitBytes;
+  static constexpr int kPieceTiles = F8 ? 2 : 1;  // a piece's boundary, in tiles
+};
 constexpr int kOffQ = 0;
-constexpr int kOffP = kOffQ + kQBytes;
-constexpr int kOffRing = kOffP + kPBytes;
-constexpr int kOffMisc = kOffRing + kRing * kUnitBytes;
 constexpr uint32_t kColO = 0, kColS = 256;      // S buffer b: 128 columns from 256 + 128 b
 constexpr int kSoftWarps = 8, kSoftThreads = 256;
-constexpr int kPieceTiles = 1;                  // a piece's boundary, in tiles
 constexpr long long kTimeoutClk = 4000000000ll;  // about 2 s
 constexpr uint64_t kDrainNs = 200000000ull;
 constexpr float kRescaleThreshold = 8.f;        // base-2 units
 
 struct Misc {
-  uint64_t full[2][kRing], empty[kRing], q_full, q_empty, s_full[2], s_free[2];
+  uint64_t full[2][kMaxRing], empty[kMaxRing], q_full, q_empty, s_full[2], s_free[2];
   uint64_t p_full[kTilePages], p_free[kTilePages], o_ready[2], o_full, o_free, drain;
   uint32_t tmem_base;
   int abort;
   float red[2][4][kRows];  // row maxima by page, double-buffered; then row sums
+  uint32_t qmax[kSoftWarps];  // e4m3: largest |q| by warp
   CtaRange range;
   long long scratch[kThreads / 32 + 1];
 };
-constexpr int kSmemBytes = kOffMisc + int(sizeof(Misc)) + 1024;
-static_assert(kSmemBytes <= 232448, "shared memory budget");
+template <bool F8>
+constexpr int smem_bytes() { return Cfg<F8>::kOffMisc + int(sizeof(Misc)) + 1024; }
+static_assert(smem_bytes<false>() <= 232448 && smem_bytes<true>() <= 232448, "shared memory budget");
 }  // namespace pair
 
 namespace {
@@ -80,6 +93,7 @@ __device__ __forceinline__ int block_tiles(const DecodeParams &p, int v) {
 }
 
 // The pieces of this pair's range, in order.
+template <bool F8>
 struct Pieces {
   const DecodeParams &p;
   const CtaRange &r;
@@ -99,19 +113,28 @@ struct Pieces {
     }
     return false;
   }
-  __device__ void advance() { pv += request_cost(tiles, kPieceTiles); ++v; }
+  __device__ void advance() { pv += request_cost(tiles, Cfg<F8>::kPieceTiles); ++v; }
 };
 
+template <bool F8>
 __device__ __forceinline__ uint32_t total_tiles(const DecodeParams &p, const CtaRange &r) {
   uint32_t n = 0;
-  for (Pieces w(p, r); w.next(); w.advance()) n += uint32_t(w.t1 - w.t0);
+  for (Pieces<F8> w(p, r); w.next(); w.advance()) n += uint32_t(w.t1 - w.t0);
   return n;
 }
 
-// Units in load order: K_0, K_1, V_0, K_2, V_1, ...  First unit of K_n and V_n.
-__device__ __forceinline__ uint32_t k_unit(uint32_t n) { return n == 0 ? 0 : kKUnits + 17 * (n - 1); }
-__device__ __forceinline__ uint32_t v_unit(uint32_t n, uint32_t total) {
-  return kKUnits + 17 * n + (n < total - 1 ? kKUnits : 0);
+// Units in load order: K_0, K_1, V_0, K_2, V_1, ...  A bf16 range runs on like
+// this across its pieces.  An e4m3 piece's first K comes after the last V of the
+// piece before: its scores wait for Q, which the softmax warps split after that
+// piece's epilogue, and K units waiting for it would keep V out of the ring.
+// First unit of K_n and V_n (`first`, `last`: of the range, or of the piece).
+template <bool F8>
+__device__ __forceinline__ uint32_t k_unit(uint32_t n, bool first) {
+  return (Cfg<F8>::kKUnits + Cfg<F8>::kVUnits) * n - (first ? 0 : Cfg<F8>::kVUnits);
+}
+template <bool F8>
+__device__ __forceinline__ uint32_t v_unit(uint32_t n, bool last) {
+  return (Cfg<F8>::kKUnits + Cfg<F8>::kVUnits) * n + (last ? 1 : 2) * Cfg<F8>::kKUnits;
 }
 // A slot has one "landed" barrier for K units and one for V units: the score
 // and PV threads wait at their own pace, and a barrier shared by both kinds
@@ -125,13 +148,15 @@ struct Landed {
     return ph;
   }
 };
-__device__ __forceinline__ int next_slot(int s) { return s + 1 == kRing ? 0 : s + 1; }
+template <bool F8>
+__device__ __forceinline__ int next_slot(int s) { return s + 1 == Cfg<F8>::kRing ? 0 : s + 1; }
 
 // ------------------------------------------------------------------ producer
 
 // One position in the tiles of a range, with the tile's pages.
+template <bool F8>
 struct TileWalk {
-  Pieces w;
+  Pieces<F8> w;
   long long t;
   bool live;
   int page[kTilePages];
@@ -169,9 +194,12 @@ struct TileWalk {
 
 // One thread produces: a warp's votes and shuffles between the units made
 // the producer the slowest role (470 cycles a unit, all 17 of a tile).
+template <bool F8>
 __device__ __forceinline__ void produce(const DecodeParams &p, const CtaRange &r, Misc &m, uint32_t sQ,
                                         uint32_t sRing, uint32_t rank, const CUtensorMap *tm_q,
-                                        const CUtensorMap *tm_k, const CUtensorMap *tm_v, int *err) {
+                                        const CUtensorMap *tm_k, const CUtensorMap *tm_k4, const CUtensorMap *tm_v,
+                                        int *err) {
+  constexpr int kKUnits = Cfg<F8>::kKUnits;
   volatile int *abort = &m.abort;
   const bool leader = rank == 0;
   int at = 0;
@@ -182,54 +210,65 @@ __device__ __forceinline__ void produce(const DecodeParams &p, const CtaRange &r
   const uint32_t q_full = map_to_rank(bar(m.q_full), 0);
   // slot of the next unit (kind 0: K, 1: V), emptied; the even CTA announces
   // both CTAs' bytes
-  auto slot = [&](int kind, uint32_t *full) {
+  auto slot = [&](int kind, uint32_t bytes, uint32_t *full) {
     const int s = at;
     if (!mbar_wait_clk(bar(m.empty[s]), lap, abort, kTimeoutClk)) return -1;
-    if (leader) mbar_arrive_expect_tx(bar(m.full[kind][s]), 2 * kUnitBytes);
-    *full = full0 + 8 * (kind * kRing + s);
-    at = next_slot(s);
+    if (leader) mbar_arrive_expect_tx(bar(m.full[kind][s]), 2 * bytes);
+    *full = full0 + 8 * (kind * kMaxRing + s);
+    at = next_slot<F8>(s);
     if (at == 0) lap ^= 1;
     return s;
   };
-  auto load_k = [&](const TileWalk &c) {
-    if (c.first()) {
+  auto load_k = [&](const TileWalk<F8> &c) {
+    if (!F8 && c.first()) {  // (e4m3: the softmax warps load and split Q)
       if (!mbar_wait_clk(bar(m.q_empty), (q_it & 1) ^ 1, abort, kTimeoutClk)) return false;
       ++q_it;
-      if (leader) mbar_arrive_expect_tx(bar(m.q_full), 2 * kQBytes);
+      if (leader) mbar_arrive_expect_tx(bar(m.q_full), 2 * Cfg<F8>::kQBytes);
       for (int i = 0; i < 9; ++i)
         tma_load_2d_pair(sQ + i * kRows * 128, tm_q, q_full, i * 64, c.w.view.row0 + int(rank) * kRows);
     }
     const int pg0 = rank ? c.page[2] : c.page[0], pg1 = rank ? c.page[3] : c.page[1];  // checked
     for (int kb = 0; kb < kKUnits; ++kb) {
       uint32_t full;
-      const int s = slot(0, &full);
+      const bool rope = F8 && kb == kKUnits - 1;  // e4m3: the last 64 dims, 64 bytes a row
+      const int s = slot(0, rope ? kUnitBytes / 2 : kUnitBytes, &full);
       if (s < 0) return false;
       const uint32_t dst = sRing + s * kUnitBytes;
-      tma_load_4d_pair(dst, tm_k, full, 0, 0, kb, pg0 * 8);
-      tma_load_4d_pair(dst + 8192, tm_k, full, 0, 0, kb, pg1 * 8);
+      if (rope) {
+        tma_load_2d_pair(dst, tm_k4, full, 512, pg0 * kPage);
+        tma_load_2d_pair(dst + 4096, tm_k4, full, 512, pg1 * kPage);
+      } else {
+        tma_load_4d_pair(dst, tm_k, full, 0, 0, kb, pg0 * 8);
+        tma_load_4d_pair(dst + 8192, tm_k, full, 0, 0, kb, pg1 * 8);
+      }
     }
     return true;
   };
   auto load_v = [&](const int (&page)[kTilePages]) {
 #pragma unroll
     for (int i = 0; i < kTilePages; ++i) {
-      for (int h = 0; h < 2; ++h) {
+      for (int h = 0; h < (F8 ? 1 : 2); ++h) {
         uint32_t full;
-        const int s = slot(1, &full);
+        const int s = slot(1, kUnitBytes, &full);
         if (s < 0) return false;
-        tma_load_4d_pair(sRing + s * kUnitBytes, tm_v, full, 0, 0, 4 * int(rank), page[i] * 8 + 4 * h);
+        tma_load_4d_pair(sRing + s * kUnitBytes, tm_v, full, 0, 0, (F8 ? 2 : 4) * int(rank), page[i] * 8 + 4 * h);
       }
     }
     return true;
   };
   // c: the next tile to load K of; its pages are read a tile early, so that
   // their latency hides behind the units of the tile before
-  TileWalk c(p, r);
+  TileWalk<F8> c(p, r);
   int last[kTilePages];  // pages of the tile whose V comes next
   bool have = false;
   while (ok && (c.live || have)) {
     int pages[kTilePages];
     const bool more = c.live;
+    if (F8 && have && more && c.first()) {
+      ok = load_v(last);
+      have = false;
+      if (!ok) break;
+    }
     if (more) {
       c.check(err);
 #pragma unroll
@@ -252,16 +291,19 @@ __device__ __forceinline__ bool warp_wait(uint32_t b, uint32_t parity, volatile 
   return __all_sync(0xffffffffu, mbar_wait_clk(b, parity, abort, kTimeoutClk));
 }
 
+template <bool F8>
 __device__ __forceinline__ void score_mmas(const DecodeParams &p, const CtaRange &r, Misc &m, uint32_t sQ,
                                            uint32_t sRing, uint32_t tmem, int *err) {
   volatile int *abort = &m.abort;
-  const uint32_t idesc = idesc_bf16_f32(128, 256, false, false);
+  constexpr int kKUnits = Cfg<F8>::kKUnits;
+  const uint32_t idesc = F8 ? idesc_e4m3_f32(128, 256, false, false) : idesc_bf16_f32(128, 256, false, false);
   const uint64_t dq = smem_desc_sw128(sQ, 16, 1024), dk = smem_desc_sw128(sRing, 16, 1024);
+  const uint64_t dk4 = smem_desc_sw64(sRing, 16, 512);  // e4m3
   Landed landed;
   uint32_t n = 0;
   uint32_t q_it = 0;
   bool ok = true;
-  for (Pieces w(p, r); ok && w.next(); w.advance()) {
+  for (Pieces<F8> w(p, r); ok && w.next(); w.advance()) {
     for (long long t = w.t0; ok && t < w.t1; ++t, ++n) {
       const int b = int(n & 1);
       ok = warp_wait(bar(m.s_free[b]), ((n >> 1) & 1) ^ 1, abort);
@@ -272,11 +314,23 @@ __device__ __forceinline__ void score_mmas(const DecodeParams &p, const CtaRange
       // orders these MMAs behind the reads of the S buffer; the waits for landed
       // units need no such fence
       tc_fence_after();
-      int s = int(k_unit(n) % kRing);
-      for (int kb = 0; ok && kb < kKUnits; ++kb, s = next_slot(s)) {
+      int s = int(k_unit<F8>(n, t == w.t0 && (F8 || n == 0)) % Cfg<F8>::kRing);
+      for (int kb = 0; ok && kb < kKUnits; ++kb, s = next_slot<F8>(s)) {
         ok = warp_wait(bar(m.full[0][s]), landed.take(s), abort);
         if (!ok) break;
         if (elect_one()) {
+          if constexpr (F8) {
+            // Q's two terms against the block of 128 dims (the last: 64, in
+            // rows of 64 bytes), 32 dims a step
+            const uint64_t dkb = kb == kKUnits - 1 ? dk4 : dk;
+#pragma unroll
+            for (int term = 0; term < 2; ++term)
+#pragma unroll
+              for (int ks = 0; ks < 4; ++ks)
+                if (ks < 2 || kb < kKUnits - 1)
+                  mma_f8_ss_pair(tmem + kColS + 128 * b, dq + ((term * kQTerm + kb * kRows * 128 + ks * 32) >> 4),
+                                 dkb + ((s * kUnitBytes + ks * 32) >> 4), idesc, kb > 0 || term > 0 || ks > 0);
+          } else
 #pragma unroll
           for (int ks = 0; ks < 4; ++ks)
             mma_bf16_ss_pair(tmem + kColS + 128 * b, dq + ((kb * kRows * 128 + ks * 32) >> 4),
@@ -298,30 +352,45 @@ __device__ __forceinline__ void score_mmas(const DecodeParams &p, const CtaRange
   __syncwarp();
 }
 
+template <bool F8>
 __device__ __forceinline__ void pv_mmas(const DecodeParams &p, const CtaRange &r, Misc &m, uint32_t sP,
                                         uint32_t sRing, uint32_t tmem, int *err) {
   volatile int *abort = &m.abort;
-  const uint32_t idesc = idesc_bf16_f32(128, 256, false, true);
-  const uint64_t dp = smem_desc_sw128(sP, 16, 1024);
-  // V, MN-major: 64-dim blocks 1 KB apart, 8-token groups 4 KB apart
-  const uint64_t dv = smem_desc_sw128(sRing, 1024, 4096);
-  const uint32_t total = total_tiles(p, r);
+  const uint32_t idesc = F8 ? idesc_e4m3_f32(128, 256, false, true) : idesc_bf16_f32(128, 256, false, true);
+  const uint32_t idesc_lo = idesc_f8_f32(128, 256, false, true, kFmtE5M2, kFmtE4M3);  // e4m3: P's lo term
+  const uint64_t dp = F8 ? smem_desc_noswz(sP, 128, 512) : smem_desc_sw128(sP, 16, 1024);
+  // V, MN-major: 128-byte blocks of dims 1 KB apart, 8-token groups 4 KB (bf16)
+  // or 2 KB (e4m3) apart
+  const uint64_t dv = smem_desc_sw128(sRing, 1024, F8 ? 2048 : 4096);
+  const uint32_t total = total_tiles<F8>(p, r);
   Landed landed;
   uint32_t n = 0;
   uint32_t o_it = 0;
   bool ok = true;
-  for (Pieces w(p, r); ok && w.next(); w.advance(), ++o_it) {
+  for (Pieces<F8> w(p, r); ok && w.next(); w.advance(), ++o_it) {
     for (long long t = w.t0; ok && t < w.t1; ++t, ++n) {
       ok = warp_wait(bar(m.o_ready[n & 1]), (n >> 1) & 1, abort);
       if (ok && t == w.t0) ok = warp_wait(bar(m.o_free), (o_it & 1) ^ 1, abort);
       tc_fence_after();
-      int s = int(v_unit(n, total) % kRing);
+      int s = int(v_unit<F8>(n, t == w.t1 - 1 && (F8 || n == total - 1)) % Cfg<F8>::kRing);
       for (int pg = 0; ok && pg < kTilePages; ++pg) {
         ok = warp_wait(bar(m.p_full[pg]), n & 1, abort);
-        for (int h = 0; ok && h < 2; ++h, s = next_slot(s)) {  // a page's two units of 32 tokens
+        constexpr int kHalves = F8 ? 1 : 2;  // units of 64 or 32 tokens
+        for (int h = 0; ok && h < kHalves; ++h, s = next_slot<F8>(s)) {
           ok = warp_wait(bar(m.full[1][s]), landed.take(s), abort);
           if (!ok) break;
           if (elect_one()) {
+            if constexpr (F8) {
+#pragma unroll
+              for (int ks = 0; ks < 2; ++ks)
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                  const uint64_t a = dp + ((pg * 2 * kPTerm + ks * 256) >> 4);
+                  const uint64_t v = dv + ((s * kUnitBytes + ks * 8192 + j * 1024) >> 4);
+                  mma_f8_ss_pair(tmem + kColO + 128 * j, a, v, idesc, t > w.t0 || pg > 0 || ks > 0);
+                  mma_f8_ss_pair(tmem + kColO + 128 * j, a + (kPTerm >> 4), v, idesc_lo, 1u);
+                }
+            } else
 #pragma unroll
             for (int ks = 0; ks < 2; ++ks)
 #pragma unroll
@@ -330,7 +399,7 @@ __device__ __forceinline__ void pv_mmas(const DecodeParams &p, const CtaRange &r
                                  dv + ((s * kUnitBytes + ks * 8192 + j * 2048) >> 4), idesc,
                                  t > w.t0 || pg > 0 || h > 0 || ks > 0);
             mma_commit_pair(bar(m.empty[s]));
-            if (h == 1) {
+            if (h == kHalves - 1) {
               mma_commit_pair(bar(m.p_free[pg]));
               if (pg == kTilePages - 1 && t == w.t1 - 1) mma_commit_pair(bar(m.o_full));
             }
@@ -374,8 +443,70 @@ __device__ __forceinline__ void st_global_v8(float *dst, const float (&v)[8]) {
                : "memory");
 }
 
+// e4m3: the block's Q rows of this CTA (bf16) as two e4m3 terms, hi + lo, of
+// 2^k q, with 2^k such that the largest |q| lies in [2^7, 2^8) (hi + lo is then
+// exact down to 2^-9 of it); rows past the block are zero.  All softmax threads,
+// once a piece, when the piece before has read Q.  2^-k goes to *qinv.
+__device__ __forceinline__ bool split_q(const DecodeParams &p, Misc &m, unsigned char *smem, const ViewReq &view,
+                                        uint32_t rank, int st, uint32_t piece, bool ok, float *qinv) {
+  constexpr int kChunks = kDqk / 8, kPer = kRows * kChunks / kSoftThreads;  // 8 dims each; 18 a thread
+  static_assert(kRows * kChunks % kSoftThreads == 0, "Q chunks");
+  const int rows = min(kRows, max(0, view.rows - int(rank) * kRows));
+  const uint4 *src = reinterpret_cast<const uint4 *>(p.q + (size_t(view.row0) + rank * kRows) * kDqk);
+  uint4 v[kPer];
+#pragma unroll
+  for (int u = 0; u < kPer; ++u) {
+    const int i = st + u * kSoftThreads;
+    v[u] = i / kChunks < rows ? __ldg(src + i) : make_uint4(0, 0, 0, 0);
+  }
+  uint32_t mx = 0;
+#pragma unroll
+  for (int u = 0; u < kPer; ++u) {
+    mx = __vmaxu2(mx, v[u].x & 0x7fff7fffu);
+    mx = __vmaxu2(mx, v[u].y & 0x7fff7fffu);
+    mx = __vmaxu2(mx, v[u].z & 0x7fff7fffu);
+    mx = __vmaxu2(mx, v[u].w & 0x7fff7fffu);
+  }
+  mx = __reduce_max_sync(0xffffffffu, max(mx & 0xffffu, mx >> 16));
+  if ((st & 31) == 0) m.qmax[st >> 5] = mx;
+  named_sync(1, kSoftThreads);
+#pragma unroll
+  for (int i = 0; i < kSoftWarps; ++i) mx = max(mx, m.qmax[i]);
+  int k = 0;  // (an Inf or NaN keeps 0)
+  if (mx < 0x7f80u) k = min(126, max(-126, 134 - int(mx >> 7)));
+  const float sc = __int_as_float((127 + k) << 23);
+  *qinv = __int_as_float((127 - k) << 23);
+  ok = ok && __all_sync(0xffffffffu, mbar_wait_clk(bar(m.q_empty), (piece & 1) ^ 1, &m.abort, kTimeoutClk));
+  if (!ok) return false;
+#pragma unroll
+  for (int u = 0; u < kPer; ++u) {
+    const int i = st + u * kSoftThreads, rr = i / kChunks, c = i - kChunks * rr;
+    const uint32_t wv[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
+    uint32_t hw[2] = {0, 0}, lw[2] = {0, 0};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float f0 = __uint_as_float(wv[e] << 16) * sc, f1 = __uint_as_float(wv[e] & 0xffff0000u) * sc;
+      const uint16_t h = float2_to_e4m3x2(f0, f1);
+      const float2 bh = e4m3x2_to_float2(h);
+      const uint16_t l = float2_to_e4m3x2(f0 - bh.x, f1 - bh.y);
+      hw[e >> 1] |= uint32_t(h) << (16 * (e & 1));
+      lw[e >> 1] |= uint32_t(l) << (16 * (e & 1));
+    }
+    // dims 8c .. 8c + 7: block c / 16, 16-byte chunk (c % 16) / 2 at its swizzled place
+    const int b = c & 15;
+    const int off = (c >> 4) * kRows * 128 + (rr >> 3) * 1024 + (rr & 7) * 128 + (((b >> 1) ^ (rr & 7)) << 4) +
+                    8 * (b & 1);
+    *reinterpret_cast<uint2 *>(smem + kOffQ + off) = make_uint2(hw[0], hw[1]);
+    *reinterpret_cast<uint2 *>(smem + kOffQ + kQTerm + off) = make_uint2(lw[0], lw[1]);
+  }
+  fence_proxy_async_smem();
+  __syncwarp();
+  return true;
+}
+
 // A failed wait never leaves the loop: the warp goes on without working, so
 // that the others find it at their barriers (later waits fail at once).
+template <bool F8>
 __device__ __forceinline__ void softmax(const DecodeParams &p, const CtaRange &r, Misc &m, unsigned char *smem,
                                         uint32_t tmem, uint32_t rank, int pair_id, int *err) {
   volatile int *abort = &m.abort;
@@ -384,8 +515,10 @@ __device__ __forceinline__ void softmax(const DecodeParams &p, const CtaRange &r
   const int row = 32 * (q & 1) + lane, pb = 2 * (q >> 1) + g;
   const uint32_t lanes = uint32_t(32 * q) << 16;
   const uint32_t t_s = tmem + lanes + kColS + 64 * g, t_o = tmem + lanes + kColO + 128 * g;
-  const float cs = p.score_scale_log2;
-  unsigned char *prow = smem + kOffP + pb * kRows * 128 + row * 128;
+  float cs = p.score_scale_log2;
+  unsigned char *prow = smem + Cfg<F8>::kOffP + pb * kRows * 128 +
+                        (F8 ? (row >> 3) * 512 + (row & 7) * 16 : row * 128);
+  const uint32_t q_full = map_to_rank(bar(m.q_full), 0);
   const uint32_t s_free0 = map_to_rank(bar(m.s_free[0]), 0);
   const uint32_t s_free1 = map_to_rank(bar(m.s_free[1]), 0);
   const uint32_t p_full = map_to_rank(bar(m.p_full[pb]), 0);
@@ -393,10 +526,16 @@ __device__ __forceinline__ void softmax(const DecodeParams &p, const CtaRange &r
   uint32_t n = 0;
   uint32_t o_it = 0;
   bool ok = true;
-  for (Pieces w(p, r); w.next(); w.advance(), ++o_it) {
+  for (Pieces<F8> w(p, r); w.next(); w.advance(), ++o_it) {
     const int grow = w.view.row0 + int(rank) * kRows + row;
     const int hi = row_view(p, w.view, min(grow, p.batch * p.heads - 1)).hi;
     const bool mine = int(rank) * kRows + row < w.view.rows;
+    if constexpr (F8) {
+      float qinv;
+      ok = split_q(p, m, smem, w.view, rank, st, o_it, ok, &qinv);
+      if (ok && lane == 0) mbar_arrive_cluster(q_full);
+      cs = p.score_scale_log2 * p.kv_scale * qinv;
+    }
     float mrun = -INFINITY, ell = 0.f, ellx = 0.f;
     for (long long t = w.t0; t < w.t1; ++t, ++n) {
       const int b = int(n & 1);
@@ -444,17 +583,29 @@ __device__ __forceinline__ void softmax(const DecodeParams &p, const CtaRange &r
       }
       // a row that has seen no token yet keeps a -inf maximum: its weights are 0
       const float mref = mrun == -INFINITY ? 0.f : mrun;
+      // bf16: the weights in pairs; e4m3: hi terms (e4m3), then lo terms (e5m2)
       uint32_t pk[32];
       float lsum[2] = {0.f, 0.f}, xsum[2] = {0.f, 0.f};
 #pragma unroll
       for (int i = 0; i < 32; ++i) {
         const float e0 = exp2_approx(fmaf(x[2 * i], cs, -mref)), e1 = exp2_approx(fmaf(x[2 * i + 1], cs, -mref));
-        __nv_bfloat162 v = __floats2bfloat162_rn(e0, e1);
-        pk[i] = *reinterpret_cast<uint32_t *>(&v);
         xsum[0] += e0;
         xsum[1] += e1;
-        lsum[0] += __uint_as_float(pk[i] << 16);
-        lsum[1] += __uint_as_float(pk[i] & 0xffff0000u);
+        if constexpr (F8) {
+          const uint16_t hi = float2_to_e4m3x2(e0, e1);
+          const float2 bh = e4m3x2_to_float2(hi);
+          const uint16_t lo = float2_to_e5m2x2(e0 - bh.x, e1 - bh.y);
+          const float2 bl = e5m2x2_to_float2(lo);
+          lsum[0] += bh.x + bl.x;
+          lsum[1] += bh.y + bl.y;
+          pk[i >> 1] = i & 1 ? pk[i >> 1] | uint32_t(hi) << 16 : hi;
+          pk[16 + (i >> 1)] = i & 1 ? pk[16 + (i >> 1)] | uint32_t(lo) << 16 : lo;
+        } else {
+          __nv_bfloat162 v = __floats2bfloat162_rn(e0, e1);
+          pk[i] = *reinterpret_cast<uint32_t *>(&v);
+          lsum[0] += __uint_as_float(pk[i] << 16);
+          lsum[1] += __uint_as_float(pk[i] & 0xffff0000u);
+        }
       }
       ell = ell * alpha + (lsum[0] + lsum[1]);
       ellx = ellx * alpha + (xsum[0] + xsum[1]);
@@ -478,7 +629,7 @@ __device__ __forceinline__ void softmax(const DecodeParams &p, const CtaRange &r
       if (ok) {
 #pragma unroll
         for (int c = 0; c < 8; ++c)
-          *reinterpret_cast<uint4 *>(prow + ((c ^ (row & 7)) << 4)) =
+          *reinterpret_cast<uint4 *>(prow + (F8 ? (c >> 2) * kPTerm + (c & 3) * 128 : (c ^ (row & 7)) << 4)) =
               make_uint4(pk[4 * c], pk[4 * c + 1], pk[4 * c + 2], pk[4 * c + 3]);
         fence_proxy_async_smem();
         __syncwarp();
@@ -493,7 +644,7 @@ __device__ __forceinline__ void softmax(const DecodeParams &p, const CtaRange &r
     const float sum = (m.red[0][0][row] + m.red[0][1][row]) + (m.red[0][2][row] + m.red[0][3][row]);
     const float sumx = (m.red[1][0][row] + m.red[1][1][row]) + (m.red[1][2][row] + m.red[1][3][row]);
     named_sync(1, kSoftThreads);  // read before the next piece writes maxima
-    const float inv = sum > 0.f ? 1.f / sum : 0.f;
+    const float inv = sum > 0.f ? p.kv_scale / sum : 0.f;
     ok = ok && __all_sync(0xffffffffu, mbar_wait_clk(bar(m.o_full), o_it & 1, abort, kTimeoutClk));
     const int c_first = sched_owner(w.pv, r.total, r.g_eff);
     if (ok) {
@@ -528,21 +679,24 @@ __device__ __forceinline__ void softmax(const DecodeParams &p, const CtaRange &r
   if (!ok) atomicOr(err, kErrTimeout);
 }
 
+template <bool F8>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     decode_pair_kernel(const __grid_constant__ DecodeParams p, const __grid_constant__ CUtensorMap tm_q,
-                       const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v) {
+                       const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_k4,
+                       const __grid_constant__ CUtensorMap tm_v) {
+  constexpr int kOffP = Cfg<F8>::kOffP, kOffRing = Cfg<F8>::kOffRing;
   extern __shared__ unsigned char smem_raw[];
   const uint32_t raw = smem_u32(smem_raw), pad = ((raw + 1023u) & ~1023u) - raw;
   unsigned char *smem = smem_raw + pad;
   const uint32_t sbase = raw + pad;
-  Misc &m = *reinterpret_cast<Misc *>(smem + kOffMisc);
+  Misc &m = *reinterpret_cast<Misc *>(smem + Cfg<F8>::kOffMisc);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t rank = cluster_rank();
   const int pair_id = int(blockIdx.x) >> 1;
   int *err = error_word(p);
 
   if (tid == 0) {
-    for (int s = 0; s < kRing; ++s) {
+    for (int s = 0; s < Cfg<F8>::kRing; ++s) {
       mbar_init(bar(m.full[0][s]), 1);
       mbar_init(bar(m.full[1][s]), 1);
       mbar_init(bar(m.empty[s]), 1);
@@ -552,7 +706,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       mbar_init(bar(m.s_free[b]), 2 * kSoftWarps);
       mbar_init(bar(m.o_ready[b]), 2 * kSoftWarps);
     }
-    mbar_init(bar(m.q_full), 1);
+    mbar_init(bar(m.q_full), F8 ? 2 * kSoftWarps : 1);
     mbar_init(bar(m.q_empty), 1);
     for (int i = 0; i < kTilePages; ++i) {
       mbar_init(bar(m.p_full[i]), 4);  // a page's two warps in each CTA
@@ -574,7 +728,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     tmem_relinquish_pair();
   }
   if (warp == 0 && lane == 0) {
-    tma_prefetch_desc(&tm_q);
+    tma_prefetch_desc(F8 ? &tm_k4 : &tm_q);
     tma_prefetch_desc(&tm_k);
     tma_prefetch_desc(&tm_v);
   }
@@ -582,7 +736,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   // blocks without pages have no partials
   for (int v = int(blockIdx.x) * kThreads + tid; v < p.pair_blocks; v += int(gridDim.x) * kThreads)
     if (block_tiles(p, v) == 0) info_ptr(p)[p.batch * p.head_groups + v] = make_int4(-1, 0, 0, 0);
-  schedule_range<kPieceTiles, true>(p.pair_blocks, pair_id, p.pairs, [&](int v) { return block_tiles(p, v); },
+  schedule_range<Cfg<F8>::kPieceTiles, true>(p.pair_blocks, pair_id, p.pairs, [&](int v) { return block_tiles(p, v); },
                                     &m.range, m.scratch);
   tc_fence_before();
   cluster_sync();  // both CTAs' barriers and TMEM are ready
@@ -592,13 +746,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 
   if (r.start < r.end) {
     if (warp == 0) {
-      if (lane == 0) produce(p, r, m, sbase + kOffQ, sbase + kOffRing, rank, &tm_q, &tm_k, &tm_v, err);
+      if (lane == 0) produce<F8>(p, r, m, sbase + kOffQ, sbase + kOffRing, rank, &tm_q, &tm_k, &tm_k4, &tm_v, err);
     } else if (warp == 1) {
-      if (rank == 0) score_mmas(p, r, m, sbase + kOffQ, sbase + kOffRing, tmem, err);
+      if (rank == 0) score_mmas<F8>(p, r, m, sbase + kOffQ, sbase + kOffRing, tmem, err);
     } else if (warp == 2) {
-      if (rank == 0) pv_mmas(p, r, m, sbase + kOffP, sbase + kOffRing, tmem, err);
+      if (rank == 0) pv_mmas<F8>(p, r, m, sbase + kOffP, sbase + kOffRing, tmem, err);
     } else if (warp >= 4) {
-      softmax(p, r, m, smem, tmem, rank, pair_id, err);
+      softmax<F8>(p, r, m, smem, tmem, rank, pair_id, err);
     }
     // no MMA may still read this CTA's shared memory, and no copy write it:
     // the MMAs waited for every copy unless a wait gave up
@@ -623,24 +777,32 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   cluster_sync();  // the pair leaves together: neither SM takes another CTA before both gave up their TMEM
 }
 
-}  // namespace
-
-cudaError_t launch_decode_pair(const DecodeParams &p, const CUtensorMap &tm_q, const CUtensorMap &tm_k,
-                               const CUtensorMap &tm_v, cudaStream_t stream) {
+template <bool F8>
+cudaError_t launch(const DecodeParams &p, const CUtensorMap &tm_q, const CUtensorMap &tm_k,
+                   const CUtensorMap &tm_k4, const CUtensorMap &tm_v, cudaStream_t stream) {
   static SmemLimitOnce smem_limit;
-  const cudaError_t e = smem_limit.ensure(decode_pair_kernel, pair::kSmemBytes);
+  const cudaError_t e = smem_limit.ensure(decode_pair_kernel<F8>, smem_bytes<F8>());
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(2 * p.pairs);
-  cfg.blockDim = dim3(pair::kThreads);
-  cfg.dynamicSmemBytes = pair::kSmemBytes;
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem_bytes<F8>();
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, decode_pair_kernel, p, tm_q, tm_k, tm_v);
+  return cudaLaunchKernelEx(&cfg, decode_pair_kernel<F8>, p, tm_q, tm_k, tm_k4, tm_v);
+}
+
+}  // namespace
+
+// tm_q is read for a bf16 cache, tm_k4 for an e4m3 one.
+cudaError_t launch_decode_pair(const DecodeParams &p, const CUtensorMap &tm_q, const CUtensorMap &tm_k,
+                               const CUtensorMap &tm_k4, const CUtensorMap &tm_v, cudaStream_t stream) {
+  return p.kv_e4m3 ? launch<true>(p, tm_q, tm_k, tm_k4, tm_v, stream)
+                   : launch<false>(p, tm_q, tm_k, tm_k4, tm_v, stream);
 }
 
 }  // namespace mla
