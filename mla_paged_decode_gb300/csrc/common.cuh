@@ -427,6 +427,17 @@ __device__ __forceinline__ int sched_owner(long long x, long long C, int g_eff) 
   return int(((x + 1) * g_eff - 1) / C);
 }
 
+// The same two with a 32-bit division where the product allows it (a 64-bit one
+// costs hundreds of cycles; views and the pair kernel start and end pieces often).
+__device__ __forceinline__ long long sched_start_short(long long c, long long C, int g_eff) {
+  const long long x = c * C;
+  return x >> 32 ? x / g_eff : (long long)(uint32_t(x) / uint32_t(g_eff));
+}
+__device__ __forceinline__ int sched_owner_short(long long x, long long C, int g_eff) {
+  const long long y = (x + 1) * g_eff - 1;
+  return y >> 32 || C >> 32 ? int(y / C) : int(uint32_t(y) / uint32_t(C));
+}
+
 __device__ __forceinline__ long long request_cost(int tiles, int piece_cost) {
   return tiles > 0 ? tiles + piece_cost : 0;
 }
@@ -458,13 +469,13 @@ __device__ __forceinline__ void schedule_range(int V, int idx, int workers, Tile
       }
       const int g_eff = int(C < (long long)workers ? C : (long long)workers);
       const bool has = g_eff > 0 && idx < g_eff;
-      const long long start = has ? sched_start(idx, C, g_eff) : 0;
+      const long long start = has ? sched_start_short(idx, C, g_eff) : 0;
       const long long excl = before + incl - cst;
       if (tid == 0) {
         r->total = C;
         r->g_eff = g_eff;
         r->start = start;
-        r->end = has ? sched_start(idx + 1, C, g_eff) : 0;
+        r->end = has ? sched_start_short(idx + 1, C, g_eff) : 0;
       }
       if (has && tiles > 0 && excl + tiles > start && excl - PC <= start) {
         r->v_begin = tid;

@@ -646,7 +646,7 @@ __device__ __forceinline__ void softmax(const DecodeParams &p, const CtaRange &r
     named_sync(1, kSoftThreads);  // read before the next piece writes maxima
     const float inv = sum > 0.f ? p.kv_scale / sum : 0.f;
     ok = ok && __all_sync(0xffffffffu, mbar_wait_clk(bar(m.o_full), o_it & 1, abort, kTimeoutClk));
-    const int c_first = sched_owner(w.pv, r.total, r.g_eff);
+    const int c_first = sched_owner_short(w.pv, r.total, r.g_eff);
     if (ok) {
       tc_fence_after();
       const size_t slot = 2 * size_t(pair_id + w.v) + rank;
@@ -671,7 +671,7 @@ __device__ __forceinline__ void softmax(const DecodeParams &p, const CtaRange &r
       if (lane == 0) mbar_arrive_cluster(o_free);
       if (mine && pb == 0) slot_lse_ptr(p)[slot * kSlotHeads + row] = mrun + log2f(sumx);
       if (st == 0 && rank == 0 && pair_id == c_first) {
-        const int c_last = sched_owner(w.pv + w.tiles - 1, r.total, r.g_eff);
+        const int c_last = sched_owner_short(w.pv + w.tiles - 1, r.total, r.g_eff);
         info_ptr(p)[p.batch * p.head_groups + w.v] = make_int4(c_first, c_last - c_first + 1, pair_id + w.v, 0);
       }
     }

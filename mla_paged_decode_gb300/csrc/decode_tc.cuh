@@ -348,8 +348,13 @@ __device__ __forceinline__ void tc_producer(const TcParams &tp, const CtaRange &
   // 129 MB L2 gives the two shared-memory stages more HBM requests in
   // flight), and carried in `ring` until its tile is loaded.
   TileCursor<FUSED, MULTI, piece_cost<F8>()> ahead(p, r, &m.view0);
+  // (views step before a look-up, not after it: the next piece's view is not
+  // needed before the first tile's copies are out)
+  bool started = false;
   auto next_ahead = [&]() {
     int pg = -1;
+    if (MULTI == 3 && started && ahead.live) ahead.step();
+    started = true;
     if (ahead.live) {
       int lp, row0;
       if (cursor_page(p, ahead, lane, &lp, &row0)) {
@@ -372,7 +377,7 @@ __device__ __forceinline__ void tc_producer(const TcParams &tp, const CtaRange &
           }
         }
       }
-      ahead.step();
+      if (MULTI != 3) ahead.step();
     }
     return pg;
   };
@@ -384,7 +389,7 @@ __device__ __forceinline__ void tc_producer(const TcParams &tp, const CtaRange &
   TileCursor<FUSED, MULTI, piece_cost<F8>()> cur(p, r, &m.view0);
   while (cur.live) {
     if (!F8 && cur.first()) {  // (e4m3: warps 9..11 load and split Q)
-      checked_len(p, cur.w.rb, err);
+      if (MULTI != 3) checked_len(p, cur.w.rb, err);  // (views: see write_empty_views)
       if (!__all_sync(0xffffffffu, mbar_wait(bar_addr(m.q_empty), (q_it & 1) ^ 1, abort, kTimeoutNs))) {
         ok = false;
         break;
@@ -396,7 +401,7 @@ __device__ __forceinline__ void tc_producer(const TcParams &tp, const CtaRange &
       last_q = q_it & 1;
       ++q_it;
     }
-    if (F8 && cur.first()) checked_len(p, cur.w.rb, err);
+    if (F8 && MULTI != 3 && cur.first()) checked_len(p, cur.w.rb, err);
     const int s = kv_it % NS;
     int lp, row0;
     const bool mine = cursor_page(p, cur, lane, &lp, &row0);
@@ -825,12 +830,16 @@ __device__ __forceinline__ void view_epilogue(uint32_t tq, const float *scale, u
 #pragma unroll
     for (int i = 0; i < 16; ++i) sc[i] = scale[hb + i];
 #pragma unroll 1
-    for (int c = 0; c < 4; ++c) {
-      uint32_t o[16];
-      tmem_ld16(tq + kColO + 64 * c + hb, o);
-      tmem_wait_ld();
+    for (int c2 = 0; c2 < 4; c2 += 2) {
+     uint32_t o[2][16];
+     tmem_ld16(tq + kColO + 64 * c2 + hb, o[0]);
+     tmem_ld16(tq + kColO + 64 * c2 + 64 + hb, o[1]);
+     tmem_wait_ld();
 #pragma unroll
-      for (int i = 0; i < 16; ++i) buf[i * 32 + lane] = __uint_as_float(o[i]) * sc[i];
+     for (int cc = 0; cc < 2; ++cc) {
+      const int c = c2 + cc;
+#pragma unroll
+      for (int i = 0; i < 16; ++i) buf[i * 32 + lane] = __uint_as_float(o[cc][i]) * sc[i];
       __syncwarp();
 #pragma unroll
       for (int j = 0; j < 4; ++j) {  // 16 rows x 8 runs of 4 dims
@@ -848,6 +857,7 @@ __device__ __forceinline__ void view_epilogue(uint32_t tq, const float *scale, u
         }
       }
       __syncwarp();
+     }
     }
   }
 }
@@ -1137,7 +1147,7 @@ __device__ __forceinline__ void tc_softmax(const TcParams &tp, const CtaRange &r
     const bool got_o = mbar_wait(bar_addr(m.o_full), o_it & 1, abort, kTimeoutNs);
     if (!named_sync_and(2, 128, got_o)) { ok = false; break; }
     tc_fence_after();
-    SplitInfo si = split_info(r, w.v, w.pv, w.tiles);
+    SplitInfo si = split_info<VIEW>(r, w.v, w.pv, w.tiles);
     bool split = si.nsplits > 1;
     size_t out_row0;
     if constexpr (VIEW) {

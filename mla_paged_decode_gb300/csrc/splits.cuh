@@ -12,11 +12,13 @@ struct SplitInfo {
   int slot;      // this CTA's slot for the request
 };
 
+template <bool SHORT = false>
 __device__ __forceinline__ SplitInfo split_info(const CtaRange &r, int v, long long pv,
                                                 int tiles) {
   SplitInfo s;
-  s.c_first = sched_owner(pv, r.total, r.g_eff);
-  int c_last = sched_owner(pv + tiles - 1, r.total, r.g_eff);
+  s.c_first = SHORT ? sched_owner_short(pv, r.total, r.g_eff) : sched_owner(pv, r.total, r.g_eff);
+  int c_last = SHORT ? sched_owner_short(pv + tiles - 1, r.total, r.g_eff)
+                     : sched_owner(pv + tiles - 1, r.total, r.g_eff);
   s.nsplits = c_last - s.c_first + 1;
   s.slot = 2 * int(blockIdx.x) + (v != r.v_begin ? 1 : 0);
   return s;
