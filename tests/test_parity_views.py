@@ -90,7 +90,54 @@ def test_shared_long_prefix(kv_dtype, width, n, heads, pages, q_len):
     check(c, *run_shared(c, [0, n], [pages]), what="long prefix")
 
 
-@pytest.mark.parametrize("kv_dtype,width", [("bf16", 0), ("bf16", WIDE), ("e4m3", WIDE)])
+@pytest.mark.parametrize("kv_dtype,width", [("bf16", 0), ("bf16", WIDE), ("e4m3", 0), ("e4m3", WIDE)])
+def test_shared_with_more_requests_than_threads(kv_dtype, width):
+    """Hundreds of requests and groups, empty groups among them: the schedule
+    walks them in chunks; the last group is large."""
+    starts, pages = [0], []
+    for k in range(90):
+        starts.append(starts[-1] + k % 4)
+        pages.append(k % 3)
+    starts.append(starts[-1] + 330)
+    pages.append(5)
+    lens = [64 * pages[k] + (13 * b) % 150 for k in range(len(pages)) for b in range(starts[k], starts[k + 1])]
+    c = make(lens, 40, 1, kv_dtype, causal_seen(1), seed=21, shared=(starts, pages), width=width)
+    check(c, *run_shared(c, starts, pages), what="many requests")
+
+
+@pytest.mark.parametrize("kv_dtype", ["bf16", "e4m3"])
+def test_window_with_more_requests_than_threads(kv_dtype):
+    lens = [(37 * b) % 300 for b in range(410)]
+    c = make(lens, 20, 1, kv_dtype, window_seen(90, 5, 1), seed=22)
+    check(c, *run_window(c, 90, 5), what="many requests")
+
+
+@pytest.mark.parametrize("kv_dtype", ["bf16", "e4m3"])
+@pytest.mark.parametrize("gain", [0.0, 40.0])
+def test_flat_and_steep_scores(kv_dtype, gain):
+    """All scores zero; one token taking nearly all the weight."""
+    c = make([1000, 65, 300], 16, 1, kv_dtype, window_seen(500, 3, 1), seed=23, q_gain=gain)
+    check(c, *run_window(c, 500, 3), what="window")
+    c = make([1000, 1001, 1090], 64, 1, kv_dtype, causal_seen(1), seed=24, shared=([0, 3], [15]), q_gain=gain,
+             width=WIDE)
+    check(c, *run_shared(c, [0, 3], [15]), what="shared")
+
+
+@pytest.mark.parametrize("width", [0, WIDE])
+def test_a_query_that_is_not_finite_stays_in_its_row(width):
+    c = make([700, 640, 655], 64, 1, "bf16", causal_seen(1), seed=25, shared=([0, 3], [9]), width=width)
+    good, glse = run_shared(c, [0, 3], [9])
+    c.q[1, 0, 7, 3] = math.nan
+    c.q[2, 0, 60, 570] = math.inf
+    out, lse = run_shared(c, [0, 3], [9])
+    rest = torch.ones(3, 1, 64, dtype=torch.bool)
+    rest[1, 0, 7] = rest[2, 0, 60] = False
+    assert torch.isfinite(out[rest]).all()
+    assert (out[rest].float() - good[rest].float()).abs().max() <= 2.0**-7 * good.float().abs().max()
+    assert not torch.isfinite(out[1, 0, 7].float()).all()
+
+
+@pytest.mark.parametrize("kv_dtype,width", [("bf16", 0), ("bf16", WIDE), ("e4m3", 0), ("e4m3", WIDE)])
 def test_shared_scores_of_a_wide_range(kv_dtype, width):
     """Running maxima that grow across tiles and rows whose weights sit on few tokens."""
     lens = [64 * 30 + 17] * 6
