@@ -816,7 +816,7 @@ static __device__ __noinline__ void zero_value_rows(unsigned char *stage, int r0
 // A view's epilogue: 16 rows at a time, a warp's 32 value dims of a chunk
 // (dims d0 + 128 c) go through its 2 KB buffer and leave as 16-byte runs, fp32
 // to the partial `part` or bf16 to `out`.  Only the block's own rows are read
-// and stored: 16 rows take 2,800 cycles, 64 rows 8,100 (the other variants'
+// and stored: 16 rows take 2,800 cycles, 64 rows 7,700 (the other variants'
 // epilogue: 6,300 and 8,100).  Asking L2 to keep the partials, as that one
 // does, cost 1 to 4 % of these calls.
 __device__ __forceinline__ void view_epilogue(uint32_t tq, const float *scale, unsigned char *stg, float *part,
@@ -830,34 +830,33 @@ __device__ __forceinline__ void view_epilogue(uint32_t tq, const float *scale, u
 #pragma unroll
     for (int i = 0; i < 16; ++i) sc[i] = scale[hb + i];
 #pragma unroll 1
-    for (int c2 = 0; c2 < 4; c2 += 2) {
-     uint32_t o[2][16];
-     tmem_ld16(tq + kColO + 64 * c2 + hb, o[0]);
-     tmem_ld16(tq + kColO + 64 * c2 + 64 + hb, o[1]);
-     tmem_wait_ld();
+    for (int c2 = 0; c2 < 4; c2 += 2) {  // two chunks' accumulators travel together
+      uint32_t o[2][16];
+      tmem_ld16(tq + kColO + 64 * c2 + hb, o[0]);
+      tmem_ld16(tq + kColO + 64 * c2 + 64 + hb, o[1]);
+      tmem_wait_ld();
 #pragma unroll
-     for (int cc = 0; cc < 2; ++cc) {
-      const int c = c2 + cc;
+      for (int cc = 0; cc < 2; ++cc) {
 #pragma unroll
-      for (int i = 0; i < 16; ++i) buf[i * 32 + lane] = __uint_as_float(o[cc][i]) * sc[i];
-      __syncwarp();
+        for (int i = 0; i < 16; ++i) buf[i * 32 + lane] = __uint_as_float(o[cc][i]) * sc[i];
+        __syncwarp();
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {  // 16 rows x 8 runs of 4 dims
-        const int h = hb + (lane >> 3) + 4 * j;
-        const float4 v = reinterpret_cast<const float4 *>(buf)[lane + 32 * j];
-        const size_t at = size_t(h) * kDv + d0 + 128 * c + 4 * (lane & 7);
-        if (h < rows) {
-          if (part) {
-            *reinterpret_cast<float4 *>(part + at) = v;
-          } else {
-            __nv_bfloat162 lo = __floats2bfloat162_rn(v.x, v.y), hi = __floats2bfloat162_rn(v.z, v.w);
-            *reinterpret_cast<uint2 *>(out + at) =
-                make_uint2(*reinterpret_cast<uint32_t *>(&lo), *reinterpret_cast<uint32_t *>(&hi));
+        for (int j = 0; j < 4; ++j) {  // 16 rows x 8 runs of 4 dims
+          const int h = hb + (lane >> 3) + 4 * j;
+          const float4 v = reinterpret_cast<const float4 *>(buf)[lane + 32 * j];
+          const size_t at = size_t(h) * kDv + d0 + 128 * (c2 + cc) + 4 * (lane & 7);
+          if (h < rows) {
+            if (part) {
+              *reinterpret_cast<float4 *>(part + at) = v;
+            } else {
+              __nv_bfloat162 lo = __floats2bfloat162_rn(v.x, v.y), hi = __floats2bfloat162_rn(v.z, v.w);
+              *reinterpret_cast<uint2 *>(out + at) =
+                  make_uint2(*reinterpret_cast<uint32_t *>(&lo), *reinterpret_cast<uint32_t *>(&hi));
+            }
           }
         }
+        __syncwarp();
       }
-      __syncwarp();
-     }
     }
   }
 }

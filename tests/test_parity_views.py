@@ -212,3 +212,24 @@ def test_bad_inputs_are_reported(what):
         ws = mla.make_workspace(c.q, c.kv, c.table)
         mla.decode_window(c.q, c.kv, c.table, c.lens, 10**6, 0, 0.1, 0, out, lse, workspace=ws)
         assert mla.check_workspace(ws) == -9
+
+
+def test_a_pool_past_4_gib():
+    """Page numbers whose byte offsets pass 32 bits."""
+    pages = 62000                                  # 4.6 GB of bf16 rows
+    small = make([500, 640], 64, 1, "bf16", causal_seen(1), seed=31, shared=([0, 2], [7]))
+    n = small.kv.shape[0]
+    kv = torch.zeros(pages, 64, 576, dtype=torch.bfloat16, device="cuda")
+    at = torch.arange(n, dtype=torch.int32, device="cuda") + (pages - n)
+    mla.pages_copy(small.kv, kv, torch.arange(n, dtype=torch.int32, device="cuda"), at)
+    small.kv = kv
+    small.table = torch.where(small.table >= 0, small.table + (pages - n), small.table)
+    check(small, *run_shared(small, [0, 2], [7]), what="shared")
+    full = small.seen
+    check(small, *run_window(small, 10**6, 0), what="window")
+    pad = torch.full((2, WIDE), -1, dtype=torch.int32, device="cuda")
+    pad[:, :small.table.shape[1]] = small.table
+    small.table = pad
+    small.q = small.q.repeat(1, 2, 1, 1).contiguous()       # two query tokens: 128 rows a request
+    small.seen = [[s[0][:-1], s[0]] for s in full]
+    check(small, *run_shared(small, [0, 2], [7]), what="shared, pairs")
