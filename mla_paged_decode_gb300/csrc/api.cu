@@ -13,6 +13,7 @@
 
 #include "common.cuh"
 #include "pages.cuh"
+#include "pair_maps.cuh"
 
 namespace mla {
 cudaError_t launch_decode_simt(const DecodeParams &p, int grid, cudaStream_t stream);
@@ -30,8 +31,8 @@ cudaError_t launch_decode_tc(const DecodeParams &p, int npv, int q_rows, int gro
                              const CUtensorMap &tm_q, const CUtensorMap &tm_kv,
                              const CUtensorMap &tm_kvg, const CUtensorMap &tm_kvb, int grid,
                              cudaStream_t stream);
-cudaError_t launch_decode_pair(const DecodeParams &p, const CUtensorMap &tm_q, const CUtensorMap &tm_k,
-                               const CUtensorMap &tm_k4, const CUtensorMap &tm_v, cudaStream_t stream);
+cudaError_t launch_decode_pair(const DecodeParams &p, const CUtensorMap &tm_q, const PairMaps &m,
+                               cudaStream_t stream);
 cudaError_t launch_lse_combine(const void *partials, const float *lses, int num_parts, void *out,
                                float *out_lse, int rows, int dim, int base2, cudaStream_t stream);
 int combine_max_parts();
@@ -314,8 +315,7 @@ int make_tensor_maps(const void *q, const void *kv, const mla_decode_desc *d, in
 // groups): one dim block of a page's 64 rows (K); the value dims of one CTA,
 // four blocks of half a bf16 page or two of an e4m3 page (V).  The last 64 dims
 // of an e4m3 page's rows come through tm_k4, 64 bytes a row.
-int make_pair_maps(const void *kv, const mla_decode_desc *d, CUtensorMap *tm_k, CUtensorMap *tm_k4,
-                   CUtensorMap *tm_v) {
+int make_pair_maps(const void *kv, const mla_decode_desc *d, mla::PairMaps *m) {
   EncodeTiled enc = encode_tiled();
   if (!enc) {
     std::snprintf(g_cuda_error, sizeof(g_cuda_error), "cuTensorMapEncodeTiled unavailable");
@@ -328,19 +328,24 @@ int make_pair_maps(const void *kv, const mla_decode_desc *d, CUtensorMap *tm_k, 
   cuuint64_t dims[4] = {x, 8, cuuint64_t(f8 ? 4 : 9), cuuint64_t(d->num_pages) * 8};
   cuuint64_t strides[3] = {row, 128, 8 * row};
   cuuint32_t box_k[4] = {x, 8, 1, 8}, box_v[4] = {x, 8, f8 ? 2u : 4u, f8 ? 8u : 4u}, es[4] = {1, 1, 1, 1};
-  CUresult r = enc(tm_k, type, 4, const_cast<void *>(kv), dims, strides, box_k, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                   CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  if (r != CUDA_SUCCESS) return tensor_map_fail("kv pair K", r);
-  r = enc(tm_v, type, 4, const_cast<void *>(kv), dims, strides, box_v, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
-          CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  if (r != CUDA_SUCCESS) return tensor_map_fail("kv pair V", r);
-  *tm_k4 = *tm_k;
+  cuuint32_t box_va[4] = {x, 8, f8 ? 2u : 4u, 1}, box_vr[4] = {x, 1, 1, 1};
+  CUresult r = CUDA_SUCCESS;
+  auto map = [&](CUtensorMap *tm, cuuint32_t *box) {
+    if (r == CUDA_SUCCESS)
+      r = enc(tm, type, 4, const_cast<void *>(kv), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  };
+  map(&m->k, box_k);
+  map(&m->v, box_v);
+  map(&m->va, box_va);
+  map(&m->vr, box_vr);
+  if (r != CUDA_SUCCESS) return tensor_map_fail("kv pair", r);
+  m->k4 = m->k;
   if (f8) {
     cuuint64_t dims4[2] = {row, cuuint64_t(d->num_pages) * mla::kPage};
     cuuint64_t strides4[1] = {row};
     cuuint32_t box4[2] = {64, mla::kPage};
-    r = enc(tm_k4, type, 2, const_cast<void *>(kv), dims4, strides4, box4, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+    r = enc(&m->k4, type, 2, const_cast<void *>(kv), dims4, strides4, box4, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
             CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     if (r != CUDA_SUCCESS) return tensor_map_fail("kv pair rope", r);
   }
@@ -507,11 +512,12 @@ int enqueue_view(mla::DecodeParams p, const void *q, const void *kv_pages, const
   int st = make_tensor_maps(q, kv_pages, d, h, 0, 1, false, false, &tm_q, &tm_kv, &tm_kvg, &tm_kvb);
   if (st != MLA_OK) return st;
   if (p.pair_blocks) {
-    CUtensorMap tm_k, tm_k4, tm_v;
-    st = make_pair_maps(kv_pages, d, &tm_k, &tm_k4, &tm_v);
+    mla::PairMaps maps;
+    st = make_pair_maps(kv_pages, d, &maps);
     if (st != MLA_OK) return st;
-    const cudaError_t e = mla::launch_decode_pair(p, tm_q, tm_k, tm_k4, tm_v, s);
+    const cudaError_t e = mla::launch_decode_pair(p, tm_q, maps, s);
     if (e != cudaSuccess) return cuda_fail(e);
+    if (p.view == mla::kViewWindow) return MLA_OK;
   }
   const cudaError_t e = mla::launch_decode_tc(p, (h + 15) / 16 * 16, h, 8, tm_q, tm_kv, tm_kvg, tm_kvb, grid, s);
   return e == cudaSuccess ? MLA_OK : cuda_fail(e);
@@ -545,6 +551,22 @@ mla::WorkspaceLayout shared_layout(const mla_decode_desc *d, int num_groups, int
   // 2 (blocks of 128 rows + grid / 2) <= rows / 64 + 2 num_groups + grid
   const int slots = v + num_groups + 2 * grid;
   return mla::workspace_layout(v, (slots + 1) / 2);
+}
+// The pair kernel takes windows of requests with more than one block of 64 rows
+// in the other kernel; its start and end take 2 to 5 us longer on a bf16 cache,
+// which rows x tokens in view (at most) have to make up for.  Measured, us a
+// call, pair kernel / blocks of 64 rows, bf16, rows x requests, window: 128 x 8,
+// 128 (0.1 M) 17.2 / 15.3; 192 x 8, 128 21.8 / 19.5; 128 x 32, 128 (0.5 M)
+// 18.0 / 21.5; 128 x 1, 4096 22.4 / 35.1; 192 x 8, 512 (0.8 M) 23.2 / 20.7;
+// 128 x 128, 512 57.6 / 64.5; 192 x 128, 4096 292 / 349; 512 x 128, 4096
+// 550 / 868; e4m3: 20.2 / 23.1, 20.2 / 26.4, 20.3 / 29.7, 25.0 / 42.6,
+// 23.5 / 29.8, 60.6 / 80.6, 252 / 312, 465 / 731.
+constexpr long long kWindowPairWork = 1LL << 19;
+bool window_pair_path(const mla_decode_desc *d, int window, int sinks) {
+  if (rows_of(d) <= kTcHeadsPerGroup) return false;
+  const long long rows = (long long)d->batch * rows_of(d);
+  const long long seen = (long long)window + sinks, most = (long long)d->max_pages_per_seq * mla::kPage;
+  return d->kv_dtype == MLA_KV_E4M3 || rows * (seen < most ? seen : most) >= kWindowPairWork;
 }
 // The pair kernel takes the shared pages when the groups fill its blocks of 128
 // rows on average and there is enough to multiply: it is a kernel more (9 to 13
@@ -903,6 +925,10 @@ int mla_decode_window(const void *q, const void *kv_pages, const int32_t *block_
   if (workspace_bytes < wl.total) return MLA_ERR_WORKSPACE;
   mla::DecodeParams p;
   p.view = mla::kViewWindow;
+  if (window_pair_path(d, window, sinks)) {
+    p.pair_blocks = d->batch * ((rows_of(d) + 127) / 128);
+    p.pairs = f.sms / 2;
+  }
   // (longer than any request: the kernel's sums with them stay in 32 bits)
   p.window = window < kMaxView ? window : kMaxView;
   p.sinks = sinks < kMaxView ? sinks : kMaxView;

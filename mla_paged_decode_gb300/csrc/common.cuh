@@ -98,7 +98,7 @@ struct DecodeParams {
   const int32_t *group_starts = nullptr;  // [num_groups + 1]
   const int32_t *shared_pages = nullptr;  // [num_groups]
   int num_groups = 0, prefix_blocks = 0;
-  // Shared pages attended by the pair kernel (csrc/decode_pair.cu) in
+  // Shared pages, or windows, attended by the pair kernel (csrc/decode_pair.cu) in
   // pair_blocks blocks of 128 rows on `pairs` CTA pairs; prefix_blocks is then 0.
   int pair_blocks = 0, pairs = 0;
   int kv_e4m3;
@@ -252,6 +252,13 @@ struct ViewReq {
   __device__ __forceinline__ int page(long long t) const {
     return t < nsink ? int(t) : int(t) - nsink + first;
   }
+  // rows of page t of the view that some row sees, as bits
+  __device__ __forceinline__ unsigned long long seen_rows(const DecodeParams &p, int t) const {
+    const int base = page(t) * kPage;
+    auto below = [](int n) { return n <= 0 ? 0ull : n >= 64 ? ~0ull : (1ull << n) - 1ull; };
+    const unsigned long long sunk = below(p.sinks - base);
+    return t < nsink ? sunk : (below(end - base) & ~below(lead - base)) | (sunk & below(end - base));
+  }
   // tokens of tile t that some row sees, counted from the tile's start
   __device__ __forceinline__ int seen(const DecodeParams &p, long long t) const {
     const int base = page(t) * kPage;
@@ -301,27 +308,37 @@ __device__ inline ViewReq shared_block(const DecodeParams &p, int v) {
   return r;
 }
 
+// Block v / B of R rows of request v mod B, through the window and the sinks.
+template <int R = 64>
+__device__ inline ViewReq window_block(const DecodeParams &p, int v) {
+  ViewReq r;
+  const int b = v % p.batch, g = v / p.batch;
+  r.req = b;
+  r.row0 = b * p.heads + R * g;
+  r.rows = min(R, p.heads - R * g);
+  const int L = checked_len(p, b, nullptr);
+  r.end = row_len(p, L, R * g + r.rows - 1);
+  if (r.end == 0) return r;
+  // the block's first query sits at position L - T + R g / q_heads
+  r.lead = max(0, L - p.q_len + (R * g) / p.q_heads + 1 - p.window);
+  r.first = r.lead / kPage;
+  r.nsink = min((p.sinks + kPage - 1) / kPage, r.first);
+  r.tiles = r.nsink + (r.end + kPage - 1) / kPage - r.first;
+  return r;
+}
+
 __device__ inline ViewReq view_req(const DecodeParams &p, int v) {
   if (p.view == kViewShared && v < p.prefix_blocks) return shared_block(p, v);
   ViewReq r;
-  const int u = p.view == kViewShared ? v - p.prefix_blocks : v;
+  if (p.view == kViewWindow) return window_block(p, v);
+  const int u = v - p.prefix_blocks;
   const int b = u % p.batch, g = u / p.batch;
   r.req = b;
   r.row0 = b * p.heads + 64 * g;
   r.rows = min(64, p.heads - 64 * g);
-  const int L = checked_len(p, b, nullptr);
-  r.end = group_len(p, L, g);
-  if (p.view == kViewShared) {
-    r.first = group_shared_pages(p, group_of_request(p, b));
-    r.tiles = max(0, (r.end + kPage - 1) / kPage - r.first);
-    return r;
-  }
-  if (r.end == 0) return r;
-  // the block's first query sits at position L - T + 64 g / q_heads
-  r.lead = max(0, L - p.q_len + (64 * g) / p.q_heads + 1 - p.window);
-  r.first = r.lead / kPage;
-  r.nsink = min((p.sinks + kPage - 1) / kPage, r.first);
-  r.tiles = r.nsink + (r.end + kPage - 1) / kPage - r.first;
+  r.end = group_len(p, checked_len(p, b, nullptr), g);
+  r.first = group_shared_pages(p, group_of_request(p, b));
+  r.tiles = max(0, (r.end + kPage - 1) / kPage - r.first);
   return r;
 }
 

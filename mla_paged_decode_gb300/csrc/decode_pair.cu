@@ -1,5 +1,6 @@
-// Shared-prefix attention on CTA pairs: the rows of a group (all heads and
-// query tokens of its requests) over the pages they share, bf16.
+// Attention of blocks of 128 rows on CTA pairs: the rows of a group (all heads
+// and query tokens of its requests) over the pages they share, or (WIN) the rows
+// of a request through its window and sinks.
 //
 // The product is [rows x 576] x [576 x tokens] and [rows x tokens] x [tokens x
 // 512]: 2176 flops per row and cached token, compute bound from about 150 rows
@@ -32,6 +33,7 @@
 // Work is split as in the decode kernel: the tiles of all blocks in one line,
 // cut into equal ranges, one per pair; every piece leaves an fp32 partial.
 #include "common.cuh"
+#include "pair_maps.cuh"
 #include "sm100.cuh"
 #include "splits.cuh"
 
@@ -88,12 +90,20 @@ using namespace pair;
 
 __device__ __forceinline__ uint32_t bar(uint64_t &b) { return smem_u32(&b); }
 
+// Block v of 128 rows: of a group's rows over its shared pages, or (WIN) of a
+// request's rows through its window.
+template <bool WIN>
+__device__ __forceinline__ ViewReq block_view(const DecodeParams &p, int v) {
+  if constexpr (WIN) return window_block<kPairRows>(p, v);
+  else return shared_block<kPairRows>(p, v);
+}
+template <bool WIN>
 __device__ __forceinline__ int block_tiles(const DecodeParams &p, int v) {
-  return (shared_block<kPairRows>(p, v).tiles + kTilePages - 1) / kTilePages;
+  return (block_view<WIN>(p, v).tiles + kTilePages - 1) / kTilePages;
 }
 
 // The pieces of this pair's range, in order.
-template <bool F8>
+template <bool F8, bool WIN>
 struct Pieces {
   const DecodeParams &p;
   const CtaRange &r;
@@ -103,7 +113,7 @@ struct Pieces {
   __device__ Pieces(const DecodeParams &p_, const CtaRange &r_) : p(p_), r(r_), v(r_.v_begin), pv(r_.p_begin) {}
   __device__ bool next() {
     while (v < p.pair_blocks && pv < r.end) {
-      view = shared_block<kPairRows>(p, v);
+      view = block_view<WIN>(p, v);
       tiles = (view.tiles + kTilePages - 1) / kTilePages;
       if (tiles == 0) { ++v; continue; }
       t0 = max(r.start, pv) - pv;
@@ -116,10 +126,10 @@ struct Pieces {
   __device__ void advance() { pv += request_cost(tiles, Cfg<F8>::kPieceTiles); ++v; }
 };
 
-template <bool F8>
+template <bool F8, bool WIN>
 __device__ __forceinline__ uint32_t total_tiles(const DecodeParams &p, const CtaRange &r) {
   uint32_t n = 0;
-  for (Pieces<F8> w(p, r); w.next(); w.advance()) n += uint32_t(w.t1 - w.t0);
+  for (Pieces<F8, WIN> w(p, r); w.next(); w.advance()) n += uint32_t(w.t1 - w.t0);
   return n;
 }
 
@@ -154,9 +164,9 @@ __device__ __forceinline__ int next_slot(int s) { return s + 1 == Cfg<F8>::kRing
 // ------------------------------------------------------------------ producer
 
 // One position in the tiles of a range, with the tile's pages.
-template <bool F8>
+template <bool F8, bool WIN>
 struct TileWalk {
-  Pieces<F8> w;
+  Pieces<F8, WIN> w;
   long long t;
   bool live;
   int page[kTilePages];
@@ -171,7 +181,7 @@ struct TileWalk {
     if (!live) return;
     const int32_t *row = w.p.block_table + size_t(w.view.req) * w.p.max_pages;
 #pragma unroll
-    for (int i = 0; i < kTilePages; ++i) page[i] = __ldg(row + min(int(t) * kTilePages + i, w.view.tiles - 1));
+    for (int i = 0; i < kTilePages; ++i) page[i] = __ldg(row + w.view.page(min(int(t) * kTilePages + i, w.view.tiles - 1)));
   }
   __device__ void check(int *err) {
 #pragma unroll
@@ -180,6 +190,11 @@ struct TileWalk {
         atomicOr(err, kErrBadPage);
         page[i] = 0;
       }
+  }
+  // WIN: rows of page i that some row of the block sees (none past the view)
+  __device__ unsigned long long seen(int i) const {
+    const int k = int(t) * kTilePages + i;
+    return k < w.view.tiles ? w.view.seen_rows(w.p, k) : 0ull;
   }
   __device__ bool first() const { return t == w.t0; }
   __device__ void step() {
@@ -194,11 +209,11 @@ struct TileWalk {
 
 // One thread produces: a warp's votes and shuffles between the units made
 // the producer the slowest role (470 cycles a unit, all 17 of a tile).
-template <bool F8>
+template <bool F8, bool WIN>
 __device__ __forceinline__ void produce(const DecodeParams &p, const CtaRange &r, Misc &m, uint32_t sQ,
                                         uint32_t sRing, uint32_t rank, const CUtensorMap *tm_q,
                                         const CUtensorMap *tm_k, const CUtensorMap *tm_k4, const CUtensorMap *tm_v,
-                                        int *err) {
+                                        const CUtensorMap *tm_va, const CUtensorMap *tm_vr, int *err) {
   constexpr int kKUnits = Cfg<F8>::kKUnits;
   volatile int *abort = &m.abort;
   const bool leader = rank == 0;
@@ -219,7 +234,7 @@ __device__ __forceinline__ void produce(const DecodeParams &p, const CtaRange &r
     if (at == 0) lap ^= 1;
     return s;
   };
-  auto load_k = [&](const TileWalk<F8> &c) {
+  auto load_k = [&](const TileWalk<F8, WIN> &c) {
     if (!F8 && c.first()) {  // (e4m3: the softmax warps load and split Q)
       if (!mbar_wait_clk(bar(m.q_empty), (q_it & 1) ^ 1, abort, kTimeoutClk)) return false;
       ++q_it;
@@ -244,41 +259,75 @@ __device__ __forceinline__ void produce(const DecodeParams &p, const CtaRange &r
     }
     return true;
   };
-  auto load_v = [&](const int (&page)[kTilePages]) {
+  auto load_v = [&](const int (&page)[kTilePages], const unsigned long long (&seen)[kTilePages]) {
 #pragma unroll
     for (int i = 0; i < kTilePages; ++i) {
       for (int h = 0; h < (F8 ? 1 : 2); ++h) {
         uint32_t full;
         const int s = slot(1, kUnitBytes, &full);
         if (s < 0) return false;
-        tma_load_4d_pair(sRing + s * kUnitBytes, tm_v, full, 0, 0, (F8 ? 2 : 4) * int(rank), page[i] * 8 + 4 * h);
+        const uint32_t dst = sRing + s * kUnitBytes;
+        constexpr int kBlocks = F8 ? 2 : 4, kAtoms = F8 ? 8 : 4;  // of a unit
+        const int block = kBlocks * int(rank), atom = page[i] * 8 + 4 * h;
+        const uint64_t rows = WIN ? seen[i] >> (32 * h) : ~0ull;
+        const uint64_t all = F8 ? ~0ull : 0xffffffffull;
+        if (!WIN || (rows & all) == all) {
+          tma_load_4d_pair(dst, tm_v, full, 0, 0, block, atom);
+          continue;
+        }
+        // Rows that the block does not see may hold anything, and weights of 0
+        // do not keep a NaN out of the product: they are loaded from past the
+        // end of the pool, which reads as zeros.
+        const int none = p.num_pages * 8;
+#pragma unroll 1
+        for (int a = 0; a < kAtoms; ++a) {
+          const uint32_t m8 = uint32_t(rows >> (8 * a)) & 0xffu;
+          if (m8 == 0xffu || m8 == 0) {
+            tma_load_4d_pair(dst + a * kBlocks * 1024, tm_va, full, 0, 0, block, m8 ? atom + a : none);
+            continue;
+          }
+#pragma unroll 1
+          for (int k = 0; k < 8 * kBlocks; ++k) {
+            const int rr = k & 7, bl = k >> 3;
+            tma_load_4d_pair(dst + a * kBlocks * 1024 + bl * 1024 + rr * 128, tm_vr, full, 0, rr, block + bl,
+                             (m8 >> rr) & 1u ? atom + a : none);
+          }
+        }
       }
     }
     return true;
   };
   // c: the next tile to load K of; its pages are read a tile early, so that
   // their latency hides behind the units of the tile before
-  TileWalk<F8> c(p, r);
-  int last[kTilePages];  // pages of the tile whose V comes next
+  TileWalk<F8, WIN> c(p, r);
+  int last[kTilePages];  // pages of the tile whose V comes next, and their seen rows (WIN)
+  unsigned long long lseen[kTilePages] = {0, 0, 0, 0};
   bool have = false;
   while (ok && (c.live || have)) {
     int pages[kTilePages];
+    unsigned long long seen[kTilePages] = {0, 0, 0, 0};
     const bool more = c.live;
     if (F8 && have && more && c.first()) {
-      ok = load_v(last);
+      ok = load_v(last, lseen);
       have = false;
       if (!ok) break;
     }
     if (more) {
       c.check(err);
 #pragma unroll
-      for (int i = 0; i < kTilePages; ++i) pages[i] = c.page[i];
+      for (int i = 0; i < kTilePages; ++i) {
+        pages[i] = c.page[i];
+        if (WIN) seen[i] = c.seen(i);
+      }
       ok = load_k(c);
       c.step();
     }
-    if (ok && have) ok = load_v(last);
+    if (ok && have) ok = load_v(last, lseen);
 #pragma unroll
-    for (int i = 0; i < kTilePages; ++i) last[i] = pages[i];
+    for (int i = 0; i < kTilePages; ++i) {
+      last[i] = pages[i];
+      lseen[i] = seen[i];
+    }
     have = more;
   }
   if (!ok) atomicOr(err, kErrTimeout);
@@ -291,7 +340,7 @@ __device__ __forceinline__ bool warp_wait(uint32_t b, uint32_t parity, volatile 
   return __all_sync(0xffffffffu, mbar_wait_clk(b, parity, abort, kTimeoutClk));
 }
 
-template <bool F8>
+template <bool F8, bool WIN>
 __device__ __forceinline__ void score_mmas(const DecodeParams &p, const CtaRange &r, Misc &m, uint32_t sQ,
                                            uint32_t sRing, uint32_t tmem, int *err) {
   volatile int *abort = &m.abort;
@@ -303,7 +352,7 @@ __device__ __forceinline__ void score_mmas(const DecodeParams &p, const CtaRange
   uint32_t n = 0;
   uint32_t q_it = 0;
   bool ok = true;
-  for (Pieces<F8> w(p, r); ok && w.next(); w.advance()) {
+  for (Pieces<F8, WIN> w(p, r); ok && w.next(); w.advance()) {
     for (long long t = w.t0; ok && t < w.t1; ++t, ++n) {
       const int b = int(n & 1);
       ok = warp_wait(bar(m.s_free[b]), ((n >> 1) & 1) ^ 1, abort);
@@ -352,7 +401,7 @@ __device__ __forceinline__ void score_mmas(const DecodeParams &p, const CtaRange
   __syncwarp();
 }
 
-template <bool F8>
+template <bool F8, bool WIN>
 __device__ __forceinline__ void pv_mmas(const DecodeParams &p, const CtaRange &r, Misc &m, uint32_t sP,
                                         uint32_t sRing, uint32_t tmem, int *err) {
   volatile int *abort = &m.abort;
@@ -362,12 +411,12 @@ __device__ __forceinline__ void pv_mmas(const DecodeParams &p, const CtaRange &r
   // V, MN-major: 128-byte blocks of dims 1 KB apart, 8-token groups 4 KB (bf16)
   // or 2 KB (e4m3) apart
   const uint64_t dv = smem_desc_sw128(sRing, 1024, F8 ? 2048 : 4096);
-  const uint32_t total = total_tiles<F8>(p, r);
+  const uint32_t total = total_tiles<F8, WIN>(p, r);
   Landed landed;
   uint32_t n = 0;
   uint32_t o_it = 0;
   bool ok = true;
-  for (Pieces<F8> w(p, r); ok && w.next(); w.advance(), ++o_it) {
+  for (Pieces<F8, WIN> w(p, r); ok && w.next(); w.advance(), ++o_it) {
     for (long long t = w.t0; ok && t < w.t1; ++t, ++n) {
       ok = warp_wait(bar(m.o_ready[n & 1]), (n >> 1) & 1, abort);
       if (ok && t == w.t0) ok = warp_wait(bar(m.o_free), (o_it & 1) ^ 1, abort);
@@ -506,7 +555,7 @@ __device__ __forceinline__ bool split_q(const DecodeParams &p, Misc &m, unsigned
 
 // A failed wait never leaves the loop: the warp goes on without working, so
 // that the others find it at their barriers (later waits fail at once).
-template <bool F8>
+template <bool F8, bool WIN>
 __device__ __forceinline__ void softmax(const DecodeParams &p, const CtaRange &r, Misc &m, unsigned char *smem,
                                         uint32_t tmem, uint32_t rank, int pair_id, int *err) {
   volatile int *abort = &m.abort;
@@ -526,9 +575,9 @@ __device__ __forceinline__ void softmax(const DecodeParams &p, const CtaRange &r
   uint32_t n = 0;
   uint32_t o_it = 0;
   bool ok = true;
-  for (Pieces<F8> w(p, r); w.next(); w.advance(), ++o_it) {
+  for (Pieces<F8, WIN> w(p, r); w.next(); w.advance(), ++o_it) {
     const int grow = w.view.row0 + int(rank) * kRows + row;
-    const int hi = row_view(p, w.view, min(grow, p.batch * p.heads - 1)).hi;
+    const RowView rv = row_view(p, w.view, min(grow, p.batch * p.heads - 1));
     const bool mine = int(rank) * kRows + row < w.view.rows;
     if constexpr (F8) {
       float qinv;
@@ -559,10 +608,19 @@ __device__ __forceinline__ void softmax(const DecodeParams &p, const CtaRange &r
 #pragma unroll
         for (int i = 0; i < 64; ++i) x[i] = 0.f;
       }
-      const int left = hi - (int(t) * kTilePages + pb) * kPage;  // tokens of the page this row sees
+      const int idx = int(t) * kTilePages + pb;  // page of the view
+      const int base = w.view.page(idx) * kPage;
+      const int left = idx < w.view.tiles ? rv.hi - base : 0;  // tokens of the page this row sees
       if (left < kPage) {
 #pragma unroll
         for (int i = 0; i < 64; ++i) x[i] = i < left ? x[i] : -INFINITY;
+      }
+      if constexpr (WIN) {
+        const int skip = rv.lo - base, sink = p.sinks - base;
+        if (skip > 0 && sink < kPage) {
+#pragma unroll
+          for (int i = 0; i < 64; ++i) x[i] = i >= skip || i < sink ? x[i] : -INFINITY;
+        }
       }
       float mx4[4] = {x[0], x[1], x[2], x[3]};
 #pragma unroll
@@ -647,10 +705,18 @@ __device__ __forceinline__ void softmax(const DecodeParams &p, const CtaRange &r
     const float inv = sum > 0.f ? p.kv_scale / sum : 0.f;
     ok = ok && __all_sync(0xffffffffu, mbar_wait_clk(bar(m.o_full), o_it & 1, abort, kTimeoutClk));
     const int c_first = sched_owner_short(w.pv, r.total, r.g_eff);
+    const int pieces = sched_owner_short(w.pv + w.tiles - 1, r.total, r.g_eff) - c_first + 1;
+    const bool split = !WIN || pieces > 1;
+    // shared pages: every piece leaves a partial, in the slots of its pair and
+    // block; a window's do when the block is cut, in the slots of the split
+    // merge, its CTA r * pairs + c standing for half r of pair c
+    const size_t slot = WIN ? 2 * size_t(rank * p.pairs + pair_id) + (w.v != r.v_begin ? 1 : 0)
+                            : 2 * size_t(pair_id + w.v) + rank;
     if (ok) {
       tc_fence_after();
-      const size_t slot = 2 * size_t(pair_id + w.v) + rank;
-      float *dst = slot_out_ptr(p) + (slot * kSlotHeads + row) * kDv + 256 * (q >> 1) + 128 * g;
+      const int d0 = 256 * (q >> 1) + 128 * g;
+      float *dst = slot_out_ptr(p) + (slot * kSlotHeads + row) * kDv + d0;
+      __nv_bfloat16 *out = p.out + size_t(grow) * kDv + d0;
 #pragma unroll 1
       for (int c = 0; c < 128; c += 32) {
         uint32_t o[32];
@@ -662,28 +728,48 @@ __device__ __forceinline__ void softmax(const DecodeParams &p, const CtaRange &r
             float v[8];
 #pragma unroll
             for (int k = 0; k < 8; ++k) v[k] = __uint_as_float(o[i + k]) * inv;
-            st_global_v8(dst + c + i, v);
+            if (split) {
+              st_global_v8(dst + c + i, v);
+            } else {
+              uint32_t h[4];
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                __nv_bfloat162 x2 = __floats2bfloat162_rn(v[2 * k], v[2 * k + 1]);
+                h[k] = *reinterpret_cast<uint32_t *>(&x2);
+              }
+              *reinterpret_cast<uint4 *>(out + c + i) = make_uint4(h[0], h[1], h[2], h[3]);
+            }
           }
         }
       }
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive_cluster(o_free);
-      if (mine && pb == 0) slot_lse_ptr(p)[slot * kSlotHeads + row] = mrun + log2f(sumx);
-      if (st == 0 && rank == 0 && pair_id == c_first) {
-        const int c_last = sched_owner_short(w.pv + w.tiles - 1, r.total, r.g_eff);
-        info_ptr(p)[p.batch * p.head_groups + w.v] = make_int4(c_first, c_last - c_first + 1, pair_id + w.v, 0);
+      if (mine && pb == 0) {
+        const float lse2 = mrun + log2f(sumx);
+        if (split) slot_lse_ptr(p)[slot * kSlotHeads + row] = lse2;
+        else p.lse[grow] = lse_out(p, lse2);
+      }
+      if (st == 0 && pair_id == c_first) {
+        if (WIN) {  // the record of this half's 64 rows
+          if (w.view.rows > int(rank) * kRows)
+            info_ptr(p)[(2 * (w.v / p.batch) + int(rank)) * p.batch + w.v % p.batch] =
+                make_int4(int(rank) * p.pairs + c_first, pieces, int(slot), 0);
+        } else if (rank == 0) {
+          info_ptr(p)[p.batch * p.head_groups + w.v] = make_int4(c_first, pieces, pair_id + w.v, 0);
+        }
       }
     }
   }
   if (!ok) atomicOr(err, kErrTimeout);
 }
 
-template <bool F8>
+template <bool F8, bool WIN>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     decode_pair_kernel(const __grid_constant__ DecodeParams p, const __grid_constant__ CUtensorMap tm_q,
                        const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_k4,
-                       const __grid_constant__ CUtensorMap tm_v) {
+                       const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_va,
+                       const __grid_constant__ CUtensorMap tm_vr) {
   constexpr int kOffP = Cfg<F8>::kOffP, kOffRing = Cfg<F8>::kOffRing;
   extern __shared__ unsigned char smem_raw[];
   const uint32_t raw = smem_u32(smem_raw), pad = ((raw + 1023u) & ~1023u) - raw;
@@ -733,11 +819,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     tma_prefetch_desc(&tm_v);
   }
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  // blocks without pages have no partials
-  for (int v = int(blockIdx.x) * kThreads + tid; v < p.pair_blocks; v += int(gridDim.x) * kThreads)
-    if (block_tiles(p, v) == 0) info_ptr(p)[p.batch * p.head_groups + v] = make_int4(-1, 0, 0, 0);
-  schedule_range<Cfg<F8>::kPieceTiles, true>(p.pair_blocks, pair_id, p.pairs, [&](int v) { return block_tiles(p, v); },
-                                    &m.range, m.scratch);
+  // blocks without pages: no partials, or the neutral pair
+  if constexpr (WIN) {
+    for (int v = int(blockIdx.x); v < p.pair_blocks; v += int(gridDim.x)) {
+      const ViewReq w = window_block<kPairRows>(p, v);
+      if (tid == 0) checked_len(p, w.req, err);
+      if (w.tiles != 0) continue;
+      if (tid < 2 && w.rows > tid * kRows)
+        info_ptr(p)[(2 * (v / p.batch) + tid) * p.batch + v % p.batch] = make_int4(-1, 0, 0, 0);
+      uint4 *dst = reinterpret_cast<uint4 *>(p.out + size_t(w.row0) * kDv);
+      for (int i = tid; i < w.rows * kDv / 8; i += kThreads) dst[i] = make_uint4(0, 0, 0, 0);
+      for (int i = tid; i < w.rows; i += kThreads) p.lse[size_t(w.row0) + i] = -INFINITY;
+    }
+  } else {
+    for (int v = int(blockIdx.x) * kThreads + tid; v < p.pair_blocks; v += int(gridDim.x) * kThreads)
+      if (block_tiles<WIN>(p, v) == 0) info_ptr(p)[p.batch * p.head_groups + v] = make_int4(-1, 0, 0, 0);
+  }
+  schedule_range<Cfg<F8>::kPieceTiles, true>(
+      p.pair_blocks, pair_id, p.pairs, [&](int v) { return block_tiles<WIN>(p, v); }, &m.range, m.scratch);
   tc_fence_before();
   cluster_sync();  // both CTAs' barriers and TMEM are ready
   tc_fence_after();
@@ -746,13 +845,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 
   if (r.start < r.end) {
     if (warp == 0) {
-      if (lane == 0) produce<F8>(p, r, m, sbase + kOffQ, sbase + kOffRing, rank, &tm_q, &tm_k, &tm_k4, &tm_v, err);
+      if (lane == 0)
+        produce<F8, WIN>(p, r, m, sbase + kOffQ, sbase + kOffRing, rank, &tm_q, &tm_k, &tm_k4, &tm_v, &tm_va,
+                         &tm_vr, err);
     } else if (warp == 1) {
-      if (rank == 0) score_mmas<F8>(p, r, m, sbase + kOffQ, sbase + kOffRing, tmem, err);
+      if (rank == 0) score_mmas<F8, WIN>(p, r, m, sbase + kOffQ, sbase + kOffRing, tmem, err);
     } else if (warp == 2) {
-      if (rank == 0) pv_mmas<F8>(p, r, m, sbase + kOffP, sbase + kOffRing, tmem, err);
+      if (rank == 0) pv_mmas<F8, WIN>(p, r, m, sbase + kOffP, sbase + kOffRing, tmem, err);
     } else if (warp >= 4) {
-      softmax<F8>(p, r, m, smem, tmem, rank, pair_id, err);
+      softmax<F8, WIN>(p, r, m, smem, tmem, rank, pair_id, err);
     }
     // no MMA may still read this CTA's shared memory, and no copy write it:
     // the MMAs waited for every copy unless a wait gave up
@@ -777,11 +878,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   cluster_sync();  // the pair leaves together: neither SM takes another CTA before both gave up their TMEM
 }
 
-template <bool F8>
-cudaError_t launch(const DecodeParams &p, const CUtensorMap &tm_q, const CUtensorMap &tm_k,
-                   const CUtensorMap &tm_k4, const CUtensorMap &tm_v, cudaStream_t stream) {
+template <bool F8, bool WIN>
+cudaError_t launch(const DecodeParams &p, const CUtensorMap &tm_q, const PairMaps &m, cudaStream_t stream) {
   static SmemLimitOnce smem_limit;
-  const cudaError_t e = smem_limit.ensure(decode_pair_kernel<F8>, smem_bytes<F8>());
+  const cudaError_t e = smem_limit.ensure(decode_pair_kernel<F8, WIN>, smem_bytes<F8>());
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(2 * p.pairs);
@@ -793,16 +893,21 @@ cudaError_t launch(const DecodeParams &p, const CUtensorMap &tm_q, const CUtenso
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, decode_pair_kernel<F8>, p, tm_q, tm_k, tm_k4, tm_v);
+  return cudaLaunchKernelEx(&cfg, decode_pair_kernel<F8, WIN>, p, tm_q, m.k, m.k4, m.v, m.va, m.vr);
 }
 
 }  // namespace
 
-// tm_q is read for a bf16 cache, tm_k4 for an e4m3 one.
-cudaError_t launch_decode_pair(const DecodeParams &p, const CUtensorMap &tm_q, const CUtensorMap &tm_k,
-                               const CUtensorMap &tm_k4, const CUtensorMap &tm_v, cudaStream_t stream) {
-  return p.kv_e4m3 ? launch<true>(p, tm_q, tm_k, tm_k4, tm_v, stream)
-                   : launch<false>(p, tm_q, tm_k, tm_k4, tm_v, stream);
+// tm_q is read for a bf16 cache, m.k4 for an e4m3 one.  A window's split merge
+// follows here; the shared pages' partials wait for the tails.
+cudaError_t launch_split_merge(const DecodeParams &p, int grid, cudaStream_t stream);
+
+cudaError_t launch_decode_pair(const DecodeParams &p, const CUtensorMap &tm_q, const PairMaps &m,
+                               cudaStream_t stream) {
+  if (p.view == kViewShared)
+    return p.kv_e4m3 ? launch<true, false>(p, tm_q, m, stream) : launch<false, false>(p, tm_q, m, stream);
+  const cudaError_t e = p.kv_e4m3 ? launch<true, true>(p, tm_q, m, stream) : launch<false, true>(p, tm_q, m, stream);
+  return e == cudaSuccess ? launch_split_merge(p, 2 * p.pairs, stream) : e;
 }
 
 }  // namespace mla

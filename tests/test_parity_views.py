@@ -36,6 +36,31 @@ def test_window(kv_dtype, heads, q_len, window, sinks):
 
 
 @pytest.mark.parametrize("kv_dtype", ["bf16", "e4m3"])
+@pytest.mark.parametrize("heads,q_len", [(128, 1), (65, 2), (100, 2), (16, 16), (80, 5), (96, 3)])
+@pytest.mark.parametrize("window,sinks", [(1, 0), (5, 4), (70, 0), (64, 64), (130, 70), (300, 200), (10**9, 3), (100, 2**31 - 1)])
+def test_window_of_many_rows(kv_dtype, heads, q_len, window, sinks):
+    """Blocks of 128 rows, whole and part full; windows that start and end in
+    every part of a page and of a tile of four (a bf16 cache takes them when
+    there are enough rows)."""
+    lens = (LENS + [256, 257, 321, 1000, 1003, 1041]) * (4 if kv_dtype == "bf16" else 1)
+    c = make(lens, heads, q_len, kv_dtype, window_seen(window, sinks, q_len), seed=heads + window % 1000)
+    base = heads % 2
+    out, lse = run_window(c, window, sinks, base)
+    check(c, out, lse, base, f"window {window} sinks {sinks}")
+
+
+@pytest.mark.parametrize("kv_dtype", ["bf16", "e4m3"])
+def test_window_of_many_rows_over_many_and_long_requests(kv_dtype):
+    lens = [9000, 4096, 12001, 8191]
+    c = make(lens, 128, 2, kv_dtype, window_seen(2500, 40, 2), seed=6)
+    check(c, *run_window(c, 2500, 40), what="long")
+    c = make([20000], 128, 1, kv_dtype, window_seen(16000, 0, 1), seed=7)
+    check(c, *run_window(c, 16000, 0), what="one")
+    c = make([(37 * b) % 300 for b in range(410)], 65, 2, kv_dtype, window_seen(90, 5, 2), seed=8)
+    check(c, *run_window(c, 90, 5), what="many")
+
+
+@pytest.mark.parametrize("kv_dtype", ["bf16", "e4m3"])
 def test_window_over_long_requests(kv_dtype):
     lens = [9000, 4096, 12001, 8191]
     c = make(lens, 64, 1, kv_dtype, window_seen(2500, 40, 1), seed=3)
