@@ -517,7 +517,7 @@ int enqueue_view(mla::DecodeParams p, const void *q, const void *kv_pages, const
     if (st != MLA_OK) return st;
     const cudaError_t e = mla::launch_decode_pair(p, tm_q, maps, s);
     if (e != cudaSuccess) return cuda_fail(e);
-    if (p.view == mla::kViewWindow) return MLA_OK;
+    if (p.view == mla::kViewWindow || p.pair_tails) return MLA_OK;
   }
   const cudaError_t e = mla::launch_decode_tc(p, (h + 15) / 16 * 16, h, 8, tm_q, tm_kv, tm_kvg, tm_kvb, grid, s);
   return e == cudaSuccess ? MLA_OK : cuda_fail(e);
@@ -548,8 +548,9 @@ int shared_blocks(const mla_decode_desc *d, int num_groups, int rows) {
 mla::WorkspaceLayout shared_layout(const mla_decode_desc *d, int num_groups, int grid) {
   const int groups = (rows_of(d) + kTcHeadsPerGroup - 1) / kTcHeadsPerGroup;
   const int v = shared_blocks(d, num_groups, 64) + d->batch * groups;
-  // 2 (blocks of 128 rows + grid / 2) <= rows / 64 + 2 num_groups + grid
-  const int slots = v + num_groups + 2 * grid;
+  // 2 (blocks of 128 rows + grid / 2) <= rows / 64 + 2 num_groups + grid, and
+  // with the tails 2 batch * ceil(request rows / 128) <= batch * (groups + 1) more
+  const int slots = v + num_groups + d->batch + 2 * grid;
   return mla::workspace_layout(v, (slots + 1) / 2);
 }
 // The pair kernel takes windows of requests with more than one block of 64 rows
@@ -932,8 +933,17 @@ int mla_decode_window(const void *q, const void *kv_pages, const int32_t *block_
   // (longer than any request: the kernel's sums with them stay in 32 bits)
   p.window = window < kMaxView ? window : kMaxView;
   p.sinks = sinks < kMaxView ? sinks : kMaxView;
-  return enqueue_view(p, q, kv_pages, block_table, seq_lens, sm_scale, lse_base, out, lse, d, workspace, wl,
-                      f.sms, reinterpret_cast<cudaStream_t>(stream));
+  // Up to 16 pieces a block: the merge takes a block's pieces one after another,
+  // and one request cut across all CTAs waits longer for it than it gains.
+  // Measured, us a call, 8 / 16 / 24 pieces / all CTAs, bf16, 64 rows: 1 request,
+  // window 2000 21.3 / 20.2 / 20.5 / 25.5, 4096 27.0 / 23.4 / 22.3 / 37.0; 4
+  // requests 22.9 / 21.1 / 22.4 / 26.0, 28.8 / 24.2 / 23.9 / 27.2; 16 rows, 4
+  // requests 18.5 / 17.9 / 19.5 / 22.9; e4m3, 64 rows: 1 request, 4096 36.3 / 31.4 /
+  // 31.8 / 44.7.
+  const long long blocks = (long long)d->batch * ((rows_of(d) + kTcHeadsPerGroup - 1) / kTcHeadsPerGroup);
+  const int grid = int(16 * blocks < f.sms ? 16 * blocks : f.sms);
+  return enqueue_view(p, q, kv_pages, block_table, seq_lens, sm_scale, lse_base, out, lse, d, workspace, wl, grid,
+                      reinterpret_cast<cudaStream_t>(stream));
 }
 
 size_t mla_decode_shared_workspace_size(const mla_decode_desc *d, int num_groups, int num_sms) {
@@ -970,7 +980,8 @@ int mla_decode_shared(const void *q, const void *kv_pages, const int32_t *block_
   p.shared_pages = shared_pages;
   p.num_groups = num_groups;
   if (pair_path(d, num_groups)) {
-    p.pair_blocks = shared_blocks(d, num_groups, 128);
+    if (rows_of(d) > kTcHeadsPerGroup) p.pair_tails = d->batch * ((rows_of(d) + 127) / 128);
+    p.pair_blocks = shared_blocks(d, num_groups, 128) + p.pair_tails;
     p.pairs = f.sms / 2;
   } else {
     p.prefix_blocks = shared_blocks(d, num_groups, 64);

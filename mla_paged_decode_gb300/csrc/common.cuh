@@ -100,7 +100,9 @@ struct DecodeParams {
   int num_groups = 0, prefix_blocks = 0;
   // Shared pages, or windows, attended by the pair kernel (csrc/decode_pair.cu) in
   // pair_blocks blocks of 128 rows on `pairs` CTA pairs; prefix_blocks is then 0.
-  int pair_blocks = 0, pairs = 0;
+  // The last pair_tails of them are the requests' own pages (0: left to the
+  // other kernel).
+  int pair_blocks = 0, pair_tails = 0, pairs = 0;
   int kv_e4m3;
   float kv_scale;             // 1 for bf16
   float score_scale_log2;     // sm_scale * log2(e): scores kept in the base-2 domain
@@ -308,16 +310,22 @@ __device__ inline ViewReq shared_block(const DecodeParams &p, int v) {
   return r;
 }
 
-// Block v / B of R rows of request v mod B, through the window and the sinks.
+// Block u / B of R rows of request u mod B: through the window and the sinks, or
+// over the request's own pages.
 template <int R = 64>
-__device__ inline ViewReq window_block(const DecodeParams &p, int v) {
+__device__ inline ViewReq request_block(const DecodeParams &p, int u) {
   ViewReq r;
-  const int b = v % p.batch, g = v / p.batch;
+  const int b = u % p.batch, g = u / p.batch;
   r.req = b;
   r.row0 = b * p.heads + R * g;
   r.rows = min(R, p.heads - R * g);
   const int L = checked_len(p, b, nullptr);
-  r.end = row_len(p, L, R * g + r.rows - 1);
+  r.end = row_len(p, L, min(p.heads, R * (g + 1)) - 1);
+  if (p.view == kViewShared) {
+    r.first = group_shared_pages(p, group_of_request(p, b));
+    r.tiles = max(0, (r.end + kPage - 1) / kPage - r.first);
+    return r;
+  }
   if (r.end == 0) return r;
   // the block's first query sits at position L - T + R g / q_heads
   r.lead = max(0, L - p.q_len + (R * g) / p.q_heads + 1 - p.window);
@@ -329,17 +337,7 @@ __device__ inline ViewReq window_block(const DecodeParams &p, int v) {
 
 __device__ inline ViewReq view_req(const DecodeParams &p, int v) {
   if (p.view == kViewShared && v < p.prefix_blocks) return shared_block(p, v);
-  ViewReq r;
-  if (p.view == kViewWindow) return window_block(p, v);
-  const int u = v - p.prefix_blocks;
-  const int b = u % p.batch, g = u / p.batch;
-  r.req = b;
-  r.row0 = b * p.heads + 64 * g;
-  r.rows = min(64, p.heads - 64 * g);
-  r.end = group_len(p, checked_len(p, b, nullptr), g);
-  r.first = group_shared_pages(p, group_of_request(p, b));
-  r.tiles = max(0, (r.end + kPage - 1) / kPage - r.first);
-  return r;
+  return request_block(p, p.view == kViewShared ? v - p.prefix_blocks : v);
 }
 
 // What row `row` (of all rows) of a block sees: tokens below `hi`, and of

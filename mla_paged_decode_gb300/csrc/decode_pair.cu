@@ -1,6 +1,6 @@
 // Attention of blocks of 128 rows on CTA pairs: the rows of a group (all heads
-// and query tokens of its requests) over the pages they share, or (WIN) the rows
-// of a request through its window and sinks.
+// and query tokens of its requests) over the pages they share, the rows of a
+// request over its own pages, or through its window and sinks.
 //
 // The product is [rows x 576] x [576 x tokens] and [rows x tokens] x [tokens x
 // 512]: 2176 flops per row and cached token, compute bound from about 150 rows
@@ -31,7 +31,8 @@
 // PV_{i+1} follows PV_i without a gap.
 //
 // Work is split as in the decode kernel: the tiles of all blocks in one line,
-// cut into equal ranges, one per pair; every piece leaves an fp32 partial.
+// cut into equal ranges, one per pair; pieces leave fp32 partials, but for
+// windows that one pair holds whole.  Q and the epilogue are a piece's boundary.
 #include "common.cuh"
 #include "pair_maps.cuh"
 #include "sm100.cuh"
@@ -42,6 +43,9 @@ using namespace sm100;
 
 namespace pair {
 constexpr int kThreads = 384;
+// kinds of the kernel: shared pages alone (all of whose rows are seen), windows,
+// shared pages and then the requests' own
+constexpr int kWhole = 0, kWindow = 1, kTails = 2;
 constexpr int kRows = 64;                       // per CTA
 constexpr int kPairRows = 128;                  // per pair
 constexpr int kTilePages = 4;
@@ -61,8 +65,10 @@ struct Cfg {
   static constexpr int kOffP = kQBytes;
   static constexpr int kOffRing = kOffP + kPBytes;
   static constexpr int kOffMisc = kOffRing + kRing * kUnitBytes;
-  static constexpr int kPieceTiles = F8 ? 2 : 1;  // a piece's boundary, in tiles
 };
+// A piece's boundary, in tiles.
+template <bool F8, int KIND>
+constexpr int kPieceTiles = KIND == kTails ? 4 : F8 ? 2 : 1;
 constexpr int kOffQ = 0;
 constexpr uint32_t kColO = 0, kColS = 256;      // S buffer b: 128 columns from 256 + 128 b
 constexpr int kSoftWarps = 8, kSoftThreads = 256;
@@ -90,20 +96,24 @@ using namespace pair;
 
 __device__ __forceinline__ uint32_t bar(uint64_t &b) { return smem_u32(&b); }
 
-// Block v of 128 rows: of a group's rows over its shared pages, or (WIN) of a
-// request's rows through its window.
-template <bool WIN>
+// Block v of 128 rows: of a group's rows over its shared pages, of a request's
+// rows over its own pages, or of a request's rows through its window.
+template <int KIND>
 __device__ __forceinline__ ViewReq block_view(const DecodeParams &p, int v) {
-  if constexpr (WIN) return window_block<kPairRows>(p, v);
-  else return shared_block<kPairRows>(p, v);
+  if constexpr (KIND == kWindow) return request_block<kPairRows>(p, v);
+  if constexpr (KIND == kTails) {
+    const int shared = p.pair_blocks - p.pair_tails;
+    if (v >= shared) return request_block<kPairRows>(p, v - shared);
+  }
+  return shared_block<kPairRows>(p, v);
 }
-template <bool WIN>
+template <int KIND>
 __device__ __forceinline__ int block_tiles(const DecodeParams &p, int v) {
-  return (block_view<WIN>(p, v).tiles + kTilePages - 1) / kTilePages;
+  return (block_view<KIND>(p, v).tiles + kTilePages - 1) / kTilePages;
 }
 
 // The pieces of this pair's range, in order.
-template <bool F8, bool WIN>
+template <bool F8, int KIND>
 struct Pieces {
   const DecodeParams &p;
   const CtaRange &r;
@@ -113,7 +123,7 @@ struct Pieces {
   __device__ Pieces(const DecodeParams &p_, const CtaRange &r_) : p(p_), r(r_), v(r_.v_begin), pv(r_.p_begin) {}
   __device__ bool next() {
     while (v < p.pair_blocks && pv < r.end) {
-      view = block_view<WIN>(p, v);
+      view = block_view<KIND>(p, v);
       tiles = (view.tiles + kTilePages - 1) / kTilePages;
       if (tiles == 0) { ++v; continue; }
       t0 = max(r.start, pv) - pv;
@@ -123,13 +133,13 @@ struct Pieces {
     }
     return false;
   }
-  __device__ void advance() { pv += request_cost(tiles, Cfg<F8>::kPieceTiles); ++v; }
+  __device__ void advance() { pv += request_cost(tiles, kPieceTiles<F8, KIND>); ++v; }
 };
 
-template <bool F8, bool WIN>
+template <bool F8, int KIND>
 __device__ __forceinline__ uint32_t total_tiles(const DecodeParams &p, const CtaRange &r) {
   uint32_t n = 0;
-  for (Pieces<F8, WIN> w(p, r); w.next(); w.advance()) n += uint32_t(w.t1 - w.t0);
+  for (Pieces<F8, KIND> w(p, r); w.next(); w.advance()) n += uint32_t(w.t1 - w.t0);
   return n;
 }
 
@@ -164,9 +174,9 @@ __device__ __forceinline__ int next_slot(int s) { return s + 1 == Cfg<F8>::kRing
 // ------------------------------------------------------------------ producer
 
 // One position in the tiles of a range, with the tile's pages.
-template <bool F8, bool WIN>
+template <bool F8, int KIND>
 struct TileWalk {
-  Pieces<F8, WIN> w;
+  Pieces<F8, KIND> w;
   long long t;
   bool live;
   int page[kTilePages];
@@ -191,7 +201,12 @@ struct TileWalk {
         page[i] = 0;
       }
   }
-  // WIN: rows of page i that some row of the block sees (none past the view)
+  // every row of the tile's pages is seen (false for some such tiles of sinks)
+  __device__ __forceinline__ bool whole() const {
+    const int k = int(t) * kTilePages - w.view.nsink, base = (w.view.first + k) * kPage;
+    return k >= 0 && base >= w.view.lead && base + kTilePages * kPage <= w.view.end;
+  }
+  // rows of page i that some row of the block sees (none past the view)
   __device__ unsigned long long seen(int i) const {
     const int k = int(t) * kTilePages + i;
     return k < w.view.tiles ? w.view.seen_rows(w.p, k) : 0ull;
@@ -207,9 +222,35 @@ struct TileWalk {
   }
 };
 
+// A unit of V of whose rows only some are seen (bit r of `rows`: row r).  The
+// others may hold anything, and weights of 0 do not keep a NaN out of the
+// product: they are loaded from past the end of the pool (`none`), as zeros.
+template <bool F8>
+static __device__ __noinline__ void load_seen(uint32_t dst, uint32_t full, const CUtensorMap *tm_v,
+                                              const CUtensorMap *tm_va, const CUtensorMap *tm_vr, int block, int atom,
+                                              int none, uint64_t rows) {
+  constexpr int kBlocks = F8 ? 2 : 4, kAtoms = F8 ? 8 : 4;
+  constexpr uint64_t kAll = F8 ? ~0ull : 0xffffffffull;
+  if ((rows & kAll) == kAll || (rows & kAll) == 0) {
+    tma_load_4d_pair(dst, tm_v, full, 0, 0, block, rows & kAll ? atom : none);
+    return;
+  }
+#pragma unroll 1
+  for (int a = 0; a < kAtoms; ++a, rows >>= 8, dst += kBlocks * 1024) {
+    const uint32_t m = uint32_t(rows) & 0xffu;
+    if (m == 0xffu || m == 0) {
+      tma_load_4d_pair(dst, tm_va, full, 0, 0, block, m ? atom + a : none);
+      continue;
+    }
+#pragma unroll 1
+    for (int k = 0; k < 8 * kBlocks; ++k)
+      tma_load_4d_pair(dst + k * 128, tm_vr, full, 0, k & 7, block + (k >> 3), (m >> (k & 7)) & 1u ? atom + a : none);
+  }
+}
+
 // One thread produces: a warp's votes and shuffles between the units made
 // the producer the slowest role (470 cycles a unit, all 17 of a tile).
-template <bool F8, bool WIN>
+template <bool F8, int KIND>
 __device__ __forceinline__ void produce(const DecodeParams &p, const CtaRange &r, Misc &m, uint32_t sQ,
                                         uint32_t sRing, uint32_t rank, const CUtensorMap *tm_q,
                                         const CUtensorMap *tm_k, const CUtensorMap *tm_k4, const CUtensorMap *tm_v,
@@ -234,7 +275,7 @@ __device__ __forceinline__ void produce(const DecodeParams &p, const CtaRange &r
     if (at == 0) lap ^= 1;
     return s;
   };
-  auto load_k = [&](const TileWalk<F8, WIN> &c) {
+  auto load_k = [&](const TileWalk<F8, KIND> &c) {
     if (!F8 && c.first()) {  // (e4m3: the softmax warps load and split Q)
       if (!mbar_wait_clk(bar(m.q_empty), (q_it & 1) ^ 1, abort, kTimeoutClk)) return false;
       ++q_it;
@@ -259,7 +300,7 @@ __device__ __forceinline__ void produce(const DecodeParams &p, const CtaRange &r
     }
     return true;
   };
-  auto load_v = [&](const int (&page)[kTilePages], const unsigned long long (&seen)[kTilePages]) {
+  auto load_v = [&](const int (&page)[kTilePages], const unsigned long long (&seen)[kTilePages], bool whole) {
 #pragma unroll
     for (int i = 0; i < kTilePages; ++i) {
       for (int h = 0; h < (F8 ? 1 : 2); ++h) {
@@ -267,68 +308,51 @@ __device__ __forceinline__ void produce(const DecodeParams &p, const CtaRange &r
         const int s = slot(1, kUnitBytes, &full);
         if (s < 0) return false;
         const uint32_t dst = sRing + s * kUnitBytes;
-        constexpr int kBlocks = F8 ? 2 : 4, kAtoms = F8 ? 8 : 4;  // of a unit
-        const int block = kBlocks * int(rank), atom = page[i] * 8 + 4 * h;
-        const uint64_t rows = WIN ? seen[i] >> (32 * h) : ~0ull;
-        const uint64_t all = F8 ? ~0ull : 0xffffffffull;
-        if (!WIN || (rows & all) == all) {
-          tma_load_4d_pair(dst, tm_v, full, 0, 0, block, atom);
-          continue;
-        }
-        // Rows that the block does not see may hold anything, and weights of 0
-        // do not keep a NaN out of the product: they are loaded from past the
-        // end of the pool, which reads as zeros.
-        const int none = p.num_pages * 8;
-#pragma unroll 1
-        for (int a = 0; a < kAtoms; ++a) {
-          const uint32_t m8 = uint32_t(rows >> (8 * a)) & 0xffu;
-          if (m8 == 0xffu || m8 == 0) {
-            tma_load_4d_pair(dst + a * kBlocks * 1024, tm_va, full, 0, 0, block, m8 ? atom + a : none);
-            continue;
-          }
-#pragma unroll 1
-          for (int k = 0; k < 8 * kBlocks; ++k) {
-            const int rr = k & 7, bl = k >> 3;
-            tma_load_4d_pair(dst + a * kBlocks * 1024 + bl * 1024 + rr * 128, tm_vr, full, 0, rr, block + bl,
-                             (m8 >> rr) & 1u ? atom + a : none);
-          }
-        }
+        const int block = (F8 ? 2 : 4) * int(rank), atom = page[i] * 8 + 4 * h;
+        if (KIND == kWhole || whole) tma_load_4d_pair(dst, tm_v, full, 0, 0, block, atom);
+        else load_seen<F8>(dst, full, tm_v, tm_va, tm_vr, block, atom, p.num_pages * 8, seen[i] >> (32 * h));
       }
     }
     return true;
   };
   // c: the next tile to load K of; its pages are read a tile early, so that
   // their latency hides behind the units of the tile before
-  TileWalk<F8, WIN> c(p, r);
-  int last[kTilePages];  // pages of the tile whose V comes next, and their seen rows (WIN)
+  TileWalk<F8, KIND> c(p, r);
+  int last[kTilePages];  // pages of the tile whose V comes next, and their seen rows
   unsigned long long lseen[kTilePages] = {0, 0, 0, 0};
-  bool have = false;
+  bool have = false, lwhole = true;
   while (ok && (c.live || have)) {
     int pages[kTilePages];
     unsigned long long seen[kTilePages] = {0, 0, 0, 0};
+    bool whole = true;
     const bool more = c.live;
     if (F8 && have && more && c.first()) {
-      ok = load_v(last, lseen);
+      ok = load_v(last, lseen, lwhole);
       have = false;
       if (!ok) break;
     }
     if (more) {
       c.check(err);
 #pragma unroll
-      for (int i = 0; i < kTilePages; ++i) {
-        pages[i] = c.page[i];
-        if (WIN) seen[i] = c.seen(i);
+      for (int i = 0; i < kTilePages; ++i) pages[i] = c.page[i];
+      if (KIND != kWhole) {
+        whole = c.whole();
+        if (!whole) {
+#pragma unroll
+          for (int i = 0; i < kTilePages; ++i) seen[i] = c.seen(i);
+        }
       }
       ok = load_k(c);
       c.step();
     }
-    if (ok && have) ok = load_v(last, lseen);
+    if (ok && have) ok = load_v(last, lseen, lwhole);
 #pragma unroll
     for (int i = 0; i < kTilePages; ++i) {
       last[i] = pages[i];
       lseen[i] = seen[i];
     }
     have = more;
+    lwhole = whole;
   }
   if (!ok) atomicOr(err, kErrTimeout);
 }
@@ -340,7 +364,7 @@ __device__ __forceinline__ bool warp_wait(uint32_t b, uint32_t parity, volatile 
   return __all_sync(0xffffffffu, mbar_wait_clk(b, parity, abort, kTimeoutClk));
 }
 
-template <bool F8, bool WIN>
+template <bool F8, int KIND>
 __device__ __forceinline__ void score_mmas(const DecodeParams &p, const CtaRange &r, Misc &m, uint32_t sQ,
                                            uint32_t sRing, uint32_t tmem, int *err) {
   volatile int *abort = &m.abort;
@@ -352,7 +376,7 @@ __device__ __forceinline__ void score_mmas(const DecodeParams &p, const CtaRange
   uint32_t n = 0;
   uint32_t q_it = 0;
   bool ok = true;
-  for (Pieces<F8, WIN> w(p, r); ok && w.next(); w.advance()) {
+  for (Pieces<F8, KIND> w(p, r); ok && w.next(); w.advance()) {
     for (long long t = w.t0; ok && t < w.t1; ++t, ++n) {
       const int b = int(n & 1);
       ok = warp_wait(bar(m.s_free[b]), ((n >> 1) & 1) ^ 1, abort);
@@ -401,7 +425,7 @@ __device__ __forceinline__ void score_mmas(const DecodeParams &p, const CtaRange
   __syncwarp();
 }
 
-template <bool F8, bool WIN>
+template <bool F8, int KIND>
 __device__ __forceinline__ void pv_mmas(const DecodeParams &p, const CtaRange &r, Misc &m, uint32_t sP,
                                         uint32_t sRing, uint32_t tmem, int *err) {
   volatile int *abort = &m.abort;
@@ -411,12 +435,12 @@ __device__ __forceinline__ void pv_mmas(const DecodeParams &p, const CtaRange &r
   // V, MN-major: 128-byte blocks of dims 1 KB apart, 8-token groups 4 KB (bf16)
   // or 2 KB (e4m3) apart
   const uint64_t dv = smem_desc_sw128(sRing, 1024, F8 ? 2048 : 4096);
-  const uint32_t total = total_tiles<F8, WIN>(p, r);
+  const uint32_t total = total_tiles<F8, KIND>(p, r);
   Landed landed;
   uint32_t n = 0;
   uint32_t o_it = 0;
   bool ok = true;
-  for (Pieces<F8, WIN> w(p, r); ok && w.next(); w.advance(), ++o_it) {
+  for (Pieces<F8, KIND> w(p, r); ok && w.next(); w.advance(), ++o_it) {
     for (long long t = w.t0; ok && t < w.t1; ++t, ++n) {
       ok = warp_wait(bar(m.o_ready[n & 1]), (n >> 1) & 1, abort);
       if (ok && t == w.t0) ok = warp_wait(bar(m.o_free), (o_it & 1) ^ 1, abort);
@@ -555,7 +579,7 @@ __device__ __forceinline__ bool split_q(const DecodeParams &p, Misc &m, unsigned
 
 // A failed wait never leaves the loop: the warp goes on without working, so
 // that the others find it at their barriers (later waits fail at once).
-template <bool F8, bool WIN>
+template <bool F8, int KIND>
 __device__ __forceinline__ void softmax(const DecodeParams &p, const CtaRange &r, Misc &m, unsigned char *smem,
                                         uint32_t tmem, uint32_t rank, int pair_id, int *err) {
   volatile int *abort = &m.abort;
@@ -575,7 +599,7 @@ __device__ __forceinline__ void softmax(const DecodeParams &p, const CtaRange &r
   uint32_t n = 0;
   uint32_t o_it = 0;
   bool ok = true;
-  for (Pieces<F8, WIN> w(p, r); w.next(); w.advance(), ++o_it) {
+  for (Pieces<F8, KIND> w(p, r); w.next(); w.advance(), ++o_it) {
     const int grow = w.view.row0 + int(rank) * kRows + row;
     const RowView rv = row_view(p, w.view, min(grow, p.batch * p.heads - 1));
     const bool mine = int(rank) * kRows + row < w.view.rows;
@@ -615,7 +639,7 @@ __device__ __forceinline__ void softmax(const DecodeParams &p, const CtaRange &r
 #pragma unroll
         for (int i = 0; i < 64; ++i) x[i] = i < left ? x[i] : -INFINITY;
       }
-      if constexpr (WIN) {
+      if constexpr (KIND == kWindow) {
         const int skip = rv.lo - base, sink = p.sinks - base;
         if (skip > 0 && sink < kPage) {
 #pragma unroll
@@ -706,12 +730,12 @@ __device__ __forceinline__ void softmax(const DecodeParams &p, const CtaRange &r
     ok = ok && __all_sync(0xffffffffu, mbar_wait_clk(bar(m.o_full), o_it & 1, abort, kTimeoutClk));
     const int c_first = sched_owner_short(w.pv, r.total, r.g_eff);
     const int pieces = sched_owner_short(w.pv + w.tiles - 1, r.total, r.g_eff) - c_first + 1;
-    const bool split = !WIN || pieces > 1;
-    // shared pages: every piece leaves a partial, in the slots of its pair and
-    // block; a window's do when the block is cut, in the slots of the split
-    // merge, its CTA r * pairs + c standing for half r of pair c
-    const size_t slot = WIN ? 2 * size_t(rank * p.pairs + pair_id) + (w.v != r.v_begin ? 1 : 0)
-                            : 2 * size_t(pair_id + w.v) + rank;
+    const bool split = KIND != kWindow || pieces > 1;
+    // shared pages and tails: every piece leaves a partial, in the slots of its
+    // pair and block; a window's do when the block is cut, in the slots of the
+    // split merge, its CTA r * pairs + c standing for half r of pair c
+    const size_t slot = KIND == kWindow ? 2 * size_t(rank * p.pairs + pair_id) + (w.v != r.v_begin ? 1 : 0)
+                                        : 2 * size_t(pair_id + w.v) + rank;
     if (ok) {
       tc_fence_after();
       const int d0 = 256 * (q >> 1) + 128 * g;
@@ -751,12 +775,12 @@ __device__ __forceinline__ void softmax(const DecodeParams &p, const CtaRange &r
         else p.lse[grow] = lse_out(p, lse2);
       }
       if (st == 0 && pair_id == c_first) {
-        if (WIN) {  // the record of this half's 64 rows
+        if (KIND == kWindow) {  // the record of this half's 64 rows
           if (w.view.rows > int(rank) * kRows)
             info_ptr(p)[(2 * (w.v / p.batch) + int(rank)) * p.batch + w.v % p.batch] =
                 make_int4(int(rank) * p.pairs + c_first, pieces, int(slot), 0);
         } else if (rank == 0) {
-          info_ptr(p)[p.batch * p.head_groups + w.v] = make_int4(c_first, pieces, pair_id + w.v, 0);
+          pair_info_ptr(p)[w.v] = make_int4(c_first, pieces, pair_id + w.v, 0);
         }
       }
     }
@@ -764,7 +788,7 @@ __device__ __forceinline__ void softmax(const DecodeParams &p, const CtaRange &r
   if (!ok) atomicOr(err, kErrTimeout);
 }
 
-template <bool F8, bool WIN>
+template <bool F8, int KIND>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     decode_pair_kernel(const __grid_constant__ DecodeParams p, const __grid_constant__ CUtensorMap tm_q,
                        const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_k4,
@@ -820,9 +844,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   }
   asm volatile("griddepcontrol.wait;" ::: "memory");
   // blocks without pages: no partials, or the neutral pair
-  if constexpr (WIN) {
+  if constexpr (KIND == kWindow) {
     for (int v = int(blockIdx.x); v < p.pair_blocks; v += int(gridDim.x)) {
-      const ViewReq w = window_block<kPairRows>(p, v);
+      const ViewReq w = request_block<kPairRows>(p, v);
       if (tid == 0) checked_len(p, w.req, err);
       if (w.tiles != 0) continue;
       if (tid < 2 && w.rows > tid * kRows)
@@ -833,10 +857,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     }
   } else {
     for (int v = int(blockIdx.x) * kThreads + tid; v < p.pair_blocks; v += int(gridDim.x) * kThreads)
-      if (block_tiles<WIN>(p, v) == 0) info_ptr(p)[p.batch * p.head_groups + v] = make_int4(-1, 0, 0, 0);
+      if (block_tiles<KIND>(p, v) == 0) pair_info_ptr(p)[v] = make_int4(-1, 0, 0, 0);
+    if (KIND == kTails)
+      for (int b = int(blockIdx.x) * kThreads + tid; b < p.batch; b += int(gridDim.x) * kThreads)
+        check_view(p, b, err);
   }
-  schedule_range<Cfg<F8>::kPieceTiles, true>(
-      p.pair_blocks, pair_id, p.pairs, [&](int v) { return block_tiles<WIN>(p, v); }, &m.range, m.scratch);
+  schedule_range<kPieceTiles<F8, KIND>, true>(
+      p.pair_blocks, pair_id, p.pairs, [&](int v) { return block_tiles<KIND>(p, v); }, &m.range, m.scratch);
   tc_fence_before();
   cluster_sync();  // both CTAs' barriers and TMEM are ready
   tc_fence_after();
@@ -846,14 +873,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   if (r.start < r.end) {
     if (warp == 0) {
       if (lane == 0)
-        produce<F8, WIN>(p, r, m, sbase + kOffQ, sbase + kOffRing, rank, &tm_q, &tm_k, &tm_k4, &tm_v, &tm_va,
+        produce<F8, KIND>(p, r, m, sbase + kOffQ, sbase + kOffRing, rank, &tm_q, &tm_k, &tm_k4, &tm_v, &tm_va,
                          &tm_vr, err);
     } else if (warp == 1) {
-      if (rank == 0) score_mmas<F8, WIN>(p, r, m, sbase + kOffQ, sbase + kOffRing, tmem, err);
+      if (rank == 0) score_mmas<F8, KIND>(p, r, m, sbase + kOffQ, sbase + kOffRing, tmem, err);
     } else if (warp == 2) {
-      if (rank == 0) pv_mmas<F8, WIN>(p, r, m, sbase + kOffP, sbase + kOffRing, tmem, err);
+      if (rank == 0) pv_mmas<F8, KIND>(p, r, m, sbase + kOffP, sbase + kOffRing, tmem, err);
     } else if (warp >= 4) {
-      softmax<F8, WIN>(p, r, m, smem, tmem, rank, pair_id, err);
+      softmax<F8, KIND>(p, r, m, smem, tmem, rank, pair_id, err);
     }
     // no MMA may still read this CTA's shared memory, and no copy write it:
     // the MMAs waited for every copy unless a wait gave up
@@ -878,10 +905,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   cluster_sync();  // the pair leaves together: neither SM takes another CTA before both gave up their TMEM
 }
 
-template <bool F8, bool WIN>
+template <bool F8, int KIND>
 cudaError_t launch(const DecodeParams &p, const CUtensorMap &tm_q, const PairMaps &m, cudaStream_t stream) {
   static SmemLimitOnce smem_limit;
-  const cudaError_t e = smem_limit.ensure(decode_pair_kernel<F8, WIN>, smem_bytes<F8>());
+  const cudaError_t e = smem_limit.ensure(decode_pair_kernel<F8, KIND>, smem_bytes<F8>());
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(2 * p.pairs);
@@ -893,21 +920,30 @@ cudaError_t launch(const DecodeParams &p, const CUtensorMap &tm_q, const PairMap
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, decode_pair_kernel<F8, WIN>, p, tm_q, m.k, m.k4, m.v, m.va, m.vr);
+  return cudaLaunchKernelEx(&cfg, decode_pair_kernel<F8, KIND>, p, tm_q, m.k, m.k4, m.v, m.va, m.vr);
 }
 
 }  // namespace
 
-// tm_q is read for a bf16 cache, m.k4 for an e4m3 one.  A window's split merge
-// follows here; the shared pages' partials wait for the tails.
+// Launched after the pair kernel: the merge of the cut blocks of windows, or of the
+// shared pages' and the tails' partials.  (Without the tails here, those follow
+// in the other kernel, and the merge after them.)
 cudaError_t launch_split_merge(const DecodeParams &p, int grid, cudaStream_t stream);
+cudaError_t launch_shared_merge(const DecodeParams &p, int grid, cudaStream_t stream);
 
+// tm_q is read for a bf16 cache, m.k4 for an e4m3 one.
 cudaError_t launch_decode_pair(const DecodeParams &p, const CUtensorMap &tm_q, const PairMaps &m,
                                cudaStream_t stream) {
-  if (p.view == kViewShared)
-    return p.kv_e4m3 ? launch<true, false>(p, tm_q, m, stream) : launch<false, false>(p, tm_q, m, stream);
-  const cudaError_t e = p.kv_e4m3 ? launch<true, true>(p, tm_q, m, stream) : launch<false, true>(p, tm_q, m, stream);
-  return e == cudaSuccess ? launch_split_merge(p, 2 * p.pairs, stream) : e;
+  const bool f8 = p.kv_e4m3 != 0;
+  if (p.view == kViewWindow) {
+    const cudaError_t e = f8 ? launch<true, kWindow>(p, tm_q, m, stream) : launch<false, kWindow>(p, tm_q, m, stream);
+    return e == cudaSuccess ? launch_split_merge(p, 2 * p.pairs, stream) : e;
+  }
+  if (p.pair_tails) {
+    const cudaError_t e = f8 ? launch<true, kTails>(p, tm_q, m, stream) : launch<false, kTails>(p, tm_q, m, stream);
+    return e == cudaSuccess ? launch_shared_merge(p, 2 * p.pairs, stream) : e;
+  }
+  return f8 ? launch<true, kWhole>(p, tm_q, m, stream) : launch<false, kWhole>(p, tm_q, m, stream);
 }
 
 }  // namespace mla

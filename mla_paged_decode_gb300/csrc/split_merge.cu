@@ -228,26 +228,27 @@ __global__ void __launch_bounds__(kMergeWarps * 32, 7) shared_merge_kernel(Decod
   const int local = row - group_start(p, g) * p.heads;
   // slots of the two sets: first, stride, number; the row's place in them
   int first[2] = {0, 0}, num[2] = {0, 0}, hl[2] = {local & 63, r & 63};
-  const int stride = p.pair_blocks ? 2 : 1;  // a pair's piece has a slot per CTA
-  const int V = p.batch * p.head_groups + p.prefix_blocks;
+  const int stride[2] = {p.pair_blocks ? 2 : 1, p.pair_tails ? 2 : 1};  // a pair's piece has a slot per CTA
   if (local >= 0) {
-    const int blocks = p.pair_blocks ? p.pair_blocks : p.prefix_blocks;
+    const int blocks = p.pair_blocks ? p.pair_blocks - p.pair_tails : p.prefix_blocks;
     const int v = p.pair_blocks ? block_base<128>(p, g) + (local >> 7) : block_base<64>(p, g) + (local >> 6);
     if (v < blocks) {
-      const int4 i = info_ptr(p)[p.pair_blocks ? V + v : v];
-      if (i.y > 0 && i.z >= 0 && (i.z + i.y) * stride <= slots)
-        first[0] = i.z * stride + ((local >> 6) & (stride - 1)), num[0] = i.y;
+      const int4 i = p.pair_blocks ? pair_info_ptr(p)[v] : info_ptr(p)[v];
+      if (i.y > 0 && i.z >= 0 && (i.z + i.y) * stride[0] <= slots)
+        first[0] = i.z * stride[0] + ((local >> 6) & (stride[0] - 1)), num[0] = i.y;
     }
   }
   {
-    const int4 i = info_ptr(p)[p.prefix_blocks + (r >> 6) * p.batch + b];
-    if (i.y > 0 && i.z >= 0 && i.z + i.y <= slots) first[1] = i.z, num[1] = i.y;
+    const int4 i = p.pair_tails ? pair_info_ptr(p)[p.pair_blocks - p.pair_tails + (r >> 7) * p.batch + b]
+                                : info_ptr(p)[p.prefix_blocks + (r >> 6) * p.batch + b];
+    if (i.y > 0 && i.z >= 0 && (i.z + i.y) * stride[1] <= slots)
+      first[1] = i.z * stride[1] + ((r >> 6) & (stride[1] - 1)), num[1] = i.y;
   }
   const int ns = num[0] + num[1];
   const float *sl = slot_lse_ptr(p);
   const float *so = slot_out_ptr(p);
   auto at = [&](int k) {
-    const int s = k < num[0] ? first[0] + k * stride : first[1] + k - num[0];
+    const int s = k < num[0] ? first[0] + k * stride[0] : first[1] + (k - num[0]) * stride[1];
     return size_t(s) * kSlotHeads + hl[k < num[0] ? 0 : 1];
   };
   // the first partials' loads go out before the weights are known
@@ -325,7 +326,7 @@ cudaError_t launch_shared_merge(const DecodeParams &p, int grid, cudaStream_t st
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  const int slots = pair_slots(p) + p.batch * p.head_groups + p.prefix_blocks + grid;
+  const int slots = pair_slots(p) + (p.pair_tails ? 0 : p.batch * p.head_groups + p.prefix_blocks + grid);
   return wide ? cudaLaunchKernelEx(&cfg, shared_merge_kernel<true>, p, slots)
               : cudaLaunchKernelEx(&cfg, shared_merge_kernel<false>, p, slots);
 }

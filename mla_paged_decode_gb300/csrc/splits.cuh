@@ -38,6 +38,10 @@ __device__ __forceinline__ float *slot_out_ptr(const DecodeParams &p) {
 __device__ __forceinline__ int4 *info_ptr(const DecodeParams &p) {
   return reinterpret_cast<int4 *>(p.ws + p.wl.info);
 }
+// Records of the pair kernel's blocks: after those of the other kernel's tails.
+__device__ __forceinline__ int4 *pair_info_ptr(const DecodeParams &p) {
+  return info_ptr(p) + (p.pair_tails ? 0 : p.batch * p.head_groups);
+}
 __device__ __forceinline__ int *error_word(const DecodeParams &p) {
   return reinterpret_cast<int *>(p.ws);
 }
