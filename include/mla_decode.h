@@ -382,7 +382,9 @@ int mla_lse_combine(const void *partials, const float *lses, int num_parts, void
  * queries' views hold does not matter; a row that only some of its q_len
  * queries see must be finite.  Arithmetic and errors as for
  * mla_decode_partial, except that lse takes the unrounded softmax weights of
- * a bf16 cache too.  Two kernels.
+ * a bf16 cache too.  Requests of more than 64 rows (q_len x num_heads) take
+ * blocks of 128 rows on pairs of SMs, with a bf16 cache when batch x rows x
+ * tokens in view reach 512 K.  Two kernels.
  */
 int mla_decode_window(const void *q, const void *kv_pages, const int32_t *block_table,
                       const int32_t *seq_lens, int window, int sinks, float sm_scale, int lse_base,
@@ -411,7 +413,8 @@ int mla_decode_window(const void *q, const void *kv_pages, const int32_t *block_
  * the shared pages in blocks, each request's rows to its own pages, and the
  * partial results are merged by their LSE.  Groups of 128 rows or more on
  * average take blocks of 128 rows on pairs of SMs when rows x tokens (64 *
- * max_pages_per_seq) reach 16 M.  The shared pages' rows must be finite, also
+ * max_pages_per_seq) reach 16 M, and then also the requests' own pages when a
+ * request has more than 64 rows.  The shared pages' rows must be finite, also
  * where a shorter request does not see them.  A request outside every group
  * or a page number outside [0, max_pages_per_seq] is reported as
  * MLA_ERR_BOUNDS by mla_decode_check_workspace.  Arithmetic as for

@@ -558,10 +558,10 @@ mla::WorkspaceLayout shared_layout(const mla_decode_desc *d, int num_groups, int
 // which rows x tokens in view (at most) have to make up for.  Measured, us a
 // call, pair kernel / blocks of 64 rows, bf16, rows x requests, window: 128 x 8,
 // 128 (0.1 M) 17.2 / 15.3; 192 x 8, 128 21.8 / 19.5; 128 x 32, 128 (0.5 M)
-// 18.0 / 21.5; 128 x 1, 4096 22.4 / 35.1; 192 x 8, 512 (0.8 M) 23.2 / 20.7;
-// 128 x 128, 512 57.6 / 64.5; 192 x 128, 4096 292 / 349; 512 x 128, 4096
-// 550 / 868; e4m3: 20.2 / 23.1, 20.2 / 26.4, 20.3 / 29.7, 25.0 / 42.6,
-// 23.5 / 29.8, 60.6 / 80.6, 252 / 312, 465 / 731.
+// 17.5 / 21.5; 65 x 32, 4096 60.9 / 72.6; 128 x 1, 4096 22.4 / 35.1; 192 x 8, 512
+// (0.8 M) 22.8 / 20.7; 128 x 128, 512 54.7 / 64.5; 192 x 128, 4096 268 / 349; 512 x
+// 128, 4096 498 / 868; e4m3: 19.8 / 23.1, 19.6 / 26.4, 20.1 / 29.7, 54.6 / 82.0,
+// 24.3 / 42.6, 23.3 / 29.8, 60.1 / 80.6, 229 / 312, 427 / 731.
 constexpr long long kWindowPairWork = 1LL << 19;
 bool window_pair_path(const mla_decode_desc *d, int window, int sinks) {
   if (rows_of(d) <= kTcHeadsPerGroup) return false;
@@ -980,6 +980,11 @@ int mla_decode_shared(const void *q, const void *kv_pages, const int32_t *block_
   p.shared_pages = shared_pages;
   p.num_groups = num_groups;
   if (pair_path(d, num_groups)) {
+    // the tails of requests with more than one block of 64 rows go along, a launch
+    // less and the pair kernel's rate; us a call, tails along / in the other kernel,
+    // bf16: 256 rows x 39 requests, 131 shared pages + 700 tokens 160 / 178, 128 x 64,
+    // 128 + 1500 136 / 166, + 1 134 / 138, 512 x 32, 400 + 1 626 / 610, + 1500
+    // 664 / 660; e4m3: 136 / 174, 123 / 161, 120 / 146, 512 / 529, 575 / 590
     if (rows_of(d) > kTcHeadsPerGroup) p.pair_tails = d->batch * ((rows_of(d) + 127) / 128);
     p.pair_blocks = shared_blocks(d, num_groups, 128) + p.pair_tails;
     p.pairs = f.sms / 2;

@@ -311,8 +311,8 @@ __device__ inline ViewReq shared_block(const DecodeParams &p, int v) {
 }
 
 // Block u / B of R rows of request u mod B: through the window and the sinks, or
-// over the request's own pages.
-template <int R = 64>
+// over the request's own pages (VIEW: p.view where the caller knows it).
+template <int R = 64, int VIEW = 0>
 __device__ inline ViewReq request_block(const DecodeParams &p, int u) {
   ViewReq r;
   const int b = u % p.batch, g = u / p.batch;
@@ -321,7 +321,7 @@ __device__ inline ViewReq request_block(const DecodeParams &p, int u) {
   r.rows = min(R, p.heads - R * g);
   const int L = checked_len(p, b, nullptr);
   r.end = row_len(p, L, min(p.heads, R * (g + 1)) - 1);
-  if (p.view == kViewShared) {
+  if ((VIEW ? VIEW : p.view) == kViewShared) {
     r.first = group_shared_pages(p, group_of_request(p, b));
     r.tiles = max(0, (r.end + kPage - 1) / kPage - r.first);
     return r;
