@@ -102,17 +102,28 @@ using namespace pair;
 __device__ __forceinline__ uint32_t bar(uint64_t &b) { return smem_u32(&b); }
 
 // Block v of 128 rows: of a group's rows over its shared pages, of a request's
-// rows over its own pages, or of a request's rows through its window.  A call, not
-// inlined into the four roles: 3 to 8 % faster with an e4m3 cache (384 rows x 32
-// requests, window 2000: 70.5 us, inlined 73.8), the same with bf16.
+// rows over its own pages, or of a request's rows through its window.
 template <int KIND>
-static __device__ __noinline__ ViewReq block_view(const DecodeParams &p, int v) {
+__device__ __forceinline__ ViewReq make_view(const DecodeParams &p, int v) {
   if constexpr (KIND == kWindow) return request_block<kPairRows, kViewWindow>(p, v);
   if constexpr (KIND == kTails) {
     const int shared = p.pair_blocks - p.pair_tails;
     if (v >= shared) return request_block<kPairRows, kViewShared>(p, v - shared);
   }
   return shared_block<kPairRows>(p, v);
+}
+template <int KIND>
+static __device__ __noinline__ ViewReq view_call(const DecodeParams &p, int v) {
+  return make_view<KIND>(p, v);
+}
+// A call for the larger kinds, not inlined into the four roles: 3 to 8 % faster with
+// an e4m3 cache (384 rows x 32 requests, window 2000: 70.5 us, inlined 73.8), the
+// same with bf16.  Shared pages alone: inlined, 231 us against 235 (bf16, 4096
+// rows over 32K shared tokens).
+template <int KIND>
+__device__ __forceinline__ ViewReq block_view(const DecodeParams &p, int v) {
+  if constexpr (KIND == kWhole) return make_view<KIND>(p, v);
+  else return view_call<KIND>(p, v);
 }
 template <int KIND>
 __device__ __forceinline__ int block_tiles(const DecodeParams &p, int v) {
