@@ -382,7 +382,10 @@ int mla_lse_combine(const void *partials, const float *lses, int num_parts, void
  * queries' views hold does not matter; a row that only some of its q_len
  * queries see must be finite.  Arithmetic and errors as for
  * mla_decode_partial, except that lse takes the unrounded softmax weights of
- * a bf16 cache too.  Requests of more than 64 rows (q_len x num_heads) take
+ * a bf16 cache too, and that with an e4m3 cache each row's q has a 2^k of its
+ * own: the two terms are exact for elements down to 2^-9 of the row's largest
+ * |q|, whatever the other rows hold, and a row with an Inf or a NaN that sees a
+ * token gives NaN.  Requests of more than 64 rows (q_len x num_heads) take
  * blocks of 128 rows on pairs of SMs, with a bf16 cache when batch x rows x
  * tokens in view reach 512 K.  Two kernels.
  */

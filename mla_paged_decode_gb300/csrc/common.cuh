@@ -599,6 +599,29 @@ __device__ __forceinline__ float2 e5m2x2_to_float2(uint16_t two) {
   return __half22float2(hh);
 }
 
+// The largest |x| of eight bf16 values, as two 16-bit lanes of bits without the
+// sign (which are ordered like the magnitudes).
+__device__ __forceinline__ uint32_t largest_bf16x8(uint4 v) {
+  return __vmaxu2(__vmaxu2(v.x & 0x7fff7fffu, v.y & 0x7fff7fffu), __vmaxu2(v.z & 0x7fff7fffu, v.w & 0x7fff7fffu));
+}
+
+// 2^k and 2^-k with which q enters as two e4m3 terms: the largest |q|, as bf16 bits
+// `mx`, comes to lie in [2^7, 2^8).  An Inf or NaN keeps k = 0.
+struct QScale {
+  float scale, inv;
+};
+__device__ __forceinline__ QScale q_scale(uint32_t mx) {
+  const int k = mx < 0x7f80u ? min(126, max(-126, 134 - int(mx >> 7))) : 0;
+  return QScale{__int_as_float((127 + k) << 23), __int_as_float((127 - k) << 23)};
+}
+// The same for a scale that one row has to itself: a row with an Inf or a NaN
+// turns into NaN (saturated to e4m3's range, an Inf would read as a number).
+__device__ __forceinline__ QScale row_q_scale(uint32_t mx) {
+  QScale s = q_scale(mx);
+  if (mx >= 0x7f80u) s.scale = __int_as_float(0x7fffffff);
+  return s;
+}
+
 __device__ __forceinline__ float2 e4m3x2_to_float2(uint16_t two) {
   uint32_t h = e4m3x2_to_f16x2(two);
   __half2 hh = *reinterpret_cast<__half2 *>(&h);

@@ -18,7 +18,7 @@
 //      (its half of N of the two PV products),
 // 17 units of 16 KB through one ring of seven; a page is read twice, from L2.
 // (e4m3 caches: five units of 128 dims and four of a page, Q and P as two fp8
-// terms each, with the decode kernel's arithmetic.)
+// terms each, with the arithmetic of the decode kernel's views.)
 //
 // Roles (384 threads): warp 0 producer, warp 1 score MMAs and TMEM, warp 2 PV
 // MMAs (both in the even CTA only), warps 4..11 softmax and epilogue.  Thread
@@ -87,7 +87,7 @@ struct Misc {
   uint32_t tmem_base;
   int abort;
   float red[2][4][kRows];  // row maxima by page, double-buffered; then row sums
-  uint32_t qmax[kSoftWarps];  // e4m3: largest |q| by warp
+  float qinv[kRows];          // e4m3: 2^-k of every row's Q
   CtaRange range;
   long long scratch[kThreads / 32 + 1];
 };
@@ -536,43 +536,51 @@ __device__ __forceinline__ void st_global_v8(float *dst, const float (&v)[8]) {
 }
 
 // e4m3: the block's Q rows of this CTA (bf16) as two e4m3 terms, hi + lo, of
-// 2^k q, with 2^k such that the largest |q| lies in [2^7, 2^8) (hi + lo is then
-// exact down to 2^-9 of it); rows past the block are zero.  All softmax threads,
-// once a piece, when the piece before has read Q.  2^-k goes to *qinv.
+// 2^k q, with a 2^k for each row such that its largest |q| lies in [2^7, 2^8) (hi +
+// lo is then exact down to 2^-9 of it).  The rows may be those of several requests:
+// with one 2^k for all of them, one request's queries would set the precision of
+// another's.  A row with an Inf or a NaN enters as NaN; rows past the block are
+// zero.  All softmax threads, a warp eight rows, once a piece, when the piece
+// before has read Q.  2^-k goes to m.qinv.
 __device__ __forceinline__ bool split_q(const DecodeParams &p, Misc &m, unsigned char *smem, const ViewReq &view,
-                                        uint32_t rank, int st, uint32_t piece, bool ok, float *qinv) {
-  constexpr int kChunks = kDqk / 8, kPer = kRows * kChunks / kSoftThreads;  // 8 dims each; 18 a thread
-  static_assert(kRows * kChunks % kSoftThreads == 0, "Q chunks");
+                                        uint32_t rank, int st, uint32_t piece, bool ok) {
+  constexpr int kChunks = kDqk / 8;                       // 8 dims each
+  constexpr int kWarpRows = kRows / kSoftWarps, kPer = kWarpRows * kChunks / 32;  // 8 rows; 18 chunks a lane
+  static_assert(kWarpRows * kChunks % 32 == 0, "Q chunks");
+  const int warp = st >> 5, lane = st & 31, first = warp * kWarpRows;
   const int rows = min(kRows, max(0, view.rows - int(rank) * kRows));
-  const uint4 *src = reinterpret_cast<const uint4 *>(p.q + (size_t(view.row0) + rank * kRows) * kDqk);
+  const uint4 *src = reinterpret_cast<const uint4 *>(p.q + (size_t(view.row0) + rank * kRows + first) * kDqk);
   uint4 v[kPer];
+  uint32_t mx[kPer];
 #pragma unroll
   for (int u = 0; u < kPer; ++u) {
-    const int i = st + u * kSoftThreads;
-    v[u] = i / kChunks < rows ? __ldg(src + i) : make_uint4(0, 0, 0, 0);
+    const int i = lane + 32 * u;
+    v[u] = first + i / kChunks < rows ? __ldg(src + i) : make_uint4(0, 0, 0, 0);
   }
-  uint32_t mx = 0;
 #pragma unroll
   for (int u = 0; u < kPer; ++u) {
-    mx = __vmaxu2(mx, v[u].x & 0x7fff7fffu);
-    mx = __vmaxu2(mx, v[u].y & 0x7fff7fffu);
-    mx = __vmaxu2(mx, v[u].z & 0x7fff7fffu);
-    mx = __vmaxu2(mx, v[u].w & 0x7fff7fffu);
+    mx[u] = largest_bf16x8(v[u]);
+    mx[u] = max(mx[u] & 0xffffu, mx[u] >> 16);
   }
-  mx = __reduce_max_sync(0xffffffffu, max(mx & 0xffffu, mx >> 16));
-  if ((st & 31) == 0) m.qmax[st >> 5] = mx;
-  named_sync(1, kSoftThreads);
+  // a row's chunks lie in the registers u of at most four rounds of loads
+  uint32_t row_mx[kWarpRows];
 #pragma unroll
-  for (int i = 0; i < kSoftWarps; ++i) mx = max(mx, m.qmax[i]);
-  int k = 0;  // (an Inf or NaN keeps 0)
-  if (mx < 0x7f80u) k = min(126, max(-126, 134 - int(mx >> 7)));
-  const float sc = __int_as_float((127 + k) << 23);
-  *qinv = __int_as_float((127 - k) << 23);
+  for (int w = 0; w < kWarpRows; ++w) {
+    uint32_t x = 0;
+#pragma unroll
+    for (int u = w * kChunks / 32; u <= ((w + 1) * kChunks - 1) / 32; ++u)
+      if ((lane + 32 * u) / kChunks == w) x = max(x, mx[u]);
+    row_mx[w] = __reduce_max_sync(0xffffffffu, x);
+    if (lane == 0) m.qinv[first + w] = row_q_scale(row_mx[w]).inv;
+  }
+  named_sync(1, kSoftThreads);  // (every thread reads its row's)
   ok = ok && __all_sync(0xffffffffu, mbar_wait_clk(bar(m.q_empty), (piece & 1) ^ 1, &m.abort, kTimeoutClk));
   if (!ok) return false;
 #pragma unroll
   for (int u = 0; u < kPer; ++u) {
-    const int i = st + u * kSoftThreads, rr = i / kChunks, c = i - kChunks * rr;
+    const int i = lane + 32 * u, w = i / kChunks, rr = first + w, c = i - kChunks * w;
+    const int w0 = 32 * u / kChunks, w1 = (32 * u + 31) / kChunks;  // the rows that round u of the loads meets
+    const float sc = row_q_scale(w == w0 ? row_mx[w0] : row_mx[w1]).scale;
     const uint32_t wv[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
     uint32_t hw[2] = {0, 0}, lw[2] = {0, 0};
 #pragma unroll
@@ -623,10 +631,9 @@ __device__ __forceinline__ void softmax(const DecodeParams &p, const CtaRange &r
     const RowView rv = row_view(p, w.view, min(grow, p.batch * p.heads - 1));
     const bool mine = int(rank) * kRows + row < w.view.rows;
     if constexpr (F8) {
-      float qinv;
-      ok = split_q(p, m, smem, w.view, rank, st, o_it, ok, &qinv);
+      ok = split_q(p, m, smem, w.view, rank, st, o_it, ok);
       if (ok && lane == 0) mbar_arrive_cluster(q_full);
-      cs = p.score_scale_log2 * p.kv_scale * qinv;
+      cs = p.score_scale_log2 * p.kv_scale * m.qinv[row];
     }
     float mrun = -INFINITY, ell = 0.f, ellx = 0.f;
     for (long long t = w.t0; t < w.t1; ++t, ++n) {

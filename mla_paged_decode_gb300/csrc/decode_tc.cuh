@@ -173,6 +173,10 @@ struct TcMisc {
   CtaRange range;
   ViewReq view0;                  // views only: the first piece's view
   long long scratch[tc::kThreadsF8 / 32 + 1];
+  // e4m3 views only: qinv and the largest |q| of every row (the latter by piece parity)
+  static constexpr int kRowScales = NS == 3 ? tc::kHeads : 1;
+  float row_qinv[4][kRowScales];
+  uint32_t row_qmax[2][kRowScales];
 };
 static_assert(sizeof(TcMisc<2>) + 1024 <= tc::kSmemBytes - tc::off_misc<false>(), "shared memory budget");
 static_assert(sizeof(TcMisc<3>) + 1024 <= tc::kSmemBytes - tc::off_misc<true>(), "shared memory budget");
@@ -883,7 +887,7 @@ __device__ __forceinline__ void tc_softmax(const TcParams &tp, const CtaRange &r
   const int row[2] = {16 * q + (lane >> 2), 16 * q + (lane >> 2) + 8};
   const int pair = 2 * (lane & 3);
   const uint32_t tq = tmem + (uint32_t(32 * q) << 16);
-  float cs = p.score_scale_log2 * p.kv_scale;
+  float cs[2] = {p.score_scale_log2 * p.kv_scale, p.score_scale_log2 * p.kv_scale};  // of the two rows
   uint32_t kv_it = 0, p_it = 0, o_it = 0;
   bool ok = true;
   // an owner mask: the gathered tiles hold other partitions' tokens too
@@ -906,7 +910,9 @@ __device__ __forceinline__ void tc_softmax(const TcParams &tp, const CtaRange &r
       __threadfence_block();
       const bool have = vv[slot] == w.v;
       if (!have) atomicOr(err, kErrTimeout);
-      cs = p.score_scale_log2 * p.kv_scale * (have ? m.qinv[slot] : 0.f);
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        cs[h] = p.score_scale_log2 * p.kv_scale * (!have ? 0.f : VIEW ? m.row_qinv[slot][row[h]] : m.qinv[slot]);
     }
     // owned tokens each of this lane's two rows sees (all w.n unless a request
     // carries several query tokens, each with its own causal bound)
@@ -1010,7 +1016,7 @@ __device__ __forceinline__ void tc_softmax(const TcParams &tp, const CtaRange &r
       for (int h = 0; h < 2; ++h) {
         tmax[h] = fmaxf(tmax[h], __shfl_xor_sync(0xffffffffu, tmax[h], 1));
         tmax[h] = fmaxf(tmax[h], __shfl_xor_sync(0xffffffffu, tmax[h], 2));
-        const float sm = tmax[h] * cs;  // cs > 0: the scaled maximum
+        const float sm = tmax[h] * cs[h];  // cs > 0: the scaled maximum
         mnew[h] = mrun[h];
         alpha[h] = 1.f;
         if (t == w.t0) {
@@ -1059,7 +1065,7 @@ __device__ __forceinline__ void tc_softmax(const TcParams &tp, const CtaRange &r
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           const float mref = MULTI && mnew[h] == -INFINITY ? 0.f : mnew[h] - kFxPLog2Scale;
-          const float2 c2 = make_float2(cs, cs), m2 = make_float2(-mref, -mref);
+          const float2 c2 = make_float2(cs[h], cs[h]), m2 = make_float2(-mref, -mref);
           unsigned char *prow = pst + (row[h] >> 3) * kFxPSbo + (row[h] & 7) * 16 + pair;
           float2 lsum = make_float2(0.f, 0.f), xsum = make_float2(0.f, 0.f);
 #pragma unroll
@@ -1090,7 +1096,7 @@ __device__ __forceinline__ void tc_softmax(const TcParams &tp, const CtaRange &r
                                 (row[h] >> 3) * atom_stride<KBG>() + (row[h] & 7) * 128 + (lane & 3) * 4;
           // a row that has seen no token yet keeps a -inf max: its P is 0
           const float mref = MULTI && mnew[h] == -INFINITY ? 0.f : mnew[h];
-          const float2 c2 = make_float2(cs, cs), m2 = make_float2(-mref, -mref);
+          const float2 c2 = make_float2(cs[h], cs[h]), m2 = make_float2(-mref, -mref);
           float2 lsum = make_float2(0.f, 0.f), xsum = make_float2(0.f, 0.f);
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
@@ -1253,6 +1259,12 @@ __device__ __forceinline__ void tc_softmax(const TcParams &tp, const CtaRange &r
 // down to 2^-2 (below that e4m3's subnormal step, 2^-9, bounds the error), so
 // the scores keep bf16 Q's precision; 2^-k goes to the softmax through a
 // slot tagged with the request.
+//
+// A view's block of shared pages holds rows of several requests.  There each row
+// has a 2^k of its own, so that no request's queries set the precision of
+// another's, and a row with an Inf or a NaN enters as NaN throughout: its scores
+// are then NaN, as the definition's are, and those of the other rows untouched.
+
 // The largest |q| (as bf16 bits without the sign) of a piece's Q rows: the
 // three warps' loads go out 16 at a time.  (Asking L2 to keep these lines
 // for the split that reads them again measured slower: they crowd out the
@@ -1274,17 +1286,42 @@ __device__ __forceinline__ uint32_t piece_q_max(const DecodeParams &p,
       v[u] = i < n ? __ldg(qg + i) : make_uint4(0, 0, 0, 0);
     }
 #pragma unroll
-    for (int u = 0; u < 16; ++u) {
-      mx = __vmaxu2(mx, v[u].x & 0x7fff7fffu);
-      mx = __vmaxu2(mx, v[u].y & 0x7fff7fffu);
-      mx = __vmaxu2(mx, v[u].z & 0x7fff7fffu);
-      mx = __vmaxu2(mx, v[u].w & 0x7fff7fffu);
-    }
+    for (int u = 0; u < 16; ++u) mx = __vmaxu2(mx, largest_bf16x8(v[u]));
   }
   mx = __reduce_max_sync(0xffffffffu, max(mx & 0xffffu, mx >> 16));
   if ((ct & 31) == 0) m.conv_max[ct >> 5] = mx;
   named_sync(3, kConvThreads);
   return max(m.conv_max[0], max(m.conv_max[1], m.conv_max[2]));
+}
+
+// The same of each of a view's rows, a warp a row (0 past the block's rows).
+template <bool FUSED, int MULTI>
+__device__ __forceinline__ void row_q_max(const DecodeParams &p, const Walk<FUSED, MULTI, kPieceCostE4m3> &w,
+                                          uint32_t *row_max, int ct) {
+  using namespace tc;
+  constexpr int kRowChunks = kDqk / 8, kWarps = kConvThreads / 32;
+  constexpr int kBatch = 5, kLoads = (kRowChunks + 31) / 32;  // 15 loads in flight
+  const int lane = ct & 31, hn = w.rows();
+  const uint4 *qg = reinterpret_cast<const uint4 *>(p.q + size_t(w.q_row0()) * kDqk);
+  for (int r0 = ct >> 5; r0 < kHeads; r0 += kWarps * kBatch) {
+    uint4 v[kBatch][kLoads];
+#pragma unroll
+    for (int b = 0; b < kBatch; ++b)
+#pragma unroll
+      for (int j = 0; j < kLoads; ++j) {
+        const int rr = r0 + kWarps * b, c = lane + 32 * j;
+        v[b][j] = rr < hn && c < kRowChunks ? __ldg(qg + rr * kRowChunks + c) : make_uint4(0, 0, 0, 0);
+      }
+#pragma unroll
+    for (int b = 0; b < kBatch; ++b) {
+      uint32_t mx = 0;
+#pragma unroll
+      for (int j = 0; j < kLoads; ++j) mx = __vmaxu2(mx, largest_bf16x8(v[b][j]));
+      mx = __reduce_max_sync(0xffffffffu, max(mx & 0xffffu, mx >> 16));
+      const int rr = r0 + kWarps * b;
+      if (lane == 0 && rr < kHeads) row_max[rr] = mx;
+    }
+  }
 }
 
 // Warps 9..11, once per request piece: the piece's largest |q| is taken
@@ -1306,20 +1343,24 @@ __device__ __forceinline__ void tc_split_q(const TcParams &tp, const CtaRange &r
   bool ok = true;
   Walk<FUSED, MULTI, kPieceCostE4m3> w(p, r, &m.view0), wa(p, r, &m.view0);  // wa: the piece after w
   bool ahead = wa.next();
-  uint32_t mx = ahead ? piece_q_max(p, wa, m, ct) : 0u;
-  if (ahead) {
+  uint32_t mx = 0;
+  // the largest |q| of piece `it`, which wa is at (a view's: of its rows, where
+  // the sync at the start of that piece makes them visible)
+  auto look_ahead = [&](uint32_t it) {
+    if (!ahead) return;
+    if constexpr (MULTI == 3) row_q_max(p, wa, m.row_qmax[it & 1], ct);
+    else mx = piece_q_max(p, wa, m, ct);
     wa.advance();
     ahead = wa.next();
-  }
+  };
+  look_ahead(0);
   for (; w.next(); w.advance(), ++q_it) {
     const bool got = mbar_wait(bar_addr(m.q_empty), (q_it & 1) ^ 1, abort, kTimeoutNs);
     if (!named_sync_and(3, kConvThreads, got)) { ok = false; break; }
     const int hn = w.rows();
     const uint4 *qg = reinterpret_cast<const uint4 *>(p.q + size_t(w.q_row0()) * kDqk);
-    // |q| bits are ordered like magnitudes; an Inf or NaN keeps k = 0
-    int k = 0;
-    if (mx < 0x7f80u) k = min(126, max(-126, 134 - int(mx >> 7)));
-    const float sc = __int_as_float((127 + k) << 23);
+    const QScale piece_scale = q_scale(mx);
+    const uint32_t *row_max = m.row_qmax[q_it & 1];
 #pragma unroll 1
     for (int u0 = 0; u0 < kPer; u0 += 16) {
       uint4 v[16];
@@ -1332,6 +1373,8 @@ __device__ __forceinline__ void tc_split_q(const TcParams &tp, const CtaRange &r
       for (int u = 0; u < 16; ++u) {
         const int i = ct + (u0 + u) * kConvThreads;
         const int rr = i / kRowChunks, c = i - kRowChunks * rr;
+        float sc = piece_scale.scale;
+        if constexpr (MULTI == 3) sc = row_q_scale(row_max[rr]).scale;
         const uint32_t wv[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
         uint32_t hw[2] = {0, 0}, lw[2] = {0, 0};
 #pragma unroll
@@ -1352,20 +1395,22 @@ __device__ __forceinline__ void tc_split_q(const TcParams &tp, const CtaRange &r
         *reinterpret_cast<uint2 *>(smem + kFxQTerm + off) = make_uint2(lw[0], lw[1]);
       }
     }
+    if constexpr (MULTI == 3) {
+      if (ct < 32) {
+        for (int rr = ct; rr < kHeads; rr += 32) m.row_qinv[q_it & 3][rr] = row_q_scale(row_max[rr]).inv;
+        __threadfence_block();
+        __syncwarp();
+      }
+    }
     if (ct == 0) {
-      m.qinv[q_it & 3] = __int_as_float((127 - k) << 23);
+      if (MULTI != 3) m.qinv[q_it & 3] = piece_scale.inv;
       __threadfence_block();
       reinterpret_cast<volatile int *>(m.qinv_v)[q_it & 3] = w.v;
     }
     fence_proxy_async_smem();
     __syncwarp();
     if (lane == 0) mbar_arrive(bar_addr(m.q_ready));
-    // the next piece's largest |q|, while this one runs
-    mx = ahead ? piece_q_max(p, wa, m, ct) : 0u;
-    if (ahead) {
-      wa.advance();
-      ahead = wa.next();
-    }
+    look_ahead(q_it + 1);  // the next piece's largest |q|, while this one runs
   }
   if (!ok) atomicOr(err, kErrTimeout);
 }
