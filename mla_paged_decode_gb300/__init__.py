@@ -2,8 +2,9 @@
 
 Argument marshalling only: every step of the computation runs in the CUDA
 kernels of ``_lib/libmla_decode.so``.  PyTorch supplies device memory and the
-current stream.  If the library is not built, every call raises: there is no
-CPU fallback.
+current stream (or the `stream` given to a call, which then also owns the
+workspace and outputs that the call allocates; the inputs have to be ready on
+it).  If the library is not built, every call raises: there is no CPU fallback.
 """
 from __future__ import annotations
 
@@ -160,6 +161,32 @@ def _stream_ptr(stream, device) -> int:
     return int(stream.cuda_stream) if stream is not None else _raw_stream(device.index)
 
 
+def _allocating_on(stream, device):
+    """The context in which a call that runs on `stream` allocates what it was
+    not given.  The caching allocator orders a block by the stream it was
+    allocated on: scratch from the current stream's pool, dropped when the call
+    returns, could go to that stream's next tensor while the kernels on
+    `stream` still use it, and its zero fill could run after them."""
+    if stream is None or int(stream.cuda_stream) == _raw_stream(device.index):
+        return _NO_SWITCH
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(stream.cuda_stream), device=device)
+    return torch.cuda.stream(stream)
+
+
+def _output(shape, dtype, device, stream):
+    """An output that the caller did not give: allocated on the call's stream
+    and kept, when it is dropped, until the current stream is done with it."""
+    where = _allocating_on(stream, device)
+    if where is _NO_SWITCH:
+        return torch.empty(shape, dtype=dtype, device=device)
+    current = torch.cuda.current_stream(device)
+    with where:
+        t = torch.empty(shape, dtype=dtype, device=device)
+    t.record_stream(current)
+    return t
+
+
 def _launch(fn, device, stream, *args):
     """fn(*args, stream) on the tensors' device; raises on a bad status."""
     s = _stream_ptr(stream, device)
@@ -261,7 +288,8 @@ def decode_partial(q, kv_pages, block_table, seq_lens, part_id: int, num_parts: 
     if out.numel() != d.batch * d.q_len * d.num_heads * 512 or lse.numel() != d.batch * d.q_len * d.num_heads:
         raise ValueError("out must be [B,1,H,512] and lse [B,1,H]")
     if workspace is None:
-        workspace = make_workspace(q, kv_pages, block_table, kv_scale)
+        with _allocating_on(stream, dev):
+            workspace = make_workspace(q, kv_pages, block_table, kv_scale)
     _need(workspace, "workspace", (torch.uint8,), dev)
     with _on(dev):
         st = load_library().mla_decode_partial(
@@ -342,11 +370,11 @@ def decode_dcp(q, kv_pages, block_table, seq_lens, num_parts: int, sm_scale: flo
     if seq_lens.numel() != B or block_table.dim() != 2 or block_table.shape[0] != B:
         raise ValueError("seq_lens / block_table do not match the batch")
     if partials is None:
-        partials = torch.empty(P, B, T, H, 512, dtype=torch.bfloat16, device=dev)
+        partials = _output((P, B, T, H, 512), torch.bfloat16, dev, stream)
     if partial_lses is None:
-        partial_lses = torch.empty(P, B, T, H, dtype=torch.float32, device=dev)
+        partial_lses = _output((P, B, T, H), torch.float32, dev, stream)
     if out is None:
-        out = torch.empty(B, T, H, 512, dtype=torch.bfloat16, device=dev)
+        out = _output((B, T, H, 512), torch.bfloat16, dev, stream)
     _need(partials, "partials", (torch.bfloat16,), dev)
     _need(partial_lses, "partial_lses", (torch.float32,), dev)
     _need(out, "out", (torch.bfloat16,), dev)
@@ -359,7 +387,8 @@ def decode_dcp(q, kv_pages, block_table, seq_lens, num_parts: int, sm_scale: flo
         if out_lse.numel() != B * T * H:
             raise ValueError("out_lse must be [B,q_len,H]")
     if workspace is None:
-        workspace = make_dcp_workspace(q, kv_pages, block_table, P, kv_scale)
+        with _allocating_on(stream, dev):
+            workspace = make_dcp_workspace(q, kv_pages, block_table, P, kv_scale)
     _need(workspace, "workspace", (torch.uint8,), dev)
     with _on(dev):
         st = load_library().mla_decode_dcp(
@@ -388,10 +417,9 @@ def dcp_local_metadata(seq_lens, req_pool_indices, req_to_token, part_id: int, n
     B = seq_lens.numel()
     if req_pool_indices.numel() != B or req_to_token.dim() != 2:
         raise ValueError("req_pool_indices must be [B] and req_to_token [slots, width]")
-    global_lens = global_lens if global_lens is not None else torch.empty(B, dtype=torch.int32, device=dev)
-    local_lens = local_lens if local_lens is not None else torch.empty(B, dtype=torch.int32, device=dev)
-    block_table = block_table if block_table is not None else torch.empty(
-        B, int(max_pages), dtype=torch.int32, device=dev)
+    global_lens = global_lens if global_lens is not None else _output((B,), torch.int32, dev, stream)
+    local_lens = local_lens if local_lens is not None else _output((B,), torch.int32, dev, stream)
+    block_table = block_table if block_table is not None else _output((B, int(max_pages)), torch.int32, dev, stream)
     for t, n in ((global_lens, "global_lens"), (local_lens, "local_lens"), (block_table, "block_table")):
         _need(t, n, (torch.int32,), dev)
     if global_lens.numel() != B or local_lens.numel() != B or block_table.numel() != B * int(max_pages):
@@ -520,7 +548,8 @@ def decode_window(q, kv_pages, block_table, seq_lens, window: int, sinks: int, s
     make_workspace's.  Entries of pages out of view may be -1."""
     dev, d = _view_args("decode_window", q, kv_pages, block_table, seq_lens, out, lse, kv_scale)
     if workspace is None:
-        workspace = make_workspace(q, kv_pages, block_table, kv_scale)
+        with _allocating_on(stream, dev):
+            workspace = make_workspace(q, kv_pages, block_table, kv_scale)
     _need(workspace, "workspace", (torch.uint8,), dev)
     _launch(load_library().mla_decode_window, dev, stream, q.data_ptr(), kv_pages.data_ptr(),
             block_table.data_ptr(), seq_lens.data_ptr(), int(window), int(sinks), float(sm_scale),
@@ -552,7 +581,8 @@ def decode_shared(q, kv_pages, block_table, seq_lens, group_starts, shared_pages
     if groups < 1 or group_starts.numel() != groups + 1:
         raise ValueError("group_starts must be [G + 1] and shared_pages [G], G >= 1")
     if workspace is None:
-        workspace = make_shared_workspace(q, kv_pages, block_table, groups, kv_scale)
+        with _allocating_on(stream, dev):
+            workspace = make_shared_workspace(q, kv_pages, block_table, groups, kv_scale)
     _need(workspace, "workspace", (torch.uint8,), dev)
     _launch(load_library().mla_decode_shared, dev, stream, q.data_ptr(), kv_pages.data_ptr(),
             block_table.data_ptr(), seq_lens.data_ptr(), group_starts.data_ptr(), shared_pages.data_ptr(),
@@ -627,9 +657,10 @@ def _opt(t):
     return t.data_ptr() if t is not None else None
 
 
-def _pages_ws(workspace, ref_counts):
+def _pages_ws(workspace, ref_counts, stream):
     if workspace is None:
-        return make_pages_workspace(ref_counts)
+        with _allocating_on(stream, ref_counts.device):
+            return make_pages_workspace(ref_counts)
     _need(workspace, "workspace", (torch.uint8,), ref_counts.device)
     return workspace
 
@@ -668,7 +699,7 @@ def pages_fork(kv_pages, block_table, seq_lens, ref_counts, parents, children, *
     n = parents.numel()
     if children.numel() != n:
         raise ValueError("parents and children must have the same length")
-    ws = _pages_ws(workspace, ref_counts)
+    ws = _pages_ws(workspace, ref_counts, stream)
     _launch(load_library().mla_pages_fork, dev, stream, kv_pages.data_ptr(), block_table.data_ptr(),
             seq_lens.data_ptr(), ref_counts.data_ptr(), parents.data_ptr(), children.data_ptr(), n,
             _pages_desc(rows, width, pages, shape[1], shape[2], code), ws.data_ptr(), ws.numel(),
@@ -684,7 +715,7 @@ def pages_alloc(block_table, seq_lens, ref_counts, new_lens, *, workspace=None, 
     _ints(new_lens, "new_lens", dev, 1)
     if new_lens.numel() != rows:
         raise ValueError("new_lens must be [num_requests]")
-    ws = _pages_ws(workspace, ref_counts)
+    ws = _pages_ws(workspace, ref_counts, stream)
     _launch(load_library().mla_pages_alloc, dev, stream, block_table.data_ptr(), seq_lens.data_ptr(),
             ref_counts.data_ptr(), new_lens.data_ptr(), _pages_desc(rows, width, pages, 64, 576, KV_BF16),
             ws.data_ptr(), ws.numel(), _opt(error_word))
@@ -719,7 +750,7 @@ def pages_compact(kv_pages, block_table, ref_counts, *, remap=None, workspace=No
         _ints(remap, "remap", dev, 1)
         if remap.numel() != pages:
             raise ValueError("remap must be [num_pages]")
-    ws = _pages_ws(workspace, ref_counts)
+    ws = _pages_ws(workspace, ref_counts, stream)
     _launch(load_library().mla_pages_compact, dev, stream, kv_pages.data_ptr(), block_table.data_ptr(),
             ref_counts.data_ptr(), _opt(remap), _pages_desc(rows, width, pages, shape[1], shape[2], code),
             ws.data_ptr(), ws.numel(), _opt(error_word))
