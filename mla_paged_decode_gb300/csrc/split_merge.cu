@@ -18,6 +18,14 @@ namespace mla {
 constexpr int kMergeWarps = 4;  // heads per CTA
 constexpr int kMergeBatch = 2;  // splits whose loads are in flight together
 
+// The base-2 LSE of a merged row whose weights sum up to `sum`: -inf only for a row
+// that saw no token.  A NaN partial (its query held a NaN or an Inf) makes the sum
+// NaN and stays NaN, as in a row that one CTA holds whole: -inf would mark the row
+// as empty, and a later merge would drop it.
+__device__ __forceinline__ float merged_lse2(float mref, float sum) {
+  return sum == 0.f ? -INFINITY : mref + log2f(sum);
+}
+
 // One warp merges row hl of request v, which the schedule split into
 // info.y >= 2 pieces (info = the record its first CTA left): the
 // LSE-weighted combine of the splits' normalised fp32 partials.  Returns this
@@ -81,7 +89,7 @@ __device__ __forceinline__ void merge_split_row(const DecodeParams &p, int4 info
     pk[2 * i] = *reinterpret_cast<uint32_t *>(&lo);
     pk[2 * i + 1] = *reinterpret_cast<uint32_t *>(&hi);
   }
-  *lse2 = sum > 0.f ? mref + log2f(sum) : -INFINITY;
+  *lse2 = merged_lse2(mref, sum);
 }
 
 __device__ __forceinline__ void store_row(__nv_bfloat16 *row, const uint32_t (&pk)[8]) {
@@ -114,7 +122,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32, 7) split_merge_kernel(Decode
   merge_split_row(p, info, hl, pk, &lse2);
   const size_t row = size_t(b) * p.heads + size_t(g) * p.heads_per_group + hl;
   store_row(p.out + row * kDv, pk);
-  if (lane == 0) p.lse[row] = lse2 > -INFINITY ? lse_out(p, lse2) : -INFINITY;
+  if (lane == 0) p.lse[row] = lse_out(p, lse2);
 }
 
 // All partitions in one call (the decode ran them in one launch): one CTA
@@ -146,7 +154,7 @@ __global__ void __launch_bounds__(kDcpMaxParts * 32) dcp_merge_combine_kernel(De
       float lse2;
       merge_split_row(p, info, hl, pk, &lse2);
       store_row(p.out + prow * kDv, pk);
-      l = lse2 > -INFINITY ? lse_out(p, lse2) : -INFINITY;
+      l = lse_out(p, lse2);
       if (lane == 0) p.lse[prow] = l;
     } else {  // written by the decode (the neutral pair if it owned nothing)
       const uint4 *src = reinterpret_cast<const uint4 *>(p.out + prow * kDv + 16 * lane);
@@ -310,7 +318,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32, 7) shared_merge_kernel(Decod
     __nv_bfloat162 hi = __floats2bfloat162_rn(acc[i].z * inv, acc[i].w * inv);
     dst[lane + 32 * i] = make_uint2(*reinterpret_cast<uint32_t *>(&lo), *reinterpret_cast<uint32_t *>(&hi));
   }
-  if (lane == 0) p.lse[row] = sum > 0.f ? lse_out(p, mref + log2f(sum)) : -INFINITY;
+  if (lane == 0) p.lse[row] = lse_out(p, merged_lse2(mref, sum));
 }
 
 cudaError_t launch_shared_merge(const DecodeParams &p, int grid, cudaStream_t stream) {
