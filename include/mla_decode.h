@@ -359,7 +359,8 @@ typedef struct mla_combine_desc {
  *            that owned no token (its partial is ignored).
  *  out       bf16 [T, H, D]:  sum_p w_p o_p / sum_p w_p with
  *            w_p = base^(lse_p - max_p lse_p).  Rows whose partitions are all
- *            -inf get out = 0 (and out_lse = -inf), never NaN.
+ *            -inf get out = 0 (and out_lse = -inf), never NaN.  A NaN among a
+ *            row's lses gives NaN.
  */
 int mla_lse_combine(const void *partials, const float *lses, int num_parts, void *out,
                     const mla_combine_desc *d, mla_stream_t stream);

@@ -568,6 +568,13 @@ __device__ __forceinline__ float bf16_bits_to_float(uint16_t b) {
   return __uint_as_float(uint32_t(b) << 16);
 }
 
+// The larger of two, NaN when either is (fmaxf drops a NaN).
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
 // Two OCP e4m3 bytes -> two exact f16 values (hardware conversion).
 __device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint16_t two) {
   uint32_t r;

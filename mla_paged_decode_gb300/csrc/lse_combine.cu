@@ -29,9 +29,10 @@ lse_combine_kernel(const __nv_bfloat16 *__restrict__ partials, const float *__re
   float *w = s_w + warp * num_parts;
   const float to2 = base2 ? 1.f : kLog2e;
 
+  // (a NaN stays: partitions that are all NaN are not partitions that own nothing)
   float mx = -INFINITY;
-  for (int q = lane; q < num_parts; q += 32) mx = fmaxf(mx, lses[size_t(q) * rows + row] * to2);
-  for (int o = 16; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+  for (int q = lane; q < num_parts; q += 32) mx = max_nan(mx, lses[size_t(q) * rows + row] * to2);
+  for (int o = 16; o; o >>= 1) mx = max_nan(mx, __shfl_xor_sync(0xffffffffu, mx, o));
 
   const int chunks = dim / 8;
   uint4 *dst = reinterpret_cast<uint4 *>(out + size_t(row) * dim);

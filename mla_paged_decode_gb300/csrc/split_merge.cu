@@ -174,7 +174,7 @@ __global__ void __launch_bounds__(kDcpMaxParts * 32) dcp_merge_combine_kernel(De
   // that the result equals mla_lse_combine's bit for bit.
   const float to2 = p.lse_base2 ? 1.f : kLog2e;
   float mx = -INFINITY;
-  for (int q = 0; q < P; ++q) mx = fmaxf(mx, s_lse[q] * to2);
+  for (int q = 0; q < P; ++q) mx = max_nan(mx, s_lse[q] * to2);
   const size_t orow = size_t(b) * rows + r;
   uint4 *dst = reinterpret_cast<uint4 *>(p.comb_out + orow * kDv);
   constexpr int kChunks = kDv / 8;  // 16-byte chunks of a row
