@@ -98,13 +98,6 @@ __device__ __forceinline__ void store_row(__nv_bfloat16 *row, const uint32_t (&p
   dst[1] = make_uint4(pk[4], pk[5], pk[6], pk[7]);
 }
 
-// The decode rewrote every record this call (requests with no owned token
-// get {-1, 0, 0}); split k > 0 lives in slot 2 (first + k): never past the
-// 2 x grid slots.
-__device__ __forceinline__ bool is_split(int4 info, int grid) {
-  return info.y > 1 && info.x >= 0 && info.x + info.y <= grid;
-}
-
 __global__ void __launch_bounds__(kMergeWarps * 32, 7) split_merge_kernel(DecodeParams p, int grid) {
   // launched as a programmatic dependent of the decode kernel: wait until its
   // grid has completed and its writes are visible
@@ -242,14 +235,14 @@ __global__ void __launch_bounds__(kMergeWarps * 32, 7) shared_merge_kernel(Decod
     const int v = p.pair_blocks ? block_base<128>(p, g) + (local >> 7) : block_base<64>(p, g) + (local >> 6);
     if (v < blocks) {
       const int4 i = p.pair_blocks ? pair_info_ptr(p)[v] : info_ptr(p)[v];
-      if (i.y > 0 && i.z >= 0 && (i.z + i.y) * stride[0] <= slots)
+      if (has_pieces(i, stride[0], slots))
         first[0] = i.z * stride[0] + ((local >> 6) & (stride[0] - 1)), num[0] = i.y;
     }
   }
   {
     const int4 i = p.pair_tails ? pair_info_ptr(p)[p.pair_blocks - p.pair_tails + (r >> 7) * p.batch + b]
                                 : info_ptr(p)[p.prefix_blocks + (r >> 6) * p.batch + b];
-    if (i.y > 0 && i.z >= 0 && (i.z + i.y) * stride[1] <= slots)
+    if (has_pieces(i, stride[1], slots))
       first[1] = i.z * stride[1] + ((r >> 6) & (stride[1] - 1)), num[1] = i.y;
   }
   const int ns = num[0] + num[1];

@@ -29,6 +29,21 @@ __device__ __forceinline__ SplitInfo split_info(const CtaRange &r, int v, long l
 __host__ __device__ __forceinline__ int pair_slots(const DecodeParams &p) {
   return 2 * (p.pair_blocks + p.pairs);
 }
+// What a merge may follow of a record {first CTA or -1, pieces, slot of the first
+// piece}.  Every call rewrites the records that its merge reads, but for a call
+// whose bounded wait gave up: what is then in them may be anything, so that the
+// checks take no sum or product of two words in 32 bits.
+//
+// A split of the decode kernel's schedule: piece 0 in slot z, piece k > 0 in slot
+// 2 (x + k), all below 2 * grid.
+__host__ __device__ __forceinline__ bool is_split(int4 info, int grid) {
+  return info.y > 1 && info.x >= 0 && (long long)info.x + info.y <= grid && info.z >= 0 && info.z < 2 * grid;
+}
+// Pieces of shared pages or tails: y runs of `stride` slots from slot z * stride on.
+__host__ __device__ __forceinline__ bool has_pieces(int4 info, int stride, int slots) {
+  return info.y > 0 && info.z >= 0 && ((long long)info.z + info.y) * stride <= slots;
+}
+
 __device__ __forceinline__ float *slot_lse_ptr(const DecodeParams &p) {
   return reinterpret_cast<float *>(p.ws + p.wl.slot_lse);
 }
