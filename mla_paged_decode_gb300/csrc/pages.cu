@@ -35,6 +35,9 @@ __device__ __forceinline__ void flag(int32_t *error_word, int bit) {
   if (error_word) atomicOr(error_word, bit);
 }
 
+// Pages that hold n >= 0 tokens (n + 63 would wrap for the largest lengths and sinks).
+__device__ __forceinline__ int pages_of(int n) { return n / kPage + (n % kPage ? 1 : 0); }
+
 // Copies `bytes` (a multiple of 16) from src to dst with all threads of the
 // CTA, four 16-byte loads of a thread in flight.
 __device__ __forceinline__ void copy_bytes(unsigned char *dst, const unsigned char *src, int bytes) {
@@ -241,7 +244,7 @@ __device__ __forceinline__ int pages_gained(const PagesTable &t, const int32_t *
   const int L = t.seq_lens[b], N = new_lens[b];
   *bad = L < 0 || N < 0 || (long long)L > (long long)t.width * kPage ||
          (long long)N > (long long)t.width * kPage;
-  return *bad ? 0 : max(0, (N + kPage - 1) / kPage - (L + kPage - 1) / kPage);
+  return *bad ? 0 : max(0, pages_of(N) - pages_of(L));
 }
 
 constexpr int kAllocThreads = 128;
@@ -269,7 +272,7 @@ __global__ void __launch_bounds__(kAllocThreads)
     return;
   }
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int first = (t.seq_lens[b] + kPage - 1) / kPage;
+  const int first = pages_of(t.seq_lens[b]);
   int32_t *row = t.block_table + size_t(b) * t.width;
   for (int i = warp; i < need; i += kAllocThreads / 32) {
     const int pg = free_page_of_rank(ws, num_chunks, before + i);
@@ -298,9 +301,9 @@ __global__ void __launch_bounds__(kFreeThreads)
     if (threadIdx.x == 0) flag(error_word, kErrPagesEntry);
     return;
   }
-  const int keep = (N + kPage - 1) / kPage;
+  const int keep = pages_of(N);
   // out of view: pages [lo, hi)
-  const int lo = (sinks + kPage - 1) / kPage;
+  const int lo = pages_of(sinks);
   const int hi = window > 0 && N >= window ? (N - window + 1) / kPage : 0;
   int32_t *row = t.block_table + size_t(b) * t.width;
   for (int i = threadIdx.x; i < t.width; i += blockDim.x) {

@@ -1,0 +1,57 @@
+"""Page operations at the ends of their ranges: sinks, windows and lengths up to
+2^31 - 1."""
+import numpy as np
+import pytest
+import torch
+
+import mla_paged_decode_gb300 as mla
+from oracle import pages_oracle as po
+from pages_cases import state
+
+pytestmark = pytest.mark.gpu
+TOP = 2**31 - 1
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _library():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    from mla_paged_decode_gb300 import build
+    build.build()
+    mla.load_library()
+
+
+def ints(x):
+    return torch.tensor(x, dtype=torch.int32, device="cuda")
+
+
+@pytest.mark.parametrize("window,sinks", [(100, TOP), (100, TOP - 63), (100, TOP - 62), (TOP, 0), (TOP, TOP), (1, TOP - 1)])
+def test_free_keeps_what_the_largest_views_see(window, sinks):
+    host = list(state(4, [640, 65, 1, 500], 40, 3, seed=70))
+    _, table, lens, counts = (torch.from_numpy(x.copy()).cuda() for x in host)
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    new = np.array([640, 65, 1, 200])
+    mla.pages_free(table, lens, counts, ints(new), window=window, sinks=sinks, error_word=err)
+    assert po.free(*host[1:], new, window, sinks) == 0 == int(err.item())
+    for got, want in zip((table, lens, counts), host[1:]):
+        np.testing.assert_array_equal(got.cpu().numpy(), want)
+
+
+def test_free_and_alloc_of_the_longest_request():
+    """A table of 2^25 pages holds every length below 2^31."""
+    width = 2**25
+    table = torch.full((1, width), -1, dtype=torch.int32, device="cuda")
+    table[0, 0], table[0, width - 2] = 2, 0
+    counts = ints([1, 0, 1, 0])
+    lens = ints([TOP - 64])                 # 2^25 - 1 pages
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    mla.pages_alloc(table, lens, counts, ints([TOP]), error_word=err)
+    assert table[0, width - 1].item() == 1 and counts.tolist() == [1, 1, 1, 0]
+    lens.fill_(TOP)
+    mla.pages_free(table, lens, counts, ints([TOP]), error_word=err)
+    assert table[0, [0, width - 2, width - 1]].tolist() == [2, 0, 1] and counts.tolist() == [1, 1, 1, 0]
+    mla.pages_free(table, lens, counts, ints([TOP]), window=1, sinks=1, error_word=err)
+    assert table[0, [0, width - 2, width - 1]].tolist() == [2, -1, 1] and counts.tolist() == [0, 1, 1, 0]
+    mla.pages_free(table, lens, counts, ints([TOP - 64]), error_word=err)
+    assert table[0, [0, width - 2, width - 1]].tolist() == [2, -1, -1] and counts.tolist() == [0, 0, 1, 0]
+    assert lens.item() == TOP - 64 and err.item() == 0
