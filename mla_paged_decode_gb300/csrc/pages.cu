@@ -55,14 +55,17 @@ __device__ __forceinline__ void copy_bytes(unsigned char *dst, const unsigned ch
   }
 }
 
-// Sum over the CTA (every thread gets it); `scratch` holds blockDim.x / 32 ints.
-__device__ __forceinline__ int block_sum(int x, int *scratch) {
-  x = __reduce_add_sync(0xffffffffu, x);
+// Sum over the CTA (every thread gets it); `scratch` holds blockDim.x / 32 of T.
+template <typename T>
+__device__ __forceinline__ T block_sum(T x, T *scratch) {
+  if constexpr (sizeof(T) == 4) x = __reduce_add_sync(0xffffffffu, x);
+  else
+    for (int o = 16; o; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
   const int nw = int(blockDim.x + 31) / 32;
   __syncthreads();
   if ((threadIdx.x & 31) == 0) scratch[threadIdx.x >> 5] = x;
   __syncthreads();
-  int total = 0;
+  T total = 0;
   for (int w = 0; w < nw; ++w) total += scratch[w];
   return total;
 }
@@ -253,13 +256,14 @@ __global__ void __launch_bounds__(kAllocThreads)
     pages_alloc_kernel(PagesTable t, const int32_t *new_lens, PagesWorkspace ws, int num_chunks,
                        int32_t *error_word) {
   wait_previous();
-  __shared__ int s_scratch[kAllocThreads / 32];
+  __shared__ long long s_scratch[kAllocThreads / 32];
   const int b = blockIdx.x;
   bool bad;
   const int need = pages_gained(t, new_lens, b, &bad);
   if (bad && threadIdx.x == 0) flag(error_word, kErrPagesEntry);
   if (need == 0) return;
-  int before = 0, total = 0;
+  // what the requests before this one ask for may pass 2^31 pages, fit or not
+  long long before = 0, total = 0;
   for (int j = threadIdx.x; j < b; j += blockDim.x) {
     bool skip;
     before += pages_gained(t, new_lens, j, &skip);
@@ -275,7 +279,7 @@ __global__ void __launch_bounds__(kAllocThreads)
   const int first = pages_of(t.seq_lens[b]);
   int32_t *row = t.block_table + size_t(b) * t.width;
   for (int i = warp; i < need; i += kAllocThreads / 32) {
-    const int pg = free_page_of_rank(ws, num_chunks, before + i);
+    const int pg = free_page_of_rank(ws, num_chunks, int(before) + i);
     if (lane != 0) continue;
     if (row[first + i] != -1) {  // a page is already there: leave it
       flag(error_word, kErrPagesEntry);

@@ -55,3 +55,17 @@ def test_free_and_alloc_of_the_longest_request():
     mla.pages_free(table, lens, counts, ints([TOP - 64]), error_word=err)
     assert table[0, [0, width - 2, width - 1]].tolist() == [2, -1, -1] and counts.tolist() == [0, 0, 1, 0]
     assert lens.item() == TOP - 64 and err.item() == 0
+
+
+def test_alloc_of_more_pages_than_32_bits_count():
+    """64 requests ask for 2^25 pages each: the ranks of those behind them pass
+    2^31.  Only the first one, which asks for two, fits."""
+    rows, width = 67, 2**25                 # a table of 9 GB
+    table = torch.full((rows, width), -1, dtype=torch.int32, device="cuda")
+    counts = torch.zeros(3000, dtype=torch.int32, device="cuda")
+    lens = torch.zeros(rows, dtype=torch.int32, device="cuda")
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    mla.pages_alloc(table, lens, counts, ints([65] + [TOP] * 64 + [1, TOP]), error_word=err)
+    assert err.item() == mla.PAGES_FULL
+    assert table[0, :3].tolist() == [0, 1, -1] and int(counts.sum()) == 2
+    assert (table[0, 2:] == -1).all() and (table[1:] == -1).all()
