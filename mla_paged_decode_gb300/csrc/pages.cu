@@ -337,7 +337,7 @@ constexpr int kDirectChunks = 2;
 // With n live pages: a free id below n is a hole, a live id from n up a
 // mover; there are m of each.  Writes the holes in order to free_list, the
 // movers by their rank among the live pages to `movers` (ranks n - m .. n),
-// every live page's rank to `rank`, {n, m} to `totals`, and to `remap` (when
+// every live page's rank to `rank` (-1 for a free one), {n, m} to `totals`, and to `remap` (when
 // given) what does not move: a live page below n, and -1 for a free one.
 __global__ void __launch_bounds__(kScanThreads)
     pages_compact_plan_kernel(const int32_t *ref_counts, int num_pages, PagesWorkspace ws, int num_chunks,
@@ -392,6 +392,7 @@ __global__ void __launch_bounds__(kScanThreads)
     if (id < num_pages) {
       if ((mask[j] >> lane) & 1u) {
         if (id < live) ws.holes[free_before] = id;
+        ws.rank[id] = -1;
         if (remap) remap[id] = -1;
       } else {
         ws.rank[id] = id - free_before;
@@ -423,17 +424,14 @@ __global__ void __launch_bounds__(kCopyThreads)
   const long long entries = (long long)t.rows * t.width;
   for (long long i = me; i < entries; i += stride) {
     const int e = t.block_table[i];
-    if (e == -1 || (e >= 0 && e < live)) continue;  // a live page below `live` stays
-    if (e < 0 || e >= t.num_pages) {
+    if (e == -1) continue;
+    // (asked below `live` too, where something may move into a free page)
+    const int rank = e < 0 || e >= t.num_pages ? -1 : ws.rank[e];
+    if (rank < 0) {  // no page, or a free one
       flag(error_word, kErrPagesEntry);
       continue;
     }
-    const int h = ws.rank[e] - (live - m);
-    if (h < 0 || h >= m || ws.movers[live - m + h] != e) {  // an entry that names a free page
-      flag(error_word, kErrPagesEntry);
-      continue;
-    }
-    t.block_table[i] = ws.holes[h];
+    if (e >= live) t.block_table[i] = ws.holes[rank - (live - m)];  // (a live page below stays)
   }
   for (long long h = me; h < m; h += stride) {
     const int from = ws.movers[live - m + h], to = ws.holes[h];

@@ -31,7 +31,7 @@ struct PagesWorkspace {
   int32_t *free_list;   // [chunks][kPagesChunk]: a chunk's free ids, ascending
   int32_t *holes;       // the same memory, as one list (compaction)
   int32_t *movers;      // [num_pages], by rank among the live pages
-  int32_t *rank;        // [num_pages]: a live page's rank
+  int32_t *rank;        // [num_pages]: a live page's rank, -1 for a free page
   int32_t *fork_count;  // the same memory as movers and rank: forks that need a page, by blocks
 };
 constexpr int kMaxForks = 1 << 19;  // what a one-chunk workspace's fork_count holds

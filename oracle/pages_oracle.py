@@ -129,7 +129,7 @@ def compact(kv, table, counts):
     for b in range(table.shape[0]):
         for i in range(table.shape[1]):
             e = int(table[b, i])
-            if e == -1 or 0 <= e < n:
+            if e == -1:
                 continue
             if not 0 <= e < counts.size or not was_live[e]:
                 err |= BAD

@@ -69,3 +69,21 @@ def test_alloc_of_more_pages_than_32_bits_count():
     assert err.item() == mla.PAGES_FULL
     assert table[0, :3].tolist() == [0, 1, -1] and int(counts.sum()) == 2
     assert (table[0, 2:] == -1).all() and (table[1:] == -1).all()
+
+
+@pytest.mark.parametrize("pages", [30, 5000])
+def test_compact_reports_entries_of_free_pages_below_the_live_ones(pages):
+    """The page is free, something moves into it, and the entry stays as it is."""
+    host = list(state(4, [640, 640, 64], pages, 144, seed=71))
+    po.free(*host[1:], np.array([640, 0, 64, 0]))
+    n = int((host[3] > 0).sum())
+    hole = 0 if host[3][0] == 0 else int(np.flatnonzero(host[3] == 0)[0])
+    assert hole < n
+    host[1][3, :2] = [hole, -1]
+    kv, table, counts = (torch.from_numpy(host[i].copy()).cuda() for i in (0, 1, 3))
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    mla.pages_compact(kv.view(torch.uint8).view(pages, 64, 576), table, counts, error_word=err)
+    assert po.compact(host[0], host[1], host[3])[0] == po.BAD and host[1][3, 0] == hole
+    assert err.item() == mla.PAGES_BAD_ENTRY
+    for got, want in zip((kv, table, counts), (host[0], host[1], host[3])):
+        np.testing.assert_array_equal(got.cpu().numpy(), want)
