@@ -219,12 +219,12 @@ __global__ void __launch_bounds__(kCopyThreads)
       int32_t *to = t.block_table + size_t(f.child) * t.width;
       for (int i = threadIdx.x; i < t.width; i += blockDim.x) {
         int e = i < held ? from[i] : -1;
-        if (e >= t.num_pages) {
+        if (e < -1 || e >= t.num_pages) {
           flag(error_word, kErrPagesEntry);
           e = -1;
         }
         if (e >= 0) atomicAdd(t.ref_counts + e, 1);
-        to[i] = i == held && fresh >= 0 ? fresh : e < 0 ? -1 : e;
+        to[i] = i == held && fresh >= 0 ? fresh : e;
       }
       if (threadIdx.x == 0) {
         t.seq_lens[f.child] = full_pool ? 0 : f.len;

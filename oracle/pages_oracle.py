@@ -52,7 +52,7 @@ def fork(kv, table, lens, counts, parents, children):
                 continue
         for i in range(full):
             e = int(old_table[p, i])
-            if e >= counts.size:
+            if e < -1 or e >= counts.size:
                 err |= BAD
             elif e >= 0:
                 row[i] = e

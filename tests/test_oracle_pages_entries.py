@@ -20,3 +20,11 @@ def test_compact_reports_an_entry_of_a_free_page_wherever_it_lies():
         for before, after in zip(others[others >= 0], table[:3][others >= 0]):
             assert remap[before] == after
             np.testing.assert_array_equal(kv[after], pages[int(before)])
+
+
+def test_fork_reports_any_entry_that_is_no_page():
+    for entry in (-2, -2**31, 40, 2**31 - 1):
+        kv, table, lens, counts = state(4, [300, 64], 40, 3, seed=6)
+        table[0, 1] = entry
+        assert po.fork(kv, table, lens, counts, np.array([0, 1]), np.array([2, 3])) == po.BAD
+        assert table[2, 1] == -1 and lens[2] == 300 and table[3, 0] == table[1, 0]

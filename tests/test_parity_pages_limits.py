@@ -87,3 +87,17 @@ def test_compact_reports_entries_of_free_pages_below_the_live_ones(pages):
     assert err.item() == mla.PAGES_BAD_ENTRY
     for got, want in zip((kv, table, counts), (host[0], host[1], host[3])):
         np.testing.assert_array_equal(got.cpu().numpy(), want)
+
+
+@pytest.mark.parametrize("entry", [-2, -2**31, 40, TOP])
+def test_fork_reports_any_entry_that_is_no_page(entry):
+    host = list(state(4, [300, 64], 40, 288, seed=72))
+    host[1][0, 1] = entry
+    kv, table, lens, counts = (torch.from_numpy(x.copy()).cuda() for x in host)
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    parents, children = np.array([0, 1]), np.array([2, 3])
+    mla.pages_fork(kv.view(torch.bfloat16), table, lens, counts, ints(parents), ints(children), error_word=err)
+    assert po.fork(*host, parents, children) == po.BAD == err.item()
+    assert host[1][2, 1] == -1
+    for got, want in zip((kv, table, lens, counts), host):
+        np.testing.assert_array_equal(got.cpu().numpy(), want)
