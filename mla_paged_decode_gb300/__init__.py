@@ -18,8 +18,8 @@ import torch
 __all__ = [
     "MlaError", "LSE_NATURAL", "LSE_BASE2", "decode_partial", "lse_combine",
     "workspace_size", "make_workspace", "check_workspace", "library_path", "load_library",
-    "decode_partial_noalloc", "decode_window", "decode_shared", "make_shared_workspace", "pages_workspace_size", "make_pages_workspace", "pages_copy",
-    "pages_fork", "pages_alloc", "pages_free", "pages_compact", "PAGES_BAD_ENTRY", "PAGES_FULL",
+    "decode_partial_noalloc", "decode_window", "decode_shared", "make_shared_workspace",
+    "pages_workspace_size", "make_pages_workspace", "pages_copy", "pages_fork", "pages_alloc", "pages_free", "pages_compact", "PAGES_BAD_ENTRY", "PAGES_FULL",
 ]
 
 LSE_NATURAL = 0
@@ -142,6 +142,15 @@ def _check(status: int):
         raise MlaError(status, msg)
 
 
+def _int32(value, name: str) -> int:
+    """An integer argument of the C calls; ctypes would cut a larger one to its
+    low 32 bits without a word (a window of 2**32 + 7 tokens to 7)."""
+    v = int(value)
+    if not -0x80000000 <= v <= 0x7fffffff:
+        raise ValueError(f"{name} = {v} does not fit into 32 bits")
+    return v
+
+
 # The current stream's handle and the current device without the Python
 # objects around them (2 us and 0.4 us of a small call's host time).
 _raw_stream = torch._C._cuda_getCurrentRawStream if hasattr(torch._C, "_cuda_getCurrentRawStream") else \
@@ -228,12 +237,13 @@ def _decode_desc(q, kv_pages, block_table, kv_scale) -> DecodeDesc:
 def _make_decode_desc(q, kv_pages, block_table, kv_scale) -> DecodeDesc:
     if q.dim() != 4:
         raise ValueError("q must be [B, q_len, H, 576]")
-    B, q_len, H, dqk = q.shape
+    B, q_len, H, dqk = (_int32(n, "a size of q") for n in q.shape)
     if kv_pages.dim() != 3:
         raise ValueError("kv_pages must be [num_pages, page_size, 576]")
     return DecodeDesc(batch=B, num_heads=H, q_len=q_len, head_dim_qk=dqk, head_dim_v=512,
-                      page_size=kv_pages.shape[1], num_pages=kv_pages.shape[0],
-                      max_pages_per_seq=block_table.shape[1] if block_table.dim() == 2 else 0,
+                      page_size=_int32(kv_pages.shape[1], "page_size"),
+                      num_pages=_int32(kv_pages.shape[0], "num_pages"),
+                      max_pages_per_seq=_int32(block_table.shape[1], "max_pages") if block_table.dim() == 2 else 0,
                       kv_dtype=_kv_dtype_code(kv_pages), kv_scale=float(kv_scale))
 
 
@@ -273,6 +283,8 @@ def decode_partial(q, kv_pages, block_table, seq_lens, part_id: int, num_parts: 
     block_table int32 [B,max_pages]; seq_lens int32 [B] (global lengths);
     out bf16 [B,1,H,512] and lse fp32 [B,1,H] are written in place.
     """
+    part_id, num_parts = _int32(part_id, "part_id"), _int32(num_parts, "num_parts")
+    lse_base = _int32(lse_base, "lse_base")
     dev = q.device
     if dev.type != "cuda":
         raise ValueError("decode_partial runs on CUDA tensors only")
@@ -294,7 +306,7 @@ def decode_partial(q, kv_pages, block_table, seq_lens, part_id: int, num_parts: 
     with _on(dev):
         st = load_library().mla_decode_partial(
             q.data_ptr(), kv_pages.data_ptr(), block_table.data_ptr(), seq_lens.data_ptr(),
-            int(part_id), int(num_parts), float(sm_scale), int(lse_base), out.data_ptr(),
+            part_id, num_parts, float(sm_scale), lse_base, out.data_ptr(),
             lse.data_ptr(), ctypes.byref(d), workspace.data_ptr(), workspace.numel(),
             _stream_ptr(stream, dev))
     _check(st)
@@ -313,6 +325,7 @@ def kv_append(kv_new, kv_pages, block_table, positions, part_id: int = 0, num_pa
     device tensor that receives bit 0 for a row whose page entry is out of
     range (that row is skipped).
     """
+    part_id, num_parts = _int32(part_id, "part_id"), _int32(num_parts, "num_parts")
     dev = kv_pages.device
     if dev.type != "cuda":
         raise ValueError("kv_append runs on CUDA tensors only")
@@ -327,14 +340,14 @@ def kv_append(kv_new, kv_pages, block_table, positions, part_id: int = 0, num_pa
         raise ValueError("kv_new must be [B, 576] and block_table [B, max_pages] for B positions")
     if error_word is not None:
         _need(error_word, "error_word", (torch.int32,), dev)
-    d = DecodeDesc(batch=B, num_heads=1, q_len=1, head_dim_qk=576, head_dim_v=512,
-                   page_size=kv_pages.shape[1], num_pages=kv_pages.shape[0],
-                   max_pages_per_seq=block_table.shape[1], kv_dtype=_kv_dtype_code(kv_pages),
+    d = DecodeDesc(batch=_int32(B, "batch"), num_heads=1, q_len=1, head_dim_qk=576, head_dim_v=512,
+                   page_size=_int32(kv_pages.shape[1], "page_size"), num_pages=_int32(kv_pages.shape[0], "num_pages"),
+                   max_pages_per_seq=_int32(block_table.shape[1], "max_pages"), kv_dtype=_kv_dtype_code(kv_pages),
                    kv_scale=float(kv_scale))
     with _on(dev):
         st = load_library().mla_kv_append(
             kv_new.data_ptr(), kv_pages.data_ptr(), block_table.data_ptr(), positions.data_ptr(),
-            int(part_id), int(num_parts), ctypes.byref(d),
+            part_id, num_parts, ctypes.byref(d),
             error_word.data_ptr() if error_word is not None else None, _stream_ptr(stream, dev))
     _check(st)
     return kv_pages
@@ -344,7 +357,7 @@ def make_dcp_workspace(q, kv_pages, block_table, num_parts: int, kv_scale: float
     """A zero-filled workspace for decode_dcp over num_parts partitions."""
     d = _decode_desc(q, kv_pages, block_table, kv_scale)
     with torch.cuda.device(q.device):
-        n = load_library().mla_decode_dcp_workspace_size(ctypes.byref(d), int(num_parts), 0)
+        n = load_library().mla_decode_dcp_workspace_size(ctypes.byref(d), _int32(num_parts, "num_parts"), 0)
     if n == 0:
         raise MlaError(-2, "cannot size a workspace for these shapes")
     return torch.zeros(n, dtype=torch.uint8, device=q.device)
@@ -358,6 +371,7 @@ def decode_dcp(q, kv_pages, block_table, seq_lens, num_parts: int, sm_scale: flo
     Returns (out [B,1,H,512], out_lse [B,1,H] or None, partials [P,B,1,H,512],
     partial_lses [P,B,1,H]); the output tensors are allocated when not given.
     """
+    num_parts, lse_base = _int32(num_parts, "num_parts"), _int32(lse_base, "lse_base")
     dev = q.device
     if dev.type != "cuda":
         raise ValueError("decode_dcp runs on CUDA tensors only")
@@ -366,7 +380,7 @@ def decode_dcp(q, kv_pages, block_table, seq_lens, num_parts: int, sm_scale: flo
     _need(block_table, "block_table", (torch.int32,), dev)
     _need(seq_lens, "seq_lens", (torch.int32,), dev)
     d = _decode_desc(q, kv_pages, block_table, kv_scale)
-    B, T, H, P = d.batch, d.q_len, d.num_heads, int(num_parts)
+    B, T, H, P = d.batch, d.q_len, d.num_heads, num_parts
     if seq_lens.numel() != B or block_table.dim() != 2 or block_table.shape[0] != B:
         raise ValueError("seq_lens / block_table do not match the batch")
     if partials is None:
@@ -393,7 +407,7 @@ def decode_dcp(q, kv_pages, block_table, seq_lens, num_parts: int, sm_scale: flo
     with _on(dev):
         st = load_library().mla_decode_dcp(
             q.data_ptr(), kv_pages.data_ptr(), block_table.data_ptr(), seq_lens.data_ptr(), P,
-            float(sm_scale), int(lse_base), partials.data_ptr(), partial_lses.data_ptr(),
+            float(sm_scale), lse_base, partials.data_ptr(), partial_lses.data_ptr(),
             out.data_ptr(), out_lse.data_ptr() if out_lse is not None else None, ctypes.byref(d),
             workspace.data_ptr(), workspace.numel(), _stream_ptr(stream, dev))
     _check(st)
@@ -408,6 +422,9 @@ def dcp_local_metadata(seq_lens, req_pool_indices, req_to_token, part_id: int, n
     rank-local page table [B, max_pages], built on the device (into the given
     buffers when passed, so a captured graph can keep reading them).
     Returns (global_lens, local_lens, block_table)."""
+    part_id, num_parts = _int32(part_id, "part_id"), _int32(num_parts, "num_parts")
+    max_pages, extra_tokens = _int32(max_pages, "max_pages"), _int32(extra_tokens, "extra_tokens")
+    pad_value = _int32(pad_value, "pad_value")
     dev = seq_lens.device
     if dev.type != "cuda":
         raise ValueError("dcp_local_metadata runs on CUDA tensors only")
@@ -419,20 +436,20 @@ def dcp_local_metadata(seq_lens, req_pool_indices, req_to_token, part_id: int, n
         raise ValueError("req_pool_indices must be [B] and req_to_token [slots, width]")
     global_lens = global_lens if global_lens is not None else _output((B,), torch.int32, dev, stream)
     local_lens = local_lens if local_lens is not None else _output((B,), torch.int32, dev, stream)
-    block_table = block_table if block_table is not None else _output((B, int(max_pages)), torch.int32, dev, stream)
+    block_table = block_table if block_table is not None else _output((B, max_pages), torch.int32, dev, stream)
     for t, n in ((global_lens, "global_lens"), (local_lens, "local_lens"), (block_table, "block_table")):
         _need(t, n, (torch.int32,), dev)
-    if global_lens.numel() != B or local_lens.numel() != B or block_table.numel() != B * int(max_pages):
+    if global_lens.numel() != B or local_lens.numel() != B or block_table.numel() != B * max_pages:
         raise ValueError("output buffers do not match the batch and max_pages")
     if error_word is not None:
         _need(error_word, "error_word", (torch.int32,), dev)
-    d = DcpMetaDesc(batch=B, num_req_slots=req_to_token.shape[0],
-                    req_to_token_width=req_to_token.shape[1], max_pages_per_seq=int(max_pages),
-                    extra_tokens=int(extra_tokens), pad_value=int(pad_value), page_size=64)
+    d = DcpMetaDesc(batch=_int32(B, "batch"), num_req_slots=_int32(req_to_token.shape[0], "slots"),
+                    req_to_token_width=_int32(req_to_token.shape[1], "width"), max_pages_per_seq=max_pages,
+                    extra_tokens=extra_tokens, pad_value=pad_value, page_size=64)
     with _on(dev):
         st = load_library().mla_dcp_local_metadata(
-            seq_lens.data_ptr(), req_pool_indices.data_ptr(), req_to_token.data_ptr(), int(part_id),
-            int(num_parts), ctypes.byref(d), global_lens.data_ptr(), local_lens.data_ptr(),
+            seq_lens.data_ptr(), req_pool_indices.data_ptr(), req_to_token.data_ptr(), part_id,
+            num_parts, ctypes.byref(d), global_lens.data_ptr(), local_lens.data_ptr(),
             block_table.data_ptr(), error_word.data_ptr() if error_word is not None else None,
             _stream_ptr(stream, dev))
     _check(st)
@@ -462,6 +479,7 @@ def selftest_bounded_wait(workspace: torch.Tensor, timeout_ns: int, stream=None)
 def lse_combine(partials, lses, num_parts: int, out, *, lse_base: int = LSE_NATURAL,
                 out_lse=None, stream=None):
     """mla_lse_combine: partials bf16 [P,T,H,D], lses fp32 [P,T,H] -> out bf16 [T,H,D]."""
+    num_parts, lse_base = _int32(num_parts, "num_parts"), _int32(lse_base, "lse_base")
     dev = partials.device
     if dev.type != "cuda":
         raise ValueError("lse_combine runs on CUDA tensors only")
@@ -477,10 +495,11 @@ def lse_combine(partials, lses, num_parts: int, out, *, lse_base: int = LSE_NATU
         _need(out_lse, "out_lse", (torch.float32,), dev)
         if out_lse.numel() != T * H:
             raise ValueError("out_lse must be [T,H]")
-    d = CombineDesc(num_tokens=T, num_heads=H, head_dim=D, lse_base=int(lse_base),
+    d = CombineDesc(num_tokens=_int32(T, "tokens"), num_heads=_int32(H, "heads"), head_dim=_int32(D, "head_dim"),
+                    lse_base=lse_base,
                     out_lse=out_lse.data_ptr() if out_lse is not None else None)
     with _on(dev):
-        st = load_library().mla_lse_combine(partials.data_ptr(), lses.data_ptr(), int(num_parts),
+        st = load_library().mla_lse_combine(partials.data_ptr(), lses.data_ptr(), num_parts,
                                             out.data_ptr(), ctypes.byref(d), _stream_ptr(stream, dev))
     _check(st)
     return out
@@ -493,6 +512,8 @@ def decode_partial_noalloc(q, kv_pages, block_table, seq_lens, part_id: int, num
     callers that cannot allocate device memory (see include/mla_decode.h).
     It uses scratch built into the library, shared by every call: calls that
     may overlap on the GPU must be serialised by the caller."""
+    part_id, num_parts = _int32(part_id, "part_id"), _int32(num_parts, "num_parts")
+    lse_base = _int32(lse_base, "lse_base")
     dev = q.device
     if dev.type != "cuda":
         raise ValueError("decode_partial_noalloc runs on CUDA tensors only")
@@ -511,7 +532,7 @@ def decode_partial_noalloc(q, kv_pages, block_table, seq_lens, part_id: int, num
     fn.restype = i32
     with _on(dev):
         st = fn(q.data_ptr(), kv_pages.data_ptr(), block_table.data_ptr(), seq_lens.data_ptr(),
-                int(part_id), int(num_parts), float(sm_scale), int(lse_base), out.data_ptr(),
+                part_id, num_parts, float(sm_scale), lse_base, out.data_ptr(),
                 lse.data_ptr(), ctypes.byref(d), _stream_ptr(stream, dev))
     _check(st)
     return out, lse
@@ -546,14 +567,15 @@ def decode_window(q, kv_pages, block_table, seq_lens, window: int, sinks: int, s
     own and the request's first `sinks` tokens.  Tensors as for
     decode_partial (q [B,q_len,H,576], 1..16 query tokens); the workspace is
     make_workspace's.  Entries of pages out of view may be -1."""
+    window, sinks, lse_base = _int32(window, "window"), _int32(sinks, "sinks"), _int32(lse_base, "lse_base")
     dev, d = _view_args("decode_window", q, kv_pages, block_table, seq_lens, out, lse, kv_scale)
     if workspace is None:
         with _allocating_on(stream, dev):
             workspace = make_workspace(q, kv_pages, block_table, kv_scale)
     _need(workspace, "workspace", (torch.uint8,), dev)
     _launch(load_library().mla_decode_window, dev, stream, q.data_ptr(), kv_pages.data_ptr(),
-            block_table.data_ptr(), seq_lens.data_ptr(), int(window), int(sinks), float(sm_scale),
-            int(lse_base), out.data_ptr(), lse.data_ptr(), ctypes.byref(d), workspace.data_ptr(),
+            block_table.data_ptr(), seq_lens.data_ptr(), window, sinks, float(sm_scale),
+            lse_base, out.data_ptr(), lse.data_ptr(), ctypes.byref(d), workspace.data_ptr(),
             workspace.numel())
     return out, lse
 
@@ -562,7 +584,7 @@ def make_shared_workspace(q, kv_pages, block_table, num_groups: int, kv_scale: f
     """A zero-filled workspace for decode_shared over num_groups groups."""
     d = _decode_desc(q, kv_pages, block_table, kv_scale)
     with torch.cuda.device(q.device):
-        n = load_library().mla_decode_shared_workspace_size(ctypes.byref(d), int(num_groups), 0)
+        n = load_library().mla_decode_shared_workspace_size(ctypes.byref(d), _int32(num_groups, "num_groups"), 0)
     if n == 0:
         raise MlaError(-2, "cannot size a workspace for these shapes")
     return torch.zeros(n, dtype=torch.uint8, device=q.device)
@@ -574,6 +596,7 @@ def decode_shared(q, kv_pages, block_table, seq_lens, group_starts, shared_pages
     (int32 [G + 1], from 0 to B) have their first shared_pages[g] (int32 [G])
     pages in common, which are read and multiplied once for the group.
     Tensors as for decode_partial; the workspace is make_shared_workspace's."""
+    lse_base = _int32(lse_base, "lse_base")
     dev, d = _view_args("decode_shared", q, kv_pages, block_table, seq_lens, out, lse, kv_scale)
     _need(group_starts, "group_starts", (torch.int32,), dev)
     _need(shared_pages, "shared_pages", (torch.int32,), dev)
@@ -586,13 +609,13 @@ def decode_shared(q, kv_pages, block_table, seq_lens, group_starts, shared_pages
     _need(workspace, "workspace", (torch.uint8,), dev)
     _launch(load_library().mla_decode_shared, dev, stream, q.data_ptr(), kv_pages.data_ptr(),
             block_table.data_ptr(), seq_lens.data_ptr(), group_starts.data_ptr(), shared_pages.data_ptr(),
-            groups, float(sm_scale), int(lse_base), out.data_ptr(), lse.data_ptr(), ctypes.byref(d),
+            _int32(groups, "groups"), float(sm_scale), lse_base, out.data_ptr(), lse.data_ptr(), ctypes.byref(d),
             workspace.data_ptr(), workspace.numel())
     return out, lse
 
 
 def pages_workspace_size(num_pages: int) -> int:
-    n = load_library().mla_pages_workspace_size(int(num_pages))
+    n = load_library().mla_pages_workspace_size(_int32(num_pages, "num_pages"))
     if n == 0:
         raise MlaError(-2, "a pool has at least one page")
     return n
@@ -621,7 +644,7 @@ def _pages_desc(rows, width, pages, page_size, row, kv_dtype):
     if d is None:
         if len(_PAGES_DESCS) > 256:
             _PAGES_DESCS.clear()
-        d = _PAGES_DESCS[key] = PagesDesc(*key)
+        d = _PAGES_DESCS[key] = PagesDesc(*(_int32(n, "a size of the pool") for n in key))
     return ctypes.byref(d)
 
 
@@ -680,7 +703,7 @@ def pages_copy(src_pages, dst_pages, src, dst, *, error_word=None, stream=None):
     if error_word is not None:
         _need(error_word, "error_word", _I32, dev)
     _launch(load_library().mla_pages_copy, dev, stream, src_pages.data_ptr(), dst_pages.data_ptr(),
-            src.data_ptr(), dst.data_ptr(), n, dst_pages.shape[0],
+            src.data_ptr(), dst.data_ptr(), _int32(n, "n"), _int32(dst_pages.shape[0], "dst_num_pages"),
             _pages_desc(0, 1, shape[0], shape[1], shape[2], code), _opt(error_word))
     return dst_pages
 
@@ -701,7 +724,7 @@ def pages_fork(kv_pages, block_table, seq_lens, ref_counts, parents, children, *
         raise ValueError("parents and children must have the same length")
     ws = _pages_ws(workspace, ref_counts, stream)
     _launch(load_library().mla_pages_fork, dev, stream, kv_pages.data_ptr(), block_table.data_ptr(),
-            seq_lens.data_ptr(), ref_counts.data_ptr(), parents.data_ptr(), children.data_ptr(), n,
+            seq_lens.data_ptr(), ref_counts.data_ptr(), parents.data_ptr(), children.data_ptr(), _int32(n, "n"),
             _pages_desc(rows, width, pages, shape[1], shape[2], code), ws.data_ptr(), ws.numel(),
             _opt(error_word))
 
@@ -726,13 +749,14 @@ def pages_free(block_table, seq_lens, ref_counts, new_lens, *, window: int = 0, 
     """mla_pages_free: every request is shortened to new_lens[b] tokens (0
     ends it, its own length leaves it) and, with a window, gives up the pages
     that decode_window(window, sinks) no longer sees."""
+    window, sinks = _int32(window, "window"), _int32(sinks, "sinks")
     dev = block_table.device
     rows, width, pages = _books(dev, block_table, seq_lens, ref_counts, error_word)
     _ints(new_lens, "new_lens", dev, 1)
     if new_lens.numel() != rows:
         raise ValueError("new_lens must be [num_requests]")
     _launch(load_library().mla_pages_free, dev, stream, block_table.data_ptr(), seq_lens.data_ptr(),
-            ref_counts.data_ptr(), new_lens.data_ptr(), int(window), int(sinks),
+            ref_counts.data_ptr(), new_lens.data_ptr(), window, sinks,
             _pages_desc(rows, width, pages, 64, 576, KV_BF16), _opt(error_word))
 
 
