@@ -87,7 +87,7 @@ def main(argv=None):
     running[1:first] = 0                 # the prompts themselves do not grow
     for step in range(a.steps):
         if step == a.steps // 2:         # every other sample ends; close the gaps
-            running[first + 1::2] = 0    # (a group's shared pages are read from its first request)
+            running[first::2] = 0
             ended = (torch.arange(rows, device=dev) >= first) & (running == 0)
             mla.pages_free(table, lens, counts, torch.where(ended, 0, lens), error_word=err)
             mla.pages_compact(kv, table, counts, workspace=ws, error_word=err)

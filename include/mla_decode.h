@@ -405,9 +405,12 @@ int mla_decode_window(const void *q, const void *kv_pages, const int32_t *block_
  *               0, the last the batch, none is below its predecessor (an empty
  *               group is allowed).
  *  shared_pages int32 [num_groups]: the first shared_pages[g] entries of the
- *               group's block-table rows are the same pages (the first
- *               request's are read; 0: nothing is shared).  A request shorter
- *               than its group's shared pages sees its own tokens only.
+ *               group's block-table rows are the same pages (0: nothing is
+ *               shared).  A request shorter than its group's shared pages sees
+ *               its own tokens only, and its row need not name the pages past
+ *               its length: they are read from a request that reaches them
+ *               all, or from the longest.  So any request of a group may end
+ *               (length 0, its row given up) while the others go on.
  *  workspace    >= mla_decode_shared_workspace_size(d, num_groups, 0) bytes,
  *               same rules as for mla_decode_partial.
  *  sm_scale     finite and > 0.

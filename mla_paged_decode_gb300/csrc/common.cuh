@@ -289,7 +289,24 @@ __device__ __forceinline__ int group_of_request(const DecodeParams &p, int b) {
   return lo;
 }
 
-// Block v of R rows over a group's shared pages.
+// The longest of requests [b0, b1), but no further than one of at least `enough`
+// tokens: {its length, itself}.
+static __device__ __noinline__ int2 longest_request(const DecodeParams &p, int b0, int b1, int enough) {
+  int2 r = make_int2(-1, b0);
+  for (int b = b0; b < b1 && r.x < enough; b += 8) {
+    int len[8];
+#pragma unroll
+    for (int u = 0; u < 8; ++u) len[u] = checked_len(p, min(b + u, b1 - 1), nullptr);
+#pragma unroll
+    for (int u = 0; u < 8; ++u)
+      if (len[u] > r.x) r = make_int2(len[u], min(b + u, b1 - 1));
+  }
+  return r;
+}
+
+// Block v of R rows over a group's shared pages.  These are read from a request that
+// reaches them all, commonly the first, or else from the longest, as far as that
+// one goes: requests that are shorter, or have ended, need not name them any more.
 template <int R = 64>
 __device__ inline ViewReq shared_block(const DecodeParams &p, int v) {
   ViewReq r;
@@ -299,13 +316,18 @@ __device__ inline ViewReq shared_block(const DecodeParams &p, int v) {
     if (block_base<R>(p, mid) <= v) lo = mid;
     else hi = mid - 1;
   }
-  const int b0 = group_start(p, lo), rows = (group_start(p, lo + 1) - b0) * p.heads;
+  const int b0 = group_start(p, lo), b1 = group_start(p, lo + 1), rows = (b1 - b0) * p.heads;
   const int k = v - block_base<R>(p, lo);
   if (k < 0 || R * k >= rows) return r;
   r.row0 = b0 * p.heads + R * k;
   r.rows = min(R, rows - R * k);
   r.req = b0;
   r.tiles = group_shared_pages(p, lo);
+  if (checked_len(p, b0, nullptr) < r.tiles * kPage) {
+    const int2 longest = longest_request(p, b0, b1, r.tiles * kPage);
+    r.req = longest.y;
+    r.tiles = min(r.tiles, (longest.x + kPage - 1) / kPage);
+  }
   r.end = r.tiles * kPage;
   return r;
 }
