@@ -421,8 +421,8 @@ int mla_decode_window(const void *q, const void *kv_pages, const int32_t *block_
  * partial results are merged by their LSE.  Groups of 128 rows or more on
  * average take blocks of 128 rows on pairs of SMs when rows x tokens (64 *
  * max_pages_per_seq) reach 16 M, and then also the requests' own pages when a
- * request has more than 64 rows.  The shared pages' rows must be finite, also
- * where a shorter request does not see them.  A request outside every group
+ * request has more than 64 rows.  A row of the shared pages that some query of the
+ * group sees must be finite, also for the others.  A request outside every group
  * or a page number outside [0, max_pages_per_seq] is reported as
  * MLA_ERR_BOUNDS by mla_decode_check_workspace.  Arithmetic as for
  * mla_decode_window.  Two or three kernels.

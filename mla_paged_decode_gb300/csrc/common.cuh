@@ -323,12 +323,13 @@ __device__ inline ViewReq shared_block(const DecodeParams &p, int v) {
   r.rows = min(R, rows - R * k);
   r.req = b0;
   r.tiles = group_shared_pages(p, lo);
-  if (checked_len(p, b0, nullptr) < r.tiles * kPage) {
-    const int2 longest = longest_request(p, b0, b1, r.tiles * kPage);
-    r.req = longest.y;
-    r.tiles = min(r.tiles, (longest.x + kPage - 1) / kPage);
-  }
   r.end = r.tiles * kPage;
+  if (checked_len(p, b0, nullptr) < r.end) {
+    const int2 longest = longest_request(p, b0, b1, r.end);
+    r.req = longest.y;
+    r.end = min(r.end, longest.x);
+    r.tiles = (r.end + kPage - 1) / kPage;
+  }
   return r;
 }
 

@@ -43,8 +43,8 @@ using namespace sm100;
 
 namespace pair {
 constexpr int kThreads = 384;
-// kinds of the kernel: shared pages alone (all of whose rows are seen), windows,
-// shared pages and then the requests' own
+// kinds of the kernel: shared pages alone (all of whose rows are seen, but for a last
+// page that no request fills), windows, shared pages and then the requests' own
 constexpr int kWhole = 0, kWindow = 1, kTails = 2;
 constexpr int kRows = 64;                       // per CTA
 constexpr int kPairRows = 128;                  // per pair
@@ -222,6 +222,7 @@ struct TileWalk {
   // Every row of the tile's pages is seen (false for some such tiles of sinks): asked
   // once a tile, as the masks of four pages cost the producer a fifth of its time.
   __device__ __forceinline__ bool whole() const {
+    if (KIND == kWhole) return w.view.end % kPage == 0 || (int(t) + 1) * kTilePages * kPage <= w.view.end;
     const int k = int(t) * kTilePages - w.view.nsink, base = (w.view.first + k) * kPage;
     return k >= 0 && base >= w.view.lead && base + kTilePages * kPage <= w.view.end;
   }
@@ -328,7 +329,7 @@ __device__ __forceinline__ void produce(const DecodeParams &p, const CtaRange &r
         if (s < 0) return false;
         const uint32_t dst = sRing + s * kUnitBytes;
         const int block = (F8 ? 2 : 4) * int(rank), atom = page[i] * 8 + 4 * h;
-        if (KIND == kWhole || whole) tma_load_4d_pair(dst, tm_v, full, 0, 0, block, atom);
+        if (whole) tma_load_4d_pair(dst, tm_v, full, 0, 0, block, atom);
         else load_seen<F8>(dst, full, tm_v, tm_va, tm_vr, block, atom, p.num_pages * 8, seen[i] >> (32 * h));
       }
     }
@@ -354,12 +355,10 @@ __device__ __forceinline__ void produce(const DecodeParams &p, const CtaRange &r
       c.check(err);
 #pragma unroll
       for (int i = 0; i < kTilePages; ++i) pages[i] = c.page[i];
-      if (KIND != kWhole) {
-        whole = c.whole();
-        if (!whole) {
+      whole = c.whole();
+      if (!whole) {
 #pragma unroll
-          for (int i = 0; i < kTilePages; ++i) seen[i] = c.seen(i);
-        }
+        for (int i = 0; i < kTilePages; ++i) seen[i] = c.seen(i);
       }
       ok = load_k(c);
       c.step();

@@ -61,6 +61,21 @@ def test_no_request_reaches_the_shared_pages(kv_dtype, width, heads, q_len):
 
 
 @pytest.mark.parametrize("kv_dtype,width", KINDS)
+@pytest.mark.parametrize("heads,q_len", [(64, 1), (100, 2)])
+@pytest.mark.parametrize("longest", [449, 257, 256, 255, 65, 1])
+def test_rows_past_every_request_may_hold_anything(kv_dtype, width, heads, q_len, longest):
+    """The last shared page is partly written: its other rows hold NaN."""
+    lens = [min(320, longest), 0, longest, min(100, longest)]
+    c = make(lens, heads, q_len, kv_dtype, causal_seen(q_len), seed=85, shared=([0, 4], [12]), width=width)
+    at = torch.arange(longest, 12 * 64, device="cuda")
+    if kv_dtype == "e4m3":
+        c.kv[c.table[2, at // 64].long(), at % 64] = 0x7F
+    else:
+        c.kv[c.table[2, at // 64].long(), at % 64] = math.nan
+    check(c, *run_shared(c, [0, 4], [12]), what=f"longest {longest}")
+
+
+@pytest.mark.parametrize("kv_dtype,width", KINDS)
 def test_all_requests_of_a_group_have_ended(kv_dtype, width):
     c = make([700, 640, 655, 300, 260], 64, 1, kv_dtype, causal_seen(1), seed=83, shared=([0, 3, 5], [10, 4]), width=width)
     end(c, [0, 1, 2])
