@@ -289,54 +289,67 @@ __device__ __forceinline__ int group_of_request(const DecodeParams &p, int b) {
   return lo;
 }
 
-// The longest of requests [b0, b1), but no further than one of at least `enough`
-// tokens: {its length, itself}.
-static __device__ __noinline__ int2 longest_request(const DecodeParams &p, int b0, int b1, int enough) {
-  int2 r = make_int2(-1, b0);
-  for (int b = b0; b < b1 && r.x < enough; b += 8) {
-    int len[8];
-#pragma unroll
-    for (int u = 0; u < 8; ++u) len[u] = checked_len(p, min(b + u, b1 - 1), nullptr);
-#pragma unroll
-    for (int u = 0; u < 8; ++u)
-      if (len[u] > r.x) r = make_int2(len[u], min(b + u, b1 - 1));
-  }
-  return r;
-}
-
-// Block v of R rows over a group's shared pages.  These are read from a request that
-// reaches them all, commonly the first, or else from the longest, as far as that
-// one goes: requests that are shorter, or have ended, need not name them any more.
-template <int R = 64>
-__device__ inline ViewReq shared_block(const DecodeParams &p, int v) {
+// Blocks of R rows of a batch with shared pages: block v < `blocks` of a group's rows
+// over its shared pages, or (OWN) block v - blocks of the requests' rows over their
+// own pages.
+//
+// The shared pages are read from a request that reaches them all, commonly the first
+// of the group, or else from the longest; the others need not name them.  Where none
+// reaches them all, only the pages that the longest one fills count as shared: its
+// last page is left to the requests' own pages, where rows that nobody sees may hold
+// anything.  (The search is one plain loop for both kinds of blocks: as a call with
+// loads eight at a time, or twice, it cost the decode kernel's views 9 and 5 %,
+// windows too.)
+template <int R, bool OWN>
+__device__ __forceinline__ ViewReq shared_view(const DecodeParams &p, int v, int blocks) {
   ViewReq r;
-  int lo = 0, hi = p.num_groups - 1;  // the last group whose blocks start at or before v
+  const bool own = OWN && v >= blocks;
+  const int u = v - blocks, b = own ? u % p.batch : 0;
+  int lo = 0, hi = p.num_groups - 1;  // the last group that starts at or before the block, or request b
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
-    if (block_base<R>(p, mid) <= v) lo = mid;
+    if (own ? p.group_starts[mid] <= b : block_base<R>(p, mid) <= v) lo = mid;
     else hi = mid - 1;
   }
-  const int b0 = group_start(p, lo), b1 = group_start(p, lo + 1), rows = (b1 - b0) * p.heads;
-  const int k = v - block_base<R>(p, lo);
-  if (k < 0 || R * k >= rows) return r;
-  r.row0 = b0 * p.heads + R * k;
-  r.rows = min(R, rows - R * k);
-  r.req = b0;
-  r.tiles = group_shared_pages(p, lo);
-  r.end = r.tiles * kPage;
-  if (checked_len(p, b0, nullptr) < r.end) {
-    const int2 longest = longest_request(p, b0, b1, r.end);
-    r.req = longest.y;
-    r.end = min(r.end, longest.x);
-    r.tiles = (r.end + kPage - 1) / kPage;
+  const int b0 = group_start(p, lo), b1 = group_start(p, lo + 1);
+  int longest = 0;
+  if (own) {
+    const int g = u / p.batch;
+    longest = checked_len(p, b, nullptr);
+    r.row0 = b * p.heads + R * g;
+    r.rows = min(R, p.heads - R * g);
+    r.end = row_len(p, longest, min(p.heads, R * (g + 1)) - 1);
+    r.req = b;
+  } else {
+    const int k = v - block_base<R>(p, lo), rows = (b1 - b0) * p.heads;
+    if (k < 0 || R * k >= rows) return r;
+    r.row0 = b0 * p.heads + R * k;
+    r.rows = min(R, rows - R * k);
+    r.req = b0;
+  }
+  int pages = group_shared_pages(p, lo);
+#pragma unroll 1
+  for (int i = b0; i < b1 && longest < pages * kPage; ++i) {
+    const int L = checked_len(p, i, nullptr);
+    if (L > longest) {
+      longest = L;
+      if (!own) r.req = i;
+    }
+  }
+  pages = min(pages, longest / kPage);
+  if (own) {
+    r.first = pages;
+    r.tiles = max(0, (r.end + kPage - 1) / kPage - pages);
+  } else {
+    r.tiles = pages;
+    r.end = pages * kPage;
   }
   return r;
 }
 
-// Block u / B of R rows of request u mod B: through the window and the sinks, or
-// over the request's own pages (VIEW: p.view where the caller knows it).
-template <int R = 64, int VIEW = 0>
-__device__ inline ViewReq request_block(const DecodeParams &p, int u) {
+// Block u / B of R rows of request u mod B, through its window and its sinks.
+template <int R = 64>
+__device__ __forceinline__ ViewReq window_block(const DecodeParams &p, int u) {
   ViewReq r;
   const int b = u % p.batch, g = u / p.batch;
   r.req = b;
@@ -344,11 +357,6 @@ __device__ inline ViewReq request_block(const DecodeParams &p, int u) {
   r.rows = min(R, p.heads - R * g);
   const int L = checked_len(p, b, nullptr);
   r.end = row_len(p, L, min(p.heads, R * (g + 1)) - 1);
-  if ((VIEW ? VIEW : p.view) == kViewShared) {
-    r.first = group_shared_pages(p, group_of_request(p, b));
-    r.tiles = max(0, (r.end + kPage - 1) / kPage - r.first);
-    return r;
-  }
   if (r.end == 0) return r;
   // the block's first query sits at position L - T + R g / q_heads
   r.lead = max(0, L - p.q_len + (R * g) / p.q_heads + 1 - p.window);
@@ -359,8 +367,7 @@ __device__ inline ViewReq request_block(const DecodeParams &p, int u) {
 }
 
 __device__ inline ViewReq view_req(const DecodeParams &p, int v) {
-  if (p.view == kViewShared && v < p.prefix_blocks) return shared_block(p, v);
-  return request_block(p, p.view == kViewShared ? v - p.prefix_blocks : v);
+  return p.view == kViewShared ? shared_view<64, true>(p, v, p.prefix_blocks) : window_block(p, v);
 }
 
 // What row `row` (of all rows) of a block sees: tokens below `hi`, and of

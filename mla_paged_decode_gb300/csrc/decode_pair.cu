@@ -43,8 +43,8 @@ using namespace sm100;
 
 namespace pair {
 constexpr int kThreads = 384;
-// kinds of the kernel: shared pages alone (all of whose rows are seen, but for a last
-// page that no request fills), windows, shared pages and then the requests' own
+// kinds of the kernel: shared pages alone (all of whose rows are seen), windows,
+// shared pages and then the requests' own
 constexpr int kWhole = 0, kWindow = 1, kTails = 2;
 constexpr int kRows = 64;                       // per CTA
 constexpr int kPairRows = 128;                  // per pair
@@ -105,12 +105,8 @@ __device__ __forceinline__ uint32_t bar(uint64_t &b) { return smem_u32(&b); }
 // rows over its own pages, or of a request's rows through its window.
 template <int KIND>
 __device__ __forceinline__ ViewReq make_view(const DecodeParams &p, int v) {
-  if constexpr (KIND == kWindow) return request_block<kPairRows, kViewWindow>(p, v);
-  if constexpr (KIND == kTails) {
-    const int shared = p.pair_blocks - p.pair_tails;
-    if (v >= shared) return request_block<kPairRows, kViewShared>(p, v - shared);
-  }
-  return shared_block<kPairRows>(p, v);
+  if constexpr (KIND == kWindow) return window_block<kPairRows>(p, v);
+  else return shared_view<kPairRows, KIND == kTails>(p, v, p.pair_blocks - p.pair_tails);
 }
 template <int KIND>
 static __device__ __noinline__ ViewReq view_call(const DecodeParams &p, int v) {
@@ -222,7 +218,6 @@ struct TileWalk {
   // Every row of the tile's pages is seen (false for some such tiles of sinks): asked
   // once a tile, as the masks of four pages cost the producer a fifth of its time.
   __device__ __forceinline__ bool whole() const {
-    if (KIND == kWhole) return w.view.end % kPage == 0 || (int(t) + 1) * kTilePages * kPage <= w.view.end;
     const int k = int(t) * kTilePages - w.view.nsink, base = (w.view.first + k) * kPage;
     return k >= 0 && base >= w.view.lead && base + kTilePages * kPage <= w.view.end;
   }
@@ -329,7 +324,7 @@ __device__ __forceinline__ void produce(const DecodeParams &p, const CtaRange &r
         if (s < 0) return false;
         const uint32_t dst = sRing + s * kUnitBytes;
         const int block = (F8 ? 2 : 4) * int(rank), atom = page[i] * 8 + 4 * h;
-        if (whole) tma_load_4d_pair(dst, tm_v, full, 0, 0, block, atom);
+        if (KIND == kWhole || whole) tma_load_4d_pair(dst, tm_v, full, 0, 0, block, atom);
         else load_seen<F8>(dst, full, tm_v, tm_va, tm_vr, block, atom, p.num_pages * 8, seen[i] >> (32 * h));
       }
     }
@@ -355,10 +350,12 @@ __device__ __forceinline__ void produce(const DecodeParams &p, const CtaRange &r
       c.check(err);
 #pragma unroll
       for (int i = 0; i < kTilePages; ++i) pages[i] = c.page[i];
-      whole = c.whole();
-      if (!whole) {
+      if (KIND != kWhole) {
+        whole = c.whole();
+        if (!whole) {
 #pragma unroll
-        for (int i = 0; i < kTilePages; ++i) seen[i] = c.seen(i);
+          for (int i = 0; i < kTilePages; ++i) seen[i] = c.seen(i);
+        }
       }
       ok = load_k(c);
       c.step();
@@ -549,37 +546,41 @@ __device__ __forceinline__ bool split_q(const DecodeParams &p, Misc &m, unsigned
   const int warp = st >> 5, lane = st & 31, first = warp * kWarpRows;
   const int rows = min(kRows, max(0, view.rows - int(rank) * kRows));
   const uint4 *src = reinterpret_cast<const uint4 *>(p.q + (size_t(view.row0) + rank * kRows + first) * kDqk);
+  // round u of a warp's loads meets row 32 u / 72 and, from lane `next_row(u)` on,
+  // the one after it
+  auto row_of = [](int u) { return 32 * u / kChunks; };
+  auto next_row = [&](int u) { return (row_of(u) + 1) * kChunks - 32 * u; };
+  const int left = (rows - first) * kChunks;
   uint4 v[kPer];
-  uint32_t mx[kPer];
+#pragma unroll
+  for (int u = 0; u < kPer; ++u) v[u] = lane + 32 * u < left ? __ldg(src + lane + 32 * u) : make_uint4(0, 0, 0, 0);
+  uint32_t row_mx[kWarpRows] = {};
 #pragma unroll
   for (int u = 0; u < kPer; ++u) {
-    const int i = lane + 32 * u;
-    v[u] = first + i / kChunks < rows ? __ldg(src + i) : make_uint4(0, 0, 0, 0);
+    const uint32_t mx = largest_bf16x8(v[u]);
+    uint32_t &row = row_mx[row_of(u)];
+    if (next_row(u) >= 32) {
+      row = __vmaxu2(row, mx);
+    } else {
+      row = __vmaxu2(row, lane < next_row(u) ? mx : 0u);
+      row_mx[row_of(u) + 1] = lane < next_row(u) ? 0u : mx;
+    }
   }
-#pragma unroll
-  for (int u = 0; u < kPer; ++u) {
-    mx[u] = largest_bf16x8(v[u]);
-    mx[u] = max(mx[u] & 0xffffu, mx[u] >> 16);
-  }
-  // a row's chunks lie in the registers u of at most four rounds of loads
-  uint32_t row_mx[kWarpRows];
+  float row_sc[kWarpRows];
 #pragma unroll
   for (int w = 0; w < kWarpRows; ++w) {
-    uint32_t x = 0;
-#pragma unroll
-    for (int u = w * kChunks / 32; u <= ((w + 1) * kChunks - 1) / 32; ++u)
-      if ((lane + 32 * u) / kChunks == w) x = max(x, mx[u]);
-    row_mx[w] = __reduce_max_sync(0xffffffffu, x);
-    if (lane == 0) m.qinv[first + w] = row_q_scale(row_mx[w]).inv;
+    const QScale s = row_q_scale(__reduce_max_sync(0xffffffffu, max(row_mx[w] & 0xffffu, row_mx[w] >> 16)));
+    row_sc[w] = s.scale;
+    if (lane == 0) m.qinv[first + w] = s.inv;
   }
   named_sync(1, kSoftThreads);  // (every thread reads its row's)
   ok = ok && __all_sync(0xffffffffu, mbar_wait_clk(bar(m.q_empty), (piece & 1) ^ 1, &m.abort, kTimeoutClk));
   if (!ok) return false;
 #pragma unroll
   for (int u = 0; u < kPer; ++u) {
-    const int i = lane + 32 * u, w = i / kChunks, rr = first + w, c = i - kChunks * w;
-    const int w0 = 32 * u / kChunks, w1 = (32 * u + 31) / kChunks;  // the rows that round u of the loads meets
-    const float sc = row_q_scale(w == w0 ? row_mx[w0] : row_mx[w1]).scale;
+    const bool next = lane >= next_row(u);
+    const int w = row_of(u) + (next ? 1 : 0), rr = first + w, c = lane + 32 * u - kChunks * w;
+    const float sc = next_row(u) < 32 && next ? row_sc[row_of(u) + 1] : row_sc[row_of(u)];
     const uint32_t wv[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
     uint32_t hw[2] = {0, 0}, lw[2] = {0, 0};
 #pragma unroll
@@ -871,7 +872,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   // blocks without pages: no partials, or the neutral pair
   if constexpr (KIND == kWindow) {
     for (int v = int(blockIdx.x); v < p.pair_blocks; v += int(gridDim.x)) {
-      const ViewReq w = request_block<kPairRows>(p, v);
+      const ViewReq w = window_block<kPairRows>(p, v);
       if (tid == 0) checked_len(p, w.req, err);
       if (w.tiles != 0) continue;
       if (tid < 2 && w.rows > tid * kRows)
