@@ -112,7 +112,8 @@ size_t mla_decode_workspace_size(const mla_decode_desc *d, int num_sms);
  *  block_table int32 [B, max_pages_per_seq]: logical page i of request b lives
  *              in physical page block_table[b][i].  Entries past the request's
  *              last page are never read.
- *  seq_lens    int32 [B]: GLOBAL sequence lengths L_b (tokens 0..L_b-1 exist).
+ *  seq_lens    int32 [B]: GLOBAL sequence lengths L_b (tokens 0..L_b-1 exist), at
+ *              most 64 * max_pages_per_seq and 2^31 - 64.
  *  part_id, num_parts
  *              the partition attends exactly to the global tokens t < L_b with
  *              t mod num_parts == part_id (round-robin owner rule).  A real DCP

@@ -164,10 +164,14 @@ __device__ __forceinline__ int part_of(const DecodeParams &p, int bv) {
   return p.fused ? bv / p.req_batch : p.part_id;
 }
 
+// Pages of the longest request: lengths and their sums with a page stay below 2^31,
+// however wide the block table is.
+constexpr int kMaxRequestPages = (1 << 25) - 1;
+
 // Clamp a global length to what the block table can hold; flag a bad one.
 __device__ __forceinline__ int checked_len(const DecodeParams &p, int b, int *err) {
   int L = p.seq_lens[b];
-  int cap = p.max_pages * kPage;
+  int cap = min(p.max_pages, kMaxRequestPages) * kPage;
   if (L < 0 || L > cap) {
     if (err) atomicOr(err, kErrBadLen);
     L = L < 0 ? 0 : cap;
@@ -276,7 +280,7 @@ __device__ __forceinline__ int block_base(const DecodeParams &p, int g) {
   return int((long long)group_start(p, g) * p.heads / R) + g;
 }
 __device__ __forceinline__ int group_shared_pages(const DecodeParams &p, int g) {
-  return min(max(p.shared_pages[g], 0), p.max_pages);
+  return min(max(p.shared_pages[g], 0), min(p.max_pages, kMaxRequestPages));
 }
 // The last group that starts at or before request b.
 __device__ __forceinline__ int group_of_request(const DecodeParams &p, int b) {

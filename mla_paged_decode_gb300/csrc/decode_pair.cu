@@ -219,7 +219,7 @@ struct TileWalk {
   // once a tile, as the masks of four pages cost the producer a fifth of its time.
   __device__ __forceinline__ bool whole() const {
     const int k = int(t) * kTilePages - w.view.nsink, base = (w.view.first + k) * kPage;
-    return k >= 0 && base >= w.view.lead && base + kTilePages * kPage <= w.view.end;
+    return k >= 0 && base >= w.view.lead && base <= w.view.end - kTilePages * kPage;
   }
   // rows of page i that some row of the block sees (none past the view)
   __device__ unsigned long long seen(int i) const {
