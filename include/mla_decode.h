@@ -422,11 +422,15 @@ int mla_decode_window(const void *q, const void *kv_pages, const int32_t *block_
  * partial results are merged by their LSE.  Groups of 128 rows or more on
  * average take blocks of 128 rows on pairs of SMs when rows x tokens (64 *
  * max_pages_per_seq) reach 16 M, and then also the requests' own pages when a
- * request has more than 64 rows.  A row of the shared pages that some query of the
- * group sees must be finite, also for the others.  A request outside every group
- * or a page number outside [0, max_pages_per_seq] is reported as
- * MLA_ERR_BOUNDS by mla_decode_check_workspace.  Arithmetic as for
- * mla_decode_window.  Two or three kernels.
+ * request has more than 64 rows.  The width of block_table stands for the
+ * tokens there, which the host does not know: with a table much wider than
+ * the requests are long, that kernel also takes short shared pages, in 6 to
+ * 20 us more, and the last bits of the result may differ from those with a
+ * narrower table.  A row of the shared pages that some query of the group
+ * sees must be finite, also for the others.  A request outside every group or
+ * a page number outside [0, max_pages_per_seq] is reported as MLA_ERR_BOUNDS
+ * by mla_decode_check_workspace.  Arithmetic as for mla_decode_window.  Two or
+ * three kernels.
  */
 size_t mla_decode_shared_workspace_size(const mla_decode_desc *d, int num_groups, int num_sms);
 

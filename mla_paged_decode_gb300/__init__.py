@@ -19,7 +19,8 @@ __all__ = [
     "MlaError", "LSE_NATURAL", "LSE_BASE2", "decode_partial", "lse_combine",
     "workspace_size", "make_workspace", "check_workspace", "library_path", "load_library",
     "decode_partial_noalloc", "decode_window", "decode_shared", "make_shared_workspace",
-    "pages_workspace_size", "make_pages_workspace", "pages_copy", "pages_fork", "pages_alloc", "pages_free", "pages_compact", "PAGES_BAD_ENTRY", "PAGES_FULL",
+    "pages_workspace_size", "make_pages_workspace", "pages_copy", "pages_fork", "pages_alloc",
+    "pages_free", "pages_compact", "PAGES_BAD_ENTRY", "PAGES_FULL",
 ]
 
 LSE_NATURAL = 0
@@ -217,7 +218,7 @@ def _kv_dtype_code(kv_pages: torch.Tensor) -> int:
 
 
 _KV_TYPES = (torch.bfloat16, torch.uint8, torch.float8_e4m3fn)
-_I32, _BF16, _F32, _U8 = (torch.int32,), (torch.bfloat16,), (torch.float32,), (torch.uint8,)
+_I32 = (torch.int32,)
 _DESCS: dict = {}
 
 

@@ -575,7 +575,12 @@ bool window_pair_path(const mla_decode_desc *d, int window, int sinks) {
 // table bound the work.  Measured, us a call, pair kernel / blocks of 64 rows in
 // the one kernel, bf16: 4096 rows x 1K shared tokens 44 / 34, 1024 x 8K 44 / 38,
 // 256 x 32K 42 / 42, 512 x 32K 57 / 62, 4096 x 8K 79 / 102, 4096 x 32K 214 / 363;
-// e4m3: 50 / 44, 53 / 43, 49 / 42, 60 / 57, 85 / 95, 193 / 277.
+// e4m3: 50 / 44, 53 / 43, 49 / 42, 60 / 57, 85 / 95, 193 / 277.  These tables were
+// as wide as the work; only the device knows the tokens.  A table made for far
+// longer requests sends short shared pages to the pair kernel too: 2,200 columns,
+// captured into a graph, 128 rows over 256 shared tokens and 100 own ones 32.5 /
+// 18.4, over 4K 32.8 / 22.5, 1024 rows over 1K 36.9 / 22.6, over 8K 47 / 41; e4m3
+// 45 / 29, 45 / 35, 50 / 35, 60 / 49.
 constexpr long long kPairWork = 16LL << 20;
 bool pair_path(const mla_decode_desc *d, int num_groups) {
   const long long rows = (long long)d->batch * rows_of(d);
@@ -927,13 +932,16 @@ int mla_decode_window(const void *q, const void *kv_pages, const int32_t *block_
   mla::DecodeParams p;
   p.view = mla::kViewWindow;
   if (window_pair_path(d, window, sinks)) {
+    // (all pairs, not 16 pieces a block as below: capped, one request of 128 rows took
+    // 34.9 us instead of 41.0 at a window of 16,000, 28.7 instead of 30.8 at 8,192, and
+    // two or four requests the same or up to 4 us more)
     p.pair_blocks = d->batch * ((rows_of(d) + 127) / 128);
     p.pairs = f.sms / 2;
   }
   // (longer than any request: the kernel's sums with them stay in 32 bits)
   p.window = window < kMaxView ? window : kMaxView;
   p.sinks = sinks < kMaxView ? sinks : kMaxView;
-  // Up to 16 pieces a block: the merge takes a block's pieces one after another,
+  // Blocks of 64 rows: up to 16 pieces a block.  The merge takes a block's pieces one after another,
   // and one request cut across all CTAs waits longer for it than it gains.
   // Measured, us a call, 8 / 16 / 24 pieces / all CTAs, bf16, 64 rows: 1 request,
   // window 2000 21.3 / 20.2 / 20.5 / 25.5, 4096 27.0 / 23.4 / 22.3 / 37.0; 4
