@@ -553,6 +553,10 @@ mla::WorkspaceLayout shared_layout(const mla_decode_desc *d, int num_groups, int
   const int slots = v + num_groups + d->batch + 2 * grid;
   return mla::workspace_layout(v, (slots + 1) / 2);
 }
+// ... and, after all that, the groups' table.
+size_t shared_workspace_bytes(const mla::WorkspaceLayout &wl, int num_groups) {
+  return mla::align256(wl.total + sizeof(int2) * size_t(num_groups));
+}
 // The pair kernel takes windows of requests with more than one block of 64 rows
 // in the other kernel; its start and end take 2 to 5 us longer on a bf16 cache,
 // which rows x tokens in view (at most) have to make up for.  Measured, us a
@@ -963,7 +967,7 @@ size_t mla_decode_shared_workspace_size(const mla_decode_desc *d, int num_groups
     if (f.sms <= 0) return 0;
     num_sms = f.sms;
   }
-  return shared_layout(d, num_groups, num_sms).total;
+  return shared_workspace_bytes(shared_layout(d, num_groups, num_sms), num_groups);
 }
 
 int mla_decode_shared(const void *q, const void *kv_pages, const int32_t *block_table,
@@ -981,12 +985,13 @@ int mla_decode_shared(const void *q, const void *kv_pages, const int32_t *block_
   DeviceFacts f = current_device(&st);
   if (st != MLA_OK) return st;
   const auto wl = shared_layout(d, num_groups, f.sms);
-  if (workspace_bytes < wl.total) return MLA_ERR_WORKSPACE;
+  if (workspace_bytes < shared_workspace_bytes(wl, num_groups)) return MLA_ERR_WORKSPACE;
   mla::DecodeParams p;
   p.view = mla::kViewShared;
   p.group_starts = group_starts;
   p.shared_pages = shared_pages;
   p.num_groups = num_groups;
+  p.group_table = reinterpret_cast<int2 *>(static_cast<unsigned char *>(workspace) + wl.total);
   if (pair_path(d, num_groups)) {
     // the tails of requests with more than one block of 64 rows go along, a launch
     // less and the pair kernel's rate; us a call, tails along / in the other kernel,

@@ -90,13 +90,14 @@ struct DecodeParams {
   // slots ends just past its last owned token.  Otherwise strided = 0.
   int strided = 0, apg = 0;
   int s_q63 = 0, s_r63 = 0, s_c64 = 0;  // strided: 63 / P, 63 mod P, 64 mod P
-  // Views (tensor-core kernel, MULTI == 3; see ViewReq): 0 none, kViewWindow
+  // Views (tensor-core kernel, MULTI >= 3; see ViewReq): 0 none, kViewWindow
   // (window, sinks) or kViewShared (groups of requests with shared pages;
   // `prefix_blocks` bounds the 64-row blocks of all groups).
   int view = 0;
   int window = 0, sinks = 0;
   const int32_t *group_starts = nullptr;  // [num_groups + 1]
   const int32_t *shared_pages = nullptr;  // [num_groups]
+  int2 *group_table = nullptr;            // [num_groups], in the workspace (see fill_group_table)
   int num_groups = 0, prefix_blocks = 0;
   // Shared pages, or windows, attended by the pair kernel (csrc/decode_pair.cu) in
   // pair_blocks blocks of 128 rows on `pairs` CTA pairs; prefix_blocks is then 0.
@@ -255,6 +256,7 @@ struct ViewReq {
   int first = 0, nsink = 0;
   int end = 0;             // tokens from here on are not seen by any row
   int lead = 0;            // window: tokens below are not seen, sinks aside
+  bool unsure = false;     // shared pages: the group's table is needed (see shared_view)
   __device__ __forceinline__ int page(long long t) const {
     return t < nsink ? int(t) : int(t) - nsink + first;
   }
@@ -293,22 +295,51 @@ __device__ __forceinline__ int group_of_request(const DecodeParams &p, int b) {
   return lo;
 }
 
+// The pages that the requests of each group attend to together, and the request whose
+// row names them: {pages, request}.  Commonly the first request of a group reaches
+// all its shared pages, and no table is needed.  Where it does not (it has ended, or
+// is shorter), they are read from a request that reaches them all, or else from the
+// longest, and then only the pages that it fills count as shared: its last page is
+// left to the requests' own, where rows that nobody sees may hold anything.
+//
+// Every CTA that meets such a group fills the table for itself, a warp a group, and
+// makes its schedule anew; all of them write the same words.  (A search by each view
+// instead, with a group's first half ended: 1,024 requests x 16 heads 509 us against
+// 134 with none ended, 512 x 128 10,190 against 377, as most views of a long batch
+// searched through half of it; and its loop in every role cost the other calls up
+// to 9 %.)
+static __device__ __noinline__ void fill_group_table(const DecodeParams &p) {
+  const int lane = threadIdx.x & 31;
+  for (int g = int(threadIdx.x) >> 5; g < p.num_groups; g += int(blockDim.x) >> 5) {
+    const int b0 = group_start(p, g), b1 = group_start(p, g + 1), pages = group_shared_pages(p, g);
+    int len = 0, who = b0;
+    for (int b = b0; b < b1; b += 128) {
+      int L[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) L[u] = b + lane + 32 * u < b1 ? checked_len(p, b + lane + 32 * u, nullptr) : 0;
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+        if (L[u] > len) len = L[u], who = b + lane + 32 * u;
+      if (__any_sync(0xffffffffu, len >= pages * kPage)) break;
+    }
+    for (int o = 16; o; o >>= 1) {  // the longest; the first of equals
+      const int l = __shfl_xor_sync(0xffffffffu, len, o), b = __shfl_xor_sync(0xffffffffu, who, o);
+      if (l > len || (l == len && b < who)) len = l, who = b;
+    }
+    if (lane == 0) p.group_table[g] = make_int2(min(pages, len / kPage), who);
+  }
+}
+
 // Blocks of R rows of a batch with shared pages: block v < `blocks` of a group's rows
 // over its shared pages, or (OWN) block v - blocks of the requests' rows over their
-// own pages.
-//
-// The shared pages are read from a request that reaches them all, commonly the first
-// of the group, or else from the longest; the others need not name them.  Where none
-// reaches them all, only the pages that the longest one fills count as shared: its
-// last page is left to the requests' own pages, where rows that nobody sees may hold
-// anything.  (The search is one plain loop for both kinds of blocks: as a call with
-// loads eight at a time, or twice, it cost the decode kernel's views 9 and 5 %,
-// windows too.)
+// own pages.  `groups`: the table, or null where it is not needed; the view then says
+// (`unsure`) if it is.
 template <int R, bool OWN>
-__device__ __forceinline__ ViewReq shared_view(const DecodeParams &p, int v, int blocks) {
+__device__ __forceinline__ ViewReq shared_view(const DecodeParams &p, int v, int blocks, const int2 *groups) {
   ViewReq r;
   const bool own = OWN && v >= blocks;
-  const int u = v - blocks, b = own ? u % p.batch : 0;
+  const int u = v - blocks, b = own ? u % p.batch : 0, L = own ? checked_len(p, b, nullptr) : 0;
+  if (own && L == 0) return r;  // (roles walk over runs of ended requests one by one)
   int lo = 0, hi = p.num_groups - 1;  // the last group that starts at or before the block, or request b
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
@@ -316,37 +347,27 @@ __device__ __forceinline__ ViewReq shared_view(const DecodeParams &p, int v, int
     else hi = mid - 1;
   }
   const int b0 = group_start(p, lo), b1 = group_start(p, lo + 1);
-  int longest = 0;
+  int2 shared = make_int2(0, b0);
+  if (groups) shared = groups[lo];
+  else shared.x = group_shared_pages(p, lo);
   if (own) {
     const int g = u / p.batch;
-    longest = checked_len(p, b, nullptr);
     r.row0 = b * p.heads + R * g;
     r.rows = min(R, p.heads - R * g);
-    r.end = row_len(p, longest, min(p.heads, R * (g + 1)) - 1);
+    r.end = row_len(p, L, min(p.heads, R * (g + 1)) - 1);
     r.req = b;
+    r.first = shared.x;
+    r.tiles = max(0, (r.end + kPage - 1) / kPage - shared.x);
+    r.unsure = !groups && L < shared.x * kPage;
   } else {
     const int k = v - block_base<R>(p, lo), rows = (b1 - b0) * p.heads;
     if (k < 0 || R * k >= rows) return r;
     r.row0 = b0 * p.heads + R * k;
     r.rows = min(R, rows - R * k);
-    r.req = b0;
-  }
-  int pages = group_shared_pages(p, lo);
-#pragma unroll 1
-  for (int i = b0; i < b1 && longest < pages * kPage; ++i) {
-    const int L = checked_len(p, i, nullptr);
-    if (L > longest) {
-      longest = L;
-      if (!own) r.req = i;
-    }
-  }
-  pages = min(pages, longest / kPage);
-  if (own) {
-    r.first = pages;
-    r.tiles = max(0, (r.end + kPage - 1) / kPage - pages);
-  } else {
-    r.tiles = pages;
-    r.end = pages * kPage;
+    r.req = shared.y;
+    r.tiles = shared.x;
+    r.end = shared.x * kPage;
+    r.unsure = !groups && checked_len(p, b0, nullptr) < r.end;
   }
   return r;
 }
@@ -370,8 +391,18 @@ __device__ __forceinline__ ViewReq window_block(const DecodeParams &p, int u) {
   return r;
 }
 
-__device__ inline ViewReq view_req(const DecodeParams &p, int v) {
-  return p.view == kViewShared ? shared_view<64, true>(p, v, p.prefix_blocks) : window_block(p, v);
+// What the roles of a CTA start from: the first piece's view, and the groups' table or
+// null (in shared memory: held in registers it made the softmax of an e4m3 cache spill).
+struct ViewStart {
+  ViewReq view;
+  const int2 *groups;
+};
+
+// MULTI: 3 windows, 4 shared pages.
+template <int MULTI>
+__device__ __forceinline__ ViewReq view_req(const DecodeParams &p, int v, const int2 *groups) {
+  if constexpr (MULTI == 3) return window_block(p, v);
+  else return shared_view<64, true>(p, v, p.prefix_blocks, groups);
 }
 
 // What row `row` (of all rows) of a block sees: tokens below `hi`, and of
@@ -379,10 +410,11 @@ __device__ inline ViewReq view_req(const DecodeParams &p, int v) {
 struct RowView {
   int lo, hi;
 };
+template <bool WINDOW>
 __device__ __forceinline__ RowView row_view(const DecodeParams &p, const ViewReq &r, int row) {
   const int b = min(row / p.heads, p.batch - 1);
   const int pos = checked_len(p, b, nullptr) - p.q_len + (row - b * p.heads) / p.q_heads;
-  return RowView{p.view == kViewWindow ? max(0, pos + 1 - p.window) : 0, min(max(0, pos + 1), r.end)};
+  return RowView{WINDOW ? max(0, pos + 1 - p.window) : 0, min(max(0, pos + 1), r.end)};
 }
 
 // Owned tokens of virtual request v (its group's widest row).
@@ -432,7 +464,6 @@ __device__ inline OwnerMask owner_mask_of(const DecodeParams &p) {
 
 template <int MULTI = 0>
 __device__ __forceinline__ int request_tiles(const DecodeParams &p, int v) {
-  if constexpr (MULTI == 3) return view_req(p, v).tiles;
   return (request_len<MULTI>(p, v, nullptr) + kTile - 1) / kTile;
 }
 
@@ -456,7 +487,7 @@ __device__ __forceinline__ int request_tiles(const DecodeParams &p, int v) {
 // Virtual requests of a launch.
 template <int MULTI = 0>
 __device__ __forceinline__ int virtual_requests(const DecodeParams &p) {
-  return p.batch * p.head_groups + (MULTI == 3 ? p.prefix_blocks : 0);
+  return p.batch * p.head_groups + (MULTI == 4 ? p.prefix_blocks : 0);
 }
 
 struct CtaRange {
@@ -589,6 +620,23 @@ __device__ __forceinline__ void schedule_range(int V, int idx, int workers, Tile
   __syncthreads();
 }
 
+// The same for shared pages, tiles_of(v, groups, &unsure); fills the groups' table when one of
+// them is unsure without it.  Returns the table or null, the same for all threads.
+template <int PC, typename Tiles>
+__device__ __forceinline__ const int2 *schedule_views(const DecodeParams &p, int V, int idx, int workers,
+                                                      Tiles tiles_of, CtaRange *r, long long *scratch) {
+  const int2 *groups = nullptr;
+#pragma unroll 1
+  for (;;) {
+    bool unsure = false;
+    schedule_range<PC, true>(V, idx, workers, [&](int v) { return tiles_of(v, groups, &unsure); }, r, scratch);
+    if (groups || !__syncthreads_or(unsure)) return groups;
+    fill_group_table(p);
+    __syncthreads();
+    groups = p.group_table;
+  }
+}
+
 // This CTA's range of a launch whose workers are its CTAs.
 template <int MULTI = 0, int PC = kPieceCost>
 __device__ inline void cta_schedule(const DecodeParams &p, CtaRange *r, long long *scratch) {
@@ -646,21 +694,43 @@ __device__ __forceinline__ uint32_t largest_bf16x8(uint4 v) {
   return __vmaxu2(__vmaxu2(v.x & 0x7fff7fffu, v.y & 0x7fff7fffu), __vmaxu2(v.z & 0x7fff7fffu, v.w & 0x7fff7fffu));
 }
 
-// 2^k and 2^-k with which q enters as two e4m3 terms: the largest |q|, as bf16 bits
-// `mx`, comes to lie in [2^7, 2^8).  An Inf or NaN keeps k = 0.
-struct QScale {
-  float scale, inv;
-};
-__device__ __forceinline__ QScale q_scale(uint32_t mx) {
+// 2^k with which q enters as two e4m3 terms: the largest |q|, as bf16 bits `mx`, comes
+// to lie in [2^7, 2^8).  An Inf or NaN keeps k = 0.
+__device__ __forceinline__ float q_scale(uint32_t mx) {
   const int k = mx < 0x7f80u ? min(126, max(-126, 134 - int(mx >> 7))) : 0;
-  return QScale{__int_as_float((127 + k) << 23), __int_as_float((127 - k) << 23)};
+  return __int_as_float((127 + k) << 23);
 }
 // The same for a scale that one row has to itself: a row with an Inf or a NaN
 // turns into NaN (saturated to e4m3's range, an Inf would read as a number).
-__device__ __forceinline__ QScale row_q_scale(uint32_t mx) {
-  QScale s = q_scale(mx);
-  if (mx >= 0x7f80u) s.scale = __int_as_float(0x7fffffff);
-  return s;
+__device__ __forceinline__ float row_q_scale(uint32_t mx) {
+  return mx < 0x7f80u ? q_scale(mx) : __int_as_float(0x7fffffff);
+}
+// 2^-k (of NaN: any finite number, as the scores are NaN already).
+__device__ __forceinline__ float inverse_q_scale(float scale) {
+  return scale == scale ? __int_as_float((254 << 23) - __float_as_int(scale)) : 1.f;
+}
+
+// 2^k of whole rows of Q that a warp holds, lane + 32 u their chunk (8 of 576 dims) in
+// v[u]: nine loads are four rows.
+template <int N>
+__device__ __forceinline__ void row_q_scales(const uint4 (&v)[N], int lane, float (&scale)[N * 32 / 72]) {
+  static_assert(N % 9 == 0, "whole rows");
+  uint32_t mx[N * 32 / 72] = {};
+#pragma unroll
+  for (int u = 0; u < N; ++u) {
+    // load u meets row 32 u / 72 and, from lane `next` on, the one after it
+    const int row = 32 * u / 72, next = (row + 1) * 72 - 32 * u;
+    const uint32_t x = largest_bf16x8(v[u]);
+    if (next >= 32) {
+      mx[row] = __vmaxu2(mx[row], x);
+    } else {
+      mx[row] = __vmaxu2(mx[row], lane < next ? x : 0u);
+      mx[row + 1] = lane < next ? 0u : x;
+    }
+  }
+#pragma unroll
+  for (int w = 0; w < N * 32 / 72; ++w)
+    scale[w] = row_q_scale(__reduce_max_sync(0xffffffffu, max(mx[w] & 0xffffu, mx[w] >> 16)));
 }
 
 __device__ __forceinline__ float2 e4m3x2_to_float2(uint16_t two) {

@@ -89,6 +89,7 @@ struct Misc {
   float red[2][4][kRows];  // row maxima by page, double-buffered; then row sums
   float qinv[kRows];          // e4m3: 2^-k of every row's Q
   CtaRange range;
+  const int2 *groups;         // shared pages: their groups' table, or null
   long long scratch[kThreads / 32 + 1];
 };
 template <bool F8>
@@ -104,27 +105,24 @@ __device__ __forceinline__ uint32_t bar(uint64_t &b) { return smem_u32(&b); }
 // Block v of 128 rows: of a group's rows over its shared pages, of a request's
 // rows over its own pages, or of a request's rows through its window.
 template <int KIND>
-__device__ __forceinline__ ViewReq make_view(const DecodeParams &p, int v) {
+__device__ __forceinline__ ViewReq make_view(const DecodeParams &p, int v, const int2 *groups) {
   if constexpr (KIND == kWindow) return window_block<kPairRows>(p, v);
-  else return shared_view<kPairRows, KIND == kTails>(p, v, p.pair_blocks - p.pair_tails);
+  else return shared_view<kPairRows, KIND == kTails>(p, v, p.pair_blocks - p.pair_tails, groups);
 }
 template <int KIND>
-static __device__ __noinline__ ViewReq view_call(const DecodeParams &p, int v) {
-  return make_view<KIND>(p, v);
+static __device__ __noinline__ ViewReq view_call(const DecodeParams &p, int v, const int2 *groups) {
+  return make_view<KIND>(p, v, groups);
 }
 // A call for the larger kinds, not inlined into the four roles: 3 to 8 % faster with
 // an e4m3 cache (384 rows x 32 requests, window 2000: 70.5 us, inlined 73.8), the
 // same with bf16.  Shared pages alone: inlined, 231 us against 235 (bf16, 4096
 // rows over 32K shared tokens).
 template <int KIND>
-__device__ __forceinline__ ViewReq block_view(const DecodeParams &p, int v) {
-  if constexpr (KIND == kWhole) return make_view<KIND>(p, v);
-  else return view_call<KIND>(p, v);
+__device__ __forceinline__ ViewReq block_view(const DecodeParams &p, int v, const int2 *groups) {
+  if constexpr (KIND == kWhole) return make_view<KIND>(p, v, groups);
+  else return view_call<KIND>(p, v, groups);
 }
-template <int KIND>
-__device__ __forceinline__ int block_tiles(const DecodeParams &p, int v) {
-  return (block_view<KIND>(p, v).tiles + kTilePages - 1) / kTilePages;
-}
+__device__ __forceinline__ int tiles_of(const ViewReq &view) { return (view.tiles + kTilePages - 1) / kTilePages; }
 
 // The pieces of this pair's range, in order.
 template <bool F8, int KIND>
@@ -134,11 +132,13 @@ struct Pieces {
   int v, tiles;
   long long pv, t0, t1;
   ViewReq view;
-  __device__ Pieces(const DecodeParams &p_, const CtaRange &r_) : p(p_), r(r_), v(r_.v_begin), pv(r_.p_begin) {}
+  const Misc &m;
+  __device__ Pieces(const DecodeParams &p_, const CtaRange &r_, const Misc &m_)
+      : p(p_), r(r_), v(r_.v_begin), pv(r_.p_begin), m(m_) {}
   __device__ bool next() {
     while (v < p.pair_blocks && pv < r.end) {
-      view = block_view<KIND>(p, v);
-      tiles = (view.tiles + kTilePages - 1) / kTilePages;
+      view = block_view<KIND>(p, v, m.groups);
+      tiles = tiles_of(view);
       if (tiles == 0) { ++v; continue; }
       t0 = max(r.start, pv) - pv;
       t1 = min(r.end, pv + tiles) - pv;
@@ -151,9 +151,9 @@ struct Pieces {
 };
 
 template <bool F8, int KIND>
-__device__ __forceinline__ uint32_t total_tiles(const DecodeParams &p, const CtaRange &r) {
+__device__ __forceinline__ uint32_t total_tiles(const DecodeParams &p, const CtaRange &r, const Misc &m) {
   uint32_t n = 0;
-  for (Pieces<F8, KIND> w(p, r); w.next(); w.advance()) n += uint32_t(w.t1 - w.t0);
+  for (Pieces<F8, KIND> w(p, r, m); w.next(); w.advance()) n += uint32_t(w.t1 - w.t0);
   return n;
 }
 
@@ -194,7 +194,7 @@ struct TileWalk {
   long long t;
   bool live;
   int page[kTilePages];
-  __device__ TileWalk(const DecodeParams &p, const CtaRange &r) : w(p, r), t(0) {
+  __device__ TileWalk(const DecodeParams &p, const CtaRange &r, const Misc &m) : w(p, r, m), t(0) {
     live = w.next();
     if (live) t = w.t0;
     load();
@@ -332,7 +332,7 @@ __device__ __forceinline__ void produce(const DecodeParams &p, const CtaRange &r
   };
   // c: the next tile to load K of; its pages are read a tile early, so that
   // their latency hides behind the units of the tile before
-  TileWalk<F8, KIND> c(p, r);
+  TileWalk<F8, KIND> c(p, r, m);
   int last[kTilePages];  // pages of the tile whose V comes next, and their seen rows
   unsigned long long lseen[kTilePages] = {0, 0, 0, 0};
   bool have = false, lwhole = true;
@@ -391,7 +391,7 @@ __device__ __forceinline__ void score_mmas(const DecodeParams &p, const CtaRange
   uint32_t n = 0;
   uint32_t q_it = 0;
   bool ok = true;
-  for (Pieces<F8, KIND> w(p, r); ok && w.next(); w.advance()) {
+  for (Pieces<F8, KIND> w(p, r, m); ok && w.next(); w.advance()) {
     for (long long t = w.t0; ok && t < w.t1; ++t, ++n) {
       const int b = int(n & 1);
       ok = warp_wait(bar(m.s_free[b]), ((n >> 1) & 1) ^ 1, abort);
@@ -450,12 +450,12 @@ __device__ __forceinline__ void pv_mmas(const DecodeParams &p, const CtaRange &r
   // V, MN-major: 128-byte blocks of dims 1 KB apart, 8-token groups 4 KB (bf16)
   // or 2 KB (e4m3) apart
   const uint64_t dv = smem_desc_sw128(sRing, 1024, F8 ? 2048 : 4096);
-  const uint32_t total = total_tiles<F8, KIND>(p, r);
+  const uint32_t total = total_tiles<F8, KIND>(p, r, m);
   Landed landed;
   uint32_t n = 0;
   uint32_t o_it = 0;
   bool ok = true;
-  for (Pieces<F8, KIND> w(p, r); ok && w.next(); w.advance(), ++o_it) {
+  for (Pieces<F8, KIND> w(p, r, m); ok && w.next(); w.advance(), ++o_it) {
     for (long long t = w.t0; ok && t < w.t1; ++t, ++n) {
       ok = warp_wait(bar(m.o_ready[n & 1]), (n >> 1) & 1, abort);
       if (ok && t == w.t0) ok = warp_wait(bar(m.o_free), (o_it & 1) ^ 1, abort);
@@ -542,45 +542,27 @@ __device__ __forceinline__ bool split_q(const DecodeParams &p, Misc &m, unsigned
                                         uint32_t rank, int st, uint32_t piece, bool ok) {
   constexpr int kChunks = kDqk / 8;                       // 8 dims each
   constexpr int kWarpRows = kRows / kSoftWarps, kPer = kWarpRows * kChunks / 32;  // 8 rows; 18 chunks a lane
-  static_assert(kWarpRows * kChunks % 32 == 0, "Q chunks");
+  static_assert(kWarpRows * kChunks == 32 * kPer, "Q chunks");
   const int warp = st >> 5, lane = st & 31, first = warp * kWarpRows;
   const int rows = min(kRows, max(0, view.rows - int(rank) * kRows));
   const uint4 *src = reinterpret_cast<const uint4 *>(p.q + (size_t(view.row0) + rank * kRows + first) * kDqk);
-  // round u of a warp's loads meets row 32 u / 72 and, from lane `next_row(u)` on,
-  // the one after it
-  auto row_of = [](int u) { return 32 * u / kChunks; };
-  auto next_row = [&](int u) { return (row_of(u) + 1) * kChunks - 32 * u; };
   const int left = (rows - first) * kChunks;
   uint4 v[kPer];
 #pragma unroll
   for (int u = 0; u < kPer; ++u) v[u] = lane + 32 * u < left ? __ldg(src + lane + 32 * u) : make_uint4(0, 0, 0, 0);
-  uint32_t row_mx[kWarpRows] = {};
-#pragma unroll
-  for (int u = 0; u < kPer; ++u) {
-    const uint32_t mx = largest_bf16x8(v[u]);
-    uint32_t &row = row_mx[row_of(u)];
-    if (next_row(u) >= 32) {
-      row = __vmaxu2(row, mx);
-    } else {
-      row = __vmaxu2(row, lane < next_row(u) ? mx : 0u);
-      row_mx[row_of(u) + 1] = lane < next_row(u) ? 0u : mx;
-    }
-  }
   float row_sc[kWarpRows];
+  row_q_scales(v, lane, row_sc);
+  if (lane == 0)
 #pragma unroll
-  for (int w = 0; w < kWarpRows; ++w) {
-    const QScale s = row_q_scale(__reduce_max_sync(0xffffffffu, max(row_mx[w] & 0xffffu, row_mx[w] >> 16)));
-    row_sc[w] = s.scale;
-    if (lane == 0) m.qinv[first + w] = s.inv;
-  }
+    for (int w = 0; w < kWarpRows; ++w) m.qinv[first + w] = inverse_q_scale(row_sc[w]);
   named_sync(1, kSoftThreads);  // (every thread reads its row's)
   ok = ok && __all_sync(0xffffffffu, mbar_wait_clk(bar(m.q_empty), (piece & 1) ^ 1, &m.abort, kTimeoutClk));
   if (!ok) return false;
 #pragma unroll
   for (int u = 0; u < kPer; ++u) {
-    const bool next = lane >= next_row(u);
-    const int w = row_of(u) + (next ? 1 : 0), rr = first + w, c = lane + 32 * u - kChunks * w;
-    const float sc = next_row(u) < 32 && next ? row_sc[row_of(u) + 1] : row_sc[row_of(u)];
+    const int w0 = 32 * u / kChunks, next = (w0 + 1) * kChunks - 32 * u;  // lanes from `next` on: the row after w0
+    const int w = w0 + (lane >= next ? 1 : 0), rr = first + w, c = lane + 32 * u - kChunks * w;
+    const float sc = next < 32 && lane >= next ? row_sc[w0 + 1] : row_sc[w0];
     const uint32_t wv[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
     uint32_t hw[2] = {0, 0}, lw[2] = {0, 0};
 #pragma unroll
@@ -626,9 +608,9 @@ __device__ __forceinline__ void softmax(const DecodeParams &p, const CtaRange &r
   uint32_t n = 0;
   uint32_t o_it = 0;
   bool ok = true;
-  for (Pieces<F8, KIND> w(p, r); w.next(); w.advance(), ++o_it) {
+  for (Pieces<F8, KIND> w(p, r, m); w.next(); w.advance(), ++o_it) {
     const int grow = w.view.row0 + int(rank) * kRows + row;
-    const RowView rv = row_view(p, w.view, min(grow, p.batch * p.heads - 1));
+    const RowView rv = row_view<KIND == kWindow>(p, w.view, min(grow, p.batch * p.heads - 1));
     const bool mine = int(rank) * kRows + row < w.view.rows;
     if constexpr (F8) {
       ok = split_q(p, m, smem, w.view, rank, st, o_it, ok);
@@ -881,15 +863,27 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       for (int i = tid; i < w.rows * kDv / 8; i += kThreads) dst[i] = make_uint4(0, 0, 0, 0);
       for (int i = tid; i < w.rows; i += kThreads) p.lse[size_t(w.row0) + i] = -INFINITY;
     }
+  }
+  if constexpr (KIND == kWindow) {
+    schedule_range<kPieceTiles<F8, KIND>, true>(
+        p.pair_blocks, pair_id, p.pairs, [&](int v) { return tiles_of(block_view<KIND>(p, v, nullptr)); }, &m.range,
+        m.scratch);
   } else {
+    const int2 *groups = schedule_views<kPieceTiles<F8, KIND>>(
+        p, p.pair_blocks, pair_id, p.pairs,
+        [&](int v, const int2 *table, bool *unsure) {
+          const ViewReq view = block_view<KIND>(p, v, table);
+          *unsure |= view.unsure;
+          return tiles_of(view);
+        },
+        &m.range, m.scratch);
+    if (tid == 0) m.groups = groups;
     for (int v = int(blockIdx.x) * kThreads + tid; v < p.pair_blocks; v += int(gridDim.x) * kThreads)
-      if (block_tiles<KIND>(p, v) == 0) pair_info_ptr(p)[v] = make_int4(-1, 0, 0, 0);
+      if (block_view<KIND>(p, v, groups).tiles == 0) pair_info_ptr(p)[v] = make_int4(-1, 0, 0, 0);
     if (KIND == kTails)
       for (int b = int(blockIdx.x) * kThreads + tid; b < p.batch; b += int(gridDim.x) * kThreads)
         check_view(p, b, err);
   }
-  schedule_range<kPieceTiles<F8, KIND>, true>(
-      p.pair_blocks, pair_id, p.pairs, [&](int v) { return block_tiles<KIND>(p, v); }, &m.range, m.scratch);
   tc_fence_before();
   cluster_sync();  // both CTAs' barriers and TMEM are ready
   tc_fence_after();

@@ -171,12 +171,13 @@ struct TcMisc {
   alignas(16) unsigned char stage_out[4][2048];  // epilogue: per-warp transpose buffer
   uint32_t conv_max[4];
   CtaRange range;
-  ViewReq view0;                  // views only: the first piece's view
+  ViewStart view0;                // views only
   long long scratch[tc::kThreadsF8 / 32 + 1];
-  // e4m3 views only: qinv and the largest |q| of every row (the latter by piece parity)
+  // e4m3 views only, of every row: the scores' scale, with 2^-k (by piece mod 4), and 2^k
+  // (by piece mod 2)
   static constexpr int kRowScales = NS == 3 ? tc::kHeads : 1;
-  float row_qinv[4][kRowScales];
-  uint32_t row_qmax[2][kRowScales];
+  float row_cs[4][kRowScales];
+  float row_q2k[2][kRowScales];
 };
 static_assert(sizeof(TcMisc<2>) + 1024 <= tc::kSmemBytes - tc::off_misc<false>(), "shared memory budget");
 static_assert(sizeof(TcMisc<3>) + 1024 <= tc::kSmemBytes - tc::off_misc<true>(), "shared memory budget");
@@ -191,7 +192,8 @@ constexpr int piece_cost() { return F8 ? kPieceCostE4m3 : kPieceCost; }
 // The requests (and tile ranges) this CTA owns, in order; every role walks it.
 // FUSED: all partitions in one launch (output row b = partition * B + input
 // request); otherwise one partition, p.part_id, and row b is request b.
-// MULTI == 3: the pieces are views (see ViewReq), one page a tile.
+// MULTI >= 3: the pieces are views (see ViewReq), one page a tile: 3 windows, 4 a batch
+// with shared pages.
 struct NoView {};
 
 template <bool FUSED, int MULTI, int PC>
@@ -201,14 +203,14 @@ struct Walk {
   int V, v, b, g, n, tiles;
   int rb, part, pc;  // input request of output row b, its partition, the map's partition coordinate
   long long pv, t0, t1;
-  std::conditional_t<MULTI == 3, ViewReq, NoView> view;
-  const ViewReq *first;  // views: the first piece's, in shared memory
-  __device__ Walk(const DecodeParams &p_, const CtaRange &r_, const ViewReq *first_)
+  std::conditional_t<MULTI >= 3, ViewReq, NoView> view;
+  const ViewStart *first;  // views only, in shared memory
+  __device__ Walk(const DecodeParams &p_, const CtaRange &r_, const ViewStart *first_)
       : p(p_), r(r_), V(virtual_requests<MULTI>(p_)), v(r_.v_begin), pv(r_.p_begin), first(first_) {}
   __device__ bool next() {
     while (v < V && pv < r.end) {
-      if constexpr (MULTI == 3) {
-        view = v == r.v_begin ? *first : view_req(p, v);
+      if constexpr (MULTI >= 3) {
+        view = v == r.v_begin ? first->view : view_req<MULTI>(p, v, first->groups);
         tiles = view.tiles;
         if (tiles == 0) { ++v; continue; }
         t0 = max(r.start, pv) - pv;
@@ -236,16 +238,16 @@ struct Walk {
   __device__ void advance() { pv += request_cost(tiles, PC); ++v; }
   // the piece's rows: the first in q / out / lse, and their number (at most 64)
   __device__ __forceinline__ int q_row0() const {
-    if constexpr (MULTI == 3) return view.row0;
+    if constexpr (MULTI >= 3) return view.row0;
     return rb * p.heads + g * tc::kHeads;
   }
   __device__ __forceinline__ int rows() const {
-    if constexpr (MULTI == 3) return view.rows;
+    if constexpr (MULTI >= 3) return view.rows;
     return min(tc::kHeads, p.heads - g * tc::kHeads);
   }
   // tokens of tile t that some row of the piece sees
   __device__ __forceinline__ int seen(long long t) const {
-    if constexpr (MULTI == 3) return view.seen(p, t);
+    if constexpr (MULTI >= 3) return view.seen(p, t);
     return min(kTile, n - int(t) * kTile);
   }
 };
@@ -256,7 +258,7 @@ struct TileCursor {
   Walk<FUSED, MULTI, PC> w;
   long long t;
   bool live;
-  __device__ TileCursor(const DecodeParams &p, const CtaRange &r, const ViewReq *first) : w(p, r, first), t(0) {
+  __device__ TileCursor(const DecodeParams &p, const CtaRange &r, const ViewStart *first) : w(p, r, first), t(0) {
     live = w.next();
     if (live) t = w.t0;
   }
@@ -307,7 +309,7 @@ __device__ __forceinline__ bool lane_page(const DecodeParams &p, int part, long 
 template <bool FUSED, int MULTI, int PC>
 __device__ __forceinline__ bool cursor_page(const DecodeParams &p, const TileCursor<FUSED, MULTI, PC> &c, int lane,
                                             int *lp, int *row0) {
-  if constexpr (MULTI == 3) {
+  if constexpr (MULTI >= 3) {
     *lp = c.w.view.page(c.t);
     *row0 = 0;
     return lane == 0;
@@ -357,7 +359,7 @@ __device__ __forceinline__ void tc_producer(const TcParams &tp, const CtaRange &
   bool started = false;
   auto next_ahead = [&]() {
     int pg = -1;
-    if (MULTI == 3 && started && ahead.live) ahead.step();
+    if (MULTI >= 3 && started && ahead.live) ahead.step();
     started = true;
     if (ahead.live) {
       int lp, row0;
@@ -381,7 +383,7 @@ __device__ __forceinline__ void tc_producer(const TcParams &tp, const CtaRange &
           }
         }
       }
-      if (MULTI != 3) ahead.step();
+      if (MULTI < 3) ahead.step();
     }
     return pg;
   };
@@ -393,7 +395,7 @@ __device__ __forceinline__ void tc_producer(const TcParams &tp, const CtaRange &
   TileCursor<FUSED, MULTI, piece_cost<F8>()> cur(p, r, &m.view0);
   while (cur.live) {
     if (!F8 && cur.first()) {  // (e4m3: warps 9..11 load and split Q)
-      if (MULTI != 3) checked_len(p, cur.w.rb, err);  // (views: see write_empty_views)
+      if (MULTI < 3) checked_len(p, cur.w.rb, err);  // (views: see write_empty_views)
       if (!__all_sync(0xffffffffu, mbar_wait(bar_addr(m.q_empty), (q_it & 1) ^ 1, abort, kTimeoutNs))) {
         ok = false;
         break;
@@ -405,7 +407,7 @@ __device__ __forceinline__ void tc_producer(const TcParams &tp, const CtaRange &
       last_q = q_it & 1;
       ++q_it;
     }
-    if (F8 && MULTI != 3 && cur.first()) checked_len(p, cur.w.rb, err);
+    if (F8 && MULTI < 3 && cur.first()) checked_len(p, cur.w.rb, err);
     const int s = kv_it % NS;
     int lp, row0;
     const bool mine = cursor_page(p, cur, lane, &lp, &row0);
@@ -527,10 +529,10 @@ __device__ __forceinline__ void tc_mma_s(const TcParams &tp, const CtaRange &r, 
       const int st = s_it % NS, sb = s_it & 1;
       const uint32_t ph = (s_it / NS) & 1;
       if (sc.first()) {
-        if (!issuer_wait<MULTI == 3>(bar_addr(q_ready), q_it & 1, abort, kTimeoutNs)) { ok = false; break; }
+        if (!issuer_wait<MULTI >= 3>(bar_addr(q_ready), q_it & 1, abort, kTimeoutNs)) { ok = false; break; }
         ++q_it;
       }
-      if (!issuer_wait<MULTI == 3>(bar_addr(m.s_free[sb]), ((s_it >> 1) & 1) ^ 1, abort, kTimeoutNs)) {
+      if (!issuer_wait<MULTI >= 3>(bar_addr(m.s_free[sb]), ((s_it >> 1) & 1) ^ 1, abort, kTimeoutNs)) {
         ok = false;
         break;
       }
@@ -538,10 +540,10 @@ __device__ __forceinline__ void tc_mma_s(const TcParams &tp, const CtaRange &r, 
       bool landed = true;
 #pragma unroll
       for (int half = 0; half < 2; ++half) {  // block 4 first, then blocks 0..3
-        landed = issuer_wait<MULTI == 3>(bar_addr(m.kv_full[st][1 - half]), ph, abort, kTimeoutNs);
+        landed = issuer_wait<MULTI >= 3>(bar_addr(m.kv_full[st][1 - half]), ph, abort, kTimeoutNs);
         if (!landed) break;
         tc_fence_after();
-        if (issuer<MULTI == 3>()) {
+        if (issuer<MULTI >= 3>()) {
 #pragma unroll
           for (int kb = half ? 0 : 4; kb < (half ? 4 : 5); ++kb) {
             const uint64_t dk = (kb < 4 ? dk0 + ((kb * kFxBlkStride) >> 4) : dk4) + st * kStageEnc;
@@ -553,13 +555,13 @@ __device__ __forceinline__ void tc_mma_s(const TcParams &tp, const CtaRange &r, 
         }
       }
       if (!landed) { ok = false; break; }
-      if (issuer<MULTI == 3>()) {
+      if (issuer<MULTI >= 3>()) {
         mma_commit(bar_addr(m.s_full[sb]));
         if (sc.last()) mma_commit(bar_addr(m.q_empty));
       }
     }
     if (!ok) atomicOr(err, kErrTimeout);
-    if (issuer<MULTI == 3>()) mma_commit(bar_addr(m.drain));
+    if (issuer<MULTI >= 3>()) mma_commit(bar_addr(m.drain));
     mbar_wait_drain(bar_addr(m.drain), 0, kDrainNs);
     return;
   }
@@ -572,15 +574,15 @@ __device__ __forceinline__ void tc_mma_s(const TcParams &tp, const CtaRange &r, 
   for (TileCursor<FUSED, MULTI, piece_cost<F8>()> sc(p, r, &m.view0); sc.live; sc.step(), ++s_it) {
     const int st = s_it & 1;
     const uint32_t ph = (s_it >> 1) & 1;
-    if (!issuer_wait<MULTI == 3>(bar_addr(m.kv_full[st][0]), ph, abort, kTimeoutNs)) {
+    if (!issuer_wait<MULTI >= 3>(bar_addr(m.kv_full[st][0]), ph, abort, kTimeoutNs)) {
       ok = false;
       break;
     }
     if (sc.first()) {
-      if (!issuer_wait<MULTI == 3>(bar_addr(q_ready), q_it & 1, abort, kTimeoutNs)) { ok = false; break; }
+      if (!issuer_wait<MULTI >= 3>(bar_addr(q_ready), q_it & 1, abort, kTimeoutNs)) { ok = false; break; }
       ++q_it;
     }
-    if (!issuer_wait<MULTI == 3>(bar_addr(m.s_free[st]), ph ^ 1, abort, kTimeoutNs)) { ok = false; break; }
+    if (!issuer_wait<MULTI >= 3>(bar_addr(m.s_free[st]), ph ^ 1, abort, kTimeoutNs)) { ok = false; break; }
     tc_fence_after();
     const uint64_t dk = dk0 + st * kStageEnc;
     const uint32_t d = tmem + kColS + 64 * (2 * st + chain);
@@ -590,11 +592,11 @@ __device__ __forceinline__ void tc_mma_s(const TcParams &tp, const CtaRange &r, 
 #pragma unroll
     for (int g = 0; g < kKb / KBG; ++g) {
       if (g > 0) {
-        landed = issuer_wait<MULTI == 3>(bar_addr(m.kv_full[st][g]), ph, abort, kTimeoutNs);
+        landed = issuer_wait<MULTI >= 3>(bar_addr(m.kv_full[st][g]), ph, abort, kTimeoutNs);
         if (!landed) break;
         tc_fence_after();
       }
-      if (issuer<MULTI == 3>()) {
+      if (issuer<MULTI >= 3>()) {
 #pragma unroll
         for (int i = 2 * KBG * g; i < 2 * KBG * (g + 1); ++i) {
           const int kb = i >> 1;
@@ -605,13 +607,13 @@ __device__ __forceinline__ void tc_mma_s(const TcParams &tp, const CtaRange &r, 
       }
     }
     if (!landed) { ok = false; break; }
-    if (issuer<MULTI == 3>()) {
+    if (issuer<MULTI >= 3>()) {
       mma_commit(bar_addr(m.s_full[st]));
       if (sc.last()) mma_commit(bar_addr(m.q_empty));
     }
   }
   if (!ok) atomicOr(err, kErrTimeout);
-  if (issuer<MULTI == 3>()) mma_commit(bar_addr(m.drain));
+  if (issuer<MULTI >= 3>()) mma_commit(bar_addr(m.drain));
   mbar_wait_drain(bar_addr(m.drain), 0, kDrainNs);
 }
 
@@ -640,19 +642,19 @@ __device__ __forceinline__ void tc_mma_pv(const TcParams &tp, const CtaRange &r,
     bool ok = true;
     for (TileCursor<FUSED, MULTI, piece_cost<F8>()> pc(p, r, &m.view0); pc.live; pc.step(), ++pv_it) {
       const int st = pv_it % NS;
-      if (!issuer_wait<MULTI == 3>(bar_addr(m.p_full[st]), (pv_it / NS) & 1, abort, kTimeoutNs)) {
+      if (!issuer_wait<MULTI >= 3>(bar_addr(m.p_full[st]), (pv_it / NS) & 1, abort, kTimeoutNs)) {
         ok = false;
         break;
       }
       const bool fresh = pc.first();
-      if (fresh && !issuer_wait<MULTI == 3>(bar_addr(m.o_free), (o_it & 1) ^ 1, abort, kTimeoutNs)) {
+      if (fresh && !issuer_wait<MULTI >= 3>(bar_addr(m.o_free), (o_it & 1) ^ 1, abort, kTimeoutNs)) {
         ok = false;
         break;
       }
       tc_fence_after();
       const uint64_t dp = dp0 + st * kStageEnc;
       const int ksteps = (pc.nv() + 31) >> 5;
-      if (issuer<MULTI == 3>())
+      if (issuer<MULTI >= 3>())
 #pragma unroll
       for (int ks = 0; ks < 2; ++ks) {
         if (ks < ksteps) {
@@ -665,7 +667,7 @@ __device__ __forceinline__ void tc_mma_pv(const TcParams &tp, const CtaRange &r,
           }
         }
       }
-      if (issuer<MULTI == 3>()) {
+      if (issuer<MULTI >= 3>()) {
         mma_commit(bar_addr(m.kv_empty[st]));
         mma_commit(bar_addr(m.p_free[st]));
         if (pc.last()) mma_commit(bar_addr(m.o_full));
@@ -673,7 +675,7 @@ __device__ __forceinline__ void tc_mma_pv(const TcParams &tp, const CtaRange &r,
       if (pc.last()) ++o_it;
     }
     if (!ok) atomicOr(err, kErrTimeout);
-    if (issuer<MULTI == 3>()) mma_commit(bar_addr(m.drain));
+    if (issuer<MULTI >= 3>()) mma_commit(bar_addr(m.drain));
     mbar_wait_drain(bar_addr(m.drain), 0, kDrainNs);
     return;
   }
@@ -691,12 +693,12 @@ __device__ __forceinline__ void tc_mma_pv(const TcParams &tp, const CtaRange &r,
   uint32_t pv_it = 0, o_it = 0;
   bool ok = true;
   for (TileCursor<FUSED, MULTI, piece_cost<F8>()> pc(p, r, &m.view0); pc.live; pc.step(), ++pv_it) {
-    if (!issuer_wait<MULTI == 3>(bar_addr(m.p_full[pv_it & 1]), (pv_it >> 1) & 1, abort, kTimeoutNs)) {
+    if (!issuer_wait<MULTI >= 3>(bar_addr(m.p_full[pv_it & 1]), (pv_it >> 1) & 1, abort, kTimeoutNs)) {
       ok = false;
       break;
     }
     const bool fresh = pc.first();
-    if (fresh && !issuer_wait<MULTI == 3>(bar_addr(m.o_free), (o_it & 1) ^ 1, abort, kTimeoutNs)) {
+    if (fresh && !issuer_wait<MULTI >= 3>(bar_addr(m.o_free), (o_it & 1) ^ 1, abort, kTimeoutNs)) {
       ok = false;
       break;
     }
@@ -704,7 +706,7 @@ __device__ __forceinline__ void tc_mma_pv(const TcParams &tp, const CtaRange &r,
     const int st = pv_it & 1;
     const uint64_t dp = dp0 + st * kStageEnc;
     const int ksteps = (pc.nv() + 15) >> 4;
-    if (issuer<MULTI == 3>())
+    if (issuer<MULTI >= 3>())
 #pragma unroll
     for (int ks = 0; ks < 4; ++ks) {
       if (ks < ksteps) {
@@ -717,7 +719,7 @@ __device__ __forceinline__ void tc_mma_pv(const TcParams &tp, const CtaRange &r,
         }
       }
     }
-    if (issuer<MULTI == 3>()) {
+    if (issuer<MULTI >= 3>()) {
       mma_commit(bar_addr(m.kv_empty[st]));
       mma_commit(bar_addr(m.p_free[st]));
       if (pc.last()) mma_commit(bar_addr(m.o_full));
@@ -725,7 +727,7 @@ __device__ __forceinline__ void tc_mma_pv(const TcParams &tp, const CtaRange &r,
     if (pc.last()) ++o_it;
   }
   if (!ok) atomicOr(err, kErrTimeout);
-  if (issuer<MULTI == 3>()) mma_commit(bar_addr(m.drain));
+  if (issuer<MULTI >= 3>()) mma_commit(bar_addr(m.drain));
   mbar_wait_drain(bar_addr(m.drain), 0, kDrainNs);
 }
 
@@ -870,7 +872,7 @@ __device__ __forceinline__ void tc_softmax(const TcParams &tp, const CtaRange &r
                            unsigned char *smem, uint32_t tmem, int *err) {
   using namespace tc;
   constexpr bool STRIDED = MULTI == 2;
-  constexpr bool VIEW = MULTI == 3;
+  constexpr bool VIEW = MULTI >= 3;
   // the sum that gives the LSE takes P before rounding (a bf16 cache's other
   // variants take the rounded P: its error, up to 2^-9 of the LSE's argument,
   // shows in the LSE of a short view)
@@ -887,7 +889,7 @@ __device__ __forceinline__ void tc_softmax(const TcParams &tp, const CtaRange &r
   const int row[2] = {16 * q + (lane >> 2), 16 * q + (lane >> 2) + 8};
   const int pair = 2 * (lane & 3);
   const uint32_t tq = tmem + (uint32_t(32 * q) << 16);
-  float cs[2] = {p.score_scale_log2 * p.kv_scale, p.score_scale_log2 * p.kv_scale};  // of the two rows
+  float cs = p.score_scale_log2 * p.kv_scale;
   uint32_t kv_it = 0, p_it = 0, o_it = 0;
   bool ok = true;
   // an owner mask: the gathered tiles hold other partitions' tokens too
@@ -910,10 +912,12 @@ __device__ __forceinline__ void tc_softmax(const TcParams &tp, const CtaRange &r
       __threadfence_block();
       const bool have = vv[slot] == w.v;
       if (!have) atomicOr(err, kErrTimeout);
-#pragma unroll
-      for (int h = 0; h < 2; ++h)
-        cs[h] = p.score_scale_log2 * p.kv_scale * (!have ? 0.f : VIEW ? m.row_qinv[slot][row[h]] : m.qinv[slot]);
+      cs = p.score_scale_log2 * p.kv_scale * (have ? m.qinv[slot] : 0.f);
     }
+    // the scores' scale of row[h]: e4m3 views have one for each row, read where it is
+    // needed (kept for both rows it spilled; a piece's slot is not written again
+    // before the softmax is past it, as the scores are at most two tiles ahead)
+    auto scale_of = [&](int h) { return F8 && VIEW ? m.row_cs[piece & 3][row[h]] : cs; };
     // owned tokens each of this lane's two rows sees (all w.n unless a request
     // carries several query tokens, each with its own causal bound)
     int nrow[2] = {0, 0};
@@ -921,7 +925,7 @@ __device__ __forceinline__ void tc_softmax(const TcParams &tp, const CtaRange &r
     RowView rv[2];  // views: what each of the two rows sees
     if constexpr (VIEW) {
 #pragma unroll
-      for (int h = 0; h < 2; ++h) rv[h] = row_view(p, w.view, w.view.row0 + row[h]);
+      for (int h = 0; h < 2; ++h) rv[h] = row_view<MULTI == 3>(p, w.view, w.view.row0 + row[h]);
     } else if (MULTI) {  // query token i of T sees the global tokens t < L - T + i + 1
       const int L = checked_len(p, w.rb, nullptr);
 #pragma unroll
@@ -1016,7 +1020,7 @@ __device__ __forceinline__ void tc_softmax(const TcParams &tp, const CtaRange &r
       for (int h = 0; h < 2; ++h) {
         tmax[h] = fmaxf(tmax[h], __shfl_xor_sync(0xffffffffu, tmax[h], 1));
         tmax[h] = fmaxf(tmax[h], __shfl_xor_sync(0xffffffffu, tmax[h], 2));
-        const float sm = tmax[h] * cs[h];  // cs > 0: the scaled maximum
+        const float sm = tmax[h] * scale_of(h);  // cs > 0: the scaled maximum
         mnew[h] = mrun[h];
         alpha[h] = 1.f;
         if (t == w.t0) {
@@ -1065,7 +1069,8 @@ __device__ __forceinline__ void tc_softmax(const TcParams &tp, const CtaRange &r
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           const float mref = MULTI && mnew[h] == -INFINITY ? 0.f : mnew[h] - kFxPLog2Scale;
-          const float2 c2 = make_float2(cs[h], cs[h]), m2 = make_float2(-mref, -mref);
+          const float csh = scale_of(h);
+          const float2 c2 = make_float2(csh, csh), m2 = make_float2(-mref, -mref);
           unsigned char *prow = pst + (row[h] >> 3) * kFxPSbo + (row[h] & 7) * 16 + pair;
           float2 lsum = make_float2(0.f, 0.f), xsum = make_float2(0.f, 0.f);
 #pragma unroll
@@ -1096,7 +1101,8 @@ __device__ __forceinline__ void tc_softmax(const TcParams &tp, const CtaRange &r
                                 (row[h] >> 3) * atom_stride<KBG>() + (row[h] & 7) * 128 + (lane & 3) * 4;
           // a row that has seen no token yet keeps a -inf max: its P is 0
           const float mref = MULTI && mnew[h] == -INFINITY ? 0.f : mnew[h];
-          const float2 c2 = make_float2(cs[h], cs[h]), m2 = make_float2(-mref, -mref);
+          const float csh = scale_of(h);
+          const float2 c2 = make_float2(csh, csh), m2 = make_float2(-mref, -mref);
           float2 lsum = make_float2(0.f, 0.f), xsum = make_float2(0.f, 0.f);
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
@@ -1160,7 +1166,7 @@ __device__ __forceinline__ void tc_softmax(const TcParams &tp, const CtaRange &r
       // shared pages: every piece leaves a partial, in the slot of its CTA
       // and virtual request (both grow along the walk, so the sum is its own),
       // after the pair kernel's slots
-      if (p.view == kViewShared) {
+      if constexpr (MULTI == 4) {
         split = true;
         si.slot = pair_slots(p) + int(blockIdx.x) + w.v;
       }
@@ -1286,7 +1292,12 @@ __device__ __forceinline__ uint32_t piece_q_max(const DecodeParams &p,
       v[u] = i < n ? __ldg(qg + i) : make_uint4(0, 0, 0, 0);
     }
 #pragma unroll
-    for (int u = 0; u < 16; ++u) mx = __vmaxu2(mx, largest_bf16x8(v[u]));
+    for (int u = 0; u < 16; ++u) {
+      mx = __vmaxu2(mx, v[u].x & 0x7fff7fffu);
+      mx = __vmaxu2(mx, v[u].y & 0x7fff7fffu);
+      mx = __vmaxu2(mx, v[u].z & 0x7fff7fffu);
+      mx = __vmaxu2(mx, v[u].w & 0x7fff7fffu);
+    }
   }
   mx = __reduce_max_sync(0xffffffffu, max(mx & 0xffffu, mx >> 16));
   if ((ct & 31) == 0) m.conv_max[ct >> 5] = mx;
@@ -1294,33 +1305,29 @@ __device__ __forceinline__ uint32_t piece_q_max(const DecodeParams &p,
   return max(m.conv_max[0], max(m.conv_max[1], m.conv_max[2]));
 }
 
-// The same of each of a view's rows, a warp a row (0 past the block's rows).
+// 2^k of each of a view's rows, eight rows a warp at a time (past the block's rows: any).
 template <bool FUSED, int MULTI>
-__device__ __forceinline__ void row_q_max(const DecodeParams &p, const Walk<FUSED, MULTI, kPieceCostE4m3> &w,
-                                          uint32_t *row_max, int ct) {
+__device__ __forceinline__ void view_q_scales(const DecodeParams &p, const Walk<FUSED, MULTI, kPieceCostE4m3> &w,
+                                              float *row_scale, int ct) {
   using namespace tc;
-  constexpr int kRowChunks = kDqk / 8, kWarps = kConvThreads / 32;
-  constexpr int kBatch = 5, kLoads = (kRowChunks + 31) / 32;  // 15 loads in flight
+  constexpr int kRowChunks = kDqk / 8, kWarpRows = 8, kLoads = kWarpRows * kRowChunks / 32;
   const int lane = ct & 31, hn = w.rows();
   const uint4 *qg = reinterpret_cast<const uint4 *>(p.q + size_t(w.q_row0()) * kDqk);
-  for (int r0 = ct >> 5; r0 < kHeads; r0 += kWarps * kBatch) {
-    uint4 v[kBatch][kLoads];
-#pragma unroll
-    for (int b = 0; b < kBatch; ++b)
-#pragma unroll
-      for (int j = 0; j < kLoads; ++j) {
-        const int rr = r0 + kWarps * b, c = lane + 32 * j;
-        v[b][j] = rr < hn && c < kRowChunks ? __ldg(qg + rr * kRowChunks + c) : make_uint4(0, 0, 0, 0);
-      }
-#pragma unroll
-    for (int b = 0; b < kBatch; ++b) {
-      uint32_t mx = 0;
-#pragma unroll
-      for (int j = 0; j < kLoads; ++j) mx = __vmaxu2(mx, largest_bf16x8(v[b][j]));
-      mx = __reduce_max_sync(0xffffffffu, max(mx & 0xffffu, mx >> 16));
-      const int rr = r0 + kWarps * b;
-      if (lane == 0 && rr < kHeads) row_max[rr] = mx;
+  for (int r0 = kWarpRows * (ct >> 5); r0 < kHeads; r0 += kWarpRows * (kConvThreads / 32)) {
+    if (r0 >= hn) {
+      if (lane < kWarpRows) row_scale[r0 + lane] = 1.f;
+      continue;
     }
+    const int left = (hn - r0) * kRowChunks;
+    uint4 v[kLoads];
+#pragma unroll
+    for (int u = 0; u < kLoads; ++u)
+      v[u] = lane + 32 * u < left ? __ldg(qg + r0 * kRowChunks + lane + 32 * u) : make_uint4(0, 0, 0, 0);
+    float scale[kWarpRows];
+    row_q_scales(v, lane, scale);
+    if (lane == 0)
+#pragma unroll
+      for (int u = 0; u < kWarpRows; ++u) row_scale[r0 + u] = scale[u];
   }
 }
 
@@ -1344,11 +1351,11 @@ __device__ __forceinline__ void tc_split_q(const TcParams &tp, const CtaRange &r
   Walk<FUSED, MULTI, kPieceCostE4m3> w(p, r, &m.view0), wa(p, r, &m.view0);  // wa: the piece after w
   bool ahead = wa.next();
   uint32_t mx = 0;
-  // the largest |q| of piece `it`, which wa is at (a view's: of its rows, where
-  // the sync at the start of that piece makes them visible)
+  // the largest |q| of piece `it`, which wa is at (a view's: its rows' scales, which
+  // the sync at the start of that piece makes visible)
   auto look_ahead = [&](uint32_t it) {
     if (!ahead) return;
-    if constexpr (MULTI == 3) row_q_max(p, wa, m.row_qmax[it & 1], ct);
+    if constexpr (MULTI >= 3) view_q_scales(p, wa, m.row_q2k[it & 1], ct);
     else mx = piece_q_max(p, wa, m, ct);
     wa.advance();
     ahead = wa.next();
@@ -1359,8 +1366,14 @@ __device__ __forceinline__ void tc_split_q(const TcParams &tp, const CtaRange &r
     if (!named_sync_and(3, kConvThreads, got)) { ok = false; break; }
     const int hn = w.rows();
     const uint4 *qg = reinterpret_cast<const uint4 *>(p.q + size_t(w.q_row0()) * kDqk);
-    const QScale piece_scale = q_scale(mx);
-    const uint32_t *row_max = m.row_qmax[q_it & 1];
+    const float piece_scale = q_scale(mx);
+    const float *row_scale = m.row_q2k[q_it & 1];
+    if (MULTI >= 3 && ct < 32) {  // (before the tag below: lane 0 writes that)
+      const float cs = p.score_scale_log2 * p.kv_scale;
+      for (int rr = ct; rr < kHeads; rr += 32) m.row_cs[q_it & 3][rr] = cs * inverse_q_scale(row_scale[rr]);
+      __threadfence_block();
+      __syncwarp();
+    }
 #pragma unroll 1
     for (int u0 = 0; u0 < kPer; u0 += 16) {
       uint4 v[16];
@@ -1373,8 +1386,7 @@ __device__ __forceinline__ void tc_split_q(const TcParams &tp, const CtaRange &r
       for (int u = 0; u < 16; ++u) {
         const int i = ct + (u0 + u) * kConvThreads;
         const int rr = i / kRowChunks, c = i - kRowChunks * rr;
-        float sc = piece_scale.scale;
-        if constexpr (MULTI == 3) sc = row_q_scale(row_max[rr]).scale;
+        const float sc = MULTI >= 3 ? row_scale[rr] : piece_scale;
         const uint32_t wv[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
         uint32_t hw[2] = {0, 0}, lw[2] = {0, 0};
 #pragma unroll
@@ -1395,15 +1407,8 @@ __device__ __forceinline__ void tc_split_q(const TcParams &tp, const CtaRange &r
         *reinterpret_cast<uint2 *>(smem + kFxQTerm + off) = make_uint2(lw[0], lw[1]);
       }
     }
-    if constexpr (MULTI == 3) {
-      if (ct < 32) {
-        for (int rr = ct; rr < kHeads; rr += 32) m.row_qinv[q_it & 3][rr] = row_q_scale(row_max[rr]).inv;
-        __threadfence_block();
-        __syncwarp();
-      }
-    }
     if (ct == 0) {
-      if (MULTI != 3) m.qinv[q_it & 3] = piece_scale.inv;
+      m.qinv[q_it & 3] = inverse_q_scale(piece_scale);
       __threadfence_block();
       reinterpret_cast<volatile int *>(m.qinv_v)[q_it & 3] = w.v;
     }
@@ -1490,19 +1495,29 @@ __global__ void __launch_bounds__(tc_threads<F8>(), 1)
   // launch's own dependent, the split merge, early as well measured slower.)
   asm volatile("griddepcontrol.wait;" ::: "memory");
   // (views leave this to a warp that has nothing to do yet)
-  if (MULTI != 3) write_empty_requests<MULTI>(p);
-  if constexpr (MULTI == 3) {
-    const int V = virtual_requests<3>(p);
+  if (MULTI < 3) write_empty_requests<MULTI>(p);
+  const int2 *groups = nullptr;
+  if constexpr (MULTI >= 3) {
+    const int V = virtual_requests<MULTI>(p);
     ViewReq mine;
-    schedule_range<piece_cost<F8>(), true>(V, int(blockIdx.x), int(gridDim.x), [&](int v) {
-      mine = view_req(p, v);
-      return mine.tiles;
-    }, &m.range, m.scratch);
+    if constexpr (MULTI == 3)
+      schedule_range<piece_cost<F8>(), true>(V, int(blockIdx.x), int(gridDim.x), [&](int v) {
+        mine = view_req<MULTI>(p, v, nullptr);
+        return mine.tiles;
+      }, &m.range, m.scratch);
+    else
+      groups = schedule_views<piece_cost<F8>()>(p, V, int(blockIdx.x), int(gridDim.x),
+                                                [&](int v, const int2 *table, bool *unsure) {
+        mine = view_req<MULTI>(p, v, table);
+        *unsure |= mine.unsure;
+        return mine.tiles;
+      }, &m.range, m.scratch);
     // the roles start from the first piece's view and its page's entry
     const int v0 = m.range.v_begin;
-    if (V > int(blockDim.x) && v0 < V) mine = view_req(p, v0);
+    if (tid == 0) m.view0.groups = groups;
+    if (V > int(blockDim.x) && v0 < V) mine = view_req<MULTI>(p, v0, groups);
     if (v0 < V && tid == (V > int(blockDim.x) ? 0 : v0)) {
-      m.view0 = mine;
+      m.view0.view = mine;
       prefetch_l2(p.block_table + size_t(mine.req) * p.max_pages + mine.page(max(m.range.start - m.range.p_begin, 0ll)));
     }
   } else {
@@ -1514,16 +1529,17 @@ __global__ void __launch_bounds__(tc_threads<F8>(), 1)
   const uint32_t tmem = m.tmem_base;
   const CtaRange r = m.range;
 
-  if (MULTI == 3 && warp == 8) write_empty_views(p);
+  if constexpr (MULTI >= 3)
+    if (warp == 8) write_empty_views<MULTI>(p, groups);
   if (r.start < r.end) {
     const uint32_t sKv = sbase + off_kv<F8>();
     if (warp == 0) {
       tc_producer<F8, FUSED, MULTI, AHEAD>(tp, r, m, sbase + kOffQ, sKv, &tm_q, &tm_kv, &tm_kvg, &tm_kvb,
                                            err);
     } else if (warp == 1 || warp == 2) {
-      if (MULTI == 3 || lane == 0) tc_mma_s<F8, FUSED, MULTI, KBG>(tp, r, m, sbase + kOffQ, sKv, tmem, warp - 1, err);
+      if (MULTI >= 3 || lane == 0) tc_mma_s<F8, FUSED, MULTI, KBG>(tp, r, m, sbase + kOffQ, sKv, tmem, warp - 1, err);
     } else if (warp == 3 || warp == 8) {
-      if (MULTI == 3 || lane == 0) tc_mma_pv<F8, FUSED, MULTI, KBG>(tp, r, m, sKv, tmem, warp == 8, err);
+      if (MULTI >= 3 || lane == 0) tc_mma_pv<F8, FUSED, MULTI, KBG>(tp, r, m, sKv, tmem, warp == 8, err);
     } else if (warp < 8) {
       tc_softmax<F8, FUSED, MULTI, KBG>(tp, r, m, smem, tmem, err);
     } else if constexpr (F8) {
@@ -1571,7 +1587,9 @@ template <bool F8>
 cudaError_t launch_tc_variants(const TcParams &tp, const CUtensorMap &tm_q,
                                const CUtensorMap &tm_kv, const CUtensorMap &tm_kvg,
                                const CUtensorMap &tm_kvb, int grid, cudaStream_t stream) {
-  if (tp.p.view) return launch_tc<F8, false, 3, F8 ? 2 : 1>(tp, tm_q, tm_kv, tm_kvg, tm_kvb, grid, stream);
+  if (tp.p.view == kViewWindow)
+    return launch_tc<F8, false, 3, F8 ? 2 : 1>(tp, tm_q, tm_kv, tm_kvg, tm_kvb, grid, stream);
+  if (tp.p.view) return launch_tc<F8, false, 4, F8 ? 2 : 1>(tp, tm_q, tm_kv, tm_kvg, tm_kvb, grid, stream);
   if (tp.p.strided)
     return tp.p.fused ? launch_tc<F8, true, 2, 2>(tp, tm_q, tm_kv, tm_kvg, tm_kvb, grid, stream)
                       : launch_tc<F8, false, 2, 2>(tp, tm_q, tm_kv, tm_kvg, tm_kvb, grid, stream);

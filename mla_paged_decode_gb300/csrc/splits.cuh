@@ -102,14 +102,15 @@ __device__ inline void write_empty_requests(const DecodeParams &p) {
 }
 
 // The same for views, by one warp of the CTA, with the checks of the inputs.
-__device__ inline void write_empty_views(const DecodeParams &p) {
-  const int lane = threadIdx.x & 31, V = virtual_requests<3>(p);
+template <int MULTI>
+__device__ inline void write_empty_views(const DecodeParams &p, const int2 *groups) {
+  const int lane = threadIdx.x & 31, V = virtual_requests<MULTI>(p);
   for (int v = blockIdx.x; v < V; v += gridDim.x) {
     if (lane == 0) check_view(p, v, error_word(p));
-    const ViewReq r = view_req(p, v);
+    const ViewReq r = view_req<MULTI>(p, v, groups);
     if (r.tiles != 0) continue;
     if (lane == 0) info_ptr(p)[v] = make_int4(-1, 0, 0, 0);
-    if (p.view == kViewShared) continue;  // the merge writes every row
+    if (MULTI == 4) continue;  // the merge writes every row
     uint4 *dst = reinterpret_cast<uint4 *>(p.out + size_t(r.row0) * kDv);
     for (int i = lane; i < r.rows * kDv / 8; i += 32) dst[i] = make_uint4(0, 0, 0, 0);
     for (int i = lane; i < r.rows; i += 32) p.lse[size_t(r.row0) + i] = -INFINITY;

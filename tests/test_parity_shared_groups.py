@@ -95,3 +95,33 @@ def test_a_bad_entry_of_the_request_that_is_read_is_reported():
                           torch.tensor([10], dtype=torch.int32, device="cuda"), SCALE, 0, out, lse, workspace=ws)
         assert mla.check_workspace(ws) == -9
         assert (out[0] == 0).all() and (lse[0] == -math.inf).all()
+
+
+@pytest.mark.parametrize("kv_dtype", ["bf16", "e4m3"])
+@pytest.mark.parametrize("heads,width,shape", [(20, 0, "many groups"), (40, WIDE, "many groups"),
+                                               (64, WIDE, "one group"), (128, WIDE, "one group"),
+                                               (16, 0, "one group")])
+def test_ended_and_short_requests_among_hundreds(kv_dtype, heads, width, shape):
+    """More requests than threads: the schedule walks them in chunks, before and
+    after the groups' readers are looked up."""
+    g = torch.Generator().manual_seed(heads)
+    if shape == "many groups":
+        starts, pages = [0], []
+        for k in range(90):
+            starts.append(starts[-1] + (k * 7) % 9)
+            pages.append((k * 5) % 7)
+    else:
+        starts, pages = [0, 410], [6]
+    lens, full = [], []
+    for k, n in enumerate(pages):
+        for _ in range(starts[k], starts[k + 1]):
+            full.append(64 * n + int(torch.randint(1, 150, (), generator=g)))
+            r = float(torch.rand((), generator=g))
+            # ended, shorter than the shared pages, or neither; one group in three has nobody at full length
+            lens.append(0 if r < 0.5 else full[-1] if r > 0.7 and k % 3 else int(full[-1] * (r - 0.4)))
+    c = make(full, heads, 1, kv_dtype, causal_seen(1), seed=86, shared=(starts, pages), width=width)
+    for b, n in enumerate(lens):
+        c.table[b, -(-n // 64):] = -1
+    c.lens.copy_(torch.tensor(lens, dtype=torch.int32))
+    c.seen = [[torch.arange(n)] for n in lens]
+    check(c, *run_shared(c, starts, pages), what=shape)
