@@ -560,12 +560,12 @@ size_t shared_workspace_bytes(const mla::WorkspaceLayout &wl, int num_groups) {
 // The pair kernel takes windows of requests with more than one block of 64 rows
 // in the other kernel; its start and end take 2 to 5 us longer on a bf16 cache,
 // which rows x tokens in view (at most) have to make up for.  Measured, us a
-// call, pair kernel / blocks of 64 rows, bf16, rows x requests, window: 128 x 8,
-// 128 (0.1 M) 17.2 / 15.3; 192 x 8, 128 21.8 / 19.5; 128 x 32, 128 (0.5 M)
-// 17.5 / 21.5; 65 x 32, 4096 60.9 / 72.6; 128 x 1, 4096 22.4 / 35.1; 192 x 8, 512
-// (0.8 M) 22.8 / 20.7; 128 x 128, 512 54.7 / 64.5; 192 x 128, 4096 268 / 349; 512 x
-// 128, 4096 498 / 868; e4m3: 19.8 / 23.1, 19.6 / 26.4, 20.1 / 29.7, 54.6 / 82.0,
-// 24.3 / 42.6, 23.3 / 29.8, 60.1 / 80.6, 229 / 312, 427 / 731.
+// call in a graph, pair kernel / blocks of 64 rows, bf16, rows x requests, window:
+// 128 x 8, 128 (0.1 M) 24.6 / 18.5; 192 x 8, 128 24.6 / 20.5; 128 x 32, 128 (0.5 M)
+// 24.6 / 27.1; 65 x 32, 4096 60 / 74; 128 x 1, 4096 (0.5 M) 27.0 / 24.7; 192 x 8, 512
+// (0.8 M) 24.6 / 22.6; 128 x 128, 512 64 / 69; 192 x 128, 4096 272 / 350; 512 x 128,
+// 4096 507 / 796; e4m3: 22.5 / 28.1, 22.6 / 28.7, 22.6 / 34.8, 52 / 80, 26.6 / 34.2,
+// 24.6 / 32.8, 65 / 90, 230 / 309, 429 / 748.
 constexpr long long kWindowPairWork = 1LL << 19;
 bool window_pair_path(const mla_decode_desc *d, int window, int sinks) {
   if (rows_of(d) <= kTcHeadsPerGroup) return false;
@@ -576,15 +576,15 @@ bool window_pair_path(const mla_decode_desc *d, int window, int sinks) {
 // The pair kernel takes the shared pages when the groups fill its blocks of 128
 // rows on average and there is enough to multiply: it is a kernel more (9 to 13
 // us), and nearly twice as fast in the long run.  Rows x tokens of the block
-// table bound the work.  Measured, us a call, pair kernel / blocks of 64 rows in
-// the one kernel, bf16: 4096 rows x 1K shared tokens 44 / 34, 1024 x 8K 44 / 38,
-// 256 x 32K 42 / 42, 512 x 32K 57 / 62, 4096 x 8K 79 / 102, 4096 x 32K 214 / 363;
-// e4m3: 50 / 44, 53 / 43, 49 / 42, 60 / 57, 85 / 95, 193 / 277.  These tables were
-// as wide as the work; only the device knows the tokens.  A table made for far
-// longer requests sends short shared pages to the pair kernel too: 2,200 columns,
-// captured into a graph, 128 rows over 256 shared tokens and 100 own ones 32.5 /
-// 18.4, over 4K 32.8 / 22.5, 1024 rows over 1K 36.9 / 22.6, over 8K 47 / 41; e4m3
-// 45 / 29, 45 / 35, 50 / 35, 60 / 49.
+// table bound the work.  Measured, us a call in a graph, pair kernel / blocks of 64
+// rows in the one kernel, 64 rows a request, 100 own tokens, bf16: 4096 rows x 1K
+// shared tokens 47 / 33, 1024 x 8K 47 / 39, 256 x 32K 47 / 40, 512 x 32K 59 / 59, 4096 x
+// 8K 82 / 101, 4096 x 32K 219 / 364; e4m3: 55 / 47, 57 / 47, 58 / 45, 64 / 59, 90 / 96,
+// 202 / 275.  These tables were as wide as the work; only the device knows the
+// tokens.  A table made for far longer requests sends short shared pages to the
+// pair kernel too: 2,200 columns, 128 rows over 256 shared tokens and 100 own ones
+// 32.5 / 18.4, over 4K 32.8 / 22.5, 1024 rows over 1K 36.9 / 22.6, over 8K 47 / 41;
+// e4m3 45 / 29, 45 / 35, 50 / 35, 60 / 49.
 constexpr long long kPairWork = 16LL << 20;
 bool pair_path(const mla_decode_desc *d, int num_groups) {
   const long long rows = (long long)d->batch * rows_of(d);
@@ -994,10 +994,10 @@ int mla_decode_shared(const void *q, const void *kv_pages, const int32_t *block_
   p.group_table = reinterpret_cast<int2 *>(static_cast<unsigned char *>(workspace) + wl.total);
   if (pair_path(d, num_groups)) {
     // the tails of requests with more than one block of 64 rows go along, a launch
-    // less and the pair kernel's rate; us a call, tails along / in the other kernel,
-    // bf16: 256 rows x 39 requests, 131 shared pages + 700 tokens 160 / 178, 128 x 64,
-    // 128 + 1500 136 / 166, + 1 134 / 138, 512 x 32, 400 + 1 626 / 610, + 1500
-    // 664 / 660; e4m3: 136 / 174, 123 / 161, 120 / 146, 512 / 529, 575 / 590
+    // less and the pair kernel's rate; us a call in a graph, tails along / in the other
+    // kernel, bf16: 256 rows x 39 requests, 131 shared pages + 700 tokens 168 / 186, 128 x
+    // 64, 128 + 1500 144 / 181, + 1 130 / 136, 512 x 32, 400 + 1 624 / 605, + 1500
+    // 665 / 683; e4m3: 150 / 185, 135 / 178, 113 / 132, 553 / 537, 606 / 619
     if (rows_of(d) > kTcHeadsPerGroup) p.pair_tails = d->batch * ((rows_of(d) + 127) / 128);
     p.pair_blocks = shared_blocks(d, num_groups, 128) + p.pair_tails;
     p.pairs = f.sms / 2;
