@@ -298,6 +298,38 @@ int mla_kv_append(const void *kv_new, void *kv_pages, const int32_t *block_table
                   const int32_t *positions, int part_id, int num_parts,
                   const mla_decode_desc *d, int32_t *error_word, mla_stream_t stream);
 
+/*
+ * Chunks: a ragged batch of rows between a contiguous buffer and the paged
+ * cache.  Row r of the buffer belongs to request b with starts[b] <= r <
+ * starts[b + 1] and is its token t = positions[b] + r - starts[b], at physical
+ * page block_table[b][t / 64], row t % 64.  Rows before starts[0] and from
+ * starts[batch] on (a batch padded to a fixed size) and rows of a request
+ * with a negative position are nobody's: nothing is read or written for them.
+ *
+ *  num_rows    rows of the buffer (0 is a no-op).
+ *  row_stride  values from one row of the buffer to the next: a multiple of 8,
+ *              at least 576, so that rows may lie inside wider ones.
+ *  *_starts    int32 [batch + 1], none below its predecessor.
+ *  positions   int32 [batch].
+ *  d, error_word
+ *              as for mla_kv_append: a row without a page is skipped
+ *              (mla_kv_read writes zeros) and bit 0 is OR-ed in.
+ *
+ * mla_kv_append_chunk writes rows into the cache: the row kv_append would
+ * write for each (bits, or e4m3 of fp32(x) / kv_scale, to nearest even,
+ * saturated), only the tokens of partition part_id of num_parts.  Two rows
+ * that go to one cache row race.  mla_kv_read reads them back as bf16: the
+ * bits, or fp32(code) * kv_scale rounded to nearest even.  One kernel each.
+ */
+int mla_kv_append_chunk(const void *kv_new, int64_t row_stride, int num_rows, void *kv_pages,
+                        const int32_t *block_table, const int32_t *chunk_starts,
+                        const int32_t *positions, int part_id, int num_parts,
+                        const mla_decode_desc *d, int32_t *error_word, mla_stream_t stream);
+
+int mla_kv_read(const void *kv_pages, const int32_t *block_table, const int32_t *read_starts,
+                const int32_t *positions, void *out, int64_t row_stride, int num_rows,
+                const mla_decode_desc *d, int32_t *error_word, mla_stream_t stream);
+
 /* Sizes of the DCP rank metadata. */
 typedef struct mla_dcp_meta_desc {
   int32_t batch;              /* B requests (0 is a no-op)                         */
@@ -439,6 +471,40 @@ int mla_decode_shared(const void *q, const void *kv_pages, const int32_t *block_
                       int num_groups, float sm_scale, int lse_base, void *out, float *lse,
                       const mla_decode_desc *d, void *workspace, size_t workspace_bytes,
                       mla_stream_t stream);
+
+/*
+ * Attention of a chunk of new tokens over the paged cache, in the absorbed
+ * form: any number of query tokens for each request, a prompt's chunk beside
+ * requests that decode one token.  The new tokens' rows are in the cache
+ * already (mla_kv_append_chunk).
+ *
+ *  q           bf16 [num_tokens, H, 576], contiguous: the requests' query
+ *              tokens, one request after the other.
+ *  chunk_starts int32 [batch + 1]: request b's queries are tokens
+ *              chunk_starts[b] .. chunk_starts[b + 1] - 1, its last n tokens: token i
+ *              of n sees the cached tokens t < seq_lens[b] - n + i + 1.  None is
+ *              below its predecessor, the last is at most num_tokens; tokens
+ *              of no request keep what out and lse hold for them.
+ *  seq_lens    int32 [batch]: lengths with the chunk.  A query that sees
+ *              nothing gets the neutral pair (0, -inf).
+ *  out, lse    bf16 [num_tokens, H, 512], fp32 [num_tokens, H].
+ *  sm_scale    finite and > 0.
+ *  d           as for mla_decode_partial (q_len: 1); num_tokens x H <= 2^30.
+ *  workspace   >= mla_prefill_workspace_size(0) bytes, whatever the batch, same
+ *              rules as for mla_decode_partial.
+ *
+ * Blocks of 128 rows (token x head) of a request on pairs of SMs, each over
+ * the pages up to its last query.  Rows of the cache past that may hold
+ * anything; a row that only some queries of a block see must be finite.
+ * Arithmetic and errors as for mla_decode_window, a start out of range being
+ * reported like a length.  Two kernels.
+ */
+size_t mla_prefill_workspace_size(int num_sms);
+
+int mla_prefill_chunk(const void *q, int num_tokens, const void *kv_pages, const int32_t *block_table,
+                      const int32_t *seq_lens, const int32_t *chunk_starts, float sm_scale, int lse_base,
+                      void *out, float *lse, const mla_decode_desc *d, void *workspace,
+                      size_t workspace_bytes, mla_stream_t stream);
 
 /*
  * Page operations.  A pool of cache pages is described by four device arrays

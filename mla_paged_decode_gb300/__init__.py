@@ -21,6 +21,7 @@ __all__ = [
     "decode_partial_noalloc", "decode_window", "decode_shared", "make_shared_workspace",
     "pages_workspace_size", "make_pages_workspace", "pages_copy", "pages_fork", "pages_alloc",
     "pages_free", "pages_compact", "PAGES_BAD_ENTRY", "PAGES_FULL",
+    "kv_append_chunk", "kv_read", "prefill_chunk", "make_prefill_workspace",
 ]
 
 LSE_NATURAL = 0
@@ -122,6 +123,15 @@ def load_library():
         for f in (lib.mla_pages_copy, lib.mla_pages_fork, lib.mla_pages_alloc, lib.mla_pages_free,
                   lib.mla_pages_compact):
             f.restype = i32
+        i64 = ctypes.c_int64
+        lib.mla_kv_append_chunk.argtypes = [vp, i64, i32, vp, vp, vp, vp, i32, i32, dd, vp, vp]
+        lib.mla_kv_append_chunk.restype = i32
+        lib.mla_kv_read.argtypes = [vp, vp, vp, vp, vp, i64, i32, dd, vp, vp]
+        lib.mla_kv_read.restype = i32
+        lib.mla_prefill_workspace_size.argtypes = [i32]
+        lib.mla_prefill_workspace_size.restype = sz
+        lib.mla_prefill_chunk.argtypes = [vp, i32, vp, vp, vp, vp, f32, i32, vp, vp, dd, vp, sz, vp]
+        lib.mla_prefill_chunk.restype = i32
         lib.mla_status_string.argtypes = [i32]
         lib.mla_status_string.restype = ctypes.c_char_p
         lib.mla_last_cuda_error.argtypes = []
@@ -612,6 +622,134 @@ def decode_shared(q, kv_pages, block_table, seq_lens, group_starts, shared_pages
             block_table.data_ptr(), seq_lens.data_ptr(), group_starts.data_ptr(), shared_pages.data_ptr(),
             _int32(groups, "groups"), float(sm_scale), lse_base, out.data_ptr(), lse.data_ptr(), ctypes.byref(d),
             workspace.data_ptr(), workspace.numel())
+    return out, lse
+
+
+_CACHE_DESCS: dict = {}
+
+
+def _cache_desc(batch, heads, kv_pages, block_table, kv_scale):
+    """The size descriptor (by reference) of a call whose queries are not
+    [B, q_len, H, 576], built once per set of sizes."""
+    key = (batch, heads, kv_pages.shape, kv_pages.dtype, block_table.shape, float(kv_scale))
+    d = _CACHE_DESCS.get(key)
+    if d is None:
+        if kv_pages.dim() != 3 or kv_pages.shape[2] != 576:
+            raise ValueError("kv_pages must be [num_pages, 64, 576]")
+        if block_table.dim() != 2 or block_table.shape[0] != batch:
+            raise ValueError("block_table must be [B, max_pages]")
+        if len(_CACHE_DESCS) > 256:
+            _CACHE_DESCS.clear()
+        d = _CACHE_DESCS[key] = DecodeDesc(
+            batch=_int32(batch, "batch"), num_heads=_int32(heads, "heads"), q_len=1, head_dim_qk=576, head_dim_v=512,
+            page_size=_int32(kv_pages.shape[1], "page_size"), num_pages=_int32(kv_pages.shape[0], "num_pages"),
+            max_pages_per_seq=_int32(block_table.shape[1], "max_pages"), kv_dtype=_kv_dtype_code(kv_pages),
+            kv_scale=float(kv_scale))
+    return ctypes.byref(d)
+
+
+def _chunk_args(what, rows, rows_name, kv_pages, block_table, starts, starts_name, positions, kv_scale, error_word):
+    """Checks what kv_append_chunk and kv_read have in common; returns the
+    device, the descriptor, the row stride and the number of rows."""
+    dev = kv_pages.device
+    if dev.type != "cuda":
+        raise ValueError(f"{what} runs on CUDA tensors only")
+    _need(kv_pages, "kv_pages", _KV_TYPES, dev)
+    _ints(block_table, "block_table", dev, 2)
+    _ints(starts, starts_name, dev, 1)
+    _ints(positions, "positions", dev, 1)
+    if not isinstance(rows, torch.Tensor) or rows.dtype != torch.bfloat16:
+        raise TypeError(f"{rows_name} must be a bf16 tensor")
+    if rows.device != dev:
+        raise ValueError(f"{rows_name} is on {rows.device}, expected {dev}")
+    if rows.dim() != 2 or rows.shape[1] != 576 or rows.stride(1) != 1:
+        raise ValueError(f"{rows_name} must be [N, 576] with rows of consecutive values")
+    B, n = positions.numel(), rows.shape[0]
+    if starts.numel() != B + 1:
+        raise ValueError(f"{starts_name} must be [B + 1] for B positions")
+    if error_word is not None:
+        _need(error_word, "error_word", _I32, dev)
+    return dev, _cache_desc(B, 1, kv_pages, block_table, kv_scale), rows.stride(0) if n > 1 else 576, \
+        _int32(n, "rows")
+
+
+def kv_append_chunk(kv_new, kv_pages, block_table, chunk_starts, positions, part_id: int = 0, num_parts: int = 1,
+                    *, kv_scale: float = 1.0, error_word=None, stream=None):
+    """mla_kv_append_chunk: rows chunk_starts[b] .. chunk_starts[b + 1] (int32
+    [B + 1]) of kv_new bf16 [N, 576] become request b's tokens positions[b]
+    (int32 [B]; negative skips the request), positions[b] + 1, ... in kv_pages
+    (bf16, or e4m3 quantised with kv_scale), where partition part_id of
+    num_parts owns them.  Rows of kv_new may lie inside wider ones."""
+    part_id, num_parts = _int32(part_id, "part_id"), _int32(num_parts, "num_parts")
+    dev, d, stride, n = _chunk_args("kv_append_chunk", kv_new, "kv_new", kv_pages, block_table, chunk_starts,
+                                    "chunk_starts", positions, kv_scale, error_word)
+    _launch(load_library().mla_kv_append_chunk, dev, stream, kv_new.data_ptr(), stride, n, kv_pages.data_ptr(),
+            block_table.data_ptr(), chunk_starts.data_ptr(), positions.data_ptr(), part_id, num_parts, d,
+            _opt(error_word))
+    return kv_pages
+
+
+def kv_read(kv_pages, block_table, read_starts, positions, out, *, kv_scale: float = 1.0, error_word=None,
+            stream=None):
+    """mla_kv_read: request b's cached tokens positions[b] (int32 [B]), ... go
+    to rows read_starts[b] .. read_starts[b + 1] (int32 [B + 1]) of out bf16
+    [N, 576], e4m3 codes times kv_scale.  Other rows of out stay as they are."""
+    dev, d, stride, n = _chunk_args("kv_read", out, "out", kv_pages, block_table, read_starts, "read_starts",
+                                    positions, kv_scale, error_word)
+    _launch(load_library().mla_kv_read, dev, stream, kv_pages.data_ptr(), block_table.data_ptr(),
+            read_starts.data_ptr(), positions.data_ptr(), out.data_ptr(), stride, n, d, _opt(error_word))
+    return out
+
+
+def make_prefill_workspace(q) -> torch.Tensor:
+    """A zero-filled workspace for prefill_chunk and prefill_expanded on q's
+    device; its size does not depend on the batch."""
+    with torch.cuda.device(q.device):
+        n = load_library().mla_prefill_workspace_size(0)
+    if n == 0:
+        raise MlaError(-8, "cannot size a workspace on this device")
+    return torch.zeros(n, dtype=torch.uint8, device=q.device)
+
+
+def _prefill_outputs(out, lse, dev, tokens, heads, dim, workspace, stream, q):
+    _need(out, "out", (torch.bfloat16,), dev)
+    _need(lse, "lse", (torch.float32,), dev)
+    if out.numel() != tokens * heads * dim or lse.numel() != tokens * heads:
+        raise ValueError(f"out must be [N, H, {dim}] and lse [N, H]")
+    if workspace is None:
+        with _allocating_on(stream, dev):
+            workspace = make_prefill_workspace(q)
+    _need(workspace, "workspace", (torch.uint8,), dev)
+    return workspace
+
+
+def prefill_chunk(q, kv_pages, block_table, seq_lens, chunk_starts, sm_scale: float, lse_base: int, out, lse, *,
+                  kv_scale: float = 1.0, workspace=None, stream=None):
+    """mla_prefill_chunk: tokens chunk_starts[b] .. chunk_starts[b + 1] (int32
+    [B + 1]) of q bf16 [N, H, 576] are the last of request b's seq_lens[b]
+    cached tokens and attend to those up to themselves; out bf16 [N, H, 512]
+    and lse fp32 [N, H] are written in place, tokens of no request left as
+    they are.  The workspace is make_prefill_workspace's."""
+    lse_base = _int32(lse_base, "lse_base")
+    dev = q.device
+    if dev.type != "cuda":
+        raise ValueError("prefill_chunk runs on CUDA tensors only")
+    _need(q, "q", (torch.bfloat16,), dev)
+    _need(kv_pages, "kv_pages", _KV_TYPES, dev)
+    _ints(block_table, "block_table", dev, 2)
+    _ints(seq_lens, "seq_lens", dev, 1)
+    _ints(chunk_starts, "chunk_starts", dev, 1)
+    if q.dim() != 3 or q.shape[2] != 576:
+        raise ValueError("q must be [N, H, 576]")
+    n, heads, _ = q.shape
+    B = seq_lens.numel()
+    if chunk_starts.numel() != B + 1:
+        raise ValueError("chunk_starts must be [B + 1] for B lengths")
+    d = _cache_desc(B, heads, kv_pages, block_table, kv_scale)
+    workspace = _prefill_outputs(out, lse, dev, n, heads, 512, workspace, stream, q)
+    _launch(load_library().mla_prefill_chunk, dev, stream, q.data_ptr(), _int32(n, "tokens"), kv_pages.data_ptr(),
+            block_table.data_ptr(), seq_lens.data_ptr(), chunk_starts.data_ptr(), float(sm_scale), lse_base,
+            out.data_ptr(), lse.data_ptr(), d, workspace.data_ptr(), workspace.numel())
     return out, lse
 
 

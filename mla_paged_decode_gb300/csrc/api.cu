@@ -27,6 +27,10 @@ cudaError_t launch_kv_append(const void *kv_new, void *kv_pages, const int32_t *
                              const int32_t *positions, int batch, int part_id, int num_parts,
                              int num_pages, int max_pages, int e4m3, float kv_scale,
                              int32_t *error_word, cudaStream_t stream);
+cudaError_t launch_kv_chunk(bool read, void *cache, void *buffer, long long stride, const int32_t *block_table,
+                            const int32_t *starts, const int32_t *positions, int rows, int batch, int part_id,
+                            int num_parts, int num_pages, int max_pages, int e4m3, float kv_scale,
+                            int32_t *error_word, cudaStream_t stream);
 cudaError_t launch_decode_tc(const DecodeParams &p, int npv, int q_rows, int groups_per_page,
                              const CUtensorMap &tm_q, const CUtensorMap &tm_kv,
                              const CUtensorMap &tm_kvg, const CUtensorMap &tm_kvb, int grid,
@@ -166,7 +170,19 @@ bool fused_path(const mla_decode_desc *d, int num_parts) {
   return num_parts >= 1 && (8 % num_parts == 0 || strided_path(d, num_parts));
 }
 
-// Q as [B*H rows, 576] bf16, one 64-column swizzled box of q_rows rows;
+// Q as [rows, 576] bf16, one 64-column swizzled box of q_rows rows.
+int make_q_map(EncodeTiled enc, const void *q, cuuint64_t rows, int q_rows, CUtensorMap *tm_q) {
+  cuuint64_t dims[2] = {cuuint64_t(mla::kDqk), rows};
+  cuuint64_t strides[1] = {cuuint64_t(mla::kDqk) * 2};
+  cuuint32_t box[2] = {64, cuuint32_t(q_rows)};
+  cuuint32_t es[2] = {1, 1};
+  CUresult r = enc(tm_q, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void *>(q), dims, strides,
+                   box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? MLA_OK : tensor_map_fail("q", r);
+}
+
+// Q (make_q_map);
 // partition rows of a bf16 cache as a 5-D view (64 dims, 8 rows of stride P,
 // 9 blocks of 64 dims, groups of 8 rows, partitions), one box = one page's
 // owned rows; of an e4m3 cache as a 3-D view (576 bytes, rows of stride P,
@@ -187,15 +203,8 @@ int make_tensor_maps(const void *q, const void *kv, const mla_decode_desc *d, in
   }
   const cuuint64_t row = cuuint64_t(mla::kDqk) * 2;
   {
-    const cuuint64_t qrows = cuuint64_t(d->q_len) * cuuint64_t(d->num_heads);
-    cuuint64_t dims[2] = {cuuint64_t(mla::kDqk), cuuint64_t(d->batch) * qrows};
-    cuuint64_t strides[1] = {row};
-    cuuint32_t box[2] = {64, cuuint32_t(q_rows)};
-    cuuint32_t es[2] = {1, 1};
-    CUresult r = enc(tm_q, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void *>(q), dims, strides,
-                     box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                     CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-    if (r != CUDA_SUCCESS) return tensor_map_fail("q", r);
+    const int st = make_q_map(enc, q, cuuint64_t(d->batch) * d->q_len * d->num_heads, q_rows, tm_q);
+    if (st != MLA_OK) return st;
   }
   if (d->kv_dtype == MLA_KV_E4M3 && strided) {
     // (144 words of 4 fp8 values, 64 page rows, pages): one box is one atom,
@@ -591,8 +600,34 @@ bool pair_path(const mla_decode_desc *d, int num_groups) {
   return rows >= 128LL * num_groups &&
          rows * mla::kPage >= kPairWork / d->max_pages_per_seq;
 }
+// Records of the chunks' blocks, one a pair, and two slots of 64 rows for each CTA.
+mla::WorkspaceLayout chunk_layout(int sms) { return mla::workspace_layout(sms, sms); }
+
 constexpr int kMaxGroups = 1 << 20;
 constexpr int kMaxView = 1 << 30;
+constexpr int kMaxChunkBatch = 1 << 20;
+
+// kv_append_chunk and kv_read: `buffer` is the contiguous side.
+int kv_chunk(bool read, void *kv_pages, void *buffer, int64_t stride, int rows, const int32_t *block_table,
+             const int32_t *starts, const int32_t *positions, int part_id, int num_parts, const mla_decode_desc *d,
+             int32_t *error_word, mla_stream_t stream) {
+  int st = check_cache_desc(d);
+  if (st != MLA_OK) return st;
+  if (rows < 0 || stride < mla::kDqk || stride > (1LL << 40)) return MLA_ERR_SHAPE;
+  if (num_parts < 1 || part_id < 0 || part_id >= num_parts) return MLA_ERR_PARTITION;
+  if (d->batch == 0 || rows == 0) return MLA_OK;
+  if (!buffer || !kv_pages || !block_table || !starts || !positions) return MLA_ERR_NULL;
+  if (!aligned(buffer, 16) || stride % 8 != 0 || !aligned(kv_pages, 16) || !aligned(block_table, 4) ||
+      !aligned(starts, 4) || !aligned(positions, 4) || !aligned(error_word, 4))
+    return MLA_ERR_ALIGN;
+  current_device(&st);
+  if (st != MLA_OK) return st;
+  const cudaError_t e = mla::launch_kv_chunk(read, kv_pages, buffer, stride, block_table, starts, positions, rows,
+                                             d->batch, part_id, num_parts, d->num_pages, d->max_pages_per_seq,
+                                             d->kv_dtype == MLA_KV_E4M3, d->kv_scale, error_word,
+                                             reinterpret_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? MLA_OK : cuda_fail(e);
+}
 
 }  // namespace
 
@@ -750,6 +785,86 @@ int mla_kv_append(const void *kv_new, void *kv_pages, const int32_t *block_table
                                         part_id, num_parts, d->num_pages, d->max_pages_per_seq,
                                         d->kv_dtype == MLA_KV_E4M3, d->kv_scale, error_word,
                                         reinterpret_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? MLA_OK : cuda_fail(e);
+}
+
+int mla_kv_append_chunk(const void *kv_new, int64_t row_stride, int num_rows, void *kv_pages,
+                        const int32_t *block_table, const int32_t *chunk_starts, const int32_t *positions,
+                        int part_id, int num_parts, const mla_decode_desc *d, int32_t *error_word,
+                        mla_stream_t stream) {
+  return kv_chunk(false, kv_pages, const_cast<void *>(kv_new), row_stride, num_rows, block_table, chunk_starts,
+                  positions, part_id, num_parts, d, error_word, stream);
+}
+
+int mla_kv_read(const void *kv_pages, const int32_t *block_table, const int32_t *read_starts,
+                const int32_t *positions, void *out, int64_t row_stride, int num_rows, const mla_decode_desc *d,
+                int32_t *error_word, mla_stream_t stream) {
+  return kv_chunk(true, const_cast<void *>(kv_pages), out, row_stride, num_rows, block_table, read_starts, positions,
+                  0, 1, d, error_word, stream);
+}
+
+size_t mla_prefill_workspace_size(int num_sms) {
+  if (num_sms <= 0) {
+    int st = 0;
+    DeviceFacts f = current_device(&st);
+    if (f.sms <= 0) return 0;
+    num_sms = f.sms;
+  }
+  return chunk_layout(num_sms).total;
+}
+
+int mla_prefill_chunk(const void *q, int num_tokens, const void *kv_pages, const int32_t *block_table,
+                      const int32_t *seq_lens, const int32_t *chunk_starts, float sm_scale, int lse_base, void *out,
+                      float *lse, const mla_decode_desc *d, void *workspace, size_t workspace_bytes,
+                      mla_stream_t stream) {
+  int st = check_desc(d);
+  if (st != MLA_OK) return st;
+  if (num_tokens < 0 || (long long)num_tokens * d->num_heads > (1LL << 30) || d->batch > kMaxChunkBatch)
+    return MLA_ERR_SHAPE;
+  if (lse_base != MLA_LSE_NATURAL && lse_base != MLA_LSE_BASE2) return MLA_ERR_ARG;
+  if (!(std::isfinite(sm_scale) && sm_scale > 0.f)) return MLA_ERR_ARG;
+  if (d->batch == 0 || num_tokens == 0) return MLA_OK;
+  if (!q || !kv_pages || !block_table || !seq_lens || !chunk_starts || !out || !lse || !workspace)
+    return MLA_ERR_NULL;
+  if (!aligned(q, 16) || !aligned(kv_pages, 16) || !aligned(out, 16) || !aligned(lse, 4) ||
+      !aligned(block_table, 4) || !aligned(seq_lens, 4) || !aligned(chunk_starts, 4) || !aligned(workspace, 256))
+    return MLA_ERR_ALIGN;
+  const DeviceFacts f = current_device(&st);
+  if (st != MLA_OK) return st;
+  mla::DecodeParams p;
+  p.wl = chunk_layout(f.sms);
+  if (workspace_bytes < p.wl.total) return MLA_ERR_WORKSPACE;
+  p.q = static_cast<const __nv_bfloat16 *>(q);
+  p.kv = kv_pages;
+  p.block_table = block_table;
+  p.seq_lens = seq_lens;
+  p.out = static_cast<__nv_bfloat16 *>(out);
+  p.lse = lse;
+  p.ws = static_cast<unsigned char *>(workspace);
+  p.view = mla::kViewChunk;
+  p.chunk_starts = chunk_starts;
+  p.chunk_tokens = num_tokens;
+  p.batch = p.req_batch = d->batch;
+  p.heads = p.q_heads = d->num_heads;
+  p.head_groups = 1;
+  p.heads_per_group = kTcHeadsPerGroup;
+  p.num_pages = d->num_pages;
+  p.max_pages = d->max_pages_per_seq;
+  p.part_id = 0;
+  p.num_parts = 1;
+  p.pairs = f.sms / 2;
+  p.pair_blocks = int((long long)num_tokens * d->num_heads / 128) + d->batch;
+  p.kv_e4m3 = d->kv_dtype == MLA_KV_E4M3;
+  p.kv_scale = p.kv_e4m3 ? d->kv_scale : 1.f;
+  p.score_scale_log2 = sm_scale * mla::kLog2e;
+  p.lse_base2 = lse_base == MLA_LSE_BASE2;
+  mla::PairMaps maps;
+  st = make_pair_maps(kv_pages, d, &maps);
+  if (st != MLA_OK) return st;
+  CUtensorMap tm_q;
+  st = make_q_map(encode_tiled(), q, cuuint64_t(num_tokens) * d->num_heads, 64, &tm_q);
+  if (st != MLA_OK) return st;
+  const cudaError_t e = mla::launch_decode_pair(p, tm_q, maps, reinterpret_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? MLA_OK : cuda_fail(e);
 }
 

@@ -99,6 +99,11 @@ struct DecodeParams {
   const int32_t *shared_pages = nullptr;  // [num_groups]
   int2 *group_table = nullptr;            // [num_groups], in the workspace (see fill_group_table)
   int num_groups = 0, prefix_blocks = 0;
+  // Chunks (kViewChunk; pair kernel): request b's query tokens are tokens
+  // chunk_starts[b] .. chunk_starts[b + 1] of the `chunk_tokens` tokens of Q, q_heads
+  // rows each, and the last of its seq_lens[b] cached ones.
+  const int32_t *chunk_starts = nullptr;  // [batch + 1]
+  int chunk_tokens = 0;
   // Shared pages, or windows, attended by the pair kernel (csrc/decode_pair.cu) in
   // pair_blocks blocks of 128 rows on `pairs` CTA pairs; prefix_blocks is then 0.
   // The last pair_tails of them are the requests' own pages (0: left to the
@@ -247,7 +252,11 @@ struct StridedMask {
 // up: rows / 64 rounded down at its first row, plus g, which leaves every
 // group at least the ids it needs (ceil(m / 64) <= floor((a + m) / 64) -
 // floor(a / 64) + 1); ids between are empty.
-constexpr int kViewWindow = 1, kViewShared = 2;
+//
+// Chunk: 128-row blocks of the requests' query tokens (ragged) over the tokens up to
+// the block's last query.  Request b's blocks have ids floor(its first row / 128) + b
+// and up, as the groups' blocks above.
+constexpr int kViewWindow = 1, kViewShared = 2, kViewChunk = 3;
 
 struct ViewReq {
   int tiles = 0;
@@ -391,6 +400,37 @@ __device__ __forceinline__ ViewReq window_block(const DecodeParams &p, int u) {
   return r;
 }
 
+// First query token of request b of a chunked batch; the tokens from chunk_start(batch)
+// on are nobody's.
+__device__ __forceinline__ int chunk_start(const DecodeParams &p, int b) {
+  return min(max(p.chunk_starts[b], 0), p.chunk_tokens);
+}
+template <int R>
+__device__ __forceinline__ int chunk_base(const DecodeParams &p, int b) {
+  return int((long long)chunk_start(p, b) * p.q_heads / R) + b;
+}
+// Block v of R rows of a chunked batch.  (Starts that fall are cut to none or to rows of
+// other requests, never to rows outside Q.)
+template <int R>
+__device__ __forceinline__ ViewReq chunk_block(const DecodeParams &p, int v) {
+  ViewReq r;
+  int lo = 0, hi = p.batch - 1;  // the last request whose blocks start at or before v
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (chunk_base<R>(p, mid) <= v) lo = mid;
+    else hi = mid - 1;
+  }
+  const int s0 = chunk_start(p, lo), n = chunk_start(p, lo + 1) - s0;
+  const long long k = v - chunk_base<R>(p, lo), rows = (long long)n * p.q_heads;
+  if (k < 0 || R * k >= rows) return r;
+  r.req = lo;
+  r.row0 = int((long long)s0 * p.q_heads + R * k);
+  r.rows = int(min((long long)R, rows - R * k));
+  r.end = max(0, checked_len(p, lo, nullptr) - n + (int(R * k) + r.rows - 1) / p.q_heads + 1);
+  r.tiles = (r.end + kPage - 1) / kPage;
+  return r;
+}
+
 // What the roles of a CTA start from: the first piece's view, and the groups' table or
 // null (in shared memory: held in registers it made the softmax of an e4m3 cache spill).
 struct ViewStart {
@@ -415,6 +455,13 @@ __device__ __forceinline__ RowView row_view(const DecodeParams &p, const ViewReq
   const int b = min(row / p.heads, p.batch - 1);
   const int pos = checked_len(p, b, nullptr) - p.q_len + (row - b * p.heads) / p.q_heads;
   return RowView{WINDOW ? max(0, pos + 1 - p.window) : 0, min(max(0, pos + 1), r.end)};
+}
+
+// The same of a row of a chunk's block.
+__device__ __forceinline__ RowView chunk_row_view(const DecodeParams &p, const ViewReq &r, int row) {
+  const int s0 = chunk_start(p, r.req), n = chunk_start(p, r.req + 1) - s0;
+  const int token = int((row - (long long)s0 * p.q_heads) / p.q_heads);
+  return RowView{0, min(max(0, checked_len(p, r.req, nullptr) - n + token + 1), r.end)};
 }
 
 // Owned tokens of virtual request v (its group's widest row).

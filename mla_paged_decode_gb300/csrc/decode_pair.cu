@@ -1,6 +1,7 @@
 // Attention of blocks of 128 rows on CTA pairs: the rows of a group (all heads
 // and query tokens of its requests) over the pages they share, the rows of a
-// request over its own pages, or through its window and sinks.
+// request over its own pages, or through its window and sinks, or the rows of a
+// chunk of new tokens over all tokens up to their own.
 //
 // The product is [rows x 576] x [576 x tokens] and [rows x tokens] x [tokens x
 // 512]: 2176 flops per row and cached token, compute bound from about 150 rows
@@ -32,7 +33,7 @@
 //
 // Work is split as in the decode kernel: the tiles of all blocks in one line,
 // cut into equal ranges, one per pair; pieces leave fp32 partials, but for
-// windows that one pair holds whole.  Q and the epilogue are a piece's boundary.
+// windows and chunks' blocks that one pair holds whole.  Q and the epilogue are a piece's boundary.
 #include "common.cuh"
 #include "pair_maps.cuh"
 #include "sm100.cuh"
@@ -44,8 +45,10 @@ using namespace sm100;
 namespace pair {
 constexpr int kThreads = 384;
 // kinds of the kernel: shared pages alone (all of whose rows are seen), windows,
-// shared pages and then the requests' own
-constexpr int kWhole = 0, kWindow = 1, kTails = 2;
+// shared pages and then the requests' own, chunks
+constexpr int kWhole = 0, kWindow = 1, kTails = 2, kChunk = 3;
+// kinds whose blocks write their rows themselves, unless they are cut
+constexpr bool writes_rows(int kind) { return kind == kWindow || kind == kChunk; }
 constexpr int kRows = 64;                       // per CTA
 constexpr int kPairRows = 128;                  // per pair
 constexpr int kTilePages = 4;
@@ -107,6 +110,7 @@ __device__ __forceinline__ uint32_t bar(uint64_t &b) { return smem_u32(&b); }
 template <int KIND>
 __device__ __forceinline__ ViewReq make_view(const DecodeParams &p, int v, const int2 *groups) {
   if constexpr (KIND == kWindow) return window_block<kPairRows>(p, v);
+  else if constexpr (KIND == kChunk) return chunk_block<kPairRows>(p, v);
   else return shared_view<kPairRows, KIND == kTails>(p, v, p.pair_blocks - p.pair_tails, groups);
 }
 template <int KIND>
@@ -610,7 +614,9 @@ __device__ __forceinline__ void softmax(const DecodeParams &p, const CtaRange &r
   bool ok = true;
   for (Pieces<F8, KIND> w(p, r, m); w.next(); w.advance(), ++o_it) {
     const int grow = w.view.row0 + int(rank) * kRows + row;
-    const RowView rv = row_view<KIND == kWindow>(p, w.view, min(grow, p.batch * p.heads - 1));
+    RowView rv;
+    if constexpr (KIND == kChunk) rv = chunk_row_view(p, w.view, min(grow, w.view.row0 + w.view.rows - 1));
+    else rv = row_view<KIND == kWindow>(p, w.view, min(grow, p.batch * p.heads - 1));
     const bool mine = int(rank) * kRows + row < w.view.rows;
     if constexpr (F8) {
       ok = split_q(p, m, smem, w.view, rank, st, o_it, ok);
@@ -738,11 +744,11 @@ __device__ __forceinline__ void softmax(const DecodeParams &p, const CtaRange &r
     ok = ok && __all_sync(0xffffffffu, mbar_wait_clk(bar(m.o_full), o_it & 1, abort, kTimeoutClk));
     const int c_first = sched_owner_short(w.pv, r.total, r.g_eff);
     const int pieces = sched_owner_short(w.pv + w.tiles - 1, r.total, r.g_eff) - c_first + 1;
-    const bool split = KIND != kWindow || pieces > 1;
+    const bool split = !writes_rows(KIND) || pieces > 1;
     // shared pages and tails: every piece leaves a partial, in the slots of its
-    // pair and block; a window's do when the block is cut, in the slots of the
-    // split merge, its CTA r * pairs + c standing for half r of pair c
-    const size_t slot = KIND == kWindow ? 2 * size_t(rank * p.pairs + pair_id) + (w.v != r.v_begin ? 1 : 0)
+    // pair and block; a window's and a chunk's do when the block is cut, in the slots
+    // of the split merge, its CTA r * pairs + c standing for half r of pair c
+    const size_t slot = writes_rows(KIND) ? 2 * size_t(rank * p.pairs + pair_id) + (w.v != r.v_begin ? 1 : 0)
                                         : 2 * size_t(pair_id + w.v) + rank;
     if (ok) {
       tc_fence_after();
@@ -783,7 +789,10 @@ __device__ __forceinline__ void softmax(const DecodeParams &p, const CtaRange &r
         else p.lse[grow] = lse_out(p, lse2);
       }
       if (st == 0 && pair_id == c_first) {
-        if (KIND == kWindow) {  // the record of this half's 64 rows
+        if (KIND == kChunk) {  // a pair begins at most one block that others go on with: the pair's record
+          if (rank == 0 && pieces > 1)
+            info_ptr(p)[pair_id] = make_int4(pieces, w.view.row0, w.view.rows, w.v != r.v_begin ? 1 : 0);
+        } else if (KIND == kWindow) {  // the record of this half's 64 rows
           if (w.view.rows > int(rank) * kRows)
             info_ptr(p)[(2 * (w.v / p.batch) + int(rank)) * p.batch + w.v % p.batch] =
                 make_int4(int(rank) * p.pairs + c_first, pieces, int(slot), 0);
@@ -864,7 +873,29 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       for (int i = tid; i < w.rows; i += kThreads) p.lse[size_t(w.row0) + i] = -INFINITY;
     }
   }
-  if constexpr (KIND == kWindow) {
+  if constexpr (KIND == kChunk) {
+    if (rank == 0 && tid == 128) info_ptr(p)[pair_id] = make_int4(0, 0, 0, 0);  // (the thread that sets it)
+    const int step = int(gridDim.x) * kThreads;
+    for (int b = int(blockIdx.x) * kThreads + tid; b < p.batch; b += step) {
+      checked_len(p, b, err);
+      const int s0 = p.chunk_starts[b], s1 = p.chunk_starts[b + 1];
+      if (s0 < 0 || s1 < s0 || s1 > p.chunk_tokens) atomicOr(err, kErrBadLen);
+    }
+    // blocks that see nothing: found by a lane each, written by the warp
+    for (int v0 = (int(blockIdx.x) * kThreads + tid) & ~31; v0 < p.pair_blocks; v0 += step) {
+      ViewReq w;
+      if (v0 + lane < p.pair_blocks) w = block_view<KIND>(p, v0 + lane, nullptr);
+      for (uint32_t left = __ballot_sync(0xffffffffu, w.rows > 0 && w.tiles == 0); left; left &= left - 1) {
+        const int from = __ffs(left) - 1;
+        const size_t row0 = __shfl_sync(0xffffffffu, w.row0, from);
+        const int rows = __shfl_sync(0xffffffffu, w.rows, from);
+        uint4 *dst = reinterpret_cast<uint4 *>(p.out + row0 * kDv);
+        for (int i = lane; i < rows * kDv / 8; i += 32) dst[i] = make_uint4(0, 0, 0, 0);
+        for (int i = lane; i < rows; i += 32) p.lse[row0 + i] = -INFINITY;
+      }
+    }
+  }
+  if constexpr (writes_rows(KIND)) {
     schedule_range<kPieceTiles<F8, KIND>, true>(
         p.pair_blocks, pair_id, p.pairs, [&](int v) { return tiles_of(block_view<KIND>(p, v, nullptr)); }, &m.range,
         m.scratch);
@@ -950,11 +981,16 @@ cudaError_t launch(const DecodeParams &p, const CUtensorMap &tm_q, const PairMap
 // in the other kernel, and the merge after them.)
 cudaError_t launch_split_merge(const DecodeParams &p, int grid, cudaStream_t stream);
 cudaError_t launch_shared_merge(const DecodeParams &p, int grid, cudaStream_t stream);
+cudaError_t launch_chunk_merge(const DecodeParams &p, cudaStream_t stream);
 
 // tm_q is read for a bf16 cache, m.k4 for an e4m3 one.
 cudaError_t launch_decode_pair(const DecodeParams &p, const CUtensorMap &tm_q, const PairMaps &m,
                                cudaStream_t stream) {
   const bool f8 = p.kv_e4m3 != 0;
+  if (p.view == kViewChunk) {
+    const cudaError_t e = f8 ? launch<true, kChunk>(p, tm_q, m, stream) : launch<false, kChunk>(p, tm_q, m, stream);
+    return e == cudaSuccess ? launch_chunk_merge(p, stream) : e;
+  }
   if (p.view == kViewWindow) {
     const cudaError_t e = f8 ? launch<true, kWindow>(p, tm_q, m, stream) : launch<false, kWindow>(p, tm_q, m, stream);
     return e == cudaSuccess ? launch_split_merge(p, 2 * p.pairs, stream) : e;

@@ -1,0 +1,157 @@
+// Chunks of rows between contiguous buffers and the paged latent cache: a ragged
+// batch of new tokens written into it (quantised to e4m3 where the cache is), and
+// cached rows read back as bf16.
+//
+//   append: row r of the chunk, token t = positions[b] + r - starts[b] of its request
+//           b, goes to cache row 64 table[b][t / 64] + t mod 64 as its bits, or as
+//           e4m3(fp32(x) / scale), rounded to nearest even and saturated.
+//   read:   the other way: the bits, or bf16(fp32(fp32(code) * scale)).
+//
+// Both move 1152 B (bf16) or 1152 + 576 B (e4m3) a row each way and compute next to
+// nothing: HBM bounds them.  A warp takes four rows, which are nine 16-byte (e4m3
+// side: 8-byte) chunks a lane, all in flight at once; its first four lanes look the
+// rows' places up, for an append while the loads are on their way.  The request of a
+// row is found by halving starts, whose few words stay in L1.
+#include "common.cuh"
+
+namespace mla {
+namespace {
+
+constexpr int kWarps = 4;
+constexpr int kRowsPerWarp = 4;
+constexpr int kLoads = kRowsPerWarp * kDqk / 8 / 32;  // chunks of 8 values a lane
+static_assert(kLoads * 32 * 8 == kRowsPerWarp * kDqk, "whole rows");
+constexpr int kErrChunkBadPage = 1;
+
+struct ChunkRows {
+  const int32_t *block_table;  // [batch, max_pages]
+  const int32_t *starts;       // [batch + 1]
+  const int32_t *positions;    // [batch]
+  int batch, rows, max_pages, num_pages, part_id, num_parts;
+  long long stride;            // values between rows of the contiguous buffer
+  float scale;
+  int32_t *error_word;
+};
+
+constexpr long long kNoRow = -1, kBadRow = -2;
+
+// The cache row of row r: kNoRow where the row is nobody's (outside all requests, of a
+// request with a negative position, or another partition's), kBadRow where the table
+// has no page for it.
+__device__ __forceinline__ long long cache_row(const ChunkRows &c, int r) {
+  if (r >= c.rows || r < c.starts[0] || r >= c.starts[c.batch]) return kNoRow;
+  int lo = 0, hi = c.batch - 1;  // the last request that starts at or before r
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (c.starts[mid] <= r) lo = mid;
+    else hi = mid - 1;
+  }
+  const int first = c.positions[lo], i = r - c.starts[lo];
+  if (first < 0 || i < 0) return kNoRow;
+  const long long t = (long long)first + i;
+  if (c.num_parts > 1 && t % c.num_parts != c.part_id) return kNoRow;
+  const long long lp = t / kPage;
+  const int pg = lp < c.max_pages ? c.block_table[(long long)lo * c.max_pages + lp] : -1;
+  if (pg < 0 || pg >= c.num_pages) return kBadRow;
+  return (long long)pg * kPage + t % kPage;
+}
+
+// Eight bf16 values as e4m3 codes of x / scale.
+__device__ __forceinline__ uint2 quantise(uint4 v, float scale) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  uint32_t o[2] = {0, 0};
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const uint32_t two = float2_to_e4m3x2(__fdiv_rn(__uint_as_float(w[k] << 16), scale),
+                                          __fdiv_rn(__uint_as_float(w[k] & 0xffff0000u), scale));
+    o[k >> 1] |= two << (16 * (k & 1));
+  }
+  return make_uint2(o[0], o[1]);
+}
+
+__device__ __forceinline__ uint4 dequantise(uint2 v, float scale) {
+  const uint32_t w[2] = {v.x, v.y};
+  uint32_t o[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const float2 f = e4m3x2_to_float2(uint16_t(w[k >> 1] >> (16 * (k & 1))));
+    __nv_bfloat162 h = __floats2bfloat162_rn(f.x * scale, f.y * scale);
+    o[k] = *reinterpret_cast<uint32_t *>(&h);
+  }
+  return make_uint4(o[0], o[1], o[2], o[3]);
+}
+
+// READ: cache -> buffer, else buffer -> cache.
+template <bool READ, bool F8>
+__global__ void __launch_bounds__(kWarps * 32) kv_chunk_kernel(const __grid_constant__ ChunkRows c,
+                                                               unsigned char *cache, __nv_bfloat16 *buffer) {
+  const int warp = int(blockIdx.x) * kWarps + int(threadIdx.x >> 5), lane = threadIdx.x & 31;
+  if (warp >= (c.rows + kRowsPerWarp - 1) / kRowsPerWarp) return;
+  const int r0 = warp * kRowsPerWarp;
+  constexpr int kChunks = kDqk / 8;           // of a row
+  constexpr int kBytes = F8 ? 8 : 16;         // of a chunk in the cache
+  uint4 v[kLoads];
+  if constexpr (!READ) {
+#pragma unroll
+    for (int u = 0; u < kLoads; ++u) {
+      const int r = r0 + (lane + 32 * u) / kChunks, k = (lane + 32 * u) % kChunks;
+      if (r < c.rows) v[u] = __ldcs(reinterpret_cast<const uint4 *>(buffer + r * c.stride) + k);
+    }
+  }
+  long long mine = kNoRow;
+  if (lane < kRowsPerWarp) {
+    mine = cache_row(c, r0 + lane);
+    if (mine == kBadRow && c.error_word) atomicOr(c.error_word, kErrChunkBadPage);
+  }
+  auto place = [&](int u) {  // chunk u of this lane in the cache, or a negative number
+    const long long row = __shfl_sync(0xffffffffu, mine, (lane + 32 * u) / kChunks);
+    return row < 0 ? row : row * (kDqk * kBytes / 8) + (lane + 32 * u) % kChunks * kBytes;
+  };
+  if constexpr (READ) {
+    uint2 w[kLoads];
+    long long at[kLoads];
+#pragma unroll
+    for (int u = 0; u < kLoads; ++u) {
+      at[u] = place(u);
+      v[u] = make_uint4(0, 0, 0, 0);
+      w[u] = make_uint2(0, 0);
+      if (at[u] < 0) continue;
+      if constexpr (F8) w[u] = __ldcs(reinterpret_cast<const uint2 *>(cache + at[u]));
+      else v[u] = __ldcs(reinterpret_cast<const uint4 *>(cache + at[u]));
+    }
+#pragma unroll
+    for (int u = 0; u < kLoads; ++u) {
+      if (at[u] == kNoRow) continue;
+      if constexpr (F8) v[u] = dequantise(w[u], c.scale);
+      const int r = r0 + (lane + 32 * u) / kChunks, k = (lane + 32 * u) % kChunks;
+      reinterpret_cast<uint4 *>(buffer + r * c.stride)[k] = v[u];
+    }
+  } else {
+#pragma unroll
+    for (int u = 0; u < kLoads; ++u) {
+      const long long at = place(u);
+      if (at < 0) continue;
+      if constexpr (F8) *reinterpret_cast<uint2 *>(cache + at) = quantise(v[u], c.scale);
+      else *reinterpret_cast<uint4 *>(cache + at) = v[u];
+    }
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_kv_chunk(bool read, void *cache, void *buffer, long long stride, const int32_t *block_table,
+                            const int32_t *starts, const int32_t *positions, int rows, int batch, int part_id,
+                            int num_parts, int num_pages, int max_pages, int e4m3, float kv_scale,
+                            int32_t *error_word, cudaStream_t stream) {
+  const ChunkRows c{block_table, starts, positions, batch,  rows,     max_pages, num_pages,
+                    part_id,     num_parts, stride,  kv_scale, error_word};
+  const int per = kWarps * kRowsPerWarp;
+  const unsigned grid = unsigned((rows + (long long)per - 1) / per);
+  auto *kernel = read ? (e4m3 ? kv_chunk_kernel<true, true> : kv_chunk_kernel<true, false>)
+                      : (e4m3 ? kv_chunk_kernel<false, true> : kv_chunk_kernel<false, false>);
+  kernel<<<grid, kWarps * 32, 0, stream>>>(c, static_cast<unsigned char *>(cache),
+                                           static_cast<__nv_bfloat16 *>(buffer));
+  return cudaGetLastError();
+}
+
+}  // namespace mla

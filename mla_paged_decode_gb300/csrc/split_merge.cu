@@ -314,6 +314,42 @@ __global__ void __launch_bounds__(kMergeWarps * 32, 7) shared_merge_kernel(Decod
   if (lane == 0) p.lse[row] = lse_out(p, merged_lse2(mref, sum));
 }
 
+// Chunks: the blocks of 128 rows that the pair kernel's schedule cut.  Pair c's record
+// is that of the block it begins and others go on with: {pieces, first row, rows, place
+// of its piece in its two slots}; half h of the block lies in the slots of "CTA"
+// h * pairs + c.  At most a block a pair is cut, so the grid is one column of warps per
+// pair, however many blocks there are.
+__global__ void __launch_bounds__(kMergeWarps * 32, 7) chunk_merge_kernel(DecodeParams p) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int c = blockIdx.x, lane = threadIdx.x & 31;
+  const int r = blockIdx.y * kMergeWarps + (threadIdx.x >> 5);  // row within the block
+  const int4 rec = info_ptr(p)[c];
+  if (rec.x < 2 || rec.x > p.pairs - c || rec.z > 128 || r >= rec.z || rec.y < 0 ||
+      (long long)rec.y + rec.z > (long long)p.chunk_tokens * p.q_heads)
+    return;
+  const int first = (r >> 6) * p.pairs + c;
+  uint32_t pk[8];
+  float lse2;
+  merge_split_row(p, make_int4(first, rec.x, 2 * first + (rec.w & 1), 0), r & 63, pk, &lse2);
+  const size_t row = size_t(rec.y) + r;
+  store_row(p.out + row * kDv, pk);
+  if (lane == 0) p.lse[row] = lse_out(p, lse2);
+}
+
+cudaError_t launch_chunk_merge(const DecodeParams &p, cudaStream_t stream) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(p.pairs, 128 / kMergeWarps);
+  cfg.blockDim = dim3(kMergeWarps * 32);
+  cfg.dynamicSmemBytes = 0;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, chunk_merge_kernel, p);
+}
+
 cudaError_t launch_shared_merge(const DecodeParams &p, int grid, cudaStream_t stream) {
   const int rows = p.batch * p.heads;
   const bool wide = rows <= 7 * grid;  // a CTA per row still fits the device in one wave
