@@ -506,6 +506,54 @@ int mla_prefill_chunk(const void *q, int num_tokens, const void *kv_pages, const
                       void *out, float *lse, const mla_decode_desc *d, void *workspace,
                       size_t workspace_bytes, mla_stream_t stream);
 
+/* Sizes and strides (in values) of an expanded prefill. */
+typedef struct mla_expanded_desc {
+  int32_t batch;     /* requests (0 is a no-op)                                   */
+  int32_t num_heads; /* 1..128                                                    */
+  int32_t q_tokens;  /* N, tokens of q (0 is a no-op); N x num_heads <= 2^30      */
+  int32_t k_tokens;  /* M, tokens of the keys, 0..2^30                            */
+  int32_t causal;    /* 1: query i of n over m keys sees the first m - n + i + 1;
+                        0: every query sees all keys of its request               */
+  int64_t q_token_stride, q_head_stride; /* every stride a multiple of 8, > 0     */
+  int64_t k_token_stride, k_head_stride;
+  int64_t rope_token_stride;
+  int64_t v_token_stride, v_head_stride;
+} mla_expanded_desc;
+
+/*
+ * Attention of many query tokens in the expanded form: keys and values of
+ * each head as the up-projection of the latent gives them, and one rope part
+ * for all heads.
+ *
+ *  q           bf16 [N, H, 192]: 128 dims of the head's own, 64 rope.
+ *  k_nope, v   bf16 [M, H, 128] each, k_rope bf16 [M, 64]: with the strides of
+ *              `d`, so that they may be parts of wider rows (of one
+ *              projection's output, of latent rows read back).  Values of a
+ *              row are consecutive; not read when M is 0.
+ *  q_starts, k_starts
+ *              int32 [batch + 1] each: request b's queries are tokens
+ *              q_starts[b] .. q_starts[b + 1] - 1, its keys likewise.  None is
+ *              below its predecessor or past N or M; query tokens of no
+ *              request keep what out and lse hold for them.
+ *  out, lse    bf16 [N, H, 128], fp32 [N, H], contiguous; a query that sees no
+ *              key gets the neutral pair (0, -inf).  Results over disjoint
+ *              keys (a chunk's own and its earlier context) merge with
+ *              mla_lse_combine.
+ *  sm_scale    finite and > 0.
+ *  workspace   >= mla_prefill_workspace_size(0) bytes, same rules as for
+ *              mla_decode_partial; starts out of range are cut to it and
+ *              reported as MLA_ERR_BOUNDS by mla_decode_check_workspace.
+ *
+ * fp32 accumulation; the softmax weights enter the second product rounded to
+ * bf16, their sum unrounded.  Keys past the last one that a block of 512
+ * queries sees may hold anything; a value row that only some of them see must
+ * be finite.  Bitwise deterministic for fixed inputs and device.  Two kernels.
+ */
+int mla_prefill_expanded(const void *q, const void *k_nope, const void *k_rope, const void *v,
+                         const int32_t *q_starts, const int32_t *k_starts, float sm_scale, int lse_base,
+                         void *out, float *lse, const mla_expanded_desc *d, void *workspace,
+                         size_t workspace_bytes, mla_stream_t stream);
+
 /*
  * Page operations.  A pool of cache pages is described by four device arrays
  * that the caller owns and the calls update in place:

@@ -21,7 +21,7 @@ __all__ = [
     "decode_partial_noalloc", "decode_window", "decode_shared", "make_shared_workspace",
     "pages_workspace_size", "make_pages_workspace", "pages_copy", "pages_fork", "pages_alloc",
     "pages_free", "pages_compact", "PAGES_BAD_ENTRY", "PAGES_FULL",
-    "kv_append_chunk", "kv_read", "prefill_chunk", "make_prefill_workspace",
+    "kv_append_chunk", "kv_read", "prefill_chunk", "prefill_expanded", "make_prefill_workspace",
 ]
 
 LSE_NATURAL = 0
@@ -71,6 +71,15 @@ class PagesDesc(ctypes.Structure):
     _fields_ = [("num_requests", ctypes.c_int32), ("max_pages_per_seq", ctypes.c_int32),
                 ("num_pages", ctypes.c_int32), ("page_size", ctypes.c_int32),
                 ("head_dim_qk", ctypes.c_int32), ("kv_dtype", ctypes.c_int32)]
+
+
+class ExpandedDesc(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int32), ("num_heads", ctypes.c_int32), ("q_tokens", ctypes.c_int32),
+                ("k_tokens", ctypes.c_int32), ("causal", ctypes.c_int32),
+                ("q_token_stride", ctypes.c_int64), ("q_head_stride", ctypes.c_int64),
+                ("k_token_stride", ctypes.c_int64), ("k_head_stride", ctypes.c_int64),
+                ("rope_token_stride", ctypes.c_int64), ("v_token_stride", ctypes.c_int64),
+                ("v_head_stride", ctypes.c_int64)]
 
 
 def load_library():
@@ -132,6 +141,9 @@ def load_library():
         lib.mla_prefill_workspace_size.restype = sz
         lib.mla_prefill_chunk.argtypes = [vp, i32, vp, vp, vp, vp, f32, i32, vp, vp, dd, vp, sz, vp]
         lib.mla_prefill_chunk.restype = i32
+        lib.mla_prefill_expanded.argtypes = [vp, vp, vp, vp, vp, vp, f32, i32, vp, vp, ctypes.POINTER(ExpandedDesc),
+                                             vp, sz, vp]
+        lib.mla_prefill_expanded.restype = i32
         lib.mla_status_string.argtypes = [i32]
         lib.mla_status_string.restype = ctypes.c_char_p
         lib.mla_last_cuda_error.argtypes = []
@@ -750,6 +762,72 @@ def prefill_chunk(q, kv_pages, block_table, seq_lens, chunk_starts, sm_scale: fl
     _launch(load_library().mla_prefill_chunk, dev, stream, q.data_ptr(), _int32(n, "tokens"), kv_pages.data_ptr(),
             block_table.data_ptr(), seq_lens.data_ptr(), chunk_starts.data_ptr(), float(sm_scale), lse_base,
             out.data_ptr(), lse.data_ptr(), d, workspace.data_ptr(), workspace.numel())
+    return out, lse
+
+
+_EXPANDED_DESCS: dict = {}
+
+
+def _stride(t, dim, least):
+    """A stride for the library: that of a dimension of one index may be
+    anything and is not used."""
+    return t.stride(dim) if t.shape[dim] > 1 else least
+
+
+def _expanded_desc(q, k_nope, k_rope, v, batch, causal):
+    key = (q.shape, q.stride(), k_nope.shape, k_nope.stride(), k_rope.shape, k_rope.stride(), v.shape, v.stride(),
+           batch, causal)
+    d = _EXPANDED_DESCS.get(key)
+    if d is None:
+        if q.dim() != 3 or q.shape[2] != 192:
+            raise ValueError("q must be [N, H, 192]")
+        n, heads, _ = q.shape
+        m = k_rope.shape[0] if k_rope.dim() == 2 else -1
+        if k_rope.dim() != 2 or k_rope.shape[1] != 64:
+            raise ValueError("k_rope must be [M, 64]")
+        if k_nope.shape != (m, heads, 128) or v.shape != (m, heads, 128):
+            raise ValueError("k_nope and v must be [M, H, 128], with q's heads and k_rope's tokens")
+        if any(t.stride(-1) != 1 for t in (q, k_nope, k_rope, v)):
+            raise ValueError("the values of a row of q, k_nope, k_rope and v must be consecutive")
+        if len(_EXPANDED_DESCS) > 256:
+            _EXPANDED_DESCS.clear()
+        d = _EXPANDED_DESCS[key] = ExpandedDesc(
+            _int32(batch, "batch"), _int32(heads, "heads"), _int32(n, "query tokens"), _int32(m, "key tokens"),
+            int(causal), _stride(q, 0, 192), _stride(q, 1, 192), _stride(k_nope, 0, 128), _stride(k_nope, 1, 128),
+            _stride(k_rope, 0, 64), _stride(v, 0, 128), _stride(v, 1, 128))
+    return ctypes.byref(d)
+
+
+def prefill_expanded(q, k_nope, k_rope, v, q_starts, k_starts, causal: bool, sm_scale: float, lse_base: int, out, lse,
+                     *, workspace=None, stream=None):
+    """mla_prefill_expanded: queries q bf16 [N, H, 192] over keys k_nope bf16
+    [M, H, 128] with k_rope bf16 [M, 64] for all heads, and values v bf16
+    [M, H, 128]; any strides with rows of consecutive values (parts of a
+    projection's output).  Request b's queries and keys are q_starts[b] ..
+    q_starts[b + 1] and k_starts[b] .. k_starts[b + 1] (int32 [B + 1] each);
+    causal: the last query sees all of them, the one before it one fewer.  out
+    bf16 [N, H, 128] and lse fp32 [N, H] are written in place.  The workspace
+    is make_prefill_workspace's."""
+    lse_base = _int32(lse_base, "lse_base")
+    dev = q.device
+    if dev.type != "cuda":
+        raise ValueError("prefill_expanded runs on CUDA tensors only")
+    for t, name in ((q, "q"), (k_nope, "k_nope"), (k_rope, "k_rope"), (v, "v")):
+        if not isinstance(t, torch.Tensor) or t.dtype != torch.bfloat16:
+            raise TypeError(f"{name} must be a bf16 tensor")
+        if t.device != dev:
+            raise ValueError(f"{name} is on {t.device}, expected {dev}")
+    _ints(q_starts, "q_starts", dev, 1)
+    _ints(k_starts, "k_starts", dev, 1)
+    B = q_starts.numel() - 1
+    if B < 0 or k_starts.numel() != B + 1:
+        raise ValueError("q_starts and k_starts must be [B + 1]")
+    d = _expanded_desc(q, k_nope, k_rope, v, B, bool(causal))
+    n, heads, _ = q.shape
+    workspace = _prefill_outputs(out, lse, dev, n, heads, 128, workspace, stream, q)
+    _launch(load_library().mla_prefill_expanded, dev, stream, q.data_ptr(), k_nope.data_ptr(), k_rope.data_ptr(),
+            v.data_ptr(), q_starts.data_ptr(), k_starts.data_ptr(), float(sm_scale), lse_base, out.data_ptr(),
+            lse.data_ptr(), d, workspace.data_ptr(), workspace.numel())
     return out, lse
 
 

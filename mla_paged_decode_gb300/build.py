@@ -24,7 +24,7 @@ OUT_DIR = os.path.join(HERE, "_lib")
 LIB_PATH = os.path.join(OUT_DIR, "libmla_decode.so")
 SOURCES = ["api.cu", "decode_simt.cu", "decode_tc.cu", "decode_tc_bf16.cu", "decode_tc_e4m3.cu",
            "decode_pair.cu", "split_merge.cu", "lse_combine.cu", "noalloc.cu", "kv_append.cu",
-           "kv_chunk.cu", "dcp_metadata.cu",
+           "kv_chunk.cu", "prefill_expanded.cu", "dcp_metadata.cu",
            "pages.cu", "selftest.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",

@@ -14,6 +14,7 @@
 #include "common.cuh"
 #include "pages.cuh"
 #include "pair_maps.cuh"
+#include "prefill_expanded.cuh"
 
 namespace mla {
 cudaError_t launch_decode_simt(const DecodeParams &p, int grid, cudaStream_t stream);
@@ -607,6 +608,42 @@ constexpr int kMaxGroups = 1 << 20;
 constexpr int kMaxView = 1 << 30;
 constexpr int kMaxChunkBatch = 1 << 20;
 
+// The expanded prefill's loads: (dims, heads, tokens) of each tensor, 64 dims of `box`
+// tokens of a head.  Without keys nothing is loaded through the maps of k and v, which
+// then describe a row of q.
+int make_expanded_maps(const void *q, const void *k_nope, const void *k_rope, const void *v,
+                       const mla_expanded_desc *d, mla::ExpandedMaps *m) {
+  EncodeTiled enc = encode_tiled();
+  if (!enc) {
+    std::snprintf(g_cuda_error, sizeof(g_cuda_error), "cuTensorMapEncodeTiled unavailable");
+    return MLA_ERR_CUDA;
+  }
+  CUresult r = CUDA_SUCCESS;
+  auto map = [&](CUtensorMap *tm, const void *base, int width, int heads, int64_t tokens, int64_t head_stride,
+                 int64_t token_stride, int box_tokens) {
+    const bool flat = heads == 0;  // (dims, tokens)
+    cuuint64_t dims[3] = {cuuint64_t(width), cuuint64_t(flat ? tokens : heads), cuuint64_t(tokens)};
+    cuuint64_t strides[2] = {cuuint64_t(flat ? token_stride : head_stride) * 2, cuuint64_t(token_stride) * 2};
+    cuuint32_t box[3] = {64, flat ? cuuint32_t(box_tokens) : 1u, cuuint32_t(box_tokens)}, es[3] = {1, 1, 1};
+    if (r == CUDA_SUCCESS)
+      r = enc(tm, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, flat ? 2 : 3, const_cast<void *>(base), dims, strides, box, es,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  };
+  const int H = d->num_heads;
+  map(&m->q, q, mla::kNope + mla::kRope, H, d->q_tokens, d->q_head_stride, d->q_token_stride, 128);
+  if (d->k_tokens == 0) {
+    m->k_nope = m->k_rope = m->v = m->va = m->vr = m->q;
+  } else {
+    map(&m->k_nope, k_nope, mla::kNope, H, d->k_tokens, d->k_head_stride, d->k_token_stride, 64);
+    map(&m->k_rope, k_rope, mla::kRope, 0, d->k_tokens, 0, d->rope_token_stride, 64);
+    map(&m->v, v, mla::kDvx, H, d->k_tokens, d->v_head_stride, d->v_token_stride, 128);
+    map(&m->va, v, mla::kDvx, H, d->k_tokens, d->v_head_stride, d->v_token_stride, 8);
+    map(&m->vr, v, mla::kDvx, H, d->k_tokens, d->v_head_stride, d->v_token_stride, 1);
+  }
+  return r == CUDA_SUCCESS ? MLA_OK : tensor_map_fail("expanded", r);
+}
+
 // kv_append_chunk and kv_read: `buffer` is the contiguous side.
 int kv_chunk(bool read, void *kv_pages, void *buffer, int64_t stride, int rows, const int32_t *block_table,
              const int32_t *starts, const int32_t *positions, int part_id, int num_parts, const mla_decode_desc *d,
@@ -810,7 +847,8 @@ size_t mla_prefill_workspace_size(int num_sms) {
     if (f.sms <= 0) return 0;
     num_sms = f.sms;
   }
-  return chunk_layout(num_sms).total;
+  const size_t chunk = chunk_layout(num_sms).total, expanded = mla::expanded_layout(num_sms / 2).total;
+  return chunk > expanded ? chunk : expanded;
 }
 
 int mla_prefill_chunk(const void *q, int num_tokens, const void *kv_pages, const int32_t *block_table,
@@ -865,6 +903,56 @@ int mla_prefill_chunk(const void *q, int num_tokens, const void *kv_pages, const
   st = make_q_map(encode_tiled(), q, cuuint64_t(num_tokens) * d->num_heads, 64, &tm_q);
   if (st != MLA_OK) return st;
   const cudaError_t e = mla::launch_decode_pair(p, tm_q, maps, reinterpret_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? MLA_OK : cuda_fail(e);
+}
+
+int mla_prefill_expanded(const void *q, const void *k_nope, const void *k_rope, const void *v,
+                         const int32_t *q_starts, const int32_t *k_starts, float sm_scale, int lse_base, void *out,
+                         float *lse, const mla_expanded_desc *d, void *workspace, size_t workspace_bytes,
+                         mla_stream_t stream) {
+  if (!d) return MLA_ERR_NULL;
+  if (d->batch < 0 || d->batch > kMaxChunkBatch || d->q_tokens < 0 || d->k_tokens < 0 || d->num_heads < 1 ||
+      d->num_heads > 128 || (long long)d->q_tokens * d->num_heads > (1LL << 30) || d->k_tokens > (1 << 30))
+    return MLA_ERR_SHAPE;
+  if (lse_base != MLA_LSE_NATURAL && lse_base != MLA_LSE_BASE2) return MLA_ERR_ARG;
+  if (!(std::isfinite(sm_scale) && sm_scale > 0.f)) return MLA_ERR_ARG;
+  if (d->causal != 0 && d->causal != 1) return MLA_ERR_ARG;
+  if (d->batch == 0 || d->q_tokens == 0) return MLA_OK;
+  const bool keys = d->k_tokens > 0;
+  if (!q || !q_starts || !k_starts || !out || !lse || !workspace || (keys && (!k_nope || !k_rope || !v)))
+    return MLA_ERR_NULL;
+  if (!aligned(q, 16) || !aligned(out, 16) || !aligned(lse, 4) || !aligned(q_starts, 4) || !aligned(k_starts, 4) ||
+      !aligned(workspace, 256) || (keys && (!aligned(k_nope, 16) || !aligned(k_rope, 16) || !aligned(v, 16))))
+    return MLA_ERR_ALIGN;
+  const int64_t strides[7] = {d->q_token_stride, d->q_head_stride, d->k_token_stride, d->k_head_stride,
+                              d->rope_token_stride, d->v_token_stride, d->v_head_stride};
+  for (int i = keys ? 6 : 1; i >= 0; --i) {
+    if (strides[i] <= 0 || strides[i] >= (1LL << 38)) return MLA_ERR_SHAPE;
+    if (strides[i] % 8 != 0) return MLA_ERR_ALIGN;
+  }
+  int st = MLA_OK;
+  const DeviceFacts f = current_device(&st);
+  if (st != MLA_OK) return st;
+  mla::ExpandedParams p;
+  p.pairs = f.sms / 2;
+  if (workspace_bytes < mla::expanded_layout(p.pairs).total) return MLA_ERR_WORKSPACE;
+  p.out = static_cast<__nv_bfloat16 *>(out);
+  p.lse = lse;
+  p.ws = static_cast<unsigned char *>(workspace);
+  p.q_starts = q_starts;
+  p.k_starts = k_starts;
+  p.batch = d->batch;
+  p.heads = d->num_heads;
+  p.q_tokens = d->q_tokens;
+  p.k_tokens = d->k_tokens;
+  p.causal = d->causal;
+  p.blocks = d->q_tokens / mla::kExpRows + d->batch;
+  p.score_scale_log2 = sm_scale * mla::kLog2e;
+  p.lse_base2 = lse_base == MLA_LSE_BASE2;
+  mla::ExpandedMaps m;
+  st = make_expanded_maps(q, keys ? k_nope : q, keys ? k_rope : q, keys ? v : q, d, &m);
+  if (st != MLA_OK) return st;
+  const cudaError_t e = mla::launch_prefill_expanded(p, m, reinterpret_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? MLA_OK : cuda_fail(e);
 }
 

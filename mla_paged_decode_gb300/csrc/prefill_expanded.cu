@@ -1,0 +1,689 @@
+// Attention of many query tokens over expanded keys and values (a head's 128 score dims
+// and 128 value dims from the latent's up-projection, 64 rope dims shared by all heads):
+//
+//   s_ij = scale (q_i . [k_j ; rope_j]),  out_i = sum_j softmax(s_i)_j v_j
+//
+// 640 flops a (query head, key): two products with a softmax between them, bound by the
+// tensor cores once a head's keys are read for some 100 queries.
+//
+// A block of 512 query tokens of one head belongs to a pair of CTAs (cta_group::2,
+// M = 256): two halves of 256 tokens, 128 of each half in either CTA.  Each CTA loads
+// half of every operand B (64 of a tile's 128 keys for the scores, 64 of the 128 value
+// dims), so that a tile costs an SM 40 KB of loads for 512 queries, and a stage is small
+// enough for three of them beside the queries (96 KB).
+//
+// TMEM (512 columns): scores of half 0 and 1 (128 each), outputs of half 0 and 1 (128
+// each).  The softmax weights of a half, bf16, overlay its scores and are operand A of
+// the second product straight from TMEM: nothing of them passes through shared memory.
+//
+// Roles (384 threads): warp 0 loads, warp 1 of the even CTA issues the MMAs, warps 4..7
+// and 8..11 the softmax of half 0 and 1, a thread a row (no exchange between threads).
+// The halves take turns on the tensor cores: S0(j+1) follows P0(j) V(j) while the
+// softmax of half 1 works on S1(j), and the other way round.  As MMAs complete in order,
+// "S_h(j) is ready" also says that P_h(j-1) V(j-1) is done, so one barrier each way and
+// half is all that the softmax needs, the rare rescale of an output (a maximum that grew
+// by more than 2^8, as in the decode kernel) and a block's epilogue included.
+//
+// Work: the 128-key tiles of all (head, block) in one line, head by head, cut into equal
+// ranges, one a pair: neighbours share a head's keys in L2, the triangle of a causal mask
+// evens out, and few queries over long keys spread over all SMs.  At most two blocks a
+// pair are cut; their pieces leave fp32 partials for a merge by their LSE.
+#include "prefill_expanded.cuh"
+#include "sm100.cuh"
+
+namespace mla {
+using namespace sm100;
+
+namespace {
+
+constexpr int kThreads = 384;
+constexpr int kHalf = 256;     // query tokens of a half
+constexpr int kKeys = 128;     // of a tile
+constexpr int kStages = 3;
+constexpr int kQHalfBytes = 3 * 128 * 128;   // [dim block of 64][128 tokens][128 B], swizzled
+constexpr int kKBytes = 3 * 64 * 128;        // [dim block of 64][64 keys][128 B]
+constexpr int kVBytes = 128 * 128;           // [128 keys][128 B]
+constexpr int kOffK = 2 * kQHalfBytes;
+constexpr int kOffV = kOffK + kStages * kKBytes;
+constexpr int kOffMisc = kOffV + kStages * kVBytes;
+constexpr uint32_t kColS = 0, kColO = 256;   // half h: + 128 h
+constexpr int kPieceTiles = 2;               // a piece's boundary (Q, first scores, epilogue) in tiles
+constexpr long long kTimeoutClk = 4000000000ll;  // about 2 s
+constexpr uint64_t kDrainNs = 200000000ull;
+constexpr float kRescaleThreshold = 8.f;     // base-2 units
+
+struct Misc {
+  uint64_t k_full[kStages], k_empty[kStages], v_full[kStages], v_empty[kStages];
+  uint64_t q_full[2], q_empty[2], s_full[2], p_full[2], o_full[2], drain;
+  uint32_t tmem_base;
+  int abort;
+  CtaRange range;
+  long long scratch[kThreads / 32 + 1];
+};
+constexpr int kSmemBytes = kOffMisc + int(sizeof(Misc)) + 1024;
+static_assert(kSmemBytes <= 232448, "shared memory budget");
+
+__device__ __forceinline__ uint32_t bar(uint64_t &b) { return smem_u32(&b); }
+__device__ __forceinline__ int *error_word(const ExpandedParams &p) { return reinterpret_cast<int *>(p.ws); }
+__device__ __forceinline__ int4 *records(const ExpandedParams &p) {
+  return reinterpret_cast<int4 *>(p.ws + expanded_layout(p.pairs).rec);
+}
+__device__ __forceinline__ float *slot_lse(const ExpandedParams &p) {
+  return reinterpret_cast<float *>(p.ws + expanded_layout(p.pairs).lse);
+}
+__device__ __forceinline__ float *slot_out(const ExpandedParams &p) {
+  return reinterpret_cast<float *>(p.ws + expanded_layout(p.pairs).out);
+}
+
+__device__ __forceinline__ int start_in(const int32_t *starts, int b, int most) {
+  return min(max(starts[b], 0), most);
+}
+
+// A block of up to 512 query tokens of one request.  Request b's blocks have ids
+// floor(its first token / 512) + b and up, which leaves it as many as it needs; ids
+// between are empty.
+struct Block {
+  int rows = 0;      // query tokens
+  int q0 = 0;        // the first of them
+  int k0 = 0;        // the request's first key
+  int hi0 = 0, nk = 0;  // row i sees the first min(max(hi0 + i, 0), nk) keys
+  int tiles = 0;     // of 128 keys that some row sees
+  int half0 = 0;     // of these, the tiles that a row of half 0 sees
+  __device__ __forceinline__ int sees(int row) const {
+    return int(min(max((long long)hi0 + row, 0ll), (long long)nk));
+  }
+  __device__ __forceinline__ int end() const { return sees(rows - 1); }
+  // tiles of half h within [t0, t1)
+  __device__ __forceinline__ int count(int h, long long t0, long long t1) const {
+    const long long n = h == 0 ? half0 : rows > kHalf ? tiles : 0;
+    return int(max(0ll, min(t1, n) - t0));
+  }
+};
+
+__device__ __forceinline__ Block make_block(const ExpandedParams &p, int u) {
+  Block b;
+  int lo = 0, hi = p.batch - 1;  // the last request whose blocks start at or before u
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (start_in(p.q_starts, mid, p.q_tokens) / kExpRows + mid <= u) lo = mid;
+    else hi = mid - 1;
+  }
+  const int s0 = start_in(p.q_starts, lo, p.q_tokens), n = start_in(p.q_starts, lo + 1, p.q_tokens) - s0;
+  const long long first = (long long)(u - s0 / kExpRows - lo) * kExpRows;
+  if (first < 0 || first >= n) return b;
+  b.rows = min(kExpRows, n - int(first));
+  b.q0 = s0 + int(first);
+  b.k0 = start_in(p.k_starts, lo, p.k_tokens);
+  b.nk = max(0, start_in(p.k_starts, lo + 1, p.k_tokens) - b.k0);
+  // (without a mask, hi0 is large enough for every row; nk <= 2^30)
+  b.hi0 = p.causal ? b.nk - n + int(first) + 1 : b.nk;
+  b.tiles = (b.end() + kKeys - 1) / kKeys;
+  b.half0 = (b.sees(min(b.rows, kHalf) - 1) + kKeys - 1) / kKeys;
+  return b;
+}
+
+// The pieces of this pair's range, in order: item v is block v % blocks of head v / blocks.
+struct Pieces {
+  const ExpandedParams &p;
+  const CtaRange &r;
+  long long v;
+  long long pv, t0, t1;
+  Block b;
+  __device__ __forceinline__ Pieces(const ExpandedParams &p_, const CtaRange &r_)
+      : p(p_), r(r_), v(r_.v_begin), pv(r_.p_begin) {}
+  __device__ __forceinline__ bool next() {
+    const long long items = (long long)p.blocks * p.heads;
+    while (v < items && pv < r.end) {
+      b = make_block(p, int(v % p.blocks));
+      if (b.tiles) {
+        t0 = max(r.start, pv) - pv;
+        t1 = min(r.end, pv + b.tiles) - pv;
+        if (t0 < t1) return true;
+      }
+      advance();
+    }
+    return false;
+  }
+  __device__ __forceinline__ void advance() {
+    pv += request_cost(b.tiles, kPieceTiles);
+    ++v;
+  }
+  __device__ __forceinline__ int head() const { return int(v / p.blocks); }
+};
+
+// This pair's range of the line of all heads' blocks, which is the line of one head
+// `heads` times over.  Block-wide.
+__device__ __forceinline__ void schedule_heads(const ExpandedParams &p, int idx, CtaRange *r, long long *scratch) {
+  const int tid = threadIdx.x, nw = kThreads / 32, lane = tid & 31, warp = tid >> 5;
+  long long mine = 0;
+  for (int u = tid; u < p.blocks; u += kThreads) mine += request_cost(make_block(p, u).tiles, kPieceTiles);
+  for (int o = 16; o; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
+  if (lane == 0) scratch[warp] = mine;
+  __syncthreads();
+  long long one = 0;
+  for (int w = 0; w < nw; ++w) one += scratch[w];
+  const long long C = one * p.heads;
+  const int g = int(C < (long long)p.pairs ? C : (long long)p.pairs);
+  const bool has = idx < g;
+  const long long start = has ? sched_start(idx, C, g) : 0, end = has ? sched_start(idx + 1, C, g) : 0;
+  const long long h0 = has ? start / one : 0, r0 = start - h0 * one;
+  if (tid == 0) {
+    r->total = C;
+    r->g_eff = g;
+    r->start = start;
+    r->end = end;
+    r->v_begin = int((h0 + 1) * p.blocks);  // where r0 lies behind the last block's tiles
+    r->p_begin = (h0 + 1) * one;
+  }
+  __syncthreads();  // (scratch is read, the defaults are written)
+  if (!has) return;
+  // the first block whose tiles end after r0; its predecessor's end at `excl - kPieceTiles`
+  long long base = 0;
+  for (int u0 = 0; u0 < p.blocks && base <= r0; u0 += kThreads) {
+    const int u = u0 + tid;
+    const int tiles = u < p.blocks ? make_block(p, u).tiles : 0;
+    const long long cst = request_cost(tiles, kPieceTiles);
+    long long incl = cst;
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long y = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += y;
+    }
+    __syncthreads();
+    if (lane == 31) scratch[warp] = incl;
+    __syncthreads();
+    long long before = 0, chunk = 0;
+    for (int w = 0; w < nw; ++w) {
+      if (w < warp) before += scratch[w];
+      chunk += scratch[w];
+    }
+    const long long excl = base + before + incl - cst;
+    if (tiles > 0 && excl + tiles > r0 && excl - kPieceTiles <= r0) {
+      r->v_begin = int(h0 * p.blocks) + u;
+      r->p_begin = h0 * one + excl;
+    }
+    base += chunk;
+  }
+  __syncthreads();
+}
+
+// ------------------------------------------------------------------ producer
+
+// The value rows of a tile of which only the first `left` (< 128) are seen: the others may
+// hold anything (the next request's rows, or what was there), and weights of 0 do not
+// keep a NaN out of the product.  They are loaded from past the end, as zeros.
+static __device__ __noinline__ void load_seen_v(uint32_t dst, uint32_t full, const CUtensorMap *tm_va,
+                                                const CUtensorMap *tm_vr, int d0, int head, int key, int left,
+                                                int none) {
+#pragma unroll 1
+  for (int a = 0; a < kKeys; a += 8) {
+    if (a + 8 <= left || a >= left) {
+      tma_load_3d_pair(dst + a * 128, tm_va, full, d0, head, a < left ? key + a : none);
+      continue;
+    }
+#pragma unroll 1
+    for (int k = a; k < a + 8; ++k)
+      tma_load_3d_pair(dst + k * 128, tm_vr, full, d0, head, k < left ? key + k : none);
+  }
+}
+
+__device__ __forceinline__ void produce(const ExpandedParams &p, const CtaRange &r, Misc &m, uint32_t sbase,
+                                        uint32_t rank, const CUtensorMap *tm_q, const CUtensorMap *tm_kn,
+                                        const CUtensorMap *tm_kr, const CUtensorMap *tm_v, const CUtensorMap *tm_va,
+                                        const CUtensorMap *tm_vr, int *err) {
+  volatile int *abort = &m.abort;
+  const bool leader = rank == 0;
+  const uint32_t k_full = map_to_rank(bar(m.k_full[0]), 0), v_full = map_to_rank(bar(m.v_full[0]), 0);
+  const uint32_t q_full = map_to_rank(bar(m.q_full[0]), 0);
+  int st = 0;
+  uint32_t lap = 1, q_lap[2] = {1, 1};  // parity of the empty barriers' last phase
+  bool ok = true;
+  for (Pieces w(p, r); ok && w.next(); w.advance()) {
+    const int head = w.head(), end = w.b.end();
+    for (long long t = w.t0; ok && t < w.t1; ++t) {
+      const int key = w.b.k0 + int(t) * kKeys, left = end - int(t) * kKeys;
+      ok = mbar_wait_clk(bar(m.k_empty[st]), lap, abort, kTimeoutClk);
+      if (!ok) break;
+      if (leader) mbar_arrive_expect_tx(bar(m.k_full[st]), 2 * kKBytes);
+      const uint32_t dk = sbase + kOffK + st * kKBytes;
+      tma_load_3d_pair(dk, tm_kn, k_full + 8 * st, 0, head, key + 64 * int(rank));
+      tma_load_3d_pair(dk + 8192, tm_kn, k_full + 8 * st, 64, head, key + 64 * int(rank));
+      tma_load_2d_pair(dk + 16384, tm_kr, k_full + 8 * st, 0, key + 64 * int(rank));
+      if (t == w.t0) {
+        for (int h = 0; ok && h < 2; ++h) {
+          if (w.b.count(h, w.t0, w.t1) == 0) continue;
+          ok = mbar_wait_clk(bar(m.q_empty[h]), q_lap[h], abort, kTimeoutClk);
+          if (!ok) break;
+          q_lap[h] ^= 1;
+          if (leader) mbar_arrive_expect_tx(bar(m.q_full[h]), 2 * kQHalfBytes);
+          for (int i = 0; i < 3; ++i)
+            tma_load_3d_pair(sbase + h * kQHalfBytes + i * 16384, tm_q, q_full + 8 * h, 64 * i, head,
+                             w.b.q0 + kHalf * h + 128 * int(rank));
+        }
+        if (!ok) break;
+      }
+      ok = mbar_wait_clk(bar(m.v_empty[st]), lap, abort, kTimeoutClk);
+      if (!ok) break;
+      if (leader) mbar_arrive_expect_tx(bar(m.v_full[st]), 2 * kVBytes);
+      const uint32_t dv = sbase + kOffV + st * kVBytes;
+      if (left >= kKeys) tma_load_3d_pair(dv, tm_v, v_full + 8 * st, 64 * int(rank), head, key);
+      else load_seen_v(dv, v_full + 8 * st, tm_va, tm_vr, 64 * int(rank), head, key, left, p.k_tokens);
+      if (++st == kStages) st = 0, lap ^= 1;
+    }
+  }
+  if (!ok) atomicOr(err, kErrTimeout);
+}
+
+// ------------------------------------------------------------------ MMAs (even CTA)
+
+// A wait of a whole warp (the same answer in every lane).
+__device__ __forceinline__ bool warp_wait(uint32_t b, uint32_t parity, volatile int *abort) {
+  return __all_sync(0xffffffffu, mbar_wait_clk(b, parity, abort, kTimeoutClk));
+}
+
+__device__ __forceinline__ void mmas(const ExpandedParams &p, const CtaRange &r, Misc &m, uint32_t sbase,
+                                     uint32_t tmem, int *err) {
+  volatile int *abort = &m.abort;
+  const uint32_t idesc_s = idesc_bf16_f32(256, 128, false, false), idesc_o = idesc_bf16_f32(256, 128, false, true);
+  const uint64_t dq = smem_desc_sw128(sbase, 16, 1024), dk = smem_desc_sw128(sbase + kOffK, 16, 1024);
+  const uint64_t dv = smem_desc_sw128(sbase + kOffV, 16384, 1024);  // MN-major: 8-key groups 1 KB apart
+  int kst = 0, vst = 0;
+  uint32_t k_lap = 0, v_lap = 0, q_lap[2] = {0, 0}, p_lap[2] = {0, 0};
+  bool ok = true;
+  for (Pieces w(p, r); ok && w.next(); w.advance()) {
+    const int n = int(w.t1 - w.t0);
+    const int cnt[2] = {w.b.count(0, w.t0, w.t1), w.b.count(1, w.t0, w.t1)};
+    for (int j = 0; ok && j <= n; ++j) {
+      if (j > 0) ok = warp_wait(bar(m.v_full[vst]), v_lap, abort);
+      if (ok && j < n) ok = warp_wait(bar(m.k_full[kst]), k_lap, abort);
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        if (ok && j > 0 && j <= cnt[h]) {
+          ok = warp_wait(bar(m.p_full[h]), p_lap[h], abort);
+          p_lap[h] ^= 1;
+          tc_fence_after();
+          if (ok && elect_one()) {
+#pragma unroll
+            for (int ks = 0; ks < 8; ++ks)
+              mma_bf16_ts_pair(tmem + kColO + 128 * h, tmem + kColS + 128 * h + 8 * ks,
+                               dv + ((vst * kVBytes + ks * 2048) >> 4), idesc_o, j > 1 || ks > 0);
+            if (j == cnt[h]) mma_commit_pair(bar(m.o_full[h]));
+          }
+          __syncwarp();
+        }
+        if (ok && j < cnt[h]) {
+          if (j == 0) {
+            ok = warp_wait(bar(m.q_full[h]), q_lap[h], abort);
+            q_lap[h] ^= 1;
+          }
+          if (ok && elect_one()) {
+#pragma unroll
+            for (int ks = 0; ks < 12; ++ks)
+              mma_bf16_ss_pair(tmem + kColS + 128 * h,
+                               dq + ((h * kQHalfBytes + (ks >> 2) * 16384 + (ks & 3) * 32) >> 4),
+                               dk + ((kst * kKBytes + (ks >> 2) * 8192 + (ks & 3) * 32) >> 4), idesc_s, ks > 0);
+            mma_commit_pair(bar(m.s_full[h]));
+            if (j == cnt[h] - 1) mma_commit_pair(bar(m.q_empty[h]));
+          }
+          __syncwarp();
+        }
+      }
+      if (!ok) break;
+      if (elect_one()) {
+        if (j > 0) mma_commit_pair(bar(m.v_empty[vst]));
+        if (j < n) mma_commit_pair(bar(m.k_empty[kst]));
+      }
+      __syncwarp();
+      if (j > 0 && ++vst == kStages) vst = 0, v_lap ^= 1;
+      if (j < n && ++kst == kStages) kst = 0, k_lap ^= 1;
+    }
+  }
+  if (elect_one()) {
+    if (!ok) atomicOr(err, kErrTimeout);
+    mma_commit_pair(bar(m.drain));
+  }
+  __syncwarp();
+}
+
+// ------------------------------------------------------------------ softmax and epilogue
+
+__device__ __forceinline__ float exp2_approx(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 r;
+  asm("{ .reg .b64 x, y, z, d; mov.b64 x, {%2, %3}; mov.b64 y, {%4, %5}; mov.b64 z, {%6, %7};\n"
+      "fma.rn.f32x2 d, x, y, z; mov.b64 {%0, %1}, d; }"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return r;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 r;
+  asm("{ .reg .b64 x, y, d; mov.b64 x, {%2, %3}; mov.b64 y, {%4, %5};\n"
+      "add.rn.f32x2 d, x, y; mov.b64 {%0, %1}, d; }"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return r;
+}
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<uint32_t *>(&v);
+}
+
+// O *= alpha (this thread's row).
+static __device__ __noinline__ void rescale_row(uint32_t taddr, float alpha) {
+  for (int c = 0; c < kDvx; c += 16) {
+    uint32_t o[16];
+    tmem_ld16(taddr + c, o);
+    tmem_wait_ld();
+#pragma unroll
+    for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
+    tmem_st16(taddr + c, o);
+  }
+  tmem_wait_st();
+}
+
+// A failed wait never leaves the loop: the warp goes on without working (later waits
+// fail at once).
+__device__ __forceinline__ void softmax(const ExpandedParams &p, const CtaRange &r, Misc &m, uint32_t tmem,
+                                        uint32_t rank, int pair_id, int *err) {
+  volatile int *abort = &m.abort;
+  const int warp = int(threadIdx.x >> 5) - 4, lane = threadIdx.x & 31;
+  const int h = warp >> 2, q = warp & 3;
+  const int row = kHalf * h + 128 * int(rank) + 32 * q + lane;  // within the block
+  const uint32_t lanes = uint32_t(32 * q) << 16;
+  const uint32_t t_s = tmem + lanes + kColS + 128 * h, t_o = tmem + lanes + kColO + 128 * h;
+  const uint32_t p_full = map_to_rank(bar(m.p_full[h]), 0);
+  const float cs = p.score_scale_log2;
+  uint32_t s_lap = 0, o_lap = 0;
+  bool ok = true;
+  for (Pieces w(p, r); w.next(); w.advance()) {
+    const int cnt = w.b.count(h, w.t0, w.t1);
+    const int sees = row < w.b.rows ? w.b.sees(row) : 0;
+    float mrun = -INFINITY;
+    float2 sum = make_float2(0.f, 0.f);
+    for (int j = 0; j < cnt; ++j) {
+      ok = ok && __all_sync(0xffffffffu, mbar_wait_clk(bar(m.s_full[h]), s_lap, abort, kTimeoutClk));
+      s_lap ^= 1;
+      if (!ok) continue;
+      tc_fence_after();
+      uint32_t a[4][32];
+#pragma unroll
+      for (int c = 0; c < 4; ++c) tmem_ld32(t_s + 32 * c, a[c]);
+      tmem_wait_ld();
+      float x[kKeys];
+#pragma unroll
+      for (int i = 0; i < kKeys; ++i) x[i] = __uint_as_float(a[i >> 5][i & 31]);
+      const int left = sees - (int(w.t0) + j) * kKeys;
+      if (left < kKeys) {
+#pragma unroll
+        for (int i = 0; i < kKeys; ++i) x[i] = i < left ? x[i] : -INFINITY;
+      }
+      float mx[4] = {x[0], x[1], x[2], x[3]};
+#pragma unroll
+      for (int i = 4; i < kKeys; i += 8)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) mx[k] = fmaxf(fmaxf(mx[k], x[i + k]), i + 4 + k < kKeys ? x[i + 4 + k] : x[i + k]);
+      const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * cs;
+      float alpha = 1.f;
+      if (j == 0) {
+        mrun = top;
+      } else if (top > mrun + kRescaleThreshold) {
+        alpha = exp2f(mrun - top);
+        mrun = top;
+        sum.x *= alpha;
+        sum.y *= alpha;
+      }
+      // a row that has seen no key yet keeps a -inf maximum: its weights are 0
+      const float mref = mrun == -INFINITY ? 0.f : mrun;
+      const float2 cs2 = make_float2(cs, cs), mn2 = make_float2(-mref, -mref);
+      if (__any_sync(0xffffffffu, alpha != 1.f)) rescale_row(t_o, alpha);
+#pragma unroll
+      for (int c = 0; c < kKeys; c += 32) {
+        uint32_t pk[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const float2 y = fma2(make_float2(x[c + 2 * i], x[c + 2 * i + 1]), cs2, mn2);
+          const float2 e = make_float2(exp2_approx(y.x), exp2_approx(y.y));
+          sum = add2(sum, e);
+          pk[i] = pack_bf16(e.x, e.y);
+        }
+        tmem_st16(t_s + c / 2, pk);
+      }
+      tmem_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cluster(p_full);
+    }
+    // ---- the piece's rows: O / sum and the LSE
+    const float total = sum.x + sum.y;
+    const float inv = total > 0.f ? 1.f / total : 0.f;
+    const float lse2 = mrun + log2f(total);
+    const int c_first = sched_owner_short(w.pv, r.total, r.g_eff);
+    const int pieces = sched_owner_short(w.pv + w.b.tiles - 1, r.total, r.g_eff) - c_first + 1;
+    // a pair's slot 0: a block that another pair began; slot 1: one that it begins
+    const size_t slot = (2 * size_t(pair_id) + (w.t0 == 0 ? 1 : 0)) * kExpRows + row;
+    const size_t orow = size_t(w.b.q0 + row) * p.heads + w.head();
+    const bool mine = row < w.b.rows;
+    if (cnt > 0) {
+      ok = ok && __all_sync(0xffffffffu, mbar_wait_clk(bar(m.o_full[h]), o_lap, abort, kTimeoutClk));
+      o_lap ^= 1;
+    }
+    if (ok) {
+      tc_fence_after();
+#pragma unroll 1
+      for (int c = 0; c < kDvx; c += 32) {
+        uint32_t o[32];
+        if (cnt > 0) {
+          tmem_ld32(t_o + c, o);
+          tmem_wait_ld();
+        } else {
+#pragma unroll
+          for (int i = 0; i < 32; ++i) o[i] = 0;
+        }
+        if (!mine) continue;
+        if (pieces > 1) {
+          float4 *dst = reinterpret_cast<float4 *>(slot_out(p) + slot * kDvx + c);
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            dst[i] = make_float4(__uint_as_float(o[4 * i]) * inv, __uint_as_float(o[4 * i + 1]) * inv,
+                                 __uint_as_float(o[4 * i + 2]) * inv, __uint_as_float(o[4 * i + 3]) * inv);
+        } else {
+          uint4 *dst = reinterpret_cast<uint4 *>(p.out + orow * kDvx + c);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            uint32_t v[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              v[k] = pack_bf16(__uint_as_float(o[8 * i + 2 * k]) * inv, __uint_as_float(o[8 * i + 2 * k + 1]) * inv);
+            dst[i] = make_uint4(v[0], v[1], v[2], v[3]);
+          }
+        }
+      }
+      tc_fence_before();
+      if (mine) {
+        if (pieces > 1) slot_lse(p)[slot] = lse2;
+        else p.lse[orow] = p.lse_base2 ? lse2 : lse2 * kLn2;
+      }
+      if (pieces > 1 && pair_id == c_first && rank == 0 && threadIdx.x == 128)
+        records(p)[pair_id] = make_int4(pieces, w.b.q0, w.b.rows, w.head());
+    }
+  }
+  if (!ok) atomicOr(err, kErrTimeout);
+}
+
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+    prefill_expanded_kernel(const __grid_constant__ ExpandedParams p, const __grid_constant__ CUtensorMap tm_q,
+                            const __grid_constant__ CUtensorMap tm_kn, const __grid_constant__ CUtensorMap tm_kr,
+                            const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_va,
+                            const __grid_constant__ CUtensorMap tm_vr) {
+  extern __shared__ unsigned char smem_raw[];
+  const uint32_t raw = smem_u32(smem_raw), pad = ((raw + 1023u) & ~1023u) - raw;
+  const uint32_t sbase = raw + pad;
+  Misc &m = *reinterpret_cast<Misc *>(smem_raw + pad + kOffMisc);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const uint32_t rank = cluster_rank();
+  const int pair_id = int(blockIdx.x) >> 1;
+  int *err = error_word(p);
+
+  if (tid == 0) {
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(bar(m.k_full[s]), 1);
+      mbar_init(bar(m.k_empty[s]), 1);
+      mbar_init(bar(m.v_full[s]), 1);
+      mbar_init(bar(m.v_empty[s]), 1);
+    }
+    for (int h = 0; h < 2; ++h) {
+      mbar_init(bar(m.q_full[h]), 1);
+      mbar_init(bar(m.q_empty[h]), 1);
+      mbar_init(bar(m.s_full[h]), 1);
+      mbar_init(bar(m.p_full[h]), 8);  // a half's four warps in each CTA
+      mbar_init(bar(m.o_full[h]), 1);
+    }
+    mbar_init(bar(m.drain), 1);
+    m.abort = 0;
+    fence_barrier_init();
+  }
+  // Allocating TMEM for a pair acts on both SMs: the other CTA has to be running by then.
+  __syncthreads();
+  cluster_sync();
+  if (warp == 1) {
+    __syncwarp();
+    tmem_alloc_pair(smem_u32(&m.tmem_base), 512);
+    tmem_relinquish_pair();
+  }
+  if (warp == 0 && lane == 0) {
+    tma_prefetch_desc(&tm_q);
+    tma_prefetch_desc(&tm_kn);
+    tma_prefetch_desc(&tm_kr);
+    tma_prefetch_desc(&tm_v);
+  }
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (rank == 0 && tid == 128) records(p)[pair_id] = make_int4(0, 0, 0, 0);  // (the thread that sets it)
+  const int step = int(gridDim.x) * kThreads;
+  for (int b = int(blockIdx.x) * kThreads + tid; b < p.batch; b += step) {
+    const int q0 = p.q_starts[b], q1 = p.q_starts[b + 1], k0 = p.k_starts[b], k1 = p.k_starts[b + 1];
+    if (q0 < 0 || q1 < q0 || q1 > p.q_tokens || k0 < 0 || k1 < k0 || k1 > p.k_tokens) atomicOr(err, kErrBadLen);
+  }
+  // blocks that see nothing: found by a lane each, written by the warp
+  for (int u0 = (int(blockIdx.x) * kThreads + tid) & ~31; u0 < p.blocks; u0 += step) {
+    Block b;
+    if (u0 + lane < p.blocks) b = make_block(p, u0 + lane);
+    for (uint32_t left = __ballot_sync(0xffffffffu, b.rows > 0 && b.tiles == 0); left; left &= left - 1) {
+      const int from = __ffs(left) - 1;
+      const size_t row0 = size_t(__shfl_sync(0xffffffffu, b.q0, from)) * p.heads;
+      const int rows = __shfl_sync(0xffffffffu, b.rows, from) * p.heads;
+      uint4 *dst = reinterpret_cast<uint4 *>(p.out + row0 * kDvx);
+      for (int i = lane; i < rows * kDvx / 8; i += 32) dst[i] = make_uint4(0, 0, 0, 0);
+      for (int i = lane; i < rows; i += 32) p.lse[row0 + i] = -INFINITY;
+    }
+  }
+  schedule_heads(p, pair_id, &m.range, m.scratch);
+  tc_fence_before();
+  cluster_sync();  // both CTAs' barriers and TMEM are ready
+  tc_fence_after();
+  const uint32_t tmem = m.tmem_base;
+  const CtaRange r = m.range;
+
+  if (r.start < r.end) {
+    if (warp == 0) {
+      if (lane == 0) produce(p, r, m, sbase, rank, &tm_q, &tm_kn, &tm_kr, &tm_v, &tm_va, &tm_vr, err);
+    } else if (warp == 1) {
+      if (rank == 0) mmas(p, r, m, sbase, tmem, err);
+    } else if (warp >= 4) {
+      softmax(p, r, m, tmem, rank, pair_id, err);
+    }
+    // no MMA may still read this CTA's shared memory, and no copy write it: the MMAs
+    // waited for every copy unless a wait gave up
+    __syncthreads();
+    if (tid == 0) {
+      mbar_wait_drain(bar(m.drain), 0, kDrainNs);
+      if (m.abort) {  // let copies in flight land
+        const uint64_t t0 = globaltimer();
+        while (globaltimer() - t0 < 1000000ull) {
+        }
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();
+  if (warp == 1) {
+    __syncwarp();
+    tc_fence_after();
+    tmem_dealloc_pair(tmem, 512);
+  }
+  cluster_sync();  // the pair leaves together: neither SM takes another CTA before both gave up their TMEM
+}
+
+// ------------------------------------------------------------------ merge
+
+// The blocks that the schedule cut: pair c's record is that of the block it begins and
+// others go on with.  A warp a row: the LSE-weighted combine of its pieces, the first in
+// slot 1 of pair c, the others in slot 0 of the pairs after it.
+constexpr int kMergeWarps = 8;
+__global__ void __launch_bounds__(kMergeWarps * 32) expanded_merge_kernel(const __grid_constant__ ExpandedParams p) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int c = blockIdx.x, lane = threadIdx.x & 31;
+  const int row = blockIdx.y * kMergeWarps + (threadIdx.x >> 5);
+  const int4 rec = records(p)[c];
+  // (a call whose bounded wait gave up may leave anything here)
+  if (rec.x < 2 || rec.x > p.pairs - c || rec.z > kExpRows || row >= rec.z || rec.y < 0 ||
+      rec.y > p.q_tokens - rec.z || rec.w < 0 || rec.w >= p.heads)
+    return;
+  const int ns = rec.x;
+  auto slot = [&](int k) { return (size_t(2) * (c + k) + (k == 0 ? 1 : 0)) * kExpRows + row; };
+  const float *sl = slot_lse(p);
+  float mx = -INFINITY;
+  for (int k = lane; k < ns; k += 32) mx = fmaxf(mx, sl[slot(k)]);
+  for (int o = 16; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+  const float mref = mx == -INFINITY ? 0.f : mx;
+  float sum = 0.f;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+  for (int k = 0; k < ns; ++k) {
+    const float w = exp2f(sl[slot(k)] - mref);
+    const float4 x = reinterpret_cast<const float4 *>(slot_out(p) + slot(k) * kDvx)[lane];
+    sum += w;
+    acc.x += w * x.x;
+    acc.y += w * x.y;
+    acc.z += w * x.z;
+    acc.w += w * x.w;
+  }
+  const float inv = sum > 0.f ? 1.f / sum : 0.f;
+  const size_t orow = size_t(rec.y + row) * p.heads + rec.w;
+  reinterpret_cast<uint2 *>(p.out + orow * kDvx)[lane] =
+      make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
+  if (lane == 0) {
+    const float lse2 = sum == 0.f ? -INFINITY : mref + log2f(sum);
+    p.lse[orow] = p.lse_base2 ? lse2 : lse2 * kLn2;
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_prefill_expanded(const ExpandedParams &p, const ExpandedMaps &m, cudaStream_t stream) {
+  static SmemLimitOnce smem_limit;
+  cudaError_t e = smem_limit.ensure(prefill_expanded_kernel, kSmemBytes);
+  if (e != cudaSuccess) return e;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(2 * p.pairs);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = kSmemBytes;
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  e = cudaLaunchKernelEx(&cfg, prefill_expanded_kernel, p, m.q, m.k_nope, m.k_rope, m.v, m.va, m.vr);
+  if (e != cudaSuccess) return e;
+  cfg.gridDim = dim3(p.pairs, kExpRows / kMergeWarps);
+  cfg.blockDim = dim3(kMergeWarps * 32);
+  cfg.dynamicSmemBytes = 0;
+  return cudaLaunchKernelEx(&cfg, expanded_merge_kernel, p);
+}
+
+}  // namespace mla
