@@ -299,7 +299,6 @@ __device__ __forceinline__ void mmas(const ExpandedParams &p, const CtaRange &r,
       for (int h = 0; h < 2; ++h) {
         if (ok && j > 0 && j <= cnt[h]) {
           ok = warp_wait(bar(m.p_full[h]), p_lap[h], abort);
-          p_lap[h] ^= 1;
           tc_fence_after();
           if (ok && elect_one()) {
 #pragma unroll
@@ -309,6 +308,7 @@ __device__ __forceinline__ void mmas(const ExpandedParams &p, const CtaRange &r,
             if (j == cnt[h]) mma_commit_pair(bar(m.o_full[h]));
           }
           __syncwarp();
+          p_lap[h] ^= 1;
         }
         if (ok && j < cnt[h]) {
           if (j == 0) {
@@ -359,12 +359,9 @@ __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
       : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
   return r;
 }
-__device__ __forceinline__ float2 add2(float2 a, float2 b) {
-  float2 r;
-  asm("{ .reg .b64 x, y, d; mov.b64 x, {%2, %3}; mov.b64 y, {%4, %5};\n"
-      "add.rn.f32x2 d, x, y; mov.b64 {%0, %1}, d; }"
-      : "=f"(r.x), "=f"(r.y)
-      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
   return r;
 }
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
@@ -372,17 +369,10 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   return *reinterpret_cast<uint32_t *>(&v);
 }
 
-// O *= alpha (this thread's row).
-static __device__ __noinline__ void rescale_row(uint32_t taddr, float alpha) {
-  for (int c = 0; c < kDvx; c += 16) {
-    uint32_t o[16];
-    tmem_ld16(taddr + c, o);
-    tmem_wait_ld();
-#pragma unroll
-    for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
-    tmem_st16(taddr + c, o);
-  }
-  tmem_wait_st();
+__device__ __forceinline__ void st_global_v8(void *dst, const uint32_t *v) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(v[0]), "r"(v[1]), "r"(v[2]),
+               "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+               : "memory");
 }
 
 // A failed wait never leaves the loop: the warp goes on without working (later waits
@@ -397,14 +387,14 @@ __device__ __forceinline__ void softmax(const ExpandedParams &p, const CtaRange 
   const uint32_t t_s = tmem + lanes + kColS + 128 * h, t_o = tmem + lanes + kColO + 128 * h;
   const uint32_t p_full = map_to_rank(bar(m.p_full[h]), 0);
   const float cs = p.score_scale_log2;
+  const bool wide = (reinterpret_cast<uintptr_t>(p.out) & 31) == 0;  // rows may begin 16 bytes off
   uint32_t s_lap = 0, o_lap = 0;
   bool ok = true;
   for (Pieces w(p, r); w.next(); w.advance()) {
     const int cnt = w.b.count(h, w.t0, w.t1);
-    const int sees = row < w.b.rows ? w.b.sees(row) : 0;
-    float mrun = -INFINITY;
-    float2 sum = make_float2(0.f, 0.f);
-    for (int j = 0; j < cnt; ++j) {
+    int left = (row < w.b.rows ? w.b.sees(row) : 0) - int(w.t0) * kKeys;  // keys from the tile on that the row sees
+    float mrun = -INFINITY, sum[4] = {0.f, 0.f, 0.f, 0.f};
+    for (int j = 0; j < cnt; ++j, left -= kKeys) {
       ok = ok && __all_sync(0xffffffffu, mbar_wait_clk(bar(m.s_full[h]), s_lap, abort, kTimeoutClk));
       s_lap ^= 1;
       if (!ok) continue;
@@ -413,54 +403,62 @@ __device__ __forceinline__ void softmax(const ExpandedParams &p, const CtaRange 
 #pragma unroll
       for (int c = 0; c < 4; ++c) tmem_ld32(t_s + 32 * c, a[c]);
       tmem_wait_ld();
-      float x[kKeys];
-#pragma unroll
-      for (int i = 0; i < kKeys; ++i) x[i] = __uint_as_float(a[i >> 5][i & 31]);
-      const int left = sees - (int(w.t0) + j) * kKeys;
       if (left < kKeys) {
 #pragma unroll
-        for (int i = 0; i < kKeys; ++i) x[i] = i < left ? x[i] : -INFINITY;
+        for (int i = 0; i < kKeys; ++i) a[i >> 5][i & 31] = i < left ? a[i >> 5][i & 31] : 0xff800000u;
       }
-      float mx[4] = {x[0], x[1], x[2], x[3]};
+      auto x = [&](int i) { return __uint_as_float(a[i >> 5][i & 31]); };
+      float mx[8];
 #pragma unroll
-      for (int i = 4; i < kKeys; i += 8)
+      for (int k = 0; k < 8; ++k) mx[k] = fmaxf(x(k), x(8 + k));
 #pragma unroll
-        for (int k = 0; k < 4; ++k) mx[k] = fmaxf(fmaxf(mx[k], x[i + k]), i + 4 + k < kKeys ? x[i + 4 + k] : x[i + k]);
-      const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * cs;
+      for (int i = 16; i < kKeys; i += 16)
+#pragma unroll
+        for (int k = 0; k < 8; ++k) mx[k] = max3(mx[k], x(i + k), x(i + 8 + k));
+      const float top = max3(max3(mx[0], mx[1], mx[2]), max3(mx[3], mx[4], mx[5]), fmaxf(mx[6], mx[7])) * cs;
       float alpha = 1.f;
       if (j == 0) {
         mrun = top;
       } else if (top > mrun + kRescaleThreshold) {
         alpha = exp2f(mrun - top);
         mrun = top;
-        sum.x *= alpha;
-        sum.y *= alpha;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) sum[k] *= alpha;
+      }
+      if (__any_sync(0xffffffffu, alpha != 1.f)) {  // O *= alpha
+#pragma unroll 1
+        for (int c = 0; c < kDvx; c += 16) {
+          uint32_t o[16];
+          tmem_ld16(t_o + c, o);
+          tmem_wait_ld();
+#pragma unroll
+          for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
+          tmem_st16(t_o + c, o);
+        }
       }
       // a row that has seen no key yet keeps a -inf maximum: its weights are 0
       const float mref = mrun == -INFINITY ? 0.f : mrun;
       const float2 cs2 = make_float2(cs, cs), mn2 = make_float2(-mref, -mref);
-      if (__any_sync(0xffffffffu, alpha != 1.f)) rescale_row(t_o, alpha);
+      // (sums one by one: the packed addition made the loop half as slow again)
+      uint32_t pk[4][16];
 #pragma unroll
-      for (int c = 0; c < kKeys; c += 32) {
-        uint32_t pk[16];
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const float2 y = fma2(make_float2(x[c + 2 * i], x[c + 2 * i + 1]), cs2, mn2);
-          const float2 e = make_float2(exp2_approx(y.x), exp2_approx(y.y));
-          sum = add2(sum, e);
-          pk[i] = pack_bf16(e.x, e.y);
-        }
-        tmem_st16(t_s + c / 2, pk);
+      for (int i = 0; i < kKeys / 2; ++i) {
+        const float2 y = fma2(make_float2(x(2 * i), x(2 * i + 1)), cs2, mn2);
+        const float e0 = exp2_approx(y.x), e1 = exp2_approx(y.y);
+        sum[i & 1] += e0;
+        sum[2 + (i & 1)] += e1;
+        pk[i >> 4][i & 15] = pack_bf16(e0, e1);
       }
+#pragma unroll
+      for (int c = 0; c < 4; ++c) tmem_st16(t_s + 16 * c, pk[c]);
       tmem_wait_st();
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive_cluster(p_full);
     }
     // ---- the piece's rows: O / sum and the LSE
-    const float total = sum.x + sum.y;
+    const float total = (sum[0] + sum[1]) + (sum[2] + sum[3]);
     const float inv = total > 0.f ? 1.f / total : 0.f;
-    const float lse2 = mrun + log2f(total);
     const int c_first = sched_owner_short(w.pv, r.total, r.g_eff);
     const int pieces = sched_owner_short(w.pv + w.b.tiles - 1, r.total, r.g_eff) - c_first + 1;
     // a pair's slot 0: a block that another pair began; slot 1: one that it begins
@@ -484,26 +482,32 @@ __device__ __forceinline__ void softmax(const ExpandedParams &p, const CtaRange 
           for (int i = 0; i < 32; ++i) o[i] = 0;
         }
         if (!mine) continue;
+#pragma unroll
+        for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * inv);
         if (pieces > 1) {
-          float4 *dst = reinterpret_cast<float4 *>(slot_out(p) + slot * kDvx + c);
+          float *dst = slot_out(p) + slot * kDvx + c;
 #pragma unroll
-          for (int i = 0; i < 8; ++i)
-            dst[i] = make_float4(__uint_as_float(o[4 * i]) * inv, __uint_as_float(o[4 * i + 1]) * inv,
-                                 __uint_as_float(o[4 * i + 2]) * inv, __uint_as_float(o[4 * i + 3]) * inv);
+          for (int i = 0; i < 32; i += 8) st_global_v8(dst + i, &o[i]);
         } else {
-          uint4 *dst = reinterpret_cast<uint4 *>(p.out + orow * kDvx + c);
+          __nv_bfloat16 *dst = p.out + orow * kDvx + c;
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            uint32_t v[4];
+          for (int i = 0; i < 32; i += 16) {
+            uint32_t v[8];
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
-              v[k] = pack_bf16(__uint_as_float(o[8 * i + 2 * k]) * inv, __uint_as_float(o[8 * i + 2 * k + 1]) * inv);
-            dst[i] = make_uint4(v[0], v[1], v[2], v[3]);
+            for (int k = 0; k < 8; ++k)
+              v[k] = pack_bf16(__uint_as_float(o[i + 2 * k]), __uint_as_float(o[i + 2 * k + 1]));
+            if (wide) {
+              st_global_v8(dst + i, v);
+            } else {
+              reinterpret_cast<uint4 *>(dst + i)[0] = make_uint4(v[0], v[1], v[2], v[3]);
+              reinterpret_cast<uint4 *>(dst + i)[1] = make_uint4(v[4], v[5], v[6], v[7]);
+            }
           }
         }
       }
       tc_fence_before();
       if (mine) {
+        const float lse2 = mrun + log2f(total);
         if (pieces > 1) slot_lse(p)[slot] = lse2;
         else p.lse[orow] = p.lse_base2 ? lse2 : lse2 * kLn2;
       }
@@ -585,7 +589,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   cluster_sync();  // both CTAs' barriers and TMEM are ready
   tc_fence_after();
   const uint32_t tmem = m.tmem_base;
-  const CtaRange r = m.range;
+  const CtaRange &r = m.range;
 
   if (r.start < r.end) {
     if (warp == 0) {
