@@ -16,8 +16,8 @@
 // each).  The softmax weights of a half, bf16, overlay its scores and are operand A of
 // the second product straight from TMEM: nothing of them passes through shared memory.
 //
-// Roles (384 threads): warp 0 loads, warp 1 of the even CTA issues the MMAs, warps 4..7
-// and 8..11 the softmax of half 0 and 1, a thread a row (no exchange between threads).
+// Roles (384 threads): warp 0 loads, warp 1 of the even CTA issues the MMAs, warp 3 looks
+// the pieces of work up, warps 4..7 and 8..11 the softmax of half 0 and 1, a thread a row (no exchange between threads).
 // The halves take turns on the tensor cores: S0(j+1) follows P0(j) V(j) while the
 // softmax of half 1 works on S1(j), and the other way round.  As MMAs complete in order,
 // "S_h(j) is ready" also says that P_h(j-1) V(j-1) is done, so one barrier each way and
@@ -39,20 +39,35 @@ namespace {
 constexpr int kThreads = 384;
 constexpr int kHalf = 256;     // query tokens of a half
 constexpr int kKeys = 128;     // of a tile
-constexpr int kStages = 3;
+constexpr int kStages = 2;     // (three are no faster, and leave no room for the epilogue's rows)
 constexpr int kQHalfBytes = 3 * 128 * 128;   // [dim block of 64][128 tokens][128 B], swizzled
 constexpr int kKBytes = 3 * 64 * 128;        // [dim block of 64][64 keys][128 B]
 constexpr int kVBytes = 128 * 128;           // [128 keys][128 B]
 constexpr int kOffK = 2 * kQHalfBytes;
 constexpr int kOffV = kOffK + kStages * kKBytes;
-constexpr int kOffMisc = kOffV + kStages * kVBytes;
+constexpr int kStageRows = 32 * 128;         // a softmax warp's 32 rows of 128 bytes on their way out
+constexpr int kOffOut = kOffV + kStages * kVBytes;
+constexpr int kOffMisc = kOffOut + 8 * kStageRows;
+constexpr int kItems = 4;                    // pieces of work looked ahead
 constexpr uint32_t kColS = 0, kColO = 256;   // half h: + 128 h
 constexpr int kPieceTiles = 2;               // a piece's boundary (Q, first scores, epilogue) in tiles
 constexpr long long kTimeoutClk = 4000000000ll;  // about 2 s
 constexpr uint64_t kDrainNs = 200000000ull;
 constexpr float kRescaleThreshold = 8.f;     // base-2 units
 
+// A piece: tiles t0 .. t0 + n of a block of a head, of which half h takes the first
+// cnt[h]; row i of the block sees the first min(max(hi0 + i, 0), nk) keys.
+struct Item {
+  int n;             // 0: no more
+  int head, q0, rows, k0, t0, hi0, nk, end;
+  int cnt[2];
+  int pieces;        // of the block, this one among them
+  int first;         // this pair begins the block
+};
+
 struct Misc {
+  Item items[kItems];
+  uint64_t item_full[kItems], item_empty[kItems];
   uint64_t k_full[kStages], k_empty[kStages], v_full[kStages], v_empty[kStages];
   uint64_t q_full[2], q_empty[2], s_full[2], p_full[2], o_full[2], drain;
   uint32_t tmem_base;
@@ -122,35 +137,6 @@ __device__ __forceinline__ Block make_block(const ExpandedParams &p, int u) {
   return b;
 }
 
-// The pieces of this pair's range, in order: item v is block v % blocks of head v / blocks.
-struct Pieces {
-  const ExpandedParams &p;
-  const CtaRange &r;
-  long long v;
-  long long pv, t0, t1;
-  Block b;
-  __device__ __forceinline__ Pieces(const ExpandedParams &p_, const CtaRange &r_)
-      : p(p_), r(r_), v(r_.v_begin), pv(r_.p_begin) {}
-  __device__ __forceinline__ bool next() {
-    const long long items = (long long)p.blocks * p.heads;
-    while (v < items && pv < r.end) {
-      b = make_block(p, int(v % p.blocks));
-      if (b.tiles) {
-        t0 = max(r.start, pv) - pv;
-        t1 = min(r.end, pv + b.tiles) - pv;
-        if (t0 < t1) return true;
-      }
-      advance();
-    }
-    return false;
-  }
-  __device__ __forceinline__ void advance() {
-    pv += request_cost(b.tiles, kPieceTiles);
-    ++v;
-  }
-  __device__ __forceinline__ int head() const { return int(v / p.blocks); }
-};
-
 // This pair's range of the line of all heads' blocks, which is the line of one head
 // `heads` times over.  Block-wide.
 __device__ __forceinline__ void schedule_heads(const ExpandedParams &p, int idx, CtaRange *r, long long *scratch) {
@@ -206,6 +192,73 @@ __device__ __forceinline__ void schedule_heads(const ExpandedParams &p, int idx,
   __syncthreads();
 }
 
+// The pieces of this pair's range, in order, by one thread, a few ahead of the others:
+// worked out by every role for itself between two pieces, this cost the softmax and the
+// MMAs some 3,800 cycles a piece.
+__device__ __forceinline__ void look_ahead(const ExpandedParams &p, Misc &m, int pair_id) {
+  const CtaRange &r = m.range;
+  int head = r.v_begin / p.blocks, u = r.v_begin - head * p.blocks, slot = 0;
+  uint32_t lap = 1;
+  long long pv = r.p_begin;
+  auto publish = [&](const Item &it) {
+    if (!mbar_wait_clk(bar(m.item_empty[slot]), lap, &m.abort, kTimeoutClk)) return false;
+    m.items[slot] = it;
+    mbar_arrive(bar(m.item_full[slot]));
+    if (++slot == kItems) slot = 0, lap ^= 1;
+    return true;
+  };
+  Item it = {};
+  while (head < p.heads && pv < r.end) {
+    const Block b = make_block(p, u);
+    const long long t0 = max(r.start, pv) - pv, t1 = min(r.end, pv + b.tiles) - pv;
+    if (b.tiles && t0 < t1) {
+      const int c_first = sched_owner_short(pv, r.total, r.g_eff);
+      it.n = int(t1 - t0);
+      it.head = head;
+      it.q0 = b.q0;
+      it.rows = b.rows;
+      it.k0 = b.k0;
+      it.t0 = int(t0);
+      it.hi0 = b.hi0;
+      it.nk = b.nk;
+      it.end = b.end();
+      it.cnt[0] = b.count(0, t0, t1);
+      it.cnt[1] = b.count(1, t0, t1);
+      it.pieces = sched_owner_short(pv + b.tiles - 1, r.total, r.g_eff) - c_first + 1;
+      it.first = pair_id == c_first;
+      if (!publish(it)) return;
+    }
+    pv += request_cost(b.tiles, kPieceTiles);
+    if (++u == p.blocks) u = 0, ++head;
+  }
+  it.n = 0;
+  publish(it);
+}
+
+// A role's way through them.  One lane a warp waits and says it has read.
+struct Items {
+  Misc &m;
+  int slot = 0;
+  uint32_t lap = 0;
+  __device__ __forceinline__ explicit Items(Misc &m_) : m(m_) {}
+  // the next piece (n = 0: none, or a wait that gave up, then also !*ok); WARP: by a
+  // whole warp, else by one thread
+  template <bool WARP>
+  __device__ __forceinline__ Item next(bool *ok) {
+    bool got = mbar_wait_clk(bar(m.item_full[slot]), lap, &m.abort, kTimeoutClk);
+    if (WARP) got = __all_sync(0xffffffffu, got);
+    if (!got) {
+      *ok = false;
+      return Item{};
+    }
+    const Item it = m.items[slot];
+    if (WARP) __syncwarp();
+    if (!WARP || (threadIdx.x & 31) == 0) mbar_arrive(bar(m.item_empty[slot]));
+    if (++slot == kItems) slot = 0, lap ^= 1;
+    return it;
+  }
+};
+
 // ------------------------------------------------------------------ producer
 
 // The value rows of a tile of which only the first `left` (< 128) are seen: the others may
@@ -226,7 +279,7 @@ static __device__ __noinline__ void load_seen_v(uint32_t dst, uint32_t full, con
   }
 }
 
-__device__ __forceinline__ void produce(const ExpandedParams &p, const CtaRange &r, Misc &m, uint32_t sbase,
+__device__ __forceinline__ void produce(const ExpandedParams &p, Misc &m, uint32_t sbase,
                                         uint32_t rank, const CUtensorMap *tm_q, const CUtensorMap *tm_kn,
                                         const CUtensorMap *tm_kr, const CUtensorMap *tm_v, const CUtensorMap *tm_va,
                                         const CUtensorMap *tm_vr, int *err) {
@@ -237,10 +290,11 @@ __device__ __forceinline__ void produce(const ExpandedParams &p, const CtaRange 
   int st = 0;
   uint32_t lap = 1, q_lap[2] = {1, 1};  // parity of the empty barriers' last phase
   bool ok = true;
-  for (Pieces w(p, r); ok && w.next(); w.advance()) {
-    const int head = w.head(), end = w.b.end();
-    for (long long t = w.t0; ok && t < w.t1; ++t) {
-      const int key = w.b.k0 + int(t) * kKeys, left = end - int(t) * kKeys;
+  Items items(m);
+  for (Item w = items.next<false>(&ok); ok && w.n; w = items.next<false>(&ok)) {
+    const int head = w.head;
+    for (int j = 0; ok && j < w.n; ++j) {
+      const int key = w.k0 + (w.t0 + j) * kKeys, left = w.end - (w.t0 + j) * kKeys;
       ok = mbar_wait_clk(bar(m.k_empty[st]), lap, abort, kTimeoutClk);
       if (!ok) break;
       if (leader) mbar_arrive_expect_tx(bar(m.k_full[st]), 2 * kKBytes);
@@ -248,16 +302,16 @@ __device__ __forceinline__ void produce(const ExpandedParams &p, const CtaRange 
       tma_load_3d_pair(dk, tm_kn, k_full + 8 * st, 0, head, key + 64 * int(rank));
       tma_load_3d_pair(dk + 8192, tm_kn, k_full + 8 * st, 64, head, key + 64 * int(rank));
       tma_load_2d_pair(dk + 16384, tm_kr, k_full + 8 * st, 0, key + 64 * int(rank));
-      if (t == w.t0) {
+      if (j == 0) {
         for (int h = 0; ok && h < 2; ++h) {
-          if (w.b.count(h, w.t0, w.t1) == 0) continue;
+          if (w.cnt[h] == 0) continue;
           ok = mbar_wait_clk(bar(m.q_empty[h]), q_lap[h], abort, kTimeoutClk);
           if (!ok) break;
           q_lap[h] ^= 1;
           if (leader) mbar_arrive_expect_tx(bar(m.q_full[h]), 2 * kQHalfBytes);
           for (int i = 0; i < 3; ++i)
             tma_load_3d_pair(sbase + h * kQHalfBytes + i * 16384, tm_q, q_full + 8 * h, 64 * i, head,
-                             w.b.q0 + kHalf * h + 128 * int(rank));
+                             w.q0 + kHalf * h + 128 * int(rank));
         }
         if (!ok) break;
       }
@@ -280,8 +334,7 @@ __device__ __forceinline__ bool warp_wait(uint32_t b, uint32_t parity, volatile 
   return __all_sync(0xffffffffu, mbar_wait_clk(b, parity, abort, kTimeoutClk));
 }
 
-__device__ __forceinline__ void mmas(const ExpandedParams &p, const CtaRange &r, Misc &m, uint32_t sbase,
-                                     uint32_t tmem, int *err) {
+__device__ __forceinline__ void mmas(Misc &m, uint32_t sbase, uint32_t tmem, int *err) {
   volatile int *abort = &m.abort;
   const uint32_t idesc_s = idesc_bf16_f32(256, 128, false, false), idesc_o = idesc_bf16_f32(256, 128, false, true);
   const uint64_t dq = smem_desc_sw128(sbase, 16, 1024), dk = smem_desc_sw128(sbase + kOffK, 16, 1024);
@@ -289,9 +342,9 @@ __device__ __forceinline__ void mmas(const ExpandedParams &p, const CtaRange &r,
   int kst = 0, vst = 0;
   uint32_t k_lap = 0, v_lap = 0, q_lap[2] = {0, 0}, p_lap[2] = {0, 0};
   bool ok = true;
-  for (Pieces w(p, r); ok && w.next(); w.advance()) {
-    const int n = int(w.t1 - w.t0);
-    const int cnt[2] = {w.b.count(0, w.t0, w.t1), w.b.count(1, w.t0, w.t1)};
+  Items items(m);
+  for (Item w = items.next<true>(&ok); ok && w.n; w = items.next<true>(&ok)) {
+    const int n = w.n, cnt[2] = {w.cnt[0], w.cnt[1]};
     for (int j = 0; ok && j <= n; ++j) {
       if (j > 0) ok = warp_wait(bar(m.v_full[vst]), v_lap, abort);
       if (ok && j < n) ok = warp_wait(bar(m.k_full[kst]), k_lap, abort);
@@ -369,15 +422,28 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   return *reinterpret_cast<uint32_t *>(&v);
 }
 
-__device__ __forceinline__ void st_global_v8(void *dst, const uint32_t *v) {
-  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(v[0]), "r"(v[1]), "r"(v[2]),
-               "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
-               : "memory");
+// Sends a warp's 32 rows of 128 bytes, lane i's row in v, to dst + i * stride (rows below
+// `rows` only): through shared memory, so that a store instruction writes four whole rows
+// and not a piece of 32 (which took the epilogue 4,000 to 6,000 cycles).
+__device__ __forceinline__ void send_rows(unsigned char *stage, const uint32_t (&v)[32], void *dst, size_t stride,
+                                          int rows) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int c = 0; c < 8; ++c)
+    *reinterpret_cast<uint4 *>(stage + lane * 128 + ((c ^ (lane & 7)) << 4)) =
+        make_uint4(v[4 * c], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3]);
+  __syncwarp();
+  const int c = lane & 7;
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    const int i = 4 * k + (lane >> 3);
+    const uint4 x = *reinterpret_cast<const uint4 *>(stage + i * 128 + ((c ^ (i & 7)) << 4));
+    if (i < rows) *reinterpret_cast<uint4 *>(static_cast<unsigned char *>(dst) + i * stride + 16 * c) = x;
+  }
+  __syncwarp();
 }
 
-// A failed wait never leaves the loop: the warp goes on without working (later waits
-// fail at once).
-__device__ __forceinline__ void softmax(const ExpandedParams &p, const CtaRange &r, Misc &m, uint32_t tmem,
+__device__ __forceinline__ void softmax(const ExpandedParams &p, Misc &m, unsigned char *smem, uint32_t tmem,
                                         uint32_t rank, int pair_id, int *err) {
   volatile int *abort = &m.abort;
   const int warp = int(threadIdx.x >> 5) - 4, lane = threadIdx.x & 31;
@@ -387,17 +453,20 @@ __device__ __forceinline__ void softmax(const ExpandedParams &p, const CtaRange 
   const uint32_t t_s = tmem + lanes + kColS + 128 * h, t_o = tmem + lanes + kColO + 128 * h;
   const uint32_t p_full = map_to_rank(bar(m.p_full[h]), 0);
   const float cs = p.score_scale_log2;
-  const bool wide = (reinterpret_cast<uintptr_t>(p.out) & 31) == 0;  // rows may begin 16 bytes off
+  unsigned char *stage = smem + kOffOut + warp * kStageRows;
   uint32_t s_lap = 0, o_lap = 0;
   bool ok = true;
-  for (Pieces w(p, r); w.next(); w.advance()) {
-    const int cnt = w.b.count(h, w.t0, w.t1);
-    int left = (row < w.b.rows ? w.b.sees(row) : 0) - int(w.t0) * kKeys;  // keys from the tile on that the row sees
+  Items items(m);
+  Item w = items.next<true>(&ok);
+  while (ok && w.n) {
+    const int cnt = h ? w.cnt[1] : w.cnt[0];
+    // keys from the tile on that the row sees
+    int left = row < w.rows ? int(min(max((long long)w.hi0 + row, 0ll), (long long)w.nk)) - w.t0 * kKeys : 0;
     float mrun = -INFINITY, sum[4] = {0.f, 0.f, 0.f, 0.f};
     for (int j = 0; j < cnt; ++j, left -= kKeys) {
-      ok = ok && __all_sync(0xffffffffu, mbar_wait_clk(bar(m.s_full[h]), s_lap, abort, kTimeoutClk));
+      ok = __all_sync(0xffffffffu, mbar_wait_clk(bar(m.s_full[h]), s_lap, abort, kTimeoutClk));
       s_lap ^= 1;
-      if (!ok) continue;
+      if (!ok) break;
       tc_fence_after();
       uint32_t a[4][32];
 #pragma unroll
@@ -458,62 +527,57 @@ __device__ __forceinline__ void softmax(const ExpandedParams &p, const CtaRange 
     }
     // ---- the piece's rows: O / sum and the LSE
     const float total = (sum[0] + sum[1]) + (sum[2] + sum[3]);
+    // (before the piece's stores: an arrival waits for those that its thread has made)
+    const Item next = items.next<true>(&ok);
     const float inv = total > 0.f ? 1.f / total : 0.f;
-    const int c_first = sched_owner_short(w.pv, r.total, r.g_eff);
-    const int pieces = sched_owner_short(w.pv + w.b.tiles - 1, r.total, r.g_eff) - c_first + 1;
+    const float lse2 = mrun + log2f(total);
     // a pair's slot 0: a block that another pair began; slot 1: one that it begins
     const size_t slot = (2 * size_t(pair_id) + (w.t0 == 0 ? 1 : 0)) * kExpRows + row;
-    const size_t orow = size_t(w.b.q0 + row) * p.heads + w.head();
-    const bool mine = row < w.b.rows;
+    const size_t orow = size_t(w.q0 + row) * p.heads + w.head;
+    const bool cut = w.pieces > 1;
+    const int rows = w.rows - (row - lane);  // from this warp's first on
     if (cnt > 0) {
       ok = ok && __all_sync(0xffffffffu, mbar_wait_clk(bar(m.o_full[h]), o_lap, abort, kTimeoutClk));
       o_lap ^= 1;
     }
-    if (ok) {
-      tc_fence_after();
-#pragma unroll 1
-      for (int c = 0; c < kDvx; c += 32) {
-        uint32_t o[32];
-        if (cnt > 0) {
-          tmem_ld32(t_o + c, o);
-          tmem_wait_ld();
-        } else {
-#pragma unroll
-          for (int i = 0; i < 32; ++i) o[i] = 0;
-        }
-        if (!mine) continue;
-#pragma unroll
-        for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * inv);
-        if (pieces > 1) {
-          float *dst = slot_out(p) + slot * kDvx + c;
-#pragma unroll
-          for (int i = 0; i < 32; i += 8) st_global_v8(dst + i, &o[i]);
-        } else {
-          __nv_bfloat16 *dst = p.out + orow * kDvx + c;
-#pragma unroll
-          for (int i = 0; i < 32; i += 16) {
-            uint32_t v[8];
-#pragma unroll
-            for (int k = 0; k < 8; ++k)
-              v[k] = pack_bf16(__uint_as_float(o[i + 2 * k]), __uint_as_float(o[i + 2 * k + 1]));
-            if (wide) {
-              st_global_v8(dst + i, v);
-            } else {
-              reinterpret_cast<uint4 *>(dst + i)[0] = make_uint4(v[0], v[1], v[2], v[3]);
-              reinterpret_cast<uint4 *>(dst + i)[1] = make_uint4(v[4], v[5], v[6], v[7]);
-            }
-          }
-        }
-      }
-      tc_fence_before();
-      if (mine) {
-        const float lse2 = mrun + log2f(total);
-        if (pieces > 1) slot_lse(p)[slot] = lse2;
+    if (!ok) break;
+    tc_fence_after();
+    // (uniform: a warp without rows has only its place in the barriers)
+    if (rows > 0) {
+      if (lane < rows) {
+        if (cut) slot_lse(p)[slot] = lse2;
         else p.lse[orow] = p.lse_base2 ? lse2 : lse2 * kLn2;
       }
-      if (pieces > 1 && pair_id == c_first && rank == 0 && threadIdx.x == 128)
-        records(p)[pair_id] = make_int4(pieces, w.b.q0, w.b.rows, w.head());
+#pragma unroll 1
+      for (int c = 0; c < kDvx; c += 64) {
+        uint32_t o[2][32];
+        if (cnt > 0) {
+          tmem_ld32(t_o + c, o[0]);
+          tmem_ld32(t_o + c + 32, o[1]);
+          tmem_wait_ld();
+#pragma unroll
+          for (int i = 0; i < 64; ++i) o[i >> 5][i & 31] = __float_as_uint(__uint_as_float(o[i >> 5][i & 31]) * inv);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 64; ++i) o[i >> 5][i & 31] = 0;
+        }
+        if (cut) {
+          float *dst = slot_out(p) + (slot - lane) * kDvx + c;
+          send_rows(stage, o[0], dst, kDvx * 4, rows);
+          send_rows(stage, o[1], dst + 32, kDvx * 4, rows);
+        } else {
+          uint32_t v[32];
+#pragma unroll
+          for (int i = 0; i < 32; ++i)
+            v[i] = pack_bf16(__uint_as_float(o[i >> 4][2 * (i & 15)]), __uint_as_float(o[i >> 4][2 * (i & 15) + 1]));
+          send_rows(stage, v, p.out + (orow - size_t(lane) * p.heads) * kDvx + c, size_t(p.heads) * kDvx * 2, rows);
+        }
+      }
     }
+    tc_fence_before();
+    if (cut && w.first && rank == 0 && threadIdx.x == 128)
+      records(p)[pair_id] = make_int4(w.pieces, w.q0, w.rows, w.head);
+    w = next;
   }
   if (!ok) atomicOr(err, kErrTimeout);
 }
@@ -533,6 +597,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   int *err = error_word(p);
 
   if (tid == 0) {
+    for (int i = 0; i < kItems; ++i) {
+      mbar_init(bar(m.item_full[i]), 1);
+      mbar_init(bar(m.item_empty[i]), rank == 0 ? 10 : 9);  // loads, softmax warps; MMAs
+    }
     for (int s = 0; s < kStages; ++s) {
       mbar_init(bar(m.k_full[s]), 1);
       mbar_init(bar(m.k_empty[s]), 1);
@@ -593,11 +661,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 
   if (r.start < r.end) {
     if (warp == 0) {
-      if (lane == 0) produce(p, r, m, sbase, rank, &tm_q, &tm_kn, &tm_kr, &tm_v, &tm_va, &tm_vr, err);
+      if (lane == 0) produce(p, m, sbase, rank, &tm_q, &tm_kn, &tm_kr, &tm_v, &tm_va, &tm_vr, err);
     } else if (warp == 1) {
-      if (rank == 0) mmas(p, r, m, sbase, tmem, err);
+      if (rank == 0) mmas(m, sbase, tmem, err);
+    } else if (warp == 3) {
+      if (lane == 0) look_ahead(p, m, pair_id);
     } else if (warp >= 4) {
-      softmax(p, r, m, tmem, rank, pair_id, err);
+      softmax(p, m, smem_raw + pad, tmem, rank, pair_id, err);
     }
     // no MMA may still read this CTA's shared memory, and no copy write it: the MMAs
     // waited for every copy unless a wait gave up
