@@ -18,6 +18,9 @@
 //
 // Roles (384 threads): warp 0 loads, warp 1 of the even CTA issues the MMAs, warp 3 looks
 // the pieces of work up, warps 4..7 and 8..11 the softmax of half 0 and 1, a thread a row (no exchange between threads).
+// A block of up to 256 tokens fits one half.  Then both work on its rows, each on every
+// second tile, and join their outputs at its end; blocks of one tile go to the halves in
+// turn.  With one half only, the softmax and the products of a tile follow one another.
 // The halves take turns on the tensor cores: S0(j+1) follows P0(j) V(j) while the
 // softmax of half 1 works on S1(j), and the other way round.  As MMAs complete in order,
 // "S_h(j) is ready" also says that P_h(j-1) V(j-1) is done, so one barrier each way and
@@ -39,39 +42,44 @@ namespace {
 constexpr int kThreads = 384;
 constexpr int kHalf = 256;     // query tokens of a half
 constexpr int kKeys = 128;     // of a tile
-constexpr int kStages = 2;     // (three are no faster, and leave no room for the epilogue's rows)
+constexpr int kKStages = 2, kVStages = 2;  // (three of either are no faster, and leave no room for the epilogue's rows)
 constexpr int kQHalfBytes = 3 * 128 * 128;   // [dim block of 64][128 tokens][128 B], swizzled
 constexpr int kKBytes = 3 * 64 * 128;        // [dim block of 64][64 keys][128 B]
 constexpr int kVBytes = 128 * 128;           // [128 keys][128 B]
 constexpr int kOffK = 2 * kQHalfBytes;
-constexpr int kOffV = kOffK + kStages * kKBytes;
-constexpr int kStageRows = 32 * 128;         // a softmax warp's 32 rows of 128 bytes on their way out
-constexpr int kOffOut = kOffV + kStages * kVBytes;
+constexpr int kOffV = kOffK + kKStages * kKBytes;
+constexpr int kStageRows = 32 * 128;         // rows of a softmax warp on their way out
+constexpr int kOffOut = kOffV + kVStages * kVBytes;
 constexpr int kOffMisc = kOffOut + 8 * kStageRows;
 constexpr int kItems = 4;                    // pieces of work looked ahead
 constexpr uint32_t kColS = 0, kColO = 256;   // half h: + 128 h
-constexpr int kPieceTiles = 2;               // a piece's boundary (Q, first scores, epilogue) in tiles
+// Work is counted in tiles of one half.  A piece's boundary (Q, first scores, epilogue):
+constexpr int kPieceCost2 = 5;
 constexpr long long kTimeoutClk = 4000000000ll;  // about 2 s
 constexpr uint64_t kDrainNs = 200000000ull;
 constexpr float kRescaleThreshold = 8.f;     // base-2 units
 
 // A piece: tiles t0 .. t0 + n of a block of a head, of which half h takes the first
-// cnt[h]; row i of the block sees the first min(max(hi0 + i, 0), nk) keys.
+// cnt[h]; row i of the block sees the first min(max(hi0 + i, 0), nk) keys.  Split: half
+// `half`, whose place the queries take, has the tiles t0, t0 + 2, ..., the other one
+// those between; the halves go on taking turns from a piece to the next.
 struct Item {
   int n;             // 0: no more
   int head, q0, rows, k0, t0, hi0, nk, end;
   int cnt[2];
   int pieces;        // of the block, this one among them
   int first;         // this pair begins the block
+  int split, half;
 };
 
 struct Misc {
   Item items[kItems];
   uint64_t item_full[kItems], item_empty[kItems];
-  uint64_t k_full[kStages], k_empty[kStages], v_full[kStages], v_empty[kStages];
-  uint64_t q_full[2], q_empty[2], s_full[2], p_full[2], o_full[2], drain;
+  uint64_t k_full[kKStages], k_empty[kKStages], v_full[kVStages], v_empty[kVStages];
+  uint64_t q_full[2], q_empty[2], s_full[2], p_full[2], o_full[2], join[2], drain;  // join: the softmax warps
   uint32_t tmem_base;
   int abort;
+  float stats[2][2][128];  // split blocks: maximum and sum of each half's rows
   CtaRange range;
   long long scratch[kThreads / 32 + 1];
 };
@@ -108,10 +116,15 @@ struct Block {
     return int(min(max((long long)hi0 + row, 0ll), (long long)nk));
   }
   __device__ __forceinline__ int end() const { return sees(rows - 1); }
-  // tiles of half h within [t0, t1)
-  __device__ __forceinline__ int count(int h, long long t0, long long t1) const {
-    const long long n = h == 0 ? half0 : rows > kHalf ? tiles : 0;
-    return int(max(0ll, min(t1, n) - t0));
+  // one half holds all rows: the halves then share them and take turns at the tiles
+  __device__ __forceinline__ bool split() const { return rows <= kHalf; }
+  __device__ __forceinline__ int weight() const { return split() ? 1 : 2; }
+  __device__ __forceinline__ long long cost() const {
+    return tiles ? (long long)tiles * weight() + kPieceCost2 : 0;
+  }
+  // tiles of half h among t0 .. t1 - 1 (not split)
+  __device__ __forceinline__ int count(int h, int t0, int t1) const {
+    return max(0, min(t1, h ? tiles : half0) - t0);
   }
 };
 
@@ -142,14 +155,15 @@ __device__ __forceinline__ Block make_block(const ExpandedParams &p, int u) {
 __device__ __forceinline__ void schedule_heads(const ExpandedParams &p, int idx, CtaRange *r, long long *scratch) {
   const int tid = threadIdx.x, nw = kThreads / 32, lane = tid & 31, warp = tid >> 5;
   long long mine = 0;
-  for (int u = tid; u < p.blocks; u += kThreads) mine += request_cost(make_block(p, u).tiles, kPieceTiles);
+  for (int u = tid; u < p.blocks; u += kThreads) mine += make_block(p, u).cost();
   for (int o = 16; o; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
   if (lane == 0) scratch[warp] = mine;
   __syncthreads();
   long long one = 0;
   for (int w = 0; w < nw; ++w) one += scratch[w];
   const long long C = one * p.heads;
-  const int g = int(C < (long long)p.pairs ? C : (long long)p.pairs);
+  // (at least two units a pair: every pair inside a block has a whole tile's first unit)
+  const int g = int(C / 2 < (long long)p.pairs ? C / 2 : (long long)p.pairs);
   const bool has = idx < g;
   const long long start = has ? sched_start(idx, C, g) : 0, end = has ? sched_start(idx + 1, C, g) : 0;
   const long long h0 = has ? start / one : 0, r0 = start - h0 * one;
@@ -163,12 +177,11 @@ __device__ __forceinline__ void schedule_heads(const ExpandedParams &p, int idx,
   }
   __syncthreads();  // (scratch is read, the defaults are written)
   if (!has) return;
-  // the first block whose tiles end after r0; its predecessor's end at `excl - kPieceTiles`
+  // the first block whose tiles end after r0; its predecessor's end at `excl - kPieceCost2`
   long long base = 0;
   for (int u0 = 0; u0 < p.blocks && base <= r0; u0 += kThreads) {
     const int u = u0 + tid;
-    const int tiles = u < p.blocks ? make_block(p, u).tiles : 0;
-    const long long cst = request_cost(tiles, kPieceTiles);
+    const long long cst = u < p.blocks ? make_block(p, u).cost() : 0;
     long long incl = cst;
     for (int o = 1; o < 32; o <<= 1) {
       const long long y = __shfl_up_sync(0xffffffffu, incl, o);
@@ -183,7 +196,7 @@ __device__ __forceinline__ void schedule_heads(const ExpandedParams &p, int idx,
       chunk += scratch[w];
     }
     const long long excl = base + before + incl - cst;
-    if (tiles > 0 && excl + tiles > r0 && excl - kPieceTiles <= r0) {
+    if (cst > 0 && excl + cst - kPieceCost2 > r0 && excl - kPieceCost2 <= r0) {
       r->v_begin = int(h0 * p.blocks) + u;
       r->p_begin = h0 * one + excl;
     }
@@ -208,27 +221,34 @@ __device__ __forceinline__ void look_ahead(const ExpandedParams &p, Misc &m, int
     return true;
   };
   Item it = {};
+  int half = 0;  // whose turn it is
   while (head < p.heads && pv < r.end) {
     const Block b = make_block(p, u);
-    const long long t0 = max(r.start, pv) - pv, t1 = min(r.end, pv + b.tiles) - pv;
-    if (b.tiles && t0 < t1) {
+    // a tile belongs to the pair that has its first unit
+    const int wgt = b.weight();
+    const int t0 = int((max(r.start, pv) - pv + wgt - 1) / wgt);
+    const int t1 = int((min(r.end, pv + (long long)b.tiles * wgt) - pv + wgt - 1) / wgt);
+    if (t0 < t1) {
       const int c_first = sched_owner_short(pv, r.total, r.g_eff);
-      it.n = int(t1 - t0);
+      it.n = t1 - t0;
       it.head = head;
       it.q0 = b.q0;
       it.rows = b.rows;
       it.k0 = b.k0;
-      it.t0 = int(t0);
+      it.t0 = t0;
       it.hi0 = b.hi0;
       it.nk = b.nk;
       it.end = b.end();
-      it.cnt[0] = b.count(0, t0, t1);
-      it.cnt[1] = b.count(1, t0, t1);
-      it.pieces = sched_owner_short(pv + b.tiles - 1, r.total, r.g_eff) - c_first + 1;
+      it.split = b.split();
+      it.half = it.split ? half : 0;
+      half = it.split ? (half + it.n) & 1 : 0;
+      it.cnt[0] = it.split ? (it.n + 1 - it.half) / 2 : b.count(0, t0, t1);
+      it.cnt[1] = it.split ? it.n - it.cnt[0] : b.count(1, t0, t1);
+      it.pieces = sched_owner_short(pv + (long long)(b.tiles - 1) * wgt, r.total, r.g_eff) - c_first + 1;
       it.first = pair_id == c_first;
       if (!publish(it)) return;
     }
-    pv += request_cost(b.tiles, kPieceTiles);
+    pv += b.cost();
     if (++u == p.blocks) u = 0, ++head;
   }
   it.n = 0;
@@ -287,43 +307,58 @@ __device__ __forceinline__ void produce(const ExpandedParams &p, Misc &m, uint32
   const bool leader = rank == 0;
   const uint32_t k_full = map_to_rank(bar(m.k_full[0]), 0), v_full = map_to_rank(bar(m.v_full[0]), 0);
   const uint32_t q_full = map_to_rank(bar(m.q_full[0]), 0);
-  int st = 0;
-  uint32_t lap = 1, q_lap[2] = {1, 1};  // parity of the empty barriers' last phase
+  int kst = 0, vst = 0;
+  uint32_t k_lap = 1, v_lap = 1, q_lap[2] = {1, 1};  // parity of the empty barriers' last phase
   bool ok = true;
   Items items(m);
+  auto load_k = [&](const Item &w, int j) {
+    const int key = w.k0 + (w.t0 + j) * kKeys + 64 * int(rank);
+    if (!mbar_wait_clk(bar(m.k_empty[kst]), k_lap, abort, kTimeoutClk)) return false;
+    if (leader) mbar_arrive_expect_tx(bar(m.k_full[kst]), 2 * kKBytes);
+    const uint32_t dst = sbase + kOffK + kst * kKBytes;
+    tma_load_3d_pair(dst, tm_kn, k_full + 8 * kst, 0, w.head, key);
+    tma_load_3d_pair(dst + 8192, tm_kn, k_full + 8 * kst, 64, w.head, key);
+    tma_load_2d_pair(dst + 16384, tm_kr, k_full + 8 * kst, 0, key);
+    if (++kst == kKStages) kst = 0, k_lap ^= 1;
+    return true;
+  };
+  auto load_v = [&](int head, int key, int left) {
+    if (!mbar_wait_clk(bar(m.v_empty[vst]), v_lap, abort, kTimeoutClk)) return false;
+    if (leader) mbar_arrive_expect_tx(bar(m.v_full[vst]), 2 * kVBytes);
+    const uint32_t dst = sbase + kOffV + vst * kVBytes;
+    if (left >= kKeys) tma_load_3d_pair(dst, tm_v, v_full + 8 * vst, 64 * int(rank), head, key);
+    else load_seen_v(dst, v_full + 8 * vst, tm_va, tm_vr, 64 * int(rank), head, key, left, p.k_tokens);
+    if (++vst == kVStages) vst = 0, v_lap ^= 1;
+    return true;
+  };
+  auto load_q = [&](const Item &w, int h) {
+    if (!mbar_wait_clk(bar(m.q_empty[h]), q_lap[h], abort, kTimeoutClk)) return false;
+    q_lap[h] ^= 1;
+    if (leader) mbar_arrive_expect_tx(bar(m.q_full[h]), 2 * kQHalfBytes);
+    for (int i = 0; i < 3; ++i)
+      tma_load_3d_pair(sbase + h * kQHalfBytes + i * 16384, tm_q, q_full + 8 * h, 64 * i, w.head,
+                       w.q0 + (w.split ? 0 : kHalf * h) + 128 * int(rank));
+    return true;
+  };
+  // Keys run a tile ahead of values, which the products need later, from piece to piece
+  // too: (head, key, keys left) is the tile whose values are still to come.  The queries
+  // of a split piece have a place that the piece before leaves free; the others wait for
+  // that piece's last scores, and the values go first.
+  int v_head = 0, v_key = 0, v_left = 0;
   for (Item w = items.next<false>(&ok); ok && w.n; w = items.next<false>(&ok)) {
-    const int head = w.head;
     for (int j = 0; ok && j < w.n; ++j) {
-      const int key = w.k0 + (w.t0 + j) * kKeys, left = w.end - (w.t0 + j) * kKeys;
-      ok = mbar_wait_clk(bar(m.k_empty[st]), lap, abort, kTimeoutClk);
-      if (!ok) break;
-      if (leader) mbar_arrive_expect_tx(bar(m.k_full[st]), 2 * kKBytes);
-      const uint32_t dk = sbase + kOffK + st * kKBytes;
-      tma_load_3d_pair(dk, tm_kn, k_full + 8 * st, 0, head, key + 64 * int(rank));
-      tma_load_3d_pair(dk + 8192, tm_kn, k_full + 8 * st, 64, head, key + 64 * int(rank));
-      tma_load_2d_pair(dk + 16384, tm_kr, k_full + 8 * st, 0, key + 64 * int(rank));
-      if (j == 0) {
-        for (int h = 0; ok && h < 2; ++h) {
-          if (w.cnt[h] == 0) continue;
-          ok = mbar_wait_clk(bar(m.q_empty[h]), q_lap[h], abort, kTimeoutClk);
-          if (!ok) break;
-          q_lap[h] ^= 1;
-          if (leader) mbar_arrive_expect_tx(bar(m.q_full[h]), 2 * kQHalfBytes);
-          for (int i = 0; i < 3; ++i)
-            tma_load_3d_pair(sbase + h * kQHalfBytes + i * 16384, tm_q, q_full + 8 * h, 64 * i, head,
-                             w.q0 + kHalf * h + 128 * int(rank));
-        }
-        if (!ok) break;
-      }
-      ok = mbar_wait_clk(bar(m.v_empty[st]), lap, abort, kTimeoutClk);
-      if (!ok) break;
-      if (leader) mbar_arrive_expect_tx(bar(m.v_full[st]), 2 * kVBytes);
-      const uint32_t dv = sbase + kOffV + st * kVBytes;
-      if (left >= kKeys) tma_load_3d_pair(dv, tm_v, v_full + 8 * st, 64 * int(rank), head, key);
-      else load_seen_v(dv, v_full + 8 * st, tm_va, tm_vr, 64 * int(rank), head, key, left, p.k_tokens);
-      if (++st == kStages) st = 0, lap ^= 1;
+      ok = load_k(w, j);
+      if (ok && j == 0 && w.split) ok = load_q(w, w.half);
+      if (ok && v_left > 0) ok = load_v(v_head, v_key, v_left);
+      if (j == 0 && !w.split)
+        for (int h = 0; ok && h < 2; ++h)
+          if (w.cnt[h]) ok = load_q(w, h);
+      v_head = w.head;
+      v_key = w.k0 + (w.t0 + j) * kKeys;
+      v_left = w.end - (w.t0 + j) * kKeys;
     }
   }
+  if (ok && v_left > 0) ok = load_v(v_head, v_key, v_left);
   if (!ok) atomicOr(err, kErrTimeout);
 }
 
@@ -340,56 +375,98 @@ __device__ __forceinline__ void mmas(Misc &m, uint32_t sbase, uint32_t tmem, int
   const uint64_t dq = smem_desc_sw128(sbase, 16, 1024), dk = smem_desc_sw128(sbase + kOffK, 16, 1024);
   const uint64_t dv = smem_desc_sw128(sbase + kOffV, 16384, 1024);  // MN-major: 8-key groups 1 KB apart
   int kst = 0, vst = 0;
-  uint32_t k_lap = 0, v_lap = 0, q_lap[2] = {0, 0}, p_lap[2] = {0, 0};
+  uint32_t k_lap = 0, v_lap = 0, q_lap = 0, p_lap = 0;  // q, p: bit h
   bool ok = true;
+  // half h's weights times the values of the tile at vst
+  auto values = [&](int h, bool begin, bool end) {
+    if (!warp_wait(bar(m.v_full[vst]), v_lap, abort) || !warp_wait(bar(m.p_full[h]), (p_lap >> h) & 1, abort))
+      return false;
+    p_lap ^= 1u << h;
+    tc_fence_after();
+    if (elect_one()) {
+      const uint32_t o = tmem + kColO + 128 * h, a = tmem + kColS + 128 * h;
+      const uint64_t v = dv + ((vst * kVBytes) >> 4);
+#pragma unroll
+      for (int ks = 0; ks < 8; ++ks) mma_bf16_ts_pair(o, a + 8 * ks, v + ((ks * 2048) >> 4), idesc_o, !begin || ks > 0);
+      if (end) mma_commit_pair(bar(m.o_full[h]));
+    }
+    __syncwarp();
+    return true;
+  };
+  // half h's scores of the tile at kst, of the queries in place qh
+  auto scores = [&](int h, int qh, bool begin, bool end) {
+    if (begin) {
+      if (!warp_wait(bar(m.q_full[qh]), (q_lap >> qh) & 1, abort)) return false;
+      q_lap ^= 1u << qh;
+    }
+    if (elect_one()) {
+      const uint64_t q = dq + ((qh * kQHalfBytes) >> 4), k = dk + ((kst * kKBytes) >> 4);
+#pragma unroll
+      for (int ks = 0; ks < 12; ++ks)
+        mma_bf16_ss_pair(tmem + kColS + 128 * h, q + (((ks >> 2) * 16384 + (ks & 3) * 32) >> 4),
+                         k + (((ks >> 2) * 8192 + (ks & 3) * 32) >> 4), idesc_s, ks > 0);
+      mma_commit_pair(bar(m.s_full[h]));
+      if (end) mma_commit_pair(bar(m.q_empty[qh]));
+    }
+    __syncwarp();
+    return true;
+  };
+  auto done_values = [&] {
+    if (elect_one()) mma_commit_pair(bar(m.v_empty[vst]));
+    __syncwarp();
+    if (++vst == kVStages) vst = 0, v_lap ^= 1;
+  };
+  auto done_scores = [&] {
+    if (elect_one()) mma_commit_pair(bar(m.k_empty[kst]));
+    __syncwarp();
+    if (++kst == kKStages) kst = 0, k_lap ^= 1;
+  };
+  // Split tiles whose weights are still to come: bit h, and whether they begin or end
+  // their half's part of a piece.  They are multiplied in the tiles' order, `next` first.
+  uint32_t owed = 0, begins = 0, ends = 0;
+  int next = 0;
+  auto settle = [&](int h) {
+    if (!values(h, (begins >> h) & 1, (ends >> h) & 1)) return false;
+    done_values();
+    owed &= ~(1u << h);
+    next = h ^ 1;
+    return true;
+  };
   Items items(m);
   for (Item w = items.next<true>(&ok); ok && w.n; w = items.next<true>(&ok)) {
-    const int n = w.n, cnt[2] = {w.cnt[0], w.cnt[1]};
+    const int n = w.n;
+    if (w.split) {
+      for (int j = 0; ok && j < n; ++j) {
+        const int h = w.half ^ (j & 1);
+        if (!owed) next = h;
+        if ((owed >> h) & 1) ok = settle(h);
+        ok = ok && warp_wait(bar(m.k_full[kst]), k_lap, abort) && scores(h, w.half, j == 0, j == n - 1);
+        if (!ok) break;
+        done_scores();
+        owed |= 1u << h;
+        begins = (begins & ~(1u << h)) | uint32_t(j < 2) << h;
+        ends = (ends & ~(1u << h)) | uint32_t(j >= n - 2) << h;
+      }
+      continue;
+    }
+    while (ok && owed) ok = settle(next);
+    // step j: the weights of tile j - 1 times its values, then tile j's scores, half by half
     for (int j = 0; ok && j <= n; ++j) {
-      if (j > 0) ok = warp_wait(bar(m.v_full[vst]), v_lap, abort);
-      if (ok && j < n) ok = warp_wait(bar(m.k_full[kst]), k_lap, abort);
+      if (j < n) ok = warp_wait(bar(m.k_full[kst]), k_lap, abort);
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        if (ok && j > 0 && j <= cnt[h]) {
-          ok = warp_wait(bar(m.p_full[h]), p_lap[h], abort);
-          tc_fence_after();
-          if (ok && elect_one()) {
-#pragma unroll
-            for (int ks = 0; ks < 8; ++ks)
-              mma_bf16_ts_pair(tmem + kColO + 128 * h, tmem + kColS + 128 * h + 8 * ks,
-                               dv + ((vst * kVBytes + ks * 2048) >> 4), idesc_o, j > 1 || ks > 0);
-            if (j == cnt[h]) mma_commit_pair(bar(m.o_full[h]));
-          }
-          __syncwarp();
-          p_lap[h] ^= 1;
+        if (ok && j > 0 && j <= w.cnt[h]) {
+          // (both halves wait for the same values)
+          ok = values(h, j == 1, j == w.cnt[h]);
         }
-        if (ok && j < cnt[h]) {
-          if (j == 0) {
-            ok = warp_wait(bar(m.q_full[h]), q_lap[h], abort);
-            q_lap[h] ^= 1;
-          }
-          if (ok && elect_one()) {
-#pragma unroll
-            for (int ks = 0; ks < 12; ++ks)
-              mma_bf16_ss_pair(tmem + kColS + 128 * h,
-                               dq + ((h * kQHalfBytes + (ks >> 2) * 16384 + (ks & 3) * 32) >> 4),
-                               dk + ((kst * kKBytes + (ks >> 2) * 8192 + (ks & 3) * 32) >> 4), idesc_s, ks > 0);
-            mma_commit_pair(bar(m.s_full[h]));
-            if (j == cnt[h] - 1) mma_commit_pair(bar(m.q_empty[h]));
-          }
-          __syncwarp();
-        }
+        if (ok && j < w.cnt[h]) ok = scores(h, h, j == 0, j == w.cnt[h] - 1);
       }
       if (!ok) break;
-      if (elect_one()) {
-        if (j > 0) mma_commit_pair(bar(m.v_empty[vst]));
-        if (j < n) mma_commit_pair(bar(m.k_empty[kst]));
-      }
-      __syncwarp();
-      if (j > 0 && ++vst == kStages) vst = 0, v_lap ^= 1;
-      if (j < n && ++kst == kStages) kst = 0, k_lap ^= 1;
+      if (j > 0) done_values();
+      if (j < n) done_scores();
     }
   }
+  while (ok && owed) ok = settle(next);
   if (elect_one()) {
     if (!ok) atomicOr(err, kErrTimeout);
     mma_commit_pair(bar(m.drain));
@@ -428,12 +505,12 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
 __device__ __forceinline__ void send_rows(unsigned char *stage, const uint32_t (&v)[32], void *dst, size_t stride,
                                           int rows) {
   const int lane = threadIdx.x & 31;
-#pragma unroll
-  for (int c = 0; c < 8; ++c)
-    *reinterpret_cast<uint4 *>(stage + lane * 128 + ((c ^ (lane & 7)) << 4)) =
-        make_uint4(v[4 * c], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3]);
-  __syncwarp();
   const int c = lane & 7;
+#pragma unroll
+  for (int k = 0; k < 8; ++k)
+    *reinterpret_cast<uint4 *>(stage + lane * 128 + ((k ^ c) << 4)) =
+        make_uint4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
+  __syncwarp();
 #pragma unroll
   for (int k = 0; k < 8; ++k) {
     const int i = 4 * k + (lane >> 3);
@@ -448,22 +525,31 @@ __device__ __forceinline__ void softmax(const ExpandedParams &p, Misc &m, unsign
   volatile int *abort = &m.abort;
   const int warp = int(threadIdx.x >> 5) - 4, lane = threadIdx.x & 31;
   const int h = warp >> 2, q = warp & 3;
-  const int row = kHalf * h + 128 * int(rank) + 32 * q + lane;  // within the block
+  const int hrow = 32 * q + lane;
   const uint32_t lanes = uint32_t(32 * q) << 16;
-  const uint32_t t_s = tmem + lanes + kColS + 128 * h, t_o = tmem + lanes + kColO + 128 * h;
+  const uint32_t t_s = tmem + lanes + kColS + 128 * h, t_o = tmem + lanes + kColO + 128 * h,
+                 t_o2 = tmem + lanes + kColO + 128 * (h ^ 1);
   const uint32_t p_full = map_to_rank(bar(m.p_full[h]), 0);
   const float cs = p.score_scale_log2;
   unsigned char *stage = smem + kOffOut + warp * kStageRows;
-  uint32_t s_lap = 0, o_lap = 0;
+  uint32_t s_lap = 0, o_lap = 0, join_lap = 0;
+  // (no hardware barrier: a warp whose wait gave up would leave the others in it)
+  auto join = [&](int k) {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bar(m.join[k]));
+    return bool(__all_sync(0xffffffffu, mbar_wait_clk(bar(m.join[k]), join_lap, abort, kTimeoutClk)));
+  };
   bool ok = true;
   Items items(m);
   Item w = items.next<true>(&ok);
   while (ok && w.n) {
     const int cnt = h ? w.cnt[1] : w.cnt[0];
+    const int row = (w.split ? 0 : kHalf * h) + 128 * int(rank) + hrow;  // within the block
     // keys from the tile on that the row sees
-    int left = row < w.rows ? int(min(max((long long)w.hi0 + row, 0ll), (long long)w.nk)) - w.t0 * kKeys : 0;
+    int left = (row < w.rows ? int(min(max((long long)w.hi0 + row, 0ll), (long long)w.nk)) : 0) -
+               (w.t0 + (w.split ? h ^ w.half : 0)) * kKeys;
     float mrun = -INFINITY, sum[4] = {0.f, 0.f, 0.f, 0.f};
-    for (int j = 0; j < cnt; ++j, left -= kKeys) {
+    for (int j = 0; j < cnt; ++j, left -= w.split ? 2 * kKeys : kKeys) {
       ok = __all_sync(0xffffffffu, mbar_wait_clk(bar(m.s_full[h]), s_lap, abort, kTimeoutClk));
       s_lap ^= 1;
       if (!ok) break;
@@ -526,40 +612,71 @@ __device__ __forceinline__ void softmax(const ExpandedParams &p, Misc &m, unsign
       if (lane == 0) mbar_arrive_cluster(p_full);
     }
     // ---- the piece's rows: O / sum and the LSE
-    const float total = (sum[0] + sum[1]) + (sum[2] + sum[3]);
+    float total = (sum[0] + sum[1]) + (sum[2] + sum[3]);
     // (before the piece's stores: an arrival waits for those that its thread has made)
     const Item next = items.next<true>(&ok);
+    if (w.split && cnt == 0) {  // the other half has the piece's only tile
+      w = next;
+      continue;
+    }
+    const bool joined = w.split && w.n > 1;
+    if (cnt > 0) {
+      ok = ok && __all_sync(0xffffffffu, mbar_wait_clk(bar(m.o_full[h]), o_lap, abort, kTimeoutClk));
+      o_lap ^= 1;
+    }
+    float mine = 1.f, other = 0.f;  // weights of the halves' outputs
+    if (joined) {  // the two halves' pieces of a row: this thread's, and that of the other half's thread
+      m.stats[h][0][hrow] = mrun;
+      m.stats[h][1][hrow] = total;
+      tc_fence_before();
+      ok = ok && join(0);  // both outputs are ready
+      const float m2 = m.stats[h ^ 1][0][hrow], top = fmaxf(mrun, m2), mref = top == -INFINITY ? 0.f : top;
+      mine = exp2f(mrun - mref);
+      other = exp2f(m2 - mref);
+      total = mine * total + other * m.stats[h ^ 1][1][hrow];
+      mrun = top;
+    }
+    if (!ok) break;
     const float inv = total > 0.f ? 1.f / total : 0.f;
     const float lse2 = mrun + log2f(total);
+    mine *= inv;
+    other *= inv;
     // a pair's slot 0: a block that another pair began; slot 1: one that it begins
     const size_t slot = (2 * size_t(pair_id) + (w.t0 == 0 ? 1 : 0)) * kExpRows + row;
     const size_t orow = size_t(w.q0 + row) * p.heads + w.head;
     const bool cut = w.pieces > 1;
     const int rows = w.rows - (row - lane);  // from this warp's first on
-    if (cnt > 0) {
-      ok = ok && __all_sync(0xffffffffu, mbar_wait_clk(bar(m.o_full[h]), o_lap, abort, kTimeoutClk));
-      o_lap ^= 1;
-    }
-    if (!ok) break;
     tc_fence_after();
     // (uniform: a warp without rows has only its place in the barriers)
     if (rows > 0) {
-      if (lane < rows) {
+      if (lane < rows && !(joined && h)) {
         if (cut) slot_lse(p)[slot] = lse2;
         else p.lse[orow] = p.lse_base2 ? lse2 : lse2 * kLn2;
       }
+      // joined: half h writes dims 64 h .. 64 h + 63
+      const int c_end = joined ? 64 * h + 64 : kDvx;
 #pragma unroll 1
-      for (int c = 0; c < kDvx; c += 64) {
+      for (int c = joined ? 64 * h : 0; c < c_end; c += 64) {
         uint32_t o[2][32];
-        if (cnt > 0) {
-          tmem_ld32(t_o + c, o[0]);
-          tmem_ld32(t_o + c + 32, o[1]);
-          tmem_wait_ld();
 #pragma unroll
-          for (int i = 0; i < 64; ++i) o[i >> 5][i & 31] = __float_as_uint(__uint_as_float(o[i >> 5][i & 31]) * inv);
-        } else {
+        for (int k = 0; k < 2; ++k) {
+          if (cnt > 0) {
+            tmem_ld32(t_o + c + 32 * k, o[k]);
+            tmem_wait_ld();
 #pragma unroll
-          for (int i = 0; i < 64; ++i) o[i >> 5][i & 31] = 0;
+            for (int i = 0; i < 32; ++i) o[k][i] = __float_as_uint(__uint_as_float(o[k][i]) * mine);
+          } else {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) o[k][i] = 0;
+          }
+          if (joined) {
+            uint32_t z[32];
+            tmem_ld32(t_o2 + c + 32 * k, z);
+            tmem_wait_ld();
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              o[k][i] = __float_as_uint(fmaf(__uint_as_float(z[i]), other, __uint_as_float(o[k][i])));
+          }
         }
         if (cut) {
           float *dst = slot_out(p) + (slot - lane) * kDvx + c;
@@ -575,7 +692,11 @@ __device__ __forceinline__ void softmax(const ExpandedParams &p, Misc &m, unsign
       }
     }
     tc_fence_before();
-    if (cut && w.first && rank == 0 && threadIdx.x == 128)
+    if (joined) {  // both outputs and their statistics are read
+      ok = join(1);
+      join_lap ^= 1;
+    }
+    if (cut && w.first && rank == 0 && (threadIdx.x & 127) == 0 && h == (joined ? 0 : w.half))
       records(p)[pair_id] = make_int4(w.pieces, w.q0, w.rows, w.head);
     w = next;
   }
@@ -601,9 +722,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       mbar_init(bar(m.item_full[i]), 1);
       mbar_init(bar(m.item_empty[i]), rank == 0 ? 10 : 9);  // loads, softmax warps; MMAs
     }
-    for (int s = 0; s < kStages; ++s) {
+    for (int s = 0; s < kKStages; ++s) {
       mbar_init(bar(m.k_full[s]), 1);
       mbar_init(bar(m.k_empty[s]), 1);
+    }
+    for (int s = 0; s < kVStages; ++s) {
       mbar_init(bar(m.v_full[s]), 1);
       mbar_init(bar(m.v_empty[s]), 1);
     }
@@ -613,6 +736,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       mbar_init(bar(m.s_full[h]), 1);
       mbar_init(bar(m.p_full[h]), 8);  // a half's four warps in each CTA
       mbar_init(bar(m.o_full[h]), 1);
+      mbar_init(bar(m.join[h]), 8);
     }
     mbar_init(bar(m.drain), 1);
     m.abort = 0;
@@ -633,7 +757,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     tma_prefetch_desc(&tm_v);
   }
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  if (rank == 0 && tid == 128) records(p)[pair_id] = make_int4(0, 0, 0, 0);  // (the thread that sets it)
+  if (rank == 0 && tid == 128) records(p)[pair_id] = make_int4(0, 0, 0, 0);  // (ordered before the one that may follow by the barriers below)
   const int step = int(gridDim.x) * kThreads;
   for (int b = int(blockIdx.x) * kThreads + tid; b < p.batch; b += step) {
     const int q0 = p.q_starts[b], q1 = p.q_starts[b + 1], k0 = p.k_starts[b], k1 = p.k_starts[b + 1];
