@@ -165,3 +165,20 @@ def test_pages_past_four_gib():
     out = torch.empty_like(rows)
     mla.kv_read(kv, table, ints([0, 100]), ints([20]), out)
     assert torch.equal(out, rows)
+
+
+@pytest.mark.parametrize("scale", [0.037, 5.5 / 448.0, 1.0, 2.0**-7, 3.0, 1.0 / 3.0, 1e-32, 1e32, 448.0, 0.011718751, 2.0**-30, 2.0**30,
+                                   2.0 - 2.0**-23, 1.0 + 2.0**-23, 2.0**-31, 0.1, 7e-9, 0.7071068, 1.9999995e-3])
+def test_every_bf16_value_is_quantised_as_the_division_says(scale):
+    """All 65,536 bf16 values, over scales inside and outside the range that the
+    quotient is worked out in without a division."""
+    bits = torch.arange(65536, dtype=torch.int32).to(torch.int16)
+    rows = torch.zeros(114 * 576, dtype=torch.int16)
+    rows[:65536] = bits
+    rows = rows.view(torch.bfloat16).view(114, 576).cuda()
+    kv = torch.zeros(2, 64, 576, dtype=torch.uint8, device="cuda")
+    table, starts, pos = ints([[1, 0]]), ints([0, 114]), ints([3])
+    s32 = torch.tensor(scale, dtype=torch.float32).double()
+    want = expected(rows, kv, table, starts, pos, s32)
+    mla.kv_append_chunk(rows, kv, table, starts, pos, kv_scale=scale)
+    assert same(kv.cpu(), want)
