@@ -179,7 +179,7 @@ __device__ __forceinline__ void schedule_heads(const ExpandedParams &p, int idx,
   if (!has) return;
   // the first block whose tiles end after r0; its predecessor's end at `excl - kPieceCost2`
   long long base = 0;
-  for (int u0 = 0; u0 < p.blocks && base <= r0; u0 += kThreads) {
+  for (int u0 = 0; u0 < p.blocks && base - kPieceCost2 <= r0; u0 += kThreads) {
     const int u = u0 + tid;
     const long long cst = u < p.blocks ? make_block(p, u).cost() : 0;
     long long incl = cst;
@@ -205,31 +205,45 @@ __device__ __forceinline__ void schedule_heads(const ExpandedParams &p, int idx,
   __syncthreads();
 }
 
-// The pieces of this pair's range, in order, by one thread, a few ahead of the others:
-// worked out by every role for itself between two pieces, this cost the softmax and the
-// MMAs some 3,800 cycles a piece.
+// The pieces of this pair's range, in order, by one warp, a few ahead of the others: worked
+// out by every role for itself between two pieces, this cost the softmax and the MMAs some
+// 3,800 cycles a piece.  A lane holds a block, so that a batch padded with empty requests
+// is passed 32 at a time.
 __device__ __forceinline__ void look_ahead(const ExpandedParams &p, Misc &m, int pair_id) {
+  constexpr uint32_t kAll = 0xffffffffu;
   const CtaRange &r = m.range;
-  int head = r.v_begin / p.blocks, u = r.v_begin - head * p.blocks, slot = 0;
+  const int lane = threadIdx.x & 31;
+  const long long start = r.start, end = r.end;
+  int head = r.v_begin / p.blocks, u0 = (r.v_begin - head * p.blocks) & ~31, held = -1, slot = 0;
   uint32_t lap = 1;
-  long long pv = r.p_begin;
-  auto publish = [&](const Item &it) {
-    if (!mbar_wait_clk(bar(m.item_empty[slot]), lap, &m.abort, kTimeoutClk)) return false;
-    m.items[slot] = it;
-    mbar_arrive(bar(m.item_full[slot]));
-    if (++slot == kItems) slot = 0, lap ^= 1;
-    return true;
-  };
-  Item it = {};
+  bool ok = true;
   int half = 0;  // whose turn it is
-  while (head < p.heads && pv < r.end) {
-    const Block b = make_block(p, u);
+  Block b;
+  long long pv = 0;   // cost before block u0 of this head
+  bool first = true;
+  while (ok && head < p.heads) {
+    if (held != u0) b = u0 + lane < p.blocks ? make_block(p, u0 + lane) : Block();
+    held = u0;
+    long long incl = b.cost();
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long y = __shfl_up_sync(kAll, incl, o);
+      if (lane >= o) incl += y;
+    }
+    if (first) {  // p_begin is the cost before block v_begin, some lane of this group
+      const int from = (r.v_begin - head * p.blocks) & 31;
+      pv = r.p_begin - __shfl_sync(kAll, incl - b.cost(), from);
+      first = false;
+    }
+    if (pv >= end) break;
+    const long long at = pv + incl - b.cost();  // of this lane's block
     // a tile belongs to the pair that has its first unit
     const int wgt = b.weight();
-    const int t0 = int((max(r.start, pv) - pv + wgt - 1) / wgt);
-    const int t1 = int((min(r.end, pv + (long long)b.tiles * wgt) - pv + wgt - 1) / wgt);
-    if (t0 < t1) {
-      const int c_first = sched_owner_short(pv, r.total, r.g_eff);
+    const int t0 = int((max(start, at) - at + wgt - 1) / wgt);
+    const int t1 = int((min(end, at + (long long)b.tiles * wgt) - at + wgt - 1) / wgt);
+    const bool mine = b.tiles > 0 && at < end && t0 < t1;
+    Item it;
+    if (mine) {
+      const int c_first = sched_owner_short(at, r.total, r.g_eff);
       it.n = t1 - t0;
       it.head = head;
       it.q0 = b.q0;
@@ -239,20 +253,35 @@ __device__ __forceinline__ void look_ahead(const ExpandedParams &p, Misc &m, int
       it.hi0 = b.hi0;
       it.nk = b.nk;
       it.end = b.end();
-      it.split = b.split();
-      it.half = it.split ? half : 0;
-      half = it.split ? (half + it.n) & 1 : 0;
-      it.cnt[0] = it.split ? (it.n + 1 - it.half) / 2 : b.count(0, t0, t1);
-      it.cnt[1] = it.split ? it.n - it.cnt[0] : b.count(1, t0, t1);
-      it.pieces = sched_owner_short(pv + (long long)(b.tiles - 1) * wgt, r.total, r.g_eff) - c_first + 1;
+      it.pieces = sched_owner_short(at + (long long)(b.tiles - 1) * wgt, r.total, r.g_eff) - c_first + 1;
       it.first = pair_id == c_first;
-      if (!publish(it)) return;
+      it.split = b.split();
     }
-    pv += b.cost();
-    if (++u == p.blocks) u = 0, ++head;
+    for (uint32_t left = __ballot_sync(kAll, mine); ok && left; left &= left - 1) {
+      const int from = __ffs(left) - 1;
+      ok = __all_sync(kAll, mbar_wait_clk(bar(m.item_empty[slot]), lap, &m.abort, kTimeoutClk));
+      const int split = __shfl_sync(kAll, int(b.split()), from), n = __shfl_sync(kAll, t1 - t0, from);
+      if (ok && lane == from) {
+        it.half = split ? half : 0;
+        it.cnt[0] = split ? (n + 1 - half) / 2 : b.count(0, t0, t1);
+        it.cnt[1] = split ? n - it.cnt[0] : b.count(1, t0, t1);
+        m.items[slot] = it;
+        mbar_arrive(bar(m.item_full[slot]));
+      }
+      __syncwarp();
+      half = split ? (half + n) & 1 : 0;
+      if (++slot == kItems) slot = 0, lap ^= 1;
+    }
+    pv += __shfl_sync(kAll, incl, 31);
+    u0 += 32;
+    if (u0 >= p.blocks) u0 = 0, ++head;
   }
-  it.n = 0;
-  publish(it);
+  ok = ok && __all_sync(kAll, mbar_wait_clk(bar(m.item_empty[slot]), lap, &m.abort, kTimeoutClk));
+  if (ok && lane == 0) {
+    m.items[slot].n = 0;
+    mbar_arrive(bar(m.item_full[slot]));
+  }
+  __syncwarp();
 }
 
 // A role's way through them.  One lane a warp waits and says it has read.
@@ -789,7 +818,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     } else if (warp == 1) {
       if (rank == 0) mmas(m, sbase, tmem, err);
     } else if (warp == 3) {
-      if (lane == 0) look_ahead(p, m, pair_id);
+      look_ahead(p, m, pair_id);
     } else if (warp >= 4) {
       softmax(p, m, smem_raw + pad, tmem, rank, pair_id, err);
     }
