@@ -409,26 +409,31 @@ template <int R>
 __device__ __forceinline__ int chunk_base(const DecodeParams &p, int b) {
   return int((long long)chunk_start(p, b) * p.q_heads / R) + b;
 }
-// Block v of R rows of a chunked batch.  (Starts that fall are cut to none or to rows of
+// Block v of R rows of a chunked batch, of request lo.  (Starts that fall are cut to none or to rows of
 // other requests, never to rows outside Q.)
 template <int R>
-__device__ __forceinline__ ViewReq chunk_block(const DecodeParams &p, int v) {
+__device__ __forceinline__ ViewReq chunk_block_of(const DecodeParams &p, int v, int lo) {
   ViewReq r;
+  r.req = lo;
+  const int s0 = chunk_start(p, lo), n = chunk_start(p, lo + 1) - s0;
+  const long long k = v - chunk_base<R>(p, lo), rows = (long long)n * p.q_heads;
+  if (k < 0 || R * k >= rows) return r;
+  r.row0 = int((long long)s0 * p.q_heads + R * k);
+  r.rows = int(min((long long)R, rows - R * k));
+  r.end = max(0, checked_len(p, lo, nullptr) - n + (int(R * k) + r.rows - 1) / p.q_heads + 1);
+  r.tiles = (r.end + kPage - 1) / kPage;
+  return r;
+}
+
+template <int R>
+__device__ __forceinline__ ViewReq chunk_block(const DecodeParams &p, int v) {
   int lo = 0, hi = p.batch - 1;  // the last request whose blocks start at or before v
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
     if (chunk_base<R>(p, mid) <= v) lo = mid;
     else hi = mid - 1;
   }
-  const int s0 = chunk_start(p, lo), n = chunk_start(p, lo + 1) - s0;
-  const long long k = v - chunk_base<R>(p, lo), rows = (long long)n * p.q_heads;
-  if (k < 0 || R * k >= rows) return r;
-  r.req = lo;
-  r.row0 = int((long long)s0 * p.q_heads + R * k);
-  r.rows = int(min((long long)R, rows - R * k));
-  r.end = max(0, checked_len(p, lo, nullptr) - n + (int(R * k) + r.rows - 1) / p.q_heads + 1);
-  r.tiles = (r.end + kPage - 1) / kPage;
-  return r;
+  return chunk_block_of<R>(p, v, lo);
 }
 
 // What the roles of a CTA start from: the first piece's view, and the groups' table or

@@ -126,6 +126,13 @@ __device__ __forceinline__ ViewReq block_view(const DecodeParams &p, int v, cons
   if constexpr (KIND == kWhole) return make_view<KIND>(p, v, groups);
   else return view_call<KIND>(p, v, groups);
 }
+// The view of block v of a chunked batch, for a role that has come to block v from an
+// earlier one, of request `from`: ids grow with the requests, so that the next one or two
+// are looked at, where a search takes a dozen loads one after the other.
+static __device__ __noinline__ ViewReq chunk_call(const DecodeParams &p, int v, int from) {
+  while (from + 1 < p.batch && chunk_base<kPairRows>(p, from + 1) <= v) ++from;
+  return chunk_block_of<kPairRows>(p, v, from);
+}
 __device__ __forceinline__ int tiles_of(const ViewReq &view) { return (view.tiles + kTilePages - 1) / kTilePages; }
 
 // The pieces of this pair's range, in order.
@@ -141,7 +148,8 @@ struct Pieces {
       : p(p_), r(r_), v(r_.v_begin), pv(r_.p_begin), m(m_) {}
   __device__ bool next() {
     while (v < p.pair_blocks && pv < r.end) {
-      view = block_view<KIND>(p, v, m.groups);
+      if constexpr (KIND == kChunk) view = v == r.v_begin ? block_view<KIND>(p, v, m.groups) : chunk_call(p, v, view.req);
+      else view = block_view<KIND>(p, v, m.groups);
       tiles = tiles_of(view);
       if (tiles == 0) { ++v; continue; }
       t0 = max(r.start, pv) - pv;
@@ -590,6 +598,30 @@ __device__ __forceinline__ bool split_q(const DecodeParams &p, Misc &m, unsigned
   return true;
 }
 
+// Sends a warp's 32 rows of 128 bytes, lane i's row in v, to dst + i * stride (rows below
+// `rows` only) through the warp's own part of P, which is free at a piece's end: a store
+// instruction then writes four whole rows.  (A lane's row 16 bytes at a time: a block of
+// one tile 17 us instead of 11.)
+template <bool F8>
+__device__ __forceinline__ void send_rows(unsigned char *own, const uint32_t (&v)[32], void *dst, size_t stride,
+                                          int rows) {
+  const int lane = threadIdx.x & 31, c = lane & 7;
+  // e4m3: 16 rows in the place of each term
+  auto place = [&](int i) { return own + (F8 ? (i >> 4) * kPTerm + (i & 15) * 128 : i * 128); };
+#pragma unroll
+  for (int k = 0; k < 8; ++k)
+    *reinterpret_cast<uint4 *>(place(lane) + ((k ^ c) << 4)) =
+        make_uint4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
+  __syncwarp();
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    const int i = 4 * k + (lane >> 3);
+    const uint4 x = *reinterpret_cast<const uint4 *>(place(i) + ((c ^ (i & 7)) << 4));
+    if (i < rows) *reinterpret_cast<uint4 *>(static_cast<unsigned char *>(dst) + i * stride + 16 * c) = x;
+  }
+  __syncwarp();
+}
+
 // A failed wait never leaves the loop: the warp goes on without working, so
 // that the others find it at their barriers (later waits fail at once).
 template <bool F8, int KIND>
@@ -612,7 +644,8 @@ __device__ __forceinline__ void softmax(const DecodeParams &p, const CtaRange &r
   uint32_t n = 0;
   uint32_t o_it = 0;
   bool ok = true;
-  for (Pieces<F8, KIND> w(p, r, m); w.next(); w.advance(), ++o_it) {
+  Pieces<F8, KIND> w(p, r, m);
+  for (bool more = w.next(); more; ++o_it) {
     const int grow = w.view.row0 + int(rank) * kRows + row;
     RowView rv;
     if constexpr (KIND == kChunk) rv = chunk_row_view(p, w.view, min(grow, w.view.row0 + w.view.rows - 1));
@@ -741,20 +774,55 @@ __device__ __forceinline__ void softmax(const DecodeParams &p, const CtaRange &r
     const float sumx = (m.red[1][0][row] + m.red[1][1][row]) + (m.red[1][2][row] + m.red[1][3][row]);
     named_sync(1, kSoftThreads);  // read before the next piece writes maxima
     const float inv = sum > 0.f ? p.kv_scale / sum : 0.f;
+    // chunks: the next piece is looked up while the products of this one end
+    const ViewReq view = w.view;
+    const long long pv = w.pv;
+    const int v = w.v, tiles = w.tiles;
+    if constexpr (KIND == kChunk) {
+      w.advance();
+      more = w.next();
+    }
     ok = ok && __all_sync(0xffffffffu, mbar_wait_clk(bar(m.o_full), o_it & 1, abort, kTimeoutClk));
-    const int c_first = sched_owner_short(w.pv, r.total, r.g_eff);
-    const int pieces = sched_owner_short(w.pv + w.tiles - 1, r.total, r.g_eff) - c_first + 1;
+    const int c_first = sched_owner_short(pv, r.total, r.g_eff);
+    const int pieces = sched_owner_short(pv + tiles - 1, r.total, r.g_eff) - c_first + 1;
     const bool split = !writes_rows(KIND) || pieces > 1;
     // shared pages and tails: every piece leaves a partial, in the slots of its
     // pair and block; a window's and a chunk's do when the block is cut, in the slots
     // of the split merge, its CTA r * pairs + c standing for half r of pair c
-    const size_t slot = writes_rows(KIND) ? 2 * size_t(rank * p.pairs + pair_id) + (w.v != r.v_begin ? 1 : 0)
-                                        : 2 * size_t(pair_id + w.v) + rank;
+    const size_t slot = writes_rows(KIND) ? 2 * size_t(rank * p.pairs + pair_id) + (v != r.v_begin ? 1 : 0)
+                                        : 2 * size_t(pair_id + v) + rank;
     if (ok) {
       tc_fence_after();
       const int d0 = 256 * (q >> 1) + 128 * g;
       float *dst = slot_out_ptr(p) + (slot * kSlotHeads + row) * kDv + d0;
       __nv_bfloat16 *out = p.out + size_t(grow) * kDv + d0;
+      if constexpr (KIND == kChunk) {
+        unsigned char *own = smem + Cfg<F8>::kOffP + pb * kRows * 128 + 32 * (q & 1) * (F8 ? 64 : 128);
+        const int rows = view.rows - (int(rank) * kRows + row - lane);  // from this warp's first on
+#pragma unroll 1
+        for (int c = 0; c < 128; c += 64) {
+          uint32_t o[2][32];
+          tmem_ld32(t_o + c, o[0]);
+          tmem_ld32(t_o + c + 32, o[1]);
+          tmem_wait_ld();
+          if (rows <= 0) continue;
+#pragma unroll
+          for (int i = 0; i < 64; ++i) o[i >> 5][i & 31] = __float_as_uint(__uint_as_float(o[i >> 5][i & 31]) * inv);
+          if (split) {
+            send_rows<F8>(own, o[0], dst - lane * kDv + c, kDv * 4, rows);
+            send_rows<F8>(own, o[1], dst - lane * kDv + c + 32, kDv * 4, rows);
+          } else {
+            uint32_t v[32];
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+              __nv_bfloat162 x2 = __floats2bfloat162_rn(__uint_as_float(o[i >> 4][2 * (i & 15)]),
+                                                        __uint_as_float(o[i >> 4][2 * (i & 15) + 1]));
+              v[i] = *reinterpret_cast<uint32_t *>(&x2);
+            }
+            send_rows<F8>(own, v, out - lane * kDv + c, kDv * 2, rows);
+          }
+        }
+      } else
 #pragma unroll 1
       for (int c = 0; c < 128; c += 32) {
         uint32_t o[32];
@@ -791,15 +859,19 @@ __device__ __forceinline__ void softmax(const DecodeParams &p, const CtaRange &r
       if (st == 0 && pair_id == c_first) {
         if (KIND == kChunk) {  // a pair begins at most one block that others go on with: the pair's record
           if (rank == 0 && pieces > 1)
-            info_ptr(p)[pair_id] = make_int4(pieces, w.view.row0, w.view.rows, w.v != r.v_begin ? 1 : 0);
+            info_ptr(p)[pair_id] = make_int4(pieces, view.row0, view.rows, v != r.v_begin ? 1 : 0);
         } else if (KIND == kWindow) {  // the record of this half's 64 rows
-          if (w.view.rows > int(rank) * kRows)
-            info_ptr(p)[(2 * (w.v / p.batch) + int(rank)) * p.batch + w.v % p.batch] =
+          if (view.rows > int(rank) * kRows)
+            info_ptr(p)[(2 * (v / p.batch) + int(rank)) * p.batch + v % p.batch] =
                 make_int4(int(rank) * p.pairs + c_first, pieces, int(slot), 0);
         } else if (rank == 0) {
-          pair_info_ptr(p)[w.v] = make_int4(c_first, pieces, pair_id + w.v, 0);
+          pair_info_ptr(p)[v] = make_int4(c_first, pieces, pair_id + v, 0);
         }
       }
+    }
+    if constexpr (KIND != kChunk) {
+      w.advance();
+      more = w.next();
     }
   }
   if (!ok) atomicOr(err, kErrTimeout);
@@ -875,6 +947,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   }
   if constexpr (KIND == kChunk) {
     if (rank == 0 && tid == 128) info_ptr(p)[pair_id] = make_int4(0, 0, 0, 0);  // (the thread that sets it)
+    // the searches below read these again and again
+    for (int i = 32 * tid; i <= min(p.batch, 2048); i += 32 * kThreads) {
+      asm volatile("prefetch.global.L1 [%0];" ::"l"(p.chunk_starts + i));
+      if (i < p.batch) asm volatile("prefetch.global.L1 [%0];" ::"l"(p.seq_lens + i));
+    }
     const int step = int(gridDim.x) * kThreads;
     for (int b = int(blockIdx.x) * kThreads + tid; b < p.batch; b += step) {
       checked_len(p, b, err);
