@@ -16,6 +16,12 @@
  *                      sglang pull 33926, implementation steps 3 (FP8 KV path)
  *                      and 4 (under DCP the fused KV write is off and the
  *                      pool's own write stores the rank's rows).
+ *  mla_kv_append_chunk, mla_kv_read
+ *                      the same for a ragged batch of many new tokens, and back.
+ *  mla_prefill_chunk   attention of a ragged chunk of new tokens over the cache.
+ *  mla_prefill_expanded
+ *                      attention of many query tokens over the keys and values
+ *                      of each head, as the latent's up-projection gives them.
  *  mla_decode_dcp      all P partitions in one call (one decode launch for P <= 8)
  *                      and their merge: the DCP ranks emulated on one GPU.
  *  mla_lse_combine     the LSE-weighted softmax merge of P partial results.
