@@ -409,8 +409,8 @@ template <int R>
 __device__ __forceinline__ int chunk_base(const DecodeParams &p, int b) {
   return int((long long)chunk_start(p, b) * p.q_heads / R) + b;
 }
-// Block v of R rows of a chunked batch, of request lo.  (Starts that fall are cut to none or to rows of
-// other requests, never to rows outside Q.)
+// Block v of R rows of a chunked batch, of request lo.  (Starts that fall are cut to none
+// or to rows of other requests, never to rows outside Q.)
 template <int R>
 __device__ __forceinline__ ViewReq chunk_block_of(const DecodeParams &p, int v, int lo) {
   ViewReq r;
@@ -425,15 +425,20 @@ __device__ __forceinline__ ViewReq chunk_block_of(const DecodeParams &p, int v, 
   return r;
 }
 
+// The last request whose blocks start at or before block v, and the block.
 template <int R>
-__device__ __forceinline__ ViewReq chunk_block(const DecodeParams &p, int v) {
-  int lo = 0, hi = p.batch - 1;  // the last request whose blocks start at or before v
+__device__ __forceinline__ int chunk_request(const DecodeParams &p, int v) {
+  int lo = 0, hi = p.batch - 1;
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
     if (chunk_base<R>(p, mid) <= v) lo = mid;
     else hi = mid - 1;
   }
-  return chunk_block_of<R>(p, v, lo);
+  return lo;
+}
+template <int R>
+__device__ __forceinline__ ViewReq chunk_block(const DecodeParams &p, int v) {
+  return chunk_block_of<R>(p, v, chunk_request<R>(p, v));
 }
 
 // What the roles of a CTA start from: the first piece's view, and the groups' table or
