@@ -775,10 +775,20 @@ def _stride(t, dim, least):
 
 
 def _expanded_desc(q, k_nope, k_rope, v, batch, causal):
-    key = (q.shape, q.stride(), k_nope.shape, k_nope.stride(), k_rope.shape, k_rope.stride(), v.shape, v.stride(),
+    """Checks the four tensors, once per set of layouts, and returns the
+    call's descriptor (by reference)."""
+    if not all(isinstance(t, torch.Tensor) for t in (q, k_nope, k_rope, v)):
+        raise TypeError("q, k_nope, k_rope and v must be tensors")
+    key = (q.shape, q.stride(), q.dtype, q.device, k_nope.shape, k_nope.stride(), k_nope.dtype, k_nope.device,
+           k_rope.shape, k_rope.stride(), k_rope.dtype, k_rope.device, v.shape, v.stride(), v.dtype, v.device,
            batch, causal)
     d = _EXPANDED_DESCS.get(key)
     if d is None:
+        for t, name in ((q, "q"), (k_nope, "k_nope"), (k_rope, "k_rope"), (v, "v")):
+            if t.dtype != torch.bfloat16:
+                raise TypeError(f"{name} must be a bf16 tensor")
+            if t.device != q.device:
+                raise ValueError(f"{name} is on {t.device}, expected {q.device}")
         if q.dim() != 3 or q.shape[2] != 192:
             raise ValueError("q must be [N, H, 192]")
         n, heads, _ = q.shape
@@ -812,11 +822,6 @@ def prefill_expanded(q, k_nope, k_rope, v, q_starts, k_starts, causal: bool, sm_
     dev = q.device
     if dev.type != "cuda":
         raise ValueError("prefill_expanded runs on CUDA tensors only")
-    for t, name in ((q, "q"), (k_nope, "k_nope"), (k_rope, "k_rope"), (v, "v")):
-        if not isinstance(t, torch.Tensor) or t.dtype != torch.bfloat16:
-            raise TypeError(f"{name} must be a bf16 tensor")
-        if t.device != dev:
-            raise ValueError(f"{name} is on {t.device}, expected {dev}")
     _ints(q_starts, "q_starts", dev, 1)
     _ints(k_starts, "k_starts", dev, 1)
     B = q_starts.numel() - 1

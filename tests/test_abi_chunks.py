@@ -138,6 +138,10 @@ def test_descriptor_checks():
     for case in bad:
         with pytest.raises(ValueError):
             mla._expanded_desc(*case, 1, True)
+    for i in range(4):
+        for other in (ok[i].float(), None, ok[i].tolist()):
+            with pytest.raises(TypeError):
+                mla._expanded_desc(*ok[:i], other, *ok[i + 1:], 1, True)
     for case in ((kv[..., :512], t), (kv[0], t), (kv, one), (kv, t.expand(3, 2))):
         with pytest.raises(ValueError):
             mla._cache_desc(1, 16, *case, 1.0)
