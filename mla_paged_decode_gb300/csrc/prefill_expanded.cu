@@ -76,7 +76,7 @@ struct Misc {
   Item items[kItems];
   uint64_t item_full[kItems], item_empty[kItems];
   uint64_t k_full[kKStages], k_empty[kKStages], v_full[kVStages], v_empty[kVStages];
-  uint64_t q_full[2], q_empty[2], s_full[2], p_full[2], o_full[2], join[2], drain;  // join: the softmax warps
+  uint64_t q_full[2], q_empty[2], s_full[2], p_full[2][2], o_full[2], join[2], drain;  // p_full: [half][64 keys]; join: the softmax warps
   uint32_t tmem_base;
   int abort;
   float stats[2][2][128];  // split blocks: maximum and sum of each half's rows
@@ -406,20 +406,26 @@ __device__ __forceinline__ void mmas(Misc &m, uint32_t sbase, uint32_t tmem, int
   int kst = 0, vst = 0;
   uint32_t k_lap = 0, v_lap = 0, q_lap = 0, p_lap = 0;  // q, p: bit h
   bool ok = true;
-  // half h's weights times the values of the tile at vst
+  // half h's weights times the values of the tile at vst; the first 64 keys' product runs
+  // while the softmax works on the others' weights (five requests of 215..667 queries: 190
+  // -> 179 us)
   auto values = [&](int h, bool begin, bool end) {
-    if (!warp_wait(bar(m.v_full[vst]), v_lap, abort) || !warp_wait(bar(m.p_full[h]), (p_lap >> h) & 1, abort))
-      return false;
-    p_lap ^= 1u << h;
-    tc_fence_after();
-    if (elect_one()) {
-      const uint32_t o = tmem + kColO + 128 * h, a = tmem + kColS + 128 * h;
-      const uint64_t v = dv + ((vst * kVBytes) >> 4);
+    if (!warp_wait(bar(m.v_full[vst]), v_lap, abort)) return false;
+    const uint32_t o = tmem + kColO + 128 * h, a = tmem + kColS + 128 * h;
+    const uint64_t v = dv + ((vst * kVBytes) >> 4);
 #pragma unroll
-      for (int ks = 0; ks < 8; ++ks) mma_bf16_ts_pair(o, a + 8 * ks, v + ((ks * 2048) >> 4), idesc_o, !begin || ks > 0);
-      if (end) mma_commit_pair(bar(m.o_full[h]));
+    for (int part = 0; part < 2; ++part) {
+      if (!warp_wait(bar(m.p_full[h][part]), (p_lap >> h) & 1, abort)) return false;
+      tc_fence_after();
+      if (elect_one()) {
+#pragma unroll
+        for (int ks = 4 * part; ks < 4 * part + 4; ++ks)
+          mma_bf16_ts_pair(o, a + 8 * ks, v + ((ks * 2048) >> 4), idesc_o, !begin || ks > 0);
+        if (part && end) mma_commit_pair(bar(m.o_full[h]));
+      }
+      __syncwarp();
     }
-    __syncwarp();
+    p_lap ^= 1u << h;
     return true;
   };
   // half h's scores of the tile at kst, of the queries in place qh
@@ -558,7 +564,7 @@ __device__ __forceinline__ void softmax(const ExpandedParams &p, Misc &m, unsign
   const uint32_t lanes = uint32_t(32 * q) << 16;
   const uint32_t t_s = tmem + lanes + kColS + 128 * h, t_o = tmem + lanes + kColO + 128 * h,
                  t_o2 = tmem + lanes + kColO + 128 * (h ^ 1);
-  const uint32_t p_full = map_to_rank(bar(m.p_full[h]), 0);
+  const uint32_t p_full = map_to_rank(bar(m.p_full[h][0]), 0);
   const float cs = p.score_scale_log2;
   unsigned char *stage = smem + kOffOut + warp * kStageRows;
   uint32_t s_lap = 0, o_lap = 0, join_lap = 0;
@@ -632,13 +638,23 @@ __device__ __forceinline__ void softmax(const ExpandedParams &p, Misc &m, unsign
         sum[i & 1] += e0;
         sum[2 + (i & 1)] += e1;
         pk[i >> 4][i & 15] = pack_bf16(e0, e1);
+        if (i == 31) {  // 64 keys' weights are on their way, and said to be there 16 keys later
+#pragma unroll
+          for (int c = 0; c < 2; ++c) tmem_st16(t_s + 16 * c, pk[c]);
+        }
+        if (i == 39) {
+          tmem_wait_st();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_cluster(p_full);
+        }
       }
 #pragma unroll
-      for (int c = 0; c < 4; ++c) tmem_st16(t_s + 16 * c, pk[c]);
+      for (int c = 2; c < 4; ++c) tmem_st16(t_s + 16 * c, pk[c]);
       tmem_wait_st();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive_cluster(p_full);
+      if (lane == 0) mbar_arrive_cluster(p_full + 8);
     }
     // ---- the piece's rows: O / sum and the LSE
     float total = (sum[0] + sum[1]) + (sum[2] + sum[3]);
@@ -763,7 +779,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       mbar_init(bar(m.q_full[h]), 1);
       mbar_init(bar(m.q_empty[h]), 1);
       mbar_init(bar(m.s_full[h]), 1);
-      mbar_init(bar(m.p_full[h]), 8);  // a half's four warps in each CTA
+      for (int part = 0; part < 2; ++part) mbar_init(bar(m.p_full[h][part]), 8);  // a half's four warps in each CTA
       mbar_init(bar(m.o_full[h]), 1);
       mbar_init(bar(m.join[h]), 8);
     }
