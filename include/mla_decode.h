@@ -315,11 +315,14 @@ int mla_kv_append(const void *kv_new, void *kv_pages, const int32_t *block_table
  *  num_rows    rows of the buffer (0 is a no-op).
  *  row_stride  values from one row of the buffer to the next: a multiple of 8,
  *              at least 576, so that rows may lie inside wider ones.
- *  *_starts    int32 [batch + 1], none below its predecessor.
+ *  *_starts    int32 [batch + 1], none below its predecessor, the first at least 0
+ *              and the last at most num_rows.
  *  positions   int32 [batch].
  *  d, error_word
  *              as for mla_kv_append: a row without a page is skipped
- *              (mla_kv_read writes zeros) and bit 0 is OR-ed in.
+ *              (mla_kv_read writes zeros) and bit 0 is OR-ed in.  Bit 1 says that
+ *              starts fall or leave the buffer; then rows may be skipped, and
+ *              no row outside the buffer is touched.
  *
  * mla_kv_append_chunk writes rows into the cache: the row kv_append would
  * write for each (bits, or e4m3 of fp32(x) / kv_scale, to nearest even,

@@ -691,7 +691,9 @@ def kv_append_chunk(kv_new, kv_pages, block_table, chunk_starts, positions, part
     [B + 1]) of kv_new bf16 [N, 576] become request b's tokens positions[b]
     (int32 [B]; negative skips the request), positions[b] + 1, ... in kv_pages
     (bf16, or e4m3 quantised with kv_scale), where partition part_id of
-    num_parts owns them.  Rows of kv_new may lie inside wider ones."""
+    num_parts owns them.  Rows of kv_new may lie inside wider ones.  Into
+    error_word (int32 [1]) goes bit 0 for rows without a page and bit 1 for
+    starts that fall or leave kv_new."""
     part_id, num_parts = _int32(part_id, "part_id"), _int32(num_parts, "num_parts")
     dev, d, stride, n = _chunk_args("kv_append_chunk", kv_new, "kv_new", kv_pages, block_table, chunk_starts,
                                     "chunk_starts", positions, kv_scale, error_word)
@@ -705,7 +707,8 @@ def kv_read(kv_pages, block_table, read_starts, positions, out, *, kv_scale: flo
             stream=None):
     """mla_kv_read: request b's cached tokens positions[b] (int32 [B]), ... go
     to rows read_starts[b] .. read_starts[b + 1] (int32 [B + 1]) of out bf16
-    [N, 576], e4m3 codes times kv_scale.  Other rows of out stay as they are."""
+    [N, 576], e4m3 codes times kv_scale.  Other rows of out stay as they are.
+    error_word as for kv_append_chunk; rows without a page become zeros."""
     dev, d, stride, n = _chunk_args("kv_read", out, "out", kv_pages, block_table, read_starts, "read_starts",
                                     positions, kv_scale, error_word)
     _launch(load_library().mla_kv_read, dev, stream, kv_pages.data_ptr(), block_table.data_ptr(),
