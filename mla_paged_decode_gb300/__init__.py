@@ -729,7 +729,7 @@ def make_prefill_workspace(q) -> torch.Tensor:
 def _prefill_outputs(out, lse, dev, tokens, heads, dim, workspace, stream, q):
     _need(out, "out", (torch.bfloat16,), dev)
     _need(lse, "lse", (torch.float32,), dev)
-    if out.numel() != tokens * heads * dim or lse.numel() != tokens * heads:
+    if out.shape != (tokens, heads, dim) or lse.shape != (tokens, heads):
         raise ValueError(f"out must be [N, H, {dim}] and lse [N, H]")
     if workspace is None:
         with _allocating_on(stream, dev):
