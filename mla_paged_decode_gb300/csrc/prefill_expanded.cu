@@ -379,8 +379,11 @@ __device__ __forceinline__ void produce(const ExpandedParams &p, Misc &m, uint32
   };
   // Keys run a tile ahead of values, which the products need later, from piece to piece
   // too: (head, key, keys left) is the tile whose values are still to come.  The queries
-  // of a split piece have a place that the piece before leaves free; the others wait for
-  // that piece's last scores, and the values go first.
+  // of a split piece after one of an odd number of tiles have a place that it leaves free.
+  // After an even number they have its place again and wait for its last scores, and so do
+  // the owed values behind them; a place that took turns by itself was no faster (100
+  // requests of 256 queries over 256 keys, 16 heads: 116.6 us against 116.1).  The queries
+  // of other pieces wait for the last scores before them, and the values go first.
   int v_head = 0, v_key = 0, v_left = 0;
   for (Item w = items.next<false>(&ok); ok && w.n; w = items.next<false>(&ok)) {
     for (int j = 0; ok && j < w.n; ++j) {
