@@ -310,7 +310,8 @@ int mla_kv_append(const void *kv_new, void *kv_pages, const int32_t *block_table
  * starts[b + 1] and is its token t = positions[b] + r - starts[b], at physical
  * page block_table[b][t / 64], row t % 64.  Rows before starts[0] and from
  * starts[batch] on (a batch padded to a fixed size) and rows of a request
- * with a negative position are nobody's: nothing is read or written for them.
+ * with a negative position are nobody's: nothing is written for them, and what
+ * they hold does not matter.
  *
  *  num_rows    rows of the buffer (0 is a no-op).
  *  row_stride  values from one row of the buffer to the next: a multiple of 8,
@@ -328,7 +329,9 @@ int mla_kv_append(const void *kv_new, void *kv_pages, const int32_t *block_table
  * write for each (bits, or e4m3 of fp32(x) / kv_scale, to nearest even,
  * saturated), only the tokens of partition part_id of num_parts.  Two rows
  * that go to one cache row race.  mla_kv_read reads them back as bf16: the
- * bits, or fp32(code) * kv_scale rounded to nearest even.  One kernel each.
+ * bits, or fp32(code) * kv_scale rounded to nearest even.  It reads the rows of
+ * all partitions: from a pool into which one rank wrote its own alone it
+ * returns, for the others', whatever the pool holds.  One kernel each.
  */
 int mla_kv_append_chunk(const void *kv_new, int64_t row_stride, int num_rows, void *kv_pages,
                         const int32_t *block_table, const int32_t *chunk_starts,
@@ -485,7 +488,10 @@ int mla_decode_shared(const void *q, const void *kv_pages, const int32_t *block_
  * Attention of a chunk of new tokens over the paged cache, in the absorbed
  * form: any number of query tokens for each request, a prompt's chunk beside
  * requests that decode one token.  The new tokens' rows are in the cache
- * already (mla_kv_append_chunk).
+ * already (mla_kv_append_chunk), those of every partition: a pool that holds one
+ * rank's rows alone is not for this call (its rows count as present), but for
+ * mla_decode_partial, which takes up to 16 query tokens a request.  Every token up
+ * to a query's own is seen; windows and sinks are mla_decode_window's.
  *
  *  q           bf16 [num_tokens, H, 576], contiguous: the requests' query
  *              tokens, one request after the other.

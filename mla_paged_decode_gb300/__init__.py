@@ -708,7 +708,8 @@ def kv_read(kv_pages, block_table, read_starts, positions, out, *, kv_scale: flo
     """mla_kv_read: request b's cached tokens positions[b] (int32 [B]), ... go
     to rows read_starts[b] .. read_starts[b + 1] (int32 [B + 1]) of out bf16
     [N, 576], e4m3 codes times kv_scale.  Other rows of out stay as they are.
-    error_word as for kv_append_chunk; rows without a page become zeros."""
+    error_word as for kv_append_chunk; rows without a page become zeros.  The
+    rows of all partitions are read: the pool has to hold them."""
     dev, d, stride, n = _chunk_args("kv_read", out, "out", kv_pages, block_table, read_starts, "read_starts",
                                     positions, kv_scale, error_word)
     _launch(load_library().mla_kv_read, dev, stream, kv_pages.data_ptr(), block_table.data_ptr(),
@@ -744,7 +745,8 @@ def prefill_chunk(q, kv_pages, block_table, seq_lens, chunk_starts, sm_scale: fl
     [B + 1]) of q bf16 [N, H, 576] are the last of request b's seq_lens[b]
     cached tokens and attend to those up to themselves; out bf16 [N, H, 512]
     and lse fp32 [N, H] are written in place, tokens of no request left as
-    they are.  The workspace is make_prefill_workspace's."""
+    they are.  The pool has to hold the rows of all partitions.  The workspace
+    is make_prefill_workspace's."""
     lse_base = _int32(lse_base, "lse_base")
     dev = q.device
     if dev.type != "cuda":
