@@ -8,7 +8,9 @@
 //   read:   the other way: the bits, or bf16(fp32(fp32(code) * scale)).
 //
 // Both move 1152 B (bf16) or 1152 + 576 B (e4m3) a row each way and compute next to
-// nothing: HBM bounds them.  A warp takes four rows, which are nine 16-byte (e4m3
+// nothing but the quotients of an e4m3 append: HBM bounds the others (65,536 bf16 rows
+// written 25.5 us, 5,910 GB/s, read 26.3; 59,600 e4m3 rows read 19.8, 5,230 GB/s; 24,200
+// rows into an e4m3 cache 13.7 us, 3,030 GB/s, all over buffers in turn).  A warp takes four rows, which are nine 16-byte (e4m3
 // side: 8-byte) chunks a lane, all in flight at once; eight lanes look each row's place
 // up, for an append while the loads are on their way.
 #include "common.cuh"

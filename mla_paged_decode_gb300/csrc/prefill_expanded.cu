@@ -33,9 +33,10 @@
 // keys spread over all SMs.  At most two blocks a pair are cut; their pieces leave fp32
 // partials for a merge by their LSE.
 //
-// Measured: 8,192 queries over as many keys, 16 heads, no mask: 377 us, 1,822 TFLOP/s, 0.97
-// of the measured cuBLAS rate; 128 heads, causal: 1,632 us, 1,684 TFLOP/s; 2,048 queries
-// over 10,240 keys, 128 heads: 965 us, 1,603.  A tile of both halves takes some 3,300
+// Measured: 8,192 queries over as many keys, 16 heads, no mask: 379 to 393 us, 1,750 to
+// 1,810 TFLOP/s, 0.93 to 0.96 of the measured cuBLAS rate; 128 heads, causal: 1,670 to
+// 1,700 us, 1,620 to 1,650; 2,048 queries over 10,240 keys, 128 heads: 1,010 us, 1,530 (all
+// three under the power cap).  A tile of both halves takes some 3,300
 // cycles where the clock is not the bound: the softmax of a half 1,500 (its 128
 // exponentials a row are 512 of them), its products 1,280, the rest hand-overs.
 #include "prefill_expanded.cuh"
